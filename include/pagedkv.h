@@ -358,6 +358,185 @@ int pkv_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pairs, in
                     pkv_dtype cache_dtype, uint32_t* device_errors, void* stream);
 
 /*
+ * Step maps: what the other calls of a serving step take, built on the GPU from
+ * the requests' lengths.
+ * Sources: openeuler.csdn.net PagedAttention notes, "Block Table 数据结构"
+ * (slot = physical_block * block_size + offset); "第34讲 …", §1.2 (the manager
+ * hands a step's requests their new blocks).
+ *
+ *   request_tables [num_request_rows][max_blocks_per_seq] int32, in/out: the
+ *         block list of every running request, kept between steps.
+ *   rows  [num_seqs] int32: the request row of each sequence of the batch
+ *         (distinct).  A negative row is a padding sequence: no context, no
+ *         queries.
+ *   cached_lens, q_lens  [num_seqs] int32: tokens a sequence has in the cache,
+ *         and those this step adds (either may be 0).
+ *   new_blocks  [num_new_blocks] int32: the blocks this step opens, in batch
+ *         order: sequence s takes the next ceil((cached + q) / 16) -
+ *         ceil(cached / 16) of them (what pkv_request_append handed out).  They
+ *         are appended to the request's row of request_tables.
+ *   block_tables [num_seqs][max_blocks_per_seq]: the first ceil(context / 16)
+ *         entries of each row are written, the rest left as they were.
+ *   context_lens [num_seqs] = cached + q; query_start_loc [num_seqs + 1].
+ *   slot_mapping [num_tokens] int64, positions [num_tokens] int32: per query
+ *         token, in batch order; -1 behind the last sequence's (num_tokens may
+ *         exceed the sum of q_lens, as in a captured step of fixed size).
+ *
+ * A row >= num_request_rows, a negative length or a context beyond the table
+ * makes the sequence a padding one; queries past num_tokens are cut off: both
+ * flag PKV_DEVERR_CONTEXT.  A block id outside [0, num_blocks), or a new_blocks
+ * list that runs out (its entries become -1), flags PKV_DEVERR_BLOCK_ID, and the
+ * tokens of such a block get slot -1.  Two sequences of one row are a caller's
+ * error (that row's entries are unspecified).
+ * At most PKV_STEP_MAPS_MAX_SEQS sequences (PKV_ERR_UNSUPPORTED beyond).
+ */
+#define PKV_STEP_MAPS_MAX_SEQS 16384
+int pkv_build_step_maps(int32_t* block_tables, int32_t* context_lens, int32_t* query_start_loc,
+                        int64_t* slot_mapping, int32_t* positions, int32_t* request_tables,
+                        const int32_t* rows, const int32_t* cached_lens, const int32_t* q_lens,
+                        const int32_t* new_blocks, int num_seqs, int num_request_rows,
+                        int max_blocks_per_seq, int num_tokens, int num_new_blocks,
+                        int block_size, int num_blocks, uint32_t* device_errors, void* stream);
+
+/*
+ * Rotary frequencies of a model, on the host: inv_freq[i], i < rotary_dim / 2,
+ * base^(-2 i / rotary_dim) scaled for a longer context by `scaling`:
+ *   PKV_ROTARY_PLAIN   not scaled
+ *   PKV_ROTARY_LINEAR  inv / factor (positions interpolated)
+ *   PKV_ROTARY_NTK     base * factor^(r / (r - 2)) for base, r = rotary_dim
+ *                      (rotary_dim 2: the base stays)
+ *   PKV_ROTARY_BANDS   wavelengths w = 2 pi / inv below original_len / high stay,
+ *                      above original_len / low are divided by factor, and in
+ *                      between by a blend, m inv + (1 - m) inv / factor with
+ *                      m = (original_len / w - low) / (high - low); low < high
+ *   PKV_ROTARY_YARN    dimensions turning more than `high` times over
+ *                      original_len stay, less than `low` times are divided by
+ *                      factor, linear ramp between (in the dimension index, its
+ *                      ends rounded outwards); attn_factor 0.1 ln(factor) + 1
+ * attn_factor_out (may be NULL) receives the factor of cosines and sines (1
+ * except for PKV_ROTARY_YARN).  base > 1, factor >= 1; original_len, low and high
+ * are read by the last two only.
+ */
+typedef enum {
+  PKV_ROTARY_PLAIN = 0,
+  PKV_ROTARY_LINEAR = 1,
+  PKV_ROTARY_NTK = 2,
+  PKV_ROTARY_BANDS = 3,
+  PKV_ROTARY_YARN = 4
+} pkv_rotary_scaling;
+int pkv_rotary_frequencies(double* inv_freq, int rotary_dim, double base,
+                           pkv_rotary_scaling scaling, double factor, double low, double high,
+                           int original_len, float* attn_factor_out);
+
+/*
+ * Rotary positions of a step's Q and K, fused with the cache write: q is
+ * rotated into q_out, k rotated into its slot of k_cache, v written to its slot
+ * of v_cache (pkv_reshape_and_cache with the rotation in front, in one pass and
+ * with one rounding).
+ *
+ *   q, k, v   [num_tokens][heads][head_dim], src_dtype; a token's heads are
+ *             contiguous, tokens q_stride / k_stride / v_stride elements apart
+ *             (multiples of 8, at least heads * head_dim): slices of a fused
+ *             projection's output will do.
+ *   q_out     [num_tokens][num_heads][head_dim] contiguous; may be q itself
+ *             (with q_stride num_heads * head_dim), must not overlap q, k or v
+ *             otherwise.
+ *   positions [num_tokens] int32.  A negative position is a padding token:
+ *             nothing is written for it.
+ *   slot_mapping [num_tokens] int64, as for pkv_reshape_and_cache (a negative
+ *             slot: K and V are not written, q is rotated all the same).
+ *   inv_freq  HOST array of rotary_dim / 2 doubles, read during the call.
+ *             Pair i of a token at position t turns by t * inv_freq[i]; the
+ *             angle is reduced exactly, for positions up to 2^30.
+ *   rotary_dim  even, 2 .. head_dim: the elements that turn; the others pass.
+ *   layout    PKV_ROTARY_HALF: pair i is elements (i, i + rotary_dim / 2);
+ *             PKV_ROTARY_INTERLEAVED: elements (2 i, 2 i + 1).
+ *   attn_factor  multiplies the rotated elements of q and k (finite).
+ *   cache_dtype  == src_dtype, or FP8_E4M3: E4M3(x / scale) of the rotated
+ *             value in fp32, saturating.
+ * num_tokens == 0 launches nothing.  At most 2^24 elements per token.
+ */
+typedef enum { PKV_ROTARY_HALF = 0, PKV_ROTARY_INTERLEAVED = 1 } pkv_rotary_layout;
+int pkv_rotary_and_cache(void* q_out, const void* q, const void* k, const void* v, void* k_cache,
+                         void* v_cache, const int64_t* slot_mapping, const int32_t* positions,
+                         const double* inv_freq, int64_t q_stride, int64_t k_stride,
+                         int64_t v_stride, int num_tokens, int num_heads, int num_kv_heads,
+                         int head_dim, int block_size, int num_blocks, int rotary_dim,
+                         pkv_rotary_layout layout, float attn_factor, pkv_dtype src_dtype,
+                         pkv_dtype cache_dtype, float k_scale, float v_scale,
+                         uint32_t* device_errors, void* stream);
+
+/*
+ * Attention with modified scores and key intervals.  With s = scale * q . k of
+ * a query at position pos and a key at position j:
+ *   softcap > 0         s becomes softcap * tanh(s / softcap)
+ *   alibi_slopes        s becomes s - alibi_slopes[h] * |pos - j|; [num_heads]
+ *                       float (device), or NULL
+ * and the query sees the keys lo <= j < hi,
+ *   lo = max(key_start[row], pos - window + 1, 0)
+ *   hi = max(pos + 1, prefix_lens[seq])            (pos + 1 for decode)
+ *   window > 0          sliding window of that many keys, the query's own one
+ *                       included; 0: none
+ *   key_start           [query rows] int32 (device): the row's first key, e.g.
+ *                       the start of its document; within a sequence it must
+ *                       not decrease from row to row.  NULL: 0
+ *   prefix_lens         prefill only, [num_seqs] int32 (device): the first keys
+ *                       of a sequence that all its queries see, in both
+ *                       directions (cut back to the context); NULL: causal
+ * A row that sees no key gets zeros.  K and V of a key that a row does not see
+ * do not reach it, whatever they hold (infinities and NaN included), and the
+ * table entries of blocks that no row of the batch sees are not read (a
+ * sequence may have returned the blocks behind its window).
+ * NULL / zero members switch a modifier off; a NULL struct switches all off.
+ */
+typedef struct {
+  float softcap;
+  const float* alibi_slopes;
+  int window;
+  const int32_t* key_start;
+  const int32_t* prefix_lens;
+} pkv_score_mods;
+
+/*
+ * Decode attention under pkv_score_mods; other arguments as for
+ * pkv_paged_attention_decode (without partition_size).  prefix_lens must be NULL.
+ * workspace: at least pkv_decode_biased_workspace_size(...) bytes, with the
+ * call's window (0 for none); a window bounds it however long the contexts are.
+ */
+size_t pkv_decode_biased_workspace_size(int num_seqs, int num_heads, int head_dim,
+                                        int max_context_len, int window);
+int pkv_paged_attention_decode_biased(void* out, const void* q, const void* k_cache,
+                                      const void* v_cache, const int32_t* block_tables,
+                                      const int32_t* context_lens, const pkv_score_mods* mods,
+                                      int num_seqs, int num_heads, int num_kv_heads,
+                                      int head_dim, int block_size, int max_blocks_per_seq,
+                                      int num_blocks, int max_context_len, float scale,
+                                      pkv_dtype q_dtype, pkv_dtype kv_dtype, float k_scale,
+                                      float v_scale, void* workspace, size_t workspace_bytes,
+                                      uint32_t* device_errors, void* stream);
+
+/*
+ * Chunked-prefill attention under pkv_score_mods; other arguments as for
+ * pkv_paged_attention_prefill_chunk.
+ * workspace: at least pkv_prefill_biased_workspace_size(...) bytes, 256-byte
+ * aligned (NULL when that is 0, as it is for 16-bit caches of head_dim 128).
+ */
+size_t pkv_prefill_biased_workspace_size(int num_seqs, int total_q, int num_heads,
+                                         int num_kv_heads, int head_dim, int max_context_len,
+                                         pkv_dtype q_dtype, pkv_dtype kv_dtype);
+int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_cache,
+                                       const void* v_cache, const int32_t* block_tables,
+                                       const int32_t* context_lens,
+                                       const int32_t* query_start_loc,
+                                       const pkv_score_mods* mods, int num_seqs, int total_q,
+                                       int max_q_len, int num_heads, int num_kv_heads,
+                                       int head_dim, int block_size, int max_blocks_per_seq,
+                                       int num_blocks, int max_context_len, float scale,
+                                       pkv_dtype q_dtype, pkv_dtype kv_dtype, float k_scale,
+                                       float v_scale, void* workspace, size_t workspace_bytes,
+                                       uint32_t* device_errors, void* stream);
+
+/*
  * Host block pool with prefix caching.  Sources: "第34讲 … vLLM 生产级系统架构
  * 全景剖析与四重加速引擎", §1.2 (KVCacheManager.allocate_slots / free, BlockPool,
  * FreeKVCacheBlockQueue), §2.2 (longest-prefix reuse with ref_cnt), §2.3

@@ -17,6 +17,7 @@ Tensor conventions:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -29,7 +30,9 @@ __all__ = [
     "paged_attention_decode_noalloc", "paged_attention_prefill_chunk", "check_errors", "status_string", "version",
     "paged_attention_prefill_tree", "cascade_workspace_size", "paged_attention_decode_cascade",
     "copy_blocks", "BlockPool", "Request", "mixed_workspace_size", "paged_attention_mixed",
-    "debug_arm_wait_timeout", "debug_prefill_pairs",
+    "debug_arm_wait_timeout", "debug_prefill_pairs", "build_step_maps", "rotary_frequencies",
+    "rotary_and_cache", "decode_biased_workspace_size", "paged_attention_decode_biased",
+    "prefill_biased_workspace_size", "paged_attention_prefill_biased",
 ]
 
 F16, BF16, FP8_E4M3 = 0, 1, 2
@@ -42,6 +45,16 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+
+
+class _ScoreMods(ctypes.Structure):
+    """pkv_score_mods"""
+    _fields_ = [("softcap", _F), ("alibi_slopes", _P), ("window", _I), ("key_start", _P),
+                ("prefix_lens", _P)]
+
+
+_ROTARY_SCALING = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+_ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
 
 
 class PagedKVError(RuntimeError):
@@ -106,6 +119,24 @@ def load():
                 [_P] * 7 + [_I] * 11 + [_F, _I, _I, _F, _F, _I, _P, _SZ, _P, _P])
             lib.pkv_copy_blocks.restype = _I
             lib.pkv_copy_blocks.argtypes = [_P, _P, _P] + [_I] * 6 + [_P, _P]
+            lib.pkv_build_step_maps.restype = _I
+            lib.pkv_build_step_maps.argtypes = [_P] * 10 + [_I] * 7 + [_P, _P]
+            lib.pkv_rotary_frequencies.restype = _I
+            lib.pkv_rotary_frequencies.argtypes = [_P, _I, ctypes.c_double, _I] + \
+                [ctypes.c_double] * 3 + [_I, _P]
+            lib.pkv_rotary_and_cache.restype = _I
+            lib.pkv_rotary_and_cache.argtypes = (
+                [_P] * 9 + [ctypes.c_int64] * 3 + [_I] * 8 + [_F, _I, _I, _F, _F, _P, _P])
+            lib.pkv_decode_biased_workspace_size.restype = _SZ
+            lib.pkv_decode_biased_workspace_size.argtypes = [_I] * 5
+            lib.pkv_paged_attention_decode_biased.restype = _I
+            lib.pkv_paged_attention_decode_biased.argtypes = (
+                [_P] * 7 + [_I] * 8 + [_F, _I, _I, _F, _F, _P, _SZ, _P, _P])
+            lib.pkv_prefill_biased_workspace_size.restype = _SZ
+            lib.pkv_prefill_biased_workspace_size.argtypes = [_I] * 8
+            lib.pkv_paged_attention_prefill_biased.restype = _I
+            lib.pkv_paged_attention_prefill_biased.argtypes = (
+                [_P] * 8 + [_I] * 10 + [_F, _I, _I, _F, _F, _P, _SZ, _P, _P])
             _I32 = ctypes.c_int32
             lib.pkv_block_pool_create.restype = _I
             lib.pkv_block_pool_create.argtypes = [_I32, _I32, _P]
@@ -389,6 +420,249 @@ def copy_blocks(k_cache, v_cache, block_pairs, device_errors=None, stream=None):
     rc = load().pkv_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(block_pairs), n, hkv, d, bs,
                                 nb, _dtype_code(k_cache), _ptr(device_errors), _stream(stream))
     _check("pkv_copy_blocks", rc)
+
+
+def _on_device(device, stream, *tensors):
+    """The stream a call launches on, after checking that its tensors are on `device`.
+
+    Returns (stream, None), or (stream, guard) when `device` is not the current one."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("tensors must be on the same CUDA device")
+    if device.type != "cuda":
+        raise ValueError("tensors must be on the CUDA device")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    away = device.index is not None and device.index != torch.cuda.current_device()
+    return stream, (torch.cuda.device(device) if away else contextlib.nullcontext())
+
+
+def _scratch_on(stream, nbytes, workspace, device):
+    """A workspace of nbytes: the caller's, or one that the launch's stream owns (so
+    that the allocator hands it out again only behind the launch)."""
+    if nbytes == 0:
+        return None, 0
+    if workspace is None:
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the tensors' device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _want(name, t, dtype, shape):
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def build_step_maps(block_tables, context_lens, query_start_loc, slot_mapping, positions,
+                    request_tables, rows, cached_lens, q_lens, new_blocks, num_blocks: int,
+                    block_size: int = 16, device_errors=None, stream=None):
+    """Block tables, context lengths, query offsets, slots and positions of a
+    step, built on the GPU from the requests' lengths (pkv_build_step_maps).
+
+    Outputs: block_tables [S, MB] int32 (entries past a context are left as they
+    were), context_lens [S] int32, query_start_loc [S + 1] int32, slot_mapping [T]
+    int64 and positions [T] int32 (-1 behind the last sequence's tokens).
+    In/out: request_tables [R, MB] int32.  Inputs: rows, cached_lens, q_lens [S]
+    int32 (a negative row: a padding sequence), new_blocks [N] int32."""
+    S, (R, MB), T = rows.numel(), request_tables.shape, slot_mapping.numel()
+    _want("block_tables", block_tables, torch.int32, (S, MB))
+    _want("context_lens", context_lens, torch.int32, (S,))
+    _want("query_start_loc", query_start_loc, torch.int32, (S + 1,))
+    _want("slot_mapping", slot_mapping, torch.int64, (T,))
+    _want("positions", positions, torch.int32, (T,))
+    _want("request_tables", request_tables, torch.int32, (R, MB))
+    _want("rows", rows, torch.int32, (S,))
+    _want("cached_lens", cached_lens, torch.int32, (S,))
+    _want("q_lens", q_lens, torch.int32, (S,))
+    _want("new_blocks", new_blocks, torch.int32, (new_blocks.numel(),))
+    stream, guard = _on_device(request_tables.device, stream, block_tables, context_lens,
+                               query_start_loc, slot_mapping, positions, rows, cached_lens, q_lens,
+                               new_blocks, device_errors)
+    with guard:
+        rc = load().pkv_build_step_maps(
+            block_tables.data_ptr(), context_lens.data_ptr(), query_start_loc.data_ptr(),
+            slot_mapping.data_ptr(), positions.data_ptr(), request_tables.data_ptr(),
+            rows.data_ptr(), cached_lens.data_ptr(), q_lens.data_ptr(), new_blocks.data_ptr(), S, R,
+            MB, T, new_blocks.numel(), block_size, num_blocks, _ptr(device_errors),
+            stream.cuda_stream)
+    _check("pkv_build_step_maps", rc)
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                       factor: float = 1.0, low: float = 1.0, high: float = 32.0,
+                       original_len: int = 0):
+    """(inv_freq [rotary_dim / 2] float64 array, attention factor) of a model's
+    rotary positions (pkv_rotary_frequencies): scaling "none", "linear", "ntk",
+    "bands" or "yarn"; low, high and original_len are read by the last two."""
+    import numpy as np
+    if scaling not in _ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROTARY_SCALING)}")
+    if rotary_dim < 2:
+        raise ValueError("rotary_dim must be at least 2")
+    inv = np.empty(rotary_dim // 2, dtype=np.float64)
+    attn = ctypes.c_float(1.0)
+    _check("pkv_rotary_frequencies", load().pkv_rotary_frequencies(
+        inv.ctypes.data, rotary_dim, base, _ROTARY_SCALING[scaling], factor, low, high,
+        original_len, ctypes.byref(attn)))
+    return inv, attn.value
+
+
+def rotary_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_freq,
+                     layout: str = "half", attn_factor: float = 1.0, k_scale: float = 1.0,
+                     v_scale: float = 1.0, device_errors=None, stream=None):
+    """Rotates q ([T, H, D]) into q_out and k ([T, Hkv, D]) into its cache slots and
+    writes v to its slots (pkv_rotary_and_cache).
+
+    q, k and v may be slices of a fused projection's output (a token's heads
+    contiguous, any token stride that is a multiple of 8 elements).  positions [T]
+    int32 (negative: padding), slot_mapping [T] int64, inv_freq: rotary_dim / 2
+    float64 values on the host; layout "half" or "interleaved"."""
+    import numpy as np
+    T, H, D = q.shape
+    hkv = k.shape[1]
+    inv = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if layout not in _ROTARY_LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(_ROTARY_LAYOUT)}")
+    if inv.ndim != 1:
+        raise ValueError("inv_freq must be one-dimensional")
+    for name, t, heads in (("q", q, H), ("k", k, hkv), ("v", v, hkv)):
+        if t.dtype != q.dtype or tuple(t.shape) != (T, heads, D):
+            raise ValueError(f"{name} must be [{T}, {heads}, {D}] of q's dtype")
+        if T and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+            raise ValueError(f"{name}: a token's heads must be contiguous")
+    _want("q_out", q_out, q.dtype, (T, H, D))
+    _want("slot_mapping", slot_mapping, torch.int64, (T,))
+    _want("positions", positions, torch.int32, (T,))
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _want(name, c, k_cache.dtype, (k_cache.shape[0], hkv, k_cache.shape[2], D))
+    stream, guard = _on_device(q.device, stream, q_out, k, v, k_cache, v_cache, slot_mapping,
+                               positions, device_errors)
+    # (a single token's stride is never stepped)
+    qs, ks, vs = (t.stride(0) if T > 1 else h * D for t, h in ((q, H), (k, hkv), (v, hkv)))
+    with guard:
+        rc = load().pkv_rotary_and_cache(
+            q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), inv.ctypes.data, qs,
+            ks, vs, T, H, hkv, D, k_cache.shape[2], k_cache.shape[0], 2 * inv.size,
+            _ROTARY_LAYOUT[layout], attn_factor, _dtype_code(q), _dtype_code(k_cache), k_scale,
+            v_scale, _ptr(device_errors), stream.cuda_stream)
+    _check("pkv_rotary_and_cache", rc)
+    return q_out
+
+
+def _biased_args(out, q, k_cache, v_cache, block_tables, context_lens, softcap, alibi_slopes,
+                 window, key_start, prefix_lens):
+    """Checks the tensors of a biased attention call; returns its pkv_score_mods."""
+    rows, H, D = q.shape
+    nb, hkv, bs, _ = k_cache.shape
+    S = context_lens.numel()
+    _want("q", q, q.dtype, (rows, H, D))
+    _want("out", out, q.dtype, (rows, H, D))
+    _want("k_cache", k_cache, k_cache.dtype, (nb, hkv, bs, D))
+    _want("v_cache", v_cache, k_cache.dtype, (nb, hkv, bs, D))
+    _want("context_lens", context_lens, torch.int32, (S,))
+    _want("block_tables", block_tables, torch.int32, (S, block_tables.shape[-1]))
+    _want("alibi_slopes", alibi_slopes, torch.float32, (H,))
+    _want("key_start", key_start, torch.int32, (rows,))
+    _want("prefix_lens", prefix_lens, torch.int32, (S,))
+    return _ScoreMods(softcap, alibi_slopes.data_ptr() if alibi_slopes is not None else None,
+                      window, key_start.data_ptr() if key_start is not None else None,
+                      prefix_lens.data_ptr() if prefix_lens is not None else None)
+
+
+def decode_biased_workspace_size(num_seqs: int, num_heads: int, head_dim: int,
+                                 max_context_len: int, window: int = 0) -> int:
+    return int(load().pkv_decode_biased_workspace_size(num_seqs, num_heads, head_dim,
+                                                       max_context_len, window))
+
+
+def paged_attention_decode_biased(out, q, k_cache, v_cache, block_tables, context_lens,
+                                  scale: float, softcap: float = 0.0, alibi_slopes=None,
+                                  window: int = 0, key_start=None,
+                                  max_context_len: int | None = None, k_scale: float = 1.0,
+                                  v_scale: float = 1.0, workspace=None, device_errors=None,
+                                  stream=None):
+    """Decode attention with capped scores (softcap), a distance bias
+    (alibi_slopes [H] float32), a sliding window and a first key per sequence
+    (key_start [S] int32): pkv_paged_attention_decode_biased.  max_context_len and
+    workspace (>= decode_biased_workspace_size bytes) as for
+    paged_attention_decode."""
+    mods = _biased_args(out, q, k_cache, v_cache, block_tables, context_lens, softcap,
+                        alibi_slopes, window, key_start, None)
+    S, H, D = q.shape
+    nb, hkv, bs, _ = k_cache.shape
+    if context_lens.numel() != S:
+        raise ValueError("context_lens must have one entry per query row")
+    stream, guard = _on_device(q.device, stream, out, k_cache, v_cache, block_tables, context_lens,
+                               alibi_slopes, key_start, device_errors)
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if S else 0
+    with guard:
+        ws, wsb = _scratch_on(stream, decode_biased_workspace_size(S, H, D, max_context_len, window),
+                              workspace, q.device)
+        rc = load().pkv_paged_attention_decode_biased(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), context_lens.data_ptr(), ctypes.addressof(mods), S, H, hkv, D,
+            bs, block_tables.shape[1], nb, max_context_len, scale, _dtype_code(q),
+            _dtype_code(k_cache), k_scale, v_scale, _ptr(ws), wsb, _ptr(device_errors),
+            stream.cuda_stream)
+    _check("pkv_paged_attention_decode_biased", rc)
+    return out
+
+
+def prefill_biased_workspace_size(num_seqs: int, total_q: int, num_heads: int, num_kv_heads: int,
+                                  head_dim: int, max_context_len: int, q_dtype: int,
+                                  kv_dtype: int) -> int:
+    return int(load().pkv_prefill_biased_workspace_size(num_seqs, total_q, num_heads, num_kv_heads,
+                                                        head_dim, max_context_len, q_dtype,
+                                                        kv_dtype))
+
+
+def paged_attention_prefill_biased(out, q, k_cache, v_cache, block_tables, context_lens,
+                                   query_start_loc, scale: float, softcap: float = 0.0,
+                                   alibi_slopes=None, window: int = 0, key_start=None,
+                                   prefix_lens=None, max_q_len: int | None = None,
+                                   max_context_len: int | None = None, k_scale: float = 1.0,
+                                   v_scale: float = 1.0, workspace=None, device_errors=None,
+                                   stream=None):
+    """Chunked-prefill attention with capped scores, a distance bias, a sliding
+    window, a first key per query row (key_start [total_q] int32: document masks)
+    and keys seen in both directions (prefix_lens [S] int32):
+    pkv_paged_attention_prefill_biased."""
+    mods = _biased_args(out, q, k_cache, v_cache, block_tables, context_lens, softcap,
+                        alibi_slopes, window, key_start, prefix_lens)
+    TQ, H, D = q.shape
+    nb, hkv, bs, _ = k_cache.shape
+    S = context_lens.numel()
+    _want("query_start_loc", query_start_loc, torch.int32, (S + 1,))
+    stream, guard = _on_device(q.device, stream, out, k_cache, v_cache, block_tables, context_lens,
+                               query_start_loc, alibi_slopes, key_start, prefix_lens, device_errors)
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if S else 0
+    if max_q_len is None:
+        max_q_len = int((query_start_loc[1:] - query_start_loc[:-1]).max().item()) if S else 0
+    qd, kd = _dtype_code(q), _dtype_code(k_cache)
+    with guard:
+        need = prefill_biased_workspace_size(S, TQ, H, hkv, D, max_context_len, qd, kd)
+        ws, wsb = _scratch_on(stream, need, workspace, q.device)
+        rc = load().pkv_paged_attention_prefill_biased(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), context_lens.data_ptr(), query_start_loc.data_ptr(),
+            ctypes.addressof(mods), S, TQ, max_q_len, H, hkv, D, bs, block_tables.shape[1], nb,
+            max_context_len, scale, qd, kd, k_scale, v_scale, _ptr(ws), wsb, _ptr(device_errors),
+            stream.cuda_stream)
+    _check("pkv_paged_attention_prefill_biased", rc)
+    return out
 
 
 class _Scratch:

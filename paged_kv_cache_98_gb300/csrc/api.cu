@@ -42,6 +42,37 @@ int pow2_at_least(int g) {
   return p;
 }
 
+// Partitions of a call whose rows see at most `window` keys (0: all): a window
+// may start in the middle of a block.
+int parts_for_window(int max_context_len, int window) {
+  long long keys = max_context_len;
+  if (window > 0 && (long long)window + pkv::kBlockSize - 1 < keys)
+    keys = (long long)window + pkv::kBlockSize - 1;
+  return parts_for((int)keys, kDefaultPartition);
+}
+
+// Checks the modifiers and fills their launch fields.
+int set_mods(pkv::AttnParams& p, const pkv_score_mods* m, int max_context_len, float scale,
+             float k_scale, int kv_dtype) {
+  p.mods = 1;
+  p.max_context = max_context_len;
+  if (!m) return PKV_OK;
+  if (!(m->softcap >= 0.0f) || !std::isfinite(m->softcap) || m->window < 0)
+    return PKV_ERR_INVALID_ARG;
+  if (m->softcap > 0.0f) {
+    const float s = scale * (kv_dtype == PKV_FP8_E4M3 ? k_scale : 1.0f);
+    if (!std::isfinite(s / m->softcap) || !std::isnormal(m->softcap * pkv::kLog2e))
+      return PKV_ERR_INVALID_ARG;
+  }
+  p.softcap = m->softcap;
+  p.cap_log2 = m->softcap * pkv::kLog2e;
+  p.alibi = m->alibi_slopes;
+  p.window = m->window;
+  p.key_start = m->key_start;
+  p.bidir_lens = m->prefix_lens;
+  return PKV_OK;
+}
+
 // Checks shared by decode and prefill.
 int check_attention_args(const void* out, const void* q, const void* k_cache,
                          const void* v_cache, const int32_t* block_tables,
@@ -92,7 +123,7 @@ int run_attention(pkv::AttnParams& p, int q_dtype, int kv_dtype, int head_dim, f
   const int g_pad = pow2_at_least(p.group);
   pkv::take_debug_hook(p);
   int rc;
-  if (pkv::tc_decode_supported(p, q_dtype, kv_dtype, head_dim))
+  if (!p.mods && pkv::tc_decode_supported(p, q_dtype, kv_dtype, head_dim))
     rc = pkv::launch_paged_decode_tc(p, q_dtype, kv_dtype, stream);
   else
     rc = pkv::launch_paged_attention_simt(p, q_dtype, kv_dtype, head_dim, g_pad, stream);
@@ -119,6 +150,13 @@ void take_debug_hook(AttnParams& p) {
 
 int launch_paged_attention_simt(const AttnParams& p, int q_dtype, int kv_dtype, int head_dim,
                                 int g_pad, cudaStream_t stream) {
+  if (p.mods) {
+    if (q_dtype == PKV_F16)
+      return kv_dtype == PKV_FP8_E4M3 ? launch_simt_mods_f16_e4m3(p, head_dim, g_pad, stream)
+                                      : launch_simt_mods_f16_f16(p, head_dim, g_pad, stream);
+    return kv_dtype == PKV_FP8_E4M3 ? launch_simt_mods_bf16_e4m3(p, head_dim, g_pad, stream)
+                                    : launch_simt_mods_bf16_bf16(p, head_dim, g_pad, stream);
+  }
   if (q_dtype == PKV_F16)
     return kv_dtype == PKV_FP8_E4M3 ? launch_simt_f16_e4m3(p, head_dim, g_pad, stream)
                                     : launch_simt_f16_f16(p, head_dim, g_pad, stream);
@@ -520,6 +558,109 @@ int pkv_paged_attention_decode_cascade(void* out, const void* q, const void* k_c
   rc = pkv::launch_paged_decode_tc(ps, q_dtype, kv_dtype, st, num_groups > 0 && max_prefix_len > 0);
   if (rc != PKV_OK) return rc;
   return pkv::launch_lse_merge(ps, q_dtype, head_dim, st);
+}
+
+size_t pkv_decode_biased_workspace_size(int num_seqs, int num_heads, int head_dim,
+                                        int max_context_len, int window) {
+  if (num_seqs <= 0 || num_heads <= 0 || head_dim <= 0 || max_context_len < 0 || window < 0)
+    return 0;
+  return split_workspace((size_t)num_seqs, num_heads, head_dim,
+                         parts_for_window(max_context_len, window));
+}
+
+int pkv_paged_attention_decode_biased(void* out, const void* q, const void* k_cache,
+                                      const void* v_cache, const int32_t* block_tables,
+                                      const int32_t* context_lens, const pkv_score_mods* mods,
+                                      int num_seqs, int num_heads, int num_kv_heads,
+                                      int head_dim, int block_size, int max_blocks_per_seq,
+                                      int num_blocks, int max_context_len, float scale,
+                                      pkv_dtype q_dtype, pkv_dtype kv_dtype, float k_scale,
+                                      float v_scale, void* workspace, size_t workspace_bytes,
+                                      uint32_t* device_errors, void* stream) {
+  int rc = check_attention_args(out, q, k_cache, v_cache, block_tables, context_lens, num_seqs,
+                                num_heads, num_kv_heads, head_dim, block_size,
+                                max_blocks_per_seq, num_blocks, max_context_len, scale, q_dtype,
+                                kv_dtype, k_scale, v_scale);
+  if (rc != PKV_OK) return rc;
+  pkv::AttnParams p{};
+  rc = set_mods(p, mods, max_context_len, scale, k_scale, kv_dtype);
+  if (rc != PKV_OK) return rc;
+  if (p.bidir_lens) return PKV_ERR_INVALID_ARG;  // a decode row is the last token
+  if (num_seqs == 0) return PKV_OK;
+  p.out = out;
+  p.q = q;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.num_seqs = num_seqs;
+  p.num_rows = num_seqs;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = num_heads / num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.partition = kDefaultPartition;
+  p.max_parts = parts_for_window(max_context_len, p.window);
+  if (p.max_parts > 16384) return PKV_ERR_UNSUPPORTED;
+  p.errors = device_errors;
+  const size_t need = split_workspace((size_t)num_seqs, num_heads, head_dim, p.max_parts);
+  return run_attention(p, q_dtype, kv_dtype, head_dim, scale, k_scale, v_scale, workspace, need,
+                       workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+size_t pkv_prefill_biased_workspace_size(int num_seqs, int total_q, int num_heads,
+                                         int num_kv_heads, int head_dim, int max_context_len,
+                                         pkv_dtype q_dtype, pkv_dtype kv_dtype) {
+  if (num_seqs <= 0 || total_q <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      max_context_len < 0)
+    return 0;
+  return split_workspace((size_t)total_q, num_heads, head_dim,
+                         parts_for(max_context_len, kDefaultPartition));
+}
+
+int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_cache,
+                                       const void* v_cache, const int32_t* block_tables,
+                                       const int32_t* context_lens,
+                                       const int32_t* query_start_loc,
+                                       const pkv_score_mods* mods, int num_seqs, int total_q,
+                                       int max_q_len, int num_heads, int num_kv_heads,
+                                       int head_dim, int block_size, int max_blocks_per_seq,
+                                       int num_blocks, int max_context_len, float scale,
+                                       pkv_dtype q_dtype, pkv_dtype kv_dtype, float k_scale,
+                                       float v_scale, void* workspace, size_t workspace_bytes,
+                                       uint32_t* device_errors, void* stream) {
+  int rc = check_attention_args(out, q, k_cache, v_cache, block_tables, context_lens, num_seqs,
+                                num_heads, num_kv_heads, head_dim, block_size,
+                                max_blocks_per_seq, num_blocks, max_context_len, scale, q_dtype,
+                                kv_dtype, k_scale, v_scale);
+  if (rc != PKV_OK) return rc;
+  if (!query_start_loc || total_q < 0 || max_q_len < 0) return PKV_ERR_INVALID_ARG;
+  pkv::AttnParams p{};
+  rc = set_mods(p, mods, max_context_len, scale, k_scale, kv_dtype);
+  if (rc != PKV_OK) return rc;
+  if (num_seqs == 0 || total_q == 0) return PKV_OK;
+  p.out = out;
+  p.q = q;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.query_start_loc = query_start_loc;
+  p.num_seqs = num_seqs;
+  p.num_rows = total_q;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = num_heads / num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.partition = kDefaultPartition;
+  p.max_parts = parts_for(max_context_len, kDefaultPartition);
+  if (p.max_parts > 16384) return PKV_ERR_UNSUPPORTED;
+  p.errors = device_errors;
+  const size_t need = split_workspace((size_t)total_q, num_heads, head_dim, p.max_parts);
+  return run_attention(p, q_dtype, kv_dtype, head_dim, scale, k_scale, v_scale, workspace, need,
+                       workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 int pkv_debug_prefill_pairs(int mode) {

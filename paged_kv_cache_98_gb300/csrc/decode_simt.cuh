@@ -28,6 +28,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "rows.cuh"
+#include "score_mods.cuh"
 
 namespace pkv {
 
@@ -105,7 +106,10 @@ __device__ __forceinline__ void load_q(const typename QT::T* src, float* f, floa
   for (int e = 0; e < N; ++e) f[e] *= scale;
 }
 
-template <class QT, class KVT, int D, int G>
+// kMods: modified scores and key intervals (score_mods.cuh).  A row's partitions
+// then start at its first visible block; the keys before its first visible one
+// get weight zero and their V rows are not read.
+template <class QT, class KVT, int D, int G, bool kMods = false>
 __global__ void __launch_bounds__(kSimtThreads, (SimtGeom<KVT, D, G>::kCtasPerSm))
     paged_attention_simt_kernel(const AttnParams p) {
   using Geo = SimtGeom<KVT, D, G>;
@@ -129,7 +133,18 @@ __global__ void __launch_bounds__(kSimtThreads, (SimtGeom<KVT, D, G>::kCtasPerSm
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = p.partition;
   int seq;
-  const int keys = row_keys(p, row, &seq);
+  int keys, kstart = 0, front = 0, pos = 0;  // kstart: key the partitions start from
+  if constexpr (kMods) {
+    const RowKeys rk = mods_row_keys(p, row, threadIdx.x == 0);
+    if (rk.hi < 0) return;
+    seq = rk.seq;
+    pos = rk.pos;
+    kstart = first_block_key(rk.lo);
+    front = rk.lo - kstart;
+    keys = rk.hi > rk.lo ? rk.hi - kstart : 0;
+  } else {
+    keys = row_keys(p, row, &seq);
+  }
   const int start = part * P;
   const bool split = p.max_parts > 1;
   const int nparts = (keys + P - 1) / P;
@@ -146,7 +161,17 @@ __global__ void __launch_bounds__(kSimtThreads, (SimtGeom<KVT, D, G>::kCtasPerSm
   }
   const int n = min(P, keys - start);  // tokens of this partition
   const int nblk = (n + kBlockSize - 1) / kBlockSize;
-  const int32_t* table = p.block_tables + (size_t)seq * p.max_blocks_per_seq + start / kBlockSize;
+  const int32_t* table =
+      p.block_tables + (size_t)seq * p.max_blocks_per_seq + (kstart + start) / kBlockSize;
+  // first visible key of this partition
+  const int f0 = kMods && part == 0 ? front : 0;
+  __shared__ float s_slope[kMods ? G : 1];
+  if constexpr (kMods) {
+    if (threadIdx.x < G)
+      s_slope[threadIdx.x] = p.alibi && threadIdx.x < p.group
+                                 ? __ldg(p.alibi + kvh * p.group + threadIdx.x) * kLog2e
+                                 : 0.0f;
+  }
 
   if (threadIdx.x == 0) s_abort = 0;
   uint64_t* my_bars = bars + warp * STAGES;
@@ -231,7 +256,15 @@ __global__ void __launch_bounds__(kSimtThreads, (SimtGeom<KVT, D, G>::kCtasPerSm
       const int idx = base + j;
       const int i = idx / G, h = idx % G;
       const int tok = tok0 + r + RPI * i;
-      logits[h * P + tok] = tok < n ? acc[j] : -INFINITY;
+      float sc = acc[j];
+      if constexpr (kMods) {
+        if (p.softcap > 0.0f) sc = p.cap_log2 * cap_tanh(sc / p.cap_log2);
+        if (p.alibi)
+          sc = fmaf(-s_slope[h], fabsf((float)(pos - (kstart + start + tok))), sc);
+        logits[h * P + tok] = tok < n && tok >= f0 ? sc : -INFINITY;
+      } else {
+        logits[h * P + tok] = tok < n ? sc : -INFINITY;
+      }
     }
     __syncwarp();
     if (lane == 0 && issued < ntiles) {
@@ -289,7 +322,7 @@ __global__ void __launch_bounds__(kSimtThreads, (SimtGeom<KVT, D, G>::kCtasPerSm
       for (int i = 0; i < TPL; ++i) {
         const int t = r + RPI * i;
         const int tok = tok0 + t;
-        if (tok < n) {
+        if (tok < n && (!kMods || tok >= f0)) {
           const uint4 w = *reinterpret_cast<const uint4*>(tile + t * ROW + c * 16);
           float vf[EPL];
           to_float(w, vf, KVT());
@@ -349,10 +382,10 @@ __global__ void __launch_bounds__(kSimtThreads, (SimtGeom<KVT, D, G>::kCtasPerSm
   }
 }
 
-template <class QT, class KVT, int D, int G>
+template <class QT, class KVT, int D, int G, bool kMods>
 int launch_simt_one(const AttnParams& p, cudaStream_t stream) {
   const size_t smem = simt_smem_bytes<KVT, D, G>(p.partition);
-  auto kern = paged_attention_simt_kernel<QT, KVT, D, G>;
+  auto kern = paged_attention_simt_kernel<QT, KVT, D, G, kMods>;
   static bool configured = false;  // per instantiation
   if (!configured) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -365,15 +398,15 @@ int launch_simt_one(const AttnParams& p, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-template <class QT, class KVT>
+template <class QT, class KVT, bool kMods = false>
 int launch_simt_typed(const AttnParams& p, int head_dim, int g_pad, cudaStream_t s) {
 #define PKV_G_CASES(DIM)                                      \
   switch (g_pad) {                                            \
-    case 1: return launch_simt_one<QT, KVT, DIM, 1>(p, s);    \
-    case 2: return launch_simt_one<QT, KVT, DIM, 2>(p, s);    \
-    case 4: return launch_simt_one<QT, KVT, DIM, 4>(p, s);    \
-    case 8: return launch_simt_one<QT, KVT, DIM, 8>(p, s);    \
-    case 16: return launch_simt_one<QT, KVT, DIM, 16>(p, s);  \
+    case 1: return launch_simt_one<QT, KVT, DIM, 1, kMods>(p, s);    \
+    case 2: return launch_simt_one<QT, KVT, DIM, 2, kMods>(p, s);    \
+    case 4: return launch_simt_one<QT, KVT, DIM, 4, kMods>(p, s);    \
+    case 8: return launch_simt_one<QT, KVT, DIM, 8, kMods>(p, s);    \
+    case 16: return launch_simt_one<QT, KVT, DIM, 16, kMods>(p, s);  \
     default: return PKV_ERR_UNSUPPORTED;                      \
   }
   if (head_dim == 64) {

@@ -60,6 +60,16 @@ struct AttnParams {
   // Prefill on E4M3 caches: per (query row, head) scale s of the split query
   // (q / s = hi + lo, both E4M3), [rows][num_heads]; null otherwise.
   const float* q8_scale;
+  // Score modifiers and key intervals (the biased entry points; all zero in
+  // plain calls, whose kernels do not read them).
+  int mods;                       // 1: the fields below apply
+  int max_context;                // the caller's bound of context_lens
+  float softcap;                  // scores become softcap * tanh(score / softcap); 0: as they are
+  float cap_log2;                 // softcap * log2(e)
+  const float* alibi;             // [num_heads] slopes of the distance bias, or null
+  int window;                     // keys a row sees up to itself; 0: all
+  const int32_t* key_start;       // [num_rows] first key of each row, or null
+  const int32_t* bidir_lens;      // [num_seqs] keys every query of a chunk sees, or null
 };
 
 // Limit of the launch's device-side waits.
@@ -76,6 +86,27 @@ int launch_reshape_and_cache(const void* k, const void* v, void* k_cache, void* 
                              float k_scale, float v_scale, uint32_t* errors,
                              cudaStream_t stream);
 
+int launch_step_maps(int32_t* block_tables, int32_t* context_lens, int32_t* query_start_loc,
+                     int64_t* slot_mapping, int32_t* positions, int32_t* request_tables,
+                     const int32_t* rows, const int32_t* cached_lens, const int32_t* q_lens,
+                     const int32_t* new_blocks, int num_seqs, int num_rows, int max_blocks,
+                     int num_tokens, int num_new, int num_blocks, uint32_t* errors,
+                     cudaStream_t stream);
+
+struct RotaryArgs {
+  void* q_out;
+  const void *q, *k, *v;
+  void *k_cache, *v_cache;
+  const int64_t* slot_mapping;
+  const int32_t* positions;
+  long long q_stride, k_stride, v_stride;  // elements between tokens
+  int num_tokens, num_heads, num_kv_heads, head_dim, num_blocks, rotary_dim;
+  int layout, src_dtype, cache_dtype;
+  float attn_factor, k_scale, v_scale;
+  uint32_t* errors;
+};
+int launch_rotary_and_cache(const RotaryArgs& a, const double* inv_freq, cudaStream_t stream);
+
 // CUDA-core paged attention (any group size up to 16) plus the merge of
 // partitions when p.max_parts > 1.  g_pad is the group size rounded up to a
 // power of two.
@@ -87,6 +118,11 @@ int launch_simt_f16_f16(const AttnParams& p, int head_dim, int g_pad, cudaStream
 int launch_simt_f16_e4m3(const AttnParams& p, int head_dim, int g_pad, cudaStream_t s);
 int launch_simt_bf16_bf16(const AttnParams& p, int head_dim, int g_pad, cudaStream_t s);
 int launch_simt_bf16_e4m3(const AttnParams& p, int head_dim, int g_pad, cudaStream_t s);
+// The same under score modifiers (p.mods).
+int launch_simt_mods_f16_f16(const AttnParams& p, int head_dim, int g_pad, cudaStream_t s);
+int launch_simt_mods_f16_e4m3(const AttnParams& p, int head_dim, int g_pad, cudaStream_t s);
+int launch_simt_mods_bf16_bf16(const AttnParams& p, int head_dim, int g_pad, cudaStream_t s);
+int launch_simt_mods_bf16_e4m3(const AttnParams& p, int head_dim, int g_pad, cudaStream_t s);
 
 // tcgen05 grouped-query decode (head_dim 128, 16-bit or E4M3 caches, 2..16
 // heads per KV head, 512-token partitions, decode rows only).

@@ -1,0 +1,98 @@
+// Modified scores and key intervals of the biased attention calls.
+//
+// A query at position pos sees the keys lo <= j < hi of its sequence,
+//   lo = max(key_start[row], pos - window + 1, 0),  hi = max(pos + 1, prefix),
+// with scores s' = cap tanh(s / cap) - slope |pos - j|.  Everything is kept in
+// base-2 units (times log2 e), as in the plain kernels.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace pkv {
+
+// Keys of one query row.  hi < 0: the row belongs to no sequence and is left
+// as it is; lo == hi: it sees nothing and its output is zero.
+struct RowKeys {
+  int seq, pos, lo, hi;
+};
+
+// Interval of a query at position pos of a sequence of ctx tokens.
+__device__ __forceinline__ void key_interval(const AttnParams& p, int row, int pos, int ctx,
+                                             int bidir, int* lo, int* hi) {
+  int h = max(pos + 1, min(bidir, ctx));
+  int l = 0;
+  if (p.key_start) l = max(l, __ldg(p.key_start + row));
+  if (p.window > 0) l = max(l, pos - p.window + 1);
+  *hi = h;
+  *lo = min(l, h);
+}
+
+// Context of sequence s, clamped to the block table and the caller's bound.
+__device__ __forceinline__ int mods_context(const AttnParams& p, int s, bool report) {
+  const int cap = min(p.max_blocks_per_seq * kBlockSize, p.max_context);
+  const int ctx = __ldg(p.context_lens + s);
+  if (ctx >= 0 && ctx <= cap) return ctx;
+  if (report) flag_error(p.errors, PKV_DEVERR_CONTEXT);
+  return ctx < 0 ? 0 : cap;
+}
+
+// A decode row is its sequence's last token; a prefill row is query i of the
+// sequence whose query_start_loc range holds it.
+__device__ __forceinline__ RowKeys mods_row_keys(const AttnParams& p, int row, bool report) {
+  RowKeys r;
+  r.seq = row;
+  if (p.query_start_loc == nullptr) {
+    const int ctx = mods_context(p, row, report);
+    r.pos = ctx - 1;
+    key_interval(p, row, r.pos, ctx, 0, &r.lo, &r.hi);
+    return r;
+  }
+  int lo = 0, hi = p.num_seqs - 1;  // largest s with query_start_loc[s] <= row
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(p.query_start_loc + mid) <= row) lo = mid; else hi = mid - 1;
+  }
+  r.seq = lo;
+  const int q0 = __ldg(p.query_start_loc + lo), q1 = __ldg(p.query_start_loc + lo + 1);
+  r.pos = r.lo = 0;
+  r.hi = -1;
+  if (row < q0 || row >= q1) return r;
+  const int ctx = mods_context(p, lo, report);
+  r.pos = ctx - (q1 - q0) + (row - q0);
+  if (r.pos < 0) {  // more queries than context
+    if (report) flag_error(p.errors, PKV_DEVERR_CONTEXT);
+    r.hi = 0;
+    return r;
+  }
+  key_interval(p, row, r.pos, ctx, p.bidir_lens ? __ldg(p.bidir_lens + lo) : 0, &r.lo, &r.hi);
+  return r;
+}
+
+// First key of a row's partitions: lo rounded down to a whole block.
+__device__ __forceinline__ int first_block_key(int lo) { return lo & ~(kBlockSize - 1); }
+
+// Partitions of a row with interval [lo, hi).
+__device__ __forceinline__ int mods_parts(const AttnParams& p, int lo, int hi) {
+  return hi > lo ? (hi - first_block_key(lo) + p.partition - 1) / p.partition : 0;
+}
+
+// tanh(x) = 1 - 2 / (e^2x + 1) on the MUFU (exponential and reciprocal, absolute
+// error about 2^-23), and x - x^3/3 + 2x^5/15 - 17x^7/315 for |x| < 1/4, where
+// that difference would cancel (truncation 62 x^8 / 2835 relative: below 4e-7).
+// Both sides together are good to about 1e-6 relative, so the capped score is
+// for any cap.  (The one-instruction tanh.approx is good to 2^-11 only: a
+// capped score of 50 would be off by 0.024, its weight by 2 %.)
+__device__ __forceinline__ float cap_tanh(float x) {
+  const float e = fast_exp2(x * (2.0f * kLog2e));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.0f));
+  const float big = fmaf(-2.0f, r, 1.0f);
+  const float x2 = x * x;
+  float poly = fmaf(x2, -17.0f / 315.0f, 2.0f / 15.0f);
+  poly = fmaf(x2, poly, -1.0f / 3.0f);
+  poly = fmaf(x2 * x, poly, x);
+  return fabsf(x) < 0.25f ? poly : big;
+}
+
+}  // namespace pkv
