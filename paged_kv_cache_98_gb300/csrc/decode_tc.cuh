@@ -50,6 +50,16 @@
 // inside the MMA, so the V rows of the MMA step holding that block are not
 // taken from the ring: the tail loader copies them (rows past the context as
 // zeros) into a small buffer of their own, which that one step reads instead.
+//
+// kMods (biased decode): scores are modified and a sequence's keys start at its
+// first visible one (score_mods.cuh).  Its items cover the keys from that key's
+// block on; the keys of the block before it get weight zero, and the MMA step
+// that holds them reads a patched copy of its V rows too (the front patch), so
+// nothing that the row does not see enters a product.  On E4M3 caches P is two
+// E4M3 terms, p = hi + lo, in separate rows of the same MMA (its N side was half
+// empty): one term alone is good to 2^-4, 2 % of the output's norm, both to 2^-8,
+// as bf16; and the query's scale is a power of two, so that hi + lo holds a bf16
+// query exactly.
 
 #ifndef PKV_DECODE_TC_CUH
 #define PKV_DECODE_TC_CUH
@@ -64,6 +74,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "rows.cuh"
+#include "score_mods.cuh"
 #include "tc.cuh"
 
 namespace pkv {
@@ -82,14 +93,15 @@ constexpr int kTilesPerPart = kPart / kTileKeys;
 constexpr int kD = 128;
 constexpr int kHalfBytes = kTileKeys * 128;       // 16 KB: 128 rows x 128 B
 constexpr int kPGroupStride = (kPart / 8) * 128;  // 8 KB between 8-head groups of 16-bit P
-constexpr int kMaxSeqs = 1024;                    // sequences per launch (host chunks more)
+// sequences per launch (host chunks more); the biased form also holds their first keys
+constexpr int max_seqs(bool mods) { return mods ? 512 : 1024; }
 constexpr int kLenBits = 9;                       // seq_pack: start << 9 | (last length - 1)
 constexpr int kTailBytes = 4096;                  // one MMA K step of V rows
 
 // With at most 8 heads (G16 false) the 16-bit Q and P keep 8 rows and the
 // descriptors' 8-row group stride is 0 (rows 8-15 alias rows 0-7; their
 // products are never read); the E4M3 Q holds the hi rows, then the lo rows.
-template <bool G16, bool FP8>
+template <bool G16, bool FP8, bool kMods = false>
 struct Layout {
   static constexpr int kTileBytes = FP8 ? kTileKeys * kD : kTileKeys * kD * 2;
   // 16-bit, at most 8 heads: three K and three V stages of 32 KB.  A clock64
@@ -98,27 +110,31 @@ struct Layout {
   // latency per two tiles) while the V stream kept up; 3 + 3 took the call
   // from 0.1715 to 0.1563 ms, 4 + 2 to 0.162 ms.
   static constexpr int kKStages = FP8 ? 4 : (G16 ? 2 : 3);
-  static constexpr int kVStages = FP8 ? (G16 ? 7 : 8) : 3;
+  static constexpr int kVStages = FP8 ? (G16 ? (kMods ? 6 : 7) : 8) : 3;
   static constexpr int kRows = G16 ? 16 : 8;               // query heads held (Q / P rows)
   static constexpr int kQRows = FP8 ? 2 * kRows : kRows;   // E4M3: hi rows, then lo rows
   static constexpr int kQHalf = kRows * 128;               // one 64-dim half of 16-bit Q
   static constexpr int kQBytes = FP8 ? kQRows * 128 : 2 * kQHalf;
   static constexpr int kQSbo = (FP8 || G16) ? 1024 : 0;
   static constexpr int kSCols = FP8 ? kQRows : 16;         // score columns per key tile
+  // E4M3 under modifiers: hi rows of P, then lo rows
+  static constexpr bool kSplitP = FP8 && kMods;
+  static constexpr int kPRows = kSplitP ? 2 * kRows : kRows;
+  static constexpr int kOCols = kPRows > 16 ? kPRows : 16;  // N of the P.V MMAs
   static constexpr int kOCol = kTilesPerPart * kSCols;     // first O^T column of an item
-  static constexpr int kBufCols = kOCol + 16 <= 128 ? 128 : 256;
+  static constexpr int kBufCols = kOCol + kOCols <= 128 ? 128 : 256;
   static constexpr int kTmemCols = 2 * kBufCols;           // two items in flight
   static constexpr int kPElem = FP8 ? 1 : 2;               // P bytes per element
-  static constexpr int kPBytes = kRows * kPart * kPElem;
-  static constexpr int kPSbo = G16 ? (kPart / (16 / kPElem)) * 128 : 0;
+  static constexpr int kPBytes = kPRows * kPart * kPElem;
+  static constexpr int kPSbo = kPRows > 8 ? (kPart / (16 / kPElem)) * 128 : 0;
   // keys of one PV MMA step (16 for 16-bit, 32 for 8-bit operands)
   static constexpr int kStepKeys = FP8 ? 32 : 16;
   static constexpr int kRowBytes = FP8 ? kD : 2 * kD;      // one cache row
 };
 
-template <bool G16, bool FP8>
+template <bool G16, bool FP8, bool kMods = false>
 struct Smem {
-  using L = Layout<G16, FP8>;
+  using L = Layout<G16, FP8, kMods>;
   // every TMA destination / MMA operand sits on a 1024-byte boundary (the
   // 128-byte swizzle repeats every 8 rows of 128 bytes)
   alignas(1024) uint8_t kring[L::kKStages][L::kTileBytes];
@@ -148,16 +164,21 @@ struct Smem {
   uint64_t pv_done;
   // per sequence: first (sequence, partition) pair << 9 | (keys of its last
   // partition - 1); entry [S] holds the total << 9
-  int seq_pack[kMaxSeqs + 1];
+  int seq_pack[max_seqs(kMods) + 1];
+  int seq_lo[kMods ? max_seqs(true) : 1];  // first visible key
   int scan[12];  // per-warp partial sums
   uint32_t tmem_base;
   int abort;
 };
 
+// Keys of a sequence's last partition, from its seq_pack entry.
+__device__ __forceinline__ int last_len(int pack) { return (pack & ((1 << kLenBits) - 1)) + 1; }
+
 struct Item {
   int seq, kvh, part, nparts, n, ntiles;
   int kstart;  // first key of the sequence's own part (cascade decode: after its shared prefix)
   int slot;    // partial slot of this partition
+  int front;   // keys of the item before the first visible one (kMods; 0..15)
 };
 
 // Context of sequence s, clamped to the block table and the launched partitions.
@@ -199,7 +220,7 @@ __device__ __forceinline__ Cursor first_cursor(const AttnParams& p, int first, i
   return c;
 }
 
-template <class SM>
+template <bool kMods = false, class SM>
 __device__ __forceinline__ bool next_item(const AttnParams& p, const SM& sm, Cursor& c,
                                           int total, Item& it, int stride) {
   if (c.k >= total) return false;
@@ -229,7 +250,12 @@ __device__ __forceinline__ bool next_item(const AttnParams& p, const SM& sm, Cur
   it.ntiles = (it.n + kTileKeys - 1) / kTileKeys;
   it.kstart = 0;
   it.slot = it.part;
-  if (p.prefix_lens != nullptr) {  // cascade decode: the keys after the shared prefix
+  it.front = 0;
+  if constexpr (kMods) {
+    const int first = sm.seq_lo[lo];
+    it.kstart = first_block_key(first);
+    if (it.part == 0) it.front = first - it.kstart;
+  } else if (p.prefix_lens != nullptr) {  // cascade decode: the keys after the shared prefix
     it.kstart = cascade_prefix(p, lo, clamped_keys(p, lo, false), false);
     it.slot += cascade_slots(p, it.kstart);
   }
@@ -254,7 +280,8 @@ constexpr int kFewKeys = 32;
 // query head) row, 32 dimensions each; unit u of rows x heads x 4: lane
 // quarter u % 4, head (u / 4) % H, sequence (u / 4) / H.  Keys in a block
 // outside the pool count as zero vectors (the main pass flags them).
-template <class QT, bool FP8, class SM>
+// (kMods: the visible keys, from the first one on, with the modified scores.)
+template <class QT, bool FP8, class SM, bool kMods = false>
 __device__ __noinline__ void few_key_rows(const AttnParams& p, const SM& sm, int first,
                                           int stride) {
   using T = typename QT::T;
@@ -269,8 +296,14 @@ __device__ __noinline__ void few_key_rows(const AttnParams& p, const SM& sm, int
     const int s = (int)(ru / H);
     const int pk = sm.seq_pack[s];
     if ((sm.seq_pack[s + 1] >> kLenBits) - (pk >> kLenBits) != 1) continue;
-    const int keys = (pk & ((1 << kLenBits) - 1)) + 1;
-    if (keys > kFewKeys) continue;
+    int keys = (pk & ((1 << kLenBits) - 1)) + 1, j0 = 0;
+    float slope = 0.0f;
+    if constexpr (kMods) {
+      j0 = sm.seq_lo[s];
+      keys += first_block_key(j0);  // end of the context
+      if (p.alibi) slope = __ldg(p.alibi + h) * kLog2e;
+    }
+    if (keys - j0 > kFewKeys) continue;
     const int kvh = h / p.group;
     float qf[32];
     const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
@@ -281,7 +314,7 @@ __device__ __noinline__ void few_key_rows(const AttnParams& p, const SM& sm, int
 #pragma unroll
     for (int d = 0; d < 32; ++d) acc[d] = 0.0f;
     constexpr int kElem = FP8 ? 1 : 2;
-    for (int j = 0; j < keys; ++j) {
+    for (int j = j0; j < keys; ++j) {
       const int blk = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + j / kBlockSize);
       const bool bok = blk >= 0 && blk < p.num_blocks;
       const size_t off = ((((size_t)(bok ? blk : 0) * p.num_kv_heads + kvh) * kBlockSize +
@@ -300,7 +333,11 @@ __device__ __noinline__ void few_key_rows(const AttnParams& p, const SM& sm, int
       }
       dot += __shfl_xor_sync(gmask, dot, 1);
       dot += __shfl_xor_sync(gmask, dot, 2);
-      const float sc = dot * p.q_scale;  // base 2 (with k_scale for E4M3)
+      float sc = dot * p.q_scale;  // base 2 (with k_scale for E4M3)
+      if constexpr (kMods) {
+        if (p.softcap > 0.0f) sc = p.cap_log2 * cap_tanh(sc / p.cap_log2);
+        sc = fmaf(-slope, (float)(keys - 1 - j), sc);
+      }
       if (sc > m) {
         const float a = exp2f(m - sc);
         l *= a;
@@ -367,12 +404,12 @@ __device__ __forceinline__ bool all_softmax(bool ok) { return all_of_group<1>(ok
 // (at least the group size): 4 for groups of at most 4 query heads, which
 // halves its exponentials, shuffles and P stores against the 8 rows Q and P
 // hold; the rows past kH keep the zeros P starts with.
-template <class QT, bool G16, bool FP8, int kCta, int kH = (G16 ? 16 : 8)>
+template <class QT, bool G16, bool FP8, int kCta, int kH = (G16 ? 16 : 8), bool kMods = false>
 __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorMap& tm_k,
                                             const CUtensorMap& tm_v, const CUtensorMap& tm_q,
                                             int kv_rows, int cta, int ncta, uint8_t* smem_raw) {
   static_assert(kCta >= tc_threads(G16, FP8) && kCta <= 384 && kCta % 32 == 0, "CTA size");
-  using L = Layout<G16, FP8>;
+  using L = Layout<G16, FP8, kMods>;
   static_assert(kH % 2 == 0 && kH <= L::kRows, "heads of the softmax");
   constexpr int KS = L::kKStages, VS = L::kVStages;
   constexpr int kThreads = kCta;
@@ -381,7 +418,8 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
   constexpr int kWarpK1 = kProd == 2 ? 8 : -1;
   constexpr int kWarpV1 = kProd == 2 ? 9 : -1;
   constexpr int kWarpPV = tc_split_mma(FP8) ? tc_threads(G16, FP8) / 32 - 1 : -1;
-  Smem<G16, FP8>& sm = *reinterpret_cast<Smem<G16, FP8>*>(
+  using SM = Smem<G16, FP8, kMods>;
+  SM& sm = *reinterpret_cast<SM*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // partials and a merge: several partitions, or cascade decode (prefix partials)
@@ -389,7 +427,7 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
   // kind::f16 (16-bit operands: 0 f16, 1 bf16) or kind::f8f6f4 (0 = E4M3)
   constexpr uint32_t kAB = (!FP8 && std::is_same<QT, BF16>::value) ? 1u : 0u;
   constexpr uint32_t kIdescS = tc::idesc_f16(kAB, 0, 0, 128, L::kSCols);
-  constexpr uint32_t kIdescO = tc::idesc_f16(kAB, 1, 0, 128, 16);
+  constexpr uint32_t kIdescO = tc::idesc_f16(kAB, 1, 0, 128, L::kOCols);
 
   // ---- set-up -------------------------------------------------------------------------
   if (threadIdx.x == 0) {
@@ -436,8 +474,14 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
     const int chunk = (S + kThreads - 1) / kThreads;
     // keys of the sequence's own part (cascade decode: those after its shared prefix)
     auto keys_of = [&](int sq, bool report) {
-      const int keys = clamped_keys(p, sq, report);
-      return keys - cascade_prefix(p, sq, keys, report);
+      if constexpr (kMods) {
+        const RowKeys rk = mods_row_keys(p, sq, report);
+        sm.seq_lo[sq] = rk.lo;
+        return rk.hi > rk.lo ? rk.hi - first_block_key(rk.lo) : 0;
+      } else {
+        const int keys = clamped_keys(p, sq, report);
+        return keys - cascade_prefix(p, sq, keys, report);
+      }
     };
     int local = 0;
     for (int i = 0; i < chunk; ++i) {
@@ -547,11 +591,11 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
       return true;
     };
     Item cur, nxt;
-    bool has = next_item(p, sm, idx, total, cur, ncta);
+    bool has = next_item<kMods>(p, sm, idx, total, cur, ncta);
     int row_cur = has ? block_row(cur) : kv_rows;
     while (has && ok) {
       // block rows are read one item ahead of their first use
-      const bool has_n = next_item(p, sm, idx, total, nxt, ncta);
+      const bool has_n = next_item<kMods>(p, sm, idx, total, nxt, ncta);
       const int row_nxt = has_n ? block_row(nxt) : kv_rows;
       if (!is_v && pi == 0) ok = load_q(cur, it);
       if (ok) ok = load_tiles(cur, row_cur);
@@ -627,8 +671,20 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
         const int b = k & 1;
         if (!wait(&sm.p_ready[b], (k >> 1) & 1)) return false;
         // the MMA step that holds the partial block reads the tail buffer
-        const bool has_tail = (x.n & (kBlockSize - 1)) != 0;
-        const int tail_step = has_tail ? ((x.n - 1) % kTileKeys) / L::kStepKeys : -1;
+        // (kMods: and the item's first step, where keys before the first visible
+        // one share it, a front patch of its own unless that step is the same)
+        bool has_tail = (x.n & (kBlockSize - 1)) != 0;
+        int tail_step = has_tail ? ((x.n - 1) % kTileKeys) / L::kStepKeys : -1;
+        const bool has_front = kMods && x.front > 0;
+        const int fslot = ntail & 1;
+        if (has_front) {
+          if (!wait(&sm.v_fixed[ntail & 3], (ntail >> 2) & 1)) return false;
+          ++ntail;
+          if (x.ntiles == 1 && tail_step == 0) {
+            has_tail = false;
+            tail_step = -1;
+          }
+        }
         const int slot = ntail & 1;
         if (has_tail) {
           if (!wait(&sm.v_fixed[ntail & 3], (ntail >> 2) & 1)) return false;
@@ -637,6 +693,7 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
         tc::fence_after_sync();
         const uint32_t pa = smem_u32(&sm.pmat[b][0]);
         const uint32_t ta = smem_u32(&sm.tail[slot][0]);
+        const uint32_t fa = smem_u32(&sm.tail[fslot][0]);
         const uint32_t d = tmem + b * L::kBufCols + L::kOCol;
         for (int t = 0; t < x.ntiles; ++t, ++vpos) {
           const int st = vpos % VS;
@@ -650,7 +707,8 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
             if (leader) {
 #pragma unroll
               for (int kk = 0; kk < kTileKeys / 32; ++kk) {
-                const uint32_t a = kk == ts ? ta : va + kk * (32 * 128);
+                uint32_t a = kk == ts ? ta : va + kk * (32 * 128);
+                if (kMods && kk == 0 && t == 0 && has_front) a = fa;
                 tc::mma_f8(d, tc::smem_desc(a, 16, 1024, tc::kLayoutSw128),
                            tc::smem_desc(pa + (t * (kTileKeys / 16) + kk * 2) * 128, 128,
                                          L::kPSbo, tc::kLayoutNone),
@@ -661,9 +719,10 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
             // V^T (MN-major: two 64-dim atoms) x P^T (K-major), 16 keys per instruction
 #pragma unroll
             for (int kk = 0; kk < kTileKeys / 16; ++kk) {
-              const bool tk = kk == ts;
+              const bool fk = kMods && kk == 0 && t == 0 && has_front;
+              const bool tk = kk == ts || fk;
               tc::mma_f16(d,
-                          tc::smem_desc(tk ? ta : va + kk * (16 * 128),
+                          tc::smem_desc(tk ? (fk ? fa : ta) : va + kk * (16 * 128),
                                         tk ? kTailBytes / 2 : kHalfBytes, 1024,
                                         tc::kLayoutSw128),
                           tc::smem_desc(pa + (t * (kTileKeys / 8) + kk * 2) * 128, 128, L::kPSbo,
@@ -673,6 +732,7 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
           }
           commit(&sm.vempty[st]);
         }
+        if (has_front) commit(&sm.tail_free[fslot]);
         if (has_tail) commit(&sm.tail_free[slot]);
         commit(&sm.o_ready[b]);
         return true;
@@ -680,10 +740,10 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
       if (!tc_split_mma(FP8)) {
         // one issuer: S(0), then per item i: S(i+1), P.V(i)
         Item nxt;
-        bool has = next_item(p, sm, idx, total, cur, ncta);
+        bool has = next_item<kMods>(p, sm, idx, total, cur, ncta);
         if (has) ok = mma_s(cur, 0);
         while (has && ok) {
-          const bool has_n = next_item(p, sm, idx, total, nxt, ncta);
+          const bool has_n = next_item<kMods>(p, sm, idx, total, nxt, ncta);
           if (has_n) ok = mma_s(nxt, it + 1);
           if (ok) ok = mma_pv(cur, it);
           cur = nxt;
@@ -692,7 +752,7 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
         }
       } else if (warp == 5) {
         // S of item k goes to TMEM buffer k % 2 once the softmax has read item k - 2's
-        while (ok && next_item(p, sm, idx, total, cur, ncta)) {
+        while (ok && next_item<kMods>(p, sm, idx, total, cur, ncta)) {
           const int b = it & 1;
           if (it >= 2) {
             ok = wait(&sm.s_free[b], ((it - 2) >> 1) & 1);
@@ -702,7 +762,7 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
           ++it;
         }
       } else {
-        while (ok && next_item(p, sm, idx, total, cur, ncta)) ok = mma_pv(cur, it++);
+        while (ok && next_item<kMods>(p, sm, idx, total, cur, ncta)) ok = mma_pv(cur, it++);
       }
       if (!ok && leader) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
       // no MMA of ours may still be running when TMEM is released
@@ -730,11 +790,11 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
     // ring's swizzle.  The slot was last read by the products of item m - 2,
     // whose completion tail_free reports (item m's cannot complete before its
     // v_fixed, so the parity is unambiguous).
-    auto load_tail = [&](const Item& x) -> bool {
-      if ((x.n & (kBlockSize - 1)) == 0) return true;
+    // (kMods: first the step that holds keys before the first visible one, the
+    // same way; one patch serves both where they are the same step)
+    auto load_patch = [&](const Item& x, int key0) -> bool {
       constexpr int kChunksPerRow = L::kRowBytes / 16;
       constexpr int kPer = L::kStepKeys * kChunksPerRow / kGroup;  // 16-B chunks per thread
-      const int key0 = ((x.n - 1) / L::kStepKeys) * L::kStepKeys;  // first key of the step
       const uint8_t* cache = static_cast<const uint8_t*>(p.v_cache);
       uint4 v[kPer];
 #pragma unroll
@@ -742,7 +802,7 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
         const int c = gtid + i * kGroup;
         const int key = key0 + c / kChunksPerRow;
         v[i] = make_uint4(0, 0, 0, 0);
-        if (key < x.n) {
+        if (key < x.n && (!kMods || key >= x.front)) {
           const int blk = __ldg(p.block_tables + (size_t)x.seq * p.max_blocks_per_seq +
                                 x.kstart / kBlockSize + x.part * (kPart / kBlockSize) +
                                 key / kBlockSize);
@@ -773,6 +833,14 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
       if (gtid == 0) mbar_arrive(&sm.v_fixed[m & 3]);
       ++ntail;
       return true;
+    };
+    auto load_tail = [&](const Item& x) -> bool {
+      const int key0 = ((x.n - 1) / L::kStepKeys) * L::kStepKeys;  // first key of the last step
+      if (kMods && x.front > 0) {
+        if (!load_patch(x, 0)) return false;
+        if (key0 == 0) return true;
+      }
+      return (x.n & (kBlockSize - 1)) == 0 || load_patch(x, key0);
     };
     if constexpr (FP8) {
       // Query rows split as q / s = hi + lo (E4M3 each, s = max|q| / 448), hi
@@ -806,8 +874,12 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
         for (int e = 0; e < EPT; ++e) amax = fmaxf(amax, fabsf(f[e]));
 #pragma unroll
         for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-        const float sc = amax > 0.0f ? amax / 448.0f : 1.0f;
-        const float inv = amax > 0.0f ? 448.0f / amax : 1.0f;
+        float sc = amax > 0.0f ? amax / 448.0f : 1.0f;
+        float inv = amax > 0.0f ? 448.0f / amax : 1.0f;
+        if constexpr (kMods) {  // the next power of two
+          sc = __uint_as_float((__float_as_uint(fmaxf(sc, 0x1p-100f)) + 0x7fffffu) & 0xff800000u);
+          inv = 1.0f / sc;
+        }
         uint8_t hi[EPT], lo[EPT];
 #pragma unroll
         for (int e = 0; e < EPT; e += 2) {
@@ -850,15 +922,15 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
       };
       uint4 qbuf[EPT / 8];
       Item cur, nxt, nxt2;
-      bool has = next_item(p, sm, idx, total, cur, ncta);
+      bool has = next_item<kMods>(p, sm, idx, total, cur, ncta);
       if (has) {
         q_fetch(cur, qbuf);
         ok = conv_q(qbuf, 0);
       }
-      bool has_n = has && next_item(p, sm, idx, total, nxt, ncta);
+      bool has_n = has && next_item<kMods>(p, sm, idx, total, nxt, ncta);
       if (has_n) q_fetch(nxt, qbuf);
       while (has && ok) {
-        const bool has_n2 = has_n && next_item(p, sm, idx, total, nxt2, ncta);
+        const bool has_n2 = has_n && next_item<kMods>(p, sm, idx, total, nxt2, ncta);
         if (has_n) {
           ok = conv_q(qbuf, it + 1);
           if (has_n2) q_fetch(nxt2, qbuf);
@@ -872,7 +944,7 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
       }
     } else {
       Item cur;
-      while (ok && next_item(p, sm, idx, total, cur, ncta)) ok = load_tail(cur);
+      while (ok && next_item<kMods>(p, sm, idx, total, cur, ncta)) ok = load_tail(cur);
     }
     if (!ok && gtid == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
   } else if (warp >= tc_threads(G16, FP8) / 32) {
@@ -895,7 +967,7 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
     Cursor idx = first_cursor(p, cta, ncta);
     Item cur, nxt, prev;
     int it = 0;
-    bool has = next_item(p, sm, idx, total, cur, ncta);
+    bool has = next_item<kMods>(p, sm, idx, total, cur, ncta);
 
     auto epilogue = [&](const Item& x, int k) -> bool {
       const int b = k & 1;
@@ -904,14 +976,26 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
       tc::fence_after_sync();
       float o[16];
       tc::tmem_ld16(tmem + lane_off + b * L::kBufCols + L::kOCol, o);
-      tc::tmem_wait_ld();
+      if constexpr (L::kSplitP && G16) {  // the lo rows' products
+        float lo16[16];
+        tc::tmem_ld16(tmem + lane_off + b * L::kBufCols + L::kOCol + 16, lo16);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < kH; ++h) o[h] += lo16[h];
+      } else {
+        tc::tmem_wait_ld();
+        if constexpr (L::kSplitP) {
+#pragma unroll
+          for (int h = 0; h < kH; ++h) o[h] += o[h + 8];
+        }
+      }
       tc::fence_before_sync();
       const int d = tid;
       // one partition and no shared prefix: straight to out
       const bool direct = !split || (x.nparts == 1 && p.prefix_lens == nullptr);
       const size_t head0 = (size_t)x.seq * p.num_heads + (size_t)x.kvh * p.group;
       // rows with few keys (always direct) are recomputed after the loop
-      const bool few = x.nparts == 1 && p.prefix_lens == nullptr && x.n <= kFewKeys;
+      const bool few = x.nparts == 1 && p.prefix_lens == nullptr && x.n - x.front <= kFewKeys;
       if (direct) {
         if (few) return true;
         OutT* dst = static_cast<OutT*>(p.out) + head0 * kD + d;
@@ -932,7 +1016,7 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
     bool have_prev = false;
     bool ok = true;
     while (has) {
-      const bool has_n = next_item(p, sm, idx, total, nxt, ncta);
+      const bool has_n = next_item<kMods>(p, sm, idx, total, nxt, ncta);
       const int b = it & 1;
       ok = all_softmax(wait_bar(&sm.s_ready[b], (it >> 1) & 1, abort, lim));
       if (!ok) break;
@@ -981,6 +1065,34 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
       float mx[16];
 #pragma unroll
       for (int h = 0; h < kH; ++h) mx[h] = -INFINITY;
+      if constexpr (kMods) {
+        // modified scores in base-2 units, tile by tile; the modifiers' tests are
+        // uniform over the launch
+        const float icap = p.softcap > 0.0f ? 1.0f / p.cap_log2 : 0.0f;
+        float slope[kH];
+#pragma unroll
+        for (int h = 0; h < kH; ++h)
+          slope[h] = p.alibi && h < p.group ? __ldg(p.alibi + cur.kvh * p.group + h) * kLog2e : 0.0f;
+        // distance of this thread's first key from the query, the context's last token
+        const int dist0 =
+            (cur.nparts - 1 - cur.part) * kPart + last_len(sm.seq_pack[cur.seq]) - 1 - tid;
+#pragma unroll
+        for (int t = 0; t < kTilesPerPart; ++t) {
+          if (t < cur.ntiles) {
+            const int key = t * kTileKeys + tid;
+            const bool valid = key < cur.n && key >= cur.front;
+            const float dist = (float)(dist0 - t * kTileKeys);
+#pragma unroll
+            for (int h = 0; h < kH; ++h) {
+              float x = s[t][h] * (FP8 ? qsh[h] : qs);
+              if (p.softcap > 0.0f) x = p.cap_log2 * cap_tanh(x * icap);
+              if (p.alibi) x = fmaf(-slope[h], dist, x);
+              s[t][h] = valid ? x : -INFINITY;
+              mx[h] = fmaxf(mx[h], s[t][h]);
+            }
+          }
+        }
+      } else {
 #pragma unroll
       for (int t = 0; t < kTilesPerPart; ++t) {
         const bool valid = t < cur.ntiles && t * kTileKeys + tid < cur.n;
@@ -989,6 +1101,7 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
           s[t][h] = valid ? s[t][h] * (FP8 ? qsh[h] : qs) : -INFINITY;
           mx[h] = fmaxf(mx[h], s[t][h]);
         }
+      }
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1)
@@ -1028,6 +1141,16 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
               uint8_t* c8 = pm + (key >> 4) * 128 + (h >> 3) * L::kPSbo + (h & 7) * 16 + (key & 15);
               c8[0] = (uint8_t)(q2 & 0xffu);
               c8[16] = (uint8_t)(q2 >> 8);
+              if constexpr (L::kSplitP) {  // what the hi term leaves, in the lo rows
+                __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(q2, __NV_E4M3);
+                const float2 hv = __half22float2(*reinterpret_cast<__half2*>(&hr));
+                const __nv_fp8x2_storage_t r2 = __nv_cvt_float2_to_fp8x2(
+                    make_float2(fmaf(e0, 256.0f, -hv.x), fmaf(e1, 256.0f, -hv.y)), __NV_SATFINITE,
+                    __NV_E4M3);
+                uint8_t* l8 = c8 + (L::kRows >> 3) * L::kPSbo;
+                l8[0] = (uint8_t)(r2 & 0xffu);
+                l8[16] = (uint8_t)(r2 >> 8);
+              }
             } else {
               uint32_t pr;
               if constexpr (std::is_same<QT, BF16>::value) {
@@ -1079,7 +1202,8 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
     }
     if (ok && have_prev) ok = epilogue(prev, it - 1);
     if (!ok && tid == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
-    if (ok && p.prefix_lens == nullptr) few_key_rows<QT, FP8>(p, sm, cta * 128 + tid, ncta * 128);
+    if (ok && p.prefix_lens == nullptr)
+      few_key_rows<QT, FP8, SM, kMods>(p, sm, cta * 128 + tid, ncta * 128);
   }
 
   tc::fence_before_sync();

@@ -134,6 +134,9 @@ bool tc_decode_supported(const AttnParams& p, int q_dtype, int kv_dtype, int hea
 int launch_paged_decode_tc(const AttnParams& p, int q_dtype, int kv_dtype, cudaStream_t stream,
                            bool dependent = false);
 
+// The same under score modifiers (p.mods).
+int launch_paged_decode_mods(const AttnParams& p, int q_dtype, int kv_dtype, cudaStream_t stream);
+
 // tcgen05 chunked-prefill attention (head_dim 128, 16-bit caches, 128 % g == 0).
 bool tc_prefill_supported(const AttnParams& p, int q_dtype, int kv_dtype, int head_dim);
 int launch_prefill_tc(const AttnParams& p, int q_dtype, int total_q, cudaStream_t stream);

@@ -148,7 +148,7 @@ int launch_mixed_typed(const AttnParams& pd, const AttnParams& pp, int total_q, 
 bool tc_mixed_supported(const AttnParams& pd, const AttnParams& pp, int q_dtype, int kv_dtype,
                         int head_dim) {
   if (kv_dtype != q_dtype || pd.group > 8) return false;
-  if (pd.num_rows > dec_tc::kMaxSeqs || pp.num_seqs > pre_tc::kMaxSeqs) return false;
+  if (pd.num_rows > dec_tc::max_seqs(false) || pp.num_seqs > pre_tc::kMaxSeqs) return false;
   return tc_decode_supported(pd, q_dtype, kv_dtype, head_dim) &&
          tc_prefill_supported(pp, q_dtype, kv_dtype, head_dim);
 }

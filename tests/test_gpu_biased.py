@@ -9,7 +9,7 @@ round:
     far below the row's largest can vanish: 2^-17 of B = sum_j |v_j| / l, l the
     sum of the weights over the largest one;
   - the scores, by at most d, which moves a weight by 2 d relative, so 2 d A:
-    fp32 products and sums (D + 8) 2^-24 S, S the row's largest scale sum |q||k|
+    fp32 products and sums (D + 8) 2^-24 S, S the row's largest |scale| sum |q||k|
     plus its bias; the cap 2^-19 of the score; exponentials 2^-21; an E4M3 cache's
     query, split in two E4M3 terms, 2^-8 S.
 The sums of all three are taken with 1 % for their products.
@@ -131,7 +131,9 @@ class Batch:
                 q = self.q[row].double().view(self.hkv, g, self.D)
                 k, v = self.k[s][a:b].transpose(0, 1), self.v[s][a:b].transpose(0, 1)  # [hkv, n, D]
                 x = self.scale * torch.einsum("hgd,hnd->hgn", q, k)
-                size = self.scale * torch.einsum("hgd,hnd->hgn", q.abs(), k.abs())
+                # S is a magnitude: |scale| (a negative scale would make d negative, and the
+                # bound smaller than the rounding of the weights alone)
+                size = abs(self.scale) * torch.einsum("hgd,hnd->hgn", q.abs(), k.abs())
                 cap = 0.0
                 if self.softcap:
                     x = self.softcap * torch.tanh(x / self.softcap)
