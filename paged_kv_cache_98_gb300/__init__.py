@@ -423,9 +423,12 @@ def copy_blocks(k_cache, v_cache, block_pairs, device_errors=None, stream=None):
 
 
 def _on_device(device, stream, *tensors):
-    """The stream a call launches on, after checking that its tensors are on `device`.
+    """(stream, guard) of a call whose tensors must be on `device`: the stream it
+    launches on, and a context that makes `device` the current one.
 
-    Returns (stream, None), or (stream, guard) when `device` is not the current one."""
+    On another stream than the current one the tensors are marked as used there,
+    so that the allocator does not hand out their memory before the launch has
+    run; ordering that stream behind the work that fills them stays the caller's."""
     for t in tensors:
         if t is not None and t.device != device:
             raise ValueError("tensors must be on the same CUDA device")
@@ -435,6 +438,10 @@ def _on_device(device, stream, *tensors):
         stream = torch.cuda.current_stream(device)
     elif stream.device != device:
         raise ValueError("the stream belongs to another device than the tensors")
+    elif stream != torch.cuda.current_stream(device):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
     away = device.index is not None and device.index != torch.cuda.current_device()
     return stream, (torch.cuda.device(device) if away else contextlib.nullcontext())
 
@@ -485,7 +492,7 @@ def build_step_maps(block_tables, context_lens, query_start_loc, slot_mapping, p
     _want("cached_lens", cached_lens, torch.int32, (S,))
     _want("q_lens", q_lens, torch.int32, (S,))
     _want("new_blocks", new_blocks, torch.int32, (new_blocks.numel(),))
-    stream, guard = _on_device(request_tables.device, stream, block_tables, context_lens,
+    stream, guard = _on_device(request_tables.device, stream, request_tables, block_tables, context_lens,
                                query_start_loc, slot_mapping, positions, rows, cached_lens, q_lens,
                                new_blocks, device_errors)
     with guard:
@@ -545,7 +552,7 @@ def rotary_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, 
     _want("positions", positions, torch.int32, (T,))
     for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
         _want(name, c, k_cache.dtype, (k_cache.shape[0], hkv, k_cache.shape[2], D))
-    stream, guard = _on_device(q.device, stream, q_out, k, v, k_cache, v_cache, slot_mapping,
+    stream, guard = _on_device(q.device, stream, q_out, q, k, v, k_cache, v_cache, slot_mapping,
                                positions, device_errors)
     # (a single token's stride is never stepped)
     qs, ks, vs = (t.stride(0) if T > 1 else h * D for t, h in ((q, H), (k, hkv), (v, hkv)))
@@ -603,7 +610,7 @@ def paged_attention_decode_biased(out, q, k_cache, v_cache, block_tables, contex
     nb, hkv, bs, _ = k_cache.shape
     if context_lens.numel() != S:
         raise ValueError("context_lens must have one entry per query row")
-    stream, guard = _on_device(q.device, stream, out, k_cache, v_cache, block_tables, context_lens,
+    stream, guard = _on_device(q.device, stream, out, q, k_cache, v_cache, block_tables, context_lens,
                                alibi_slopes, key_start, device_errors)
     if max_context_len is None:
         max_context_len = int(context_lens.max().item()) if S else 0
@@ -645,7 +652,7 @@ def paged_attention_prefill_biased(out, q, k_cache, v_cache, block_tables, conte
     nb, hkv, bs, _ = k_cache.shape
     S = context_lens.numel()
     _want("query_start_loc", query_start_loc, torch.int32, (S + 1,))
-    stream, guard = _on_device(q.device, stream, out, k_cache, v_cache, block_tables, context_lens,
+    stream, guard = _on_device(q.device, stream, out, q, k_cache, v_cache, block_tables, context_lens,
                                query_start_loc, alibi_slopes, key_start, prefix_lens, device_errors)
     if max_context_len is None:
         max_context_len = int(context_lens.max().item()) if S else 0

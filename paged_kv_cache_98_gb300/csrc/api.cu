@@ -615,6 +615,9 @@ size_t pkv_prefill_biased_workspace_size(int num_seqs, int total_q, int num_head
   if (num_seqs <= 0 || total_q <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       max_context_len < 0)
     return 0;
+  // tensor cores: the split query of an E4M3 cache; CUDA cores: split-K partials
+  if (head_dim == 128)
+    return kv_dtype == PKV_FP8_E4M3 ? pkv::prefill_q8_bytes(total_q, num_heads) : 0;
   return split_workspace((size_t)total_q, num_heads, head_dim,
                          parts_for(max_context_len, kDefaultPartition));
 }
@@ -658,6 +661,15 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
   p.max_parts = parts_for(max_context_len, kDefaultPartition);
   if (p.max_parts > 16384) return PKV_ERR_UNSUPPORTED;
   p.errors = device_errors;
+  if (head_dim == 128) {
+    if (!pkv::prefill_mods_supported(p, head_dim)) return PKV_ERR_UNSUPPORTED;
+    const bool fp8 = kv_dtype == PKV_FP8_E4M3;
+    p.q_scale = scale * pkv::kLog2e * (fp8 ? k_scale : 1.0f);
+    p.v_scale = fp8 ? v_scale : 1.0f;
+    pkv::take_debug_hook(p);
+    return pkv::launch_prefill_mods(p, q_dtype, kv_dtype, total_q, workspace, workspace_bytes,
+                                    static_cast<cudaStream_t>(stream));
+  }
   const size_t need = split_workspace((size_t)total_q, num_heads, head_dim, p.max_parts);
   return run_attention(p, q_dtype, kv_dtype, head_dim, scale, k_scale, v_scale, workspace, need,
                        workspace_bytes, static_cast<cudaStream_t>(stream));

@@ -77,22 +77,28 @@ __device__ __forceinline__ int mods_parts(const AttnParams& p, int lo, int hi) {
   return hi > lo ? (hi - first_block_key(lo) + p.partition - 1) / p.partition : 0;
 }
 
+// tanh(x) for |x| <= kTanhPoly as x + x^3 q(x^2), q of degree 3: its coefficients
+// minimise the largest relative error there (iteratively reweighted least
+// squares on Chebyshev points); with fp32 rounding 8e-7 relative.
+constexpr float kTanhPoly = 0.75f;
+constexpr float kTanh3 = -0.333296686f, kTanh5 = 0.132682368f, kTanh7 = -0.0502779521f,
+                kTanh9 = 0.0131058358f;
+__device__ __forceinline__ float tanh_poly(float x) {
+  const float x2 = x * x;
+  const float q = fmaf(x2, fmaf(x2, fmaf(x2, kTanh9, kTanh7), kTanh5), kTanh3);
+  return fmaf(x2 * x, q, x);
+}
+
 // tanh(x) = 1 - 2 / (e^2x + 1) on the MUFU (exponential and reciprocal, absolute
-// error about 2^-23), and x - x^3/3 + 2x^5/15 - 17x^7/315 for |x| < 1/4, where
-// that difference would cancel (truncation 62 x^8 / 2835 relative: below 4e-7).
-// Both sides together are good to about 1e-6 relative, so the capped score is
-// for any cap.  (The one-instruction tanh.approx is good to 2^-11 only: a
-// capped score of 50 would be off by 0.024, its weight by 2 %.)
+// error about 2^-23), the polynomial where that difference would cancel.  Both
+// are good to 1e-6 relative, so the capped score is for any cap.  (The one-
+// instruction tanh.approx is good to 2^-11 only: a capped score of 50 would be
+// off by 0.024, its weight by 2 %.)
 __device__ __forceinline__ float cap_tanh(float x) {
   const float e = fast_exp2(x * (2.0f * kLog2e));
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.0f));
-  const float big = fmaf(-2.0f, r, 1.0f);
-  const float x2 = x * x;
-  float poly = fmaf(x2, -17.0f / 315.0f, 2.0f / 15.0f);
-  poly = fmaf(x2, poly, -1.0f / 3.0f);
-  poly = fmaf(x2 * x, poly, x);
-  return fabsf(x) < 0.25f ? poly : big;
+  return fabsf(x) <= kTanhPoly ? tanh_poly(x) : fmaf(-2.0f, r, 1.0f);
 }
 
 }  // namespace pkv
