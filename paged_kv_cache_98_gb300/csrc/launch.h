@@ -157,6 +157,14 @@ bool prefill_mods_supported(const AttnParams& p, int head_dim);
 int launch_prefill_mods(const AttnParams& p, int q_dtype, int kv_dtype, int total_q, void* workspace,
                         size_t workspace_bytes, cudaStream_t stream);
 
+// Its kernels with capped scores, a distance bias, or both (q8: the split query).
+int launch_prefill_cap(const AttnParams& p, int q_dtype, int total_q, const uint8_t* q8,
+                       cudaStream_t stream);
+int launch_prefill_bias(const AttnParams& p, int q_dtype, int total_q, const uint8_t* q8,
+                        cudaStream_t stream);
+int launch_prefill_cap_bias(const AttnParams& p, int q_dtype, int total_q, const uint8_t* q8,
+                            cudaStream_t stream);
+
 // One launch for a mixed batch: pd describes the decode rows (as for
 // launch_paged_decode_tc), pp the prefill chunks (as for launch_prefill_tc);
 // the CTAs are split between the two (prefill_ctas > 0 fixes the chunks'

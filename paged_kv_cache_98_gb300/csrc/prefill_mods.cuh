@@ -1,0 +1,996 @@
+// Biased chunked prefill on the tcgen05 tensor cores (head_dim 128, fp16/bf16 or
+// E4M3 caches, any group size up to 16): capped scores, a distance bias, and an
+// interval of visible keys per query row (score_mods.cuh).  The mathematics and
+// the layouts are those of prefill_tc.cuh; what differs:
+//
+//  * The plain kernel's softmax (one thread per row, 128 scores in registers) is
+//    bound by its own instruction latency: one warp per scheduler works while the
+//    other waits for its MMAs.  Modified scores double its instructions (ncu, a
+//    cap of 50 on the mixed batch's chunks: 51.6 M against 29.1 M, issue slots 42 %
+//    used, no pipe above 34 %), and took 130 us against 80.  Here two threads share
+//    a row, 64 keys each, so that four softmax warps per scheduler hide each other's
+//    latency; the two exchange their maxima through shared memory, one barrier per
+//    tile.
+//  * An item (two query tiles of whole tokens) walks the key tiles from its first
+//    row's first key to its last row's last one; blocks before and behind those are
+//    not read.  64 keys that every row of a warp sees are not masked; 64 that none
+//    sees cost neither scores nor exponentials, only zeros for P.
+//  * A distance bias grows towards the query, so the running max would move, and O
+//    be rescaled, at nearly every tile of a walk towards it; those kernels walk the
+//    tiles from the last one back.
+//  * A key hidden from a row has weight zero, but in the product 0 * inf is NaN: a
+//    row whose output is not finite is computed again from its own keys alone, in
+//    fp32, after the main loop, so that a hidden infinity never reaches it.  Finite
+//    inputs never take that path.
+//  * E4M3 caches: P is two E4M3 terms, p = hi + lo, in two products: one term alone
+//    is good to 2^-4, 2 % of the output's norm, both to 2^-8, as bf16.
+#ifndef PKV_PREFILL_MODS_CUH
+#define PKV_PREFILL_MODS_CUH
+
+#include "prefill_tc.cuh"
+#include "score_mods.cuh"
+
+namespace pkv {
+namespace pre_mods {
+namespace {
+using namespace pre_tc;
+
+// Modifiers that a kernel is built for, as bits: tests in the tile loop instead
+// would have every case pay the registers of all.
+constexpr int kModCap = 1, kModBias = 2;
+
+constexpr int kTileWarps = 4;  // softmax warps of a query tile
+constexpr int kSoftWarps = 2 * kTileWarps;
+constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 1;
+constexpr int kModProd = 3;  // producer warps
+constexpr int kModThreads = 32 * (kSoftWarps + 1 + kModProd);
+// Registers per thread: the launch gives 168 to each of 384 threads; the two softmax
+// warpgroups take over what the third (issuer and producers) returns:
+// 256 * 208 + 128 * 80 <= 384 * 168.
+constexpr int kSoftRegs = 208, kOtherRegs = 80;
+static_assert(32 * kSoftWarps * kSoftRegs + 128 * kOtherRegs <= kModThreads * 168 && kModThreads == 384,
+              "setmaxnreg may only share out what the launch holds");
+constexpr int kChunk = 32;  // keys whose weights are packed and stored together
+// Two E4M3 terms: w <= 2, P holds 128 w.  The headroom that one term spends on
+// fewer rescales goes to small weights here: they keep a code down to 2^-17, and a
+// row's tail of many of them is not lost.
+constexpr float kMove8 = 1.0f;
+constexpr float kPMods8 = 128.0f;
+
+struct ModSmem {
+  alignas(1024) uint8_t ring[kStages][kTileBytes];
+  alignas(1024) uint8_t q[2][kTileBytes];
+  alignas(1024) uint8_t tail[kTailBytes];
+  int seq_start[kMaxSeqs + 1];  // prefix of items per sequence (one KV head's)
+  int seq_qlen[kMaxSeqs];
+  int seq_ctx[kMaxSeqs];
+  int seq_q0[kMaxSeqs];
+  int scan[kModThreads / 32];
+  uint64_t full[kRingBars];
+  uint64_t empty[kRingBars];
+  uint64_t q_full;
+  uint64_t q_empty;
+  uint64_t s_ready[2];  // per query tile
+  uint64_t p_ready[2];
+  uint64_t o_done[2];
+  uint64_t o_free[2];
+  uint64_t tail_full;
+  uint64_t tail_free;
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+  int redo[2];  // a row of this query tile came out not finite
+};
+
+struct ModItem {
+  int seq, kvh, ctx, q0;
+  int bidir;           // keys every query of the sequence sees (0: causal)
+  int t0[2], nt[2];    // first token (within the chunk) and tokens of tiles a, b
+  int pos0[2];         // absolute position of each tile's first token
+  int kt0, nk;         // key tiles [kt0, nk) of the item (nk 0: no row sees a key)
+  int last[2];         // last step of each query tile (-1: its rows see nothing)
+  int lo_block, end_block;  // blocks any row sees
+  int tail_step;       // MMA step of key tile nk - 1 holding the partial last block, else -1
+};
+
+// Steps kt0 .. nk - 1 of an item; the key tile of step i, backwards under a bias.
+template <int kMods>
+__device__ __forceinline__ int tile_of(const ModItem& x, int i) {
+  return (kMods & kModBias) ? x.nk - 1 - (i - x.kt0) : i;
+}
+
+template <int kMods, bool kFP8>
+__device__ __forceinline__ bool next_mod_item(const AttnParams& p, const ModSmem& sm, int& idx,
+                                              int total, ModItem& it, int stride) {
+  if (idx >= total) return false;
+  const int k = idx;
+  idx += stride;
+  it.kvh = k % p.num_kv_heads;
+  const int pair = k / p.num_kv_heads;
+  int lo = 0, hi = p.num_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sm.seq_start[mid] <= pair) lo = mid; else hi = mid - 1;
+  }
+  const int rpt = kRowsM / p.group;  // tokens per query tile
+  const int qlen = sm.seq_qlen[lo];
+  it.seq = lo;
+  it.ctx = sm.seq_ctx[lo];
+  it.q0 = sm.seq_q0[lo];
+  it.bidir = p.bidir_lens ? min(__ldg(p.bidir_lens + lo), it.ctx) : 0;
+  // the sequence's last pair of tiles, the longest without a window, first
+  const int mp = sm.seq_start[lo + 1] - 1 - pair;
+  int lo_min = INT_MAX, hi_max = 0, end[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    it.t0[x] = (2 * mp + x) * rpt;
+    it.nt[x] = max(0, min(rpt, qlen - it.t0[x]));
+    it.pos0[x] = it.ctx - qlen + it.t0[x];
+    end[x] = 0;
+    if (it.nt[x] > 0) {
+      // the first row has the tile's smallest first key, the last row that sees a
+      // key its largest end
+      const int* start = p.key_start ? p.key_start + it.q0 + it.t0[x] : nullptr;
+      int pos = it.pos0[x] + it.nt[x] - 1;
+      int h = max(pos + 1, it.bidir), first = 0;
+      while (start && pos >= it.pos0[x] && __ldg(start + (pos - it.pos0[x])) >= h) {
+        --pos;
+        h = pos >= it.pos0[x] ? max(pos + 1, it.bidir) : 0;
+      }
+      if (start) first = max(first, __ldg(start));
+      if (p.window > 0) first = max(first, it.pos0[x] - p.window + 1);
+      if (first < h) {
+        end[x] = (h - 1) / kTileKeys + 1;
+        lo_min = min(lo_min, first);
+        hi_max = max(hi_max, h);
+      }
+    }
+  }
+  it.nk = max(end[0], end[1]);
+  it.kt0 = it.nk > 0 ? lo_min / kTileKeys : 0;
+  it.lo_block = it.nk > 0 ? lo_min / kBlockSize : 0;
+  it.end_block = (hi_max + kBlockSize - 1) / kBlockSize;
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    it.last[x] = end[x] > 0 ? ((kMods & kModBias) ? it.nk : end[x]) - 1 : -1;
+  const bool partial = (it.ctx & (kBlockSize - 1)) != 0;
+  it.tail_step = partial && (it.ctx - 1) / kTileKeys == it.nk - 1
+                     ? ((it.ctx - 1) % kTileKeys) / (kFP8 ? 2 * kBlockSize : kBlockSize)
+                     : -1;
+  return true;
+}
+
+// All softmax threads of query tile qt agree on `ok` (named barrier 1 + qt).
+__device__ __forceinline__ bool all_of_tile(bool ok, int qt) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(1 + qt), "n"(32 * kTileWarps)
+      : "memory");
+  return r != 0;
+}
+
+// Largest magnitude of three values.
+__device__ __forceinline__ float absmax3(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The scores of a tile's 128 keys from k0 on, modified in place.  a > 0 takes a raw
+// score to base-2 units, C = cap log2(e) is the cap in them.  Returns the factor
+// still to be applied, which the exponential's own multiply-add carries: a where the
+// score is only masked, 1 after a cap or a bias.
+//
+// The cap is C tanh(a s / C).  Where every score of the warp stays below 3/4 of
+// the cap, the usual case, it is s T(s^2), T(u) = a (1 + k3 c^2 u + k5 c^4 u^2 + ...),
+// c = a / C: the polynomial of tanh with the scales folded into its coefficients, six
+// operations on packed pairs and no exponential beside the softmax's own.  Otherwise
+// C - 2 C / (2^(2 c log2(e) s) + 1): two more MUFU results per score, off by at most
+// 2^-22 C.  (Folding either into the exponential's argument saves operations, but
+// has the code of the exponentials twice: 145 us against 130 for the mixed batch's
+// chunks, the difference waiting for instructions.)
+template <int kMods>
+__device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, float a, float slope,
+                                               int pos, int k0) {
+  if constexpr (kMods == 0) return a;
+  if constexpr ((kMods & kModCap) != 0) {
+    const float c = a / p.cap_log2, C = p.cap_log2;
+    float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kTileKeys; i += 2)
+      top[(i >> 1) & 3] = absmax3(top[(i >> 1) & 3], sv[i], sv[i + 1]);
+    const float most = absmax3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
+    if (__all_sync(kFull, most <= kTanhPoly && c <= 16.0f)) {
+      const float c2 = c * c;
+      const float t1 = a * c2, t2 = t1 * c2, t3 = t2 * c2, t4 = t3 * c2;
+      const float2 q0 = make_float2(a, a), q1 = make_float2(t1 * kTanh3, t1 * kTanh3),
+                   q2 = make_float2(t2 * kTanh5, t2 * kTanh5),
+                   q3 = make_float2(t3 * kTanh7, t3 * kTanh7),
+                   q4 = make_float2(t4 * kTanh9, t4 * kTanh9);
+#pragma unroll
+      for (int i = 0; i < kTileKeys; i += 2) {
+        const float2 x = make_float2(sv[i], sv[i + 1]), u = __fmul2_rn(x, x);
+        const float2 t =
+            __ffma2_rn(u, __ffma2_rn(u, __ffma2_rn(u, __ffma2_rn(u, q4, q3), q2), q1), q0);
+        const float2 y = __fmul2_rn(x, t);
+        sv[i] = y.x;
+        sv[i + 1] = y.y;
+      }
+    } else {
+      const float k = 2.0f * kLog2e * c;
+#pragma unroll
+      for (int i = 0; i < kTileKeys; ++i) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(sv[i] * k) + 1.0f));
+        sv[i] = fmaf(r, -2.0f * C, C);
+      }
+    }
+  }
+  if constexpr ((kMods & kModBias) != 0) {
+    // distance bias of key k0 + i: -slope |pos - k0 - i|; without the absolute value
+    // where every row of the warp is behind the tile
+    const float f = (kMods & kModCap) != 0 ? 1.0f : a;
+    const float d0 = (float)(pos - k0), b0 = -slope * d0;
+    if (__all_sync(kFull, pos >= k0 + kTileKeys - 1)) {
+#pragma unroll
+      for (int i = 0; i < kTileKeys; ++i) sv[i] = fmaf(sv[i], f, fmaf(slope, (float)i, b0));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTileKeys; ++i) sv[i] = fmaf(sv[i], f, -slope * fabsf(d0 - (float)i));
+    }
+  }
+  return 1.0f;
+}
+
+// Two E4M3 terms of the weights x, y: codes of kPMods8 w, and of what those leave.
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t* hi, uint32_t* lo) {
+  const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x * kPMods8, y * kPMods8),
+                                                           __NV_SATFINITE, __NV_E4M3);
+  __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h2, __NV_E4M3);
+  const float2 hv = __half22float2(*reinterpret_cast<__half2*>(&hr));
+  *hi = h2;
+  *lo = __nv_cvt_float2_to_fp8x2(make_float2(fmaf(x, kPMods8, -hv.x), fmaf(y, kPMods8, -hv.y)),
+                                 __NV_SATFINITE, __NV_E4M3);
+}
+
+// O (+)= P V: P in TMEM at a (16 columns for every 32 keys), V 16-bit in steps of 16
+// keys or E4M3 in steps of 32 (hi terms, then lo terms); step ts (if >= 0) takes its V
+// rows from the tail buffer.
+template <bool kFP8>
+__device__ __forceinline__ void issue_mods_pv(uint32_t d, uint32_t a, uint64_t dv, uint64_t dtail,
+                                              int ts, uint32_t acc0, uint32_t idesc) {
+  if constexpr (kFP8) {
+#pragma unroll
+    for (int kk = 0; kk < kTileKeys / 32; ++kk) {
+      const uint64_t b = kk == ts ? dtail : dv + (uint64_t)((kk * (32 * 128)) >> 4);
+      mma_f8_tmem_a(d, a + 16 * kk, b, idesc, acc0 | (kk != 0 ? 1u : 0u));
+      mma_f8_tmem_a(d, a + 16 * kk + 8, b, idesc, 1);
+    }
+  } else {
+#pragma unroll
+    for (int kk = 0; kk < kTileKeys / 16; ++kk) {
+      const uint64_t b = kk == ts ? dtail : dv + (uint64_t)((kk * (kBlockSize * 128)) >> 4);
+      mma_f16_tmem_a(d, a + 8 * kk, b, idesc, acc0 | (kk != 0 ? 1u : 0u));
+    }
+  }
+}
+
+// One row (a query token's head) from its own keys alone, in fp32 (the plain online
+// softmax, exp2f).  Four lanes share the row, 32 dimensions each; gmask is their
+// mask.
+template <class QT, bool kFP8>
+__device__ __forceinline__ void exact_row(const AttnParams& p, int seq, int row, int h, int pos,
+                                          int lo, int hi, unsigned gmask) {
+  constexpr int kElem = kFP8 ? 1 : 2;
+  using T = typename QT::T;
+  const int quarter = threadIdx.x & 3, kvh = h / p.group;
+  const float slope = p.alibi ? __ldg(p.alibi + h) * kLog2e : 0.0f;
+  const size_t at = ((size_t)row * p.num_heads + h) * kD + quarter * 32;
+  float qf[32], acc[32], m = -INFINITY, l = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    to_float(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + at) + c), qf + 8 * c,
+             QT());
+#pragma unroll
+  for (int d = 0; d < 32; ++d) acc[d] = 0.0f;
+  for (int j = lo; j < hi; ++j) {
+    const int blk = __ldg(p.block_tables + (size_t)seq * p.max_blocks_per_seq + j / kBlockSize);
+    const bool bok = blk >= 0 && blk < p.num_blocks;
+    const size_t off = ((((size_t)(bok ? blk : 0) * p.num_kv_heads + kvh) * kBlockSize +
+                         j % kBlockSize) * kD + quarter * 32) * kElem;
+    float kv[32], dot = 0.0f;
+    if (bok) {
+      const uint4* kp = reinterpret_cast<const uint4*>(p.k_cache + off);
+#pragma unroll
+      for (int c = 0; c < 32 * kElem / 16; ++c) {
+        if constexpr (kFP8) to_float(__ldg(kp + c), kv + 16 * c, E4M3());
+        else to_float(__ldg(kp + c), kv + 8 * c, QT());
+      }
+#pragma unroll
+      for (int d = 0; d < 32; ++d) dot = fmaf(qf[d], kv[d], dot);
+    }
+    dot += __shfl_xor_sync(gmask, dot, 1);
+    dot += __shfl_xor_sync(gmask, dot, 2);
+    float sc = dot * p.q_scale;
+    if (p.softcap > 0.0f) sc = p.cap_log2 * cap_tanh(sc / p.cap_log2);
+    sc = fmaf(-slope, fabsf((float)(pos - j)), sc);
+    if (!(sc <= m)) {  // (a NaN score too: the row's result is NaN)
+      const float a = exp2f(m - sc);
+      l *= a;
+#pragma unroll
+      for (int d = 0; d < 32; ++d) acc[d] *= a;
+      m = sc;
+    }
+    const float w = exp2f(sc - m);
+    l += w;
+    if (bok) {
+      const uint4* vp = reinterpret_cast<const uint4*>(p.v_cache + off);
+#pragma unroll
+      for (int c = 0; c < 32 * kElem / 16; ++c) {
+        if constexpr (kFP8) to_float(__ldg(vp + c), kv + 16 * c, E4M3());
+        else to_float(__ldg(vp + c), kv + 8 * c, QT());
+      }
+#pragma unroll
+      for (int d = 0; d < 32; ++d) acc[d] = fmaf(w, kv[d], acc[d]);
+    }
+  }
+  const float inv = p.v_scale / l;
+  T* op = static_cast<T*>(p.out) + at;
+#pragma unroll
+  for (int d = 0; d < 32; ++d) store_out(op + d, acc[d] * inv);
+}
+
+// The rows of query tile qt of this CTA's items whose output is not finite, again
+// by exact_row: eight rows at a time per warp, `w` of the tile's.
+template <class QT, bool kFP8, int kMods>
+__device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem& sm, int cta, int ncta,
+                                       int total, int qt, int w) {
+  using T = typename QT::T;
+  const int lane = threadIdx.x & 31, g = p.group;
+  const unsigned gmask = 0xFu << (lane & 28);
+  int idx = cta;
+  ModItem x;
+  while (next_mod_item<kMods, kFP8>(p, sm, idx, total, x, ncta)) {
+    const int nt = qt ? x.nt[1] : x.nt[0], t0 = qt ? x.t0[1] : x.t0[0];
+    const int pos0 = qt ? x.pos0[1] : x.pos0[0];
+    for (int r = w * 8 + (lane >> 2); r < nt * g; r += 8 * kTileWarps) {
+      const int tok = r / g, row = x.q0 + t0 + tok, h = x.kvh * g + r % g;
+      int lo, hi;
+      key_interval(p, row, pos0 + tok, x.ctx, x.bidir, &lo, &hi);
+      if (lo >= hi) continue;
+      const uint4* o = reinterpret_cast<const uint4*>(
+          static_cast<const T*>(p.out) + ((size_t)row * p.num_heads + h) * kD + (lane & 3) * 32);
+      bool odd = false;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float f[8];
+        to_float(o[c], f, QT());
+#pragma unroll
+        for (int e = 0; e < 8; ++e) odd |= !(fabsf(f[e]) < INFINITY);
+      }
+      if (__any_sync(gmask, odd)) exact_row<QT, kFP8>(p, x.seq, row, h, pos0 + tok, lo, hi, gmask);
+    }
+  }
+}
+
+// Barriers, tensor memory, and the per-sequence tables; ends with the CTA synchronised.
+__device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem& sm, const CUtensorMap& tm_k,
+                                           const CUtensorMap& tm_v, const CUtensorMap& tm_q) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRingBars; ++s) {
+      mbar_init(&sm.full[s], kModProd);
+      mbar_init(&sm.empty[s], 1);
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sm.s_ready[x], 1);
+      mbar_init(&sm.p_ready[x], 1);
+      mbar_init(&sm.o_done[x], 1);
+      mbar_init(&sm.o_free[x], kTileWarps);
+      sm.redo[x] = 0;
+    }
+    mbar_init(&sm.tail_full, 1);
+    mbar_init(&sm.tail_free, 1);
+    mbar_init(&sm.mma_done, 1);
+    sm.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp >= kWarpTma && lane == 0) {
+    tc::prefetch_tmap(&tm_k);
+    tc::prefetch_tmap(&tm_v);
+    tc::prefetch_tmap(&tm_q);
+  }
+  if (warp == kWarpMma) {
+    tc::tmem_alloc(&sm.tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  const int S = p.num_seqs, tid = threadIdx.x;
+  const int chunk = (S + kModThreads - 1) / kModThreads;
+  const int cap = min(p.max_blocks_per_seq * kBlockSize, p.max_context);
+  const int per_item = 2 * (kRowsM / p.group);  // tokens
+  int local = 0;
+  for (int i = 0; i < chunk; ++i) {
+    const int sq = tid * chunk + i;
+    if (sq < S) {
+      const int q0 = __ldg(p.query_start_loc + sq);
+      int qlen = __ldg(p.query_start_loc + sq + 1) - q0;
+      int ctx = __ldg(p.context_lens + sq);
+      if (ctx < 0 || ctx > cap || qlen < 0 || qlen > ctx || q0 < 0 || qlen > p.num_rows - q0) {
+        flag_error(p.errors, PKV_DEVERR_CONTEXT);
+        ctx = ctx < 0 ? 0 : min(ctx, cap);
+        qlen = qlen < 0 ? 0 : min(qlen, ctx);
+        if (q0 < 0 || qlen > p.num_rows - q0) qlen = 0;
+      }
+      sm.seq_qlen[sq] = qlen;
+      sm.seq_ctx[sq] = ctx;
+      sm.seq_q0[sq] = q0;
+      local += (qlen + per_item - 1) / per_item;
+    }
+  }
+  int incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sm.scan[warp] = incl;
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < warp; ++w) base += sm.scan[w];
+  int run = base + incl - local;
+  for (int i = 0; i < chunk; ++i) {
+    const int sq = tid * chunk + i;
+    if (sq < S) {
+      sm.seq_start[sq] = run;
+      run += (sm.seq_qlen[sq] + per_item - 1) / per_item;
+    }
+  }
+  if (tid == kModThreads - 1) sm.seq_start[S] = base + incl;
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+}
+
+// TMA producer pw of three: per item the query tiles, then per step its key tile's K
+// boxes, the tail rows of V where the tile holds the context's partial last block,
+// and its V boxes (blocks j with j % 3 == pw), into the ring.
+template <bool kFP8, int kMods>
+__device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
+                                              const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                              const CUtensorMap& tm_q, int kv_rows, int cta,
+                                              int ncta, int total, int pw) {
+  constexpr int kStageBytes = kFP8 ? kTileBytes / 2 : kTileBytes;
+  constexpr int nst = kFP8 ? kStages8 : kStages;
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  const int lane = threadIdx.x & 31, g = p.group;
+  const int mine = (8 - pw + kModProd - 1) / kModProd;  // blocks per tile
+  const bool my_lane = (lane & 7) % kModProd == pw;
+  uint8_t* const ring = &sm.ring[0][0];
+  int idx = cta;
+  uint32_t pos = 0;
+  int nitem = 0, ntail = 0;
+  bool ok = true;
+  ModItem x;
+  // table entry of block 32 c + lane (kBeyond outside the visible blocks), read ahead
+  // of its use, checked when used
+  auto fetch = [&](int c) -> int {
+    const int b = 32 * c + lane;
+    return b >= x.lo_block && b < x.end_block
+               ? __ldg(p.block_tables + (size_t)x.seq * p.max_blocks_per_seq + b)
+               : kBeyond;
+  };
+  auto to_row = [&](int blk) -> int {
+    if (blk == kBeyond) return kv_rows;
+    if (blk >= 0 && blk < p.num_blocks) return (blk * p.num_kv_heads + x.kvh) * kBlockSize;
+    flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
+    return kv_rows;
+  };
+  auto issue = [&](int t, int row, bool is_v) -> bool {
+    const int st = pos % nst;
+    // test hook: these boxes are never issued, so every wait for the tile runs out
+    const bool skip = pw == 0 && cta == 0 && p.skip_copy > 0 && pos + 1 == (uint32_t)p.skip_copy;
+    bool good = true;
+    if (lane == 0) {
+      if (pos >= (uint32_t)nst) good = wait_bar(&sm.empty[st], ((pos / nst) - 1) & 1, abort, lim);
+      if (good && !skip) mbar_arrive_expect_tx(&sm.full[st], mine * (kStageBytes / 8));
+    }
+    if (!__shfl_sync(kFull, (int)good, 0)) return false;
+    if (!skip && (lane >> 3) == (t & 3) && my_lane) {
+      uint8_t* dst = ring + (size_t)st * kStageBytes + (lane & 7) * (kBlockSize * 128);
+      const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+      tc::tma_load_2d(dst, map, 0, row, &sm.full[st]);
+      if (!kFP8) tc::tma_load_2d(dst + kHalf, map, 64, row, &sm.full[st]);
+    }
+    __syncwarp();
+    ++pos;
+    return true;
+  };
+  // V rows of the MMA step that holds the partial last block, rows past the context
+  // as zeros, with the ring's swizzle
+  auto load_tail = [&]() -> bool {
+    bool good = true;
+    if (lane == 0 && ntail >= 1) good = wait_bar(&sm.tail_free, (ntail - 1) & 1, abort, lim);
+    if (!__shfl_sync(kFull, (int)good, 0)) return false;
+    constexpr int kRowChunks = kFP8 ? 8 : 16;  // 16-byte chunks per row
+    const int key0 = (x.nk - 1) * kTileKeys + x.tail_step * (kFP8 ? 2 * kBlockSize : kBlockSize);
+#pragma unroll
+    for (int i = 0; i < kTailBytes / 16 / 32; ++i) {
+      const int c = lane + 32 * i;
+      const int r = c / kRowChunks, ch = c % kRowChunks;
+      const int key = key0 + r;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (key < x.ctx && key / kBlockSize < x.end_block) {
+        const int blk =
+            __ldg(p.block_tables + (size_t)x.seq * p.max_blocks_per_seq + key / kBlockSize);
+        if (blk >= 0 && blk < p.num_blocks)
+          v = __ldg(reinterpret_cast<const uint4*>(
+                        p.v_cache + (((size_t)blk * p.num_kv_heads + x.kvh) * kBlockSize +
+                                     (key & (kBlockSize - 1))) * (kRowChunks * 16)) + ch);
+      }
+      *reinterpret_cast<uint4*>(&sm.tail[0] + (ch >> 3) * (kTailBytes / 2) + r * 128 +
+                                (((ch & 7) ^ (r & 7)) << 4)) = v;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.tail_full);
+    ++ntail;
+    return true;
+  };
+  while (ok && next_mod_item<kMods, kFP8>(p, sm, idx, total, x, ncta)) {
+    if (x.nk == 0) continue;
+    bool good = true;
+    if (pw == 0 && lane == 0) {
+      if (nitem >= 1) good = wait_bar(&sm.q_empty, (nitem - 1) & 1, abort, lim);
+      if (good) {
+        const int nq = x.nt[1] > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(&sm.q_full, nq * (kRowsM / g * g * kD * 2));
+        for (int qt = 0; qt < nq; ++qt) {
+          uint8_t* dq = &sm.q[qt][0];
+          const int tok = x.q0 + x.t0[qt];
+          // 16-bit: the two 64-dimension halves; E4M3: hi rows, then the lo rows
+          // (num_rows tokens further on)
+          tc::tma_load_3d(dq, &tm_q, 0, x.kvh * g, tok, &sm.q_full);
+          tc::tma_load_3d(dq + kHalf, &tm_q, kFP8 ? 0 : 64, x.kvh * g, kFP8 ? p.num_rows + tok : tok,
+                          &sm.q_full);
+        }
+      }
+    }
+    ok = __shfl_sync(kFull, (int)good, 0) != 0;
+    // block rows of the 32-block chunk (four key tiles) in use; the next one read ahead
+    constexpr int kStep = (kMods & kModBias) ? -1 : 1;
+    int cur_c = tile_of<kMods>(x, x.kt0) >> 2, cur_row = to_row(fetch(cur_c));
+    int pre_raw = fetch(cur_c + kStep);
+    for (int i = x.kt0; ok && i < x.nk; ++i) {
+      const int t = tile_of<kMods>(x, i);
+      if ((t >> 2) != cur_c) {
+        cur_c = t >> 2;
+        cur_row = to_row(pre_raw);
+        pre_raw = fetch(cur_c + kStep);
+      }
+      ok = issue(t, cur_row, false);
+      if (ok && pw == 0 && t == x.nk - 1 && x.tail_step >= 0) ok = load_tail();
+      if (ok) ok = issue(t, cur_row, true);
+    }
+    ++nitem;
+  }
+  if (!ok && lane == 0) {
+    flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+    for (uint32_t y = pos > (uint32_t)nst ? pos - nst : 0; y < pos; ++y)
+      mbar_wait(&sm.full[y % nst], (y / nst) & 1, 10000000ull);
+  }
+}
+
+// MMA issuer.  Order per item: S_a, S_b of the first step, then for each step i
+//   P_a(i) V, S_a(i + 1), P_b(i) V, S_b(i + 1)
+// so that one query tile's softmax works while the tensor pipe serves the other.
+template <class QT, bool kFP8, int kMods>
+__device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem& sm, uint32_t tmem, int cta,
+                                            int ncta, int total) {
+  constexpr int kStageBytes = kFP8 ? kTileBytes / 2 : kTileBytes;
+  constexpr int nst = kFP8 ? kStages8 : kStages;
+  constexpr uint32_t kAB = !kFP8 && std::is_same<QT, BF16>::value ? 1u : 0u;
+  constexpr uint32_t kIdescS = tc::idesc_f16(kAB, 0, 0, 128, 128);
+  constexpr uint32_t kIdescO = tc::idesc_f16(kAB, 0, 1, 128, 128);
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  const bool leader = tc::elect_one();
+  auto commit = [&](uint64_t* bar) {
+    if (leader) tc::mma_commit(bar);
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // every lane takes the same result
+    return __shfl_sync(kFull, (int)wait_bar(bar, parity, abort, lim), 0) != 0;
+  };
+  int idx = cta;
+  uint32_t pos = 0;
+  uint32_t np[2] = {0, 0};   // P tiles consumed per query tile
+  uint32_t nit[2] = {0, 0};  // items per query tile
+  int nitem = 0, ntail = 0;
+  bool ok = true;
+  ModItem x;
+  auto acquire = [&](int& st) -> bool {
+    st = pos % nst;
+    const bool r = wait(&sm.full[st], (pos / nst) & 1);
+    ++pos;
+    if (r) tc::fence_after_sync();
+    return r;
+  };
+  const uint64_t dq[2] = {tc::smem_desc(smem_u32(&sm.q[0][0]), 16, 1024, tc::kLayoutSw128),
+                          tc::smem_desc(smem_u32(&sm.q[1][0]), 16, 1024, tc::kLayoutSw128)};
+  const uint64_t dk0 = tc::smem_desc(smem_u32(&sm.ring[0][0]), 16, 1024, tc::kLayoutSw128);
+  const uint64_t dv0 =
+      tc::smem_desc(smem_u32(&sm.ring[0][0]), kFP8 ? 16 : kHalf, 1024, tc::kLayoutSw128);
+  const uint64_t dtail =
+      tc::smem_desc(smem_u32(&sm.tail[0]), kFP8 ? 16 : kTailBytes / 2, 1024, tc::kLayoutSw128);
+  auto mma_s = [&](int qt, int st) {
+    if (leader) {
+      const uint64_t dk = dk0 + (uint64_t)(st * (kStageBytes >> 4));
+      if constexpr (kFP8) issue_scores8(tmem + qt * 128, qt ? dq[1] : dq[0], dk, kIdescS);
+      else issue_scores(tmem + qt * 128, qt ? dq[1] : dq[0], dk, kIdescS);
+    }
+    commit(&sm.s_ready[qt]);
+  };
+  auto mma_pv = [&](int qt, int st, int i) -> bool {
+    if (!wait(&sm.p_ready[qt], np[qt] & 1)) return false;
+    ++np[qt];
+    if (i == x.kt0 && nit[qt] >= 1 && !wait(&sm.o_free[qt], (nit[qt] - 1) & 1))
+      return false;  // the previous item's O has been read out
+    tc::fence_after_sync();
+    if (leader) {
+      const uint64_t dv = dv0 + (uint64_t)(st * (kStageBytes >> 4));
+      const int ts = tile_of<kMods>(x, i) == x.nk - 1 ? x.tail_step : -1;
+      const uint32_t d = tmem + kColO + qt * 128, a = tmem + qt * 128, acc = i != x.kt0;
+      issue_mods_pv<kFP8>(d, a, dv, dtail, ts, acc, kIdescO);
+    }
+    if (i == x.last[qt]) commit(&sm.o_done[qt]);
+    return true;
+  };
+  while (ok && next_mod_item<kMods, kFP8>(p, sm, idx, total, x, ncta)) {
+    if (x.nk == 0) continue;
+    const bool ha = x.last[0] >= 0, hb = x.last[1] >= 0;
+    int kst = 0, vst = 0;
+    ok = wait(&sm.q_full, nitem & 1);
+    if (ok) {
+      tc::fence_after_sync();
+      ok = acquire(kst);
+    }
+    if (ok) {
+      if (ha) mma_s(0, kst);
+      if (hb) mma_s(1, kst);
+      commit(&sm.empty[kst]);
+      if (x.nk - x.kt0 == 1) commit(&sm.q_empty);
+    }
+    for (int i = x.kt0; ok && i < x.nk; ++i) {
+      const bool more = i + 1 < x.nk;
+      ok = acquire(vst);
+      if (ok && x.tail_step >= 0 && tile_of<kMods>(x, i) == x.nk - 1) {
+        ok = wait(&sm.tail_full, ntail & 1);
+        if (ok) tc::fence_after_sync();
+      }
+      if (ok && i <= x.last[0]) ok = mma_pv(0, vst, i);
+      if (ok && more) {
+        ok = acquire(kst);
+        if (ok && i + 1 <= x.last[0]) mma_s(0, kst);
+      }
+      if (ok && i <= x.last[1]) ok = mma_pv(1, vst, i);
+      if (!ok) break;
+      commit(&sm.empty[vst]);
+      if (more) {
+        if (i + 1 <= x.last[1]) mma_s(1, kst);
+        commit(&sm.empty[kst]);
+        if (i + 1 == x.nk - 1) commit(&sm.q_empty);
+      }
+    }
+    if (ok && x.tail_step >= 0) {
+      commit(&sm.tail_free);
+      ++ntail;
+    }
+    if (ha) ++nit[0];
+    if (hb) ++nit[1];
+    ++nitem;
+  }
+  if (!ok && leader) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+  commit(&sm.mma_done);
+  mbar_wait(&sm.mma_done, 0, 100000000ull);
+}
+
+// Softmax and epilogue: thread = row of query tile qt.
+template <class QT, bool kFP8, int kMods>
+__device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, uint32_t tmem, int cta,
+                                             int ncta, int total) {
+  using OutT = typename QT::T;
+  constexpr float kMove = kFP8 ? kMove8 : kRescaleAt;
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qt = warp / kTileWarps, g = p.group;
+  const int r = threadIdx.x & 127;  // row = TMEM lane
+  const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t s_col = tmem + lane_off + qt * 128;
+  const uint32_t o_col = tmem + lane_off + kColO + qt * 128;
+  // scores are scaled inside the exponent; a negative scale is folded in by negating
+  // them, a zero one taken as 1e-30
+  const bool neg = p.q_scale < 0.0f;
+  const float qa = fmaxf(fabsf(p.q_scale), 1e-30f);
+  const int tok = r / g, head_in = r - tok * g;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // the warp's lanes agree
+    return __all_sync(kFull, wait_bar(bar, parity, abort, lim)) != 0;
+  };
+  int idx = cta;
+  uint32_t ns = 0, nit = 0;  // S tiles and items of this query tile
+  bool ok = true;
+  ModItem x;
+  while (ok && next_mod_item<kMods, kFP8>(p, sm, idx, total, x, ncta)) {
+    const int nt = qt ? x.nt[1] : x.nt[0], t0 = qt ? x.t0[1] : x.t0[0];
+    const int last = qt ? x.last[1] : x.last[0];
+    const int pos = (qt ? x.pos0[1] : x.pos0[0]) + tok;
+    // rows past the tile's tokens compute on whatever Q holds there; never stored
+    const bool valid = r < nt * g;
+    const int row = x.q0 + t0 + tok, h = x.kvh * g + head_in;
+    const size_t head = (size_t)row * p.num_heads + h;
+    OutT* orow = static_cast<OutT*>(p.out) + head * kD;
+    int lo = 0, hi = INT_MAX;
+    if (valid) {
+      key_interval(p, row, pos, x.ctx, x.bidir, &lo, &hi);
+      // first keys that decrease from row to row: blocks before lo_block are not here
+      if (lo < hi && (last < 0 || lo < x.lo_block * kBlockSize))
+        flag_error(p.errors, PKV_DEVERR_CONTEXT);
+    }
+    const bool empty = lo >= hi;  // zeros, whatever O and l hold
+    if (last < 0) {               // no row of the tile sees a key
+      if (valid) {
+#pragma unroll
+        for (int i = 0; i < kD / 8; ++i) reinterpret_cast<uint4*>(orow)[i] = make_uint4(0, 0, 0, 0);
+      }
+      continue;
+    }
+    const float slope = (kMods & kModBias) && valid ? __ldg(p.alibi + h) * kLog2e : 0.0f;
+    // E4M3 caches: the row's query scale s (q / s = hi + lo) joins the score scale
+    const float a = kFP8 && valid ? qa * __ldg(p.q8_scale + head) : qa;
+    float m_run = -INFINITY;
+    float2 l2[4];  // partial row sums (independent chains, packed pairs)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l2[i] = make_float2(0.0f, 0.0f);
+    for (int i = x.kt0; i <= last; ++i, ++ns) {
+      const int k0 = tile_of<kMods>(x, i) * kTileKeys;
+      const bool good = wait(&sm.s_ready[qt], ns & 1);
+      const bool none = __all_sync(kFull, hi <= k0 || lo >= k0 + kTileKeys || empty);
+      const bool whole = __all_sync(kFull, lo <= k0 && hi >= k0 + kTileKeys);
+      // ---- the row's largest score in these keys ---------------------------------------------
+      float mt = -INFINITY;
+      float sv[kTileKeys], f = 1.0f;
+      if (good && !none) {
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < kTileKeys; c += 32) tc::tmem_ld32(s_col + c, sv + c);
+        tc::tmem_wait_ld();
+        if (neg) {
+#pragma unroll
+          for (int c = 0; c < kTileKeys; ++c) sv[c] = -sv[c];
+        }
+        f = modify_scores<kMods>(p, sv, a, slope, pos, k0);
+        if (!whole) {  // an interval of some row of the warp ends in these keys
+#pragma unroll
+          for (int c = 0; c < kTileKeys; ++c)
+            sv[c] = k0 + c >= lo && k0 + c < hi ? sv[c] : -INFINITY;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kTileKeys; c += 2)
+          mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
+        mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+      }
+      ok = all_of_tile(good, qt);
+      if (!ok) break;
+      // move the running max (and rescale O) only on a large increase; O is complete
+      // up to the step before (this S was issued after its product)
+      const bool fresh = m_run == -INFINITY;  // no key seen so far
+      const bool need = mt > m_run + kMove;
+      float alpha = 1.0f;
+      if (need) {
+        alpha = fresh ? 0.0f : fast_exp2(m_run - mt);
+        m_run = mt;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) l2[c] = __fmul2_rn(l2[c], make_float2(alpha, alpha));
+      }
+      const float m = m_run == -INFINITY ? 0.0f : m_run;  // 2^(-inf - 0) = 0
+      // ---- weights, over the scores (hidden keys are -inf: weight 0) -----------------------
+      if (none) {
+        float z[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) z[c] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kTileKeys / kChunk; ++c) tc::tmem_st16(s_col + 16 * c, z);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kTileKeys / kChunk; ++c) {
+          // 16 columns: packed 16-bit pairs, or 8 of four E4M3 codes (hi) and 8 of lo
+          float pk[16];
+          uint32_t h0 = 0, r0 = 0;
+#pragma unroll
+          for (int e = 0; e < kChunk; e += 2) {
+            const float x = fast_exp2(fmaf(sv[kChunk * c + e], f, -m));
+            const float y = fast_exp2(fmaf(sv[kChunk * c + e + 1], f, -m));
+            l2[(e >> 1) & 3] = __fadd2_rn(l2[(e >> 1) & 3], make_float2(x, y));
+            if constexpr (!kFP8) {
+              pk[e >> 1] = __uint_as_float(pack2<QT>(x, y));
+            } else {
+              uint32_t h1, r1;
+              split_pair(x, y, &h1, &r1);
+              if (e & 2) {
+                pk[e >> 2] = __uint_as_float(h0 | (h1 << 16));
+                pk[8 + (e >> 2)] = __uint_as_float(r0 | (r1 << 16));
+              } else {
+                h0 = h1;
+                r0 = r1;
+              }
+            }
+          }
+          tc::tmem_st16(s_col + 16 * c, pk);
+        }
+      }
+      // the product of this step adds onto O: rescale it first
+      if (i > x.kt0 && __any_sync(kFull, need)) {
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 32) {
+          float ov[32];
+          tc::tmem_ld32(o_col + c, ov);
+          tc::tmem_wait_ld();
+          // (a row that had seen no key: zeros, although 0 * inf may be there)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = fresh && need ? 0.0f : ov[e] * alpha;
+          tc::tmem_st32(o_col + c, ov);
+        }
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      tc::named_sync(1 + qt, 32 * kTileWarps);
+      if (r == 0) mbar_arrive(&sm.p_ready[qt]);
+    }
+    if (!ok) break;
+    // ---- epilogue: O / l ------------------------------------------------------------------
+    const float l = ((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y)) +
+              ((l2[2].x + l2[2].y) + (l2[3].x + l2[3].y));
+    ok = all_of_tile(wait(&sm.o_done[qt], nit & 1), qt);
+    if (!ok) break;
+    tc::fence_after_sync();
+    // (E4M3: P held kPMods8 w, and V its codes)
+    const float inv = valid && !empty ? p.v_scale / (kFP8 ? kPMods8 * l : l) : 0.0f;
+    bool odd = false;  // an output that is not finite
+#pragma unroll 1
+    for (int c = 0; c < kD; c += 32) {
+      float ov[32];
+      tc::tmem_ld32(o_col + c, ov);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        ov[e] = empty ? 0.0f : ov[e] * inv;
+        odd |= !(fabsf(ov[e]) < INFINITY);
+      }
+      if (valid) {
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint4 w;
+          w.x = pack2<QT>(ov[q4 * 8 + 0], ov[q4 * 8 + 1]);
+          w.y = pack2<QT>(ov[q4 * 8 + 2], ov[q4 * 8 + 3]);
+          w.z = pack2<QT>(ov[q4 * 8 + 4], ov[q4 * 8 + 5]);
+          w.w = pack2<QT>(ov[q4 * 8 + 6], ov[q4 * 8 + 7]);
+          reinterpret_cast<uint4*>(orow + c)[q4] = w;
+        }
+      }
+    }
+    if (odd && valid) sm.redo[qt] = 1;
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.o_free[qt]);
+    ++nit;
+  }
+  if (!ok && r == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+  // every warp of the tile leaves the loop here, whatever it met, and sees the others'
+  // stores and flag behind this barrier
+  ok = all_of_tile(ok, qt);
+  if (ok && sm.redo[qt]) redo_rows<QT, kFP8, kMods>(p, sm, cta, ncta, total, qt, warp % kTileWarps);
+}
+
+template <class QT, bool kFP8, int kMods>
+__global__ void __launch_bounds__(kModThreads, 1)
+    prefill_mods_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_q, int kv_rows) {
+  extern __shared__ uint8_t smem_raw[];
+  ModSmem& sm = *reinterpret_cast<ModSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                            ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  mods_setup(p, sm, tm_k, tm_v, tm_q);
+  const uint32_t tmem = sm.tmem_base;
+  const int cta = blockIdx.x, ncta = gridDim.x;
+  const int total = sm.seq_start[p.num_seqs] * p.num_kv_heads;
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kWarpMma)
+      mods_issuer<QT, kFP8, kMods>(p, sm, tmem, cta, ncta, total);
+    else
+      mods_producer<kFP8, kMods>(p, sm, tm_k, tm_v, tm_q, kv_rows, cta, ncta, total, warp - kWarpTma);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    mods_softmax<QT, kFP8, kMods>(p, sm, tmem, cta, ncta, total);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <class QT, bool kFP8, int kMods>
+int launch_mods(const AttnParams& p, int total_q, const uint8_t* q8, cudaStream_t stream) {
+  const bool bf16 = std::is_same<QT, BF16>::value;
+  const uint64_t kv_rows = (uint64_t)p.num_blocks * p.num_kv_heads * kBlockSize;
+  const uint32_t g = (uint32_t)p.group, tokens = kRowsM / g, heads = (uint32_t)p.num_heads;
+  CUtensorMap tk, tv, tq;
+  const bool maps =
+      kFP8 ? make_map_e4m3(&tk, p.k_cache, kv_rows, 16) && make_map_e4m3(&tv, p.v_cache, kv_rows, 16) &&
+                 make_map_q3d_e4m3(&tq, q8, 2 * (uint64_t)total_q, heads, g, tokens)
+           : make_map_2d(&tk, p.k_cache, kv_rows, bf16, 16) &&
+                 make_map_2d(&tv, p.v_cache, kv_rows, bf16, 16) &&
+                 make_map_q3d(&tq, p.q, (uint64_t)total_q, heads, bf16, g, tokens);
+  if (!maps) return PKV_ERR_CUDA;
+  const size_t smem = sizeof(ModSmem) + 1024;
+  static_assert(sizeof(ModSmem) + 1024 <= 232448, "shared memory budget of one CTA");
+  static_assert(offsetof(ModSmem, ring) % 1024 == 0 && offsetof(ModSmem, q) % 1024 == 0 &&
+                    offsetof(ModSmem, tail) % 1024 == 0,
+                "swizzled buffers must start on 1024-byte boundaries");
+  auto kern = prefill_mods_kernel<QT, kFP8, kMods>;
+  // the kernel's register shares add up to what 384 x 168 hold; with fewer its
+  // warpgroups would wait for registers without end
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
+  if (fa.numRegs * kModThreads < 32 * kSoftWarps * kSoftRegs + 128 * kOtherRegs) return PKV_ERR_CUDA;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess)
+    return PKV_ERR_CUDA;
+  // launches of at most kMaxSeqs sequences each; their query rows stay absolute
+  for (int s0 = 0; s0 < p.num_seqs; s0 += kMaxSeqs) {
+    AttnParams c = p;
+    c.num_seqs = p.num_seqs - s0 < kMaxSeqs ? p.num_seqs - s0 : kMaxSeqs;
+    c.block_tables = p.block_tables + (size_t)s0 * p.max_blocks_per_seq;
+    c.context_lens = p.context_lens + s0;
+    c.query_start_loc = p.query_start_loc + s0;
+    if (p.bidir_lens) c.bidir_lens = p.bidir_lens + s0;
+    // an upper bound of the items: every sequence's pairs of query tiles, times the KV heads
+    const long long tiles = (total_q + (long long)tokens - 1) / tokens + c.num_seqs;
+    const long long items = (tiles + c.num_seqs) / 2 * p.num_kv_heads;
+    const int sms = sm_count();
+    const int grid = (int)(items < sms ? (items > 0 ? items : 1) : sms);
+    kern<<<grid, kModThreads, smem, stream>>>(c, tk, tv, tq, (int)kv_rows);
+    if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+  }
+  return PKV_OK;
+}
+
+// q8: the split query of an E4M3 cache, or null
+template <int kMods>
+int launch_mods_typed(const AttnParams& p, int q_dtype, int total_q, const uint8_t* q8,
+                      cudaStream_t stream) {
+  if (q_dtype == PKV_BF16)
+    return q8 ? launch_mods<BF16, true, kMods>(p, total_q, q8, stream)
+              : launch_mods<BF16, false, kMods>(p, total_q, q8, stream);
+  return q8 ? launch_mods<F16, true, kMods>(p, total_q, q8, stream)
+            : launch_mods<F16, false, kMods>(p, total_q, q8, stream);
+}
+
+}  // namespace
+}  // namespace pre_mods
+}  // namespace pkv
+
+#endif  // PKV_PREFILL_MODS_CUH

@@ -1,0 +1,9 @@
+// Biased chunked prefill with capped scores.
+#include "prefill_mods.cuh"
+
+namespace pkv {
+int launch_prefill_cap(const AttnParams& p, int q_dtype, int total_q, const uint8_t* q8,
+                       cudaStream_t stream) {
+  return pre_mods::launch_mods_typed<pre_mods::kModCap>(p, q_dtype, total_q, q8, stream);
+}
+}  // namespace pkv

@@ -44,18 +44,6 @@
 // the rows of such chunks are recomputed in fp32 after the main loop, as the
 // causal rows at the start of a prompt are.
 //
-// Biased mode (kMods): scores are modified and a row sees an interval of keys
-// (score_mods.cuh).  An item walks the key tiles from its first row's first key
-// to its last row's last one, blocks before that first key are not read, a
-// tile that every row of a warp sees whole skips the mask, and one that none of
-// them sees writes zeros for P without an exponential.  Any group size works: a
-// query tile holds 128 / g whole tokens.  A key hidden from a row has weight
-// zero, but in the product 0 * inf is NaN: a row whose output comes out not
-// finite is recomputed from its own keys alone, in fp32, after the main loop (so
-// an infinite V that a row does not see never reaches it; finite inputs never
-// take that path).  On E4M3 caches P is two E4M3 terms, p = hi + lo, in two
-// products: one term alone is good to 2^-4, 2 % of the output's norm.
-//
 // Warps: 0-3 softmax + epilogue of tile a, 4-7 of tile b, 8 TMEM owner + MMA
 // issuer, 9-11 TMA producers.  A K/V tile is 16 boxes of 16 rows x 128 B (one
 // per block and half); the boxes of each tile are spread over the three
@@ -74,7 +62,6 @@
 
 #include "common.cuh"
 #include "launch.h"
-#include "score_mods.cuh"
 #include "tc.cuh"
 
 namespace pkv {
@@ -102,11 +89,6 @@ constexpr float kRescaleAt = 8.0f;
 // down to 2^-13 keep a code.
 constexpr float kRescaleAt8 = 4.0f;
 constexpr float kPScale8 = 16.0f;
-// Biased mode, two E4M3 terms: w <= 2, P holds 128 w.  The headroom that one term
-// spends on fewer rescales goes to small weights here: they keep a code down to
-// 2^-17, and a row's tail of many of them is not lost.
-constexpr float kRescaleMods8 = 1.0f;
-constexpr float kPScaleMods8 = 128.0f;
 // Causal rows that see at most this many keys are recomputed in fp32 on the
 // CUDA cores after the main loop: with so few keys the 16-bit rounding of the
 // softmax weights (relative 2^-9 each) does not average out.
@@ -137,7 +119,6 @@ struct Smem {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
-  int redo;  // biased mode: a row of this CTA came out not finite
 };
 
 struct Item {
@@ -151,9 +132,6 @@ struct Item {
   int chunk;         // key chunk of the item (its partial slots)
   int first[2];      // first key tile of each warpgroup in the item
   int last[2];       // last key tile of each warpgroup (-1: none)
-  int bidir;         // biased mode: keys every query sees (0: causal)
-  int lo_block;      // biased mode: first block any row sees, and the end of those
-  int end_block;
   int step;          // key tiles between a warpgroup's tiles: 1, or 2 (shared-prefix mode)
   int tail_step;     // 16-key MMA step of the last key tile holding a partial block, else -1
 };
@@ -168,7 +146,7 @@ __device__ __forceinline__ int key_chunks(const AttnParams& p, int ctx) {
 }
 
 // kFP8: E4M3 caches, whose P.V MMAs take 32 keys per step (16 for 16-bit).
-template <bool kAlt, bool kFP8 = false, bool kMods = false>
+template <bool kAlt, bool kFP8 = false>
 __device__ __forceinline__ bool next_item(const AttnParams& p, const Smem& sm, int& idx,
                                           int total, Item& it, int stride) {
   if (idx >= total) return false;
@@ -197,8 +175,6 @@ __device__ __forceinline__ bool next_item(const AttnParams& p, const Smem& sm, i
   it.kt0 = kAlt && p.prefix_chunk > 0 ? it.chunk * (p.prefix_chunk / kTileKeys) : 0;
   const int kt1 = kAlt && p.prefix_chunk > 0 ? it.kt0 + p.prefix_chunk / kTileKeys : INT_MAX;
   it.nk = 0;
-  it.bidir = kMods && p.bidir_lens ? __ldg(p.bidir_lens + lo) : 0;
-  int lo_min = INT_MAX, hi_max = 0;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     it.t0[x] = (alt ? mp : 2 * mp + x) * rpt;
@@ -206,33 +182,7 @@ __device__ __forceinline__ bool next_item(const AttnParams& p, const Smem& sm, i
     it.pos0[x] = kAlt ? it.ctx - 1 : it.ctx - qlen + it.t0[x];
     const int last = kAlt ? it.pos0[x] : it.pos0[x] + it.nt[x] - 1;
     it.nkt[x] = it.nt[x] > 0 ? min(kt1, last / kTileKeys + 1) : 0;
-    if constexpr (kMods) {
-      // the first row has the tile's smallest first key, the last row that sees a
-      // key its largest end
-      const int* start = p.key_start ? p.key_start + it.q0 + it.t0[x] : nullptr;
-      int hi = 0, first = 0;
-      if (it.nt[x] > 0) {
-        int end = last;  // position of the row looked at
-        hi = max(end + 1, min(it.bidir, it.ctx));
-        while (start && end >= it.pos0[x] && __ldg(start + (end - it.pos0[x])) >= hi) {
-          --end;
-          hi = end >= it.pos0[x] ? max(end + 1, min(it.bidir, it.ctx)) : 0;
-        }
-        if (start) first = max(first, __ldg(start));
-        if (p.window > 0) first = max(first, it.pos0[x] - p.window + 1);
-      }
-      it.nkt[x] = first < hi ? (hi - 1) / kTileKeys + 1 : 0;
-      if (it.nkt[x] > 0) {
-        lo_min = min(lo_min, first);
-        hi_max = max(hi_max, hi);
-      }
-    }
     it.nk = max(it.nk, it.nkt[x]);
-  }
-  if constexpr (kMods) {
-    it.kt0 = it.nk > 0 ? lo_min / kTileKeys : 0;
-    it.lo_block = it.nk > 0 ? lo_min / kBlockSize : 0;
-    it.end_block = (hi_max + kBlockSize - 1) / kBlockSize;
   }
   const bool partial = (it.ctx & (kBlockSize - 1)) != 0;
   it.tail_step = partial && (it.ctx - 1) / kTileKeys == it.nk - 1
@@ -243,7 +193,6 @@ __device__ __forceinline__ bool next_item(const AttnParams& p, const Smem& sm, i
   for (int x = 0; x < 2; ++x) {
     it.first[x] = it.kt0 + (alt ? x : 0);
     const int end = alt ? it.nk : it.nkt[x];
-    // (biased mode: a tile without visible keys has nkt 0)
     it.last[x] = it.nt[x] > 0 && end > it.first[x]
                      ? it.first[x] + (end - 1 - it.first[x]) / it.step * it.step
                      : -1;
@@ -340,34 +289,6 @@ __device__ __forceinline__ void exp_quads8(const float* sv, float qa, float m, f
   }
 }
 
-// The same for two E4M3 terms of kPScaleMods8 * 2^x: hi, and what hi leaves.
-__device__ __forceinline__ void exp_quads8_split(const float* sv, float qa, float m, float2* l2,
-                                                 float* hi, float* lo) {
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    float e[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = fast_exp2(fmaf(sv[4 * c + i], qa, -m));
-    l2[(2 * c) & 3] = __fadd2_rn(l2[(2 * c) & 3], make_float2(e[0], e[1]));
-    l2[(2 * c + 1) & 3] = __fadd2_rn(l2[(2 * c + 1) & 3], make_float2(e[2], e[3]));
-    uint32_t h = 0, r = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(
-          make_float2(e[i] * kPScaleMods8, e[i + 1] * kPScaleMods8), __NV_SATFINITE, __NV_E4M3);
-      __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h2, __NV_E4M3);
-      const float2 hv = __half22float2(*reinterpret_cast<__half2*>(&hr));
-      const __nv_fp8x2_storage_t r2 = __nv_cvt_float2_to_fp8x2(
-          make_float2(fmaf(e[i], kPScaleMods8, -hv.x), fmaf(e[i + 1], kPScaleMods8, -hv.y)),
-          __NV_SATFINITE, __NV_E4M3);
-      h |= (uint32_t)h2 << (8 * i);
-      r |= (uint32_t)r2 << (8 * i);
-    }
-    hi[c] = __uint_as_float(h);
-    lo[c] = __uint_as_float(r);
-  }
-}
-
 // D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit operands: A is M lanes x K
 // elements, two elements per 32-bit column (the lower half holds the even one).
 __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
@@ -437,115 +358,6 @@ __device__ __forceinline__ void issue_pv8(uint32_t d, uint32_t a, uint64_t dv, u
   for (int kk = 0; kk < kTileKeys / 32; ++kk) {
     const uint64_t b = kk == ts ? dtail : dv + (uint64_t)((kk * (32 * 128)) >> 4);
     mma_f8_tmem_a(d, a + kk * 8, b, idesc, acc0 | (kk != 0 ? 1u : 0u));
-  }
-}
-
-// The same with P as two E4M3 terms, hi at a and lo 32 columns further.
-__device__ __forceinline__ void issue_pv8_split(uint32_t d, uint32_t a, uint64_t dv, uint64_t dtail,
-                                                int ts, uint32_t acc0, uint32_t idesc) {
-  issue_pv8(d, a, dv, dtail, ts, acc0, idesc);
-  issue_pv8(d, a + 32, dv, dtail, ts, 1, idesc);
-}
-
-// Biased mode: one row (a query token's head) from its own keys alone, in fp32
-// (the plain online softmax, exp2f).  Four lanes share the row, 32 dimensions
-// each; gmask is their mask.
-template <class QT, bool kFP8>
-__device__ __forceinline__ void exact_row(const AttnParams& p, int trow, int row, int h, int pos,
-                                          int lo, int hi, unsigned gmask) {
-  constexpr int kElem = kFP8 ? 1 : 2;
-  using T = typename QT::T;
-  const int quarter = threadIdx.x & 3, kvh = h / p.group;
-  const float slope = p.alibi ? __ldg(p.alibi + h) * kLog2e : 0.0f;
-  const size_t at = ((size_t)row * p.num_heads + h) * kD + quarter * 32;
-  float qf[32], acc[32], m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    to_float(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + at) + c), qf + 8 * c,
-             QT());
-#pragma unroll
-  for (int d = 0; d < 32; ++d) acc[d] = 0.0f;
-  for (int j = lo; j < hi; ++j) {
-    const int blk = __ldg(p.block_tables + (size_t)trow * p.max_blocks_per_seq + j / kBlockSize);
-    const bool bok = blk >= 0 && blk < p.num_blocks;
-    const size_t off = ((((size_t)(bok ? blk : 0) * p.num_kv_heads + kvh) * kBlockSize +
-                         j % kBlockSize) * kD + quarter * 32) * kElem;
-    float kv[32], dot = 0.0f;
-    if (bok) {
-      const uint4* kp = reinterpret_cast<const uint4*>(p.k_cache + off);
-#pragma unroll
-      for (int c = 0; c < 32 * kElem / 16; ++c) {
-        if constexpr (kFP8) to_float(__ldg(kp + c), kv + 16 * c, E4M3());
-        else to_float(__ldg(kp + c), kv + 8 * c, QT());
-      }
-#pragma unroll
-      for (int d = 0; d < 32; ++d) dot = fmaf(qf[d], kv[d], dot);
-    }
-    dot += __shfl_xor_sync(gmask, dot, 1);
-    dot += __shfl_xor_sync(gmask, dot, 2);
-    float sc = dot * p.q_scale;
-    if (p.softcap > 0.0f) sc = p.cap_log2 * cap_tanh(sc / p.cap_log2);
-    sc = fmaf(-slope, fabsf((float)(pos - j)), sc);
-    if (!(sc <= m)) {  // (a NaN score too: the row's result is NaN)
-      const float a = exp2f(m - sc);
-      l *= a;
-#pragma unroll
-      for (int d = 0; d < 32; ++d) acc[d] *= a;
-      m = sc;
-    }
-    const float w = exp2f(sc - m);
-    l += w;
-    if (bok) {
-      const uint4* vp = reinterpret_cast<const uint4*>(p.v_cache + off);
-#pragma unroll
-      for (int c = 0; c < 32 * kElem / 16; ++c) {
-        if constexpr (kFP8) to_float(__ldg(vp + c), kv + 16 * c, E4M3());
-        else to_float(__ldg(vp + c), kv + 8 * c, QT());
-      }
-#pragma unroll
-      for (int d = 0; d < 32; ++d) acc[d] = fmaf(w, kv[d], acc[d]);
-    }
-  }
-  const float inv = p.v_scale / l;
-  T* op = static_cast<T*>(p.out) + at;
-#pragma unroll
-  for (int d = 0; d < 32; ++d) store_out(op + d, acc[d] * inv);
-}
-
-// Biased mode: the rows of this CTA's items whose output is not finite, again by
-// exact_row.  Each softmax warp takes the 32 rows it stored, eight at a time.
-template <class QT, bool kFP8>
-__device__ __noinline__ void redo_rows(const AttnParams& p, const Smem& sm, int cta, int ncta,
-                                       int total, int qt, int warp_in_group) {
-  using T = typename QT::T;
-  const int lane = threadIdx.x & 31, g = p.group;
-  const unsigned gmask = 0xFu << (lane & 28);
-  __syncwarp();  // the rows' stores, by other lanes, are seen
-  int idx = cta;
-  Item x;
-  while (next_item<false, kFP8, true>(p, sm, idx, total, x, ncta)) {
-    const int nt = qt ? x.nt[1] : x.nt[0], t0 = qt ? x.t0[1] : x.t0[0];
-    const int pos0 = qt ? x.pos0[1] : x.pos0[0];
-    for (int i = 0; i < 4; ++i) {
-      const int r = warp_in_group * 32 + i * 8 + (lane >> 2);
-      if (r >= nt * g) continue;
-      const int tok = r / g, row = x.q0 + t0 + tok, h = x.kvh * g + r % g;
-      int lo, hi;
-      key_interval(p, row, pos0 + tok, x.ctx, x.bidir, &lo, &hi);
-      if (lo >= hi) continue;
-      const uint4* o = reinterpret_cast<const uint4*>(
-          static_cast<const T*>(p.out) + ((size_t)row * p.num_heads + h) * kD + (lane & 3) * 32);
-      bool odd = false;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float f[8];
-        to_float(o[c], f, QT());
-#pragma unroll
-        for (int e = 0; e < 8; ++e) odd |= !(fabsf(f[e]) < INFINITY);
-      }
-      if (__any_sync(gmask, odd))
-        exact_row<QT, kFP8>(p, x.trow, row, h, pos0 + tok, lo, hi, gmask);
-    }
   }
 }
 
@@ -654,7 +466,7 @@ __device__ __noinline__ void few_key_rows(const AttnParams& p, const SM& sm, int
 // Barriers, tensor memory, and the per-sequence tables (query length,
 // context, first query row, the prefix of work units, the prefix of rows
 // recomputed in fp32) of a prefill launch; ends with the CTA synchronised.
-template <bool kTree, bool kAlt, bool kMods = false>
+template <bool kTree, bool kAlt>
 __device__ __forceinline__ void prefill_setup(const AttnParams& p, Smem& sm,
                                               const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                               const CUtensorMap& tm_q) {
@@ -678,7 +490,6 @@ __device__ __forceinline__ void prefill_setup(const AttnParams& p, Smem& sm,
     mbar_init(&sm.tail_free, 1);
     mbar_init(&sm.mma_done, 1);
     sm.abort = 0;
-    if (kMods) sm.redo = 0;
     fence_barrier_init();
   }
   if (warp >= 9 && lane == 0) {
@@ -695,17 +506,7 @@ __device__ __forceinline__ void prefill_setup(const AttnParams& p, Smem& sm,
     // of tile pairs
     const int S = p.num_seqs, tid = threadIdx.x;
     const int chunk = (S + kThreads - 1) / kThreads;
-    const int cap = kMods ? min(p.max_blocks_per_seq * kBlockSize, p.max_context)
-                          : p.max_blocks_per_seq * kBlockSize;
-    // 128-row query tiles of a chunk (biased mode: of whole tokens)
-    auto tiles_of = [&](int qlen) {
-      if constexpr (kMods) {
-        const int rpt = kRowsM / g;
-        return (qlen + rpt - 1) / rpt;
-      } else {
-        return (qlen * g + kRowsM - 1) / kRowsM;
-      }
-    };
+    const int cap = p.max_blocks_per_seq * kBlockSize;
     int local = 0, local2 = 0;
     for (int i = 0; i < chunk; ++i) {
       const int sq = tid * chunk + i;
@@ -724,10 +525,10 @@ __device__ __forceinline__ void prefill_setup(const AttnParams& p, Smem& sm,
         sm.seq_qlen[sq] = qlen;
         sm.seq_ctx[sq] = ctx;
         sm.seq_q0[sq] = q0;
-        const int tiles = tiles_of(qlen);
+        const int tiles = (qlen * g + kRowsM - 1) / kRowsM;
         const int units = kAlt ? tiles : (tiles + 1) / 2;
         local += ctx > 0 ? units * key_chunks<kAlt>(p, ctx) : 0;
-        local2 += kMods ? 0 : few_rows<kTree, kAlt>(qlen, ctx);
+        local2 += few_rows<kTree, kAlt>(qlen, ctx);
       }
     }
     int incl = local, incl2 = local2;
@@ -755,10 +556,10 @@ __device__ __forceinline__ void prefill_setup(const AttnParams& p, Smem& sm,
       const int sq = tid * chunk + i;
       if (sq < S) {
         sm.few_start[sq] = run2;
-        run2 += kMods ? 0 : few_rows<kTree, kAlt>(sm.seq_qlen[sq], sm.seq_ctx[sq]);
+        run2 += few_rows<kTree, kAlt>(sm.seq_qlen[sq], sm.seq_ctx[sq]);
         sm.seq_start[sq] = run;
         const int c = sm.seq_ctx[sq];
-        const int tiles = tiles_of(sm.seq_qlen[sq]);
+        const int tiles = (sm.seq_qlen[sq] * g + kRowsM - 1) / kRowsM;
         run += c > 0 ? (kAlt ? tiles : (tiles + 1) / 2) * key_chunks<kAlt>(p, c) : 0;
       }
     }
@@ -775,7 +576,7 @@ __device__ __forceinline__ void prefill_setup(const AttnParams& p, Smem& sm,
 // The TMA producer warps (9..11) of a prefill launch: per work item the query
 // tile(s), then per key tile its K boxes, the tail rows of V where the tile
 // holds the context's partial last block, and its V boxes, into the ring.
-template <bool kAlt, bool kFP8, bool kMods = false>
+template <bool kAlt, bool kFP8>
 __device__ __forceinline__ void prefill_producers(const AttnParams& p, Smem& sm,
                                                   const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                                   const CUtensorMap& tm_q, int kv_rows, int cta,
@@ -802,8 +603,7 @@ __device__ __forceinline__ void prefill_producers(const AttnParams& p, Smem& sm,
     // read ahead of its use, checked when used
     auto fetch = [&](int c) -> int {
       const int b = 32 * c + lane;
-      return (kMods ? b >= x.lo_block && b < x.end_block
-                    : b < (x.ctx + kBlockSize - 1) / kBlockSize)
+      return b < (x.ctx + kBlockSize - 1) / kBlockSize
                  ? __ldg(p.block_tables + (size_t)x.trow * p.max_blocks_per_seq + b)
                  : kBeyond;
     };
@@ -881,16 +681,14 @@ __device__ __forceinline__ void prefill_producers(const AttnParams& p, Smem& sm,
       ++ntail;
       return true;
     };
-    while (ok && next_item<kAlt, kFP8, kMods>(p, sm, idx, total, x, ncta)) {
-      if (kMods && x.nk == 0) continue;  // no row of the item sees a key
+    while (ok && next_item<kAlt, kFP8>(p, sm, idx, total, x, ncta)) {
       bool good = true;
       if (pw == 0 && lane == 0) {
         if (nitem >= 1) good = wait_bar(&sm.q_empty, (nitem - 1) & 1, abort, lim);
         if (good) {
           // shared-prefix mode: one query tile, in q[1]
           const int nq = alt ? 1 : (x.nt[1] > 0 ? 2 : 1);
-          mbar_arrive_expect_tx(&sm.q_full,
-                                nq * (kMods ? kRowsM / g * g * (kD * 2) : kTileBytes));
+          mbar_arrive_expect_tx(&sm.q_full, nq * kTileBytes);
           for (int qt = 0; qt < nq; ++qt) {
             uint8_t* dq = &sm.q[alt ? 1 : qt][0];
             const int tok = x.q0 + x.t0[qt];
@@ -954,52 +752,6 @@ __device__ __forceinline__ void prefill_producers(const AttnParams& p, Smem& sm,
   }
 }
 
-// Biased mode: the scores of a tile's 128 keys from kbase on, modified in place.
-// `a` takes a raw score to base-2 units.  Returns the positive factor still to be
-// applied to the result, which the exponential's own multiply-add then carries:
-// the caller's scale where nothing is modified, the cap after tanh, 1 after a bias.
-__device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, float a, float slope,
-                                               int pos, int kbase) {
-  float f = fmaxf(fabsf(a), 1e-30f);
-  if (p.softcap > 0.0f) {
-    const float c = a / p.cap_log2;
-    float top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kTileKeys; ++i) {
-      sv[i] *= c;
-      top = fmaxf(top, fabsf(sv[i]));
-    }
-    // scores well below the cap, the usual case: the polynomial alone, on packed pairs
-    if (__all_sync(kFull, top <= kTanhPoly)) {
-#pragma unroll
-      for (int i = 0; i < kTileKeys; i += 2) {
-        const float2 x = make_float2(sv[i], sv[i + 1]), x2 = __fmul2_rn(x, x);
-        float2 q = __ffma2_rn(x2, make_float2(kTanh9, kTanh9), make_float2(kTanh7, kTanh7));
-        q = __ffma2_rn(x2, q, make_float2(kTanh5, kTanh5));
-        q = __ffma2_rn(x2, q, make_float2(kTanh3, kTanh3));
-        const float2 y = __ffma2_rn(__fmul2_rn(x2, x), q, x);
-        sv[i] = y.x;
-        sv[i + 1] = y.y;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kTileKeys; ++i) sv[i] = cap_tanh(sv[i]);
-    }
-    f = p.cap_log2;
-  } else if (a < 0.0f) {
-#pragma unroll
-    for (int i = 0; i < kTileKeys; ++i) sv[i] = -sv[i];
-  }
-  if (p.alibi) {
-    const float d0 = (float)(pos - kbase);
-#pragma unroll
-    for (int i = 0; i < kTileKeys; ++i)
-      sv[i] = fmaf(sv[i], f, -slope * fabsf(d0 - (float)i));
-    f = 1.0f;
-  }
-  return f;
-}
-
 // kFP8: E4M3 caches (not with kAlt).  K and V tiles are [128 keys][128 B] (16
 // KB, one box per block), eight to the ring; the query comes split per row as
 // q / s = hi + lo in E4M3 (rows of hi, then the same rows of lo, at token
@@ -1007,14 +759,11 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
 // on 8-bit MMAs, scaled by s and k_scale in the softmax; P is E4M3 of
 // kPScale8 w in TMEM, O = P V on 8-bit MMAs, divided by kPScale8 l and
 // multiplied by v_scale.
-template <class QT, bool kTree, bool kAlt, bool kFP8 = false, bool kMods = false>
+template <class QT, bool kTree, bool kAlt, bool kFP8 = false>
 __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensorMap& tm_k,
                                              const CUtensorMap& tm_v, const CUtensorMap& tm_q,
                                              int kv_rows, int cta, int ncta, uint8_t* smem_raw) {
   static_assert(!(kFP8 && kAlt), "E4M3 caches have no shared-prefix mode");
-  static_assert(!(kMods && (kTree || kAlt)), "modifiers are for causal chunks");
-  constexpr float kScaleP = kMods ? kPScaleMods8 : kPScale8;
-  constexpr float kMove = kFP8 ? (kMods ? kRescaleMods8 : kRescaleAt8) : kRescaleAt;
   constexpr int kStageBytes = kFP8 ? kTileBytes / 2 : kTileBytes;
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~uintptr_t(1023));
@@ -1025,14 +774,14 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
   constexpr uint32_t kIdescO = tc::idesc_f16(kFP8 ? 0u : kAB, 0, 1, 128, 128);
   const int g = p.group;
 
-  prefill_setup<kTree, kAlt, kMods>(p, sm, tm_k, tm_v, tm_q);
+  prefill_setup<kTree, kAlt>(p, sm, tm_k, tm_v, tm_q);
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
   const unsigned long long lim = wait_limit(p);
   const int total = sm.seq_start[p.num_seqs] * p.num_kv_heads;
 
   if (warp >= 9) {
-    prefill_producers<kAlt, kFP8, kMods>(p, sm, tm_k, tm_v, tm_q, kv_rows, cta, ncta, total, abort, lim);
+    prefill_producers<kAlt, kFP8>(p, sm, tm_k, tm_v, tm_q, kv_rows, cta, ncta, total, abort, lim);
   } else if (warp == 8) {
     // ---- MMA issuer --------------------------------------------------------------------
     // Order per item: S_a(0), S_b(0), then for each key tile t:
@@ -1099,10 +848,7 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
         if (leader) {
           const uint64_t dv = dv0 + (uint64_t)(st * (kStageBytes >> 4));
           const int ts = t == x.nk - 1 ? x.tail_step : -1;
-          if constexpr (kFP8 && kMods)
-            issue_pv8_split(tmem + kColO + qt * 128, tmem + qt * 128, dv, dtail, ts,
-                            t != x.first[qt], kIdescO);
-          else if constexpr (kFP8)
+          if constexpr (kFP8)
             issue_pv8(tmem + kColO + qt * 128, tmem + qt * 128, dv, dtail, ts, t != x.first[qt],
                       kIdescO);
           else
@@ -1147,8 +893,7 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
         }
         return true;
       };
-      while (ok && next_item<kAlt, kFP8, kMods>(p, sm, idx, total, x, ncta)) {
-        if (kMods && x.nk == 0) continue;
+      while (ok && next_item<kAlt, kFP8>(p, sm, idx, total, x, ncta)) {
         const bool ha = x.last[0] >= 0;
         const bool hb = x.last[1] >= 0;
         int kst = 0, vst = 0;
@@ -1213,7 +958,7 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
     uint32_t ns = 0, nit = 0;  // S tiles and items of this query tile
     bool ok = true;
     Item x;
-    while (ok && next_item<kAlt, kFP8, kMods>(p, sm, idx, total, x, ncta)) {
+    while (ok && next_item<kAlt, kFP8>(p, sm, idx, total, x, ncta)) {
       // this warpgroup's fields of the item, in registers
       const int nt = qt ? x.nt[1] : x.nt[0];
       const int t0 = qt ? x.t0[1] : x.t0[0];
@@ -1237,30 +982,10 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
 #pragma unroll 4
           for (int i = 0; i < kD / 4; ++i) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (kMods && valid) {  // no row of the tile sees a key
-          int lo, hi;
-          key_interval(p, x.q0 + t0 + tok, pos0 + tok, x.ctx, x.bidir, &lo, &hi);
-          if (lo < hi) flag_error(p.errors, PKV_DEVERR_CONTEXT);  // first keys that decrease
-          uint4* z = reinterpret_cast<uint4*>(static_cast<OutT*>(p.out) + head * kD);
-#pragma unroll 4
-          for (int i = 0; i < kD / 8; ++i) z[i] = make_uint4(0, 0, 0, 0);
-        }
         continue;
       }
       const int qpos = pos0 + (kAlt ? 0 : tok);
       // E4M3 caches: the row's query scale s (q / s = hi + lo) joins the score scale
-      // biased mode: the row's keys (rows past the tile's tokens: any)
-      int key_lo = 0, key_hi = INT_MAX;
-      float slope = 0.0f;
-      if constexpr (kMods) {
-        if (valid) {
-          key_interval(p, x.q0 + t0 + tok, qpos, x.ctx, x.bidir, &key_lo, &key_hi);
-          // first keys that decrease from row to row: blocks before lo_block are not here
-          if (key_lo < key_hi && key_lo < x.lo_block * kBlockSize)
-            flag_error(p.errors, PKV_DEVERR_CONTEXT);
-          if (p.alibi) slope = __ldg(p.alibi + x.kvh * g + tid % g) * kLog2e;
-        }
-      }
       const float qa_r = kFP8 ? qa * (valid ? __ldg(p.q8_scale + head) : 1.0f) : qa;
       // draft-tree mode: the row's visible chunk keys, from the chunk's first position
       const int cbase = pos0 - t0;
@@ -1278,22 +1003,7 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
         for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_col + 32 * c, sv + 32 * c);
         tc::tmem_wait_ld();
         const int kbase = t * kTileKeys;
-        float qa_t = qa_r;  // scale of this tile's (modified) scores
-        if constexpr (kMods) {
-          if (__all_sync(kFull, key_hi <= kbase || key_lo >= kbase + kTileKeys || key_lo >= key_hi)) {
-            // no row of this warp sees a key of the tile
-#pragma unroll
-            for (int c = 0; c < 16; ++c) sv[c] = 0.0f;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) tc::tmem_st16(s_col + 16 * h, sv);
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            tc::named_sync(1 + qt, 128);
-            if (tid == 0) mbar_arrive(&sm.p_ready[qt]);
-            continue;
-          }
-          qa_t = modify_scores(p, sv, kFP8 ? (neg ? -qa_r : qa_r) : qs, slope, qpos, kbase);
-        } else if (neg) {
+        if (neg) {
 #pragma unroll
           for (int c = 0; c < kTileKeys; ++c) sv[c] = -sv[c];
         }
@@ -1321,14 +1031,7 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
             sv[c] = (vw[c >> 5] >> (c & 31)) & 1u ? sv[c] : -INFINITY;
             mx[c & 7] = fmaxf(mx[c & 7], sv[c]);
           }
-        } else if (kMods && !__all_sync(kFull, key_lo <= kbase && key_hi >= kbase + kTileKeys)) {
-          // an interval of some row of the warp ends in this tile
-#pragma unroll
-          for (int c = 0; c < kTileKeys; ++c) {
-            sv[c] = kbase + c >= key_lo && kbase + c < key_hi ? sv[c] : -INFINITY;
-            mx[c & 7] = fmaxf(mx[c & 7], sv[c]);
-          }
-        } else if (!kMods && kbase + kTileKeys - 1 > pos0) {
+        } else if (kbase + kTileKeys - 1 > pos0) {
           // the causal boundary crosses this tile: hidden keys become -inf
 #pragma unroll
           for (int c = 0; c < kTileKeys; ++c) {
@@ -1342,32 +1045,18 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
         }
         const float mt =
             fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * qa_t;
+                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * qa_r;
         // move the running max (and rescale O) only on a large increase; O is
         // complete up to tile t-1 (S of tile t was issued after its product)
-        const bool need = mt > m_run + kMove;
+        const bool need = mt > m_run + (kFP8 ? kRescaleAt8 : kRescaleAt);
         float alpha = 1.0f;
-        // (biased mode: a row's first visible key may come in a later tile)
-        const bool fresh = kMods && m_run == -INFINITY;
         if (need) {
           alpha = (t == first) ? 0.0f : fast_exp2(m_run - mt);
           m_run = mt;
 #pragma unroll
           for (int i = 0; i < 4; ++i) l2[i] = __fmul2_rn(l2[i], make_float2(alpha, alpha));
         }
-        // a row that has seen no key yet: 2^(-inf - 0) = 0
-        const float m_exp = kMods && m_run == -INFINITY ? 0.0f : m_run;
-        if constexpr (kFP8 && kMods) {
-          // hi terms over the first 32 columns of S, lo terms over the next
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float ph[16], pl[16];
-            exp_quads8_split(sv + h * 64, qa_t, m_exp, l2, ph, pl);
-            exp_quads8_split(sv + h * 64 + 32, qa_t, m_exp, l2, ph + 8, pl + 8);
-            tc::tmem_st16(s_col + 16 * h, ph);
-            tc::tmem_st16(s_col + 32 + 16 * h, pl);
-          }
-        } else if constexpr (kFP8) {
+        if constexpr (kFP8) {
           // P over the first 32 columns of S: keys 4c .. 4c + 3 in column c
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -1381,7 +1070,7 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             float pk[16];
-            exp_pairs<QT>(sv + h * 32, qa_t, m_exp, l2, pk);
+            exp_pairs<QT>(sv + h * 32, qa_r, m_run, l2, pk);
             tc::tmem_st16(s_col + 16 * h, pk);
           }
         }
@@ -1393,7 +1082,7 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
             tc::tmem_ld32(o_col + 32 * c, ov);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = kMods && fresh && need ? 0.0f : ov[i] * alpha;
+            for (int i = 0; i < 32; ++i) ov[i] *= alpha;
             tc::tmem_st32(o_col + 32 * c, ov);
           }
         }
@@ -1410,28 +1099,18 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
       const float l = ((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y)) +
                       ((l2[2].x + l2[2].y) + (l2[3].x + l2[3].y));
       // (E4M3: P held kPScale8 w, and V its codes: v_scale / (kPScale8 l))
-      const bool empty = kMods && key_lo >= key_hi;  // zeros, whatever O and l hold
-      const float inv =
-          valid && !empty ? (kFP8 ? p.v_scale / (kScaleP * l) : 1.0f / l) : 0.0f;
+      const float inv = valid ? (kFP8 ? p.v_scale / (kPScale8 * l) : 1.0f / l) : 0.0f;
       OutT* orow = static_cast<OutT*>(p.out) + head * kD;
       // shared-prefix mode: the normalised partial and its log-sum-exp (base 2,
       // scaled units), in the warpgroup's slot of the chunk
       const bool part = kAlt && slot < p.max_parts;
       float* prow = part ? p.o_part + (head * p.max_parts + slot) * kD : nullptr;
       if (part && valid) p.lse[head * p.max_parts + slot] = m_run + log2f(l);
-      bool odd = false;  // an output that is not finite
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         float ov[32];
         tc::tmem_ld32(o_col + 32 * c, ov);
         tc::tmem_wait_ld();
-        if constexpr (kMods) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            ov[i] = empty ? 0.0f : ov[i];
-            odd |= !(fabsf(ov[i] * inv) < INFINITY);
-          }
-        }
         if (part) {
           if (valid) {
 #pragma unroll
@@ -1440,7 +1119,7 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
                   make_float4(ov[q4 * 4] * inv, ov[q4 * 4 + 1] * inv, ov[q4 * 4 + 2] * inv,
                               ov[q4 * 4 + 3] * inv);
           }
-        } else if (valid && (kMods || !(!kAlt && (kTree ? cbase < kFewKeys : qpos < kFewKeys)))) {
+        } else if (valid && !(!kAlt && (kTree ? cbase < kFewKeys : qpos < kFewKeys))) {
           // (rows of few keys are written by few_key_rows after the loop)
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
@@ -1453,19 +1132,13 @@ __device__ __forceinline__ void prefill_body(const AttnParams& p, const CUtensor
           }
         }
       }
-      if (kMods && odd && valid && !empty) sm.redo = 1;
       tc::fence_before_sync();
       tc::named_sync(1 + qt, 128);
       if (tid == 0) mbar_arrive(&sm.o_free[qt]);
       ++nit;
     }
     if (!ok && tid == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
-    if constexpr (kMods) {
-      // (each warp sees what its own lanes set: __syncwarp; other warps' rows are theirs)
-      __syncwarp();
-      if (ok && *static_cast<volatile int*>(&sm.redo))
-        redo_rows<QT, kFP8>(p, sm, cta, ncta, total, qt, warp & 3);
-    } else if constexpr (!kAlt) {
+    if constexpr (!kAlt) {
       if (ok) few_key_rows<QT, kTree, Smem, kFP8>(p, sm, cta * 256 + qt * 128 + tid, ncta * 256);
     }
   }
