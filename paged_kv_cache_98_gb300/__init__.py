@@ -422,52 +422,75 @@ def copy_blocks(k_cache, v_cache, block_pairs, device_errors=None, stream=None):
     _check("pkv_copy_blocks", rc)
 
 
-def _on_device(device, stream, *tensors):
-    """(stream, guard) of a call whose tensors must be on `device`: the stream it
+# (the raw handle of a device's current stream, without a Stream object around it)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_device(device, stream, specs):
+    """Checks the tensors of a call and returns (stream handle, guard): the stream it
     launches on, and a context that makes `device` the current one.
 
-    On another stream than the current one the tensors are marked as used there,
-    so that the allocator does not hand out their memory before the launch has
-    run; ordering that stream behind the work that fills them stays the caller's."""
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("tensors must be on the same CUDA device")
+    specs: (name, tensor or None, dtype, shape) each; they must be contiguous and on
+    `device`.  On another stream than the current one the tensors are marked as used
+    there, so that the allocator does not hand out their memory before the launch
+    has run; ordering that stream behind the work that fills them stays the
+    caller's."""
+    for name, t, dtype, shape in specs:
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, as the other tensors are")
+    return _stream_on(device, stream, [x[1] for x in specs] if stream is not None else ())
+
+
+def _word(t):
+    """The device error word's spec: any tensor on the device, its first four bytes."""
+    return ("device_errors", t, None, None) if t is None else ("device_errors", t, t.dtype, t.shape)
+
+
+def _stream_on(device, stream, tensors):
     if device.type != "cuda":
         raise ValueError("tensors must be on the CUDA device")
+    index = device.index
+    guard = _HERE_ALREADY if index == torch.cuda.current_device() else torch.cuda.device(device)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        return (_raw_stream(index) if _raw_stream is not None
+                else torch.cuda.current_stream(device).cuda_stream), guard
+    if stream.device != device:
         raise ValueError("the stream belongs to another device than the tensors")
-    elif stream != torch.cuda.current_stream(device):
+    if stream != torch.cuda.current_stream(device):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-    away = device.index is not None and device.index != torch.cuda.current_device()
-    return stream, (torch.cuda.device(device) if away else contextlib.nullcontext())
+    return stream.cuda_stream, guard
+
+
+_HERE_ALREADY = contextlib.nullcontext()
 
 
 def _scratch_on(stream, nbytes, workspace, device):
     """A workspace of nbytes: the caller's, or one that the launch's stream owns (so
-    that the allocator hands it out again only behind the launch)."""
+    that the allocator hands it out again only behind the launch).  `stream` as the
+    caller gave it, None for the current one."""
     if nbytes == 0:
         return None, 0
     if workspace is None:
-        with torch.cuda.stream(stream):
+        if stream is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the tensors' device")
-    return workspace, workspace.numel() * workspace.element_size()
-
-
-def _want(name, t, dtype, shape):
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    elif stream is not None:
+        workspace.record_stream(stream)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def build_step_maps(block_tables, context_lens, query_start_loc, slot_mapping, positions,
@@ -481,28 +504,23 @@ def build_step_maps(block_tables, context_lens, query_start_loc, slot_mapping, p
     int64 and positions [T] int32 (-1 behind the last sequence's tokens).
     In/out: request_tables [R, MB] int32.  Inputs: rows, cached_lens, q_lens [S]
     int32 (a negative row: a padding sequence), new_blocks [N] int32."""
-    S, (R, MB), T = rows.numel(), request_tables.shape, slot_mapping.numel()
-    _want("block_tables", block_tables, torch.int32, (S, MB))
-    _want("context_lens", context_lens, torch.int32, (S,))
-    _want("query_start_loc", query_start_loc, torch.int32, (S + 1,))
-    _want("slot_mapping", slot_mapping, torch.int64, (T,))
-    _want("positions", positions, torch.int32, (T,))
-    _want("request_tables", request_tables, torch.int32, (R, MB))
-    _want("rows", rows, torch.int32, (S,))
-    _want("cached_lens", cached_lens, torch.int32, (S,))
-    _want("q_lens", q_lens, torch.int32, (S,))
-    _want("new_blocks", new_blocks, torch.int32, (new_blocks.numel(),))
-    stream, guard = _on_device(request_tables.device, stream, request_tables, block_tables, context_lens,
-                               query_start_loc, slot_mapping, positions, rows, cached_lens, q_lens,
-                               new_blocks, device_errors)
+    S, (R, MB), T, N = rows.numel(), request_tables.shape, slot_mapping.numel(), new_blocks.numel()
+    i32 = torch.int32
+    raw, guard = _on_device(request_tables.device, stream, (
+        ("block_tables", block_tables, i32, (S, MB)), ("context_lens", context_lens, i32, (S,)),
+        ("query_start_loc", query_start_loc, i32, (S + 1,)),
+        ("slot_mapping", slot_mapping, torch.int64, (T,)), ("positions", positions, i32, (T,)),
+        ("request_tables", request_tables, i32, (R, MB)), ("rows", rows, i32, (S,)),
+        ("cached_lens", cached_lens, i32, (S,)), ("q_lens", q_lens, i32, (S,)),
+        ("new_blocks", new_blocks, i32, (N,)), _word(device_errors)))
     with guard:
-        rc = load().pkv_build_step_maps(
+        rc = (_lib or load()).pkv_build_step_maps(
             block_tables.data_ptr(), context_lens.data_ptr(), query_start_loc.data_ptr(),
             slot_mapping.data_ptr(), positions.data_ptr(), request_tables.data_ptr(),
             rows.data_ptr(), cached_lens.data_ptr(), q_lens.data_ptr(), new_blocks.data_ptr(), S, R,
-            MB, T, new_blocks.numel(), block_size, num_blocks, _ptr(device_errors),
-            stream.cuda_stream)
-    _check("pkv_build_step_maps", rc)
+            MB, T, N, block_size, num_blocks, _ptr(device_errors), raw)
+    if rc:
+        raise PagedKVError("pkv_build_step_maps", rc)
 
 
 def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
@@ -543,48 +561,56 @@ def rotary_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, 
     if inv.ndim != 1:
         raise ValueError("inv_freq must be one-dimensional")
     for name, t, heads in (("q", q, H), ("k", k, hkv), ("v", v, hkv)):
-        if t.dtype != q.dtype or tuple(t.shape) != (T, heads, D):
+        if t.dtype is not q.dtype or t.shape != (T, heads, D):
             raise ValueError(f"{name} must be [{T}, {heads}, {D}] of q's dtype")
+        if t.device != q.device:
+            raise ValueError(f"{name} must be on {q.device}, as q is")
         if T and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
             raise ValueError(f"{name}: a token's heads must be contiguous")
-    _want("q_out", q_out, q.dtype, (T, H, D))
-    _want("slot_mapping", slot_mapping, torch.int64, (T,))
-    _want("positions", positions, torch.int32, (T,))
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _want(name, c, k_cache.dtype, (k_cache.shape[0], hkv, k_cache.shape[2], D))
-    stream, guard = _on_device(q.device, stream, q_out, q, k, v, k_cache, v_cache, slot_mapping,
-                               positions, device_errors)
+    nb, _, bs, _ = k_cache.shape
+    raw, guard = _on_device(q.device, stream, (
+        ("q_out", q_out, q.dtype, (T, H, D)), ("slot_mapping", slot_mapping, torch.int64, (T,)),
+        ("positions", positions, torch.int32, (T,)),
+        ("k_cache", k_cache, k_cache.dtype, (nb, hkv, bs, D)),
+        ("v_cache", v_cache, k_cache.dtype, (nb, hkv, bs, D)),
+        _word(device_errors)))
+    if stream is not None:
+        _stream_on(q.device, stream, (q, k, v))
     # (a single token's stride is never stepped)
-    qs, ks, vs = (t.stride(0) if T > 1 else h * D for t, h in ((q, H), (k, hkv), (v, hkv)))
+    qs, ks, vs = (q.stride(0), k.stride(0), v.stride(0)) if T > 1 else (H * D, hkv * D, hkv * D)
     with guard:
-        rc = load().pkv_rotary_and_cache(
+        rc = (_lib or load()).pkv_rotary_and_cache(
             q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), inv.ctypes.data, qs,
-            ks, vs, T, H, hkv, D, k_cache.shape[2], k_cache.shape[0], 2 * inv.size,
-            _ROTARY_LAYOUT[layout], attn_factor, _dtype_code(q), _dtype_code(k_cache), k_scale,
-            v_scale, _ptr(device_errors), stream.cuda_stream)
-    _check("pkv_rotary_and_cache", rc)
+            ks, vs, T, H, hkv, D, bs, nb, 2 * inv.size, _ROTARY_LAYOUT[layout], attn_factor,
+            _dtype_code(q), _dtype_code(k_cache), k_scale, v_scale, _ptr(device_errors), raw)
+    if rc:
+        raise PagedKVError("pkv_rotary_and_cache", rc)
     return q_out
 
 
-def _biased_args(out, q, k_cache, v_cache, block_tables, context_lens, softcap, alibi_slopes,
-                 window, key_start, prefix_lens):
-    """Checks the tensors of a biased attention call; returns its pkv_score_mods."""
+def _biased_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, softcap,
+                 alibi_slopes, window, key_start, prefix_lens, device_errors, stream):
+    """Checks the tensors of a biased attention call; returns its pkv_score_mods, the
+    stream handle and the device guard."""
     rows, H, D = q.shape
     nb, hkv, bs, _ = k_cache.shape
-    S = context_lens.numel()
-    _want("q", q, q.dtype, (rows, H, D))
-    _want("out", out, q.dtype, (rows, H, D))
-    _want("k_cache", k_cache, k_cache.dtype, (nb, hkv, bs, D))
-    _want("v_cache", v_cache, k_cache.dtype, (nb, hkv, bs, D))
-    _want("context_lens", context_lens, torch.int32, (S,))
-    _want("block_tables", block_tables, torch.int32, (S, block_tables.shape[-1]))
-    _want("alibi_slopes", alibi_slopes, torch.float32, (H,))
-    _want("key_start", key_start, torch.int32, (rows,))
-    _want("prefix_lens", prefix_lens, torch.int32, (S,))
+    S, i32 = context_lens.numel(), torch.int32
+    kv = (nb, hkv, bs, D)
+    if not 0 <= window < 1 << 31:
+        raise ValueError("window must be at least 0 and below 2^31")
+    raw, guard = _on_device(q.device, stream, (
+        ("q", q, q.dtype, (rows, H, D)), ("out", out, q.dtype, (rows, H, D)),
+        ("k_cache", k_cache, k_cache.dtype, kv), ("v_cache", v_cache, k_cache.dtype, kv),
+        ("context_lens", context_lens, i32, (S,)),
+        ("block_tables", block_tables, i32, (S, block_tables.shape[-1])),
+        ("query_start_loc", query_start_loc, i32, (S + 1,)),
+        ("alibi_slopes", alibi_slopes, torch.float32, (H,)),
+        ("key_start", key_start, i32, (rows,)), ("prefix_lens", prefix_lens, i32, (S,)),
+        _word(device_errors)))
     return _ScoreMods(softcap, alibi_slopes.data_ptr() if alibi_slopes is not None else None,
                       window, key_start.data_ptr() if key_start is not None else None,
-                      prefix_lens.data_ptr() if prefix_lens is not None else None)
+                      prefix_lens.data_ptr() if prefix_lens is not None else None), raw, guard
 
 
 def decode_biased_workspace_size(num_seqs: int, num_heads: int, head_dim: int,
@@ -604,26 +630,25 @@ def paged_attention_decode_biased(out, q, k_cache, v_cache, block_tables, contex
     (key_start [S] int32): pkv_paged_attention_decode_biased.  max_context_len and
     workspace (>= decode_biased_workspace_size bytes) as for
     paged_attention_decode."""
-    mods = _biased_args(out, q, k_cache, v_cache, block_tables, context_lens, softcap,
-                        alibi_slopes, window, key_start, None)
     S, H, D = q.shape
-    nb, hkv, bs, _ = k_cache.shape
     if context_lens.numel() != S:
         raise ValueError("context_lens must have one entry per query row")
-    stream, guard = _on_device(q.device, stream, out, q, k_cache, v_cache, block_tables, context_lens,
-                               alibi_slopes, key_start, device_errors)
+    mods, raw, guard = _biased_args(out, q, k_cache, v_cache, block_tables, context_lens, None, softcap,
+                                    alibi_slopes, window, key_start, None, device_errors, stream)
+    nb, hkv, bs, _ = k_cache.shape
     if max_context_len is None:
         max_context_len = int(context_lens.max().item()) if S else 0
+    lib = _lib or load()
     with guard:
-        ws, wsb = _scratch_on(stream, decode_biased_workspace_size(S, H, D, max_context_len, window),
-                              workspace, q.device)
-        rc = load().pkv_paged_attention_decode_biased(
+        ws, wsb = _scratch_on(stream, lib.pkv_decode_biased_workspace_size(
+            S, H, D, max_context_len, window), workspace, q.device)
+        rc = lib.pkv_paged_attention_decode_biased(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), context_lens.data_ptr(), ctypes.addressof(mods), S, H, hkv, D,
             bs, block_tables.shape[1], nb, max_context_len, scale, _dtype_code(q),
-            _dtype_code(k_cache), k_scale, v_scale, _ptr(ws), wsb, _ptr(device_errors),
-            stream.cuda_stream)
-    _check("pkv_paged_attention_decode_biased", rc)
+            _dtype_code(k_cache), k_scale, v_scale, ws, wsb, _ptr(device_errors), raw)
+    if rc:
+        raise PagedKVError("pkv_paged_attention_decode_biased", rc)
     return out
 
 
@@ -646,29 +671,28 @@ def paged_attention_prefill_biased(out, q, k_cache, v_cache, block_tables, conte
     window, a first key per query row (key_start [total_q] int32: document masks)
     and keys seen in both directions (prefix_lens [S] int32):
     pkv_paged_attention_prefill_biased."""
-    mods = _biased_args(out, q, k_cache, v_cache, block_tables, context_lens, softcap,
-                        alibi_slopes, window, key_start, prefix_lens)
     TQ, H, D = q.shape
+    mods, raw, guard = _biased_args(out, q, k_cache, v_cache, block_tables, context_lens,
+                                    query_start_loc, softcap, alibi_slopes, window, key_start,
+                                    prefix_lens, device_errors, stream)
     nb, hkv, bs, _ = k_cache.shape
     S = context_lens.numel()
-    _want("query_start_loc", query_start_loc, torch.int32, (S + 1,))
-    stream, guard = _on_device(q.device, stream, out, q, k_cache, v_cache, block_tables, context_lens,
-                               query_start_loc, alibi_slopes, key_start, prefix_lens, device_errors)
     if max_context_len is None:
         max_context_len = int(context_lens.max().item()) if S else 0
     if max_q_len is None:
         max_q_len = int((query_start_loc[1:] - query_start_loc[:-1]).max().item()) if S else 0
     qd, kd = _dtype_code(q), _dtype_code(k_cache)
+    lib = _lib or load()
     with guard:
-        need = prefill_biased_workspace_size(S, TQ, H, hkv, D, max_context_len, qd, kd)
-        ws, wsb = _scratch_on(stream, need, workspace, q.device)
-        rc = load().pkv_paged_attention_prefill_biased(
+        ws, wsb = _scratch_on(stream, lib.pkv_prefill_biased_workspace_size(
+            S, TQ, H, hkv, D, max_context_len, qd, kd), workspace, q.device)
+        rc = lib.pkv_paged_attention_prefill_biased(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), context_lens.data_ptr(), query_start_loc.data_ptr(),
             ctypes.addressof(mods), S, TQ, max_q_len, H, hkv, D, bs, block_tables.shape[1], nb,
-            max_context_len, scale, qd, kd, k_scale, v_scale, _ptr(ws), wsb, _ptr(device_errors),
-            stream.cuda_stream)
-    _check("pkv_paged_attention_prefill_biased", rc)
+            max_context_len, scale, qd, kd, k_scale, v_scale, ws, wsb, _ptr(device_errors), raw)
+    if rc:
+        raise PagedKVError("pkv_paged_attention_prefill_biased", rc)
     return out
 
 

@@ -15,11 +15,14 @@
 // fraction go through sincospif.  No table is read, so there is none to size for
 // the longest context.
 //
-// A CTA takes a tile of tokens and a share of their rows: it first turns the
-// tile's angles into cosines and sines in shared memory (one thread per token
-// and pair), then streams rows, a thread per 16-byte chunk (the half layout: the
-// two chunks of eight pairs).  Rotation in fp32, one rounding on the way out (to
-// 16 bits, or straight to E4M3 after the division by the scale).  HBM bound.
+// A warp takes a token, or a share of its rows.  A row is D / 8 lanes, one 16-byte
+// chunk each, so two (D = 128) or four rows move at once, four times over before
+// the first is needed; a lane's chunk is the same in every row, so its cosines and
+// sines are computed once and stay in registers.  In the half layout the other
+// element of a pair is in another lane's chunk and comes by shuffle (or, where the
+// halves are not whole chunks, from global memory again).  Rotation in fp32, one
+// rounding on the way out (to 16 bits, or straight to E4M3 after the division by the
+// scale).  HBM bound for many tokens, by the launch for few.
 
 #include <cmath>
 
@@ -30,7 +33,9 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = 64;  // head_dim 128
+constexpr int kDeep = 4;       // row groups loaded ahead
 
 struct RotParams {
   uint8_t* q_out;
@@ -42,16 +47,15 @@ struct RotParams {
   const int64_t* slots;
   const int32_t* positions;
   long long q_stride, k_stride, v_stride;  // elements between tokens
-  int num_tokens, num_heads, num_kv_heads, head_dim, pairs;
+  int num_tokens, num_heads, num_kv_heads, pairs;
+  int parts, rows_per_part;  // warps per token, and the rows (of Q, K, V in order) of each
   long long num_slots;
   float factor, k_scale, v_scale;
   uint32_t* errors;
-  int tile;  // tokens per CTA
   unsigned long long phase[kMaxPairs];
 };
 
-template <class T>
-__device__ __forceinline__ uint32_t e4m3x4(const T* f, float scale) {
+__device__ __forceinline__ uint32_t e4m3x4(const float* f, float scale) {
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -60,145 +64,159 @@ __device__ __forceinline__ uint32_t e4m3x4(const T* f, float scale) {
   return w;
 }
 
-// Where a row of Q, K or V goes: 16-bit elements, or E4M3 codes of x / scale.
-struct Dst {
-  uint8_t* p;
-  bool fp8;
-  float scale;
-};
-
-template <class QT, int N>
-__device__ __forceinline__ void load_n(const uint8_t* src, float* f) {
-  if constexpr (N == 8) {
-    to_float(__ldg(reinterpret_cast<const uint4*>(src)), f, QT());
-  } else {
-    f[0] = static_cast<float>(*reinterpret_cast<const typename QT::T*>(src));
-  }
-}
-
-template <class QT, bool FP8, int N>
-__device__ __forceinline__ void store_n(const Dst& d, int elem, const float* f) {
-  if (FP8 && d.fp8) {
-    if constexpr (N == 8) {
-      *reinterpret_cast<uint2*>(d.p + elem) = make_uint2(e4m3x4(f, d.scale), e4m3x4(f + 4, d.scale));
-    } else {
-      d.p[elem] = __nv_cvt_float_to_fp8(__fdiv_rn(f[0], d.scale), __NV_SATFINITE, __NV_E4M3);
-    }
-  } else if constexpr (N == 8) {
-    *reinterpret_cast<uint4*>(d.p + 2 * (size_t)elem) = pack8(f, QT());
-  } else {
-    store_out(reinterpret_cast<typename QT::T*>(d.p) + elem, f[0]);
-  }
-}
-
-// kHalf: half layout, else interleaved.  N: elements per access, 8, or 1 for a
-// half layout whose halves are not whole 16-byte chunks.
-template <class QT, bool FP8, bool kHalf, int N>
+// kHalf: half layout, else interleaved.  kWhole: the half layout's halves are whole
+// 16-byte chunks.
+template <class QT, bool FP8, int D, bool kHalf, bool kWhole>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotParams p) {
-  extern __shared__ float trig[];  // [tile][2][pairs]: cosines, then sines
-  const int t0 = blockIdx.x * p.tile, nt = min(p.tile, p.num_tokens - t0);
-  for (int i = threadIdx.x; i < nt * p.pairs; i += kThreads) {
-    const int t = i / p.pairs, j = i - t * p.pairs;
-    const int pos = __ldg(p.positions + t0 + t);
-    const unsigned long long turn = (unsigned long long)(long long)pos * p.phase[j];
-    float s, c;
-    sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
-    trig[(2 * t) * p.pairs + j] = c * p.factor;
-    trig[(2 * t + 1) * p.pairs + j] = s * p.factor;
-  }
-  __syncthreads();
+  using T = typename QT::T;
+  constexpr int kLanes = D / 8;         // lanes per row
+  constexpr int kRows = 32 / kLanes;    // rows at once
+  constexpr int kElem = FP8 ? 1 : 2;    // bytes per cache element
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, c = lane % kLanes;
+  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int tok = (int)(unit / p.parts), part = (int)(unit - (long long)tok * p.parts);
+  if (tok >= p.num_tokens) return;
+  const int pos = __ldg(p.positions + tok);
+  if (pos < 0) return;  // padding: nothing is written
+  const int64_t slot = __ldg(p.slots + tok);
+  const bool cached = slot >= 0 && slot < p.num_slots;
+  if (slot >= p.num_slots && part == 0 && lane == 0) flag_error(p.errors, PKV_DEVERR_SLOT);
+  const int H = p.num_heads, hk = p.num_kv_heads;
+  const int r_end = min((part + 1) * p.rows_per_part, cached ? H + 2 * hk : H);
 
-  const int D = p.head_dim, rot = 2 * p.pairs;
-  // units of a rotated row: the half layout's pairs of chunks, then single chunks
-  const int paired = kHalf ? p.pairs / N : 0;
-  const int per_row = kHalf ? paired + (D - rot) / N : D / N;
-  const int per_v = D / N;
-  const int rot_units = (p.num_heads + p.num_kv_heads) * per_row;
-  const int units = rot_units + p.num_kv_heads * per_v;
-  for (int i = blockIdx.y * kThreads + threadIdx.x; i < nt * units; i += gridDim.y * kThreads) {
-    const int t = i / units;
-    int u = i - t * units;
-    const int tok = t0 + t;
-    if (__ldg(p.positions + tok) < 0) continue;  // padding: nothing is written
-    const bool is_v = u >= rot_units;
-    if (is_v) u -= rot_units;
-    const int per = is_v ? per_v : per_row;
-    int h = u / per;
-    u -= h * per;
-    const uint8_t* src;
-    Dst d;
-    if (!is_v && h < p.num_heads) {
-      src = p.q + 2 * (tok * p.q_stride + (long long)h * D);
-      d = {p.q_out + 2 * ((long long)tok * p.num_heads + h) * D, false, 1.0f};
-    } else {
-      if (!is_v) h -= p.num_heads;
-      const int64_t slot = __ldg(p.slots + tok);
-      if (slot < 0) continue;  // not cached
-      if (slot >= p.num_slots) {
-        if (!is_v && h == 0 && u == 0) flag_error(p.errors, PKV_DEVERR_SLOT);
-        continue;
-      }
-      src = is_v ? p.v + 2 * (tok * p.v_stride + (long long)h * D)
-                 : p.k + 2 * (tok * p.k_stride + (long long)h * D);
-      const long long row = ((slot / kBlockSize) * p.num_kv_heads + h) * kBlockSize + slot % kBlockSize;
-      d = {(is_v ? p.v_cache : p.k_cache) + row * D * (FP8 ? 1 : 2), FP8,
-           is_v ? p.v_scale : p.k_scale};
+  // this lane's eight elements in every row; those below rot turn
+  const int e0 = 8 * c, half = p.pairs, rot = 2 * half;
+  const uint8_t* qs = p.q + 2 * (tok * p.q_stride + e0);
+  const uint8_t* ks = p.k + 2 * (tok * p.k_stride + e0);
+  const uint8_t* vs = p.v + 2 * (tok * p.v_stride + e0);
+  uint8_t* qd = p.q_out + 2 * ((long long)tok * H * D + e0);
+  const long long at = cached ? ((slot / kBlockSize) * hk * kBlockSize + slot % kBlockSize) * D + e0 : 0;
+  uint8_t* kd = p.k_cache + at * kElem;
+  uint8_t* vd = p.v_cache + at * kElem;
+  auto load = [&](int r) -> uint4 {
+    const uint8_t* s = r < H ? qs + (long long)r * (2 * D)
+                             : (r < H + hk ? ks + (long long)(r - H) * (2 * D)
+                                           : vs + (long long)(r - H - hk) * (2 * D));
+    return *reinterpret_cast<const uint4*>(s);
+  };
+  const int r0 = part * p.rows_per_part;
+  uint4 w[kDeep];
+#pragma unroll
+  for (int i = 0; i < kDeep; ++i) {
+    const int r = r0 + i * kRows + sub;
+    w[i] = r < r_end ? load(r) : make_uint4(0, 0, 0, 0);
+  }
+
+  // cosines and sines (with the factor) while the first rows are on their way
+  constexpr int kAngles = kHalf ? 8 : 4;
+  float cs[kAngles], sn[kAngles];
+#pragma unroll
+  for (int i = 0; i < kAngles; ++i) {
+    const int e = kHalf ? e0 + i : e0 + 2 * i;
+    const int j = kHalf ? (e < half ? e : e - half) : e >> 1;
+    const unsigned long long turn =
+        (unsigned long long)(long long)pos * p.phase[e < rot ? j : 0];
+    sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+    cs[i] *= p.factor;
+    // the second element of a pair adds the first one's sine, the first subtracts the other's
+    sn[i] *= kHalf && e < half ? -p.factor : p.factor;
+  }
+  // the lane that holds the other halves of this lane's pairs
+  const int other = kHalf && kWhole && e0 < rot
+                        ? sub * kLanes + (e0 < half ? c + half / 8 : c - half / 8)
+                        : lane;
+
+  for (int base = r0; base < r_end; base += kDeep * kRows) {
+    uint4 nx[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      const int r = base + (kDeep + i) * kRows + sub;
+      nx[i] = r < r_end ? load(r) : make_uint4(0, 0, 0, 0);
     }
-    const float* cs = trig + 2 * t * p.pairs;
-    const float* sn = cs + p.pairs;
-    if (kHalf && !is_v && u < paired) {
-      float a[N], b[N], x[N], y[N];
-      load_n<QT, N>(src + 2 * u * N, a);
-      load_n<QT, N>(src + 2 * (u * N + p.pairs), b);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float c = cs[u * N + e], s = sn[u * N + e];
-        x[e] = a[e] * c - b[e] * s;
-        y[e] = b[e] * c + a[e] * s;
-      }
-      store_n<QT, FP8, N>(d, u * N, x);
-      store_n<QT, FP8, N>(d, u * N + p.pairs, y);
-    } else {
-      const int e0 = is_v ? u * N : (kHalf ? rot + (u - paired) * N : u * N);
-      float a[N];
-      load_n<QT, N>(src + 2 * e0, a);
-      if constexpr (!kHalf) {
-        if (!is_v) {
+    for (int i = 0; i < kDeep; ++i) {
+      const int r = base + i * kRows + sub;
+      const bool turns = r < H + hk;
+      float x[8], y[8];
+      to_float(w[i], x, QT());
+      if constexpr (kHalf) {
+        if constexpr (kWhole) {
+          uint4 o;
+          o.x = __shfl_sync(kFull, w[i].x, other);
+          o.y = __shfl_sync(kFull, w[i].y, other);
+          o.z = __shfl_sync(kFull, w[i].z, other);
+          o.w = __shfl_sync(kFull, w[i].w, other);
+          to_float(o, y, QT());
+        } else {
+          const T* row = reinterpret_cast<const T*>(
+              (r < H ? qs + (long long)r * (2 * D) : ks + (long long)(r - H) * (2 * D)) - 2 * e0);
 #pragma unroll
-          for (int e = 0; e < N; e += 2) {
-            const int j = (e0 + e) / 2;
-            if (j < p.pairs) {
-              const float x = a[e], y = a[e + 1];
-              a[e] = x * cs[j] - y * sn[j];
-              a[e + 1] = y * cs[j] + x * sn[j];
-            }
+          for (int e = 0; e < 8; ++e)
+            y[e] = r < r_end && turns && e0 + e < rot
+                       ? (float)row[e0 + e < half ? e0 + e + half : e0 + e - half]
+                       : 0.0f;
+          __syncwarp();  // (q_out may be q: every lane has read the row)
+        }
+        if (turns) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (kWhole ? e0 < rot : e0 + e < rot) x[e] = x[e] * cs[e] + y[e] * sn[e];
+        }
+      } else if (turns) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (e0 + 2 * e < rot) {
+            const float a = x[2 * e], b = x[2 * e + 1];
+            x[2 * e] = a * cs[e] - b * sn[e];
+            x[2 * e + 1] = b * cs[e] + a * sn[e];
           }
         }
       }
-      store_n<QT, FP8, N>(d, e0, a);
+      if (r < r_end) {
+        // elements that only pass keep their bits
+        const bool pass = !turns || e0 >= rot;
+        if (r < H) {
+          *reinterpret_cast<uint4*>(qd + (long long)r * (2 * D)) = pass ? w[i] : pack8(x, QT());
+        } else {
+          const bool is_v = r >= H + hk;
+          uint8_t* d = (is_v ? vd : kd) + (long long)(r - H - (is_v ? hk : 0)) * (kBlockSize * D * kElem);
+          if constexpr (FP8) {
+            const float sc = is_v ? p.v_scale : p.k_scale;
+            *reinterpret_cast<uint2*>(d) = make_uint2(e4m3x4(x, sc), e4m3x4(x + 4, sc));
+          } else {
+            *reinterpret_cast<uint4*>(d) = pass ? w[i] : pack8(x, QT());
+          }
+        }
+      }
     }
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) w[i] = nx[i];
   }
 }
 
-template <class QT, bool FP8>
+template <class QT, bool FP8, int D>
 int launch_typed(RotParams& p, bool half, cudaStream_t stream) {
-  const bool whole = !half || p.pairs % 8 == 0;
-  auto kern = !half ? rotary_kernel<QT, FP8, false, 8>
-                    : (whole ? rotary_kernel<QT, FP8, true, 8> : rotary_kernel<QT, FP8, true, 1>);
-  // enough CTAs for every SM: tiles of four tokens, or single tokens whose rows
-  // are shared by several CTAs
-  const int sms = sm_count();
-  p.tile = p.num_tokens >= 8 * sms ? 4 : 1;
-  const int tiles = (p.num_tokens + p.tile - 1) / p.tile;
-  const int n = whole ? 8 : 1;
-  const long long units = (long long)p.tile * (p.num_heads + 2 * p.num_kv_heads) * (p.head_dim / n);
-  long long split = (4LL * sms + tiles - 1) / tiles;
-  const long long most = (units + kThreads - 1) / kThreads;
-  if (split > most) split = most;
-  if (split < 1) split = 1;
-  const dim3 grid((unsigned)tiles, (unsigned)split);
-  kern<<<grid, kThreads, (size_t)p.tile * 2 * p.pairs * sizeof(float), stream>>>(p);
+  auto kern = !half ? rotary_kernel<QT, FP8, D, false, true>
+              : p.pairs % 8 == 0 ? rotary_kernel<QT, FP8, D, true, true>
+                                 : rotary_kernel<QT, FP8, D, true, false>;
+  // Warps per token: one where the tokens alone fill the GPU (eight warps on every
+  // SM), else enough to, in steps of the rows that a warp has in flight at once.
+  const int rows = p.num_heads + 2 * p.num_kv_heads, step = kDeep * (32 / (D / 8));
+  const long long want = (8LL * sm_count() + p.num_tokens - 1) / p.num_tokens;
+  long long per = (rows + want - 1) / want;
+  per = (per + step - 1) / step * step;
+  p.rows_per_part = (int)per;
+  p.parts = (int)((rows + per - 1) / per);
+  const long long ctas = ((long long)p.num_tokens * p.parts + kWarps - 1) / kWarps;
+  if (ctas > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  kern<<<(unsigned)ctas, kThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <class QT, bool FP8>
+int launch_dim(RotParams& p, int head_dim, bool half, cudaStream_t stream) {
+  return head_dim == 64 ? launch_typed<QT, FP8, 64>(p, half, stream)
+                        : launch_typed<QT, FP8, 128>(p, half, stream);
 }
 
 }  // namespace
@@ -219,7 +237,6 @@ int launch_rotary_and_cache(const RotaryArgs& a, const double* inv_freq, cudaStr
   p.num_tokens = a.num_tokens;
   p.num_heads = a.num_heads;
   p.num_kv_heads = a.num_kv_heads;
-  p.head_dim = a.head_dim;
   p.pairs = a.rotary_dim / 2;
   p.num_slots = (long long)a.num_blocks * kBlockSize;
   p.factor = a.attn_factor;
@@ -233,10 +250,10 @@ int launch_rotary_and_cache(const RotaryArgs& a, const double* inv_freq, cudaStr
   }
   const bool fp8 = a.cache_dtype == PKV_FP8_E4M3, half = a.layout == PKV_ROTARY_HALF;
   if (a.src_dtype == PKV_BF16)
-    return fp8 ? launch_typed<BF16, true>(p, half, stream)
-               : launch_typed<BF16, false>(p, half, stream);
-  return fp8 ? launch_typed<F16, true>(p, half, stream)
-             : launch_typed<F16, false>(p, half, stream);
+    return fp8 ? launch_dim<BF16, true>(p, a.head_dim, half, stream)
+               : launch_dim<BF16, false>(p, a.head_dim, half, stream);
+  return fp8 ? launch_dim<F16, true>(p, a.head_dim, half, stream)
+             : launch_dim<F16, false>(p, a.head_dim, half, stream);
 }
 
 }  // namespace pkv
