@@ -435,6 +435,7 @@ def _on_device(device, stream, specs):
     there, so that the allocator does not hand out their memory before the launch
     has run; ordering that stream behind the work that fills them stays the
     caller's."""
+    index = -1 if device.index is None else device.index
     for name, t, dtype, shape in specs:
         if t is None:
             continue
@@ -444,7 +445,7 @@ def _on_device(device, stream, specs):
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if t.device != device:
+        if t.get_device() != index:
             raise ValueError(f"{name} must be on {device}, as the other tensors are")
     return _stream_on(device, stream, [x[1] for x in specs] if stream is not None else ())
 
@@ -560,13 +561,16 @@ def rotary_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, 
         raise ValueError(f"layout must be one of {sorted(_ROTARY_LAYOUT)}")
     if inv.ndim != 1:
         raise ValueError("inv_freq must be one-dimensional")
+    strides = []
     for name, t, heads in (("q", q, H), ("k", k, hkv), ("v", v, hkv)):
         if t.dtype is not q.dtype or t.shape != (T, heads, D):
             raise ValueError(f"{name} must be [{T}, {heads}, {D}] of q's dtype")
-        if t.device != q.device:
+        if t.get_device() != q.get_device():
             raise ValueError(f"{name} must be on {q.device}, as q is")
-        if T and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+        s0, s1, s2 = t.stride()
+        if T and (s2 != 1 or (heads > 1 and s1 != D)):
             raise ValueError(f"{name}: a token's heads must be contiguous")
+        strides.append(s0 if T > 1 else heads * D)  # (a single token's is never stepped)
     nb, _, bs, _ = k_cache.shape
     raw, guard = _on_device(q.device, stream, (
         ("q_out", q_out, q.dtype, (T, H, D)), ("slot_mapping", slot_mapping, torch.int64, (T,)),
@@ -576,13 +580,11 @@ def rotary_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, 
         _word(device_errors)))
     if stream is not None:
         _stream_on(q.device, stream, (q, k, v))
-    # (a single token's stride is never stepped)
-    qs, ks, vs = (q.stride(0), k.stride(0), v.stride(0)) if T > 1 else (H * D, hkv * D, hkv * D)
     with guard:
         rc = (_lib or load()).pkv_rotary_and_cache(
             q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), inv.ctypes.data, qs,
-            ks, vs, T, H, hkv, D, bs, nb, 2 * inv.size, _ROTARY_LAYOUT[layout], attn_factor,
+            v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), inv.ctypes.data,
+            *strides, T, H, hkv, D, bs, nb, 2 * inv.size, _ROTARY_LAYOUT[layout], attn_factor,
             _dtype_code(q), _dtype_code(k_cache), k_scale, v_scale, _ptr(device_errors), raw)
     if rc:
         raise PagedKVError("pkv_rotary_and_cache", rc)

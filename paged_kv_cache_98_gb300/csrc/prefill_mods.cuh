@@ -15,6 +15,8 @@
 //    row's first key to its last row's last one; blocks before and behind those are
 //    not read.  64 keys that every row of a warp sees are not masked; 64 that none
 //    sees cost neither scores nor exponentials, only zeros for P.
+//  * A running CTA takes over the next item not launched yet instead of owning a fixed
+//    share.
 //  * A distance bias grows towards the query, so the running max would move, and O
 //    be rescaled, at nearly every tile of a walk towards it; those kernels walk the
 //    tiles from the last one back.
@@ -57,6 +59,9 @@ constexpr int kChunk = 32;  // keys whose weights are packed and stored together
 constexpr float kMove8 = 1.0f;
 constexpr float kPMods8 = 128.0f;
 
+constexpr int kAhead = 4;   // items a CTA may ask for before the slowest warp takes them
+constexpr int kRedo = 64;   // items listed for recomputation; more of them: all items are looked at
+
 struct ModSmem {
   alignas(1024) uint8_t ring[kStages][kTileBytes];
   alignas(1024) uint8_t q[2][kTileBytes];
@@ -77,9 +82,15 @@ struct ModSmem {
   uint64_t tail_full;
   uint64_t tail_free;
   uint64_t mma_done;
+  // answers to the requests for further items: request m in slot m % kAhead
+  alignas(16) unsigned long long next[kAhead][2];
+  uint64_t next_full[kAhead];
+  uint64_t next_read[kAhead];
   uint32_t tmem_base;
   int abort;
-  int redo[2];  // a row of this query tile came out not finite
+  // items with a row that came out not finite, by query tile (a few may be listed twice)
+  int redo_n[2];
+  int redo[2][kRedo];
 };
 
 struct ModItem {
@@ -99,12 +110,15 @@ __device__ __forceinline__ int tile_of(const ModItem& x, int i) {
   return (kMods & kModBias) ? x.nk - 1 - (i - x.kt0) : i;
 }
 
+// Item k of the launch, or (k past the last one) an item without keys or rows.
 template <int kMods, bool kFP8>
-__device__ __forceinline__ bool next_mod_item(const AttnParams& p, const ModSmem& sm, int& idx,
-                                              int total, ModItem& it, int stride) {
-  if (idx >= total) return false;
-  const int k = idx;
-  idx += stride;
+__device__ __forceinline__ void make_item(const AttnParams& p, const ModSmem& sm, int k, int total,
+                                          ModItem& it) {
+  if (k >= total) {
+    it = ModItem{};
+    it.last[0] = it.last[1] = it.tail_step = -1;
+    return;
+  }
   it.kvh = k % p.num_kv_heads;
   const int pair = k / p.num_kv_heads;
   int lo = 0, hi = p.num_seqs - 1;
@@ -157,7 +171,60 @@ __device__ __forceinline__ bool next_mod_item(const AttnParams& p, const ModSmem
   it.tail_step = partial && (it.ctx - 1) / kTileKeys == it.nk - 1
                      ? ((it.ctx - 1) % kTileKeys) / (kFP8 ? 2 * kBlockSize : kBlockSize)
                      : -1;
+}
+
+// Items differ in length (documents, windows, causal chunks), so a CTA does not own a
+// fixed share: the grid has a CTA per item, and a running CTA takes over the next one
+// not launched yet (clusterlaunchcontrol) each time it begins one.  Round robin over
+// 152 CTAs left the longest 30 % above the mean for the packed documents.
+//
+// Producer warp 0 asks, at the start of its n-th item, for the item after it; every
+// warp reads the answer when it gets there.  No request follows one that found the
+// grid empty: that answer ends every warp's loop.
+__device__ __forceinline__ bool ask_next(ModSmem& sm, uint32_t m, volatile int* abort,
+                                         unsigned long long lim) {
+  const int slot = m % kAhead;
+  if (m >= kAhead && !wait_bar(&sm.next_read[slot], ((m / kAhead) - 1) & 1, abort, lim)) return false;
+  mbar_arrive_expect_tx(&sm.next_full[slot], 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::
+          "r"(smem_u32(&sm.next[slot][0])),
+      "r"(smem_u32(&sm.next_full[slot]))
+      : "memory");
   return true;
+}
+
+// The n-th item of this CTA, for the whole warp: 1 and its index in *k, 0 when there is
+// none, -1 when the wait gave up.
+__device__ __forceinline__ int take_next(ModSmem& sm, uint32_t n, int* k, volatile int* abort,
+                                         unsigned long long lim) {
+  if (n == 0) {
+    *k = blockIdx.x;
+    return 1;
+  }
+  const uint32_t m = n - 1;
+  const int slot = m % kAhead;
+  int got = -1;
+  uint32_t index = 0;
+  if ((threadIdx.x & 31) == 0 && wait_bar(&sm.next_full[slot], (m / kAhead) & 1, abort, lim)) {
+    const unsigned long long a = *static_cast<volatile unsigned long long*>(&sm.next[slot][0]);
+    const unsigned long long b = *static_cast<volatile unsigned long long*>(&sm.next[slot][1]);
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "mov.b128 r, {%2, %3};\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(yes), "=r"(index)
+        : "l"(a), "l"(b));
+    got = (int)yes;
+    fence_proxy_async_smem();  // the slot is read before a later answer overwrites it
+    mbar_arrive(&sm.next_read[slot]);
+  }
+  *k = (int)__shfl_sync(kFull, index, 0);
+  return __shfl_sync(kFull, got, 0);
 }
 
 // All softmax threads of query tile qt agree on `ok` (named barrier 1 + qt).
@@ -345,17 +412,19 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, int seq, int row,
   for (int d = 0; d < 32; ++d) store_out(op + d, acc[d] * inv);
 }
 
-// The rows of query tile qt of this CTA's items whose output is not finite, again
+// The rows of query tile qt, in the items listed, whose output is not finite, again
 // by exact_row: eight rows at a time per warp, `w` of the tile's.
 template <class QT, bool kFP8, int kMods>
-__device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem& sm, int cta, int ncta,
-                                       int total, int qt, int w) {
+__device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem& sm, int total, int qt,
+                                       int w) {
   using T = typename QT::T;
   const int lane = threadIdx.x & 31, g = p.group;
   const unsigned gmask = 0xFu << (lane & 28);
-  int idx = cta;
+  const bool all = sm.redo_n[qt] > kRedo;
+  const int n = all ? total : sm.redo_n[qt];
   ModItem x;
-  while (next_mod_item<kMods, kFP8>(p, sm, idx, total, x, ncta)) {
+  for (int i = 0; i < n; ++i) {
+    make_item<kMods, kFP8>(p, sm, all ? i : sm.redo[qt][i], total, x);
     const int nt = qt ? x.nt[1] : x.nt[0], t0 = qt ? x.t0[1] : x.t0[0];
     const int pos0 = qt ? x.pos0[1] : x.pos0[0];
     for (int r = w * 8 + (lane >> 2); r < nt * g; r += 8 * kTileWarps) {
@@ -394,7 +463,11 @@ __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem& sm, con
       mbar_init(&sm.p_ready[x], 1);
       mbar_init(&sm.o_done[x], 1);
       mbar_init(&sm.o_free[x], kTileWarps);
-      sm.redo[x] = 0;
+      sm.redo_n[x] = 0;
+    }
+    for (int i = 0; i < kAhead; ++i) {
+      mbar_init(&sm.next_full[i], 1);
+      mbar_init(&sm.next_read[i], kSoftWarps + 1 + kModProd);
     }
     mbar_init(&sm.tail_full, 1);
     mbar_init(&sm.tail_free, 1);
@@ -464,8 +537,8 @@ __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem& sm, con
 template <bool kFP8, int kMods>
 __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
                                               const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                              const CUtensorMap& tm_q, int kv_rows, int cta,
-                                              int ncta, int total, int pw) {
+                                              const CUtensorMap& tm_q, int kv_rows, int total,
+                                              int pw) {
   constexpr int kStageBytes = kFP8 ? kTileBytes / 2 : kTileBytes;
   constexpr int nst = kFP8 ? kStages8 : kStages;
   volatile int* abort = &sm.abort;
@@ -474,8 +547,7 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
   const int mine = (8 - pw + kModProd - 1) / kModProd;  // blocks per tile
   const bool my_lane = (lane & 7) % kModProd == pw;
   uint8_t* const ring = &sm.ring[0][0];
-  int idx = cta;
-  uint32_t pos = 0;
+  uint32_t pos = 0, n = 0;
   int nitem = 0, ntail = 0;
   bool ok = true;
   ModItem x;
@@ -496,7 +568,7 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
   auto issue = [&](int t, int row, bool is_v) -> bool {
     const int st = pos % nst;
     // test hook: these boxes are never issued, so every wait for the tile runs out
-    const bool skip = pw == 0 && cta == 0 && p.skip_copy > 0 && pos + 1 == (uint32_t)p.skip_copy;
+    const bool skip = pw == 0 && blockIdx.x == 0 && p.skip_copy > 0 && pos + 1 == (uint32_t)p.skip_copy;
     bool good = true;
     if (lane == 0) {
       if (pos >= (uint32_t)nst) good = wait_bar(&sm.empty[st], ((pos / nst) - 1) & 1, abort, lim);
@@ -544,9 +616,23 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
     ++ntail;
     return true;
   };
-  while (ok && next_mod_item<kMods, kFP8>(p, sm, idx, total, x, ncta)) {
-    if (x.nk == 0) continue;
+  for (; ok; ++n) {
+    int k;
+    const int got = take_next(sm, n, &k, abort, lim);
+    if (got <= 0) {
+      ok = got == 0;
+      break;
+    }
     bool good = true;
+    if (pw == 0) {
+      if (lane == 0) good = ask_next(sm, n, abort, lim);
+      if (!__shfl_sync(kFull, (int)good, 0)) {
+        ok = false;
+        break;
+      }
+    }
+    make_item<kMods, kFP8>(p, sm, k, total, x);
+    if (x.nk == 0) continue;
     if (pw == 0 && lane == 0) {
       if (nitem >= 1) good = wait_bar(&sm.q_empty, (nitem - 1) & 1, abort, lim);
       if (good) {
@@ -583,6 +669,8 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
   }
   if (!ok && lane == 0) {
     flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+    // an answer still on its way lands before the CTA goes away (requests 0 .. n)
+    if (pw == 0) mbar_wait(&sm.next_full[n % kAhead], (n / kAhead) & 1, 10000000ull);
     for (uint32_t y = pos > (uint32_t)nst ? pos - nst : 0; y < pos; ++y)
       mbar_wait(&sm.full[y % nst], (y / nst) & 1, 10000000ull);
   }
@@ -592,8 +680,7 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
 //   P_a(i) V, S_a(i + 1), P_b(i) V, S_b(i + 1)
 // so that one query tile's softmax works while the tensor pipe serves the other.
 template <class QT, bool kFP8, int kMods>
-__device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem& sm, uint32_t tmem, int cta,
-                                            int ncta, int total) {
+__device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem& sm, uint32_t tmem, int total) {
   constexpr int kStageBytes = kFP8 ? kTileBytes / 2 : kTileBytes;
   constexpr int nst = kFP8 ? kStages8 : kStages;
   constexpr uint32_t kAB = !kFP8 && std::is_same<QT, BF16>::value ? 1u : 0u;
@@ -608,8 +695,7 @@ __device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem& sm, ui
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // every lane takes the same result
     return __shfl_sync(kFull, (int)wait_bar(bar, parity, abort, lim), 0) != 0;
   };
-  int idx = cta;
-  uint32_t pos = 0;
+  uint32_t pos = 0, n = 0;
   uint32_t np[2] = {0, 0};   // P tiles consumed per query tile
   uint32_t nit[2] = {0, 0};  // items per query tile
   int nitem = 0, ntail = 0;
@@ -652,7 +738,14 @@ __device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem& sm, ui
     if (i == x.last[qt]) commit(&sm.o_done[qt]);
     return true;
   };
-  while (ok && next_mod_item<kMods, kFP8>(p, sm, idx, total, x, ncta)) {
+  for (; ok; ++n) {
+    int k;
+    const int got = take_next(sm, n, &k, abort, lim);
+    if (got <= 0) {
+      ok = got == 0;
+      break;
+    }
+    make_item<kMods, kFP8>(p, sm, k, total, x);
     if (x.nk == 0) continue;
     const bool ha = x.last[0] >= 0, hb = x.last[1] >= 0;
     int kst = 0, vst = 0;
@@ -703,8 +796,7 @@ __device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem& sm, ui
 
 // Softmax and epilogue: thread = row of query tile qt.
 template <class QT, bool kFP8, int kMods>
-__device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, uint32_t tmem, int cta,
-                                             int ncta, int total) {
+__device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, uint32_t tmem, int total) {
   using OutT = typename QT::T;
   constexpr float kMove = kFP8 ? kMove8 : kRescaleAt;
   volatile int* abort = &sm.abort;
@@ -723,11 +815,17 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // the warp's lanes agree
     return __all_sync(kFull, wait_bar(bar, parity, abort, lim)) != 0;
   };
-  int idx = cta;
+  uint32_t n = 0;
   uint32_t ns = 0, nit = 0;  // S tiles and items of this query tile
   bool ok = true;
   ModItem x;
-  while (ok && next_mod_item<kMods, kFP8>(p, sm, idx, total, x, ncta)) {
+  for (;; ++n) {
+    int k;
+    const int got = take_next(sm, n, &k, abort, lim);
+    // (the tile's warps leave the loop together: each passes the same barriers)
+    ok = all_of_tile(got >= 0, qt);
+    if (!ok || got == 0) break;
+    make_item<kMods, kFP8>(p, sm, k, total, x);
     const int nt = qt ? x.nt[1] : x.nt[0], t0 = qt ? x.t0[1] : x.t0[0];
     const int last = qt ? x.last[1] : x.last[0];
     const int pos = (qt ? x.pos0[1] : x.pos0[0]) + tok;
@@ -760,37 +858,44 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
     for (int i = 0; i < 4; ++i) l2[i] = make_float2(0.0f, 0.0f);
     for (int i = x.kt0; i <= last; ++i, ++ns) {
       const int k0 = tile_of<kMods>(x, i) * kTileKeys;
-      const bool good = wait(&sm.s_ready[qt], ns & 1);
-      const bool none = __all_sync(kFull, hi <= k0 || lo >= k0 + kTileKeys || empty);
-      const bool whole = __all_sync(kFull, lo <= k0 && hi >= k0 + kTileKeys);
-      // ---- the row's largest score in these keys ---------------------------------------------
-      float mt = -INFINITY;
-      float sv[kTileKeys], f = 1.0f;
-      if (good && !none) {
-        tc::fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < kTileKeys; c += 32) tc::tmem_ld32(s_col + c, sv + c);
-        tc::tmem_wait_ld();
-        if (neg) {
-#pragma unroll
-          for (int c = 0; c < kTileKeys; ++c) sv[c] = -sv[c];
-        }
-        f = modify_scores<kMods>(p, sv, a, slope, pos, k0);
-        if (!whole) {  // an interval of some row of the warp ends in these keys
-#pragma unroll
-          for (int c = 0; c < kTileKeys; ++c)
-            sv[c] = k0 + c >= lo && k0 + c < hi ? sv[c] : -INFINITY;
-        }
-        float mx[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mx[c] = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kTileKeys; c += 2)
-          mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
-        mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
-      }
-      ok = all_of_tile(good, qt);
+      ok = all_of_tile(wait(&sm.s_ready[qt], ns & 1), qt);
       if (!ok) break;
+      tc::fence_after_sync();
+      if (__all_sync(kFull, hi <= k0 || lo >= k0 + kTileKeys || empty)) {
+        // no row of the warp sees a key of the tile
+        float z[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) z[c] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kTileKeys / kChunk; ++c) tc::tmem_st16(s_col + 16 * c, z);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        tc::named_sync(1 + qt, 32 * kTileWarps);
+        if (r == 0) mbar_arrive(&sm.p_ready[qt]);
+        continue;
+      }
+      float sv[kTileKeys];
+#pragma unroll
+      for (int c = 0; c < kTileKeys; c += 32) tc::tmem_ld32(s_col + c, sv + c);
+      tc::tmem_wait_ld();
+      if (neg) {
+#pragma unroll
+        for (int c = 0; c < kTileKeys; ++c) sv[c] = -sv[c];
+      }
+      const float f = modify_scores<kMods>(p, sv, a, slope, pos, k0);
+      if (!__all_sync(kFull, lo <= k0 && hi >= k0 + kTileKeys)) {
+        // an interval of some row of the warp ends in this tile: hidden keys become -inf
+#pragma unroll
+        for (int c = 0; c < kTileKeys; ++c)
+          sv[c] = k0 + c >= lo && k0 + c < hi ? sv[c] : -INFINITY;
+      }
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mx[c] = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < kTileKeys; c += 2)
+        mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
       // move the running max (and rescale O) only on a large increase; O is complete
       // up to the step before (this S was issued after its product)
       const bool fresh = m_run == -INFINITY;  // no key seen so far
@@ -803,40 +908,32 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
         for (int c = 0; c < 4; ++c) l2[c] = __fmul2_rn(l2[c], make_float2(alpha, alpha));
       }
       const float m = m_run == -INFINITY ? 0.0f : m_run;  // 2^(-inf - 0) = 0
-      // ---- weights, over the scores (hidden keys are -inf: weight 0) -----------------------
-      if (none) {
-        float z[16];
+      // weights, over the scores read (hidden keys are -inf: weight 0)
 #pragma unroll
-        for (int c = 0; c < 16; ++c) z[c] = 0.0f;
+      for (int c = 0; c < kTileKeys / kChunk; ++c) {
+        // 16 columns: packed 16-bit pairs, or 8 of four E4M3 codes (hi) and 8 of lo
+        float pk[16];
+        uint32_t h0 = 0, r0 = 0;
 #pragma unroll
-        for (int c = 0; c < kTileKeys / kChunk; ++c) tc::tmem_st16(s_col + 16 * c, z);
-      } else {
-#pragma unroll
-        for (int c = 0; c < kTileKeys / kChunk; ++c) {
-          // 16 columns: packed 16-bit pairs, or 8 of four E4M3 codes (hi) and 8 of lo
-          float pk[16];
-          uint32_t h0 = 0, r0 = 0;
-#pragma unroll
-          for (int e = 0; e < kChunk; e += 2) {
-            const float x = fast_exp2(fmaf(sv[kChunk * c + e], f, -m));
-            const float y = fast_exp2(fmaf(sv[kChunk * c + e + 1], f, -m));
-            l2[(e >> 1) & 3] = __fadd2_rn(l2[(e >> 1) & 3], make_float2(x, y));
-            if constexpr (!kFP8) {
-              pk[e >> 1] = __uint_as_float(pack2<QT>(x, y));
+        for (int e = 0; e < kChunk; e += 2) {
+          const float x = fast_exp2(fmaf(sv[kChunk * c + e], f, -m));
+          const float y = fast_exp2(fmaf(sv[kChunk * c + e + 1], f, -m));
+          l2[(e >> 1) & 3] = __fadd2_rn(l2[(e >> 1) & 3], make_float2(x, y));
+          if constexpr (!kFP8) {
+            pk[e >> 1] = __uint_as_float(pack2<QT>(x, y));
+          } else {
+            uint32_t h1, r1;
+            split_pair(x, y, &h1, &r1);
+            if (e & 2) {
+              pk[e >> 2] = __uint_as_float(h0 | (h1 << 16));
+              pk[8 + (e >> 2)] = __uint_as_float(r0 | (r1 << 16));
             } else {
-              uint32_t h1, r1;
-              split_pair(x, y, &h1, &r1);
-              if (e & 2) {
-                pk[e >> 2] = __uint_as_float(h0 | (h1 << 16));
-                pk[8 + (e >> 2)] = __uint_as_float(r0 | (r1 << 16));
-              } else {
-                h0 = h1;
-                r0 = r1;
-              }
+              h0 = h1;
+              r0 = r1;
             }
           }
-          tc::tmem_st16(s_col + 16 * c, pk);
         }
+        tc::tmem_st16(s_col + 16 * c, pk);
       }
       // the product of this step adds onto O: rescale it first
       if (i > x.kt0 && __any_sync(kFull, need)) {
@@ -888,7 +985,10 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
         }
       }
     }
-    if (odd && valid) sm.redo[qt] = 1;
+    if (__any_sync(kFull, odd && valid) && lane == 0) {
+      const int at = atomicAdd(&sm.redo_n[qt], 1);
+      if (at < kRedo) sm.redo[qt][at] = k;
+    }
     tc::fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.o_free[qt]);
@@ -898,7 +998,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
   // every warp of the tile leaves the loop here, whatever it met, and sees the others'
   // stores and flag behind this barrier
   ok = all_of_tile(ok, qt);
-  if (ok && sm.redo[qt]) redo_rows<QT, kFP8, kMods>(p, sm, cta, ncta, total, qt, warp % kTileWarps);
+  if (ok && sm.redo_n[qt] > 0) redo_rows<QT, kFP8, kMods>(p, sm, total, qt, warp % kTileWarps);
 }
 
 template <class QT, bool kFP8, int kMods>
@@ -912,17 +1012,16 @@ __global__ void __launch_bounds__(kModThreads, 1)
   const int warp = threadIdx.x >> 5;
   mods_setup(p, sm, tm_k, tm_v, tm_q);
   const uint32_t tmem = sm.tmem_base;
-  const int cta = blockIdx.x, ncta = gridDim.x;
   const int total = sm.seq_start[p.num_seqs] * p.num_kv_heads;
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kWarpMma)
-      mods_issuer<QT, kFP8, kMods>(p, sm, tmem, cta, ncta, total);
+      mods_issuer<QT, kFP8, kMods>(p, sm, tmem, total);
     else
-      mods_producer<kFP8, kMods>(p, sm, tm_k, tm_v, tm_q, kv_rows, cta, ncta, total, warp - kWarpTma);
+      mods_producer<kFP8, kMods>(p, sm, tm_k, tm_v, tm_q, kv_rows, total, warp - kWarpTma);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    mods_softmax<QT, kFP8, kMods>(p, sm, tmem, cta, ncta, total);
+    mods_softmax<QT, kFP8, kMods>(p, sm, tmem, total);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -967,12 +1066,11 @@ int launch_mods(const AttnParams& p, int total_q, const uint8_t* q8, cudaStream_
     c.context_lens = p.context_lens + s0;
     c.query_start_loc = p.query_start_loc + s0;
     if (p.bidir_lens) c.bidir_lens = p.bidir_lens + s0;
-    // an upper bound of the items: every sequence's pairs of query tiles, times the KV heads
-    const long long tiles = (total_q + (long long)tokens - 1) / tokens + c.num_seqs;
-    const long long items = (tiles + c.num_seqs) / 2 * p.num_kv_heads;
-    const int sms = sm_count();
-    const int grid = (int)(items < sms ? (items > 0 ? items : 1) : sms);
-    kern<<<grid, kModThreads, smem, stream>>>(c, tk, tv, tq, (int)kv_rows);
+    // a CTA per item: an upper bound of them (every sequence's pairs of query tiles, the
+    // last of each perhaps short, times the KV heads); those past the last do nothing
+    const long long pairs = total_q / (2 * (long long)tokens) + c.num_seqs;
+    const long long items = pairs * p.num_kv_heads;
+    kern<<<(unsigned)items, kModThreads, smem, stream>>>(c, tk, tv, tq, (int)kv_rows);
     if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   }
   return PKV_OK;
