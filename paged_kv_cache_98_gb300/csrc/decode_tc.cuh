@@ -1136,17 +1136,16 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
             sum[h + 1] += e1;
             if constexpr (FP8) {
               // E4M3 with a 2^8 scale (weights are <= 1)
-              const __nv_fp8x2_storage_t q2 = __nv_cvt_float2_to_fp8x2(
-                  make_float2(e0 * 256.0f, e1 * 256.0f), __NV_SATFINITE, __NV_E4M3);
+              uint32_t q2, r2;
+              if constexpr (L::kSplitP)
+                split_e4m3(make_float2(e0 * 256.0f, e1 * 256.0f), &q2, &r2);
+              else
+                q2 = __nv_cvt_float2_to_fp8x2(make_float2(e0 * 256.0f, e1 * 256.0f), __NV_SATFINITE,
+                                              __NV_E4M3);
               uint8_t* c8 = pm + (key >> 4) * 128 + (h >> 3) * L::kPSbo + (h & 7) * 16 + (key & 15);
               c8[0] = (uint8_t)(q2 & 0xffu);
               c8[16] = (uint8_t)(q2 >> 8);
               if constexpr (L::kSplitP) {  // what the hi term leaves, in the lo rows
-                __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(q2, __NV_E4M3);
-                const float2 hv = __half22float2(*reinterpret_cast<__half2*>(&hr));
-                const __nv_fp8x2_storage_t r2 = __nv_cvt_float2_to_fp8x2(
-                    make_float2(fmaf(e0, 256.0f, -hv.x), fmaf(e1, 256.0f, -hv.y)), __NV_SATFINITE,
-                    __NV_E4M3);
                 uint8_t* l8 = c8 + (L::kRows >> 3) * L::kPSbo;
                 l8[0] = (uint8_t)(r2 & 0xffu);
                 l8[16] = (uint8_t)(r2 >> 8);

@@ -3,18 +3,20 @@
 // interval of visible keys per query row (score_mods.cuh).  The mathematics and
 // the layouts are those of prefill_tc.cuh; what differs:
 //
-//  * The plain kernel's softmax (one thread per row, 128 scores in registers) is
-//    bound by its own instruction latency: one warp per scheduler works while the
-//    other waits for its MMAs.  Modified scores double its instructions (ncu, a
-//    cap of 50 on the mixed batch's chunks: 51.6 M against 29.1 M, issue slots 42 %
-//    used, no pipe above 34 %), and took 130 us against 80.  Here two threads share
-//    a row, 64 keys each, so that four softmax warps per scheduler hide each other's
-//    latency; the two exchange their maxima through shared memory, one barrier per
-//    tile.
+//  * The plain kernel's softmax (one thread per row, 128 scores in registers, two
+//    warps per scheduler that take turns with their MMAs) is bound by the latency of
+//    its own instructions, not by a pipe (ncu, a cap of 50 on the mixed batch's
+//    chunks: no pipe above 34 %), so what it costs to modify a score is instructions
+//    and registers: one kernel per set of modifiers, scores modified in place (the
+//    exponentials' code stands once), and the two softmax warpgroups take over the
+//    registers that issuer and producers do not need.  Two threads per row, which
+//    exchange their maxima, were slower (cap 145 -> 179 us: 96 registers spill, and
+//    the exchange is a barrier per tile); so was reading the scores twice from TMEM to
+//    hold fewer (120 against 93 us with the modifiers off).
 //  * An item (two query tiles of whole tokens) walks the key tiles from its first
 //    row's first key to its last row's last one; blocks before and behind those are
-//    not read.  64 keys that every row of a warp sees are not masked; 64 that none
-//    sees cost neither scores nor exponentials, only zeros for P.
+//    not read.  A tile that every row of a warp sees is not masked; one that none sees
+//    costs no exponentials, only zeros for P.
 //  * A running CTA takes over the next item not launched yet instead of owning a fixed
 //    share.
 //  * A distance bias grows towards the query, so the running max would move, and O
@@ -53,11 +55,12 @@ constexpr int kSoftRegs = 208, kOtherRegs = 80;
 static_assert(32 * kSoftWarps * kSoftRegs + 128 * kOtherRegs <= kModThreads * 168 && kModThreads == 384,
               "setmaxnreg may only share out what the launch holds");
 constexpr int kChunk = 32;  // keys whose weights are packed and stored together
-// Two E4M3 terms: w <= 2, P holds 128 w.  The headroom that one term spends on
-// fewer rescales goes to small weights here: they keep a code down to 2^-17, and a
-// row's tail of many of them is not lost.
-constexpr float kMove8 = 1.0f;
-constexpr float kPMods8 = 128.0f;
+// Two E4M3 terms: P holds 2^8 w, and the running max moves at half a power of two, so
+// that 2^8 w <= 363 < 448.  The headroom that one term spends on fewer rescales goes to
+// small weights here: they keep a code down to 2^-17, and a row's tail of many of them
+// is not lost.  The scale is in the exponent (2^(score - m + 8)), and so in the sums.
+constexpr float kMove8 = 0.5f;
+constexpr float kScaleLog8 = 8.0f;
 
 constexpr int kAhead = 4;   // items a CTA may ask for before the slowest warp takes them
 constexpr int kRedo = 64;   // items listed for recomputation; more of them: all items are looked at
@@ -312,17 +315,6 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
     }
   }
   return 1.0f;
-}
-
-// Two E4M3 terms of the weights x, y: codes of kPMods8 w, and of what those leave.
-__device__ __forceinline__ void split_pair(float x, float y, uint32_t* hi, uint32_t* lo) {
-  const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x * kPMods8, y * kPMods8),
-                                                           __NV_SATFINITE, __NV_E4M3);
-  __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h2, __NV_E4M3);
-  const float2 hv = __half22float2(*reinterpret_cast<__half2*>(&hr));
-  *hi = h2;
-  *lo = __nv_cvt_float2_to_fp8x2(make_float2(fmaf(x, kPMods8, -hv.x), fmaf(y, kPMods8, -hv.y)),
-                                 __NV_SATFINITE, __NV_E4M3);
 }
 
 // O (+)= P V: P in TMEM at a (16 columns for every 32 keys), V 16-bit in steps of 16
@@ -907,7 +899,8 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
 #pragma unroll
         for (int c = 0; c < 4; ++c) l2[c] = __fmul2_rn(l2[c], make_float2(alpha, alpha));
       }
-      const float m = m_run == -INFINITY ? 0.0f : m_run;  // 2^(-inf - 0) = 0
+      // (2^(-inf - 0) = 0)
+      const float m = (m_run == -INFINITY ? 0.0f : m_run) - (kFP8 ? kScaleLog8 : 0.0f);
       // weights, over the scores read (hidden keys are -inf: weight 0)
 #pragma unroll
       for (int c = 0; c < kTileKeys / kChunk; ++c) {
@@ -923,7 +916,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
             pk[e >> 1] = __uint_as_float(pack2<QT>(x, y));
           } else {
             uint32_t h1, r1;
-            split_pair(x, y, &h1, &r1);
+            split_e4m3(make_float2(x, y), &h1, &r1);
             if (e & 2) {
               pk[e >> 2] = __uint_as_float(h0 | (h1 << 16));
               pk[8 + (e >> 2)] = __uint_as_float(r0 | (r1 << 16));
@@ -960,8 +953,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
     ok = all_of_tile(wait(&sm.o_done[qt], nit & 1), qt);
     if (!ok) break;
     tc::fence_after_sync();
-    // (E4M3: P held kPMods8 w, and V its codes)
-    const float inv = valid && !empty ? p.v_scale / (kFP8 ? kPMods8 * l : l) : 0.0f;
+    const float inv = valid && !empty ? p.v_scale / l : 0.0f;  // (E4M3: V's codes, scaled)
     bool odd = false;  // an output that is not finite
 #pragma unroll 1
     for (int c = 0; c < kD; c += 32) {
