@@ -102,18 +102,16 @@ __device__ __forceinline__ float cap_tanh(float x) {
 }
 
 // Two E4M3 terms of each of the pair x (0 <= x <= 448, a softmax weight times a power
-// of two): codes *hi of x rounded to four significant bits, codes *lo of what that
-// leaves.  The rounding is Veltkamp's split (c = x (2^20 + 1), hi = c - (c - x)) on the
-// packed fp32 pair: converting hi back from its codes instead takes four conversions
-// a pair in place of two, and those set the pace (E4M3 prefix prompts 220 -> 180 us).  hi + lo is good to 2^-8 of x; below E4M3's normal range,
-// x < 2^-6, to 1.5 * 2^-10.
+// of two): codes *hi of x rounded to four significant bits (on the bits of the fp32
+// number: three of the mantissa stay), codes *lo of what that leaves.  Two
+// conversions a pair, instead of the four that converting hi back from its codes
+// would take.  hi + lo is good to 2^-8 of x; below E4M3's normal range, x < 2^-6, to
+// 1.5 * 2^-10.
 __device__ __forceinline__ void split_e4m3(float2 x, uint32_t* hi, uint32_t* lo) {
-  const float2 c = __fmul2_rn(x, make_float2(1048577.0f, 1048577.0f));
-  const float2 d = __fadd2_rn(c, make_float2(-x.x, -x.y));
-  const float2 h = __fadd2_rn(c, make_float2(-d.x, -d.y));
-  const float2 r = __fadd2_rn(x, make_float2(-h.x, -h.y));
-  *hi = __nv_cvt_float2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
-  *lo = __nv_cvt_float2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
+  const float hx = __uint_as_float((__float_as_uint(x.x) + 0x80000u) & 0xfff00000u);
+  const float hy = __uint_as_float((__float_as_uint(x.y) + 0x80000u) & 0xfff00000u);
+  *hi = __nv_cvt_float2_to_fp8x2(make_float2(hx, hy), __NV_SATFINITE, __NV_E4M3);
+  *lo = __nv_cvt_float2_to_fp8x2(make_float2(x.x - hx, x.y - hy), __NV_SATFINITE, __NV_E4M3);
 }
 
 }  // namespace pkv

@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSeqs = PKV_STEP_MAPS_MAX_SEQS;
+constexpr int kPer = 4;  // sequences per thread and round of the prefix sums
 
 struct MapParams {
   int32_t* block_tables;
@@ -76,14 +77,23 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapParams p) 
   const int S = p.num_seqs;
   const bool first = blockIdx.x == 0;
 
-  // 64-bit sums: a batch of bad lengths must not wrap into a good-looking one
+  // 64-bit sums: a batch of bad lengths must not wrap into a good-looking one.  Each
+  // thread takes kPer consecutive sequences, whose loads are on their way together.
   long long base_q = 0, base_g = 0;
-  for (int s0 = 0; s0 < S; s0 += kThreads) {
-    const int s = s0 + tid;
-    Seq x = {-1, 0, 0};
-    if (s < S) x = load_seq(p, s, first);
-    const int ctx = x.cached + x.q;
-    const long long q = x.q, g = blocks_of(ctx) - blocks_of(x.cached);
+  for (int s0 = 0; s0 < S; s0 += kThreads * kPer) {
+    const int sb = s0 + tid * kPer;
+    Seq x[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      x[i] = {-1, 0, 0};
+      if (sb + i < S) x[i] = load_seq(p, sb + i, first);
+    }
+    long long q = 0, g = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      q += x[i].q;
+      g += blocks_of(x[i].cached + x[i].q) - blocks_of(x[i].cached);
+    }
     long long iq = q, ig = g;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -108,10 +118,17 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapParams p) 
       tq += part_q[w];
       tg += part_g[w];
     }
-    if (s < S) {
-      qsl[s] = (int)min(base_q + wq + iq - q, (long long)p.num_tokens);
-      off[s] = (int)min(base_g + wg + ig - g, (long long)p.num_new);
-      if (first) p.context_lens[s] = ctx;
+    long long rq = base_q + wq + iq - q, rg = base_g + wg + ig - g;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (sb + i < S) {
+        const int ctx = x[i].cached + x[i].q;
+        qsl[sb + i] = (int)min(rq, (long long)p.num_tokens);
+        off[sb + i] = (int)min(rg, (long long)p.num_new);
+        if (first) p.context_lens[sb + i] = ctx;
+        rq += x[i].q;
+        rg += blocks_of(ctx) - blocks_of(x[i].cached);
+      }
     }
     base_q += tq;
     base_g += tg;
