@@ -615,9 +615,8 @@ size_t pkv_prefill_biased_workspace_size(int num_seqs, int total_q, int num_head
   if (num_seqs <= 0 || total_q <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       max_context_len < 0)
     return 0;
-  // tensor cores: the split query of an E4M3 cache; CUDA cores: split-K partials
-  if (head_dim == 128)
-    return kv_dtype == PKV_FP8_E4M3 ? pkv::prefill_q8_bytes(total_q, num_heads) : 0;
+  // tensor cores: none; CUDA cores: split-K partials
+  if (head_dim == 128) return 0;
   return split_workspace((size_t)total_q, num_heads, head_dim,
                          parts_for(max_context_len, kDefaultPartition));
 }
@@ -667,7 +666,7 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
     p.q_scale = scale * pkv::kLog2e * (fp8 ? k_scale : 1.0f);
     p.v_scale = fp8 ? v_scale : 1.0f;
     pkv::take_debug_hook(p);
-    return pkv::launch_prefill_mods(p, q_dtype, kv_dtype, total_q, workspace, workspace_bytes,
+    return pkv::launch_prefill_mods(p, q_dtype, kv_dtype, total_q,
                                     static_cast<cudaStream_t>(stream));
   }
   const size_t need = split_workspace((size_t)total_q, num_heads, head_dim, p.max_parts);

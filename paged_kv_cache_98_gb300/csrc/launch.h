@@ -146,23 +146,16 @@ size_t prefill_q8_bytes(int total_q, int num_heads);
 int launch_prefill_tc_fp8(const AttnParams& p, int q_dtype, int total_q, void* workspace,
                           size_t workspace_bytes, cudaStream_t stream);
 
-// The query split alone: hi and lo rows (*q8) and scales in the workspace, scales
-// rounded up to powers of two with pow2.
-int launch_split_query(const AttnParams& p, int q_dtype, int total_q, void* workspace,
-                       size_t workspace_bytes, bool pow2, const uint8_t** q8, const float** q8_scale,
-                       cudaStream_t stream);
-// Chunked prefill under score modifiers (p.mods), head_dim 128, any group size;
-// E4M3 caches split the query into the workspace (prefill_q8_bytes).
+// Chunked prefill under score modifiers (p.mods), head_dim 128, any group size; its
+// kernels with capped scores, a distance bias, or both.
 bool prefill_mods_supported(const AttnParams& p, int head_dim);
-int launch_prefill_mods(const AttnParams& p, int q_dtype, int kv_dtype, int total_q, void* workspace,
-                        size_t workspace_bytes, cudaStream_t stream);
-
-// Its kernels with capped scores, a distance bias, or both (q8: the split query).
-int launch_prefill_cap(const AttnParams& p, int q_dtype, int total_q, const uint8_t* q8,
-                       cudaStream_t stream);
-int launch_prefill_bias(const AttnParams& p, int q_dtype, int total_q, const uint8_t* q8,
+int launch_prefill_mods(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
                         cudaStream_t stream);
-int launch_prefill_cap_bias(const AttnParams& p, int q_dtype, int total_q, const uint8_t* q8,
+int launch_prefill_cap(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+                       cudaStream_t stream);
+int launch_prefill_bias(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+                        cudaStream_t stream);
+int launch_prefill_cap_bias(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
                             cudaStream_t stream);
 
 // One launch for a mixed batch: pd describes the decode rows (as for

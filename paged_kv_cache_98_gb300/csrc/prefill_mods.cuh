@@ -26,8 +26,12 @@
 //    row whose output is not finite is computed again from its own keys alone, in
 //    fp32, after the main loop, so that a hidden infinity never reaches it.  Finite
 //    inputs never take that path.
-//  * E4M3 caches: P is two E4M3 terms, p = hi + lo, in two products: one term alone
-//    is good to 2^-4, 2 % of the output's norm, both to 2^-8, as bf16.
+//  * E4M3 caches: six more warps turn each K or V tile into the query's 16-bit type
+//    (exactly) where it lands, once for both query tiles, and everything
+//    behind is as for 16-bit caches: no rounding but theirs, and no pass over the query.
+//    8-bit products instead need the query and P as two E4M3 terms each to be as good
+//    (one term of P alone is 2 % of the output's norm), and that splitting is on the
+//    softmax warps: 211 us against 132 for the same prompts on a 16-bit cache.
 #ifndef PKV_PREFILL_MODS_CUH
 #define PKV_PREFILL_MODS_CUH
 
@@ -46,36 +50,41 @@ constexpr int kModCap = 1, kModBias = 2;
 constexpr int kTileWarps = 4;  // softmax warps of a query tile
 constexpr int kSoftWarps = 2 * kTileWarps;
 constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 1;
-constexpr int kModProd = 3;  // producer warps
-constexpr int kModThreads = 32 * (kSoftWarps + 1 + kModProd);
-// Registers per thread: the launch gives 168 to each of 384 threads; the two softmax
-// warpgroups take over what the third (issuer and producers) returns:
-// 256 * 208 + 128 * 80 <= 384 * 168.
-constexpr int kSoftRegs = 208, kOtherRegs = 80;
-static_assert(32 * kSoftWarps * kSoftRegs + 128 * kOtherRegs <= kModThreads * 168 && kModThreads == 384,
+// Warps beside softmax and issuer, and threads of the CTA: three producers, or (E4M3
+// caches) one and six that convert its tiles.
+constexpr int kConverters = 6;
+constexpr int mod_producers(bool fp8) { return fp8 ? 1 : 3; }
+constexpr int mod_extra(bool fp8) { return mod_producers(fp8) + (fp8 ? kConverters : 0); }
+constexpr int mod_threads(bool fp8) { return 32 * (kSoftWarps + 1 + mod_extra(fp8)); }
+// Registers per thread: the launch gives 168 to each of 384 threads, 128 to each of
+// 512; the two softmax warpgroups take over what the others (issuer and producers)
+// return.
+constexpr int soft_regs(bool fp8) { return fp8 ? 192 : 208; }
+constexpr int other_regs(bool fp8) { return fp8 ? 64 : 80; }
+constexpr int launch_regs(bool fp8) { return fp8 ? 128 : 168; }
+constexpr bool regs_fit(bool fp8) {
+  return 32 * kSoftWarps * soft_regs(fp8) + (mod_threads(fp8) - 32 * kSoftWarps) * other_regs(fp8) <=
+         mod_threads(fp8) * launch_regs(fp8);
+}
+static_assert(regs_fit(false) && regs_fit(true) && mod_threads(false) == 384 && mod_threads(true) == 512,
               "setmaxnreg may only share out what the launch holds");
 constexpr int kChunk = 32;  // keys whose weights are packed and stored together
-// Two E4M3 terms: P holds 2^8 w, and the running max moves at half a power of two, so
-// that 2^8 w <= 363 < 448.  The headroom that one term spends on fewer rescales goes to
-// small weights here: they keep a code down to 2^-17, and a row's tail of many of them
-// is not lost.  The scale is in the exponent (2^(score - m + 8)), and so in the sums.
-constexpr float kMove8 = 0.5f;
-constexpr float kScaleLog8 = 8.0f;
-
 constexpr int kAhead = 4;   // items a CTA may ask for before the slowest warp takes them
 constexpr int kRedo = 64;   // items listed for recomputation; more of them: all items are looked at
 
+template <bool kFP8>
 struct ModSmem {
   alignas(1024) uint8_t ring[kStages][kTileBytes];
   alignas(1024) uint8_t q[2][kTileBytes];
-  alignas(1024) uint8_t tail[kTailBytes];
+  alignas(1024) uint8_t tail[kTailBytes];  // V rows of a partial block (16-bit caches)
   int seq_start[kMaxSeqs + 1];  // prefix of items per sequence (one KV head's)
   int seq_qlen[kMaxSeqs];
   int seq_ctx[kMaxSeqs];
   int seq_q0[kMaxSeqs];
-  int scan[kModThreads / 32];
-  uint64_t full[kRingBars];
-  uint64_t empty[kRingBars];
+  int scan[mod_threads(kFP8) / 32];
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  uint64_t staged[kStages];  // an E4M3 tile has landed in the second half of its stage
   uint64_t q_full;
   uint64_t q_empty;
   uint64_t s_ready[2];  // per query tile
@@ -105,6 +114,7 @@ struct ModItem {
   int last[2];         // last step of each query tile (-1: its rows see nothing)
   int lo_block, end_block;  // blocks any row sees
   int tail_step;       // MMA step of key tile nk - 1 holding the partial last block, else -1
+                       // (E4M3 caches: -1)
 };
 
 // Steps kt0 .. nk - 1 of an item; the key tile of step i, backwards under a bias.
@@ -115,7 +125,7 @@ __device__ __forceinline__ int tile_of(const ModItem& x, int i) {
 
 // Item k of the launch, or (k past the last one) an item without keys or rows.
 template <int kMods, bool kFP8>
-__device__ __forceinline__ void make_item(const AttnParams& p, const ModSmem& sm, int k, int total,
+__device__ __forceinline__ void make_item(const AttnParams& p, const ModSmem<kFP8>& sm, int k, int total,
                                           ModItem& it) {
   if (k >= total) {
     it = ModItem{};
@@ -170,9 +180,9 @@ __device__ __forceinline__ void make_item(const AttnParams& p, const ModSmem& sm
 #pragma unroll
   for (int x = 0; x < 2; ++x)
     it.last[x] = end[x] > 0 ? ((kMods & kModBias) ? it.nk : end[x]) - 1 : -1;
-  const bool partial = (it.ctx & (kBlockSize - 1)) != 0;
+  const bool partial = !kFP8 && (it.ctx & (kBlockSize - 1)) != 0;
   it.tail_step = partial && (it.ctx - 1) / kTileKeys == it.nk - 1
-                     ? ((it.ctx - 1) % kTileKeys) / (kFP8 ? 2 * kBlockSize : kBlockSize)
+                     ? ((it.ctx - 1) % kTileKeys) / kBlockSize
                      : -1;
 }
 
@@ -184,7 +194,8 @@ __device__ __forceinline__ void make_item(const AttnParams& p, const ModSmem& sm
 // Producer warp 0 asks, at the start of its n-th item, for the item after it; every
 // warp reads the answer when it gets there.  No request follows one that found the
 // grid empty: that answer ends every warp's loop.
-__device__ __forceinline__ bool ask_next(ModSmem& sm, uint32_t m, volatile int* abort,
+template <bool kFP8>
+__device__ __forceinline__ bool ask_next(ModSmem<kFP8>& sm, uint32_t m, volatile int* abort,
                                          unsigned long long lim) {
   const int slot = m % kAhead;
   if (m >= kAhead && !wait_bar(&sm.next_read[slot], ((m / kAhead) - 1) & 1, abort, lim)) return false;
@@ -199,7 +210,8 @@ __device__ __forceinline__ bool ask_next(ModSmem& sm, uint32_t m, volatile int* 
 
 // The n-th item of this CTA, for the whole warp: 1 and its index in *k, 0 when there is
 // none, -1 when the wait gave up.
-__device__ __forceinline__ int take_next(ModSmem& sm, uint32_t n, int* k, volatile int* abort,
+template <bool kFP8>
+__device__ __forceinline__ int take_next(ModSmem<kFP8>& sm, uint32_t n, int* k, volatile int* abort,
                                          unsigned long long lim) {
   if (n == 0) {
     *k = blockIdx.x;
@@ -317,28 +329,6 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
   return 1.0f;
 }
 
-// O (+)= P V: P in TMEM at a (16 columns for every 32 keys), V 16-bit in steps of 16
-// keys or E4M3 in steps of 32 (hi terms, then lo terms); step ts (if >= 0) takes its V
-// rows from the tail buffer.
-template <bool kFP8>
-__device__ __forceinline__ void issue_mods_pv(uint32_t d, uint32_t a, uint64_t dv, uint64_t dtail,
-                                              int ts, uint32_t acc0, uint32_t idesc) {
-  if constexpr (kFP8) {
-#pragma unroll
-    for (int kk = 0; kk < kTileKeys / 32; ++kk) {
-      const uint64_t b = kk == ts ? dtail : dv + (uint64_t)((kk * (32 * 128)) >> 4);
-      mma_f8_tmem_a(d, a + 16 * kk, b, idesc, acc0 | (kk != 0 ? 1u : 0u));
-      mma_f8_tmem_a(d, a + 16 * kk + 8, b, idesc, 1);
-    }
-  } else {
-#pragma unroll
-    for (int kk = 0; kk < kTileKeys / 16; ++kk) {
-      const uint64_t b = kk == ts ? dtail : dv + (uint64_t)((kk * (kBlockSize * 128)) >> 4);
-      mma_f16_tmem_a(d, a + 8 * kk, b, idesc, acc0 | (kk != 0 ? 1u : 0u));
-    }
-  }
-}
-
 // One row (a query token's head) from its own keys alone, in fp32 (the plain online
 // softmax, exp2f).  Four lanes share the row, 32 dimensions each; gmask is their
 // mask.
@@ -407,7 +397,7 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, int seq, int row,
 // The rows of query tile qt, in the items listed, whose output is not finite, again
 // by exact_row: eight rows at a time per warp, `w` of the tile's.
 template <class QT, bool kFP8, int kMods>
-__device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem& sm, int total, int qt,
+__device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem<kFP8>& sm, int total, int qt,
                                        int w) {
   using T = typename QT::T;
   const int lane = threadIdx.x & 31, g = p.group;
@@ -440,13 +430,16 @@ __device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem& sm, i
 }
 
 // Barriers, tensor memory, and the per-sequence tables; ends with the CTA synchronised.
-__device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem& sm, const CUtensorMap& tm_k,
+template <bool kFP8>
+__device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem<kFP8>& sm, const CUtensorMap& tm_k,
                                            const CUtensorMap& tm_v, const CUtensorMap& tm_q) {
+  constexpr int kModThreads = mod_threads(kFP8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kRingBars; ++s) {
-      mbar_init(&sm.full[s], kModProd);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.full[s], kFP8 ? kConverters : mod_producers(false));
       mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.staged[s], 1);
     }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
@@ -459,7 +452,7 @@ __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem& sm, con
     }
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(&sm.next_full[i], 1);
-      mbar_init(&sm.next_read[i], kSoftWarps + 1 + kModProd);
+      mbar_init(&sm.next_read[i], kSoftWarps + 1 + mod_extra(kFP8));
     }
     mbar_init(&sm.tail_full, 1);
     mbar_init(&sm.tail_free, 1);
@@ -523,16 +516,18 @@ __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem& sm, con
   tc::fence_after_sync();
 }
 
-// TMA producer pw of three: per item the query tiles, then per step its key tile's K
-// boxes, the tail rows of V where the tile holds the context's partial last block,
-// and its V boxes (blocks j with j % 3 == pw), into the ring.
+// TMA producer pw: per item the query tiles, then per step its key tile's K boxes, the
+// tail rows of V where the tile holds the context's partial last block, and its V
+// boxes, into the ring.  The boxes are dealt out to the producers block by block; an
+// E4M3 tile, half as large, lands in the second half of its stage.
 template <bool kFP8, int kMods>
-__device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
+__device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>& sm,
                                               const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                               const CUtensorMap& tm_q, int kv_rows, int total,
                                               int pw) {
-  constexpr int kStageBytes = kFP8 ? kTileBytes / 2 : kTileBytes;
-  constexpr int nst = kFP8 ? kStages8 : kStages;
+  constexpr int nst = kStages, kModProd = mod_producers(kFP8);
+  constexpr int kLoadBytes = kFP8 ? kTileBytes / 2 : kTileBytes;
+  uint64_t* const landed = kFP8 ? sm.staged : sm.full;
   volatile int* abort = &sm.abort;
   const unsigned long long lim = wait_limit(p);
   const int lane = threadIdx.x & 31, g = p.group;
@@ -564,14 +559,14 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
     bool good = true;
     if (lane == 0) {
       if (pos >= (uint32_t)nst) good = wait_bar(&sm.empty[st], ((pos / nst) - 1) & 1, abort, lim);
-      if (good && !skip) mbar_arrive_expect_tx(&sm.full[st], mine * (kStageBytes / 8));
+      if (good && !skip) mbar_arrive_expect_tx(&landed[st], mine * (kLoadBytes / 8));
     }
     if (!__shfl_sync(kFull, (int)good, 0)) return false;
     if (!skip && (lane >> 3) == (t & 3) && my_lane) {
-      uint8_t* dst = ring + (size_t)st * kStageBytes + (lane & 7) * (kBlockSize * 128);
+      uint8_t* dst = ring + (size_t)st * kTileBytes + (kFP8 ? kHalf : 0) + (lane & 7) * (kBlockSize * 128);
       const CUtensorMap* map = is_v ? &tm_v : &tm_k;
-      tc::tma_load_2d(dst, map, 0, row, &sm.full[st]);
-      if (!kFP8) tc::tma_load_2d(dst + kHalf, map, 64, row, &sm.full[st]);
+      tc::tma_load_2d(dst, map, 0, row, &landed[st]);
+      if (!kFP8) tc::tma_load_2d(dst + kHalf, map, 64, row, &landed[st]);
     }
     __syncwarp();
     ++pos;
@@ -583,8 +578,8 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
     bool good = true;
     if (lane == 0 && ntail >= 1) good = wait_bar(&sm.tail_free, (ntail - 1) & 1, abort, lim);
     if (!__shfl_sync(kFull, (int)good, 0)) return false;
-    constexpr int kRowChunks = kFP8 ? 8 : 16;  // 16-byte chunks per row
-    const int key0 = (x.nk - 1) * kTileKeys + x.tail_step * (kFP8 ? 2 * kBlockSize : kBlockSize);
+    constexpr int kRowChunks = 16;  // 16-byte chunks per row
+    const int key0 = (x.nk - 1) * kTileKeys + x.tail_step * kBlockSize;
 #pragma unroll
     for (int i = 0; i < kTailBytes / 16 / 32; ++i) {
       const int c = lane + 32 * i;
@@ -633,11 +628,8 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
         for (int qt = 0; qt < nq; ++qt) {
           uint8_t* dq = &sm.q[qt][0];
           const int tok = x.q0 + x.t0[qt];
-          // 16-bit: the two 64-dimension halves; E4M3: hi rows, then the lo rows
-          // (num_rows tokens further on)
           tc::tma_load_3d(dq, &tm_q, 0, x.kvh * g, tok, &sm.q_full);
-          tc::tma_load_3d(dq + kHalf, &tm_q, kFP8 ? 0 : 64, x.kvh * g, kFP8 ? p.num_rows + tok : tok,
-                          &sm.q_full);
+          tc::tma_load_3d(dq + kHalf, &tm_q, 64, x.kvh * g, tok, &sm.q_full);
         }
       }
     }
@@ -664,18 +656,126 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem& sm,
     // an answer still on its way lands before the CTA goes away (requests 0 .. n)
     if (pw == 0) mbar_wait(&sm.next_full[n % kAhead], (n / kAhead) & 1, 10000000ull);
     for (uint32_t y = pos > (uint32_t)nst ? pos - nst : 0; y < pos; ++y)
-      mbar_wait(&sm.full[y % nst], (y / nst) & 1, 10000000ull);
+      mbar_wait(&landed[y % nst], (y / nst) & 1, 10000000ull);
   }
+}
+
+// 16 E4M3 codes as 16-bit elements (each code is one of either type): exponent and
+// mantissa moved to the top of the 16-bit type's fields, and the difference of the
+// exponents' offsets, 2^120 or 2^8, multiplied in; that makes subnormal codes right
+// too, and needs none of the conversions that issue every few cycles.  A NaN code would
+// come out as 480; it is made one afterwards.
+template <class QT>
+__device__ __forceinline__ void widen16(const uint4& w, uint4* a, uint4* b) {
+  constexpr bool kBf = std::is_same<QT, BF16>::value;
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[8], odd = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    odd |= (u[i] & 0x7f7f7f7fu) + 0x01010101u;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t x = __byte_perm(u[i], 0u, j ? 0x3424 : 0x1404);  // codes in the high bytes
+      const uint32_t y = (x & 0x80008000u) | ((x & 0x7f007f00u) >> (kBf ? 4 : 1));
+      if constexpr (kBf) {
+        const __nv_bfloat162 k = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));
+        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), k);
+        o[2 * i + j] = *reinterpret_cast<const uint32_t*>(&r);
+      } else {
+        const __half2 k = __halves2half2(__ushort_as_half(0x5c00), __ushort_as_half(0x5c00));
+        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&y), k);
+        o[2 * i + j] = *reinterpret_cast<const uint32_t*>(&r);
+      }
+    }
+  }
+  if (odd & 0x80808080u) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t v = i < 2 ? w.x : (i < 4 ? w.y : (i < 6 ? w.z : w.w));
+      const uint32_t h = (i & 1) ? v >> 16 : v & 0xffffu;
+      uint32_t nan = 0;
+      if ((h & 0x7fu) == 0x7fu) nan |= 0x7fffu;
+      if ((h & 0x7f00u) == 0x7f00u) nan |= 0x7fff0000u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k == i) o[k] |= nan;
+    }
+  }
+  *a = make_uint4(o[0], o[1], o[2], o[3]);
+  *b = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Converter cw of six on an E4M3 cache: each tile that has landed, in ring order, from
+// [128 rows][128 B] in the second half of its stage to [2 halves][128 rows][128 B], all
+// with the 128-byte swizzle, the V rows past the context as zeros.  Row r of the codes
+// lies where row r of the second half of the elements will, so a warp that reads
+// whole rows before it writes them needs no order with the others.
+template <class QT, int kMods>
+__device__ __forceinline__ void mods_converter(const AttnParams& p, ModSmem<true>& sm, int total,
+                                               int cw) {
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  const int lane = threadIdx.x & 31, c = lane & 7;
+  uint32_t pos = 0;
+  bool ok = true;
+  ModItem x;
+  auto convert = [&](int rows) -> bool {
+    const int st = pos % kStages;
+    bool good = true;
+    if (lane == 0) good = wait_bar(&sm.staged[st], (pos / kStages) & 1, abort, lim);
+    if (!__shfl_sync(kFull, (int)good, 0)) return false;
+    ++pos;
+    uint8_t* tile = &sm.ring[st][0];
+    // four rows a turn, the next turn's codes read ahead (rolled: beside the softmax's
+    // code the instruction cache has little room, see above)
+    auto codes = [&](int u) {
+      const int r = 4 * u + (lane >> 3);
+      return *reinterpret_cast<const uint4*>(tile + kHalf + r * 128 + ((c ^ (r & 7)) << 4));
+    };
+    uint4 w = codes(cw);
+#pragma unroll 1
+    for (int u = cw; u < kTileKeys / 4; u += kConverters) {
+      const int r = 4 * u + (lane >> 3);
+      uint4 nw = w;
+      if (u + kConverters < kTileKeys / 4) nw = codes(u + kConverters);
+      uint4 a, b;
+      widen16<QT>(r < rows ? w : make_uint4(0, 0, 0, 0), &a, &b);
+      __syncwarp();  // the four rows have been read
+      // chunks 2 (c % 4) and 2 (c % 4) + 1 of half c / 4; the halves' lanes store them
+      // in opposite order, so that eight lanes hit eight different bank groups
+      uint8_t* d = tile + (c >> 2) * kHalf + r * 128;
+      const int k0 = 2 * (c & 3) + (c >> 2), k1 = k0 ^ 1;
+      *reinterpret_cast<uint4*>(d + ((k0 ^ (r & 7)) << 4)) = c >> 2 ? b : a;
+      *reinterpret_cast<uint4*>(d + ((k1 ^ (r & 7)) << 4)) = c >> 2 ? a : b;
+      w = nw;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.full[st]);
+    return true;
+  };
+  for (uint32_t n = 0; ok; ++n) {
+    int k;
+    const int got = take_next(sm, n, &k, abort, lim);
+    if (got <= 0) {
+      ok = got == 0;
+      break;
+    }
+    make_item<kMods, true>(p, sm, k, total, x);
+    for (int i = x.kt0; ok && i < x.nk; ++i)
+      ok = convert(kTileKeys) && convert(x.ctx - tile_of<kMods>(x, i) * kTileKeys);
+  }
+  if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
 }
 
 // MMA issuer.  Order per item: S_a, S_b of the first step, then for each step i
 //   P_a(i) V, S_a(i + 1), P_b(i) V, S_b(i + 1)
 // so that one query tile's softmax works while the tensor pipe serves the other.
 template <class QT, bool kFP8, int kMods>
-__device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem& sm, uint32_t tmem, int total) {
-  constexpr int kStageBytes = kFP8 ? kTileBytes / 2 : kTileBytes;
-  constexpr int nst = kFP8 ? kStages8 : kStages;
-  constexpr uint32_t kAB = !kFP8 && std::is_same<QT, BF16>::value ? 1u : 0u;
+__device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem<kFP8>& sm, uint32_t tmem, int total) {
+  constexpr int kStageBytes = kTileBytes;
+  constexpr int nst = kStages;
+  constexpr uint32_t kAB = std::is_same<QT, BF16>::value ? 1u : 0u;
   constexpr uint32_t kIdescS = tc::idesc_f16(kAB, 0, 0, 128, 128);
   constexpr uint32_t kIdescO = tc::idesc_f16(kAB, 0, 1, 128, 128);
   volatile int* abort = &sm.abort;
@@ -703,15 +803,12 @@ __device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem& sm, ui
   const uint64_t dq[2] = {tc::smem_desc(smem_u32(&sm.q[0][0]), 16, 1024, tc::kLayoutSw128),
                           tc::smem_desc(smem_u32(&sm.q[1][0]), 16, 1024, tc::kLayoutSw128)};
   const uint64_t dk0 = tc::smem_desc(smem_u32(&sm.ring[0][0]), 16, 1024, tc::kLayoutSw128);
-  const uint64_t dv0 =
-      tc::smem_desc(smem_u32(&sm.ring[0][0]), kFP8 ? 16 : kHalf, 1024, tc::kLayoutSw128);
-  const uint64_t dtail =
-      tc::smem_desc(smem_u32(&sm.tail[0]), kFP8 ? 16 : kTailBytes / 2, 1024, tc::kLayoutSw128);
+  const uint64_t dv0 = tc::smem_desc(smem_u32(&sm.ring[0][0]), kHalf, 1024, tc::kLayoutSw128);
+  const uint64_t dtail = tc::smem_desc(smem_u32(&sm.tail[0]), kTailBytes / 2, 1024, tc::kLayoutSw128);
   auto mma_s = [&](int qt, int st) {
     if (leader) {
       const uint64_t dk = dk0 + (uint64_t)(st * (kStageBytes >> 4));
-      if constexpr (kFP8) issue_scores8(tmem + qt * 128, qt ? dq[1] : dq[0], dk, kIdescS);
-      else issue_scores(tmem + qt * 128, qt ? dq[1] : dq[0], dk, kIdescS);
+      issue_scores(tmem + qt * 128, qt ? dq[1] : dq[0], dk, kIdescS);
     }
     commit(&sm.s_ready[qt]);
   };
@@ -725,7 +822,7 @@ __device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem& sm, ui
       const uint64_t dv = dv0 + (uint64_t)(st * (kStageBytes >> 4));
       const int ts = tile_of<kMods>(x, i) == x.nk - 1 ? x.tail_step : -1;
       const uint32_t d = tmem + kColO + qt * 128, a = tmem + qt * 128, acc = i != x.kt0;
-      issue_mods_pv<kFP8>(d, a, dv, dtail, ts, acc, kIdescO);
+      issue_pv(d, a, dv, dtail, ts, acc, kIdescO);
     }
     if (i == x.last[qt]) commit(&sm.o_done[qt]);
     return true;
@@ -788,9 +885,8 @@ __device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem& sm, ui
 
 // Softmax and epilogue: thread = row of query tile qt.
 template <class QT, bool kFP8, int kMods>
-__device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, uint32_t tmem, int total) {
+__device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>& sm, uint32_t tmem, int total) {
   using OutT = typename QT::T;
-  constexpr float kMove = kFP8 ? kMove8 : kRescaleAt;
   volatile int* abort = &sm.abort;
   const unsigned long long lim = wait_limit(p);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -842,8 +938,6 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
       continue;
     }
     const float slope = (kMods & kModBias) && valid ? __ldg(p.alibi + h) * kLog2e : 0.0f;
-    // E4M3 caches: the row's query scale s (q / s = hi + lo) joins the score scale
-    const float a = kFP8 && valid ? qa * __ldg(p.q8_scale + head) : qa;
     float m_run = -INFINITY;
     float2 l2[4];  // partial row sums (independent chains, packed pairs)
 #pragma unroll
@@ -874,7 +968,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
 #pragma unroll
         for (int c = 0; c < kTileKeys; ++c) sv[c] = -sv[c];
       }
-      const float f = modify_scores<kMods>(p, sv, a, slope, pos, k0);
+      const float f = modify_scores<kMods>(p, sv, qa, slope, pos, k0);
       if (!__all_sync(kFull, lo <= k0 && hi >= k0 + kTileKeys)) {
         // an interval of some row of the warp ends in this tile: hidden keys become -inf
 #pragma unroll
@@ -891,7 +985,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
       // move the running max (and rescale O) only on a large increase; O is complete
       // up to the step before (this S was issued after its product)
       const bool fresh = m_run == -INFINITY;  // no key seen so far
-      const bool need = mt > m_run + kMove;
+      const bool need = mt > m_run + kRescaleAt;
       float alpha = 1.0f;
       if (need) {
         alpha = fresh ? 0.0f : fast_exp2(m_run - mt);
@@ -899,32 +993,18 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
 #pragma unroll
         for (int c = 0; c < 4; ++c) l2[c] = __fmul2_rn(l2[c], make_float2(alpha, alpha));
       }
-      // (2^(-inf - 0) = 0)
-      const float m = (m_run == -INFINITY ? 0.0f : m_run) - (kFP8 ? kScaleLog8 : 0.0f);
+      const float m = m_run == -INFINITY ? 0.0f : m_run;  // 2^(-inf - 0) = 0
       // weights, over the scores read (hidden keys are -inf: weight 0)
 #pragma unroll
       for (int c = 0; c < kTileKeys / kChunk; ++c) {
-        // 16 columns: packed 16-bit pairs, or 8 of four E4M3 codes (hi) and 8 of lo
         float pk[16];
-        uint32_t h0 = 0, r0 = 0;
+        const float2 f2 = make_float2(f, f), m2 = make_float2(-m, -m);
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) {
-          const float x = fast_exp2(fmaf(sv[kChunk * c + e], f, -m));
-          const float y = fast_exp2(fmaf(sv[kChunk * c + e + 1], f, -m));
-          l2[(e >> 1) & 3] = __fadd2_rn(l2[(e >> 1) & 3], make_float2(x, y));
-          if constexpr (!kFP8) {
-            pk[e >> 1] = __uint_as_float(pack2<QT>(x, y));
-          } else {
-            uint32_t h1, r1;
-            split_e4m3(make_float2(x, y), &h1, &r1);
-            if (e & 2) {
-              pk[e >> 2] = __uint_as_float(h0 | (h1 << 16));
-              pk[8 + (e >> 2)] = __uint_as_float(r0 | (r1 << 16));
-            } else {
-              h0 = h1;
-              r0 = r1;
-            }
-          }
+          const float2 y = __ffma2_rn(make_float2(sv[kChunk * c + e], sv[kChunk * c + e + 1]), f2, m2);
+          const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+          l2[(e >> 1) & 3] = __fadd2_rn(l2[(e >> 1) & 3], w);
+          pk[e >> 1] = __uint_as_float(pack2<QT>(w.x, w.y));
         }
         tc::tmem_st16(s_col + 16 * c, pk);
       }
@@ -953,7 +1033,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
     ok = all_of_tile(wait(&sm.o_done[qt], nit & 1), qt);
     if (!ok) break;
     tc::fence_after_sync();
-    const float inv = valid && !empty ? p.v_scale / l : 0.0f;  // (E4M3: V's codes, scaled)
+    const float inv = valid && !empty ? p.v_scale / l : 0.0f;
     bool odd = false;  // an output that is not finite
 #pragma unroll 1
     for (int c = 0; c < kD; c += 32) {
@@ -994,25 +1074,27 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem& sm, u
 }
 
 template <class QT, bool kFP8, int kMods>
-__global__ void __launch_bounds__(kModThreads, 1)
+__global__ void __launch_bounds__(mod_threads(kFP8), 1)
     prefill_mods_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_q, int kv_rows) {
   extern __shared__ uint8_t smem_raw[];
-  ModSmem& sm = *reinterpret_cast<ModSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                            ~uintptr_t(1023));
+  using SM = ModSmem<kFP8>;
+  SM& sm = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
   mods_setup(p, sm, tm_k, tm_v, tm_q);
   const uint32_t tmem = sm.tmem_base;
   const int total = sm.seq_start[p.num_seqs] * p.num_kv_heads;
   if (warp >= kSoftWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(kFP8)));
     if (warp == kWarpMma)
       mods_issuer<QT, kFP8, kMods>(p, sm, tmem, total);
-    else
+    else if (warp < kWarpTma + mod_producers(kFP8))
       mods_producer<kFP8, kMods>(p, sm, tm_k, tm_v, tm_q, kv_rows, total, warp - kWarpTma);
+    else if constexpr (kFP8)
+      mods_converter<QT, kMods>(p, sm, total, warp - kWarpTma - mod_producers(true));
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(soft_regs(kFP8)));
     mods_softmax<QT, kFP8, kMods>(p, sm, tmem, total);
   }
   tc::fence_before_sync();
@@ -1024,29 +1106,29 @@ __global__ void __launch_bounds__(kModThreads, 1)
 }
 
 template <class QT, bool kFP8, int kMods>
-int launch_mods(const AttnParams& p, int total_q, const uint8_t* q8, cudaStream_t stream) {
+int launch_mods(const AttnParams& p, int total_q, cudaStream_t stream) {
   const bool bf16 = std::is_same<QT, BF16>::value;
   const uint64_t kv_rows = (uint64_t)p.num_blocks * p.num_kv_heads * kBlockSize;
   const uint32_t g = (uint32_t)p.group, tokens = kRowsM / g, heads = (uint32_t)p.num_heads;
   CUtensorMap tk, tv, tq;
   const bool maps =
-      kFP8 ? make_map_e4m3(&tk, p.k_cache, kv_rows, 16) && make_map_e4m3(&tv, p.v_cache, kv_rows, 16) &&
-                 make_map_q3d_e4m3(&tq, q8, 2 * (uint64_t)total_q, heads, g, tokens)
-           : make_map_2d(&tk, p.k_cache, kv_rows, bf16, 16) &&
-                 make_map_2d(&tv, p.v_cache, kv_rows, bf16, 16) &&
-                 make_map_q3d(&tq, p.q, (uint64_t)total_q, heads, bf16, g, tokens);
+      (kFP8 ? make_map_e4m3(&tk, p.k_cache, kv_rows, 16) && make_map_e4m3(&tv, p.v_cache, kv_rows, 16)
+            : make_map_2d(&tk, p.k_cache, kv_rows, bf16, 16) &&
+                  make_map_2d(&tv, p.v_cache, kv_rows, bf16, 16)) &&
+      make_map_q3d(&tq, p.q, (uint64_t)total_q, heads, bf16, g, tokens);
   if (!maps) return PKV_ERR_CUDA;
-  const size_t smem = sizeof(ModSmem) + 1024;
-  static_assert(sizeof(ModSmem) + 1024 <= 232448, "shared memory budget of one CTA");
-  static_assert(offsetof(ModSmem, ring) % 1024 == 0 && offsetof(ModSmem, q) % 1024 == 0 &&
-                    offsetof(ModSmem, tail) % 1024 == 0,
+  using SM = ModSmem<kFP8>;
+  const size_t smem = sizeof(SM) + 1024;
+  static_assert(sizeof(SM) + 1024 <= 232448, "shared memory budget of one CTA");
+  static_assert(offsetof(SM, ring) % 1024 == 0 && offsetof(SM, q) % 1024 == 0 &&
+                    offsetof(SM, tail) % 1024 == 0,
                 "swizzled buffers must start on 1024-byte boundaries");
   auto kern = prefill_mods_kernel<QT, kFP8, kMods>;
-  // the kernel's register shares add up to what 384 x 168 hold; with fewer its
+  // the kernel's register shares add up to what its launch holds; with fewer its
   // warpgroups would wait for registers without end
   cudaFuncAttributes fa;
   if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
-  if (fa.numRegs * kModThreads < 32 * kSoftWarps * kSoftRegs + 128 * kOtherRegs) return PKV_ERR_CUDA;
+  if (fa.numRegs != launch_regs(kFP8)) return PKV_ERR_CUDA;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return PKV_ERR_CUDA;
@@ -1062,21 +1144,21 @@ int launch_mods(const AttnParams& p, int total_q, const uint8_t* q8, cudaStream_
     // last of each perhaps short, times the KV heads); those past the last do nothing
     const long long pairs = total_q / (2 * (long long)tokens) + c.num_seqs;
     const long long items = pairs * p.num_kv_heads;
-    kern<<<(unsigned)items, kModThreads, smem, stream>>>(c, tk, tv, tq, (int)kv_rows);
+    kern<<<(unsigned)items, mod_threads(kFP8), smem, stream>>>(c, tk, tv, tq, (int)kv_rows);
     if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   }
   return PKV_OK;
 }
 
-// q8: the split query of an E4M3 cache, or null
 template <int kMods>
-int launch_mods_typed(const AttnParams& p, int q_dtype, int total_q, const uint8_t* q8,
+int launch_mods_typed(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
                       cudaStream_t stream) {
+  const bool fp8 = kv_dtype == PKV_FP8_E4M3;
   if (q_dtype == PKV_BF16)
-    return q8 ? launch_mods<BF16, true, kMods>(p, total_q, q8, stream)
-              : launch_mods<BF16, false, kMods>(p, total_q, q8, stream);
-  return q8 ? launch_mods<F16, true, kMods>(p, total_q, q8, stream)
-            : launch_mods<F16, false, kMods>(p, total_q, q8, stream);
+    return fp8 ? launch_mods<BF16, true, kMods>(p, total_q, stream)
+               : launch_mods<BF16, false, kMods>(p, total_q, stream);
+  return fp8 ? launch_mods<F16, true, kMods>(p, total_q, stream)
+             : launch_mods<F16, false, kMods>(p, total_q, stream);
 }
 
 }  // namespace

@@ -11,20 +11,13 @@ bool prefill_mods_supported(const AttnParams& p, int head_dim) {
          2 * (uint64_t)p.num_rows * p.num_heads < (1ull << 31) && tmap_available();
 }
 
-int launch_prefill_mods(const AttnParams& p, int q_dtype, int kv_dtype, int total_q, void* workspace,
-                        size_t workspace_bytes, cudaStream_t stream) {
-  AttnParams c = p;
-  const uint8_t* q8 = nullptr;
-  if (kv_dtype == PKV_FP8_E4M3) {
-    const int rc = launch_split_query(p, q_dtype, total_q, workspace, workspace_bytes, true, &q8,
-                                      &c.q8_scale, stream);
-    if (rc != PKV_OK) return rc;
-  }
+int launch_prefill_mods(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+                        cudaStream_t stream) {
   if (p.softcap > 0.0f)
-    return p.alibi ? launch_prefill_cap_bias(c, q_dtype, total_q, q8, stream)
-                   : launch_prefill_cap(c, q_dtype, total_q, q8, stream);
-  return p.alibi ? launch_prefill_bias(c, q_dtype, total_q, q8, stream)
-                 : pre_mods::launch_mods_typed<0>(c, q_dtype, total_q, q8, stream);
+    return p.alibi ? launch_prefill_cap_bias(p, q_dtype, kv_dtype, total_q, stream)
+                   : launch_prefill_cap(p, q_dtype, kv_dtype, total_q, stream);
+  return p.alibi ? launch_prefill_bias(p, q_dtype, kv_dtype, total_q, stream)
+                 : pre_mods::launch_mods_typed<0>(p, q_dtype, kv_dtype, total_q, stream);
 }
 
 }  // namespace pkv

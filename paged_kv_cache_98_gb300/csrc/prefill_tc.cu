@@ -42,14 +42,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // first.  hi rows [rows][heads][128 B], then the lo rows, then s [rows][heads].
 constexpr int kPerHalf = 2;
 
-// pow2: s is the next power of two above that (the biased call: hi + lo then hold
-// a bf16 query exactly, but for elements below 2^-15 of the row's largest).
 template <class QT>
 __global__ void __launch_bounds__(256) split_query_kernel(const typename QT::T* __restrict__ q,
                                                           uint8_t* __restrict__ hi,
                                                           uint8_t* __restrict__ lo,
                                                           float* __restrict__ scale,
-                                                          long long row_heads, bool pow2) {
+                                                          long long row_heads) {
   const long long half = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 4;
   const int lane = threadIdx.x & 15;
   uint4 raw[kPerHalf];
@@ -69,12 +67,7 @@ __global__ void __launch_bounds__(256) split_query_kernel(const typename QT::T* 
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
 #pragma unroll
     for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o, 16));
-    float inv = amax > 0.0f ? 448.0f / amax : 1.0f;
-    float sc = amax > 0.0f ? amax / 448.0f : 1.0f;
-    if (pow2) {
-      sc = __uint_as_float((__float_as_uint(fmaxf(sc, 0x1p-100f)) + 0x7fffffu) & 0xff800000u);
-      inv = 1.0f / sc;
-    }
+    const float inv = amax > 0.0f ? 448.0f / amax : 1.0f;
     uint32_t h4[2] = {0, 0}, l4[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
@@ -91,7 +84,7 @@ __global__ void __launch_bounds__(256) split_query_kernel(const typename QT::T* 
     if (w < row_heads) {
       reinterpret_cast<uint2*>(hi + w * kD)[lane] = make_uint2(h4[0], h4[1]);
       reinterpret_cast<uint2*>(lo + w * kD)[lane] = make_uint2(l4[0], l4[1]);
-      if (lane == 0) scale[w] = sc;
+      if (lane == 0) scale[w] = amax > 0.0f ? amax / 448.0f : 1.0f;
     }
   }
 }
@@ -229,9 +222,8 @@ size_t prefill_q8_bytes(int total_q, int num_heads) {
   return round256(2 * rh * kD) + round256(rh * sizeof(float));
 }
 
-int launch_split_query(const AttnParams& p, int q_dtype, int total_q, void* workspace,
-                       size_t workspace_bytes, bool pow2, const uint8_t** q8, const float** q8_scale,
-                       cudaStream_t stream) {
+int launch_prefill_tc_fp8(const AttnParams& p, int q_dtype, int total_q, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
   const size_t need = prefill_q8_bytes(total_q, p.num_heads);
   if (!workspace || workspace_bytes < need) return PKV_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_ERR_INVALID_ARG;
@@ -242,26 +234,18 @@ int launch_split_query(const AttnParams& p, int q_dtype, int total_q, void* work
   // sixteen threads per kPerHalf (row, head)s
   const long long blocks = (((long long)rh + kPerHalf - 1) / kPerHalf * 16 + 255) / 256;
   if (blocks > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  if (q_dtype == PKV_BF16)
-    split_query_kernel<BF16><<<(unsigned)blocks, 256, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(p.q), hi, lo, scale, (long long)rh, pow2);
-  else
-    split_query_kernel<F16><<<(unsigned)blocks, 256, 0, stream>>>(
-        static_cast<const __half*>(p.q), hi, lo, scale, (long long)rh, pow2);
-  *q8 = hi;
-  *q8_scale = scale;
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
-}
-
-int launch_prefill_tc_fp8(const AttnParams& p, int q_dtype, int total_q, void* workspace,
-                          size_t workspace_bytes, cudaStream_t stream) {
   AttnParams c = p;
-  const uint8_t* q8;
-  const int rc = launch_split_query(p, q_dtype, total_q, workspace, workspace_bytes, false, &q8,
-                                    &c.q8_scale, stream);
-  if (rc != PKV_OK) return rc;
-  return q_dtype == PKV_BF16 ? launch_typed<BF16>(c, total_q, stream, q8)
-                             : launch_typed<F16>(c, total_q, stream, q8);
+  c.q8_scale = scale;
+  if (q_dtype == PKV_BF16) {
+    split_query_kernel<BF16><<<(unsigned)blocks, 256, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(p.q), hi, lo, scale, (long long)rh);
+    if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+    return launch_typed<BF16>(c, total_q, stream, hi);
+  }
+  split_query_kernel<F16><<<(unsigned)blocks, 256, 0, stream>>>(
+      static_cast<const __half*>(p.q), hi, lo, scale, (long long)rh);
+  if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+  return launch_typed<F16>(c, total_q, stream, hi);
 }
 
 }  // namespace pkv

@@ -546,3 +546,45 @@ def test_steps_of_a_small_server(kv):
         # the worst case above is loose: on the whole the outputs are far nearer
         far = float((got - want).norm() / want.norm())
         assert far < (2.0 ** -6 if kv == "same" else 2.0 ** -3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_prefill_every_e4m3_code(dtype):
+    """A window of one key returns that key's V: every code of an E4M3 cache, subnormal and
+    NaN ones among them, in every position of a tile."""
+    b = Batch(61, [(200, 200)], H=4, hkv=1, dtype=dtype, kv="e4m3", window=1)
+    codes = torch.arange(200 * 128, dtype=torch.int64).view(200, 128)
+    codes = ((codes * 37 + codes // 256) % 256).to(torch.uint8)
+    for s in range(200):
+        b.vc.view(torch.uint8)[int(b.tables[0, s // 16]), 0, s % 16] = codes[s].to(DEV)
+    b.vs = 0.5
+    got = b.call().double().cpu()
+    want = codes.view(torch.float8_e4m3fn).double().mul(0.5)[:, None].expand(200, 4, 128)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(kv="e4m3"), dict(alibi=True), dict(kv="e4m3", alibi=True, softcap=9.0)])
+@pytest.mark.parametrize("skip", [1, 2, 5])
+def test_prefill_wait_runs_out(kw, skip):
+    """A tile copy that never comes: the call reports it, and the next one is whole."""
+    b = Batch(67, [(300, 700), (40, 40)], H=8, hkv=2, **kw)
+    good = b.call()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.debug_arm_wait_timeout(skip, 20000)
+    b.call(errors=err)
+    assert pkv.check_errors(err) & 8
+    assert torch.equal(b.call(errors=err), good)
+    assert pkv.check_errors(err) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(window=200), dict(kv="e4m3", softcap=9.0)])
+def test_decode_wait_runs_out(kw):
+    b = Decode(71, [900, 40, 1300], H=8, hkv=2, **kw)
+    good = b.call()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.debug_arm_wait_timeout(2, 20000)
+    b.call(errors=err)
+    assert pkv.check_errors(err) & 8
+    assert torch.equal(b.call(errors=err), good)
+    assert pkv.check_errors(err) == 0
