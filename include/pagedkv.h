@@ -388,6 +388,8 @@ int pkv_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pairs, in
  * list that runs out (its entries become -1), flags PKV_DEVERR_BLOCK_ID, and the
  * tokens of such a block get slot -1.  Two sequences of one row are a caller's
  * error (that row's entries are unspecified).
+ * No output may share memory with an input or another output
+ * (PKV_ERR_INVALID_ARG): lengths are not updated in place.
  * At most PKV_STEP_MAPS_MAX_SEQS sequences (PKV_ERR_UNSUPPORTED beyond).
  */
 #define PKV_STEP_MAPS_MAX_SEQS 16384
@@ -440,7 +442,7 @@ int pkv_rotary_frequencies(double* inv_freq, int rotary_dim, double base,
  *             projection's output will do.
  *   q_out     [num_tokens][num_heads][head_dim] contiguous; may be q itself
  *             (with q_stride num_heads * head_dim), must not overlap q, k or v
- *             otherwise.
+ *             otherwise.  The caches overlap nothing else.
  *   positions [num_tokens] int32.  A negative position is a padding token:
  *             nothing is written for it.
  *   slot_mapping [num_tokens] int64, as for pkv_reshape_and_cache (a negative
@@ -488,6 +490,7 @@ int pkv_rotary_and_cache(void* q_out, const void* q, const void* k, const void* 
  * table entries of blocks that no row of the batch sees are not read (a
  * sequence may have returned the blocks behind its window).
  * NULL / zero members switch a modifier off; a NULL struct switches all off.
+ * In these calls out must not overlap q or the caches (PKV_ERR_INVALID_ARG).
  */
 typedef struct {
   float softcap;
@@ -519,7 +522,10 @@ int pkv_paged_attention_decode_biased(void* out, const void* q, const void* k_ca
  * Chunked-prefill attention under pkv_score_mods; other arguments as for
  * pkv_paged_attention_prefill_chunk.
  * workspace: at least pkv_prefill_biased_workspace_size(...) bytes, 256-byte
- * aligned (NULL when that is 0, as it is for 16-bit caches of head_dim 128).
+ * aligned (NULL when that is 0, as it is for head_dim 128).
+ * head_dim 128 runs on the tensor cores, for caches of up to 2^31 rows
+ * (num_blocks * num_kv_heads * 16; PKV_ERR_UNSUPPORTED beyond); head_dim 64 on the
+ * CUDA cores, a query row at a time.
  */
 size_t pkv_prefill_biased_workspace_size(int num_seqs, int total_q, int num_heads,
                                          int num_kv_heads, int head_dim, int max_context_len,

@@ -73,6 +73,16 @@ int set_mods(pkv::AttnParams& p, const pkv_score_mods* m, int max_context_len, f
   return PKV_OK;
 }
 
+// Rows of the biased calls are computed again from q and the caches where an output is
+// not finite, so out must be memory of its own.
+bool out_is_apart(const void* out, const void* q, const void* k_cache, const void* v_cache,
+                  long long rows, int num_heads, int head_dim, long long cache_elems, int kv_dtype) {
+  const unsigned long long n = 2ull * rows * num_heads * head_dim;
+  const unsigned long long c = cache_elems * (kv_dtype == PKV_FP8_E4M3 ? 1ull : 2ull);
+  return !pkv::bytes_overlap(out, n, q, n) && !pkv::bytes_overlap(out, n, k_cache, c) &&
+         !pkv::bytes_overlap(out, n, v_cache, c);
+}
+
 // Checks shared by decode and prefill.
 int check_attention_args(const void* out, const void* q, const void* k_cache,
                          const void* v_cache, const int32_t* block_tables,
@@ -587,6 +597,9 @@ int pkv_paged_attention_decode_biased(void* out, const void* q, const void* k_ca
   if (rc != PKV_OK) return rc;
   if (p.bidir_lens) return PKV_ERR_INVALID_ARG;  // a decode row is the last token
   if (num_seqs == 0) return PKV_OK;
+  const long long cache = (long long)num_blocks * num_kv_heads * pkv::kBlockSize * head_dim;
+  if (!out_is_apart(out, q, k_cache, v_cache, num_seqs, num_heads, head_dim, cache, kv_dtype))
+    return PKV_ERR_INVALID_ARG;
   p.out = out;
   p.q = q;
   p.k_cache = static_cast<const uint8_t*>(k_cache);
@@ -642,6 +655,9 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
   rc = set_mods(p, mods, max_context_len, scale, k_scale, kv_dtype);
   if (rc != PKV_OK) return rc;
   if (num_seqs == 0 || total_q == 0) return PKV_OK;
+  const long long cache = (long long)num_blocks * num_kv_heads * pkv::kBlockSize * head_dim;
+  if (!out_is_apart(out, q, k_cache, v_cache, total_q, num_heads, head_dim, cache, kv_dtype))
+    return PKV_ERR_INVALID_ARG;
   p.out = out;
   p.q = q;
   p.k_cache = static_cast<const uint8_t*>(k_cache);

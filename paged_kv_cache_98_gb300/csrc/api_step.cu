@@ -11,10 +11,12 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Do [a, a + na) and [b, b + nb) share a byte?
-bool overlap(const void* a, unsigned long long na, const void* b, unsigned long long nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
+struct Range {
+  const void* p;
+  unsigned long long bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+  return a.bytes > 0 && b.bytes > 0 && pkv::bytes_overlap(a.p, a.bytes, b.p, b.bytes);
 }
 
 }  // namespace
@@ -41,6 +43,19 @@ int pkv_build_step_maps(int32_t* block_tables, int32_t* context_lens, int32_t* q
   if (block_size != pkv::kBlockSize) return PKV_ERR_UNSUPPORTED;
   if (num_seqs > PKV_STEP_MAPS_MAX_SEQS) return PKV_ERR_UNSUPPORTED;
   if ((long long)max_blocks_per_seq * pkv::kBlockSize > (1LL << 30)) return PKV_ERR_UNSUPPORTED;
+  // CTAs read the inputs while others write: no output may share memory with an
+  // input or with another output (lengths updated in place, tables that are one)
+  const unsigned long long S = num_seqs, row = 4ull * max_blocks_per_seq;
+  const Range out[] = {{block_tables, S * row}, {context_lens, 4 * S}, {query_start_loc, 4 * (S + 1)},
+                       {slot_mapping, 8ull * num_tokens}, {positions, 4ull * num_tokens},
+                       {request_tables, S > 0 ? num_request_rows * row : 0}};
+  const Range in[] = {{rows, 4 * S}, {cached_lens, 4 * S}, {q_lens, 4 * S}, {new_blocks, 4ull * num_new_blocks}};
+  for (int i = 0; i < 6; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return PKV_ERR_INVALID_ARG;
+    for (int j = 0; j < 4; ++j)
+      if (overlap(out[i], in[j])) return PKV_ERR_INVALID_ARG;
+  }
   return pkv::launch_step_maps(block_tables, context_lens, query_start_loc, slot_mapping,
                                positions, request_tables, rows, cached_lens, q_lens, new_blocks,
                                num_seqs, num_request_rows, max_blocks_per_seq, num_tokens,
@@ -132,11 +147,16 @@ int pkv_rotary_and_cache(void* q_out, const void* q, const void* k, const void* 
     return PKV_ERR_INVALID_ARG;
   // q_out may be q with the same layout; any other overlap would be read after it is written
   const unsigned long long t1 = (unsigned long long)num_tokens - 1;
-  const unsigned long long nq = 2 * (t1 * q_stride + qrow), no = 2 * (t1 + 1) * qrow;
-  if (!(q_out == q && q_stride == qrow) && overlap(q_out, no, q, nq)) return PKV_ERR_INVALID_ARG;
-  if (overlap(q_out, no, k, 2 * (t1 * k_stride + krow)) ||
-      overlap(q_out, no, v, 2 * (t1 * v_stride + krow)))
-    return PKV_ERR_INVALID_ARG;
+  const Range ro{q_out, 2 * (t1 + 1) * qrow}, rq{q, 2 * (t1 * q_stride + qrow)};
+  const Range rk{k, 2 * (t1 * k_stride + krow)}, rv{v, 2 * (t1 * v_stride + krow)};
+  const unsigned long long nc = (unsigned long long)num_blocks * pkv::kBlockSize * krow *
+                                (cache_dtype == PKV_FP8_E4M3 ? 1 : 2);
+  if (!(q_out == q && q_stride == qrow) && overlap(ro, rq)) return PKV_ERR_INVALID_ARG;
+  if (overlap(ro, rk) || overlap(ro, rv)) return PKV_ERR_INVALID_ARG;
+  for (const Range& c : {Range{k_cache, nc}, Range{v_cache, nc}})
+    if (overlap(c, ro) || overlap(c, rq) || overlap(c, rk) || overlap(c, rv))
+      return PKV_ERR_INVALID_ARG;
+  if (overlap({k_cache, nc}, {v_cache, nc})) return PKV_ERR_INVALID_ARG;
   pkv::RotaryArgs a{q_out, q, k, v, k_cache, v_cache, slot_mapping, positions,
                     q_stride, k_stride, v_stride, num_tokens, num_heads, num_kv_heads, head_dim,
                     num_blocks, rotary_dim, (int)layout, (int)src_dtype, (int)cache_dtype,

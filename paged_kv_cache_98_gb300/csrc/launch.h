@@ -8,6 +8,12 @@
 
 namespace pkv {
 
+// Do [a, a + na) and [b, b + nb) share a byte?
+inline bool bytes_overlap(const void* a, unsigned long long na, const void* b, unsigned long long nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
 // Longest a device-side wait may take before the kernel gives up, flags
 // PKV_DEVERR_TIMEOUT and returns (about 2 s).
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;

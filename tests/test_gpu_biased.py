@@ -588,3 +588,28 @@ def test_decode_wait_runs_out(kw):
     assert pkv.check_errors(err) & 8
     assert torch.equal(b.call(errors=err), good)
     assert pkv.check_errors(err) == 0
+
+
+def test_prefill_many_sequences():
+    """More sequences than one launch's tables hold."""
+    seqs = [(1 + s % 3, 1 + s % 3 + (s * 7) % 50) for s in range(1100)]
+    run(Batch(73, seqs, H=2, hkv=1, window=20, softcap=15.0))
+    run(Batch(74, seqs[:1030], H=2, hkv=2, kv="e4m3", prefix=[s % 60 for s in range(1030)]))
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+def test_blocks_past_four_gigabytes(kv):
+    """Caches whose byte offsets do not fit 32 bits: the sequences live in the last blocks."""
+    dec = Decode(79, [40, 700], H=8, hkv=8, window=600, kv=kv)
+    dec4 = Decode(79, [40, 700], H=16, hkv=8, softcap=9.0, kv=kv)
+    pre = Batch(80, [(70, 200)], H=8, hkv=8, alibi=True, kv=kv)
+    for b in (dec, dec4, pre):
+        blocks = 5 * 2 ** 30 // (8 * 16 * 128 * (1 if kv == "e4m3" else 2))
+        shift = blocks - b.nb
+        for name in ("kc", "vc"):
+            small = getattr(b, name)
+            big = torch.empty((blocks, 8, 16, 128), dtype=small.dtype, device=DEV)
+            big[shift:].view(torch.uint8).copy_(small.view(torch.uint8))
+            setattr(b, name, big)
+        b.tables = np.where(b.tables >= 0, b.tables + shift, b.tables)
+        b.check(b.call())

@@ -21,9 +21,9 @@ def lib():
 # ---- step maps -------------------------------------------------------------------------------
 
 def _maps(lib, **over):
-    a = dict(block_tables=256, context_lens=256, query_start_loc=256, slot_mapping=256,
-             positions=256, request_tables=512, rows=512, cached_lens=512, q_lens=512,
-             new_blocks=512, num_seqs=2, num_request_rows=4, max_blocks=8, num_tokens=4,
+    a = dict(block_tables=4096, context_lens=8192, query_start_loc=8448, slot_mapping=8704,
+             positions=8960, request_tables=12288, rows=512, cached_lens=768, q_lens=1024,
+             new_blocks=1280, num_seqs=2, num_request_rows=4, max_blocks=8, num_tokens=4,
              num_new=2, block_size=16, num_blocks=64, errors=None, stream=None)
     a.update(over)
     return lib.pkv_build_step_maps(*a.values())
@@ -36,6 +36,10 @@ def _maps(lib, **over):
     (dict(q_lens=None), -1), (dict(new_blocks=None), -1), (dict(num_seqs=-1), -1),
     (dict(num_request_rows=0), -1), (dict(max_blocks=0), -1), (dict(num_tokens=-1), -1),
     (dict(num_new=-1), -1), (dict(num_blocks=0), -1), (dict(slot_mapping=260), -1),
+    # outputs over inputs (lengths in place) and over one another
+    (dict(context_lens=768), -1), (dict(context_lens=1020), -1), (dict(query_start_loc=1028), -1),
+    (dict(block_tables=12288), -1), (dict(request_tables=4096 - 4), -1), (dict(positions=8704 + 28), -1),
+    (dict(slot_mapping=1280), -1), (dict(positions=8196), -1),
     (dict(block_size=32), -2), (dict(num_seqs=16385), -2), (dict(max_blocks=1 << 27), -2),
 ])
 def test_maps_refusals(lib, over, status):
@@ -71,6 +75,8 @@ def _rot(lib, **over):
     # q_out over q with another layout, over k, over v
     (dict(q_out=1 << 22, qs=1536), -1), (dict(q_out=(1 << 22) + 2048), -1),
     (dict(q_out=(1 << 23) + 512), -1), (dict(q_out=(1 << 24) - 4096), -1),
+    (dict(k_cache=1 << 26), -1), (dict(v_cache=(1 << 25) + 64), -1), (dict(k_cache=1 << 20), -1),
+    (dict(v_cache=1 << 24), -1),
     (dict(tokens=0), 0),
 ])
 def test_rotary_refusals(lib, over, status):
@@ -154,7 +160,7 @@ def _mods(**over):
 
 
 def _decode(lib, mods=None, **over):
-    a = dict(out=256, q=256, k_cache=512, v_cache=512, block_tables=1024, context_lens=2048,
+    a = dict(out=1 << 20, q=1 << 21, k_cache=1 << 22, v_cache=1 << 23, block_tables=1024, context_lens=2048,
              mods=ctypes.addressof(mods) if mods else None, num_seqs=2, num_heads=8,
              num_kv_heads=2, head_dim=128, block_size=16, max_blocks_per_seq=4, num_blocks=8,
              max_context_len=64, scale=0.1, q_dtype=1, kv_dtype=1, k_scale=1.0, v_scale=1.0,
@@ -164,7 +170,7 @@ def _decode(lib, mods=None, **over):
 
 
 def _prefill(lib, mods=None, **over):
-    a = dict(out=256, q=256, k_cache=512, v_cache=512, block_tables=1024, context_lens=2048,
+    a = dict(out=1 << 20, q=1 << 21, k_cache=1 << 22, v_cache=1 << 23, block_tables=1024, context_lens=2048,
              qsl=4096, mods=ctypes.addressof(mods) if mods else None, num_seqs=2, total_q=6,
              max_q_len=4, num_heads=8, num_kv_heads=2, head_dim=128, block_size=16,
              max_blocks_per_seq=4, num_blocks=8, max_context_len=64, scale=0.1, q_dtype=1,
@@ -182,6 +188,8 @@ def _prefill(lib, mods=None, **over):
     (None, dict(num_heads=6, num_kv_heads=4), -1), (None, dict(num_heads=34), -2),
     (None, dict(q_dtype=2), -2), (None, dict(q_dtype=0), -2), (None, dict(out=None), -1),
     (None, dict(q=264), -1), (None, dict(scale=math.nan), -1),
+    (None, dict(out=1 << 21), -1), (None, dict(out=(1 << 21) + 2048), -1), (None, dict(out=1 << 22), -1),
+    (None, dict(out=(1 << 23) + 4096), -1),
     (None, dict(kv_dtype=2, k_scale=-1.0), -1), (None, dict(num_seqs=0), 0)])
 def test_biased_refusals(lib, call, mods, over, status):
     assert call(lib, _mods(**mods) if mods else None, **over) == status
