@@ -521,15 +521,9 @@ int pkv_paged_attention_decode_biased(void* out, const void* q, const void* k_ca
 /*
  * Chunked-prefill attention under pkv_score_mods; other arguments as for
  * pkv_paged_attention_prefill_chunk.
- * workspace: at least pkv_prefill_biased_workspace_size(...) bytes, 256-byte
- * aligned (NULL when that is 0, as it is for head_dim 128).
- * head_dim 128 runs on the tensor cores, for caches of up to 2^31 rows
- * (num_blocks * num_kv_heads * 16; PKV_ERR_UNSUPPORTED beyond); head_dim 64 on the
- * CUDA cores, a query row at a time.
+ * No workspace.  Caches of up to 2^31 rows (num_blocks * num_kv_heads * 16) and
+ * queries of up to 2^31 heads (total_q * num_heads); PKV_ERR_UNSUPPORTED beyond.
  */
-size_t pkv_prefill_biased_workspace_size(int num_seqs, int total_q, int num_heads,
-                                         int num_kv_heads, int head_dim, int max_context_len,
-                                         pkv_dtype q_dtype, pkv_dtype kv_dtype);
 int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_cache,
                                        const void* v_cache, const int32_t* block_tables,
                                        const int32_t* context_lens,
@@ -539,8 +533,7 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
                                        int head_dim, int block_size, int max_blocks_per_seq,
                                        int num_blocks, int max_context_len, float scale,
                                        pkv_dtype q_dtype, pkv_dtype kv_dtype, float k_scale,
-                                       float v_scale, void* workspace, size_t workspace_bytes,
-                                       uint32_t* device_errors, void* stream);
+                                       float v_scale, uint32_t* device_errors, void* stream);
 
 /*
  * Host block pool with prefix caching.  Sources: "第34讲 … vLLM 生产级系统架构

@@ -32,7 +32,7 @@ __all__ = [
     "copy_blocks", "BlockPool", "Request", "mixed_workspace_size", "paged_attention_mixed",
     "debug_arm_wait_timeout", "debug_prefill_pairs", "build_step_maps", "rotary_frequencies",
     "rotary_and_cache", "decode_biased_workspace_size", "paged_attention_decode_biased",
-    "prefill_biased_workspace_size", "paged_attention_prefill_biased",
+    "paged_attention_prefill_biased",
 ]
 
 F16, BF16, FP8_E4M3 = 0, 1, 2
@@ -132,11 +132,9 @@ def load():
             lib.pkv_paged_attention_decode_biased.restype = _I
             lib.pkv_paged_attention_decode_biased.argtypes = (
                 [_P] * 7 + [_I] * 8 + [_F, _I, _I, _F, _F, _P, _SZ, _P, _P])
-            lib.pkv_prefill_biased_workspace_size.restype = _SZ
-            lib.pkv_prefill_biased_workspace_size.argtypes = [_I] * 8
             lib.pkv_paged_attention_prefill_biased.restype = _I
             lib.pkv_paged_attention_prefill_biased.argtypes = (
-                [_P] * 8 + [_I] * 10 + [_F, _I, _I, _F, _F, _P, _SZ, _P, _P])
+                [_P] * 8 + [_I] * 10 + [_F, _I, _I, _F, _F, _P, _P])
             _I32 = ctypes.c_int32
             lib.pkv_block_pool_create.restype = _I
             lib.pkv_block_pool_create.argtypes = [_I32, _I32, _P]
@@ -654,21 +652,12 @@ def paged_attention_decode_biased(out, q, k_cache, v_cache, block_tables, contex
     return out
 
 
-def prefill_biased_workspace_size(num_seqs: int, total_q: int, num_heads: int, num_kv_heads: int,
-                                  head_dim: int, max_context_len: int, q_dtype: int,
-                                  kv_dtype: int) -> int:
-    return int(load().pkv_prefill_biased_workspace_size(num_seqs, total_q, num_heads, num_kv_heads,
-                                                        head_dim, max_context_len, q_dtype,
-                                                        kv_dtype))
-
-
 def paged_attention_prefill_biased(out, q, k_cache, v_cache, block_tables, context_lens,
                                    query_start_loc, scale: float, softcap: float = 0.0,
                                    alibi_slopes=None, window: int = 0, key_start=None,
                                    prefix_lens=None, max_q_len: int | None = None,
                                    max_context_len: int | None = None, k_scale: float = 1.0,
-                                   v_scale: float = 1.0, workspace=None, device_errors=None,
-                                   stream=None):
+                                   v_scale: float = 1.0, device_errors=None, stream=None):
     """Chunked-prefill attention with capped scores, a distance bias, a sliding
     window, a first key per query row (key_start [total_q] int32: document masks)
     and keys seen in both directions (prefix_lens [S] int32):
@@ -683,16 +672,13 @@ def paged_attention_prefill_biased(out, q, k_cache, v_cache, block_tables, conte
         max_context_len = int(context_lens.max().item()) if S else 0
     if max_q_len is None:
         max_q_len = int((query_start_loc[1:] - query_start_loc[:-1]).max().item()) if S else 0
-    qd, kd = _dtype_code(q), _dtype_code(k_cache)
-    lib = _lib or load()
     with guard:
-        ws, wsb = _scratch_on(stream, lib.pkv_prefill_biased_workspace_size(
-            S, TQ, H, hkv, D, max_context_len, qd, kd), workspace, q.device)
-        rc = lib.pkv_paged_attention_prefill_biased(
+        rc = (_lib or load()).pkv_paged_attention_prefill_biased(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), context_lens.data_ptr(), query_start_loc.data_ptr(),
             ctypes.addressof(mods), S, TQ, max_q_len, H, hkv, D, bs, block_tables.shape[1], nb,
-            max_context_len, scale, qd, kd, k_scale, v_scale, ws, wsb, _ptr(device_errors), raw)
+            max_context_len, scale, _dtype_code(q), _dtype_code(k_cache), k_scale, v_scale,
+            _ptr(device_errors), raw)
     if rc:
         raise PagedKVError("pkv_paged_attention_prefill_biased", rc)
     return out

@@ -622,18 +622,6 @@ int pkv_paged_attention_decode_biased(void* out, const void* q, const void* k_ca
                        workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
-size_t pkv_prefill_biased_workspace_size(int num_seqs, int total_q, int num_heads,
-                                         int num_kv_heads, int head_dim, int max_context_len,
-                                         pkv_dtype q_dtype, pkv_dtype kv_dtype) {
-  if (num_seqs <= 0 || total_q <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
-      max_context_len < 0)
-    return 0;
-  // tensor cores: none; CUDA cores: split-K partials
-  if (head_dim == 128) return 0;
-  return split_workspace((size_t)total_q, num_heads, head_dim,
-                         parts_for(max_context_len, kDefaultPartition));
-}
-
 int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_cache,
                                        const void* v_cache, const int32_t* block_tables,
                                        const int32_t* context_lens,
@@ -643,8 +631,7 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
                                        int head_dim, int block_size, int max_blocks_per_seq,
                                        int num_blocks, int max_context_len, float scale,
                                        pkv_dtype q_dtype, pkv_dtype kv_dtype, float k_scale,
-                                       float v_scale, void* workspace, size_t workspace_bytes,
-                                       uint32_t* device_errors, void* stream) {
+                                       float v_scale, uint32_t* device_errors, void* stream) {
   int rc = check_attention_args(out, q, k_cache, v_cache, block_tables, context_lens, num_seqs,
                                 num_heads, num_kv_heads, head_dim, block_size,
                                 max_blocks_per_seq, num_blocks, max_context_len, scale, q_dtype,
@@ -672,22 +659,14 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
   p.group = num_heads / num_kv_heads;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.num_blocks = num_blocks;
-  p.partition = kDefaultPartition;
-  p.max_parts = parts_for(max_context_len, kDefaultPartition);
-  if (p.max_parts > 16384) return PKV_ERR_UNSUPPORTED;
   p.errors = device_errors;
-  if (head_dim == 128) {
-    if (!pkv::prefill_mods_supported(p, head_dim)) return PKV_ERR_UNSUPPORTED;
-    const bool fp8 = kv_dtype == PKV_FP8_E4M3;
-    p.q_scale = scale * pkv::kLog2e * (fp8 ? k_scale : 1.0f);
-    p.v_scale = fp8 ? v_scale : 1.0f;
-    pkv::take_debug_hook(p);
-    return pkv::launch_prefill_mods(p, q_dtype, kv_dtype, total_q,
-                                    static_cast<cudaStream_t>(stream));
-  }
-  const size_t need = split_workspace((size_t)total_q, num_heads, head_dim, p.max_parts);
-  return run_attention(p, q_dtype, kv_dtype, head_dim, scale, k_scale, v_scale, workspace, need,
-                       workspace_bytes, static_cast<cudaStream_t>(stream));
+  if (!pkv::prefill_mods_supported(p)) return PKV_ERR_UNSUPPORTED;
+  const bool fp8 = kv_dtype == PKV_FP8_E4M3;
+  p.q_scale = scale * pkv::kLog2e * (fp8 ? k_scale : 1.0f);
+  p.v_scale = fp8 ? v_scale : 1.0f;
+  pkv::take_debug_hook(p);
+  return pkv::launch_prefill_mods(p, q_dtype, kv_dtype, head_dim, total_q,
+                                  static_cast<cudaStream_t>(stream));
 }
 
 int pkv_debug_prefill_pairs(int mode) {

@@ -136,9 +136,8 @@ __global__ void __launch_bounds__(kSimtThreads, (SimtGeom<KVT, D, G>::kCtasPerSm
   int keys, kstart = 0, front = 0, pos = 0;  // kstart: key the partitions start from
   if constexpr (kMods) {
     const RowKeys rk = mods_row_keys(p, row, threadIdx.x == 0);
-    if (rk.hi < 0) return;
-    seq = rk.seq;
-    pos = rk.pos;
+    seq = row;
+    pos = rk.hi - 1;
     kstart = first_block_key(rk.lo);
     front = rk.lo - kstart;
     keys = rk.hi > rk.lo ? rk.hi - kstart : 0;

@@ -90,6 +90,38 @@ bool make_map_q3d(CUtensorMap* m, const void* base, uint64_t tokens, uint32_t he
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_rows(CUtensorMap* m, const void* base, uint64_t rows, uint32_t d, int type,
+                   uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const uint32_t elem = type == PKV_FP8_E4M3 ? 1 : 2;
+  cuuint64_t dims[2] = {d, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {d * elem};
+  cuuint32_t box[2] = {d * elem > 128 ? 128 / elem : d, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m,
+            type == PKV_FP8_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+            : type == PKV_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            d * elem < 128 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_map_heads(CUtensorMap* m, const void* base, uint64_t tokens, uint32_t heads, uint32_t d,
+                    bool bf16, uint32_t box_heads, uint32_t box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {d, heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {d * 2, (cuuint64_t)heads * d * 2};
+  cuuint32_t box[3] = {64, box_heads, box_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {
   static int n = 0;
   if (n == 0) {

@@ -152,17 +152,27 @@ size_t prefill_q8_bytes(int total_q, int num_heads);
 int launch_prefill_tc_fp8(const AttnParams& p, int q_dtype, int total_q, void* workspace,
                           size_t workspace_bytes, cudaStream_t stream);
 
-// Chunked prefill under score modifiers (p.mods), head_dim 128, any group size; its
-// kernels with capped scores, a distance bias, or both.
-bool prefill_mods_supported(const AttnParams& p, int head_dim);
-int launch_prefill_mods(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+// Chunked prefill under score modifiers (p.mods), any group size up to 16; its kernels
+// by modifiers and head dimension.
+bool prefill_mods_supported(const AttnParams& p);
+int launch_prefill_mods(const AttnParams& p, int q_dtype, int kv_dtype, int head_dim, int total_q,
                         cudaStream_t stream);
-int launch_prefill_cap(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
-                       cudaStream_t stream);
-int launch_prefill_bias(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
-                        cudaStream_t stream);
-int launch_prefill_cap_bias(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+int launch_prefill_keys_d64(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
                             cudaStream_t stream);
+int launch_prefill_keys_d128(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+                             cudaStream_t stream);
+int launch_prefill_cap_d64(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+                           cudaStream_t stream);
+int launch_prefill_cap_d128(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+                            cudaStream_t stream);
+int launch_prefill_bias_d64(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+                            cudaStream_t stream);
+int launch_prefill_bias_d128(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+                             cudaStream_t stream);
+int launch_prefill_cap_bias_d64(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+                                cudaStream_t stream);
+int launch_prefill_cap_bias_d128(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+                                 cudaStream_t stream);
 
 // One launch for a mixed batch: pd describes the decode rows (as for
 // launch_paged_decode_tc), pp the prefill chunks (as for launch_prefill_tc);
@@ -181,6 +191,13 @@ bool make_map_q3d(CUtensorMap* m, const void* base, uint64_t tokens, uint32_t he
 bool make_map_e4m3(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows);
 bool make_map_q3d_e4m3(CUtensorMap* m, const void* base, uint64_t tokens, uint32_t heads,
                        uint32_t box_heads, uint32_t box_tokens);
+// Cache rows of d (64 or 128) elements of `type` (a pkv_dtype), boxes of box_rows rows of
+// at most 128 bytes with the 128-byte swizzle (rows of 64 bytes: as they are).
+bool make_map_rows(CUtensorMap* m, const void* base, uint64_t rows, uint32_t d, int type,
+                   uint32_t box_rows);
+// A 16-bit query [tokens][heads][d], boxes of 64 columns x box_heads x box_tokens.
+bool make_map_heads(CUtensorMap* m, const void* base, uint64_t tokens, uint32_t heads, uint32_t d,
+                    bool bf16, uint32_t box_heads, uint32_t box_tokens);
 int sm_count();
 
 int launch_lse_merge(const AttnParams& p, int q_dtype, int head_dim, cudaStream_t stream);

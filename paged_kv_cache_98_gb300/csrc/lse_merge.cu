@@ -34,10 +34,10 @@ constexpr int kMergeWarps = 8;
 // Partitions holding this (row, head)'s partials; 0 for an empty context.
 // Returns -1 when the partition was written to out directly (no merge).
 __device__ __forceinline__ int row_parts(const AttnParams& p, int row) {
-  if (p.mods) {  // the partitions of the row's key interval; no sequence's row: leave it
+  if (p.mods) {  // the partitions of the row's key interval
     const RowKeys rk = mods_row_keys(p, row, false);
     const int np = mods_parts(p, rk.lo, rk.hi);
-    return rk.hi < 0 || np == 1 ? -1 : min(np, p.max_parts);
+    return np == 1 ? -1 : min(np, p.max_parts);
   }
   int seq;
   const int keys = row_keys(p, row, &seq);

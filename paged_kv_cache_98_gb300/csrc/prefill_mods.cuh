@@ -1,5 +1,5 @@
-// Biased chunked prefill on the tcgen05 tensor cores (head_dim 128, fp16/bf16 or
-// E4M3 caches, any group size up to 16): capped scores, a distance bias, and an
+// Biased chunked prefill on the tcgen05 tensor cores (head_dim 64 or 128, fp16/bf16
+// or E4M3 caches, any group size up to 16): capped scores, a distance bias, and an
 // interval of visible keys per query row (score_mods.cuh).  The mathematics and
 // the layouts are those of prefill_tc.cuh; what differs:
 //
@@ -329,39 +329,51 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
   return 1.0f;
 }
 
+// Scores: S (128 rows x 128 keys, fp32 in TMEM at d) = Q K^T over D dimensions, 16 a
+// step, within 64-dimension halves of 16 KB.
+template <int D>
+__device__ __forceinline__ void issue_mods_scores(uint32_t d, uint64_t dq, uint64_t dk,
+                                                  uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+    tc::mma_f16(d, dq + off, dk + off, idesc, kk > 0);
+  }
+}
+
 // One row (a query token's head) from its own keys alone, in fp32 (the plain online
-// softmax, exp2f).  Four lanes share the row, 32 dimensions each; gmask is their
+// softmax, exp2f).  Four lanes share the row, D / 4 dimensions each; gmask is their
 // mask.
-template <class QT, bool kFP8>
+template <class QT, bool kFP8, int D>
 __device__ __forceinline__ void exact_row(const AttnParams& p, int seq, int row, int h, int pos,
                                           int lo, int hi, unsigned gmask) {
-  constexpr int kElem = kFP8 ? 1 : 2;
+  constexpr int kElem = kFP8 ? 1 : 2, kDims = D / 4;
   using T = typename QT::T;
   const int quarter = threadIdx.x & 3, kvh = h / p.group;
   const float slope = p.alibi ? __ldg(p.alibi + h) * kLog2e : 0.0f;
-  const size_t at = ((size_t)row * p.num_heads + h) * kD + quarter * 32;
-  float qf[32], acc[32], m = -INFINITY, l = 0.0f;
+  const size_t at = ((size_t)row * p.num_heads + h) * D + quarter * kDims;
+  float qf[kDims], acc[kDims], m = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
+  for (int c = 0; c < kDims / 8; ++c)
     to_float(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + at) + c), qf + 8 * c,
              QT());
 #pragma unroll
-  for (int d = 0; d < 32; ++d) acc[d] = 0.0f;
+  for (int d = 0; d < kDims; ++d) acc[d] = 0.0f;
   for (int j = lo; j < hi; ++j) {
     const int blk = __ldg(p.block_tables + (size_t)seq * p.max_blocks_per_seq + j / kBlockSize);
     const bool bok = blk >= 0 && blk < p.num_blocks;
     const size_t off = ((((size_t)(bok ? blk : 0) * p.num_kv_heads + kvh) * kBlockSize +
-                         j % kBlockSize) * kD + quarter * 32) * kElem;
-    float kv[32], dot = 0.0f;
+                         j % kBlockSize) * D + quarter * kDims) * kElem;
+    float kv[kDims], dot = 0.0f;
     if (bok) {
       const uint4* kp = reinterpret_cast<const uint4*>(p.k_cache + off);
 #pragma unroll
-      for (int c = 0; c < 32 * kElem / 16; ++c) {
+      for (int c = 0; c < kDims * kElem / 16; ++c) {
         if constexpr (kFP8) to_float(__ldg(kp + c), kv + 16 * c, E4M3());
         else to_float(__ldg(kp + c), kv + 8 * c, QT());
       }
 #pragma unroll
-      for (int d = 0; d < 32; ++d) dot = fmaf(qf[d], kv[d], dot);
+      for (int d = 0; d < kDims; ++d) dot = fmaf(qf[d], kv[d], dot);
     }
     dot += __shfl_xor_sync(gmask, dot, 1);
     dot += __shfl_xor_sync(gmask, dot, 2);
@@ -372,7 +384,7 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, int seq, int row,
       const float a = exp2f(m - sc);
       l *= a;
 #pragma unroll
-      for (int d = 0; d < 32; ++d) acc[d] *= a;
+      for (int d = 0; d < kDims; ++d) acc[d] *= a;
       m = sc;
     }
     const float w = exp2f(sc - m);
@@ -380,23 +392,23 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, int seq, int row,
     if (bok) {
       const uint4* vp = reinterpret_cast<const uint4*>(p.v_cache + off);
 #pragma unroll
-      for (int c = 0; c < 32 * kElem / 16; ++c) {
+      for (int c = 0; c < kDims * kElem / 16; ++c) {
         if constexpr (kFP8) to_float(__ldg(vp + c), kv + 16 * c, E4M3());
         else to_float(__ldg(vp + c), kv + 8 * c, QT());
       }
 #pragma unroll
-      for (int d = 0; d < 32; ++d) acc[d] = fmaf(w, kv[d], acc[d]);
+      for (int d = 0; d < kDims; ++d) acc[d] = fmaf(w, kv[d], acc[d]);
     }
   }
   const float inv = p.v_scale / l;
   T* op = static_cast<T*>(p.out) + at;
 #pragma unroll
-  for (int d = 0; d < 32; ++d) store_out(op + d, acc[d] * inv);
+  for (int d = 0; d < kDims; ++d) store_out(op + d, acc[d] * inv);
 }
 
 // The rows of query tile qt, in the items listed, whose output is not finite, again
 // by exact_row: eight rows at a time per warp, `w` of the tile's.
-template <class QT, bool kFP8, int kMods>
+template <class QT, bool kFP8, int kMods, int D>
 __device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem<kFP8>& sm, int total, int qt,
                                        int w) {
   using T = typename QT::T;
@@ -415,16 +427,16 @@ __device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem<kFP8>&
       key_interval(p, row, pos0 + tok, x.ctx, x.bidir, &lo, &hi);
       if (lo >= hi) continue;
       const uint4* o = reinterpret_cast<const uint4*>(
-          static_cast<const T*>(p.out) + ((size_t)row * p.num_heads + h) * kD + (lane & 3) * 32);
+          static_cast<const T*>(p.out) + ((size_t)row * p.num_heads + h) * D + (lane & 3) * (D / 4));
       bool odd = false;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         float f[8];
         to_float(o[c], f, QT());
 #pragma unroll
         for (int e = 0; e < 8; ++e) odd |= !(fabsf(f[e]) < INFINITY);
       }
-      if (__any_sync(gmask, odd)) exact_row<QT, kFP8>(p, x.seq, row, h, pos0 + tok, lo, hi, gmask);
+      if (__any_sync(gmask, odd)) exact_row<QT, kFP8, D>(p, x.seq, row, h, pos0 + tok, lo, hi, gmask);
     }
   }
 }
@@ -520,13 +532,15 @@ __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem<kFP8>& s
 // tail rows of V where the tile holds the context's partial last block, and its V
 // boxes, into the ring.  The boxes are dealt out to the producers block by block; an
 // E4M3 tile, half as large, lands in the second half of its stage.
-template <bool kFP8, int kMods>
+template <bool kFP8, int kMods, int D>
 __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>& sm,
                                               const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                               const CUtensorMap& tm_q, int kv_rows, int total,
                                               int pw) {
   constexpr int nst = kStages, kModProd = mod_producers(kFP8);
-  constexpr int kLoadBytes = kFP8 ? kTileBytes / 2 : kTileBytes;
+  constexpr int kRow = D * (kFP8 ? 1 : 2);       // bytes of a cache row
+  constexpr int kLoadBytes = kTileKeys * kRow;
+  constexpr int kBoxRow = kRow < 128 ? kRow : 128;  // bytes of a row in a box
   uint64_t* const landed = kFP8 ? sm.staged : sm.full;
   volatile int* abort = &sm.abort;
   const unsigned long long lim = wait_limit(p);
@@ -563,10 +577,11 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
     }
     if (!__shfl_sync(kFull, (int)good, 0)) return false;
     if (!skip && (lane >> 3) == (t & 3) && my_lane) {
-      uint8_t* dst = ring + (size_t)st * kTileBytes + (kFP8 ? kHalf : 0) + (lane & 7) * (kBlockSize * 128);
+      uint8_t* dst = ring + (size_t)st * kTileBytes + (kFP8 ? kHalf : 0) +
+                     (lane & 7) * (kBlockSize * kBoxRow);
       const CUtensorMap* map = is_v ? &tm_v : &tm_k;
       tc::tma_load_2d(dst, map, 0, row, &landed[st]);
-      if (!kFP8) tc::tma_load_2d(dst + kHalf, map, 64, row, &landed[st]);
+      if (kRow > 128) tc::tma_load_2d(dst + kHalf, map, 64, row, &landed[st]);
     }
     __syncwarp();
     ++pos;
@@ -578,10 +593,10 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
     bool good = true;
     if (lane == 0 && ntail >= 1) good = wait_bar(&sm.tail_free, (ntail - 1) & 1, abort, lim);
     if (!__shfl_sync(kFull, (int)good, 0)) return false;
-    constexpr int kRowChunks = 16;  // 16-byte chunks per row
+    constexpr int kRowChunks = D / 8;  // 16-byte chunks per row
     const int key0 = (x.nk - 1) * kTileKeys + x.tail_step * kBlockSize;
 #pragma unroll
-    for (int i = 0; i < kTailBytes / 16 / 32; ++i) {
+    for (int i = 0; i < kBlockSize * kRowChunks / 32; ++i) {
       const int c = lane + 32 * i;
       const int r = c / kRowChunks, ch = c % kRowChunks;
       const int key = key0 + r;
@@ -624,12 +639,12 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
       if (nitem >= 1) good = wait_bar(&sm.q_empty, (nitem - 1) & 1, abort, lim);
       if (good) {
         const int nq = x.nt[1] > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(&sm.q_full, nq * (kRowsM / g * g * kD * 2));
+        mbar_arrive_expect_tx(&sm.q_full, nq * (kRowsM / g * g * D * 2));
         for (int qt = 0; qt < nq; ++qt) {
           uint8_t* dq = &sm.q[qt][0];
           const int tok = x.q0 + x.t0[qt];
           tc::tma_load_3d(dq, &tm_q, 0, x.kvh * g, tok, &sm.q_full);
-          tc::tma_load_3d(dq + kHalf, &tm_q, 64, x.kvh * g, tok, &sm.q_full);
+          if (D > 64) tc::tma_load_3d(dq + kHalf, &tm_q, 64, x.kvh * g, tok, &sm.q_full);
         }
       }
     }
@@ -683,16 +698,19 @@ __device__ __forceinline__ void widen16(const uint32_t* u, uint4* a, uint4* b) {
 }
 
 // Converter cw of six on an E4M3 cache: each tile that has landed, in ring order, from
-// [128 rows][128 B] in the second half of its stage to [2 halves][128 rows][128 B], all
-// with the 128-byte swizzle, the V rows past the context as zeros.  Row r of the codes
-// lies where row r of the second half of the elements will, so a warp that reads
-// whole rows before it writes them needs no order with the others.
-template <class QT, int kMods>
+// [128 rows][D B] in the second half of its stage to [D / 64 halves][128 rows][128 B], the
+// V rows past the context as zeros; all with the 128-byte swizzle, but for the 64-byte
+// rows of D = 64, which land as they are.  Row r of the codes lies where row r of the
+// second half of the elements will (or beside all of them), so a warp that reads whole
+// rows before it writes them needs no order with the others.
+template <class QT, int kMods, int D>
 __device__ __forceinline__ void mods_converter(const AttnParams& p, ModSmem<true>& sm, int total,
                                                int cw) {
   volatile int* abort = &sm.abort;
   const unsigned long long lim = wait_limit(p);
-  const int lane = threadIdx.x & 31, c = lane & 7;
+  constexpr int kLanes = D / 16;         // 16-code chunks, and lanes, per row
+  constexpr int kRows = 32 / kLanes;     // rows a turn
+  const int lane = threadIdx.x & 31, c = lane % kLanes;
   uint32_t pos = 0;
   bool ok = true;
   ModItem x;
@@ -703,28 +721,30 @@ __device__ __forceinline__ void mods_converter(const AttnParams& p, ModSmem<true
     if (!__shfl_sync(kFull, (int)good, 0)) return false;
     ++pos;
     uint8_t* tile = &sm.ring[st][0];
-    // four rows a turn, the next turn's codes read ahead (rolled: beside the softmax's
-    // code the instruction cache has little room, see above)
+    // the next turn's codes are read ahead (rolled: beside the softmax's code the
+    // instruction cache has little room, see above)
     auto codes = [&](int u) {
-      const int r = 4 * u + (lane >> 3);
-      return *reinterpret_cast<const uint4*>(tile + kHalf + r * 128 + ((c ^ (r & 7)) << 4));
+      const int r = kRows * u + lane / kLanes;
+      return *reinterpret_cast<const uint4*>(tile + kHalf + r * D +
+                                             ((D == 128 ? c ^ (r & 7) : c) << 4));
     };
     uint4 w = codes(cw);
 #pragma unroll 1
-    for (int u = cw; u < kTileKeys / 4; u += kConverters) {
-      const int r = 4 * u + (lane >> 3);
+    for (int u = cw; u < kTileKeys / kRows; u += kConverters) {
+      const int r = kRows * u + lane / kLanes;
       uint4 nw = w;
-      if (u + kConverters < kTileKeys / 4) nw = codes(u + kConverters);
+      if (u + kConverters < kTileKeys / kRows) nw = codes(u + kConverters);
       if (rows < kTileKeys && r >= rows) w = make_uint4(0, 0, 0, 0);
       // chunks 2 (c % 4) and 2 (c % 4) + 1 of half c / 4; the halves' lanes store them
-      // in opposite order, so that eight lanes hit eight different bank groups
+      // in opposite order, so that eight lanes hit eight different bank groups (D = 64:
+      // the swizzle of two rows does that)
       const bool up = c >> 2;
       const uint32_t v[4] = {up ? w.z : w.x, up ? w.w : w.y, up ? w.x : w.z, up ? w.y : w.w};
       uint4 a, b;
       widen16<QT>(v, &a, &b);
-      __syncwarp();  // the four rows have been read
+      __syncwarp();  // the rows have been read
       uint8_t* d = tile + (c >> 2) * kHalf + r * 128;
-      const int k0 = (2 * (c & 3) + (c >> 2)) ^ (r & 7);
+      const int k0 = (2 * (c & 3) + (up ? 1 : 0)) ^ (r & 7);
       *reinterpret_cast<uint4*>(d + (k0 << 4)) = a;
       *reinterpret_cast<uint4*>(d + ((k0 ^ 1) << 4)) = b;
       w = nw;
@@ -751,13 +771,13 @@ __device__ __forceinline__ void mods_converter(const AttnParams& p, ModSmem<true
 // MMA issuer.  Order per item: S_a, S_b of the first step, then for each step i
 //   P_a(i) V, S_a(i + 1), P_b(i) V, S_b(i + 1)
 // so that one query tile's softmax works while the tensor pipe serves the other.
-template <class QT, bool kFP8, int kMods>
+template <class QT, bool kFP8, int kMods, int D>
 __device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem<kFP8>& sm, uint32_t tmem, int total) {
   constexpr int kStageBytes = kTileBytes;
   constexpr int nst = kStages;
   constexpr uint32_t kAB = std::is_same<QT, BF16>::value ? 1u : 0u;
   constexpr uint32_t kIdescS = tc::idesc_f16(kAB, 0, 0, 128, 128);
-  constexpr uint32_t kIdescO = tc::idesc_f16(kAB, 0, 1, 128, 128);
+  constexpr uint32_t kIdescO = tc::idesc_f16(kAB, 0, 1, 128, D);
   volatile int* abort = &sm.abort;
   const unsigned long long lim = wait_limit(p);
   const bool leader = tc::elect_one();
@@ -788,7 +808,7 @@ __device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem<kFP8>& 
   auto mma_s = [&](int qt, int st) {
     if (leader) {
       const uint64_t dk = dk0 + (uint64_t)(st * (kStageBytes >> 4));
-      issue_scores(tmem + qt * 128, qt ? dq[1] : dq[0], dk, kIdescS);
+      issue_mods_scores<D>(tmem + qt * 128, qt ? dq[1] : dq[0], dk, kIdescS);
     }
     commit(&sm.s_ready[qt]);
   };
@@ -864,7 +884,7 @@ __device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem<kFP8>& 
 }
 
 // Softmax and epilogue: thread = row of query tile qt.
-template <class QT, bool kFP8, int kMods>
+template <class QT, bool kFP8, int kMods, int D>
 __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>& sm, uint32_t tmem, int total) {
   using OutT = typename QT::T;
   volatile int* abort = &sm.abort;
@@ -901,7 +921,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
     const bool valid = r < nt * g;
     const int row = x.q0 + t0 + tok, h = x.kvh * g + head_in;
     const size_t head = (size_t)row * p.num_heads + h;
-    OutT* orow = static_cast<OutT*>(p.out) + head * kD;
+    OutT* orow = static_cast<OutT*>(p.out) + head * D;
     int lo = 0, hi = INT_MAX;
     if (valid) {
       key_interval(p, row, pos, x.ctx, x.bidir, &lo, &hi);
@@ -913,7 +933,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
     if (last < 0) {               // no row of the tile sees a key
       if (valid) {
 #pragma unroll
-        for (int i = 0; i < kD / 8; ++i) reinterpret_cast<uint4*>(orow)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(orow)[i] = make_uint4(0, 0, 0, 0);
       }
       continue;
     }
@@ -991,7 +1011,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
       // the product of this step adds onto O: rescale it first
       if (i > x.kt0 && __any_sync(kFull, need)) {
 #pragma unroll 1
-        for (int c = 0; c < kD; c += 32) {
+        for (int c = 0; c < D; c += 32) {
           float ov[32];
           tc::tmem_ld32(o_col + c, ov);
           tc::tmem_wait_ld();
@@ -1016,7 +1036,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
     const float inv = valid && !empty ? p.v_scale / l : 0.0f;
     bool odd = false;  // an output that is not finite
 #pragma unroll 1
-    for (int c = 0; c < kD; c += 32) {
+    for (int c = 0; c < D; c += 32) {
       float ov[32];
       tc::tmem_ld32(o_col + c, ov);
       tc::tmem_wait_ld();
@@ -1050,10 +1070,10 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
   // every warp of the tile leaves the loop here, whatever it met, and sees the others'
   // stores and flag behind this barrier
   ok = all_of_tile(ok, qt);
-  if (ok && sm.redo_n[qt] > 0) redo_rows<QT, kFP8, kMods>(p, sm, total, qt, warp % kTileWarps);
+  if (ok && sm.redo_n[qt] > 0) redo_rows<QT, kFP8, kMods, D>(p, sm, total, qt, warp % kTileWarps);
 }
 
-template <class QT, bool kFP8, int kMods>
+template <class QT, bool kFP8, int kMods, int D>
 __global__ void __launch_bounds__(mod_threads(kFP8), 1)
     prefill_mods_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
@@ -1068,14 +1088,14 @@ __global__ void __launch_bounds__(mod_threads(kFP8), 1)
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(kFP8)));
     if (warp == kWarpMma)
-      mods_issuer<QT, kFP8, kMods>(p, sm, tmem, total);
+      mods_issuer<QT, kFP8, kMods, D>(p, sm, tmem, total);
     else if (warp < kWarpTma + mod_producers(kFP8))
-      mods_producer<kFP8, kMods>(p, sm, tm_k, tm_v, tm_q, kv_rows, total, warp - kWarpTma);
+      mods_producer<kFP8, kMods, D>(p, sm, tm_k, tm_v, tm_q, kv_rows, total, warp - kWarpTma);
     else if constexpr (kFP8)
-      mods_converter<QT, kMods>(p, sm, total, warp - kWarpTma - mod_producers(true));
+      mods_converter<QT, kMods, D>(p, sm, total, warp - kWarpTma - mod_producers(true));
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(soft_regs(kFP8)));
-    mods_softmax<QT, kFP8, kMods>(p, sm, tmem, total);
+    mods_softmax<QT, kFP8, kMods, D>(p, sm, tmem, total);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -1085,25 +1105,24 @@ __global__ void __launch_bounds__(mod_threads(kFP8), 1)
   }
 }
 
-template <class QT, bool kFP8, int kMods>
+template <class QT, bool kFP8, int kMods, int D>
 int launch_mods(const AttnParams& p, int total_q, cudaStream_t stream) {
   const bool bf16 = std::is_same<QT, BF16>::value;
   const uint64_t kv_rows = (uint64_t)p.num_blocks * p.num_kv_heads * kBlockSize;
   const uint32_t g = (uint32_t)p.group, tokens = kRowsM / g, heads = (uint32_t)p.num_heads;
   CUtensorMap tk, tv, tq;
-  const bool maps =
-      (kFP8 ? make_map_e4m3(&tk, p.k_cache, kv_rows, 16) && make_map_e4m3(&tv, p.v_cache, kv_rows, 16)
-            : make_map_2d(&tk, p.k_cache, kv_rows, bf16, 16) &&
-                  make_map_2d(&tv, p.v_cache, kv_rows, bf16, 16)) &&
-      make_map_q3d(&tq, p.q, (uint64_t)total_q, heads, bf16, g, tokens);
-  if (!maps) return PKV_ERR_CUDA;
+  const int type = kFP8 ? PKV_FP8_E4M3 : (bf16 ? PKV_BF16 : PKV_F16);
+  if (!make_map_rows(&tk, p.k_cache, kv_rows, D, type, kBlockSize) ||
+      !make_map_rows(&tv, p.v_cache, kv_rows, D, type, kBlockSize) ||
+      !make_map_heads(&tq, p.q, (uint64_t)total_q, heads, D, bf16, g, tokens))
+    return PKV_ERR_CUDA;
   using SM = ModSmem<kFP8>;
   const size_t smem = sizeof(SM) + 1024;
   static_assert(sizeof(SM) + 1024 <= 232448, "shared memory budget of one CTA");
   static_assert(offsetof(SM, ring) % 1024 == 0 && offsetof(SM, q) % 1024 == 0 &&
                     offsetof(SM, tail) % 1024 == 0,
                 "swizzled buffers must start on 1024-byte boundaries");
-  auto kern = prefill_mods_kernel<QT, kFP8, kMods>;
+  auto kern = prefill_mods_kernel<QT, kFP8, kMods, D>;
   // the kernel's register shares add up to what its launch holds; with fewer its
   // warpgroups would wait for registers without end
   cudaFuncAttributes fa;
@@ -1131,15 +1150,15 @@ int launch_mods(const AttnParams& p, int total_q, cudaStream_t stream) {
   return PKV_OK;
 }
 
-template <int kMods>
-int launch_mods_typed(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
-                      cudaStream_t stream) {
+template <int kMods, int D>
+int launch_mods_dim(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
+                    cudaStream_t stream) {
   const bool fp8 = kv_dtype == PKV_FP8_E4M3;
   if (q_dtype == PKV_BF16)
-    return fp8 ? launch_mods<BF16, true, kMods>(p, total_q, stream)
-               : launch_mods<BF16, false, kMods>(p, total_q, stream);
-  return fp8 ? launch_mods<F16, true, kMods>(p, total_q, stream)
-             : launch_mods<F16, false, kMods>(p, total_q, stream);
+    return fp8 ? launch_mods<BF16, true, kMods, D>(p, total_q, stream)
+               : launch_mods<BF16, false, kMods, D>(p, total_q, stream);
+  return fp8 ? launch_mods<F16, true, kMods, D>(p, total_q, stream)
+             : launch_mods<F16, false, kMods, D>(p, total_q, stream);
 }
 
 }  // namespace

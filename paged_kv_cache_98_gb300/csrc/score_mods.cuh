@@ -11,13 +11,8 @@
 
 namespace pkv {
 
-// Keys of one query row.  hi < 0: the row belongs to no sequence and is left
-// as it is; lo == hi: it sees nothing and its output is zero.
-struct RowKeys {
-  int seq, pos, lo, hi;
-};
-
-// Interval of a query at position pos of a sequence of ctx tokens.
+// Interval of a query at position pos of a sequence of ctx tokens; lo == hi: it sees
+// nothing and its output is zero.
 __device__ __forceinline__ void key_interval(const AttnParams& p, int row, int pos, int ctx,
                                              int bidir, int* lo, int* hi) {
   int h = max(pos + 1, min(bidir, ctx));
@@ -28,44 +23,20 @@ __device__ __forceinline__ void key_interval(const AttnParams& p, int row, int p
   *lo = min(l, h);
 }
 
-// Context of sequence s, clamped to the block table and the caller's bound.
-__device__ __forceinline__ int mods_context(const AttnParams& p, int s, bool report) {
-  const int cap = min(p.max_blocks_per_seq * kBlockSize, p.max_context);
-  const int ctx = __ldg(p.context_lens + s);
-  if (ctx >= 0 && ctx <= cap) return ctx;
-  if (report) flag_error(p.errors, PKV_DEVERR_CONTEXT);
-  return ctx < 0 ? 0 : cap;
-}
-
-// A decode row is its sequence's last token; a prefill row is query i of the
-// sequence whose query_start_loc range holds it.
+// Keys of a decode row, its sequence's last token: the query's position is hi - 1.  A
+// context beyond the block table or the caller's bound is clamped and flagged.
+struct RowKeys {
+  int lo, hi;
+};
 __device__ __forceinline__ RowKeys mods_row_keys(const AttnParams& p, int row, bool report) {
-  RowKeys r;
-  r.seq = row;
-  if (p.query_start_loc == nullptr) {
-    const int ctx = mods_context(p, row, report);
-    r.pos = ctx - 1;
-    key_interval(p, row, r.pos, ctx, 0, &r.lo, &r.hi);
-    return r;
-  }
-  int lo = 0, hi = p.num_seqs - 1;  // largest s with query_start_loc[s] <= row
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.query_start_loc + mid) <= row) lo = mid; else hi = mid - 1;
-  }
-  r.seq = lo;
-  const int q0 = __ldg(p.query_start_loc + lo), q1 = __ldg(p.query_start_loc + lo + 1);
-  r.pos = r.lo = 0;
-  r.hi = -1;
-  if (row < q0 || row >= q1) return r;
-  const int ctx = mods_context(p, lo, report);
-  r.pos = ctx - (q1 - q0) + (row - q0);
-  if (r.pos < 0) {  // more queries than context
+  const int cap = min(p.max_blocks_per_seq * kBlockSize, p.max_context);
+  int ctx = __ldg(p.context_lens + row);
+  if (ctx < 0 || ctx > cap) {
     if (report) flag_error(p.errors, PKV_DEVERR_CONTEXT);
-    r.hi = 0;
-    return r;
+    ctx = ctx < 0 ? 0 : cap;
   }
-  key_interval(p, row, r.pos, ctx, p.bidir_lens ? __ldg(p.bidir_lens + lo) : 0, &r.lo, &r.hi);
+  RowKeys r;
+  key_interval(p, row, ctx - 1, ctx, 0, &r.lo, &r.hi);
   return r;
 }
 

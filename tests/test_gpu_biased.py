@@ -115,10 +115,11 @@ class Batch:
         out = torch.full_like(q, 5.0) if out is None else out
         kw = dict(softcap=self.softcap, alibi_slopes=slopes, window=self.window, key_start=start,
                   max_context_len=int(self.ctx.max()) if len(self.ctx) else 0, k_scale=self.ks, v_scale=self.vs,
-                  workspace=workspace, device_errors=errors, stream=stream)
+                  device_errors=errors, stream=stream)
         torch.cuda.synchronize()
         if self.is_decode:
-            return pkv.paged_attention_decode_biased(out, q, self.kc, self.vc, bt, cl, self.scale, **kw)
+            return pkv.paged_attention_decode_biased(out, q, self.kc, self.vc, bt, cl, self.scale,
+                                                     workspace=workspace, **kw)
         return pkv.paged_attention_prefill_biased(out, q, self.kc, self.vc, bt, cl, qsl, self.scale,
                                                   prefix_lens=prefix, max_q_len=int(self.q_len.max()), **kw)
 
@@ -343,6 +344,9 @@ PREFILL = [
     dict(H=8, hkv=2, prefix=[0, 9, 30, 40, 0, 100, 100, 512], softcap=12.0, alibi=True),
     dict(H=8, hkv=2, prefix=[1, 2, 40, 35, 9, 64, 290, 600], window=60, dtype="fp16"),
     dict(H=4, hkv=4, D=64, softcap=30.0, window=90), dict(H=5, hkv=1, D=64, alibi=True),
+    dict(H=8, hkv=2, D=64, dtype="fp16"), dict(H=16, hkv=1, D=64, alibi=True, softcap=6.0),
+    dict(H=8, hkv=2, D=64, kv="e4m3", prefix=[1, 2, 40, 35, 9, 64, 290, 600]),
+    dict(H=7, hkv=1, D=64, kv="e4m3", dtype="fp16", alibi=True, starts=docs([2, 50, 51, 130, 200, 290])),
     dict(H=8, hkv=2, kv="e4m3", softcap=30.0), dict(H=8, hkv=2, kv="e4m3", alibi=True, dtype="fp16"),
     dict(H=16, hkv=2, kv="e4m3", prefix=[1, 2, 40, 35, 9, 64, 290, 600]),
     dict(H=14, hkv=2, kv="e4m3", window=70, dtype="fp16"),
@@ -359,7 +363,8 @@ def test_prefill(kw):
 @pytest.mark.parametrize("kw", [
     dict(H=8, hkv=2, window=200, softcap=40.0), dict(H=8, hkv=1, starts=docs([100, 131, 300, 301, 555])),
     dict(H=4, hkv=1, prefix=[400], dtype="fp16"), dict(H=4, hkv=1, kv="e4m3", window=300),
-    dict(H=3, hkv=1, alibi=True)])
+    dict(H=3, hkv=1, alibi=True), dict(H=4, hkv=1, D=64, softcap=40.0),
+    dict(H=4, hkv=1, D=64, kv="e4m3", window=300, alibi=True)])
 def test_prefill_long_chunk(kw):
     run(Batch(23, [(650, 650)], **kw))
     if "prefix" not in kw:
@@ -548,23 +553,24 @@ def test_steps_of_a_small_server(kv):
         assert far < (2.0 ** -6 if kv == "same" else 2.0 ** -3)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-def test_prefill_every_e4m3_code(dtype):
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 128), ("bf16", 64), ("fp16", 64)])
+def test_prefill_every_e4m3_code(dtype, D):
     """A window of one key returns that key's V: every code of an E4M3 cache, subnormal and
     NaN ones among them, in every position of a tile."""
-    b = Batch(61, [(200, 200)], H=4, hkv=1, dtype=dtype, kv="e4m3", window=1)
-    codes = torch.arange(200 * 128, dtype=torch.int64).view(200, 128)
+    b = Batch(61, [(200, 200)], H=4, hkv=1, D=D, dtype=dtype, kv="e4m3", window=1)
+    codes = torch.arange(200 * D, dtype=torch.int64).view(200, D)
     codes = ((codes * 37 + codes // 256) % 256).to(torch.uint8)
     for s in range(200):
         b.vc.view(torch.uint8)[int(b.tables[0, s // 16]), 0, s % 16] = codes[s].to(DEV)
     b.vs = 0.5
     got = b.call().double().cpu()
-    want = codes.view(torch.float8_e4m3fn).double().mul(0.5)[:, None].expand(200, 4, 128)
+    want = codes.view(torch.float8_e4m3fn).double().mul(0.5)[:, None].expand(200, 4, D)
     assert torch.equal(torch.isnan(got), torch.isnan(want))
     assert torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0))
 
 
-@pytest.mark.parametrize("kw", [dict(), dict(kv="e4m3"), dict(alibi=True), dict(kv="e4m3", alibi=True, softcap=9.0)])
+@pytest.mark.parametrize("kw", [dict(), dict(kv="e4m3"), dict(alibi=True), dict(kv="e4m3", alibi=True, softcap=9.0),
+                                dict(D=64), dict(D=64, kv="e4m3")])
 @pytest.mark.parametrize("skip", [1, 2, 5])
 def test_prefill_wait_runs_out(kw, skip):
     """A tile copy that never comes: the call reports it, and the next one is whole."""

@@ -174,7 +174,7 @@ def _prefill(lib, mods=None, **over):
              qsl=4096, mods=ctypes.addressof(mods) if mods else None, num_seqs=2, total_q=6,
              max_q_len=4, num_heads=8, num_kv_heads=2, head_dim=128, block_size=16,
              max_blocks_per_seq=4, num_blocks=8, max_context_len=64, scale=0.1, q_dtype=1,
-             kv_dtype=1, k_scale=1.0, v_scale=1.0, workspace=None, workspace_bytes=0, errors=None,
+             kv_dtype=1, k_scale=1.0, v_scale=1.0, errors=None,
              stream=None)
     a.update(over)
     return lib.pkv_paged_attention_prefill_biased(*a.values())
