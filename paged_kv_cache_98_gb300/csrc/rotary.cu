@@ -32,7 +32,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = 64;  // head_dim 128
 constexpr int kDeep = 4;       // row groups loaded ahead

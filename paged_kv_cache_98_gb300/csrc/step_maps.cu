@@ -145,10 +145,9 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapParams p) 
     for (int s = tid; s <= S; s += kThreads) p.query_start_loc[s] = qsl[s];
 
   // ---- table rows: kChunk entries of a sequence's row per warp -------------------------------
-  const long long items = (long long)S * p.chunks;
-  for (long long it = (long long)blockIdx.x * kWarps + warp; it < items;
-       it += (long long)gridDim.x * kWarps) {
-    const int s = (int)(it / p.chunks), c = (int)(it % p.chunks);
+  const uint32_t items = (uint32_t)S * (uint32_t)p.chunks;  // (below 2^31, checked on the host)
+  for (uint32_t it = blockIdx.x * kWarps + warp; it < items; it += gridDim.x * kWarps) {
+    const int s = (int)(it / (uint32_t)p.chunks), c = (int)(it - (uint32_t)s * p.chunks);
     const Seq x = load_seq(p, s, false);
     const int have = blocks_of(x.cached), need = blocks_of(x.cached + x.q);
     const int b1 = min(need, (c + 1) * kChunk);
@@ -220,6 +219,7 @@ int launch_step_maps(int32_t* block_tables, int32_t* context_lens, int32_t* quer
                            2 * (kMaxSeqs + 1) * (int)sizeof(int)) != cudaSuccess)
     return PKV_ERR_CUDA;
   const long long warps = (long long)num_seqs * p.chunks;
+  if (warps >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
   long long ctas = (warps + kWarps - 1) / kWarps;
   const long long for_tokens = ((long long)num_tokens + kThreads - 1) / kThreads;
   if (for_tokens > ctas) ctas = for_tokens;
