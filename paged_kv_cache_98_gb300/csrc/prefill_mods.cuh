@@ -268,13 +268,13 @@ __device__ __forceinline__ float absmax3(float a, float b, float c) {
 // still to be applied, which the exponential's own multiply-add carries: a where the
 // score is only masked, 1 after a cap or a bias.
 //
-// The cap is C tanh(a s / C).  Where every score of the warp stays below 3/4 of
+// The cap is C tanh(a s / C).  Where every score of the warp stays below half
 // the cap, the usual case, it is s T(s^2), T(u) = a (1 + k3 c^2 u + k5 c^4 u^2 + ...),
-// c = a / C: the polynomial of tanh with the scales folded into its coefficients, six
+// c = a / C: the polynomial of tanh with the scales folded into its coefficients, five
 // operations on packed pairs and no exponential beside the softmax's own.  Otherwise
 // C - 2 C / (2^(2 c log2(e) s) + 1): two more MUFU results per score, off by at most
 // 2^-22 C.  (Folding either into the exponential's argument saves operations, but
-// has the code of the exponentials twice: 145 us against 130 for the mixed batch's
+// has the code of the exponentials twice: 145 us against 130, with a longer polynomial, for the mixed batch's
 // chunks, the difference waiting for instructions.)
 template <int kMods>
 __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, float a, float slope,
@@ -289,16 +289,14 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
     const float most = absmax3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
     if (__all_sync(kFull, most <= kTanhPoly && c <= 16.0f)) {
       const float c2 = c * c;
-      const float t1 = a * c2, t2 = t1 * c2, t3 = t2 * c2, t4 = t3 * c2;
+      const float t1 = a * c2, t2 = t1 * c2, t3 = t2 * c2;
       const float2 q0 = make_float2(a, a), q1 = make_float2(t1 * kTanh3, t1 * kTanh3),
                    q2 = make_float2(t2 * kTanh5, t2 * kTanh5),
-                   q3 = make_float2(t3 * kTanh7, t3 * kTanh7),
-                   q4 = make_float2(t4 * kTanh9, t4 * kTanh9);
+                   q3 = make_float2(t3 * kTanh7, t3 * kTanh7);
 #pragma unroll
       for (int i = 0; i < kTileKeys; i += 2) {
         const float2 x = make_float2(sv[i], sv[i + 1]), u = __fmul2_rn(x, x);
-        const float2 t =
-            __ffma2_rn(u, __ffma2_rn(u, __ffma2_rn(u, __ffma2_rn(u, q4, q3), q2), q1), q0);
+        const float2 t = __ffma2_rn(u, __ffma2_rn(u, __ffma2_rn(u, q3, q2), q1), q0);
         const float2 y = __fmul2_rn(x, t);
         sv[i] = y.x;
         sv[i + 1] = y.y;

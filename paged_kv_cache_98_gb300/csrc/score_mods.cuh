@@ -48,15 +48,14 @@ __device__ __forceinline__ int mods_parts(const AttnParams& p, int lo, int hi) {
   return hi > lo ? (hi - first_block_key(lo) + p.partition - 1) / p.partition : 0;
 }
 
-// tanh(x) for |x| <= kTanhPoly as x + x^3 q(x^2), q of degree 3: its coefficients
+// tanh(x) for |x| <= kTanhPoly as x + x^3 q(x^2), q of degree 2: its coefficients
 // minimise the largest relative error there (iteratively reweighted least
-// squares on Chebyshev points); with fp32 rounding 8e-7 relative.
-constexpr float kTanhPoly = 0.75f;
-constexpr float kTanh3 = -0.333296686f, kTanh5 = 0.132682368f, kTanh7 = -0.0502779521f,
-                kTanh9 = 0.0131058358f;
+// squares on Chebyshev points); with fp32 rounding 7e-7 relative.
+constexpr float kTanhPoly = 0.5f;
+constexpr float kTanh3 = -0.333281606f, kTanh5 = 0.132053599f, kTanh7 = -0.044750642f;
 __device__ __forceinline__ float tanh_poly(float x) {
   const float x2 = x * x;
-  const float q = fmaf(x2, fmaf(x2, fmaf(x2, kTanh9, kTanh7), kTanh5), kTanh3);
+  const float q = fmaf(x2, fmaf(x2, kTanh7, kTanh5), kTanh3);
   return fmaf(x2 * x, q, x);
 }
 
