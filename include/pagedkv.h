@@ -446,7 +446,8 @@ int pkv_rotary_frequencies(double* inv_freq, int rotary_dim, double base,
  *   positions [num_tokens] int32.  A negative position is a padding token:
  *             nothing is written for it.
  *   slot_mapping [num_tokens] int64, as for pkv_reshape_and_cache (a negative
- *             slot: K and V are not written, q is rotated all the same).
+ *             slot: K and V are not written, q is rotated all the same).  Two
+ *             tokens of one slot are a caller's error (its rows are unspecified).
  *   inv_freq  HOST array of rotary_dim / 2 doubles, read during the call.
  *             Pair i of a token at position t turns by t * inv_freq[i]; the
  *             angle is reduced exactly, for positions up to 2^30.

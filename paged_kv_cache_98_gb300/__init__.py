@@ -450,7 +450,11 @@ def _on_device(device, stream, specs):
 
 def _word(t):
     """The device error word's spec: any tensor on the device, its first four bytes."""
-    return ("device_errors", t, None, None) if t is None else ("device_errors", t, t.dtype, t.shape)
+    if t is None:
+        return "device_errors", None, None, None
+    if t.numel() * t.element_size() < 4:
+        raise ValueError("device_errors must hold at least four bytes")
+    return "device_errors", t, t.dtype, t.shape
 
 
 def _stream_on(device, stream, tensors):

@@ -385,13 +385,8 @@ template <class QT, class KVT, int D, int G, bool kMods>
 int launch_simt_one(const AttnParams& p, cudaStream_t stream) {
   const size_t smem = simt_smem_bytes<KVT, D, G>(p.partition);
   auto kern = paged_attention_simt_kernel<QT, KVT, D, G, kMods>;
-  static bool configured = false;  // per instantiation
-  if (!configured) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)simt_smem_bytes<KVT, D, G>(kMaxPartition)) != cudaSuccess)
-      return PKV_ERR_CUDA;
-    configured = true;
-  }
+  static std::atomic<unsigned long long> configured{0};  // per instantiation
+  if (!smem_once(kern, simt_smem_bytes<KVT, D, G>(kMaxPartition), configured)) return PKV_ERR_CUDA;
   dim3 grid(p.num_rows, p.num_kv_heads, p.max_parts);
   kern<<<grid, kSimtThreads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;

@@ -48,13 +48,8 @@ int launch_tc_typed(const AttnParams& p, cudaStream_t stream, bool dependent) {
   static_assert(L::kStepKeys * L::kRowBytes == kTailBytes, "tail buffer = one MMA step of V");
   auto kern = paged_decode_tc_kernel<QT, G16, FP8, kH, kMods>;
   constexpr int kMaxSeqs = max_seqs(kMods);
-  static bool configured = false;
-  if (!configured) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
-      return PKV_ERR_CUDA;
-    configured = true;
-  }
+  static std::atomic<unsigned long long> configured{0};
+  if (!smem_once(kern, smem, configured)) return PKV_ERR_CUDA;
   using OutT = typename QT::T;
   // launches of at most kMaxSeqs sequences each (their rows are independent)
   for (int r0 = 0; r0 < p.num_rows; r0 += kMaxSeqs) {

@@ -6,7 +6,24 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace pkv {
+
+// Gives a kernel its dynamic shared memory, once per device: `done` (one per kernel)
+// holds a bit for each device it has been given on.
+template <class Kern>
+bool smem_once(Kern kern, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
+      cudaSuccess)
+    return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
 
 // Do [a, a + na) and [b, b + nb) share a byte?
 inline bool bytes_overlap(const void* a, unsigned long long na, const void* b, unsigned long long nb) {

@@ -177,7 +177,10 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapParams p) 
 
   // ---- tokens: slot and position, -1 behind the last sequence ------------------------------------
   const int total = qsl[S];
-  for (int t = blockIdx.x * kThreads + tid; t < p.num_tokens; t += gridDim.x * kThreads) {
+  // (64 bits: the index steps past num_tokens by up to a grid)
+  for (long long i = (long long)blockIdx.x * kThreads + tid; i < p.num_tokens;
+       i += gridDim.x * kThreads) {
+    const int t = (int)i;
     int64_t slot = -1;
     int pos = -1;
     if (t < total) {

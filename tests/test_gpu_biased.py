@@ -405,6 +405,25 @@ def test_prefill_hidden_infinities(kw):
         assert torch.isfinite(got[:3].float()).all()
 
 
+@pytest.mark.parametrize("kw", [dict(H=8, hkv=2), dict(H=8, hkv=2, kv="e4m3", dtype="fp16"),
+                                dict(H=4, hkv=4, D=64), dict(H=8, hkv=2, softcap=9.0, alibi=True)])
+@pytest.mark.parametrize("odd", [float("nan"), float("inf")])
+def test_queries_that_are_not_finite_stay_in_their_rows(kw, odd):
+    """One element of a row and head: its output is not a number throughout where the
+    element is none (an infinite one makes scores of both signs, and the largest of
+    them inf - inf), all the others are what they were."""
+    for b, row in ((Batch(39, [(150, 400), (3, 60)], **kw), 131), (Decode(40, [33, 700, 200], **kw), 1)):
+        if math.isinf(odd) and b.softcap:
+            continue  # (capped, an infinite score is a finite one)
+        q = b.q.clone()
+        q[row, 2, 7] = odd
+        got = b.call(q=q.to(DEV))
+        assert torch.isnan(got[row, 2].float()).all()
+        mine = got.clone()
+        mine[row, 2] = b.plain()[0][row, 2].to(mine.dtype).to(DEV)
+        b.check(mine)
+
+
 def test_prefill_rows_behind_the_last_sequence_stay():
     for kw in (dict(H=8, hkv=2), dict(H=8, hkv=2, D=64), dict(H=8, hkv=2, kv="e4m3")):
         b = Batch(41, [(5, 20), (30, 600), (0, 0)], window=40, **kw)

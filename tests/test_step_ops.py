@@ -229,6 +229,7 @@ def test_biased_binding_refusals():
                       (dict(key_start=torch.zeros(3, dtype=torch.int32)), ValueError),
                       (dict(context_lens=torch.zeros(3, dtype=torch.int32)), ValueError),
                       (dict(out=torch.empty(2, 8, 128, dtype=torch.float16)), TypeError),
+                      (dict(device_errors=torch.zeros(3, dtype=torch.uint8)), ValueError),
                       (dict(), ValueError)]:  # on the CPU
         with pytest.raises(exc):
             pkv.paged_attention_decode_biased(**{**t, **over})
