@@ -457,7 +457,7 @@ __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem<kFP8>& s
     mbar_init(&sm.q_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sm.s_ready[x], 1);
-      mbar_init(&sm.p_ready[x], 1);
+      mbar_init(&sm.p_ready[x], kTileWarps);
       mbar_init(&sm.o_done[x], 1);
       mbar_init(&sm.o_free[x], kTileWarps);
       sm.redo_n[x] = 0;
@@ -910,9 +910,8 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
   for (;; ++n) {
     int k;
     const int got = take_next(sm, n, &k, abort, lim);
-    // (the tile's warps leave the loop together: each passes the same barriers)
-    ok = all_of_tile(got >= 0, qt);
-    if (!ok || got == 0) break;
+    ok = got >= 0;
+    if (got <= 0) break;
     make_item<kMods, kFP8>(p, sm, k, total, x);
     const int nt = qt ? x.nt[1] : x.nt[0], t0 = qt ? x.t0[1] : x.t0[0];
     const int last = qt ? x.last[1] : x.last[0];
@@ -944,7 +943,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
     for (int i = 0; i < 4; ++i) l2[i] = make_float2(0.0f, 0.0f);
     for (int i = x.kt0; i <= last; ++i, ++ns) {
       const int k0 = tile_of<kMods>(x, i) * kTileKeys;
-      ok = all_of_tile(wait(&sm.s_ready[qt], ns & 1), qt);
+      ok = wait(&sm.s_ready[qt], ns & 1);
       if (!ok) break;
       tc::fence_after_sync();
       if (__all_sync(kFull, hi <= k0 || lo >= k0 + kTileKeys || empty)) {
@@ -956,8 +955,8 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
         for (int c = 0; c < kTileKeys / kChunk; ++c) tc::tmem_st16(s_col + 16 * c, z);
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        tc::named_sync(1 + qt, 32 * kTileWarps);
-        if (r == 0) mbar_arrive(&sm.p_ready[qt]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready[qt]);
         continue;
       }
       float sv[kTileKeys];
@@ -1023,14 +1022,14 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      tc::named_sync(1 + qt, 32 * kTileWarps);
-      if (r == 0) mbar_arrive(&sm.p_ready[qt]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_ready[qt]);
     }
     if (!ok) break;
     // ---- epilogue: O / l ------------------------------------------------------------------
     const float l = ((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y)) +
               ((l2[2].x + l2[2].y) + (l2[3].x + l2[3].y));
-    ok = all_of_tile(wait(&sm.o_done[qt], nit & 1), qt);
+    ok = wait(&sm.o_done[qt], nit & 1);
     if (!ok) break;
     tc::fence_after_sync();
     const float inv = valid && !empty ? p.v_scale / l : 0.0f;
@@ -1066,7 +1065,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
     if (lane == 0) mbar_arrive(&sm.o_free[qt]);
     ++nit;
   }
-  if (!ok && r == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+  if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
   // every warp of the tile leaves the loop here, whatever it met, and sees the others'
   // stores and flag behind this barrier
   ok = all_of_tile(ok, qt);
