@@ -47,15 +47,35 @@ using namespace pre_tc;
 // would have every case pay the registers of all.
 constexpr int kModCap = 1, kModBias = 2;
 
+// Waits for a barrier's phase, at most limit_ns or until the CTA gives up; the clock is
+// only read once the wait has been long (reading it takes longer than most waits).
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         unsigned long long limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !mbar_test(bar, parity); ++it) {
+    if ((it & 63u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort) return false;
+      if (now - t0 > limit_ns) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
 constexpr int kTileWarps = 4;  // softmax warps of a query tile
 constexpr int kSoftWarps = 2 * kTileWarps;
-constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 1;
-// Warps beside softmax and issuer, and threads of the CTA: three producers, or (E4M3
-// caches) one and six that convert its tiles.
-constexpr int kConverters = 6;
-constexpr int mod_producers(bool fp8) { return fp8 ? 1 : 3; }
+constexpr int kIssuers = 2;  // one per query tile
+constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + kIssuers;
+// Warps beside softmax and issuers, and threads of the CTA: two producers, or (E4M3
+// caches) one and five that convert its tiles.
+constexpr int kConverters = 5;
+constexpr int mod_producers(bool fp8) { return fp8 ? 1 : 2; }
 constexpr int mod_extra(bool fp8) { return mod_producers(fp8) + (fp8 ? kConverters : 0); }
-constexpr int mod_threads(bool fp8) { return 32 * (kSoftWarps + 1 + mod_extra(fp8)); }
+constexpr int mod_threads(bool fp8) { return 32 * (kSoftWarps + kIssuers + mod_extra(fp8)); }
 // Registers per thread: the launch gives 168 to each of 384 threads, 128 to each of
 // 512; the two softmax warpgroups take over what the others (issuer and producers)
 // return.
@@ -69,8 +89,24 @@ constexpr bool regs_fit(bool fp8) {
 static_assert(regs_fit(false) && regs_fit(true) && mod_threads(false) == 384 && mod_threads(true) == 512,
               "setmaxnreg may only share out what the launch holds");
 constexpr int kChunk = 32;  // keys whose weights are packed and stored together
-constexpr int kAhead = 4;   // items a CTA may ask for before the slowest warp takes them
+constexpr int kStepKeys = kTileKeys / 2;  // keys of a step: half a loaded tile
+constexpr int kAhead = 4;   // items made before the slowest warp takes them
 constexpr int kRedo = 64;   // items listed for recomputation; more of them: all items are looked at
+
+// Two query tiles of a sequence and KV head, and the keys they see.
+struct ModItem {
+  int k;               // its number in the launch, -1: no further item
+  int seq, kvh, ctx, q0;
+  int bidir;           // keys every query of the sequence sees (0: causal)
+  int t0[2], nt[2];    // first token (within the chunk) and tokens of tiles a, b
+  int pos0[2];         // absolute position of each tile's first token
+  int h0, nh;          // halves [h0, nh) of key tiles (64 keys) of the item
+  int kt0, nk;         // the key tiles [kt0, nk) they lie in (nk 0: no row sees a key)
+  int last[2];         // last step of each query tile (-1: its rows see nothing)
+  int lo_block, end_block;  // blocks any row sees
+  int tail_step;       // MMA step of key tile nk - 1 holding the partial last block, in half
+                       // nh - 1, else -1 (E4M3 caches: -1)
+};
 
 template <bool kFP8>
 struct ModSmem {
@@ -87,17 +123,18 @@ struct ModSmem {
   uint64_t staged[kStages];  // an E4M3 tile has landed in the second half of its stage
   uint64_t q_full;
   uint64_t q_empty;
-  uint64_t s_ready[2];  // per query tile
-  uint64_t p_ready[2];
-  uint64_t o_done[2];
+  uint64_t s_ready[2][2];  // per query tile and score buffer
+  uint64_t p_ready[2][2];
+  uint64_t o_done[2][2];  // the product of that buffer's P
   uint64_t o_free[2];
   uint64_t tail_full;
   uint64_t tail_free;
-  uint64_t mma_done;
-  // answers to the requests for further items: request m in slot m % kAhead
-  alignas(16) unsigned long long next[kAhead][2];
-  uint64_t next_full[kAhead];
-  uint64_t next_read[kAhead];
+  uint64_t mma_done[kIssuers];
+  alignas(16) unsigned long long answer[2];  // to the request for a further item
+  uint64_t answer_full;
+  ModItem item[kAhead];  // item n of the CTA in slot n % kAhead
+  uint64_t item_full[kAhead];
+  uint64_t item_read[kAhead];
   uint32_t tmem_base;
   int abort;
   // items with a row that came out not finite, by query tile (a few may be listed twice)
@@ -105,22 +142,15 @@ struct ModSmem {
   int redo[2][kRedo];
 };
 
-struct ModItem {
-  int seq, kvh, ctx, q0;
-  int bidir;           // keys every query of the sequence sees (0: causal)
-  int t0[2], nt[2];    // first token (within the chunk) and tokens of tiles a, b
-  int pos0[2];         // absolute position of each tile's first token
-  int kt0, nk;         // key tiles [kt0, nk) of the item (nk 0: no row sees a key)
-  int last[2];         // last step of each query tile (-1: its rows see nothing)
-  int lo_block, end_block;  // blocks any row sees
-  int tail_step;       // MMA step of key tile nk - 1 holding the partial last block, else -1
-                       // (E4M3 caches: -1)
-};
-
-// Steps kt0 .. nk - 1 of an item; the key tile of step i, backwards under a bias.
+// Loads go through an item's key tiles, kt0 + i being the i-th one (backwards under a
+// bias: nk - 1 - i), the products through their halves, step v = 0 .. nh - h0 - 1.
 template <int kMods>
 __device__ __forceinline__ int tile_of(const ModItem& x, int i) {
-  return (kMods & kModBias) ? x.nk - 1 - (i - x.kt0) : i;
+  return (kMods & kModBias) ? x.nk - 1 - i : x.kt0 + i;
+}
+template <int kMods>
+__device__ __forceinline__ int half_of(const ModItem& x, int v) {
+  return (kMods & kModBias) ? x.nh - 1 - v : x.h0 + v;
 }
 
 // Item k of the launch, or (k past the last one) an item without keys or rows.
@@ -129,9 +159,11 @@ __device__ __forceinline__ void make_item(const AttnParams& p, const ModSmem<kFP
                                           ModItem& it) {
   if (k >= total) {
     it = ModItem{};
+    it.k = k;
     it.last[0] = it.last[1] = it.tail_step = -1;
     return;
   }
+  it.k = k;
   it.kvh = k % p.num_kv_heads;
   const int pair = k / p.num_kv_heads;
   int lo = 0, hi = p.num_seqs - 1;
@@ -167,21 +199,23 @@ __device__ __forceinline__ void make_item(const AttnParams& p, const ModSmem<kFP
       if (start) first = max(first, __ldg(start));
       if (p.window > 0) first = max(first, it.pos0[x] - p.window + 1);
       if (first < h) {
-        end[x] = (h - 1) / kTileKeys + 1;
+        end[x] = (h - 1) / kStepKeys + 1;
         lo_min = min(lo_min, first);
         hi_max = max(hi_max, h);
       }
     }
   }
-  it.nk = max(end[0], end[1]);
-  it.kt0 = it.nk > 0 ? lo_min / kTileKeys : 0;
+  it.nh = max(end[0], end[1]);
+  it.nk = (it.nh + 1) / 2;
+  it.h0 = it.nk > 0 ? lo_min / kStepKeys : 0;
+  it.kt0 = it.h0 / 2;
   it.lo_block = it.nk > 0 ? lo_min / kBlockSize : 0;
   it.end_block = (hi_max + kBlockSize - 1) / kBlockSize;
 #pragma unroll
   for (int x = 0; x < 2; ++x)
-    it.last[x] = end[x] > 0 ? ((kMods & kModBias) ? it.nk : end[x]) - 1 : -1;
+    it.last[x] = end[x] > 0 ? ((kMods & kModBias) ? it.nh : end[x]) - 1 - it.h0 : -1;
   const bool partial = !kFP8 && (it.ctx & (kBlockSize - 1)) != 0;
-  it.tail_step = partial && (it.ctx - 1) / kTileKeys == it.nk - 1
+  it.tail_step = partial && (it.ctx - 1) / kStepKeys == it.nh - 1
                      ? ((it.ctx - 1) % kTileKeys) / kBlockSize
                      : -1;
 }
@@ -191,55 +225,56 @@ __device__ __forceinline__ void make_item(const AttnParams& p, const ModSmem<kFP
 // not launched yet (clusterlaunchcontrol) each time it begins one.  Round robin over
 // 152 CTAs left the longest 30 % above the mean for the packed documents.
 //
-// Producer warp 0 asks, at the start of its n-th item, for the item after it; every
-// warp reads the answer when it gets there.  No request follows one that found the
-// grid empty: that answer ends every warp's loop.
+// Producer warp 0 makes the items, for all warps: it asks for the one after next when it
+// begins one, and leaves each in shared memory, ahead of the warps that need it (made by
+// every warp for itself, an item cost the softmax 2500 cycles of index arithmetic and
+// dependent loads).  No request follows one that found the grid empty; an item -1 ends
+// every warp's loop.
 template <bool kFP8>
-__device__ __forceinline__ bool ask_next(ModSmem<kFP8>& sm, uint32_t m, volatile int* abort,
-                                         unsigned long long lim) {
-  const int slot = m % kAhead;
-  if (m >= kAhead && !wait_bar(&sm.next_read[slot], ((m / kAhead) - 1) & 1, abort, lim)) return false;
-  mbar_arrive_expect_tx(&sm.next_full[slot], 16);
+__device__ __forceinline__ void ask_next(ModSmem<kFP8>& sm) {
+  mbar_arrive_expect_tx(&sm.answer_full, 16);
   asm volatile(
       "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::
-          "r"(smem_u32(&sm.next[slot][0])),
-      "r"(smem_u32(&sm.next_full[slot]))
+          "r"(smem_u32(&sm.answer[0])),
+      "r"(smem_u32(&sm.answer_full))
       : "memory");
-  return true;
 }
 
-// The n-th item of this CTA, for the whole warp: 1 and its index in *k, 0 when there is
-// none, -1 when the wait gave up.
+// The answer to request m, for one thread: an item's number, -1 where there is none, -2
+// when the wait gave up.
 template <bool kFP8>
-__device__ __forceinline__ int take_next(ModSmem<kFP8>& sm, uint32_t n, int* k, volatile int* abort,
+__device__ __forceinline__ int next_item(ModSmem<kFP8>& sm, uint32_t m, volatile int* abort,
                                          unsigned long long lim) {
-  if (n == 0) {
-    *k = blockIdx.x;
-    return 1;
-  }
-  const uint32_t m = n - 1;
-  const int slot = m % kAhead;
-  int got = -1;
-  uint32_t index = 0;
-  if ((threadIdx.x & 31) == 0 && wait_bar(&sm.next_full[slot], (m / kAhead) & 1, abort, lim)) {
-    const unsigned long long a = *static_cast<volatile unsigned long long*>(&sm.next[slot][0]);
-    const unsigned long long b = *static_cast<volatile unsigned long long*>(&sm.next[slot][1]);
-    uint32_t yes;
-    asm volatile(
-        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
-        "mov.b128 r, {%2, %3};\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t"
-        "mov.u32 %1, 0;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
-        : "=r"(yes), "=r"(index)
-        : "l"(a), "l"(b));
-    got = (int)yes;
-    fence_proxy_async_smem();  // the slot is read before a later answer overwrites it
-    mbar_arrive(&sm.next_read[slot]);
-  }
-  *k = (int)__shfl_sync(kFull, index, 0);
-  return __shfl_sync(kFull, got, 0);
+  if (!wait_for(&sm.answer_full, m & 1, abort, lim)) return -2;
+  const unsigned long long a = *static_cast<volatile unsigned long long*>(&sm.answer[0]);
+  const unsigned long long b = *static_cast<volatile unsigned long long*>(&sm.answer[1]);
+  uint32_t yes, index;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "mov.b128 r, {%2, %3};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(yes), "=r"(index)
+      : "l"(a), "l"(b));
+  fence_proxy_async_smem();  // read before a later answer overwrites it
+  return yes ? (int)index : -1;
+}
+
+// The n-th item of this CTA, for a warp, or (kOne) for one thread of it; false when the
+// wait gave up.
+template <bool kOne, bool kFP8>
+__device__ __forceinline__ bool take_item(ModSmem<kFP8>& sm, uint32_t n, ModItem& x, volatile int* abort,
+                                          unsigned long long lim) {
+  const int slot = n % kAhead;
+  bool ok = wait_for(&sm.item_full[slot], (n / kAhead) & 1, abort, lim);
+  if (!kOne) ok = __all_sync(kFull, ok);
+  if (!ok) return false;
+  x = sm.item[slot];
+  if (!kOne) __syncwarp();
+  if (kOne || (threadIdx.x & 31) == 0) mbar_arrive(&sm.item_read[slot]);
+  return true;
 }
 
 // All softmax threads of query tile qt agree on `ok` (named barrier 1 + qt).
@@ -263,7 +298,7 @@ __device__ __forceinline__ float absmax3(float a, float b, float c) {
   return r;
 }
 
-// The scores of a tile's 128 keys from k0 on, modified in place.  a > 0 takes a raw
+// The scores of a step's 64 keys from k0 on, modified in place.  a > 0 takes a raw
 // score to base-2 units, C = cap log2(e) is the cap in them.  Returns the factor
 // still to be applied, which the exponential's own multiply-add carries: a where the
 // score is only masked, 1 after a cap or a bias.
@@ -285,7 +320,7 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
     const float c = a / p.cap_log2, C = p.cap_log2;
     float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < kTileKeys; i += 2)
+    for (int i = 0; i < kStepKeys; i += 2)
       top[(i >> 1) & 3] = absmax3(top[(i >> 1) & 3], sv[i], sv[i + 1]);
     const float most = absmax3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
     if (__all_sync(kFull, most <= kTanhPoly && c <= 16.0f)) {
@@ -295,7 +330,7 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
                    q2 = make_float2(t2 * kTanh5, t2 * kTanh5),
                    q3 = make_float2(t3 * kTanh7, t3 * kTanh7);
 #pragma unroll
-      for (int i = 0; i < kTileKeys; i += 2) {
+      for (int i = 0; i < kStepKeys; i += 2) {
         const float2 x = make_float2(sv[i], sv[i + 1]), u = __fmul2_rn(x, x);
         const float2 t = __ffma2_rn(u, __ffma2_rn(u, __ffma2_rn(u, q3, q2), q1), q0);
         const float2 y = __fmul2_rn(x, t);
@@ -305,7 +340,7 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
     } else {
       const float k = 2.0f * kLog2e * c;
 #pragma unroll
-      for (int i = 0; i < kTileKeys; ++i) {
+      for (int i = 0; i < kStepKeys; ++i) {
         float r;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(sv[i] * k) + 1.0f));
         sv[i] = fmaf(r, -2.0f * C, C);
@@ -317,19 +352,19 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
     // where every row of the warp is behind the tile
     const float f = (kMods & kModCap) != 0 ? 1.0f : a;
     const float d0 = (float)(pos - k0), b0 = -slope * d0;
-    if (__all_sync(kFull, pos >= k0 + kTileKeys - 1)) {
+    if (__all_sync(kFull, pos >= k0 + kStepKeys - 1)) {
 #pragma unroll
-      for (int i = 0; i < kTileKeys; ++i) sv[i] = fmaf(sv[i], f, fmaf(slope, (float)i, b0));
+      for (int i = 0; i < kStepKeys; ++i) sv[i] = fmaf(sv[i], f, fmaf(slope, (float)i, b0));
     } else {
 #pragma unroll
-      for (int i = 0; i < kTileKeys; ++i) sv[i] = fmaf(sv[i], f, -slope * fabsf(d0 - (float)i));
+      for (int i = 0; i < kStepKeys; ++i) sv[i] = fmaf(sv[i], f, -slope * fabsf(d0 - (float)i));
     }
   }
   return 1.0f;
 }
 
-// Scores: S (128 rows x 128 keys, fp32 in TMEM at d) = Q K^T over D dimensions, 16 a
-// step, within 64-dimension halves of 16 KB.
+// Scores: S (128 rows x 64 keys, fp32 in TMEM at d) = Q K^T over D dimensions, 16 an MMA,
+// within 64-dimension halves of 16 KB.
 template <int D>
 __device__ __forceinline__ void issue_mods_scores(uint32_t d, uint64_t dq, uint64_t dk,
                                                   uint32_t idesc) {
@@ -337,6 +372,17 @@ __device__ __forceinline__ void issue_mods_scores(uint32_t d, uint64_t dq, uint6
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
     tc::mma_f16(d, dq + off, dk + off, idesc, kk > 0);
+  }
+}
+
+// Output: O (at d) (+)= P (TMEM at a, 16 keys per 8 columns) V, 16 keys an MMA; the one
+// numbered ts (if >= 0) takes its V rows from the tail buffer.
+__device__ __forceinline__ void issue_mods_pv(uint32_t d, uint32_t a, uint64_t dv, uint64_t dtail,
+                                              int ts, uint32_t acc0, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < kStepKeys / 16; ++kk) {
+    const uint64_t b = kk == ts ? dtail : dv + (uint64_t)((kk * (kBlockSize * 128)) >> 4);
+    mma_f16_tmem_a(d, a + kk * 8, b, idesc, acc0 | (kk != 0 ? 1u : 0u));
   }
 }
 
@@ -450,25 +496,28 @@ __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem<kFP8>& s
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.full[s], kFP8 ? kConverters : mod_producers(false));
-      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.empty[s], kIssuers);
       mbar_init(&sm.staged[s], 1);
     }
     mbar_init(&sm.q_full, 1);
-    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.q_empty, kIssuers);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&sm.s_ready[x], 1);
-      mbar_init(&sm.p_ready[x], kTileWarps);
-      mbar_init(&sm.o_done[x], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sm.s_ready[x][b], 1);
+        mbar_init(&sm.p_ready[x][b], kTileWarps);
+        mbar_init(&sm.o_done[x][b], 1);
+      }
       mbar_init(&sm.o_free[x], kTileWarps);
+      mbar_init(&sm.mma_done[x], 1);
       sm.redo_n[x] = 0;
     }
     for (int i = 0; i < kAhead; ++i) {
-      mbar_init(&sm.next_full[i], 1);
-      mbar_init(&sm.next_read[i], kSoftWarps + 1 + mod_extra(kFP8));
+      mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.item_read[i], kSoftWarps + kIssuers + mod_extra(kFP8) - 1);
     }
+    mbar_init(&sm.answer_full, 1);
     mbar_init(&sm.tail_full, 1);
-    mbar_init(&sm.tail_free, 1);
-    mbar_init(&sm.mma_done, 1);
+    mbar_init(&sm.tail_free, kIssuers);
     sm.abort = 0;
     fence_barrier_init();
   }
@@ -572,7 +621,7 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
     const bool skip = pw == 0 && blockIdx.x == 0 && p.skip_copy > 0 && pos + 1 == (uint32_t)p.skip_copy;
     bool good = true;
     if (lane == 0) {
-      if (pos >= (uint32_t)nst) good = wait_bar(&sm.empty[st], ((pos / nst) - 1) & 1, abort, lim);
+      if (pos >= (uint32_t)nst) good = wait_for(&sm.empty[st], ((pos / nst) - 1) & 1, abort, lim);
       if (good && !skip) mbar_arrive_expect_tx(&landed[st], mine * (kLoadBytes / 8));
     }
     if (!__shfl_sync(kFull, (int)good, 0)) return false;
@@ -591,7 +640,7 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
   // as zeros, with the ring's swizzle
   auto load_tail = [&]() -> bool {
     bool good = true;
-    if (lane == 0 && ntail >= 1) good = wait_bar(&sm.tail_free, (ntail - 1) & 1, abort, lim);
+    if (lane == 0 && ntail >= 1) good = wait_for(&sm.tail_free, (ntail - 1) & 1, abort, lim);
     if (!__shfl_sync(kFull, (int)good, 0)) return false;
     constexpr int kRowChunks = D / 8;  // 16-byte chunks per row
     const int key0 = (x.nk - 1) * kTileKeys + x.tail_step * kBlockSize;
@@ -618,25 +667,40 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
     ++ntail;
     return true;
   };
+  uint32_t asked = 0;
   for (; ok; ++n) {
-    int k;
-    const int got = take_next(sm, n, &k, abort, lim);
-    if (got <= 0) {
-      ok = got == 0;
-      break;
-    }
     bool good = true;
     if (pw == 0) {
-      if (lane == 0) good = ask_next(sm, n, abort, lim);
-      if (!__shfl_sync(kFull, (int)good, 0)) {
+      int k = blockIdx.x;
+      if (lane == 0 && n > 0) k = next_item(sm, n - 1, abort, lim);
+      k = __shfl_sync(kFull, k, 0);
+      if (k == -2) {
         ok = false;
         break;
       }
+      if (k >= 0) {
+        if (lane == 0) ask_next(sm);
+        ++asked;
+        make_item<kMods, kFP8>(p, sm, k, total, x);
+      }
+      if (lane == 0) {
+        const int slot = n % kAhead;
+        if (n >= kAhead) good = wait_for(&sm.item_read[slot], ((n / kAhead) - 1) & 1, abort, lim);
+        if (good) {
+          if (k >= 0) sm.item[slot] = x;
+          else sm.item[slot].k = -1;
+          mbar_arrive(&sm.item_full[slot]);
+        }
+      }
+      ok = __shfl_sync(kFull, (int)good, 0) != 0;
+      if (!ok || k < 0) break;
+    } else {
+      ok = take_item<false>(sm, n, x, abort, lim);
+      if (!ok || x.k < 0) break;
     }
-    make_item<kMods, kFP8>(p, sm, k, total, x);
     if (x.nk == 0) continue;
     if (pw == 0 && lane == 0) {
-      if (nitem >= 1) good = wait_bar(&sm.q_empty, (nitem - 1) & 1, abort, lim);
+      if (nitem >= 1) good = wait_for(&sm.q_empty, (nitem - 1) & 1, abort, lim);
       if (good) {
         const int nq = x.nt[1] > 0 ? 2 : 1;
         mbar_arrive_expect_tx(&sm.q_full, nq * (kRowsM / g * g * D * 2));
@@ -651,9 +715,9 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
     ok = __shfl_sync(kFull, (int)good, 0) != 0;
     // block rows of the 32-block chunk (four key tiles) in use; the next one read ahead
     constexpr int kStep = (kMods & kModBias) ? -1 : 1;
-    int cur_c = tile_of<kMods>(x, x.kt0) >> 2, cur_row = to_row(fetch(cur_c));
+    int cur_c = tile_of<kMods>(x, 0) >> 2, cur_row = to_row(fetch(cur_c));
     int pre_raw = fetch(cur_c + kStep);
-    for (int i = x.kt0; ok && i < x.nk; ++i) {
+    for (int i = 0; ok && i < x.nk - x.kt0; ++i) {
       const int t = tile_of<kMods>(x, i);
       if ((t >> 2) != cur_c) {
         cur_c = t >> 2;
@@ -668,8 +732,8 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
   }
   if (!ok && lane == 0) {
     flag_error(p.errors, PKV_DEVERR_TIMEOUT);
-    // an answer still on its way lands before the CTA goes away (requests 0 .. n)
-    if (pw == 0) mbar_wait(&sm.next_full[n % kAhead], (n / kAhead) & 1, 10000000ull);
+    // an answer still on its way lands before the CTA goes away
+    if (pw == 0 && asked > 0) mbar_wait(&sm.answer_full, (asked - 1) & 1, 10000000ull);
     for (uint32_t y = pos > (uint32_t)nst ? pos - nst : 0; y < pos; ++y)
       mbar_wait(&landed[y % nst], (y / nst) & 1, 10000000ull);
   }
@@ -717,7 +781,7 @@ __device__ __forceinline__ void mods_converter(const AttnParams& p, ModSmem<true
   auto convert = [&](int rows) -> bool {
     const int st = pos % kStages;
     bool good = true;
-    if (lane == 0) good = wait_bar(&sm.staged[st], (pos / kStages) & 1, abort, lim);
+    if (lane == 0) good = wait_for(&sm.staged[st], (pos / kStages) & 1, abort, lim);
     if (!__shfl_sync(kFull, (int)good, 0)) return false;
     ++pos;
     uint8_t* tile = &sm.ring[st][0];
@@ -755,132 +819,118 @@ __device__ __forceinline__ void mods_converter(const AttnParams& p, ModSmem<true
     return true;
   };
   for (uint32_t n = 0; ok; ++n) {
-    int k;
-    const int got = take_next(sm, n, &k, abort, lim);
-    if (got <= 0) {
-      ok = got == 0;
-      break;
-    }
-    make_item<kMods, true>(p, sm, k, total, x);
-    for (int i = x.kt0; ok && i < x.nk; ++i)
+    ok = take_item<false>(sm, n, x, abort, lim);
+    if (!ok || x.k < 0) break;
+    for (int i = 0; ok && i < x.nk - x.kt0; ++i)
       ok = convert(kTileKeys) && convert(x.ctx - tile_of<kMods>(x, i) * kTileKeys);
   }
   if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
 }
 
-// MMA issuer.  Order per item: S_a, S_b of the first step, then for each step i
-//   P_a(i) V, S_a(i + 1), P_b(i) V, S_b(i + 1)
-// so that one query tile's softmax works while the tensor pipe serves the other.
+// MMA issuer of query tile qt, one thread.  The tile has two score buffers, so that its
+// softmax has the next step's scores at hand: the scores of step v follow the product of
+// step v - 2, which frees their buffer.  One issuer for both query tiles was the
+// bottleneck: 1500 cycles per tile and step, of which the products take a third.
 template <class QT, bool kFP8, int kMods, int D>
-__device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem<kFP8>& sm, uint32_t tmem, int total) {
-  constexpr int kStageBytes = kTileBytes;
-  constexpr int nst = kStages;
+__device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem<kFP8>& sm, uint32_t tmem,
+                                            int total, int qt) {
   constexpr uint32_t kAB = std::is_same<QT, BF16>::value ? 1u : 0u;
-  constexpr uint32_t kIdescS = tc::idesc_f16(kAB, 0, 0, 128, 128);
+  constexpr uint32_t kIdescS = tc::idesc_f16(kAB, 0, 0, 128, kStepKeys);
   constexpr uint32_t kIdescO = tc::idesc_f16(kAB, 0, 1, 128, D);
-  volatile int* abort = &sm.abort;
-  const unsigned long long lim = wait_limit(p);
-  const bool leader = tc::elect_one();
-  auto commit = [&](uint64_t* bar) {
-    if (leader) tc::mma_commit(bar);
-  };
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // every lane takes the same result
-    return __shfl_sync(kFull, (int)wait_bar(bar, parity, abort, lim), 0) != 0;
-  };
-  uint32_t pos = 0, n = 0;
-  uint32_t np[2] = {0, 0};   // P tiles consumed per query tile
-  uint32_t nit[2] = {0, 0};  // items per query tile
-  int nitem = 0, ntail = 0;
-  bool ok = true;
-  ModItem x;
-  auto acquire = [&](int& st) -> bool {
-    st = pos % nst;
-    const bool r = wait(&sm.full[st], (pos / nst) & 1);
-    ++pos;
-    if (r) tc::fence_after_sync();
-    return r;
-  };
-  const uint64_t dq[2] = {tc::smem_desc(smem_u32(&sm.q[0][0]), 16, 1024, tc::kLayoutSw128),
-                          tc::smem_desc(smem_u32(&sm.q[1][0]), 16, 1024, tc::kLayoutSw128)};
-  const uint64_t dk0 = tc::smem_desc(smem_u32(&sm.ring[0][0]), 16, 1024, tc::kLayoutSw128);
-  const uint64_t dv0 = tc::smem_desc(smem_u32(&sm.ring[0][0]), kHalf, 1024, tc::kLayoutSw128);
-  const uint64_t dtail = tc::smem_desc(smem_u32(&sm.tail[0]), kTailBytes / 2, 1024, tc::kLayoutSw128);
-  auto mma_s = [&](int qt, int st) {
-    if (leader) {
-      const uint64_t dk = dk0 + (uint64_t)(st * (kStageBytes >> 4));
-      issue_mods_scores<D>(tmem + qt * 128, qt ? dq[1] : dq[0], dk, kIdescS);
-    }
-    commit(&sm.s_ready[qt]);
-  };
-  auto mma_pv = [&](int qt, int st, int i) -> bool {
-    if (!wait(&sm.p_ready[qt], np[qt] & 1)) return false;
-    ++np[qt];
-    if (i == x.kt0 && nit[qt] >= 1 && !wait(&sm.o_free[qt], (nit[qt] - 1) & 1))
-      return false;  // the previous item's O has been read out
-    tc::fence_after_sync();
-    if (leader) {
-      const uint64_t dv = dv0 + (uint64_t)(st * (kStageBytes >> 4));
-      const int ts = tile_of<kMods>(x, i) == x.nk - 1 ? x.tail_step : -1;
-      const uint32_t d = tmem + kColO + qt * 128, a = tmem + qt * 128, acc = i != x.kt0;
-      issue_pv(d, a, dv, dtail, ts, acc, kIdescO);
-    }
-    if (i == x.last[qt]) commit(&sm.o_done[qt]);
-    return true;
-  };
-  for (; ok; ++n) {
-    int k;
-    const int got = take_next(sm, n, &k, abort, lim);
-    if (got <= 0) {
-      ok = got == 0;
-      break;
-    }
-    make_item<kMods, kFP8>(p, sm, k, total, x);
-    if (x.nk == 0) continue;
-    const bool ha = x.last[0] >= 0, hb = x.last[1] >= 0;
-    int kst = 0, vst = 0;
-    ok = wait(&sm.q_full, nitem & 1);
-    if (ok) {
-      tc::fence_after_sync();
-      ok = acquire(kst);
-    }
-    if (ok) {
-      if (ha) mma_s(0, kst);
-      if (hb) mma_s(1, kst);
-      commit(&sm.empty[kst]);
-      if (x.nk - x.kt0 == 1) commit(&sm.q_empty);
-    }
-    for (int i = x.kt0; ok && i < x.nk; ++i) {
-      const bool more = i + 1 < x.nk;
-      ok = acquire(vst);
-      if (ok && x.tail_step >= 0 && tile_of<kMods>(x, i) == x.nk - 1) {
-        ok = wait(&sm.tail_full, ntail & 1);
-        if (ok) tc::fence_after_sync();
+  constexpr uint64_t kStage = kTileBytes >> 4;          // in descriptor units
+  constexpr uint64_t kInTile = (kStepKeys * 128) >> 4;  // a tile's second half of keys
+  constexpr int kBack = (kMods & kModBias) != 0;
+  static_assert((kStages & (kStages - 1)) == 0, "ring positions wrap");
+  if (tc::elect_one()) {
+    volatile int* abort = &sm.abort;
+    const unsigned long long lim = wait_limit(p);
+    const uint64_t dq = tc::smem_desc(smem_u32(&sm.q[qt][0]), 16, 1024, tc::kLayoutSw128);
+    const uint64_t dk = tc::smem_desc(smem_u32(&sm.ring[0][0]), 16, 1024, tc::kLayoutSw128);
+    const uint64_t dv = tc::smem_desc(smem_u32(&sm.ring[0][0]), kHalf, 1024, tc::kLayoutSw128);
+    const uint64_t dtail =
+        tc::smem_desc(smem_u32(&sm.tail[0]), kTailBytes / 2, 1024, tc::kLayoutSw128);
+    const uint32_t s_col = tmem + qt * 128, o_col = tmem + kColO + qt * 128;
+    uint32_t at_k = 0, at_v = 1;  // ring positions of the scores' K and the products' V tile
+    uint32_t ns = 0, np = 0;      // score steps issued, P consumed
+    uint32_t nit = 0, nitem = 0, ntail = 0;  // items with steps of this tile, items, tails
+    bool ok = true;
+    ModItem x;
+    for (uint32_t n = 0; ok; ++n) {
+      ok = take_item<true>(sm, n, x, abort, lim);
+      if (!ok || x.k < 0) break;
+      if (x.nk == 0) continue;
+      const int steps = x.nh - x.h0, last = qt ? x.last[1] : x.last[0];
+      const int tail_half = x.tail_step >= 0 ? x.nh - 1 : -1;
+      int hs = half_of<kMods>(x, 0), hp = hs;  // halves of the scores' and the products' step
+      bool new_k = true, new_v = true;         // their tile has not been waited for
+      // scores of step v
+      auto scores = [&](int v) -> bool {
+        if (new_k) {
+          if (!wait_for(&sm.full[at_k % kStages], (at_k / kStages) & 1, abort, lim)) return false;
+          tc::fence_after_sync();
+        }
+        if (v <= last) {
+          const uint32_t b = ns++ & 1;
+          issue_mods_scores<D>(s_col + b * kStepKeys, dq,
+                               dk + (at_k % kStages) * kStage + (hs & 1) * kInTile, kIdescS);
+          tc::mma_commit(&sm.s_ready[qt][b]);
+        }
+        new_k = v + 1 == steps || (hs & 1) != kBack;
+        if (new_k) {  // the tile's last step
+          tc::mma_commit(&sm.empty[at_k % kStages]);
+          at_k += 2;
+        }
+        hs += kBack ? -1 : 1;
+        if (v + 1 == steps) tc::mma_commit(&sm.q_empty);
+        return true;
+      };
+      ok = wait_for(&sm.q_full, nitem & 1, abort, lim);
+      if (ok) tc::fence_after_sync();
+#pragma unroll 1
+      for (int v = -2; ok && v < steps; ++v) {
+        if (v >= 0) {
+          if (new_v) {
+            ok = wait_for(&sm.full[at_v % kStages], (at_v / kStages) & 1, abort, lim);
+            if (!ok) break;
+          }
+          if (hp == tail_half) {
+            ok = wait_for(&sm.tail_full, ntail & 1, abort, lim);
+            if (!ok) break;
+          }
+          if (v <= last) {
+            const uint32_t b = np & 1;
+            ok = wait_for(&sm.p_ready[qt][b], (np >> 1) & 1, abort, lim);
+            if (ok && v == 0 && nit > 0)  // the previous item's O has been read out
+              ok = wait_for(&sm.o_free[qt], (nit - 1) & 1, abort, lim);
+            if (!ok) break;
+            ++np;
+            tc::fence_after_sync();
+            issue_mods_pv(o_col, s_col + b * kStepKeys,
+                          dv + (at_v % kStages) * kStage + (hp & 1) * kInTile, dtail,
+                          hp == tail_half ? x.tail_step & 3 : -1, v != 0, kIdescO);
+            tc::mma_commit(&sm.o_done[qt][b]);
+          }
+          new_v = v + 1 == steps || (hp & 1) != kBack;
+          if (new_v) {
+            tc::mma_commit(&sm.empty[at_v % kStages]);
+            at_v += 2;
+          }
+          hp += kBack ? -1 : 1;
+        }
+        if (v + 2 < steps) ok = scores(v + 2);
       }
-      if (ok && i <= x.last[0]) ok = mma_pv(0, vst, i);
-      if (ok && more) {
-        ok = acquire(kst);
-        if (ok && i + 1 <= x.last[0]) mma_s(0, kst);
+      if (ok && x.tail_step >= 0) {
+        tc::mma_commit(&sm.tail_free);
+        ++ntail;
       }
-      if (ok && i <= x.last[1]) ok = mma_pv(1, vst, i);
-      if (!ok) break;
-      commit(&sm.empty[vst]);
-      if (more) {
-        if (i + 1 <= x.last[1]) mma_s(1, kst);
-        commit(&sm.empty[kst]);
-        if (i + 1 == x.nk - 1) commit(&sm.q_empty);
-      }
+      if (last >= 0) ++nit;
+      ++nitem;
     }
-    if (ok && x.tail_step >= 0) {
-      commit(&sm.tail_free);
-      ++ntail;
-    }
-    if (ha) ++nit[0];
-    if (hb) ++nit[1];
-    ++nitem;
+    if (!ok) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+    tc::mma_commit(&sm.mma_done[qt]);
+    mbar_wait(&sm.mma_done[qt], 0, 100000000ull);
   }
-  if (!ok && leader) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
-  commit(&sm.mma_done);
-  mbar_wait(&sm.mma_done, 0, 100000000ull);
+  __syncwarp();
 }
 
 // Softmax and epilogue: thread = row of query tile qt.
@@ -901,18 +951,15 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
   const float qa = fmaxf(fabsf(p.q_scale), 1e-30f);
   const int tok = r / g, head_in = r - tok * g;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // the warp's lanes agree
-    return __all_sync(kFull, wait_bar(bar, parity, abort, lim)) != 0;
+    return __all_sync(kFull, wait_for(bar, parity, abort, lim)) != 0;
   };
   uint32_t n = 0;
-  uint32_t ns = 0, nit = 0;  // S tiles and items of this query tile
+  uint32_t ns = 0;  // steps of this query tile
   bool ok = true;
   ModItem x;
   for (;; ++n) {
-    int k;
-    const int got = take_next(sm, n, &k, abort, lim);
-    ok = got >= 0;
-    if (got <= 0) break;
-    make_item<kMods, kFP8>(p, sm, k, total, x);
+    ok = take_item<false>(sm, n, x, abort, lim);
+    if (!ok || x.k < 0) break;
     const int nt = qt ? x.nt[1] : x.nt[0], t0 = qt ? x.t0[1] : x.t0[0];
     const int last = qt ? x.last[1] : x.last[0];
     const int pos = (qt ? x.pos0[1] : x.pos0[0]) + tok;
@@ -941,48 +988,48 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
     float2 l2[4];  // partial row sums (independent chains, packed pairs)
 #pragma unroll
     for (int i = 0; i < 4; ++i) l2[i] = make_float2(0.0f, 0.0f);
-    for (int i = x.kt0; i <= last; ++i, ++ns) {
-      const int k0 = tile_of<kMods>(x, i) * kTileKeys;
-      ok = wait(&sm.s_ready[qt], ns & 1);
+    for (int v = 0; v <= last; ++v, ++ns) {
+      const int k0 = half_of<kMods>(x, v) * kStepKeys, b = ns & 1;
+      const uint32_t s_at = s_col + b * kStepKeys;
+      ok = wait(&sm.s_ready[qt][b], (ns >> 1) & 1);
       if (!ok) break;
       tc::fence_after_sync();
-      if (__all_sync(kFull, hi <= k0 || lo >= k0 + kTileKeys || empty)) {
-        // no row of the warp sees a key of the tile
+      if (__all_sync(kFull, hi <= k0 || lo >= k0 + kStepKeys || empty)) {
+        // no row of the warp sees a key of the step
         float z[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) z[c] = 0.0f;
 #pragma unroll
-        for (int c = 0; c < kTileKeys / kChunk; ++c) tc::tmem_st16(s_col + 16 * c, z);
+        for (int c = 0; c < kStepKeys / kChunk; ++c) tc::tmem_st16(s_at + 16 * c, z);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_ready[qt]);
+        if (lane == 0) mbar_arrive(&sm.p_ready[qt][b]);
         continue;
       }
-      float sv[kTileKeys];
+      float sv[kStepKeys];
 #pragma unroll
-      for (int c = 0; c < kTileKeys; c += 32) tc::tmem_ld32(s_col + c, sv + c);
+      for (int c = 0; c < kStepKeys; c += 32) tc::tmem_ld32(s_at + c, sv + c);
       tc::tmem_wait_ld();
       if (neg) {
 #pragma unroll
-        for (int c = 0; c < kTileKeys; ++c) sv[c] = -sv[c];
+        for (int c = 0; c < kStepKeys; ++c) sv[c] = -sv[c];
       }
       const float f = modify_scores<kMods>(p, sv, qa, slope, pos, k0);
-      if (!__all_sync(kFull, lo <= k0 && hi >= k0 + kTileKeys)) {
+      if (!__all_sync(kFull, lo <= k0 && hi >= k0 + kStepKeys)) {
         // an interval of some row of the warp ends in this tile: hidden keys become -inf
 #pragma unroll
-        for (int c = 0; c < kTileKeys; ++c)
+        for (int c = 0; c < kStepKeys; ++c)
           sv[c] = k0 + c >= lo && k0 + c < hi ? sv[c] : -INFINITY;
       }
       float mx[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) mx[c] = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < kTileKeys; c += 2)
+      for (int c = 0; c < kStepKeys; c += 2)
         mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
       const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
-      // move the running max (and rescale O) only on a large increase; O is complete
-      // up to the step before (this S was issued after its product)
+      // move the running max (and rescale O) only on a large increase
       const bool fresh = m_run == -INFINITY;  // no key seen so far
       const bool need = mt > m_run + kRescaleAt;
       float alpha = 1.0f;
@@ -995,7 +1042,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
       const float m = m_run == -INFINITY ? 0.0f : m_run;  // 2^(-inf - 0) = 0
       // weights, over the scores read (hidden keys are -inf: weight 0)
 #pragma unroll
-      for (int c = 0; c < kTileKeys / kChunk; ++c) {
+      for (int c = 0; c < kStepKeys / kChunk; ++c) {
         float pk[16];
         const float2 f2 = make_float2(f, f), m2 = make_float2(-m, -m);
 #pragma unroll
@@ -1005,10 +1052,13 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
           l2[(e >> 1) & 3] = __fadd2_rn(l2[(e >> 1) & 3], w);
           pk[e >> 1] = __uint_as_float(pack2<QT>(w.x, w.y));
         }
-        tc::tmem_st16(s_col + 16 * c, pk);
+        tc::tmem_st16(s_at + 16 * c, pk);
       }
-      // the product of this step adds onto O: rescale it first
-      if (i > x.kt0 && __any_sync(kFull, need)) {
+      // the product of this step adds onto O: rescale it first, once the one before is done
+      if (v > 0 && __any_sync(kFull, need)) {
+        ok = wait(&sm.o_done[qt][(ns - 1) & 1], ((ns - 1) >> 1) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float ov[32];
@@ -1023,47 +1073,67 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_ready[qt]);
+      if (lane == 0) mbar_arrive(&sm.p_ready[qt][b]);
     }
     if (!ok) break;
     // ---- epilogue: O / l ------------------------------------------------------------------
     const float l = ((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y)) +
               ((l2[2].x + l2[2].y) + (l2[3].x + l2[3].y));
-    ok = wait(&sm.o_done[qt], nit & 1);
+    ok = wait(&sm.o_done[qt][(ns - 1) & 1], ((ns - 1) >> 1) & 1);
     if (!ok) break;
     tc::fence_after_sync();
     const float inv = valid && !empty ? p.v_scale / l : 0.0f;
-    bool odd = false;  // an output that is not finite
+    // four lanes exchange their rows' 16-byte pieces, so that they store 64 contiguous
+    // bytes of one row at a time (a piece of 32 rows in each store instead cost 5300 cycles
+    // an item); the four rows' places in the output, -1 where there is none
+    int place[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      place[i] = __shfl_sync(kFull, valid ? row * p.num_heads + h : -1, (lane & 28) + i);
+    const bool up2 = lane & 2, up1 = lane & 1;
+    float2 z = make_float2(0.0f, 0.0f);  // NaN behind an output that is not finite
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       float ov[32];
       tc::tmem_ld32(o_col + c, ov);
       tc::tmem_wait_ld();
+      uint32_t w1[16];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        ov[e] = empty ? 0.0f : ov[e] * inv;
-        odd |= !(fabsf(ov[e]) < INFINITY);
+      for (int e = 0; e < 32; e += 2) {
+        const float2 o2 = __fmul2_rn(make_float2(ov[e], ov[e + 1]), make_float2(inv, inv));
+        z = __ffma2_rn(o2, make_float2(0.0f, 0.0f), z);
+        w1[e >> 1] = empty ? 0u : pack2<QT>(o2.x, o2.y);
       }
-      if (valid) {
+      uint4 w[4];
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          uint4 w;
-          w.x = pack2<QT>(ov[q4 * 8 + 0], ov[q4 * 8 + 1]);
-          w.y = pack2<QT>(ov[q4 * 8 + 2], ov[q4 * 8 + 3]);
-          w.z = pack2<QT>(ov[q4 * 8 + 4], ov[q4 * 8 + 5]);
-          w.w = pack2<QT>(ov[q4 * 8 + 6], ov[q4 * 8 + 7]);
-          reinterpret_cast<uint4*>(orow + c)[q4] = w;
-        }
-      }
+      for (int i = 0; i < 4; ++i)
+        w[i] = make_uint4(w1[4 * i], w1[4 * i + 1], w1[4 * i + 2], w1[4 * i + 3]);
+      auto swap = [&](uint4& a, uint4& b, bool up, int mask) {  // a of the upper lane for b of the lower
+        uint4 t = up ? a : b;
+        t.x = __shfl_xor_sync(kFull, t.x, mask);
+        t.y = __shfl_xor_sync(kFull, t.y, mask);
+        t.z = __shfl_xor_sync(kFull, t.z, mask);
+        t.w = __shfl_xor_sync(kFull, t.w, mask);
+        if (up) a = t; else b = t;
+      };
+      swap(w[0], w[2], up2, 2);
+      swap(w[1], w[3], up2, 2);
+      swap(w[0], w[1], up1, 1);
+      swap(w[2], w[3], up1, 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (place[i] >= 0)
+          *reinterpret_cast<uint4*>(static_cast<OutT*>(p.out) + (size_t)place[i] * D + c +
+                                    8 * (lane & 3)) = w[i];
     }
+    const bool odd = !empty && (z.x != z.x || z.y != z.y);
     if (__any_sync(kFull, odd && valid) && lane == 0) {
       const int at = atomicAdd(&sm.redo_n[qt], 1);
-      if (at < kRedo) sm.redo[qt][at] = k;
+      if (at < kRedo) sm.redo[qt][at] = x.k;
     }
     tc::fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.o_free[qt]);
-    ++nit;
   }
   if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
   // every warp of the tile leaves the loop here, whatever it met, and sees the others'
@@ -1086,8 +1156,8 @@ __global__ void __launch_bounds__(mod_threads(kFP8), 1)
   const int total = sm.seq_start[p.num_seqs] * p.num_kv_heads;
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(kFP8)));
-    if (warp == kWarpMma)
-      mods_issuer<QT, kFP8, kMods, D>(p, sm, tmem, total);
+    if (warp < kWarpTma)
+      mods_issuer<QT, kFP8, kMods, D>(p, sm, tmem, total, __shfl_sync(kFull, warp - kWarpMma, 0));
     else if (warp < kWarpTma + mod_producers(kFP8))
       mods_producer<kFP8, kMods, D>(p, sm, tm_k, tm_v, tm_q, kv_rows, total, warp - kWarpTma);
     else if constexpr (kFP8)
