@@ -3,35 +3,43 @@
 // interval of visible keys per query row (score_mods.cuh).  The mathematics and
 // the layouts are those of prefill_tc.cuh; what differs:
 //
-//  * The plain kernel's softmax (one thread per row, 128 scores in registers, two
-//    warps per scheduler that take turns with their MMAs) is bound by the latency of
-//    its own instructions, not by a pipe (ncu, a cap of 50 on the mixed batch's
-//    chunks: no pipe above 34 %), so what it costs to modify a score is instructions
-//    and registers: one kernel per set of modifiers, scores modified in place (the
-//    exponentials' code stands once), and the two softmax warpgroups take over the
-//    registers that issuer and producers do not need.  Two threads per row, which
-//    exchange their maxima, were slower (cap 145 -> 179 us: 96 registers spill, and
-//    the exchange is a barrier per tile); so was reading the scores twice from TMEM to
-//    hold fewer (120 against 93 us with the modifiers off).
-//  * An item (two query tiles of whole tokens) walks the key tiles from its first
-//    row's first key to its last row's last one; blocks before and behind those are
-//    not read.  A tile that every row of a warp sees is not masked; one that none sees
-//    costs no exponentials, only zeros for P.
+//  * What a modified score costs is instructions of the softmax (one thread per row, two
+//    warps per scheduler), whose code is long and fetched anew at each step; so there is
+//    one kernel per set of modifiers, scores are modified in place (the exponentials' code
+//    stands once), and a step is 64 keys, half of a loaded tile.  Four warps per scheduler,
+//    two per row with 32 keys each and their maxima exchanged, were slower (a cap on the
+//    mixed batch's chunks 122 against 110 us), and so were steps of 128 keys (124).
+//  * A query tile has two score buffers, so that its softmax has the next step's scores at
+//    hand, and an issuer of its own (both from one: cap 128, packed documents 171 against
+//    124 us; an issuer's single thread needs 1500 cycles for a tile's step).  Score MMAs of
+//    64 keys take nearly as long as of 128; that is what bounds the kernel without
+//    modifiers (91 us on the chunks; the plain kernel's 128-key MMAs 83).
+//  * An item (two query tiles of whole tokens) walks the keys from its first row's first
+//    one to its last row's last one; blocks before and behind those are not read.  A
+//    step that every row of a warp sees is not masked; one that none sees costs no
+//    exponentials, only zeros for P.
 //  * A running CTA takes over the next item not launched yet instead of owning a fixed
-//    share.
+//    share.  Items are short (the packed documents': 11 steps), so what each costs once
+//    counts: one warp makes them ahead of the others, and four lanes gather 64 bytes of a
+//    row before they store (167 -> 124 us for the documents, with the steps above).
 //  * A distance bias grows towards the query, so the running max would move, and O
-//    be rescaled, at nearly every tile of a walk towards it; those kernels walk the
-//    tiles from the last one back.
+//    be rescaled, at nearly every step of a walk towards it; those kernels walk from the
+//    last key back.
 //  * A key hidden from a row has weight zero, but in the product 0 * inf is NaN: a
 //    row whose output is not finite is computed again from its own keys alone, in
 //    fp32, after the main loop, so that a hidden infinity never reaches it.  Finite
 //    inputs never take that path.
-//  * E4M3 caches: six more warps turn each K or V tile into the query's 16-bit type
+//  * E4M3 caches: five more warps turn each K or V tile into the query's 16-bit type
 //    (exactly) where it lands, once for both query tiles, and everything
 //    behind is as for 16-bit caches: no rounding but theirs, and no pass over the query.
 //    8-bit products instead need the query and P as two E4M3 terms each to be as good
 //    (one term of P alone is 2 % of the output's norm), and that splitting is on the
 //    softmax warps: 211 us against 132 for the same prompts on a 16-bit cache.
+//
+// Measured (cold caches, kernel and launch): window 1024 and cap 50 on 4 chunks of 512
+// behind 2048 tokens, 32 query heads, 8 KV heads, 63 us (540 TFLOP/s of the visible
+// products); documents packed into 8191 tokens with a bias 124 us (650); six prompts with
+// two-way prefixes on an E4M3 cache 138 us (655).
 #ifndef PKV_PREFILL_MODS_CUH
 #define PKV_PREFILL_MODS_CUH
 
@@ -76,11 +84,12 @@ constexpr int kConverters = 5;
 constexpr int mod_producers(bool fp8) { return fp8 ? 1 : 2; }
 constexpr int mod_extra(bool fp8) { return mod_producers(fp8) + (fp8 ? kConverters : 0); }
 constexpr int mod_threads(bool fp8) { return 32 * (kSoftWarps + kIssuers + mod_extra(fp8)); }
-// Registers per thread: the launch gives 168 to each of 384 threads, 128 to each of
-// 512; the two softmax warpgroups take over what the others (issuer and producers)
-// return.
-constexpr int soft_regs(bool fp8) { return fp8 ? 192 : 208; }
-constexpr int other_regs(bool fp8) { return fp8 ? 64 : 80; }
+// Registers per thread: the launch gives 168 to each of 384 threads, enough for all, and
+// 128 to each of 512 (E4M3 caches), of which the two softmax warpgroups take over what
+// the others return.  (Stated for both: without, the compiler lays the 16-bit kernels out
+// 3 % slower.)
+constexpr int soft_regs(bool fp8) { return fp8 ? 152 : 168; }
+constexpr int other_regs(bool fp8) { return fp8 ? 104 : 168; }
 constexpr int launch_regs(bool fp8) { return fp8 ? 128 : 168; }
 constexpr bool regs_fit(bool fp8) {
   return 32 * kSoftWarps * soft_regs(fp8) + (mod_threads(fp8) - 32 * kSoftWarps) * other_regs(fp8) <=
@@ -308,10 +317,10 @@ __device__ __forceinline__ float absmax3(float a, float b, float c) {
 // c = a / C: the polynomial of tanh with the scales folded into its coefficients, five
 // operations on packed pairs and no exponential beside the softmax's own.  Otherwise
 // C - 2 C / (2^(2 c log2(e) s) + 1): two more MUFU results per score, off by at most
-// 2^-22 C.  The mixed batch's chunks: 118 us with the polynomial (126 with one of degree
-// 9 that holds up to 3/4 of the cap), 160 without, 91 uncapped.  (Folding either into the
-// exponential's argument saves operations, but has the code of the exponentials twice:
-// 145 us against 130, the difference waiting for instructions.)
+// 2^-22 C.  The mixed batch's chunks: 109 us with the polynomial, 147 without, 91
+// uncapped.  (One of degree 9 that holds up to 3/4 of the cap took 8 us more; folding
+// either into the exponential's argument saves operations, but has the code of the
+// exponentials twice, and was slower by 15.)
 template <int kMods>
 __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, float a, float slope,
                                                int pos, int k0) {
@@ -761,7 +770,7 @@ __device__ __forceinline__ void widen16(const uint32_t* u, uint4* a, uint4* b) {
   *b = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// Converter cw of six on an E4M3 cache: each tile that has landed, in ring order, from
+// Converter cw of five on an E4M3 cache: each tile that has landed, in ring order, from
 // [128 rows][D B] in the second half of its stage to [D / 64 halves][128 rows][128 B], the
 // V rows past the context as zeros; all with the 128-byte swizzle, but for the 64-byte
 // rows of D = 64, which land as they are.  Row r of the codes lies where row r of the
@@ -1197,9 +1206,8 @@ int launch_mods(const AttnParams& p, int total_q, cudaStream_t stream) {
   cudaFuncAttributes fa;
   if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
   if (fa.numRegs != launch_regs(kFP8)) return PKV_ERR_CUDA;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return PKV_ERR_CUDA;
+  static std::atomic<unsigned long long> configured{0};
+  if (!smem_once(kern, smem, configured)) return PKV_ERR_CUDA;
   // launches of at most kMaxSeqs sequences each; their query rows stay absolute
   for (int s0 = 0; s0 < p.num_seqs; s0 += kMaxSeqs) {
     AttnParams c = p;
