@@ -470,7 +470,9 @@ int pkv_rotary_and_cache(void* q_out, const void* q, const void* k, const void* 
                          uint32_t* device_errors, void* stream);
 
 /*
- * Attention with modified scores and key intervals.  With s = scale * q . k of
+ * Attention with modified scores and key intervals (these two calls, the step maps and
+ * the rotary positions above have no counterpart in the source pages; the models that
+ * the pages' serving engines run need them next to the paged cache).  With s = scale * q . k of
  * a query at position pos and a key at position j:
  *   softcap > 0         s becomes softcap * tanh(s / softcap)
  *   alibi_slopes        s becomes s - alibi_slopes[h] * |pos - j|; [num_heads]
@@ -492,6 +494,8 @@ int pkv_rotary_and_cache(void* q_out, const void* q, const void* k, const void* 
  * sequence may have returned the blocks behind its window).
  * NULL / zero members switch a modifier off; a NULL struct switches all off.
  * In these calls out must not overlap q or the caches (PKV_ERR_INVALID_ARG).
+ * On E4M3 caches the softmax weights keep 16-bit precision: the decode call rounds
+ * them to two E4M3 terms (2^-8 relative, as bf16), the prefill call to the query's type.
  */
 typedef struct {
   float softcap;

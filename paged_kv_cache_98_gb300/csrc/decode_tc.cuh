@@ -59,7 +59,11 @@
 // E4M3 terms, p = hi + lo, in separate rows of the same MMA (its N side was half
 // empty): one term alone is good to 2^-4, 2 % of the output's norm, both to 2^-8,
 // as bf16; and the query's scale is a power of two, so that hi + lo holds a bf16
-// query exactly.
+// query exactly.  Bound by HBM on 16-bit caches, as the plain form: 32 sequences with a
+// cap and a window of 4096 keys, 478 MB, take 85 us with the merge (5 us), 5.6 TB/s.  8
+// sequences of 100,000 and more E4M3 keys, 232 MB from their rows' first keys on, take 52
+// us, 4.5 TB/s: half the bytes per key leave the softmax, with a cap and two terms, to
+// bound it (DRAM at 57 %, two of nine stalled warps waiting for instructions).
 
 #ifndef PKV_DECODE_TC_CUH
 #define PKV_DECODE_TC_CUH

@@ -13,9 +13,12 @@
 // bytes per sequence out of L2) instead of waiting for another CTA or a second
 // launch; then warps copy table rows and threads fill tokens.  Nothing read is
 // written in the same launch: the request tables are read below have_s and
-// written from have_s on, so CTAs need no order among themselves.  Bound by the
-// launch and that prefix pass for small batches, by the copied bytes for large
-// ones.
+// written from have_s on, so CTAs need no order among themselves.
+//
+// Bound by the launch and the latency of that prefix pass (its loads, then the copies
+// that wait for the sums), not by its bytes: 9.3 us in a graph for 8 decode rows, 11.4 us
+// for 1000 mixed sequences with 3.4 MB of tables (0.5 us of traffic).  Four sequences per
+// thread, so that 1000 take one round: 13.4 us with one.
 
 #include "common.cuh"
 #include "launch.h"
