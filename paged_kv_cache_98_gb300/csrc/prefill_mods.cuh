@@ -10,10 +10,11 @@
 //    two per row with 32 keys each and their maxima exchanged, were slower (a cap on the
 //    mixed batch's chunks 122 against 110 us), and so were steps of 128 keys (124).
 //  * A query tile has two score buffers, so that its softmax has the next step's scores at
-//    hand, and an issuer of its own (both from one: cap 128, packed documents 171 against
-//    124 us; an issuer's single thread needs 1500 cycles for a tile's step).  Score MMAs of
-//    64 keys take nearly as long as of 128; that is what bounds the kernel without
-//    modifiers (91 us on the chunks; the plain kernel's 128-key MMAs 83).
+//    hand.  Two issuers share the MMAs (all from one: cap 128 against 109, packed documents
+//    171 against 124 us; an issuer's single thread needs 1500 cycles for a tile's step; four
+//    of them slow the softmax beside them: cap 119).  Score MMAs of 64 keys take 72 % of the
+//    time of 128; that and the issuers bound the kernel without modifiers (85 us on the
+//    chunks, as the plain kernel's 83).
 //  * An item (two query tiles of whole tokens) walks the keys from its first row's first
 //    one to its last row's last one; blocks before and behind those are not read.  A
 //    step that every row of a warp sees is not masked; one that none sees costs no
@@ -21,7 +22,7 @@
 //  * A running CTA takes over the next item not launched yet instead of owning a fixed
 //    share.  Items are short (the packed documents': 11 steps), so what each costs once
 //    counts: one warp makes them ahead of the others, and four lanes gather 64 bytes of a
-//    row before they store (167 -> 124 us for the documents, with the steps above).
+//    row before they store (134 -> 124 us for the documents).
 //  * A distance bias grows towards the query, so the running max would move, and O
 //    be rescaled, at nearly every step of a walk towards it; those kernels walk from the
 //    last key back.
@@ -38,7 +39,7 @@
 //
 // Measured (cold caches, kernel and launch): window 1024 and cap 50 on 4 chunks of 512
 // behind 2048 tokens, 32 query heads, 8 KV heads, 63 us (540 TFLOP/s of the visible
-// products); documents packed into 8191 tokens with a bias 124 us (650); six prompts with
+// products); documents packed into 8191 tokens with a bias 126 us (640); six prompts with
 // two-way prefixes on an E4M3 cache 138 us (655).
 #ifndef PKV_PREFILL_MODS_CUH
 #define PKV_PREFILL_MODS_CUH
@@ -76,7 +77,15 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
 
 constexpr int kTileWarps = 4;  // softmax warps of a query tile
 constexpr int kSoftWarps = 2 * kTileWarps;
-constexpr int kIssuers = 2;  // one per query tile
+constexpr int kIssuers = 2;
+// What the issuers share out: scores and products of both query tiles, or the query
+// tiles.  By role, the products' order keeps the two softmax warpgroups in step; that
+// suits them while they are not bound by the pipes they share (the mixed batch's chunks
+// without modifiers 85 us against 91, with a bias 88 against 101; short items as the
+// packed documents' 126 against 124), not with a cap (118 against 109; with a bias, too,
+// 130 against 126) or where converter warps work beside them (E4M3 prompts 142 against
+// 138).
+constexpr bool by_role(bool fp8, int mods) { return !fp8 && (mods & kModCap) == 0; }
 constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + kIssuers;
 // Warps beside softmax and issuers, and threads of the CTA: two producers, or (E4M3
 // caches) one and five that convert its tiles.
@@ -317,7 +326,7 @@ __device__ __forceinline__ float absmax3(float a, float b, float c) {
 // c = a / C: the polynomial of tanh with the scales folded into its coefficients, five
 // operations on packed pairs and no exponential beside the softmax's own.  Otherwise
 // C - 2 C / (2^(2 c log2(e) s) + 1): two more MUFU results per score, off by at most
-// 2^-22 C.  The mixed batch's chunks: 109 us with the polynomial, 147 without, 91
+// 2^-22 C.  The mixed batch's chunks: 109 us with the polynomial, 147 without, 85
 // uncapped.  (One of degree 9 that holds up to 3/4 of the cap took 8 us more; folding
 // either into the exponential's argument saves operations, but has the code of the
 // exponentials twice, and was slower by 15.)
@@ -497,19 +506,20 @@ __device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem<kFP8>&
 }
 
 // Barriers, tensor memory, and the per-sequence tables; ends with the CTA synchronised.
-template <bool kFP8>
+template <bool kFP8, int kMods>
 __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem<kFP8>& sm, const CUtensorMap& tm_k,
                                            const CUtensorMap& tm_v, const CUtensorMap& tm_q) {
   constexpr int kModThreads = mod_threads(kFP8);
+  constexpr int kUsers = by_role(kFP8, kMods) ? 1 : 2;  // issuers that give back K, V, Q and tail
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.full[s], kFP8 ? kConverters : mod_producers(false));
-      mbar_init(&sm.empty[s], kIssuers);
+      mbar_init(&sm.empty[s], kUsers);
       mbar_init(&sm.staged[s], 1);
     }
     mbar_init(&sm.q_full, 1);
-    mbar_init(&sm.q_empty, kIssuers);
+    mbar_init(&sm.q_empty, kUsers);
     for (int x = 0; x < 2; ++x) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(&sm.s_ready[x][b], 1);
@@ -526,7 +536,7 @@ __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem<kFP8>& s
     }
     mbar_init(&sm.answer_full, 1);
     mbar_init(&sm.tail_full, 1);
-    mbar_init(&sm.tail_free, kIssuers);
+    mbar_init(&sm.tail_free, kUsers);
     sm.abort = 0;
     fence_barrier_init();
   }
@@ -836,108 +846,230 @@ __device__ __forceinline__ void mods_converter(const AttnParams& p, ModSmem<true
   if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
 }
 
-// MMA issuer of query tile qt, one thread.  The tile has two score buffers, so that its
-// softmax has the next step's scores at hand: the scores of step v follow the product of
-// step v - 2, which frees their buffer.  One issuer for both query tiles was the
-// bottleneck: 1500 cycles per tile and step, of which the products take a third.
+// MMA issuers, one thread each.  A query tile has two score buffers, so that its softmax
+// has the next step's scores at hand; scores of step v go where P of step v - 2 was,
+// behind its product.  (One issuer for all was the bottleneck: 1500 cycles for a query
+// tile's step, most of them waits, commits and their latencies, not MMAs.)
+//
+// By role: the scores of both query tiles.
 template <class QT, bool kFP8, int kMods, int D>
-__device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem<kFP8>& sm, uint32_t tmem,
-                                            int total, int qt) {
+__device__ __forceinline__ bool issue_all_scores(const AttnParams& p, ModSmem<kFP8>& sm, uint32_t tmem) {
   constexpr uint32_t kAB = std::is_same<QT, BF16>::value ? 1u : 0u;
-  constexpr uint32_t kIdescS = tc::idesc_f16(kAB, 0, 0, 128, kStepKeys);
-  constexpr uint32_t kIdescO = tc::idesc_f16(kAB, 0, 1, 128, D);
+  constexpr uint32_t kIdesc = tc::idesc_f16(kAB, 0, 0, 128, kStepKeys);
   constexpr uint64_t kStage = kTileBytes >> 4;          // in descriptor units
   constexpr uint64_t kInTile = (kStepKeys * 128) >> 4;  // a tile's second half of keys
   constexpr int kBack = (kMods & kModBias) != 0;
   static_assert((kStages & (kStages - 1)) == 0, "ring positions wrap");
-  if (tc::elect_one()) {
-    volatile int* abort = &sm.abort;
-    const unsigned long long lim = wait_limit(p);
-    const uint64_t dq = tc::smem_desc(smem_u32(&sm.q[qt][0]), 16, 1024, tc::kLayoutSw128);
-    const uint64_t dk = tc::smem_desc(smem_u32(&sm.ring[0][0]), 16, 1024, tc::kLayoutSw128);
-    const uint64_t dv = tc::smem_desc(smem_u32(&sm.ring[0][0]), kHalf, 1024, tc::kLayoutSw128);
-    const uint64_t dtail =
-        tc::smem_desc(smem_u32(&sm.tail[0]), kTailBytes / 2, 1024, tc::kLayoutSw128);
-    const uint32_t s_col = tmem + qt * 128, o_col = tmem + kColO + qt * 128;
-    uint32_t at_k = 0, at_v = 1;  // ring positions of the scores' K and the products' V tile
-    uint32_t ns = 0, np = 0;      // score steps issued, P consumed
-    uint32_t nit = 0, nitem = 0, ntail = 0;  // items with steps of this tile, items, tails
-    bool ok = true;
-    ModItem x;
-    for (uint32_t n = 0; ok; ++n) {
-      ok = take_item<true>(sm, n, x, abort, lim);
-      if (!ok || x.k < 0) break;
-      if (x.nk == 0) continue;
-      const int steps = x.nh - x.h0, last = qt ? x.last[1] : x.last[0];
-      const int tail_half = x.tail_step >= 0 ? x.nh - 1 : -1;
-      int hs = half_of<kMods>(x, 0), hp = hs;  // halves of the scores' and the products' step
-      bool new_k = true, new_v = true;         // their tile has not been waited for
-      // scores of step v
-      auto scores = [&](int v) -> bool {
-        if (new_k) {
-          if (!wait_for(&sm.full[at_k % kStages], (at_k / kStages) & 1, abort, lim)) return false;
-          tc::fence_after_sync();
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  const uint64_t dq[2] = {tc::smem_desc(smem_u32(&sm.q[0][0]), 16, 1024, tc::kLayoutSw128),
+                          tc::smem_desc(smem_u32(&sm.q[1][0]), 16, 1024, tc::kLayoutSw128)};
+  const uint64_t dk = tc::smem_desc(smem_u32(&sm.ring[0][0]), 16, 1024, tc::kLayoutSw128);
+  uint32_t at = 0, ns[2] = {0, 0}, nitem = 0;  // ring position of the K tile, steps issued, items
+  ModItem x;
+  for (uint32_t n = 0;; ++n) {
+    if (!take_item<true>(sm, n, x, abort, lim)) return false;
+    if (x.k < 0) return true;
+    if (x.nk == 0) continue;
+    const int steps = x.nh - x.h0, last[2] = {x.last[0], x.last[1]};
+    int half = half_of<kMods>(x, 0);
+    bool fresh = true;  // the step's tile has not been waited for
+    if (!wait_for(&sm.q_full, nitem & 1, abort, lim)) return false;
+#pragma unroll 1
+    for (int v = 0; v < steps; ++v) {
+      if (fresh && !wait_for(&sm.full[at % kStages], (at / kStages) & 1, abort, lim)) return false;
+#pragma unroll
+      for (int qt = 0; qt < 2; ++qt) {
+        if (v > last[qt]) continue;
+        const uint32_t b = ns[qt] & 1;
+        if (ns[qt] >= 2 && !wait_for(&sm.o_done[qt][b], ((ns[qt] >> 1) - 1) & 1, abort, lim))
+          return false;
+        ++ns[qt];
+        tc::fence_after_sync();
+        issue_mods_scores<D>(tmem + qt * 128 + b * kStepKeys, dq[qt],
+                             dk + (at % kStages) * kStage + (half & 1) * kInTile, kIdesc);
+        tc::mma_commit(&sm.s_ready[qt][b]);
+      }
+      fresh = v + 1 == steps || (half & 1) != kBack;  // the tile's last step
+      if (fresh) {
+        tc::mma_commit(&sm.empty[at % kStages]);
+        at += 2;
+      }
+      half += kBack ? -1 : 1;
+    }
+    tc::mma_commit(&sm.q_empty);
+    ++nitem;
+  }
+}
+
+// By role: the products of both query tiles.
+template <class QT, bool kFP8, int kMods, int D>
+__device__ __forceinline__ bool issue_all_products(const AttnParams& p, ModSmem<kFP8>& sm, uint32_t tmem) {
+  constexpr uint32_t kAB = std::is_same<QT, BF16>::value ? 1u : 0u;
+  constexpr uint32_t kIdesc = tc::idesc_f16(kAB, 0, 1, 128, D);
+  constexpr uint64_t kStage = kTileBytes >> 4;
+  constexpr uint64_t kInTile = (kStepKeys * 128) >> 4;
+  constexpr int kBack = (kMods & kModBias) != 0;
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  const uint64_t dv = tc::smem_desc(smem_u32(&sm.ring[0][0]), kHalf, 1024, tc::kLayoutSw128);
+  const uint64_t dtail =
+      tc::smem_desc(smem_u32(&sm.tail[0]), kTailBytes / 2, 1024, tc::kLayoutSw128);
+  uint32_t at = 1, np[2] = {0, 0};        // ring position of the V tile, P consumed
+  uint32_t nit[2] = {0, 0}, ntail = 0;    // items with steps of a query tile, tails
+  ModItem x;
+  for (uint32_t n = 0;; ++n) {
+    if (!take_item<true>(sm, n, x, abort, lim)) return false;
+    if (x.k < 0) return true;
+    if (x.nk == 0) continue;
+    const int steps = x.nh - x.h0, last[2] = {x.last[0], x.last[1]};
+    const int tail_half = x.tail_step >= 0 ? x.nh - 1 : -1;
+    int half = half_of<kMods>(x, 0);
+    bool fresh = true;
+#pragma unroll 1
+    for (int v = 0; v < steps; ++v) {
+      if (fresh && !wait_for(&sm.full[at % kStages], (at / kStages) & 1, abort, lim)) return false;
+      if (half == tail_half && !wait_for(&sm.tail_full, ntail & 1, abort, lim)) return false;
+#pragma unroll
+      for (int qt = 0; qt < 2; ++qt) {
+        if (v > last[qt]) continue;
+        const uint32_t b = np[qt] & 1;
+        if (!wait_for(&sm.p_ready[qt][b], (np[qt] >> 1) & 1, abort, lim)) return false;
+        if (v == 0 && nit[qt] > 0 && !wait_for(&sm.o_free[qt], (nit[qt] - 1) & 1, abort, lim))
+          return false;  // the previous item's O has been read out
+        ++np[qt];
+        tc::fence_after_sync();
+        issue_mods_pv(tmem + kColO + qt * 128, tmem + qt * 128 + b * kStepKeys,
+                      dv + (at % kStages) * kStage + (half & 1) * kInTile, dtail,
+                      half == tail_half ? x.tail_step & 3 : -1, v != 0, kIdesc);
+        tc::mma_commit(&sm.o_done[qt][b]);
+      }
+      fresh = v + 1 == steps || (half & 1) != kBack;
+      if (fresh) {
+        tc::mma_commit(&sm.empty[at % kStages]);
+        at += 2;
+      }
+      half += kBack ? -1 : 1;
+    }
+    if (x.tail_step >= 0) {
+      tc::mma_commit(&sm.tail_free);
+      ++ntail;
+    }
+    nit[0] += last[0] >= 0;
+    nit[1] += last[1] >= 0;
+  }
+}
+
+// By query tile: scores and products of tile qt.  (qt is the same in every lane by a
+// shuffle: MMA operands that the compiler takes for different ones come out wrong.)
+template <class QT, bool kFP8, int kMods, int D>
+__device__ __forceinline__ bool issue_tile(const AttnParams& p, ModSmem<kFP8>& sm, uint32_t tmem, int qt) {
+  constexpr uint32_t kAB = std::is_same<QT, BF16>::value ? 1u : 0u;
+  constexpr uint32_t kIdescS = tc::idesc_f16(kAB, 0, 0, 128, kStepKeys);
+  constexpr uint32_t kIdescO = tc::idesc_f16(kAB, 0, 1, 128, D);
+  constexpr uint64_t kStage = kTileBytes >> 4;
+  constexpr uint64_t kInTile = (kStepKeys * 128) >> 4;
+  constexpr int kBack = (kMods & kModBias) != 0;
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  const uint64_t dq = tc::smem_desc(smem_u32(&sm.q[qt][0]), 16, 1024, tc::kLayoutSw128);
+  const uint64_t dk = tc::smem_desc(smem_u32(&sm.ring[0][0]), 16, 1024, tc::kLayoutSw128);
+  const uint64_t dv = tc::smem_desc(smem_u32(&sm.ring[0][0]), kHalf, 1024, tc::kLayoutSw128);
+  const uint64_t dtail =
+      tc::smem_desc(smem_u32(&sm.tail[0]), kTailBytes / 2, 1024, tc::kLayoutSw128);
+  const uint32_t s_col = tmem + qt * 128, o_col = tmem + kColO + qt * 128;
+  uint32_t at_k = 0, at_v = 1;  // ring positions of the scores' K and the products' V tile
+  uint32_t ns = 0, np = 0;      // score steps issued, P consumed
+  uint32_t nit = 0, nitem = 0, ntail = 0;  // items with steps of this tile, items, tails
+  bool ok = true;
+  ModItem x;
+  for (uint32_t n = 0; ok; ++n) {
+    ok = take_item<true>(sm, n, x, abort, lim);
+    if (!ok || x.k < 0) break;
+    if (x.nk == 0) continue;
+    const int steps = x.nh - x.h0, last = qt ? x.last[1] : x.last[0];
+    const int tail_half = x.tail_step >= 0 ? x.nh - 1 : -1;
+    int hs = half_of<kMods>(x, 0), hp = hs;  // halves of the scores' and the products' step
+    bool new_k = true, new_v = true;         // their tile has not been waited for
+    // scores of step v
+    auto scores = [&](int v) -> bool {
+      if (new_k) {
+        if (!wait_for(&sm.full[at_k % kStages], (at_k / kStages) & 1, abort, lim)) return false;
+        tc::fence_after_sync();
+      }
+      if (v <= last) {
+        const uint32_t b = ns++ & 1;
+        issue_mods_scores<D>(s_col + b * kStepKeys, dq,
+                             dk + (at_k % kStages) * kStage + (hs & 1) * kInTile, kIdescS);
+        tc::mma_commit(&sm.s_ready[qt][b]);
+      }
+      new_k = v + 1 == steps || (hs & 1) != kBack;
+      if (new_k) {  // the tile's last step
+        tc::mma_commit(&sm.empty[at_k % kStages]);
+        at_k += 2;
+      }
+      hs += kBack ? -1 : 1;
+      if (v + 1 == steps) tc::mma_commit(&sm.q_empty);
+      return true;
+    };
+    ok = wait_for(&sm.q_full, nitem & 1, abort, lim);
+    if (ok) tc::fence_after_sync();
+#pragma unroll 1
+    for (int v = -2; ok && v < steps; ++v) {
+      if (v >= 0) {
+        if (new_v) {
+          ok = wait_for(&sm.full[at_v % kStages], (at_v / kStages) & 1, abort, lim);
+          if (!ok) break;
+        }
+        if (hp == tail_half) {
+          ok = wait_for(&sm.tail_full, ntail & 1, abort, lim);
+          if (!ok) break;
         }
         if (v <= last) {
-          const uint32_t b = ns++ & 1;
-          issue_mods_scores<D>(s_col + b * kStepKeys, dq,
-                               dk + (at_k % kStages) * kStage + (hs & 1) * kInTile, kIdescS);
-          tc::mma_commit(&sm.s_ready[qt][b]);
+          const uint32_t b = np & 1;
+          ok = wait_for(&sm.p_ready[qt][b], (np >> 1) & 1, abort, lim);
+          if (ok && v == 0 && nit > 0)  // the previous item's O has been read out
+            ok = wait_for(&sm.o_free[qt], (nit - 1) & 1, abort, lim);
+          if (!ok) break;
+          ++np;
+          tc::fence_after_sync();
+          issue_mods_pv(o_col, s_col + b * kStepKeys,
+                        dv + (at_v % kStages) * kStage + (hp & 1) * kInTile, dtail,
+                        hp == tail_half ? x.tail_step & 3 : -1, v != 0, kIdescO);
+          tc::mma_commit(&sm.o_done[qt][b]);
         }
-        new_k = v + 1 == steps || (hs & 1) != kBack;
-        if (new_k) {  // the tile's last step
-          tc::mma_commit(&sm.empty[at_k % kStages]);
-          at_k += 2;
+        new_v = v + 1 == steps || (hp & 1) != kBack;
+        if (new_v) {
+          tc::mma_commit(&sm.empty[at_v % kStages]);
+          at_v += 2;
         }
-        hs += kBack ? -1 : 1;
-        if (v + 1 == steps) tc::mma_commit(&sm.q_empty);
-        return true;
-      };
-      ok = wait_for(&sm.q_full, nitem & 1, abort, lim);
-      if (ok) tc::fence_after_sync();
-#pragma unroll 1
-      for (int v = -2; ok && v < steps; ++v) {
-        if (v >= 0) {
-          if (new_v) {
-            ok = wait_for(&sm.full[at_v % kStages], (at_v / kStages) & 1, abort, lim);
-            if (!ok) break;
-          }
-          if (hp == tail_half) {
-            ok = wait_for(&sm.tail_full, ntail & 1, abort, lim);
-            if (!ok) break;
-          }
-          if (v <= last) {
-            const uint32_t b = np & 1;
-            ok = wait_for(&sm.p_ready[qt][b], (np >> 1) & 1, abort, lim);
-            if (ok && v == 0 && nit > 0)  // the previous item's O has been read out
-              ok = wait_for(&sm.o_free[qt], (nit - 1) & 1, abort, lim);
-            if (!ok) break;
-            ++np;
-            tc::fence_after_sync();
-            issue_mods_pv(o_col, s_col + b * kStepKeys,
-                          dv + (at_v % kStages) * kStage + (hp & 1) * kInTile, dtail,
-                          hp == tail_half ? x.tail_step & 3 : -1, v != 0, kIdescO);
-            tc::mma_commit(&sm.o_done[qt][b]);
-          }
-          new_v = v + 1 == steps || (hp & 1) != kBack;
-          if (new_v) {
-            tc::mma_commit(&sm.empty[at_v % kStages]);
-            at_v += 2;
-          }
-          hp += kBack ? -1 : 1;
-        }
-        if (v + 2 < steps) ok = scores(v + 2);
+        hp += kBack ? -1 : 1;
       }
-      if (ok && x.tail_step >= 0) {
-        tc::mma_commit(&sm.tail_free);
-        ++ntail;
-      }
-      if (last >= 0) ++nit;
-      ++nitem;
+      if (v + 2 < steps) ok = scores(v + 2);
     }
+    if (ok && x.tail_step >= 0) {
+      tc::mma_commit(&sm.tail_free);
+      ++ntail;
+    }
+    if (last >= 0) ++nit;
+    ++nitem;
+  }
+  return ok;
+}
+
+template <class QT, bool kFP8, int kMods, int D>
+__device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem<kFP8>& sm, uint32_t tmem, int i) {
+  i = __shfl_sync(kFull, i, 0);
+  if (tc::elect_one()) {
+    bool ok;
+    if constexpr (by_role(kFP8, kMods))
+      ok = i == 0 ? issue_all_scores<QT, kFP8, kMods, D>(p, sm, tmem)
+                  : issue_all_products<QT, kFP8, kMods, D>(p, sm, tmem);
+    else
+      ok = issue_tile<QT, kFP8, kMods, D>(p, sm, tmem, i);
     if (!ok) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
-    tc::mma_commit(&sm.mma_done[qt]);
-    mbar_wait(&sm.mma_done[qt], 0, 100000000ull);
+    tc::mma_commit(&sm.mma_done[i]);
+    mbar_wait(&sm.mma_done[i], 0, 100000000ull);
   }
   __syncwarp();
 }
@@ -1160,13 +1292,13 @@ __global__ void __launch_bounds__(mod_threads(kFP8), 1)
   using SM = ModSmem<kFP8>;
   SM& sm = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
-  mods_setup(p, sm, tm_k, tm_v, tm_q);
+  mods_setup<kFP8, kMods>(p, sm, tm_k, tm_v, tm_q);
   const uint32_t tmem = sm.tmem_base;
   const int total = sm.seq_start[p.num_seqs] * p.num_kv_heads;
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(kFP8)));
     if (warp < kWarpTma)
-      mods_issuer<QT, kFP8, kMods, D>(p, sm, tmem, total, __shfl_sync(kFull, warp - kWarpMma, 0));
+      mods_issuer<QT, kFP8, kMods, D>(p, sm, tmem, warp - kWarpMma);
     else if (warp < kWarpTma + mod_producers(kFP8))
       mods_producer<kFP8, kMods, D>(p, sm, tm_k, tm_v, tm_q, kv_rows, total, warp - kWarpTma);
     else if constexpr (kFP8)
