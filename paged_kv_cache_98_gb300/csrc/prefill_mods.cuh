@@ -22,7 +22,7 @@
 //  * A running CTA takes over the next item not launched yet instead of owning a fixed
 //    share.  Items are short (the packed documents': 11 steps), so what each costs once
 //    counts: one warp makes them ahead of the others, and four lanes gather 64 bytes of a
-//    row before they store (134 -> 124 us for the documents).
+//    row before they store (134 -> 120 us for the documents).
 //  * A distance bias grows towards the query, so the running max would move, and O
 //    be rescaled, at nearly every step of a walk towards it; those kernels walk from the
 //    last key back.
@@ -39,7 +39,7 @@
 //
 // Measured (cold caches, kernel and launch): window 1024 and cap 50 on 4 chunks of 512
 // behind 2048 tokens, 32 query heads, 8 KV heads, 63 us (540 TFLOP/s of the visible
-// products); documents packed into 8191 tokens with a bias 126 us (640); six prompts with
+// products); documents packed into 8191 tokens with a bias 120 us (670); six prompts with
 // two-way prefixes on an E4M3 cache 138 us (655).
 #ifndef PKV_PREFILL_MODS_CUH
 #define PKV_PREFILL_MODS_CUH
@@ -81,11 +81,14 @@ constexpr int kIssuers = 2;
 // What the issuers share out: scores and products of both query tiles, or the query
 // tiles.  By role, the products' order keeps the two softmax warpgroups in step; that
 // suits them while they are not bound by the pipes they share (the mixed batch's chunks
-// without modifiers 85 us against 91, with a bias 88 against 101; short items as the
-// packed documents' 126 against 124), not with a cap (118 against 109; with a bias, too,
-// 130 against 126) or where converter warps work beside them (E4M3 prompts 142 against
-// 138).
-constexpr bool by_role(bool fp8, int mods) { return !fp8 && (mods & kModCap) == 0; }
+// without modifiers 85 us against 91, with a bias 88 to 92 against 101), not with a cap (118
+// against 109; with a bias, too, 130 against 126) or where converter warps work beside
+// them (E4M3 prompts 142 against 138), nor in the short items that first keys leave
+// (packed documents 123 against 116), where the query tiles differ in length.
+template <bool kFP8, int kMods>
+__device__ __forceinline__ bool by_role(const AttnParams& p) {
+  return !kFP8 && (kMods & kModCap) == 0 && p.key_start == nullptr;
+}
 constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + kIssuers;
 // Warps beside softmax and issuers, and threads of the CTA: two producers, or (E4M3
 // caches) one and five that convert its tiles.
@@ -510,16 +513,16 @@ template <bool kFP8, int kMods>
 __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem<kFP8>& sm, const CUtensorMap& tm_k,
                                            const CUtensorMap& tm_v, const CUtensorMap& tm_q) {
   constexpr int kModThreads = mod_threads(kFP8);
-  constexpr int kUsers = by_role(kFP8, kMods) ? 1 : 2;  // issuers that give back K, V, Q and tail
+  const int users = by_role<kFP8, kMods>(p) ? 1 : 2;  // issuers that give back K, V, Q and tail
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.full[s], kFP8 ? kConverters : mod_producers(false));
-      mbar_init(&sm.empty[s], kUsers);
+      mbar_init(&sm.empty[s], users);
       mbar_init(&sm.staged[s], 1);
     }
     mbar_init(&sm.q_full, 1);
-    mbar_init(&sm.q_empty, kUsers);
+    mbar_init(&sm.q_empty, users);
     for (int x = 0; x < 2; ++x) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(&sm.s_ready[x][b], 1);
@@ -536,7 +539,7 @@ __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem<kFP8>& s
     }
     mbar_init(&sm.answer_full, 1);
     mbar_init(&sm.tail_full, 1);
-    mbar_init(&sm.tail_free, kUsers);
+    mbar_init(&sm.tail_free, users);
     sm.abort = 0;
     fence_barrier_init();
   }
@@ -1062,7 +1065,7 @@ __device__ __forceinline__ void mods_issuer(const AttnParams& p, ModSmem<kFP8>& 
   i = __shfl_sync(kFull, i, 0);
   if (tc::elect_one()) {
     bool ok;
-    if constexpr (by_role(kFP8, kMods))
+    if (by_role<kFP8, kMods>(p))
       ok = i == 0 ? issue_all_scores<QT, kFP8, kMods, D>(p, sm, tmem)
                   : issue_all_products<QT, kFP8, kMods, D>(p, sm, tmem);
     else
