@@ -60,10 +60,12 @@
 // empty): one term alone is good to 2^-4, 2 % of the output's norm, both to 2^-8,
 // as bf16; and the query's scale is a power of two, so that hi + lo holds a bf16
 // query exactly.  Bound by HBM on 16-bit caches, as the plain form: 32 sequences with a
-// cap and a window of 4096 keys, 478 MB, take 85 us with the merge (5 us), 5.6 TB/s.  8
-// sequences of 100,000 and more E4M3 keys, 232 MB from their rows' first keys on, take 52
-// us, 4.5 TB/s: half the bytes per key leave the softmax, with a cap and two terms, to
-// bound it (DRAM at 57 %, two of nine stalled warps waiting for instructions).
+// cap and a window of 4096 keys, 478 MB, take 85 us with the merge (5 us), 5.6 TB/s.  The
+// modifiers add nothing to a call of this size (8 sequences of 28,672 E4M3 keys, from cold
+// caches: 107 us plain, 107 with a cap); what keeps a smaller one below that rate is what
+// any has, its start, its last partitions and the merge: 8 sequences of 100,000 and more
+// E4M3 keys, 232 MB from their rows' first keys on, 52 us.  Three contexts of up to 700
+// keys, all latency, 13.5 us in a graph (15.5 with cap and bias element by element).
 
 #ifndef PKV_DECODE_TC_CUH
 #define PKV_DECODE_TC_CUH
@@ -959,6 +961,7 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     using OutT = typename QT::T;
     const float qs = p.q_scale;
+    const float icap = kMods && p.softcap > 0.0f ? 1.0f / p.cap_log2 : 0.0f;
     // rows of sequences without context get zeros when no merge follows
     if (!split) {
       for (int s = cta; s < p.num_rows; s += ncta) {
@@ -1070,32 +1073,48 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
 #pragma unroll
       for (int h = 0; h < kH; ++h) mx[h] = -INFINITY;
       if constexpr (kMods) {
-        // modified scores in base-2 units, tile by tile; the modifiers' tests are
-        // uniform over the launch
-        const float icap = p.softcap > 0.0f ? 1.0f / p.cap_log2 : 0.0f;
-        float slope[kH];
+        // modified scores in base-2 units (the modifiers' tests are uniform over the launch);
+        // tiles past the item's are left out at their end
+        auto each = [&](auto f) {
 #pragma unroll
-        for (int h = 0; h < kH; ++h)
-          slope[h] = p.alibi && h < p.group ? __ldg(p.alibi + cur.kvh * p.group + h) * kLog2e : 0.0f;
-        // distance of this thread's first key from the query, the context's last token
-        const int dist0 =
-            (cur.nparts - 1 - cur.part) * kPart + last_len(sm.seq_pack[cur.seq]) - 1 - tid;
+          for (int t = 0; t < kTilesPerPart; ++t)
+            if (t < cur.ntiles) {
 #pragma unroll
-        for (int t = 0; t < kTilesPerPart; ++t) {
-          if (t < cur.ntiles) {
-            const int key = t * kTileKeys + tid;
-            const bool valid = key < cur.n && key >= cur.front;
-            const float dist = (float)(dist0 - t * kTileKeys);
-#pragma unroll
-            for (int h = 0; h < kH; ++h) {
-              float x = s[t][h] * (FP8 ? qsh[h] : qs);
-              if (p.softcap > 0.0f) x = p.cap_log2 * cap_tanh(x * icap);
-              if (p.alibi) x = fmaf(-slope[h], dist, x);
-              s[t][h] = valid ? x : -INFINITY;
-              mx[h] = fmaxf(mx[h], s[t][h]);
+              for (int h = 0; h < kH; ++h) f(t, h, s[t][h]);
             }
+        };
+        each([&](int, int h, float& x) { x *= FP8 ? qsh[h] : qs; });
+        if (p.softcap > 0.0f) {
+          float top = 0.0f;
+          each([&](int, int, float& x) { top = fmaxf(top, fabsf(x)); });
+          // where all scores of the warp stay below half the cap, the usual case, tanh's
+          // polynomial with the cap folded into its coefficients, x (1 + k3 x^2 + ...)
+          if (__all_sync(kFull, top * icap <= kTanhPoly && icap <= 16.0f)) {
+            const float i2 = icap * icap, k3 = kTanh3 * i2, k5 = kTanh5 * i2 * i2,
+                        k7 = kTanh7 * i2 * i2 * i2;
+            each([&](int, int, float& x) {
+              const float u = x * x;
+              x *= fmaf(u, fmaf(u, fmaf(u, k7, k5), k3), 1.0f);
+            });
+          } else {
+            each([&](int, int, float& x) { x = p.cap_log2 * cap_tanh(x * icap); });
           }
         }
+        if (p.alibi) {
+          float slope[kH];
+#pragma unroll
+          for (int h = 0; h < kH; ++h)
+            slope[h] = h < p.group ? __ldg(p.alibi + cur.kvh * p.group + h) * kLog2e : 0.0f;
+          // distance of this thread's first key from the query, the context's last token
+          const int dist0 =
+              (cur.nparts - 1 - cur.part) * kPart + last_len(sm.seq_pack[cur.seq]) - 1 - tid;
+          each([&](int t, int h, float& x) { x = fmaf(-slope[h], (float)(dist0 - t * kTileKeys), x); });
+        }
+        each([&](int t, int h, float& x) {
+          const int key = t * kTileKeys + tid;
+          x = key < cur.n && key >= cur.front ? x : -INFINITY;
+          mx[h] = fmaxf(mx[h], x);
+        });
       } else {
 #pragma unroll
       for (int t = 0; t < kTilesPerPart; ++t) {
