@@ -615,6 +615,29 @@ def test_decode_wait_runs_out(kw):
     assert pkv.check_errors(err) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(dtype="fp16", D=64), dict(window=300), dict(alibi=True), dict(softcap=60.0),
+                                dict(kv="e4m3"), dict(starts=lambda s, p: p - p % 200)])
+def test_prefill_large_scores(kw):
+    """Scores of hundreds, whose running maximum moves at many steps."""
+    run(Batch(83, [(150, 900), (70, 330)], H=8, hkv=2, spread=12.0, **kw), whole=False)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(alibi=True, dtype="fp16"), dict(window=90), dict(D=64, alibi=True), dict(softcap=20.0),
+    dict(softcap=20.0, alibi=True, D=64), dict(starts=lambda s, p: p - p % 50), dict(kv="e4m3"),
+    dict(prefix=[(7 * s) % 90 for s in range(60)])],
+    ids=lambda k: "-".join(k) or "keys")
+def test_prefill_more_items_than_processors(kw):
+    """Several hundred items of mixed lengths (empty ones, one key, query tiles that end apart):
+    each processor takes many, one after another."""
+    r = np.random.RandomState(7)
+    seqs = []
+    for s in range(60):
+        n = int(r.randint(0, 40)) if s % 3 else int(r.randint(40, 300 if s % 9 == 0 else 70))
+        seqs.append((n, n + (0 if s % 4 == 0 else int(r.randint(0, 400)))))
+    run(Batch(79, seqs, H=8, hkv=8, **kw))
+
+
 def test_prefill_many_sequences():
     """More sequences than one launch's tables hold."""
     seqs = [(1 + s % 3, 1 + s % 3 + (s * 7) % 50) for s in range(1100)]
