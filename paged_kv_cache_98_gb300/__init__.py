@@ -478,9 +478,11 @@ _HERE_ALREADY = contextlib.nullcontext()
 
 
 def _scratch_on(stream, nbytes, workspace, device):
-    """A workspace of nbytes: the caller's, or one that the launch's stream owns (so
-    that the allocator hands it out again only behind the launch).  `stream` as the
-    caller gave it, None for the current one."""
+    """(workspace of nbytes, its size): the caller's, or one that the launch's stream
+    owns (so that the allocator hands it out again only behind the launch).  `stream`
+    as the caller gave it, None for the current one.  The call holds the tensor until
+    the library has returned: a block freed before the launch may go to another
+    thread's work on the same stream first."""
     if nbytes == 0:
         return None, 0
     if workspace is None:
@@ -493,7 +495,7 @@ def _scratch_on(stream, nbytes, workspace, device):
         raise ValueError("the workspace must be contiguous and on the tensors' device")
     elif stream is not None:
         workspace.record_stream(stream)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def build_step_maps(block_tables, context_lens, query_start_loc, slot_mapping, positions,
@@ -650,7 +652,7 @@ def paged_attention_decode_biased(out, q, k_cache, v_cache, block_tables, contex
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), context_lens.data_ptr(), ctypes.addressof(mods), S, H, hkv, D,
             bs, block_tables.shape[1], nb, max_context_len, scale, _dtype_code(q),
-            _dtype_code(k_cache), k_scale, v_scale, ws, wsb, _ptr(device_errors), raw)
+            _dtype_code(k_cache), k_scale, v_scale, _ptr(ws), wsb, _ptr(device_errors), raw)
     if rc:
         raise PagedKVError("pkv_paged_attention_decode_biased", rc)
     return out

@@ -1,0 +1,62 @@
+"""What the Python binding of the serving-step operators holds and does around a launch,
+shown on the CPU: the library is replaced by one that looks instead of launching."""
+import contextlib
+import weakref
+
+import pytest
+import torch
+
+import paged_kv_cache_98_gb300 as pkv
+
+
+class Watcher:
+    """Stands in for the library: a workspace of `need` bytes, and `launched` called where
+    a kernel would be."""
+
+    def __init__(self, need, launched):
+        self.need, self.launched = need, launched
+
+    def pkv_decode_biased_workspace_size(self, *a):
+        return self.need
+
+    def pkv_paged_attention_decode_biased(self, *a):
+        return self.launched(a) or 0
+
+
+def _decode_args():
+    return dict(out=torch.empty(2, 8, 128, dtype=torch.bfloat16), q=torch.empty(2, 8, 128, dtype=torch.bfloat16),
+                k_cache=torch.empty(4, 2, 16, 128, dtype=torch.bfloat16),
+                v_cache=torch.empty(4, 2, 16, 128, dtype=torch.bfloat16),
+                block_tables=torch.zeros(2, 64, dtype=torch.int32),
+                context_lens=torch.zeros(2, dtype=torch.int32), scale=0.1)
+
+
+@pytest.fixture
+def on_cpu(monkeypatch):
+    """The binding's calls as they run on the GPU, on CPU tensors."""
+    monkeypatch.setattr(pkv, "_stream_on", lambda device, stream, tensors: (7, contextlib.nullcontext()))
+    return monkeypatch
+
+
+def test_decode_workspace_lives_until_the_launch(on_cpu):
+    """The workspace that the call allocates is still the call's own when the kernel is
+    launched: another thread may allocate while the library runs without the
+    interpreter's lock."""
+    made, alive = [], []
+    empty = torch.empty
+
+    def watched(*a, **k):
+        t = empty(*a, **k)
+        made.append((weakref.ref(t), t.data_ptr()))
+        return t
+
+    def launched(args):
+        (ref, ptr), = made
+        alive.append(ref() is not None)
+        assert getattr(args[20], "value", args[20]) == ptr and args[21] == 4096
+
+    t = _decode_args()
+    on_cpu.setattr(pkv, "_lib", Watcher(4096, launched))
+    on_cpu.setattr(torch, "empty", watched)
+    pkv.paged_attention_decode_biased(max_context_len=1024, **t)
+    assert alive == [True]
