@@ -525,7 +525,7 @@ int pkv_paged_attention_decode_biased(void* out, const void* q, const void* k_ca
 
 /*
  * Chunked-prefill attention under pkv_score_mods; other arguments as for
- * pkv_paged_attention_prefill_chunk.
+ * pkv_paged_attention_prefill_chunk (max_q_len only has to be at least 0).
  * No workspace.  Caches of up to 2^31 rows (num_blocks * num_kv_heads * 16) and
  * queries of up to 2^31 heads (total_q * num_heads); PKV_ERR_UNSUPPORTED beyond.
  */

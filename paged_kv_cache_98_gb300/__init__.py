@@ -667,7 +667,8 @@ def paged_attention_prefill_biased(out, q, k_cache, v_cache, block_tables, conte
     """Chunked-prefill attention with capped scores, a distance bias, a sliding
     window, a first key per query row (key_start [total_q] int32: document masks)
     and keys seen in both directions (prefix_lens [S] int32):
-    pkv_paged_attention_prefill_biased."""
+    pkv_paged_attention_prefill_biased.  Without max_context_len a context may be as
+    long as the block table; max_q_len sizes nothing here and may be left out."""
     TQ, H, D = q.shape
     mods, raw, guard = _biased_args(out, q, k_cache, v_cache, block_tables, context_lens,
                                     query_start_loc, softcap, alibi_slopes, window, key_start,
@@ -675,9 +676,9 @@ def paged_attention_prefill_biased(out, q, k_cache, v_cache, block_tables, conte
     nb, hkv, bs, _ = k_cache.shape
     S = context_lens.numel()
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if S else 0
+        max_context_len = min(block_tables.shape[1] * bs, 2**31 - 1)
     if max_q_len is None:
-        max_q_len = int((query_start_loc[1:] - query_start_loc[:-1]).max().item()) if S else 0
+        max_q_len = TQ
     with guard:
         rc = (_lib or load()).pkv_paged_attention_prefill_biased(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),

@@ -60,3 +60,27 @@ def test_decode_workspace_lives_until_the_launch(on_cpu):
     on_cpu.setattr(torch, "empty", watched)
     pkv.paged_attention_decode_biased(max_context_len=1024, **t)
     assert alive == [True]
+
+
+def test_prefill_reads_nothing_back(on_cpu):
+    """Lengths that are left out are bounded by what the host knows: no wait for the GPU
+    (which a capture could not hold)."""
+    seen = {}
+
+    class Prefill:
+        @staticmethod
+        def pkv_paged_attention_prefill_biased(*a):
+            seen.update(seqs=a[8], rows=a[9], max_q_len=a[10], max_context_len=a[17])
+            return 0
+
+    def read(*a, **k):
+        raise AssertionError("a device value was read")
+
+    t = _decode_args()
+    t["query_start_loc"] = torch.tensor([0, 1, 2], dtype=torch.int32)
+    on_cpu.setattr(pkv, "_lib", Prefill())
+    on_cpu.setattr(torch.Tensor, "item", read)
+    pkv.paged_attention_prefill_biased(**t)
+    assert seen == dict(seqs=2, rows=2, max_q_len=2, max_context_len=64 * 16)
+    pkv.paged_attention_prefill_biased(max_context_len=100, **t)
+    assert seen["max_context_len"] == 100
