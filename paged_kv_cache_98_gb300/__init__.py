@@ -643,7 +643,8 @@ def paged_attention_decode_biased(out, q, k_cache, v_cache, block_tables, contex
                                     alibi_slopes, window, key_start, None, device_errors, stream)
     nb, hkv, bs, _ = k_cache.shape
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if S else 0
+        with torch.cuda.stream(stream):  # behind what fills the lengths
+            max_context_len = int(context_lens.max().item()) if S else 0
     lib = _lib or load()
     with guard:
         ws, wsb = _scratch_on(stream, lib.pkv_decode_biased_workspace_size(

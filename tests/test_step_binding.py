@@ -84,3 +84,32 @@ def test_prefill_reads_nothing_back(on_cpu):
     assert seen == dict(seqs=2, rows=2, max_q_len=2, max_context_len=64 * 16)
     pkv.paged_attention_prefill_biased(max_context_len=100, **t)
     assert seen["max_context_len"] == 100
+
+
+def test_decode_reads_lengths_on_the_stream_it_launches_on(on_cpu):
+    """A left-out max_context_len is read behind the work that fills context_lens, which the
+    caller ordered before `stream`, not before the current one."""
+    inside, seen = [], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        inside.append(s)
+        yield
+        inside.pop()
+
+    most = torch.Tensor.max
+
+    def watched(t, *a, **k):
+        seen.append(list(inside))
+        return most(t, *a, **k)
+
+    t = _decode_args()
+    t["context_lens"] += 40
+    on_cpu.setattr(pkv, "_lib", Watcher(0, lambda a: seen.append(a[14])))
+    on_cpu.setattr(torch.cuda, "stream", stream)
+    on_cpu.setattr(torch.Tensor, "max", watched)
+    pkv.paged_attention_decode_biased(stream="side", **t)
+    assert seen == [["side"], 40]
+    seen.clear()
+    pkv.paged_attention_decode_biased(**t)
+    assert seen == [[], 40] or seen == [[None], 40]
