@@ -494,6 +494,7 @@ int pkv_rotary_and_cache(void* q_out, const void* q, const void* k, const void* 
  * sequence may have returned the blocks behind its window).
  * NULL / zero members switch a modifier off; a NULL struct switches all off.
  * In these calls out must not overlap q or the caches (PKV_ERR_INVALID_ARG).
+ * A call without sequences or without query rows does nothing; the arrays of none may be NULL.
  * On E4M3 caches the softmax weights keep 16-bit precision: the decode call rounds
  * them to two E4M3 terms (2^-8 relative, as bf16), the prefill call to the query's type.
  */

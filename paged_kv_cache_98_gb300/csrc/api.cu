@@ -73,6 +73,13 @@ int set_mods(pkv::AttnParams& p, const pkv_score_mods* m, int max_context_len, f
   return PKV_OK;
 }
 
+// Stands in for the address of an array of no elements, which may be null.
+alignas(16) const unsigned char kNothing[16] = {};
+template <class T>
+const T* given(const T* p, bool has_elements) {
+  return p || has_elements ? p : reinterpret_cast<const T*>(kNothing);
+}
+
 // Rows of the biased calls are computed again from q and the caches where an output is
 // not finite, so out must be memory of its own.
 bool out_is_apart(const void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -587,7 +594,9 @@ int pkv_paged_attention_decode_biased(void* out, const void* q, const void* k_ca
                                       pkv_dtype q_dtype, pkv_dtype kv_dtype, float k_scale,
                                       float v_scale, void* workspace, size_t workspace_bytes,
                                       uint32_t* device_errors, void* stream) {
-  int rc = check_attention_args(out, q, k_cache, v_cache, block_tables, context_lens, num_seqs,
+  const bool any = num_seqs != 0;
+  int rc = check_attention_args(given(out, any), given(q, any), k_cache, v_cache,
+                                given(block_tables, any), given(context_lens, any), num_seqs,
                                 num_heads, num_kv_heads, head_dim, block_size,
                                 max_blocks_per_seq, num_blocks, max_context_len, scale, q_dtype,
                                 kv_dtype, k_scale, v_scale);
@@ -632,7 +641,9 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
                                        int num_blocks, int max_context_len, float scale,
                                        pkv_dtype q_dtype, pkv_dtype kv_dtype, float k_scale,
                                        float v_scale, uint32_t* device_errors, void* stream) {
-  int rc = check_attention_args(out, q, k_cache, v_cache, block_tables, context_lens, num_seqs,
+  const bool any = num_seqs != 0, rows = any && total_q != 0;
+  int rc = check_attention_args(given(out, rows), given(q, rows), k_cache, v_cache,
+                                given(block_tables, any), given(context_lens, any), num_seqs,
                                 num_heads, num_kv_heads, head_dim, block_size,
                                 max_blocks_per_seq, num_blocks, max_context_len, scale, q_dtype,
                                 kv_dtype, k_scale, v_scale);

@@ -113,3 +113,22 @@ def test_decode_reads_lengths_on_the_stream_it_launches_on(on_cpu):
     seen.clear()
     pkv.paged_attention_decode_biased(**t)
     assert seen == [[], 40] or seen == [[None], 40]
+
+
+def test_empty_batches_are_nothing_to_do():
+    """No sequences, or sequences without queries: tensors of no elements have no address,
+    and the calls return what they were given."""
+    from paged_kv_cache_98_gb300 import _build
+    _build.build()
+    lib = pkv.load()
+    tail = [8, 2, 128, 16, 4, 8, 64, 0.1, 1, 1, 1.0, 1.0]  # heads .. v_scale
+    kc, vc = 1 << 22, 1 << 23
+    decode = lambda n, head_dim=128: lib.pkv_paged_attention_decode_biased(  # noqa: E731
+        None, None, kc, vc, None, None, None, n, *tail[:2], head_dim, *tail[3:], None, 0, None, None)
+    prefill = lambda n, rows, bt, cl: lib.pkv_paged_attention_prefill_biased(  # noqa: E731
+        None, None, kc, vc, bt, cl, 4096, None, n, rows, 0, *tail, None, None)
+    assert decode(0) == 0
+    assert decode(0, 96) == -2 and decode(1) == -1  # other arguments are still looked at
+    assert prefill(0, 0, None, None) == 0
+    assert prefill(3, 0, 1024, 2048) == 0
+    assert prefill(3, 1, 1024, 2048) == -1 and prefill(3, 0, None, 2048) == -1
