@@ -15,6 +15,9 @@ constexpr int kCascadeChunk = 2048;  // keys per partial of the shared-prefix pa
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// The error word is written by a 32-bit atomic.
+bool aligned_word(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 bool is16bit(int dt) { return dt == PKV_F16 || dt == PKV_BF16; }
 
 int effective_partition(int partition_size, int max_context_len) {
@@ -601,6 +604,7 @@ int pkv_paged_attention_decode_biased(void* out, const void* q, const void* k_ca
                                 max_blocks_per_seq, num_blocks, max_context_len, scale, q_dtype,
                                 kv_dtype, k_scale, v_scale);
   if (rc != PKV_OK) return rc;
+  if (!aligned_word(device_errors)) return PKV_ERR_INVALID_ARG;
   pkv::AttnParams p{};
   rc = set_mods(p, mods, max_context_len, scale, k_scale, kv_dtype);
   if (rc != PKV_OK) return rc;
@@ -648,7 +652,8 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
                                 max_blocks_per_seq, num_blocks, max_context_len, scale, q_dtype,
                                 kv_dtype, k_scale, v_scale);
   if (rc != PKV_OK) return rc;
-  if (!query_start_loc || total_q < 0 || max_q_len < 0) return PKV_ERR_INVALID_ARG;
+  if (!query_start_loc || total_q < 0 || max_q_len < 0 || !aligned_word(device_errors))
+    return PKV_ERR_INVALID_ARG;
   pkv::AttnParams p{};
   rc = set_mods(p, mods, max_context_len, scale, k_scale, kv_dtype);
   if (rc != PKV_OK) return rc;

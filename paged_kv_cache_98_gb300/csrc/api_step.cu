@@ -38,7 +38,8 @@ int pkv_build_step_maps(int32_t* block_tables, int32_t* context_lens, int32_t* q
     return PKV_ERR_INVALID_ARG;
   if (num_tokens > 0 && (!slot_mapping || !positions)) return PKV_ERR_INVALID_ARG;
   if (num_new_blocks > 0 && !new_blocks) return PKV_ERR_INVALID_ARG;
-  if (!aligned(slot_mapping, 8) || !aligned(block_tables, 4) || !aligned(request_tables, 4))
+  if (!aligned(slot_mapping, 8) || !aligned(block_tables, 4) || !aligned(request_tables, 4) ||
+      !aligned(device_errors, 4))
     return PKV_ERR_INVALID_ARG;
   if (block_size != pkv::kBlockSize) return PKV_ERR_UNSUPPORTED;
   if (num_seqs > PKV_STEP_MAPS_MAX_SEQS) return PKV_ERR_UNSUPPORTED;
@@ -129,7 +130,7 @@ int pkv_rotary_and_cache(void* q_out, const void* q, const void* k, const void* 
   if (cache_dtype == PKV_FP8_E4M3 && (!(k_scale > 0.0f) || !(v_scale > 0.0f) ||
                                       !std::isfinite(k_scale) || !std::isfinite(v_scale)))
     return PKV_ERR_INVALID_ARG;
-  if (!inv_freq) return PKV_ERR_INVALID_ARG;
+  if (!inv_freq || !aligned(device_errors, 4)) return PKV_ERR_INVALID_ARG;
   // |t * inv_freq| in turns stays below 2^52, where a double still has a fraction
   for (int i = 0; i < rotary_dim / 2; ++i)
     if (!(std::fabs(inv_freq[i]) <= 1.0e3)) return PKV_ERR_INVALID_ARG;

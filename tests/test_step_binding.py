@@ -1,6 +1,7 @@
 """What the Python binding of the serving-step operators holds and does around a launch,
 shown on the CPU: the library is replaced by one that looks instead of launching."""
 import contextlib
+import ctypes
 import weakref
 
 import pytest
@@ -132,3 +133,22 @@ def test_empty_batches_are_nothing_to_do():
     assert prefill(0, 0, None, None) == 0
     assert prefill(3, 0, 1024, 2048) == 0
     assert prefill(3, 1, 1024, 2048) == -1 and prefill(3, 0, None, 2048) == -1
+
+
+def test_error_words_off_their_alignment_are_refused():
+    """The error word is written by a 32-bit atomic: an address between words would fault."""
+    from paged_kv_cache_98_gb300 import _build
+    _build.build()
+    lib = pkv.load()
+    tail = [2, 8, 2, 128, 16, 4, 8, 64, 0.1, 1, 1, 1.0, 1.0]
+    for word in (4096 + 1, 4096 + 2):
+        assert lib.pkv_paged_attention_decode_biased(
+            1 << 20, 1 << 21, 1 << 22, 1 << 23, 1024, 2048, None, *tail, None, 0, word, None) == -1
+        assert lib.pkv_paged_attention_prefill_biased(
+            1 << 20, 1 << 21, 1 << 22, 1 << 23, 1024, 2048, 3072, None, 2, 6, 4, *tail[1:], word, None) == -1
+        assert lib.pkv_build_step_maps(
+            4096, 8192, 8448, 8704, 8960, 12288, 512, 768, 1024, 1280, 2, 4, 8, 4, 2, 16, 64, word, None) == -1
+        inv = (ctypes.c_double * 64)(*([1.0] * 64))
+        assert lib.pkv_rotary_and_cache(
+            1 << 20, 1 << 22, 1 << 23, 1 << 24, 1 << 25, 1 << 26, 256, 256, ctypes.cast(inv, ctypes.c_void_p),
+            1024, 256, 256, 4, 8, 2, 128, 16, 8, 128, 0, 1.0, 1, 1, 1.0, 1.0, word, None) == -1
