@@ -26,10 +26,10 @@
 //  * A distance bias grows towards the query, so the running max would move, and O
 //    be rescaled, at nearly every step of a walk towards it; those kernels walk from the
 //    last key back.
-//  * A key hidden from a row has weight zero, but in the product 0 * inf is NaN: a
-//    row whose output is not finite is computed again from its own keys alone, in
-//    fp32, after the main loop, so that a hidden infinity never reaches it.  Finite
-//    inputs never take that path.
+//  * A key hidden from a row has weight zero, but in the product 0 * inf is NaN: rows whose
+//    output is not finite are looked at again after the main loop (redo_rows), by the warp
+//    that wrote them, so that a hidden infinity never reaches them.  Finite inputs never
+//    take that path.
 //  * E4M3 caches: five more warps turn each K or V tile into the query's 16-bit type
 //    (exactly) where it lands, once for both query tiles, and everything
 //    behind is as for 16-bit caches: no rounding but theirs, and no pass over the query.
@@ -112,7 +112,11 @@ static_assert(regs_fit(false) && regs_fit(true) && mod_threads(false) == 384 && 
 constexpr int kChunk = 32;  // keys whose weights are packed and stored together
 constexpr int kStepKeys = kTileKeys / 2;  // keys of a step: half a loaded tile
 constexpr int kAhead = 4;   // items made before the slowest warp takes them
-constexpr int kRedo = 64;   // items listed for recomputation; more of them: all items are looked at
+// Items that a softmax warp can list for redo_rows.  A CTA whose list could not take what
+// it has under way and one more leaves the rest of the grid to others: when it asks for
+// item n + 1, its warps have listed items up to n - 2 - kAhead.
+constexpr int kRedo = 32;
+constexpr int kUnderWay = kAhead + 3;
 
 // Two query tiles of a sequence and KV head, and the keys they see.
 struct ModItem {
@@ -158,9 +162,10 @@ struct ModSmem {
   uint64_t item_read[kAhead];
   uint32_t tmem_base;
   int abort;
-  // items with a row that came out not finite, by query tile (a few may be listed twice)
-  int redo_n[2];
-  int redo[2][kRedo];
+  // items with rows that came out not finite, by softmax warp (its rows as bits)
+  int redo_n[kSoftWarps];
+  int redo_item[kSoftWarps][kRedo];
+  uint32_t redo_rows[kSoftWarps][kRedo];
 };
 
 // Loads go through an item's key tiles, kt0 + i being the i-th one (backwards under a
@@ -298,20 +303,6 @@ __device__ __forceinline__ bool take_item(ModSmem<kFP8>& sm, uint32_t n, ModItem
   return true;
 }
 
-// All softmax threads of query tile qt agree on `ok` (named barrier 1 + qt).
-__device__ __forceinline__ bool all_of_tile(bool ok, int qt) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)ok), "r"(1 + qt), "n"(32 * kTileWarps)
-      : "memory");
-  return r != 0;
-}
-
 // Largest magnitude of three values.
 __device__ __forceinline__ float absmax3(float a, float b, float c) {
   float r;
@@ -408,8 +399,8 @@ __device__ __forceinline__ void issue_mods_pv(uint32_t d, uint32_t a, uint64_t d
 }
 
 // One row (a query token's head) from its own keys alone, in fp32 (the plain online
-// softmax, exp2f).  Four lanes share the row, D / 4 dimensions each; gmask is their
-// mask.
+// softmax, exp2f), into those elements of its output that are not finite.  Four lanes
+// share the row, D / 4 dimensions each; gmask is their mask.
 template <class QT, bool kFP8, int D>
 __device__ __forceinline__ void exact_row(const AttnParams& p, int seq, int row, int h, int pos,
                                           int lo, int hi, unsigned gmask) {
@@ -470,41 +461,118 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, int seq, int row,
   const float inv = p.v_scale / l;
   T* op = static_cast<T*>(p.out) + at;
 #pragma unroll
-  for (int d = 0; d < kDims; ++d) store_out(op + d, acc[d] * inv);
+  for (int d = 0; d < kDims; ++d) {
+    const float o = acc[d] * inv;
+    if (fabsf(o) < INFINITY && !(fabsf((float)op[d]) < INFINITY)) store_out(op + d, o);
+  }
 }
 
-// The rows of query tile qt, in the items listed, whose output is not finite, again
-// by exact_row: eight rows at a time per warp, `w` of the tile's.
+// What an element of V is, from its bits: 0 finite, 1 NaN, 2 and 3 the infinities.
+template <class QT, bool kFP8>
+__device__ __forceinline__ int odd_kind(uint32_t bits) {
+  if constexpr (kFP8) {
+    return (bits & 0x7fu) == 0x7fu ? 1 : 0;
+  } else {
+    constexpr uint32_t kExp = std::is_same<QT, BF16>::value ? 0x7f80u : 0x7c00u;
+    if ((bits & kExp) != kExp) return 0;
+    return (bits & 0x7fffu) != kExp ? 1 : (bits & 0x8000u) ? 3 : 2;
+  }
+}
+
+// The rows listed by softmax warp `warp`: their softmax sums are numbers, but an element of
+// the output is not.  Where a V that the row sees is not finite in that dimension, so is
+// the element, as the weights are positive; else a V of the item that is hidden from the
+// row has reached it, and the row is computed again from its own keys (exact_row).
+//
+// Which it is takes one pass over the V rows of the item: each lane has D / 32 dimensions
+// and keeps the last key so far with a NaN and with either infinity.  Rows see intervals of
+// keys whose ends do not decrease, so the pass stops at each row's end in turn and asks
+// whether such a key is at or behind its first one.  The pass costs about what loading the
+// item did.  Rows are computed again only beside a V that their neighbours in the item see
+// and they do not, a tile's worth or two for each such V.
 template <class QT, bool kFP8, int kMods, int D>
-__device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem<kFP8>& sm, int total, int qt,
-                                       int w) {
+__device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem<kFP8>& sm, int total, int warp) {
   using T = typename QT::T;
-  const int lane = threadIdx.x & 31, g = p.group;
+  constexpr int kElem = kFP8 ? 1 : 2, kDims = D / 32, kBits = 8 * kElem;
+  const int lane = threadIdx.x & 31, g = p.group, qt = warp / kTileWarps;
+  const int r0 = 32 * (warp % kTileWarps);  // the warp's first row of the tile
   const unsigned gmask = 0xFu << (lane & 28);
-  const bool all = sm.redo_n[qt] > kRedo;
-  const int n = all ? total : sm.redo_n[qt];
+  const int n = sm.redo_n[warp];
   ModItem x;
   for (int i = 0; i < n; ++i) {
-    make_item<kMods, kFP8>(p, sm, all ? i : sm.redo[qt][i], total, x);
-    const int nt = qt ? x.nt[1] : x.nt[0], t0 = qt ? x.t0[1] : x.t0[0];
-    const int pos0 = qt ? x.pos0[1] : x.pos0[0];
-    for (int r = w * 8 + (lane >> 2); r < nt * g; r += 8 * kTileWarps) {
-      const int tok = r / g, row = x.q0 + t0 + tok, h = x.kvh * g + r % g;
+    make_item<kMods, kFP8>(p, sm, sm.redo_item[warp][i], total, x);
+    const uint32_t rows = sm.redo_rows[warp][i];
+    const int t0 = qt ? x.t0[1] : x.t0[0], pos0 = qt ? x.pos0[1] : x.pos0[0];
+    const int32_t* table = p.block_tables + (size_t)x.seq * p.max_blocks_per_seq;
+    int last[3][kDims];  // last key with a NaN, +inf, -inf
+    uint32_t unseen[kDims];  // rows whose element is not finite without a key of theirs
+#pragma unroll
+    for (int e = 0; e < kDims; ++e) {
+      last[0][e] = last[1][e] = last[2][e] = -1;
+      unseen[e] = 0;
+    }
+    int j = x.lo_block * kBlockSize;
+    auto scan_to = [&](int end) {  // keys [j, end), whole blocks where they last
+      while (j < end) {
+        const int b = j / kBlockSize, f = j % kBlockSize, m = min(kBlockSize, end - b * kBlockSize);
+        const int blk = __ldg(table + b);
+        if (blk >= 0 && blk < p.num_blocks) {  // (else zeros)
+          const uint8_t* v = p.v_cache + ((size_t)blk * p.num_kv_heads + x.kvh) * (kBlockSize * D * kElem) +
+                             lane * (kDims * kElem);
+          unsigned long long w[kBlockSize];
+#pragma unroll
+          for (int t = 0; t < kBlockSize; ++t) {
+            const uint8_t* s = v + t * (D * kElem);
+            w[t] = 0;
+            if (t >= f && t < m) {
+              if constexpr (kDims * kElem == 8) w[t] = __ldg(reinterpret_cast<const unsigned long long*>(s));
+              else if constexpr (kDims * kElem == 4) w[t] = __ldg(reinterpret_cast<const uint32_t*>(s));
+              else w[t] = __ldg(reinterpret_cast<const unsigned short*>(s));
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < kBlockSize; ++t)
+#pragma unroll
+            for (int e = 0; e < kDims; ++e) {
+              const int kind = odd_kind<QT, kFP8>((uint32_t)(w[t] >> (e * kBits)) & ((1u << kBits) - 1u));
+              if (kind == 1) last[0][e] = b * kBlockSize + t;
+              if (kind == 2) last[1][e] = b * kBlockSize + t;
+              if (kind == 3) last[2][e] = b * kBlockSize + t;
+            }
+        }
+        j = b * kBlockSize + m;
+      }
+    };
+    for (uint32_t todo = rows; todo != 0; todo &= todo - 1) {
+      const int rw = __ffs(todo) - 1, tok = (r0 + rw) / g;
+      const int row = x.q0 + t0 + tok, h = x.kvh * g + (r0 + rw) % g;
       int lo, hi;
       key_interval(p, row, pos0 + tok, x.ctx, x.bidir, &lo, &hi);
-      if (lo >= hi) continue;
-      const uint4* o = reinterpret_cast<const uint4*>(
-          static_cast<const T*>(p.out) + ((size_t)row * p.num_heads + h) * D + (lane & 3) * (D / 4));
-      bool odd = false;
+      scan_to(hi);
+      T* o = static_cast<T*>(p.out) + ((size_t)row * p.num_heads + h) * D + lane * kDims;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        float f[8];
-        to_float(o[c], f, QT());
-#pragma unroll
-        for (int e = 0; e < 8; ++e) odd |= !(fabsf(f[e]) < INFINITY);
+      for (int e = 0; e < kDims; ++e) {
+        if (fabsf((float)o[e]) < INFINITY) continue;
+        const bool nan = last[0][e] >= lo, up = last[1][e] >= lo, down = last[2][e] >= lo;
+        if (!nan && !up && !down) unseen[e] |= 1u << rw;
+        else store_out(o + e, nan || up == down ? NAN : up ? INFINITY : -INFINITY);
       }
-      if (__any_sync(gmask, odd)) exact_row<QT, kFP8, D>(p, x.seq, row, h, pos0 + tok, lo, hi, gmask);
     }
+    scan_to(min(x.end_block * kBlockSize, x.ctx));
+    uint32_t again = 0;
+#pragma unroll
+    for (int e = 0; e < kDims; ++e)  // (no such V in the whole item: the sum itself overflowed)
+      if (last[0][e] >= 0 || last[1][e] >= 0 || last[2][e] >= 0) again |= unseen[e];
+    again = __reduce_or_sync(kFull, again);
+    __syncwarp();
+    for (int c = lane >> 2; c < __popc(again); c += 8) {
+      const int rw = (int)__fns(again, 0, c + 1), tok = (r0 + rw) / g;
+      const int row = x.q0 + t0 + tok, h = x.kvh * g + (r0 + rw) % g;
+      int lo, hi;
+      key_interval(p, row, pos0 + tok, x.ctx, x.bidir, &lo, &hi);
+      exact_row<QT, kFP8, D>(p, x.seq, row, h, pos0 + tok, lo, hi, gmask);
+    }
+    __syncwarp();
   }
 }
 
@@ -531,8 +599,8 @@ __device__ __forceinline__ void mods_setup(const AttnParams& p, ModSmem<kFP8>& s
       }
       mbar_init(&sm.o_free[x], kTileWarps);
       mbar_init(&sm.mma_done[x], 1);
-      sm.redo_n[x] = 0;
     }
+    for (int w = 0; w < kSoftWarps; ++w) sm.redo_n[w] = 0;
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(&sm.item_full[i], 1);
       mbar_init(&sm.item_read[i], kSoftWarps + kIssuers + mod_extra(kFP8) - 1);
@@ -693,16 +761,20 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
   for (; ok; ++n) {
     bool good = true;
     if (pw == 0) {
-      int k = blockIdx.x;
-      if (lane == 0 && n > 0) k = next_item(sm, n - 1, abort, lim);
+      int k = n == 0 ? (int)blockIdx.x : -1;
+      if (lane == 0 && n > 0 && asked == n) k = next_item(sm, n - 1, abort, lim);
       k = __shfl_sync(kFull, k, 0);
       if (k == -2) {
         ok = false;
         break;
       }
       if (k >= 0) {
-        if (lane == 0) ask_next(sm);
-        ++asked;
+        // (not for more items than the lists of redo_rows can take)
+        const int listed = lane < kSoftWarps ? *static_cast<volatile int*>(&sm.redo_n[lane]) : 0;
+        if (__all_sync(kFull, listed + kUnderWay <= kRedo)) {
+          if (lane == 0) ask_next(sm);
+          ++asked;
+        }
         make_item<kMods, kFP8>(p, sm, k, total, x);
       }
       if (lane == 0) {
@@ -1270,20 +1342,24 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
           *reinterpret_cast<uint4*>(static_cast<OutT*>(p.out) + (size_t)place[i] * D + c +
                                     8 * (lane & 3)) = w[i];
     }
-    const bool odd = !empty && (z.x != z.x || z.y != z.y);
-    if (__any_sync(kFull, odd && valid) && lane == 0) {
-      const int at = atomicAdd(&sm.redo_n[qt], 1);
-      if (at < kRedo) sm.redo[qt][at] = x.k;
+    // (where the sum of the weights is no number, a score that the row sees is none)
+    const bool odd = valid && !empty && l > 0.0f && l < INFINITY && (z.x != z.x || z.y != z.y);
+    const uint32_t odd_rows = __ballot_sync(kFull, odd);
+    if (odd_rows != 0 && lane == 0) {
+      const int at = sm.redo_n[warp];  // (below kRedo: the producer sees to it)
+      if (at < kRedo) {
+        sm.redo_item[warp][at] = x.k;
+        sm.redo_rows[warp][at] = odd_rows;
+        *static_cast<volatile int*>(&sm.redo_n[warp]) = at + 1;
+      }
     }
     tc::fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.o_free[qt]);
   }
   if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
-  // every warp of the tile leaves the loop here, whatever it met, and sees the others'
-  // stores and flag behind this barrier
-  ok = all_of_tile(ok, qt);
-  if (ok && sm.redo_n[qt] > 0) redo_rows<QT, kFP8, kMods, D>(p, sm, total, qt, warp % kTileWarps);
+  __syncwarp();
+  if (ok && sm.redo_n[warp] > 0) redo_rows<QT, kFP8, kMods, D>(p, sm, total, warp);
 }
 
 template <class QT, bool kFP8, int kMods, int D>

@@ -1,0 +1,105 @@
+"""Infinities and NaN in the K and V that some rows of a biased attention call see and
+others do not, against a plain 64-bit softmax.
+
+An output element sum_j w_j v_j whose row sees a v_j that is not finite is the infinity
+of their sign, or NaN (the weights are positive): compared as such.  All others are
+within the bounds of test_gpu_biased.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_98_gb300 as pkv
+from test_gpu_biased import DEV, Batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    from paged_kv_cache_98_gb300 import _build
+    _build.build()
+    pkv.load()
+    torch.cuda.init()
+
+
+def plant(b, what):
+    """Sets V (which "v") or K ("k") of tokens: what is a list of (which, sequence, token,
+    dimensions, value); in an E4M3 cache every such value is its NaN."""
+    for name, cache, host in (("v", b.vc, b.v), ("k", b.kc, b.k)):
+        mine = [w for w in what if w[0] == name]
+        if not mine:
+            continue
+        flat = cache.cpu().clone()
+        for _, s, tok, dims, value in mine:
+            if b.kv == "e4m3":
+                flat.view(torch.uint8)[int(b.tables[s, tok // 16]), :, tok % 16, dims] = 0x7F
+                host[s][tok, :, dims] = math.nan
+            else:
+                flat[int(b.tables[s, tok // 16]), :, tok % 16, dims] = value
+                host[s][tok, :, dims] = value
+        cache.copy_(flat)
+
+
+def check(b, got):
+    want, bound = b.plain()
+    got = got.double().cpu()
+    finite = torch.isfinite(want)
+    assert not finite.all() and finite.any()
+    off = (got - want).abs()
+    bad = ~(off <= bound) & finite
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} elements, first {bad.nonzero()[0].tolist()}"
+    odd = ~finite
+    same = (torch.isnan(got) & torch.isnan(want)) | (got == want)
+    assert same[odd].all(), (odd & ~same).nonzero()[0].tolist()
+
+
+def twice(b):
+    """Called two times: the same bits."""
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got, again = b.call(errors=err), b.call(errors=err)
+    assert pkv.check_errors(err) == 0
+    assert torch.equal(got.view(torch.int16), again.view(torch.int16))
+    return got
+
+
+KINDS = [math.inf, -math.inf, math.nan]
+
+
+@pytest.mark.parametrize("kw", [
+    dict(H=8, hkv=2), dict(H=8, hkv=2, window=50), dict(H=8, hkv=8, D=64, alibi=True, dtype="fp16"),
+    dict(H=14, hkv=2, softcap=9.0), dict(H=8, hkv=2, kv="e4m3", dtype="fp16", window=70),
+    dict(H=4, hkv=2, D=64, kv="e4m3"), dict(H=16, hkv=1, softcap=9.0, alibi=True, window=33),
+    dict(H=8, hkv=2, prefix=[100, 130])],
+    ids=lambda k: "-".join(f"{a}{b if isinstance(b, (int, str, float)) else ''}" for a, b in k.items()))
+def test_hidden_and_visible(kw):
+    """Tokens whose V is not finite in some dimensions, in documents of their own and in
+    others' sight: before, inside and behind the rows of an item."""
+    starts = None if "window" in kw or "prefix" in kw else lambda s, p: max([0] + [c for c in (70, 140, 290) if c <= p])
+    b = Batch(101, [(200, 200), (20, 300), (150, 400)][:2 if "prefix" in kw else 3], starts=starts, **kw)
+    D = b.D
+    what = [("v", 0, 3, slice(0, 5), math.inf), ("v", 0, 69, slice(4, D), -math.inf), ("v", 0, 71, [7, D - 1], math.nan),
+            ("v", 0, 150, slice(2, 3), math.inf), ("v", 0, 150, slice(9, 10), -math.inf),
+            ("v", 1, 289, slice(0, D, 3), math.inf), ("v", 1, 299, slice(1, 2), math.nan)]
+    if "prefix" not in kw:
+        what += [("v", 2, 255, slice(0, D), math.nan), ("v", 2, 333, slice(D // 2, D), math.inf)]
+    lo = np.concatenate(b.lo)
+    what = [w for w in what if not (w[1] == 1 and w[2] < lo[200])]  # (blocks that are in no table)
+    plant(b, what)
+    check(b, twice(b))
+
+
+@pytest.mark.parametrize("kw", [dict(H=8, hkv=8), dict(H=8, hkv=8, D=64, alibi=True, dtype="fp16"),
+                                dict(H=8, hkv=8, kv="e4m3", softcap=9.0)],
+                         ids=lambda k: "-".join(k))
+def test_more_odd_items_than_a_processor_lists(kw):
+    """Six thousand items, every one with rows that a hidden V would reach and rows that see
+    it: a processor lists as many as it can and leaves the others of the grid alone."""
+    r = np.random.RandomState(5)
+    lens = [int(x) for x in r.randint(12, 24, 800)]
+    b = Batch(103, [(n, n) for n in lens], starts=lambda s, p: 9 if p >= 9 else 0, **kw)
+    plant(b, [("v", s, 4, slice(s % 7, b.D, 7), KINDS[s % 3]) for s in range(800)] +
+             [("v", s, 10, slice(s % 5, b.D, 11), KINDS[s % 2]) for s in range(0, 800, 4)])
+    check(b, twice(b))
