@@ -653,7 +653,8 @@ def paged_attention_decode_biased(out, q, k_cache, v_cache, block_tables, contex
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), context_lens.data_ptr(), ctypes.addressof(mods), S, H, hkv, D,
             bs, block_tables.shape[1], nb, max_context_len, scale, _dtype_code(q),
-            _dtype_code(k_cache), k_scale, v_scale, _ptr(ws), wsb, _ptr(device_errors), raw)
+            _dtype_code(k_cache), k_scale, v_scale, None if ws is None else ws.data_ptr(), wsb,
+            _ptr(device_errors), raw)
     if rc:
         raise PagedKVError("pkv_paged_attention_decode_biased", rc)
     return out
