@@ -315,18 +315,21 @@ __device__ __forceinline__ float absmax3(float a, float b, float c) {
 // still to be applied, which the exponential's own multiply-add carries: a where the
 // score is only masked, 1 after a cap or a bias.
 //
-// The cap is C tanh(a s / C).  Where every score of the warp stays below half
-// the cap, the usual case, it is s T(s^2), T(u) = a (1 + k3 c^2 u + k5 c^4 u^2 + ...),
+// The cap is C tanh(a s / C).  For a row whose scores all stay below half the cap, the
+// usual case, it is s T(s^2), T(u) = a (1 + k3 c^2 u + k5 c^4 u^2 + ...),
 // c = a / C: the polynomial of tanh with the scales folded into its coefficients, five
 // operations on packed pairs and no exponential beside the softmax's own.  Otherwise
 // C - 2 C / (2^(2 c log2(e) s) + 1): two more MUFU results per score, off by at most
-// 2^-22 C.  The mixed batch's chunks: 109 us with the polynomial, 147 without, 85
-// uncapped.  (One of degree 9 that holds up to 3/4 of the cap took 8 us more; folding
-// either into the exponential's argument saves operations, but has the code of the
+// 2^-22 C, as much as the product behind the row's largest score is.  Each row chooses for
+// itself (by a vote of the warp, a neighbour's large score, or what Q holds past the tile's
+// tokens, would have cost the others their precision): a warp with rows of both kinds
+// runs both.  The mixed batch's chunks: 106 us with the polynomial, 135
+// without, 80 uncapped.  (One of degree 9 that holds up to 3/4 of the cap took 8 us more;
+// folding either into the exponential's argument saves operations, but has the code of the
 // exponentials twice, and was slower by 15.)
 template <int kMods>
 __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, float a, float slope,
-                                               int pos, int k0) {
+                                               int pos, int k0, bool valid) {
   if constexpr (kMods == 0) return a;
   if constexpr ((kMods & kModCap) != 0) {
     const float c = a / p.cap_log2, C = p.cap_log2;
@@ -335,7 +338,7 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
     for (int i = 0; i < kStepKeys; i += 2)
       top[(i >> 1) & 3] = absmax3(top[(i >> 1) & 3], sv[i], sv[i + 1]);
     const float most = absmax3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
-    if (__all_sync(kFull, most <= kTanhPoly && c <= 16.0f)) {
+    if ((most <= kTanhPoly || !valid) && c <= 256.0f) {
       const float c2 = c * c;
       const float t1 = a * c2, t2 = t1 * c2, t3 = t2 * c2;
       const float2 q0 = make_float2(a, a), q1 = make_float2(t1 * kTanh3, t1 * kTanh3),
@@ -358,6 +361,7 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
         sv[i] = fmaf(r, -2.0f * C, C);
       }
     }
+    __syncwarp();
   }
   if constexpr ((kMods & kModBias) != 0) {
     // distance bias of key k0 + i: -slope |pos - k0 - i|; without the absolute value
@@ -1231,7 +1235,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
 #pragma unroll
         for (int c = 0; c < kStepKeys; ++c) sv[c] = -sv[c];
       }
-      const float f = modify_scores<kMods>(p, sv, qa, slope, pos, k0);
+      const float f = modify_scores<kMods>(p, sv, qa, slope, pos, k0, valid);
       if (!__all_sync(kFull, lo <= k0 && hi >= k0 + kStepKeys)) {
         // an interval of some row of the warp ends in this tile: hidden keys become -inf
 #pragma unroll

@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import paged_kv_cache_98_gb300 as pkv
-from test_gpu_biased import DEV, Batch
+from test_gpu_biased import DEV, Batch, Decode
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +103,43 @@ def test_more_odd_items_than_a_processor_lists(kw):
     plant(b, [("v", s, 4, slice(s % 7, b.D, 7), KINDS[s % 3]) for s in range(800)] +
              [("v", s, 10, slice(s % 5, b.D, 11), KINDS[s % 2]) for s in range(0, 800, 4)])
     check(b, twice(b))
+
+
+# ---- which form of the cap --------------------------------------------------------------------
+
+def bits(t):
+    return t.view(torch.int16).cpu()
+
+
+@pytest.mark.parametrize("kw", [dict(H=8, hkv=2), dict(H=14, hkv=2, dtype="fp16"), dict(H=8, hkv=2, kv="e4m3"),
+                                dict(H=4, hkv=4, D=64, alibi=True)],
+                         ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()))
+def test_large_scores_beside_small_ones_under_a_large_cap(kw):
+    """One row whose scores pass half a cap of a million; its neighbours' scores are near one
+    and keep their own precision."""
+    b = Batch(107, [(60, 90), (30, 200)], softcap=1e6, **kw)
+    b.q[17] *= 2.0 ** 13 if b.dtype == "fp16" else 2.0 ** 20
+    if b.dtype == "fp16":
+        b.scale *= 2.0 ** 8
+        b.q[:17] *= 2.0 ** -8
+        b.q[18:] *= 2.0 ** -8
+    got = b.call()
+    b.check(got, skip=[17])  # (its own scores are a step of their type apart, which is thousands)
+    assert torch.isfinite(got[17].float()).all()
+
+
+@pytest.mark.parametrize("kw", [dict(H=14, hkv=2, dtype="fp16"), dict(H=8, hkv=2), dict(H=5, hkv=1, D=64, dtype="fp16")],
+                         ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()))
+def test_neighbours_in_the_batch_choose_nothing(kw):
+    """A chunk's bits, with small and with large queries of the sequence after it, and
+    after a call that leaves large queries in the processors' memory."""
+    b = Batch(113, [(90, 90)] * 8 + [(10, 90), (10, 90)], softcap=30.0, **kw)
+    n = int(b.qsl[-2])
+    big = Batch(115, [(128, 128)] * 64, H=8, hkv=8, D=b.D, dtype=b.dtype, spread=1e4)
+    plain = [bits(b.call())[:n]]
+    big.call()
+    plain.append(bits(b.call())[:n])
+    q = b.q.clone()
+    q[n:] *= 1e3
+    plain.append(bits(b.call(q=q.to(DEV)))[:n])
+    assert torch.equal(plain[0], plain[1]) and torch.equal(plain[0], plain[2])
