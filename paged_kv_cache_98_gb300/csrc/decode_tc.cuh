@@ -1085,8 +1085,12 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
         };
         each([&](int, int h, float& x) { x *= FP8 ? qsh[h] : qs; });
         if (p.softcap > 0.0f) {
+          // (of the keys that the row sees)
           float top = 0.0f;
-          each([&](int, int, float& x) { top = fmaxf(top, fabsf(x)); });
+          each([&](int t, int, float& x) {
+            const int key = t * kTileKeys + tid;
+            if (key < cur.n && key >= cur.front) top = fmaxf(top, fabsf(x));
+          });
           // where all scores of the warp stay below half the cap, the usual case, tanh's
           // polynomial with the cap folded into its coefficients, x (1 + k3 x^2 + ...)
           if (__all_sync(kFull, top * icap <= kTanhPoly && icap <= 16.0f)) {

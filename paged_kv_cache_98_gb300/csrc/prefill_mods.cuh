@@ -323,13 +323,17 @@ __device__ __forceinline__ float absmax3(float a, float b, float c) {
 // 2^-22 C, as much as the product behind the row's largest score is.  Each row chooses for
 // itself (by a vote of the warp, a neighbour's large score, or what Q holds past the tile's
 // tokens, would have cost the others their precision): a warp with rows of both kinds
-// runs both.  The mixed batch's chunks: 106 us with the polynomial, 135
+// runs both.  Keys hidden from the row have no say either: where a score is large, the
+// largest that the row sees is found from tensor memory, in a rolled loop (the hidden ones
+// zeroed in registers instead, code beside the path that is taken, cost 5 us of 59 with a
+// window).  The mixed batch's chunks: 106 us with the polynomial, 140
 // without, 80 uncapped.  (One of degree 9 that holds up to 3/4 of the cap took 8 us more;
 // folding either into the exponential's argument saves operations, but has the code of the
 // exponentials twice, and was slower by 15.)
 template <int kMods>
 __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, float a, float slope,
-                                               int pos, int k0, bool valid) {
+                                               uint32_t s_at, int pos, int k0, int lo, int hi,
+                                               bool valid) {
   if constexpr (kMods == 0) return a;
   if constexpr ((kMods & kModCap) != 0) {
     const float c = a / p.cap_log2, C = p.cap_log2;
@@ -337,7 +341,21 @@ __device__ __forceinline__ float modify_scores(const AttnParams& p, float* sv, f
 #pragma unroll
     for (int i = 0; i < kStepKeys; i += 2)
       top[(i >> 1) & 3] = absmax3(top[(i >> 1) & 3], sv[i], sv[i + 1]);
-    const float most = absmax3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
+    float most = absmax3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
+    if (__any_sync(kFull, !(most <= kTanhPoly) && (lo > k0 || hi < k0 + kStepKeys))) {
+      // a large one may be hidden: the largest that the row sees, from the scores read again
+      most = 0.0f;
+#pragma unroll 1
+      for (int i = 0; i < kStepKeys; i += 16) {
+        float s[16];
+        tc::tmem_ld16(s_at + i, s);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (k0 + i + e >= lo && k0 + i + e < hi) most = fmaxf(most, fabsf(s[e]));
+      }
+      most *= c;
+    }
     if ((most <= kTanhPoly || !valid) && c <= 256.0f) {
       const float c2 = c * c;
       const float t1 = a * c2, t2 = t1 * c2, t3 = t2 * c2;
@@ -1235,7 +1253,7 @@ __device__ __forceinline__ void mods_softmax(const AttnParams& p, ModSmem<kFP8>&
 #pragma unroll
         for (int c = 0; c < kStepKeys; ++c) sv[c] = -sv[c];
       }
-      const float f = modify_scores<kMods>(p, sv, qa, slope, pos, k0, valid);
+      const float f = modify_scores<kMods>(p, sv, qa, slope, s_at, pos, k0, lo, hi, valid);
       if (!__all_sync(kFull, lo <= k0 && hi >= k0 + kStepKeys)) {
         // an interval of some row of the warp ends in this tile: hidden keys become -inf
 #pragma unroll

@@ -143,3 +143,33 @@ def test_neighbours_in_the_batch_choose_nothing(kw):
     q[n:] *= 1e3
     plain.append(bits(b.call(q=q.to(DEV)))[:n])
     assert torch.equal(plain[0], plain[1]) and torch.equal(plain[0], plain[2])
+
+
+@pytest.mark.parametrize("cls,kw", [
+    (Batch, dict(H=8, hkv=2)), (Batch, dict(H=8, hkv=2, window=50)), (Batch, dict(H=8, hkv=8, D=64, alibi=True)),
+    (Batch, dict(H=8, hkv=2, window=70, dtype="fp16")),
+    (Decode, dict(H=8, hkv=2, dtype="fp16")), (Decode, dict(H=8, hkv=2, window=50, dtype="fp16")),
+    (Decode, dict(H=16, hkv=1, window=50, dtype="fp16")), (Decode, dict(H=4, hkv=4, window=50))],
+    ids=lambda k: k.__name__ if isinstance(k, type) else "-".join(f"{a}{b}" for a, b in k.items()))
+@pytest.mark.parametrize("value", [math.inf, -1e4])
+def test_hidden_scores_choose_nothing(cls, kw, value):
+    """K that no row sees, behind the contexts and before the windows, at zero and then not:
+    the same bits.  In a chunk also K that only later rows see: the earlier ones' bits."""
+    seqs = [(60, 90), (41, 203), (1, 333)] if cls is Batch else [90, 203, 333, 29, *range(101, 700, 13)]
+    b = cls(109, seqs, softcap=30.0, **kw)
+    later = 40 if cls is Batch else 0  # in the first sequence: seen by its rows from 10 on
+
+    def call(x):
+        kc = b.kc.cpu().clone()
+        for s, c in enumerate(b.ctx):
+            first = int(b.lo[s].min())
+            for tok in list(range(first // 16 * 16, first)) + list(range(c, -(-c // 16) * 16)):
+                kc[int(b.tables[s, tok // 16]), :, tok % 16] = x
+        if later:
+            kc[int(b.tables[0, later // 16]), :, later % 16] = x
+        b.kc.copy_(kc)
+        return bits(b.call())
+
+    zero, odd = call(0.0), call(value)
+    rows = [r for r in range(b.rows) if not later or r < 10 or r >= int(b.qsl[1])]
+    assert torch.equal(zero[rows], odd[rows])
