@@ -1085,11 +1085,12 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
         };
         each([&](int, int h, float& x) { x *= FP8 ? qsh[h] : qs; });
         if (p.softcap > 0.0f) {
-          // (of the keys that the row sees)
+          // (of the keys and heads that are the item's: hidden keys, and the heads past the
+          // group that Q's box brings along, have no say)
           float top = 0.0f;
-          each([&](int t, int, float& x) {
+          each([&](int t, int h, float& x) {
             const int key = t * kTileKeys + tid;
-            if (key < cur.n && key >= cur.front) top = fmaxf(top, fabsf(x));
+            if (h < p.group && key < cur.n && key >= cur.front) top = fmaxf(top, fabsf(x));
           });
           // where all scores of the warp stay below half the cap, the usual case, tanh's
           // polynomial with the cap folded into its coefficients, x (1 + k3 x^2 + ...)

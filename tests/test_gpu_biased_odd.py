@@ -173,3 +173,15 @@ def test_hidden_scores_choose_nothing(cls, kw, value):
     zero, odd = call(0.0), call(value)
     rows = [r for r in range(b.rows) if not later or r < 10 or r >= int(b.qsl[1])]
     assert torch.equal(zero[rows], odd[rows])
+
+
+@pytest.mark.parametrize("kw", [dict(H=6, hkv=2, dtype="fp16"), dict(H=5, hkv=1, dtype="fp16", window=100),
+                                dict(H=12, hkv=1, dtype="fp16"), dict(H=5, hkv=1, kv="e4m3", dtype="fp16")],
+                         ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()))
+def test_heads_past_the_group_choose_nothing(kw):
+    """Every other sequence's bits, with small and with large queries of those between: the
+    rows of Q that a group leaves free hold the next heads."""
+    b = Decode(117, list(range(60, 700, 9)), softcap=30.0, **kw)
+    q = b.q.clone()
+    q[1::2] *= 1e3
+    assert torch.equal(bits(b.call())[::2], bits(b.call(q=q.to(DEV)))[::2])
