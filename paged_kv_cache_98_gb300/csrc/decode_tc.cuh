@@ -351,7 +351,8 @@ __device__ __noinline__ void few_key_rows(const AttnParams& p, const SM& sm, int
         for (int d = 0; d < 32; ++d) acc[d] *= a;
         m = sc;
       }
-      const float w = exp2f(sc - m);
+      // (a score of -inf has no weight, also where no other has come yet)
+      const float w = sc == -INFINITY ? 0.0f : exp2f(sc - m);
       l += w;
       if (bok) {
         const uint4* vp = reinterpret_cast<const uint4*>(p.v_cache + off);

@@ -466,7 +466,8 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, int seq, int row,
       for (int d = 0; d < kDims; ++d) acc[d] *= a;
       m = sc;
     }
-    const float w = exp2f(sc - m);
+    // (a score of -inf has no weight, also where no other has come yet)
+    const float w = sc == -INFINITY ? 0.0f : exp2f(sc - m);
     l += w;
     if (l != l) break;  // so is every output of the row (the four lanes agree)
     if (bok) {

@@ -185,3 +185,41 @@ def test_heads_past_the_group_choose_nothing(kw):
     q = b.q.clone()
     q[1::2] *= 1e3
     assert torch.equal(bits(b.call())[::2], bits(b.call(q=q.to(DEV)))[::2])
+
+
+# ---- scores of minus infinity -------------------------------------------------------------------
+
+def sink(b, s, toks):
+    """K of the tokens such that every head's score is -inf: a weight of zero."""
+    b.q[:, :, 0] = b.q[:, :, 0].abs() + 0.5
+    kc = b.kc.cpu().clone()
+    for t in toks:
+        kc[int(b.tables[s, t // 16]), :, t % 16, 0] = -math.inf
+    b.kc.copy_(kc)
+
+
+LOW = [dict(H=8, hkv=2), dict(H=8, hkv=2, dtype="fp16", alibi=True), dict(H=16, hkv=1), dict(H=3, hkv=3),
+       dict(H=4, hkv=2, D=64, dtype="fp16"), dict(H=14, hkv=2)]
+
+
+@pytest.mark.parametrize("kw", LOW, ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()))
+def test_decode_first_score_is_minus_infinity(kw):
+    """As many keys as are recomputed key by key, and more: the others share the weight."""
+    b = Decode(121, [2, 20, 32, 33, 34, 513, 1025], **kw)
+    for s in range(len(b.ctx)):
+        sink(b, s, [0])
+        b.lo[s] = b.lo[s] + 1
+    b.check(b.call())
+
+
+@pytest.mark.parametrize("kw", [dict(H=8, hkv=2), dict(H=4, hkv=4, D=64, dtype="fp16", alibi=True)],
+                         ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()))
+def test_prefill_first_score_is_minus_infinity_in_rows_recomputed(kw):
+    b = Batch(125, [(64, 64), (30, 100)], **kw)
+    plant(b, [("v", 0, 40, slice(0, b.D, 2), math.inf)])  # hidden from the rows before it
+    sink(b, 0, [0])
+    b.lo[0] = np.maximum(b.lo[0], 1)
+    got = b.call()
+    assert torch.isnan(got[0].float()).all()  # it sees that key alone
+    got[0] = 0
+    check(b, got)
