@@ -288,8 +288,10 @@ __global__ void __launch_bounds__(kSimtThreads, (SimtGeom<KVT, D, G>::kCtasPerSm
 #pragma unroll
       for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
       float sum = 0.0f;
+      // scores of -inf alone: weights 2^(-inf - 0) = 0, not 2^(inf - inf)
+      const float top = kMods && m == -INFINITY ? 0.0f : m;
       for (int t = lane; t < nblk * kBlockSize; t += 32) {
-        const float e = t < n ? fast_exp2(lh[t] - m) : 0.0f;
+        const float e = t < n ? fast_exp2(lh[t] - top) : 0.0f;
         lh[t] = e;
         sum += e;
       }
@@ -372,7 +374,8 @@ __global__ void __launch_bounds__(kSimtThreads, (SimtGeom<KVT, D, G>::kCtasPerSm
     float acc = 0.0f;
 #pragma unroll
     for (int w = 0; w < kSimtWarps; ++w) acc += red[(w * G + h) * D + d];
-    const float val = acc * (p.v_scale / s_l[h]);
+    // (no weight in this partition, while others may have some: a partial of zeros)
+    const float val = kMods && !direct && s_l[h] == 0.0f ? 0.0f : acc * (p.v_scale / s_l[h]);
     const size_t head = (size_t)row * p.num_heads + (size_t)kvh * p.group + h;
     if (direct) {
       store_out(static_cast<OutT*>(p.out) + head * D + d, val);

@@ -1149,6 +1149,8 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
         sum[h] = 0.0f;
         mx[h] = fmaxf(fmaxf(sm.red_max[0][h], sm.red_max[1][h]),
                       fmaxf(sm.red_max[2][h], sm.red_max[3][h]));
+        // scores of -inf alone: weights 2^(-inf - 0) = 0, not 2^(inf - inf)
+        if (kMods && mx[h] == -INFINITY) mx[h] = 0.0f;
       }
       // P[h][key] in the K-major core-matrix layout (8 keys per 16-byte row of a
       // 16-bit core matrix, 16 keys for E4M3), and its row sums
@@ -1215,6 +1217,8 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
         const float l =
             (sm.red_sum[0][tid] + sm.red_sum[1][tid]) + (sm.red_sum[2][tid] + sm.red_sum[3][tid]);
         sm.stat_inv[b][tid] = p.v_scale / (FP8 ? l * 256.0f : l);
+        // (no weight in this partition, while others may have some: a partial of zeros)
+        if (kMods && l == 0.0f && cur.nparts > 1) sm.stat_inv[b][tid] = 0.0f;
         sm.stat_lse[b][tid] = m + log2f(l);
       }
 

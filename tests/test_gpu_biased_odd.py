@@ -212,6 +212,19 @@ def test_decode_first_score_is_minus_infinity(kw):
     b.check(b.call())
 
 
+@pytest.mark.parametrize("kw", LOW, ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()))
+def test_decode_scores_of_a_whole_partition_are_minus_infinity(kw):
+    """The last partition's, the first one's: the row is the others'.  All: NaN."""
+    b = Decode(123, [513, 1030, 1100, 600], **kw)
+    for s, lo, hi in ((0, 0, 512), (1, 0, 1024), (2, 600, 1100)):
+        sink(b, s, [t for t in range(b.ctx[s]) if not lo <= t < hi])
+        b.lo[s], b.hi[s] = b.lo[s] * 0 + lo, b.hi[s] * 0 + hi
+    sink(b, 3, range(600))
+    got = b.call()
+    b.check(got, skip=[3])
+    assert torch.isnan(got[3].float()).all()
+
+
 @pytest.mark.parametrize("kw", [dict(H=8, hkv=2), dict(H=4, hkv=4, D=64, dtype="fp16", alibi=True)],
                          ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()))
 def test_prefill_first_score_is_minus_infinity_in_rows_recomputed(kw):
