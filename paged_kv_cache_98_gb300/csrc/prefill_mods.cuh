@@ -711,7 +711,7 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
   const bool my_lane = (lane & 7) % kModProd == pw;
   uint8_t* const ring = &sm.ring[0][0];
   uint32_t pos = 0, n = 0;
-  int nitem = 0, ntail = 0;
+  int nitem = 0, ntail = 0, nquery = 0;  // items with keys, tails, items whose Q is asked for
   bool ok = true;
   ModItem x;
   // table entry of block 32 c + lane (kBeyond outside the visible blocks), read ahead
@@ -821,6 +821,7 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
       if (good) {
         const int nq = x.nt[1] > 0 ? 2 : 1;
         mbar_arrive_expect_tx(&sm.q_full, nq * (kRowsM / g * g * D * 2));
+        ++nquery;
         for (int qt = 0; qt < nq; ++qt) {
           uint8_t* dq = &sm.q[qt][0];
           const int tok = x.q0 + x.t0[qt];
@@ -849,8 +850,9 @@ __device__ __forceinline__ void mods_producer(const AttnParams& p, ModSmem<kFP8>
   }
   if (!ok && lane == 0) {
     flag_error(p.errors, PKV_DEVERR_TIMEOUT);
-    // an answer still on its way lands before the CTA goes away
+    // an answer, Q and tiles still on their way land before the CTA goes away
     if (pw == 0 && asked > 0) mbar_wait(&sm.answer_full, (asked - 1) & 1, 10000000ull);
+    if (nquery > 0) mbar_wait(&sm.q_full, (nquery - 1) & 1, 10000000ull);
     for (uint32_t y = pos > (uint32_t)nst ? pos - nst : 0; y < pos; ++y)
       mbar_wait(&landed[y % nst], (y / nst) & 1, 10000000ull);
   }

@@ -596,7 +596,7 @@ __device__ __forceinline__ void prefill_producers(const AttnParams& p, Smem& sm,
     uint8_t* const ring = &sm.ring[0][0];  // stage 4 (shared-prefix mode) is q[0]
     int idx = cta;
     uint32_t pos = 0;
-    int nitem = 0, ntail = 0;
+    int nitem = 0, ntail = 0, nquery = 0;  // (nquery: Q tiles asked for)
     bool ok = true;
     Item x;
     // block id of block 32c + lane of the item's context (kBeyond past it);
@@ -689,6 +689,7 @@ __device__ __forceinline__ void prefill_producers(const AttnParams& p, Smem& sm,
           // shared-prefix mode: one query tile, in q[1]
           const int nq = alt ? 1 : (x.nt[1] > 0 ? 2 : 1);
           mbar_arrive_expect_tx(&sm.q_full, nq * kTileBytes);
+          ++nquery;
           for (int qt = 0; qt < nq; ++qt) {
             uint8_t* dq = &sm.q[alt ? 1 : qt][0];
             const int tok = x.q0 + x.t0[qt];
@@ -748,6 +749,7 @@ __device__ __forceinline__ void prefill_producers(const AttnParams& p, Smem& sm,
       flag_error(p.errors, PKV_DEVERR_TIMEOUT);
       for (uint32_t y = pos > (uint32_t)nst ? pos - nst : 0; y < pos; ++y)
         mbar_wait(&sm.full[y % nst], (y / nst) & 1, 10000000ull);
+      if (nquery > 0) mbar_wait(&sm.q_full, (nquery - 1) & 1, 10000000ull);
     }
   }
 }
