@@ -449,8 +449,9 @@ int pkv_rotary_frequencies(double* inv_freq, int rotary_dim, double base,
  *             slot: K and V are not written, q is rotated all the same).  Two
  *             tokens of one slot are a caller's error (its rows are unspecified).
  *   inv_freq  HOST array of rotary_dim / 2 doubles, read during the call.
- *             Pair i of a token at position t turns by t * inv_freq[i]; the
- *             angle is reduced exactly, for positions up to 2^30.
+ *             Pair i of a token at position t turns by t * inv_freq[i]
+ *             (|inv_freq[i]| <= 1000), reduced to a fraction of a turn in
+ *             integers: off by less than 2^-31 turns at every position.
  *   rotary_dim  even, 2 .. head_dim: the elements that turn; the others pass.
  *   layout    PKV_ROTARY_HALF: pair i is elements (i, i + rotary_dim / 2);
  *             PKV_ROTARY_INTERLEAVED: elements (2 i, 2 i + 1).

@@ -131,7 +131,7 @@ int pkv_rotary_and_cache(void* q_out, const void* q, const void* k, const void* 
                                       !std::isfinite(k_scale) || !std::isfinite(v_scale)))
     return PKV_ERR_INVALID_ARG;
   if (!inv_freq || !aligned(device_errors, 4)) return PKV_ERR_INVALID_ARG;
-  // |t * inv_freq| in turns stays below 2^52, where a double still has a fraction
+  // (the range for which the phases are good to 2^-63 turns)
   for (int i = 0; i < rotary_dim / 2; ++i)
     if (!(std::fabs(inv_freq[i]) <= 1.0e3)) return PKV_ERR_INVALID_ARG;
   if (num_tokens == 0) return PKV_OK;

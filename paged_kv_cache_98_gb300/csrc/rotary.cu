@@ -11,9 +11,9 @@
 // and fp64 runs at 1/60 of fp32 here.  The angle is taken modulo one turn in
 // integers instead: the host gives phase[i] = frac(inv_freq[i] / 2 pi) * 2^64,
 // and t * phase[i] mod 2^64 is the fraction of a turn, exact but for phase's own
-// rounding (below 2^-24 turns for every t < 2^30 and |inv_freq| <= 1, as models have).  Its top 32 bits as a signed
-// fraction go through sincospif.  No table is read, so there is none to size for
-// the longest context.
+// rounding, 2^-63 turns, so off by less than 2^-32 turns at any position.  Its top 32
+// bits as a signed fraction go through sincospif.  No table is read, so there is none to
+// size for the longest context.
 //
 // A warp takes a token, or a share of its rows.  A row is D / 8 lanes, one 16-byte
 // chunk each, so two (D = 128) or four rows move at once, four times over before
@@ -226,6 +226,18 @@ int launch_dim(RotParams& p, int head_dim, bool half, cudaStream_t stream) {
                         : launch_typed<QT, FP8, 128>(p, half, stream);
 }
 
+// frac(inv / 2 pi) * 2^64 for |inv| <= 1e3, to within 1.5: inv / 2 pi as the sum of two
+// doubles (1 / 2 pi is one, kHi + kLo; the product's rounding comes by fma), of which the
+// first one's fraction and the second are whole numbers of 2^-64 turns or nearly.
+unsigned long long phase_of(double inv) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+  const double turns = inv * kHi, rest = std::fma(inv, kHi, -turns) + inv * kLo;
+  const unsigned long long whole =
+      (unsigned long long)(std::fabs(turns - std::trunc(turns)) * 0x1p64);
+  return (turns < 0.0 ? 0ull - whole : whole) +
+         (unsigned long long)std::llrint(rest * 0x1p64);
+}
+
 }  // namespace
 
 int launch_rotary_and_cache(const RotaryArgs& a, const double* inv_freq, cudaStream_t stream) {
@@ -250,11 +262,7 @@ int launch_rotary_and_cache(const RotaryArgs& a, const double* inv_freq, cudaStr
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
   p.errors = a.errors;
-  for (int i = 0; i < p.pairs; ++i) {
-    const double turns = inv_freq[i] / 6.283185307179586476925286766559;
-    const double frac = turns - std::floor(turns);  // [0, 1)
-    p.phase[i] = frac < 1.0 ? (unsigned long long)(frac * 0x1p64) : 0ull;
-  }
+  for (int i = 0; i < p.pairs; ++i) p.phase[i] = phase_of(inv_freq[i]);
   const bool fp8 = a.cache_dtype == PKV_FP8_E4M3, half = a.layout == PKV_ROTARY_HALF;
   if (a.src_dtype == PKV_BF16)
     return fp8 ? launch_dim<BF16, true>(p, a.head_dim, half, stream)
