@@ -80,14 +80,22 @@ constexpr int kSoftWarps = 2 * kTileWarps;
 constexpr int kIssuers = 2;
 // What the issuers share out: scores and products of both query tiles, or the query
 // tiles.  By role, the products' order keeps the two softmax warpgroups in step; that
-// suits them while they are not bound by the pipes they share (the mixed batch's chunks
-// without modifiers 85 us against 91, with a bias 88 to 92 against 101), not with a cap (118
-// against 109; with a bias, too, 130 against 126) or where converter warps work beside
-// them (E4M3 prompts 142 against 138), nor in the short items that first keys leave
-// (packed documents 123 against 116), where the query tiles differ in length.
+// suits them while they are not bound by the pipes they share, in items of many steps, not
+// with a cap (118 us against 109 on the mixed batch's chunks; with a bias, too, 130 against
+// 126) or where converter warps work beside them (E4M3 prompts 142 against 138).  Measured
+// without a cap, by role against by tile, keys only and with a bias: those chunks 82
+// against 92 and 87 against 98; with a window of 1024 50 / 51 and 51 / 55, of 256 equal;
+// 8191 tokens with a window of 64 49 / 48 and 59 / 53 (32 KV heads 78 / 70 and 82 / 75);
+// cut into documents of 50 tokens 50 / 49 and 59 / 55, of 200 59 / 56 and 68 / 63, of 800
+// 82 / 86 and 94 / 91, of 2000 136 / 146 and 148 / 156, of 5000 231 / 256 and 247 / 268.
+// So by role where items are long by the call's own sizes: no window, or one of at least
+// 512.  How long first keys leave them is not known at the launch; they are taken for
+// short ones, which costs documents of thousands of tokens 5 to 13 %.
+constexpr int kLongWindow = 512;
 template <bool kFP8, int kMods>
 __device__ __forceinline__ bool by_role(const AttnParams& p) {
-  return !kFP8 && (kMods & kModCap) == 0 && p.key_start == nullptr;
+  return !kFP8 && (kMods & kModCap) == 0 && p.key_start == nullptr &&
+         (p.window == 0 || p.window >= kLongWindow);
 }
 constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + kIssuers;
 // Warps beside softmax and issuers, and threads of the CTA: two producers, or (E4M3
