@@ -496,8 +496,12 @@ int pkv_rotary_and_cache(void* q_out, const void* q, const void* k, const void* 
  * NULL / zero members switch a modifier off; a NULL struct switches all off.
  * In these calls out must not overlap q or the caches (PKV_ERR_INVALID_ARG).
  * A call without sequences or without query rows does nothing; the arrays of none may be NULL.
- * On E4M3 caches the softmax weights keep 16-bit precision: the decode call rounds
- * them to two E4M3 terms (2^-8 relative, as bf16), the prefill call to the query's type.
+ * Rounding.  Scores, maxima, sums and outputs are fp32, the output rounded once.  The
+ * softmax weights are rounded to the query's type (head_dim 64 and one head per KV head in
+ * decode: not at all).  On E4M3 caches the prefill call widens K and V to the query's type,
+ * exactly; the decode call of head_dim 128 and 2 or more heads per KV head takes query and
+ * weights as two E4M3 terms each, good to 2^-8: as bf16 has them (of a bf16 query, elements
+ * below 2^-8 of the row's largest lose bits below 2^-17 of it), three bits fewer than fp16.
  */
 typedef struct {
   float softcap;

@@ -59,13 +59,20 @@
 // E4M3 terms, p = hi + lo, in separate rows of the same MMA (its N side was half
 // empty): one term alone is good to 2^-4, 2 % of the output's norm, both to 2^-8,
 // as bf16; and the query's scale is a power of two, so that hi + lo holds a bf16
-// query exactly.  Bound by HBM on 16-bit caches, as the plain form: 32 sequences with a
-// cap and a window of 4096 keys, 478 MB, take 85 us with the merge (5 us), 5.6 TB/s.  The
-// modifiers add nothing to a call of this size (8 sequences of 28,672 E4M3 keys, from cold
-// caches: 107 us plain, 107 with a cap); what keeps a smaller one below that rate is what
-// any has, its start, its last partitions and the merge: 8 sequences of 100,000 and more
-// E4M3 keys, 232 MB from their rows' first keys on, 52 us.  Three contexts of up to 700
-// keys, all latency, 13.5 us in a graph (15.5 with cap and bias element by element).
+// query exactly, but for elements below 2^-8 of the row's largest (what falls below E4M3's
+// codes is lost, 2^-17 of that largest).  An fp16 query and weights keep 8 of their 11
+// bits: the same two terms serve both types, and the output is then off by 9e-4 of its norm
+// (2e-4 with fp32 products; a third term has not been tried).
+//
+// Bound by HBM on 16-bit caches, as the plain form: 32 sequences with a
+// cap and a window of 4096 keys, 478 MB, take 85 us with the merge (5 us), 5.6 TB/s.  On
+// E4M3 caches a call takes about 17 us and then gains speed with its size: 8 sequences, 32
+// query and 8 KV heads, from cold caches, of 2048 / 8192 / 16,384 / 28,672 / 65,536 /
+// 131,072 keys 21.5 / 43 / 71 / 104 / 188 / 349 us (plain 21.5 / 43 / 70 / 103 / 188 / 344,
+// with a cap 22.5 / 43 / 71 / 107 / 193 / 353), so the first 270 MB go at 5 TB/s, what is
+// past 470 MB at 7.  8 sequences of 100,000 and more keys, 232 MB from their rows' first
+// keys on, 52 us.  Three contexts of up to 700 keys, all latency, 8.3 us with the merge,
+// one behind the other in a graph.
 
 #ifndef PKV_DECODE_TC_CUH
 #define PKV_DECODE_TC_CUH

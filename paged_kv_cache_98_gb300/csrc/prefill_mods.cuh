@@ -37,10 +37,11 @@
 //    (one term of P alone is 2 % of the output's norm), and that splitting is on the
 //    softmax warps: 211 us against 132 for the same prompts on a 16-bit cache.
 //
-// Measured (cold caches, kernel and launch): window 1024 and cap 50 on 4 chunks of 512
-// behind 2048 tokens, 32 query heads, 8 KV heads, 63 us (540 TFLOP/s of the visible
-// products); documents packed into 8191 tokens with a bias 120 us (670); six prompts with
-// two-way prefixes on an E4M3 cache 138 us (655).
+// Measured (calls one behind the other, on changing inputs): window 1024 and cap 50 on 4
+// chunks of 512 behind 2048 tokens, 32 query heads, 8 KV heads, 60 us (572 TFLOP/s of the
+// visible products); documents packed into 8191 tokens with a bias 118 us (685); six
+// prompts with two-way prefixes on an E4M3 cache 135 us (674).  head_dim 64, from cold
+// caches: those chunks 56 us with window and cap, 71 without (keys only; head_dim 128: 78).
 #ifndef PKV_PREFILL_MODS_CUH
 #define PKV_PREFILL_MODS_CUH
 
@@ -520,7 +521,10 @@ __device__ __forceinline__ int odd_kind(uint32_t bits) {
 // keys whose ends do not decrease, so the pass stops at each row's end in turn and asks
 // whether such a key is at or behind its first one.  The pass costs about what loading the
 // item did.  Rows are computed again only beside a V that their neighbours in the item see
-// and they do not, a tile's worth or two for each such V.
+// and they do not, a tile's worth or two for each such V.  A prompt of 8192 tokens, 32 query
+// and 8 KV heads: 0.37 ms, with one infinite V in its first token 3.4 ms (the pass over
+// every item), with a NaN in token 5000 18.9 ms (beside that the 63 tokens before it, their
+// 5000 keys one by one).
 template <class QT, bool kFP8, int kMods, int D>
 __device__ __noinline__ void redo_rows(const AttnParams& p, const ModSmem<kFP8>& sm, int total, int warp) {
   using T = typename QT::T;

@@ -16,9 +16,10 @@
 // written from have_s on, so CTAs need no order among themselves.
 //
 // Bound by the launch and the latency of that prefix pass (its loads, then the copies
-// that wait for the sums), not by its bytes: 9.3 us in a graph for 8 decode rows, 11.4 us
-// for 1000 mixed sequences with 3.4 MB of tables (0.5 us of traffic).  Four sequences per
-// thread, so that 1000 take one round: 13.4 us with one.
+// that wait for the sums), not by its bytes: one behind the other in a graph, where an empty
+// launch takes 0.6 us, 3.3 us for 8 decode rows, 5.6 us for 1000 mixed sequences with 3.4 MB
+// of tables (0.5 us of traffic).  Four sequences per thread, so that 1000 take one round
+// (2 us less than with one each).
 
 #include "common.cuh"
 #include "launch.h"
