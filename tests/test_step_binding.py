@@ -152,3 +152,20 @@ def test_error_words_off_their_alignment_are_refused():
         assert lib.pkv_rotary_and_cache(
             1 << 20, 1 << 22, 1 << 23, 1 << 24, 1 << 25, 1 << 26, 256, 256, ctypes.cast(inv, ctypes.c_void_p),
             1024, 256, 256, 4, 8, 2, 128, 16, 8, 128, 0, 1.0, 1, 1, 1.0, 1.0, word, None) == -1
+
+
+def test_empty_batches_through_the_binding(on_cpu):
+    """Tensors without rows, through the library itself: nothing is launched."""
+    from paged_kv_cache_98_gb300 import _build
+    _build.build()
+    e = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype)  # noqa: E731
+    kc, vc = e(4, 2, 16, 128), e(4, 2, 16, 128)
+    i32 = dict(dtype=torch.int32)
+    assert pkv.paged_attention_decode_biased(e(0, 8, 128), e(0, 8, 128), kc, vc, e(0, 3, **i32), e(0, **i32),
+                                             0.1, softcap=30.0).shape[0] == 0
+    for n in (0, 3):
+        assert pkv.paged_attention_prefill_biased(
+            e(0, 8, 128), e(0, 8, 128), kc, vc, e(n, 3, **i32), torch.zeros(n, **i32),
+            torch.zeros(n + 1, **i32), 0.1, window=20).shape[0] == 0
+    assert pkv.rotary_and_cache(e(0, 8, 128), e(0, 8, 128), e(0, 2, 128), e(0, 2, 128), kc, vc,
+                                e(0, dtype=torch.int64), e(0, **i32), [1.0] * 64).shape[0] == 0
