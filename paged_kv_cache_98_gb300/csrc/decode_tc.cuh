@@ -568,7 +568,6 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
       }
       return row;
     };
-    int nquery = 0;  // items whose Q is asked for (lane 0 of the first K producer)
     auto load_q = [&](const Item& x, int k) -> bool {
       if constexpr (FP8) return true;  // the converter warps build the split query
       const int b = k & 1;
@@ -577,7 +576,6 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
         if (k >= 2) good = wait_bar(&sm.q_empty[b], ((k - 2) >> 1) & 1, abort, lim);
         if (good) {
           mbar_arrive_expect_tx(&sm.q_full[b], L::kQBytes);
-          nquery = k + 1;
           const int row = x.seq * p.num_heads + x.kvh * p.group;
           tc::tma_load_2d(&sm.q[b][0], &tm_q, 0, row, &sm.q_full[b]);
           tc::tma_load_2d(&sm.q[b][L::kQHalf], &tm_q, 64, row, &sm.q_full[b]);
@@ -625,7 +623,8 @@ __device__ __forceinline__ void decode_body(const AttnParams& p, const CUtensorM
       // let copies already issued land before the CTA goes away
       for (uint32_t x = pos > nst ? pos - nst : 0; x < pos; ++x)
         mbar_wait(&full[x % nst], (x / nst) & 1, 10000000ull);
-      for (int k = nquery > 2 ? nquery - 2 : 0; k < nquery; ++k)
+      // Q of the last items (if the last one's was never asked for, its wait runs out)
+      for (int k = it > 3 ? it - 3 : 0; !FP8 && !is_v && pi == 0 && k < it; ++k)
         mbar_wait(&sm.q_full[k & 1], (k >> 1) & 1, 10000000ull);
     }
   } else if (warp == 5 || warp == kWarpPV) {
