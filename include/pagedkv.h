@@ -516,6 +516,9 @@ typedef struct {
  * pkv_paged_attention_decode (without partition_size).  prefix_lens must be NULL.
  * workspace: at least pkv_decode_biased_workspace_size(...) bytes, with the
  * call's window (0 for none); a window bounds it however long the contexts are.
+ * It holds nothing between calls, but is the call's until it has run: calls that
+ * may run at the same time (on other streams, in graphs replayed side by side)
+ * take one each.
  */
 size_t pkv_decode_biased_workspace_size(int num_seqs, int num_heads, int head_dim,
                                         int max_context_len, int window);

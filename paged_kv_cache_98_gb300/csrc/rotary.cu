@@ -28,7 +28,7 @@
 // of each head turning), 336 MB, in 52.6 us, 6.4 TB/s (CTAs of 256 threads 55.5; an
 // earlier form with a CTA per token and the angles in shared memory 71); by the launch
 // for few: 64 tokens 3.6 us, one call behind the other in a graph, where an empty launch takes
-// 0.6.  2080 tokens into an E4M3 cache, 47 MB, take 11.8 us that way and 14.1 alone, against
+// 0.6.  2080 tokens into an E4M3 cache, 47 MB, take 11.8 us that way and 14.3 alone, against
 // 6.9 for their bytes: the launch makes one warp of each token there, three or four per
 // scheduler, each with its angles and its codes to compute (issue slots 53 % busy), where
 // the registers would hold five; more warps of fewer rows have not been measured.
