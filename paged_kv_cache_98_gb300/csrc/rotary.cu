@@ -230,10 +230,13 @@ int launch_dim(RotParams& p, int head_dim, bool half, cudaStream_t stream) {
 
 // frac(inv / 2 pi) * 2^64 for |inv| <= 1e3, to within 1.5: inv / 2 pi as the sum of two
 // doubles (1 / 2 pi is one, kHi + kLo; the product's rounding comes by fma), of which the
-// first one's fraction and the second are whole numbers of 2^-64 turns or nearly.
+// first one's fraction and the second are whole numbers of 2^-64 turns or nearly.  (The
+// product is volatile so that no compiler takes it unrounded into the difference below,
+// which would count its rounding twice.)
 unsigned long long phase_of(double inv) {
   constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
-  const double turns = inv * kHi, rest = std::fma(inv, kHi, -turns) + inv * kLo;
+  const volatile double product = inv * kHi;
+  const double turns = product, rest = std::fma(inv, kHi, -turns) + inv * kLo;
   const unsigned long long whole =
       (unsigned long long)(std::fabs(turns - std::trunc(turns)) * 0x1p64);
   return (turns < 0.0 ? 0ull - whole : whole) +
