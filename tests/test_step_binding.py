@@ -145,7 +145,7 @@ def test_error_words_off_their_alignment_are_refused():
         assert lib.pkv_paged_attention_decode_biased(
             1 << 20, 1 << 21, 1 << 22, 1 << 23, 1024, 2048, None, *tail, None, 0, word, None) == -1
         assert lib.pkv_paged_attention_prefill_biased(
-            1 << 20, 1 << 21, 1 << 22, 1 << 23, 1024, 2048, 3072, None, 2, 6, 4, *tail[1:], word, None) == -1
+            1 << 20, 1 << 21, 1 << 22, 1 << 23, 1024, 2048, 3584, None, 2, 6, 4, *tail[1:], word, None) == -1
         assert lib.pkv_build_step_maps(
             4096, 8192, 8448, 8704, 8960, 12288, 512, 768, 1024, 1280, 2, 4, 8, 4, 2, 16, 64, word, None) == -1
         inv = (ctypes.c_double * 64)(*([1.0] * 64))
