@@ -264,7 +264,7 @@ def prepare(case, seed):
                   counts=ints(np.isin(np.arange(nb), ids[:at])),
                   new=torch.empty(case["seqs"], dtype=torch.int32, device=dev))
     caches = torch.randn((case["layers"], 2, nb, hk, BLOCK, d), generator=g, device=dev, dtype=dt)
-    st.update(caches=caches, k_caches=[x[0] for x in caches], v_caches=[x[1] for x in caches])
+    st.update(caches=caches, k_caches=caches[:, 0], v_caches=caches[:, 1])
     return st
 
 
