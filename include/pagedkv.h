@@ -65,6 +65,8 @@ typedef enum {
 #define PKV_DEVERR_CONTEXT 0x2u     /* context/query length beyond the table or launch bounds */
 #define PKV_DEVERR_SLOT 0x4u        /* slot_mapping entry >= num_blocks * block_size */
 #define PKV_DEVERR_TIMEOUT 0x8u     /* a wait on an asynchronous copy or MMA gave up */
+#define PKV_DEVERR_NO_BLOCKS 0x10u  /* fewer free blocks than a resize asks for */
+#define PKV_DEVERR_SHARED 0x20u     /* tokens would move into a block that others hold too */
 
 /*
  * Scatter new keys and values into the paged caches through a slot mapping.
@@ -548,6 +550,112 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
                                        int num_blocks, int max_context_len, float scale,
                                        pkv_dtype q_dtype, pkv_dtype kv_dtype, float k_scale,
                                        float v_scale, uint32_t* device_errors, void* stream);
+
+/*
+ * Requests whose block lists live on the GPU (these calls have no counterpart in the
+ * source pages).  A program that keeps its request tables
+ * there (pkv_build_step_maps) also keeps ref_counts [num_blocks] int32: how many entries
+ * of its requests' lists name each block, 0 for a free one.  These calls hold the counts
+ * up to date, so beams, samples and drafted tokens need no host pool (pkv_block_pool_*
+ * is the host's own bookkeeping; a block belongs to one of the two).
+ *
+ * pkv_fork_requests: the rows of a step from those of the one before.  Row i of
+ * tables_out becomes the first ceil(lens[p] / 16) entries of row p = parents[i] of
+ * tables (the entries behind are left as they were), lens_out[i] = lens[p].  A negative
+ * parent gives an empty row.  Every block gains a reference for each new row that names
+ * it and loses one for each old row, so a parent named twice is forked, one named once
+ * moved, and one not named at all freed: its blocks that nothing else holds have count 0
+ * from then on.
+ *   tables [num_in][max_blocks_per_seq], lens [num_in], parents [num_out] int32
+ *   tables_out [num_out][max_blocks_per_seq], lens_out [num_out]: memory of their own.
+ * A parent >= num_in gives an empty row, a length outside the table is cut back: both
+ * flag PKV_DEVERR_CONTEXT.  An entry outside the pool is copied, but not counted, and
+ * flags PKV_DEVERR_BLOCK_ID.  At most PKV_FORK_MAX_ROWS rows on either side
+ * (PKV_ERR_UNSUPPORTED beyond).
+ */
+#define PKV_FORK_MAX_ROWS 65536
+int pkv_fork_requests(int32_t* tables_out, int32_t* lens_out, const int32_t* tables,
+                      const int32_t* lens, int32_t* ref_counts, const int32_t* parents,
+                      int num_out, int num_in, int max_blocks_per_seq, int block_size,
+                      int num_blocks, uint32_t* device_errors, void* stream);
+
+/*
+ * pkv_resize_requests: requests grow and shrink.  Sequence i of the batch is row rows[i]
+ * of request_tables (distinct; negative: a padding sequence) and goes from
+ * cached_lens[i] to new_lens[i] tokens.  In this order:
+ *   1. entries ceil(new / 16) .. ceil(cached / 16) - 1 of sequences that shrink give
+ *      their blocks back (one reference each) and become -1; length 0 frees a request;
+ *   2. a sequence that grows and whose last block is partial and held more than once
+ *      gets a block of its own for it, the copy-on-write of pkv_request_append: of
+ *      holders that all grow in this call the last one in batch order keeps the block.
+ *      block_pairs [num_seqs][2] receives (source, copy), or (-1, -1), for
+ *      pkv_copy_blocks_layers before the new tokens are written;
+ *   3. entries ceil(cached / 16) .. ceil(new / 16) - 1 of those that grow are opened.
+ * Blocks for 2 and 3 are the free ones (count 0 after 1) in the order of their ids,
+ * handed out in batch order, a sequence's copy first.  Where a sequence's do not suffice,
+ * it and all behind it that need blocks keep their cached length and everything they have
+ * (PKV_DEVERR_NO_BLOCKS).
+ *   granted_lens [num_seqs]: new, or cached where blocks did not suffice, 0 for padding
+ *   new_blocks [num_new_blocks]: the opened blocks of 3 in batch order, as
+ *         pkv_build_step_maps takes them (with q_lens = granted - cached of what grows),
+ *         -1 behind the last.  A list that is too short is cut and flagged
+ *         PKV_DEVERR_BLOCK_ID (the tables have the blocks all the same).
+ * A row >= num_request_rows or a length outside the table makes the sequence a padding
+ * one (PKV_DEVERR_CONTEXT); an entry outside the pool is taken for one that nobody else
+ * holds, and not counted (PKV_DEVERR_BLOCK_ID).  Two sequences of one row are a caller's
+ * error (that row's entries and the counts of its blocks are unspecified).
+ * No output may share memory with an input or another output.  At most
+ * PKV_STEP_MAPS_MAX_SEQS sequences and 2^30 blocks (PKV_ERR_UNSUPPORTED beyond).
+ */
+int pkv_resize_requests(int32_t* request_tables, int32_t* ref_counts, const int32_t* rows,
+                        const int32_t* cached_lens, const int32_t* new_lens,
+                        int32_t* granted_lens, int32_t* new_blocks, int32_t* block_pairs,
+                        int num_seqs, int num_request_rows, int max_blocks_per_seq,
+                        int num_new_blocks, int block_size, int num_blocks,
+                        uint32_t* device_errors, void* stream);
+
+/*
+ * pkv_copy_blocks in the caches of all layers in one launch (one for every
+ * PKV_LAYERS_PER_LAUNCH layers).
+ *   k_caches, v_caches  HOST arrays of num_layers device pointers, read during the call;
+ *         every cache as for pkv_copy_blocks, all of one shape, none overlapping another.
+ *   block_pairs  as for pkv_copy_blocks; a pair with a negative source is skipped without
+ *         a flag (what pkv_resize_requests writes for a sequence that copies nothing).
+ */
+#define PKV_LAYERS_PER_LAUNCH 128
+int pkv_copy_blocks_layers(void* const* k_caches, void* const* v_caches, int num_layers,
+                           const int32_t* block_pairs, int num_pairs, int num_kv_heads,
+                           int head_dim, int block_size, int num_blocks, pkv_dtype cache_dtype,
+                           uint32_t* device_errors, void* stream);
+
+/*
+ * Kept tokens of each sequence moved together, in place, in the caches of all layers:
+ * the accepted path of a draft tree behind the context that it was drafted for, or what
+ * is left of a long context when tokens are dropped.  Of sequence s the tokens
+ * [0, base_lens[s]) stay where they are, and the j-th of its list, the token at place
+ * keep[keep_start_loc[s] + j], goes to place base_lens[s] + j (K and V, every layer).
+ *   block_tables [num_seqs][max_blocks_per_seq], context_lens, base_lens [num_seqs],
+ *   keep_start_loc [num_seqs + 1] (non-decreasing), keep [num_keep] int32
+ *   new_lens [num_seqs]: base + the list's length (pkv_resize_requests with it gives the
+ *         blocks behind back)
+ *   ref_counts NULL, or [num_blocks]: a sequence of which a token would move into a block
+ *         that is held more than once is left as it was, new_lens = its context, and
+ *         flagged PKV_DEVERR_SHARED.  Without counts the blocks from base_lens on must
+ *         be the sequence's alone.
+ * A list must ascend within [base_lens, context_lens): a sequence whose list does not, or
+ * whose lengths are outside the table or the list's offsets outside [0, num_keep], is left
+ * as it was (new_lens = its context cut back to the table; PKV_DEVERR_CONTEXT).  A token
+ * in a block outside the pool does not move, nor does one whose place is there
+ * (PKV_DEVERR_BLOCK_ID).  Positions are kept as they were rotated.
+ * Caches as for pkv_copy_blocks_layers.
+ */
+int pkv_compact_tokens(void* const* k_caches, void* const* v_caches, int num_layers,
+                       const int32_t* block_tables, const int32_t* context_lens,
+                       const int32_t* base_lens, const int32_t* keep_start_loc,
+                       const int32_t* keep, int32_t* new_lens, const int32_t* ref_counts,
+                       int num_seqs, int num_keep, int num_kv_heads, int head_dim, int block_size,
+                       int max_blocks_per_seq, int num_blocks, pkv_dtype cache_dtype,
+                       uint32_t* device_errors, void* stream);
 
 /*
  * Host block pool with prefix caching.  Sources: "第34讲 … vLLM 生产级系统架构

@@ -32,7 +32,7 @@ __all__ = [
     "copy_blocks", "BlockPool", "Request", "mixed_workspace_size", "paged_attention_mixed",
     "debug_arm_wait_timeout", "debug_prefill_pairs", "build_step_maps", "rotary_frequencies",
     "rotary_and_cache", "decode_biased_workspace_size", "paged_attention_decode_biased",
-    "paged_attention_prefill_biased",
+    "paged_attention_prefill_biased", "fork_requests", "resize_requests", "copy_blocks_layers", "compact_tokens",
 ]
 
 F16, BF16, FP8_E4M3 = 0, 1, 2
@@ -135,6 +135,14 @@ def load():
             lib.pkv_paged_attention_prefill_biased.restype = _I
             lib.pkv_paged_attention_prefill_biased.argtypes = (
                 [_P] * 8 + [_I] * 10 + [_F, _I, _I, _F, _F, _P, _P])
+            lib.pkv_fork_requests.restype = _I
+            lib.pkv_fork_requests.argtypes = [_P] * 6 + [_I] * 5 + [_P, _P]
+            lib.pkv_resize_requests.restype = _I
+            lib.pkv_resize_requests.argtypes = [_P] * 8 + [_I] * 6 + [_P, _P]
+            lib.pkv_copy_blocks_layers.restype = _I
+            lib.pkv_copy_blocks_layers.argtypes = [_P, _P, _I, _P] + [_I] * 6 + [_P, _P]
+            lib.pkv_compact_tokens.restype = _I
+            lib.pkv_compact_tokens.argtypes = [_P, _P, _I] + [_P] * 7 + [_I] * 8 + [_P, _P]
             _I32 = ctypes.c_int32
             lib.pkv_block_pool_create.restype = _I
             lib.pkv_block_pool_create.argtypes = [_I32, _I32, _P]
@@ -691,6 +699,137 @@ def paged_attention_prefill_biased(out, q, k_cache, v_cache, block_tables, conte
     if rc:
         raise PagedKVError("pkv_paged_attention_prefill_biased", rc)
     return out
+
+
+def fork_requests(tables_out, lens_out, tables, lens, ref_counts, parents, block_size: int = 16,
+                  device_errors=None, stream=None):
+    """Rows of a step from those of the one before (pkv_fork_requests): row i of tables_out
+    [N, MB] becomes row parents[i] of tables [M, MB] (its entries past the length are left as
+    they were), lens_out[i] = lens[parents[i]], and ref_counts [num_blocks] int32 follow.  A
+    negative parent: an empty row; a row that no parent names gives its blocks up."""
+    N, (M, MB), i32 = parents.numel(), tables.shape, torch.int32
+    raw, guard = _on_device(tables.device, stream, (
+        ("tables_out", tables_out, i32, (N, MB)), ("lens_out", lens_out, i32, (N,)),
+        ("tables", tables, i32, (M, MB)), ("lens", lens, i32, (M,)),
+        ("ref_counts", ref_counts, i32, (ref_counts.numel(),)), ("parents", parents, i32, (N,)),
+        _word(device_errors)))
+    with guard:
+        rc = (_lib or load()).pkv_fork_requests(
+            tables_out.data_ptr(), lens_out.data_ptr(), tables.data_ptr(), lens.data_ptr(),
+            ref_counts.data_ptr(), parents.data_ptr(), N, M, MB, block_size, ref_counts.numel(),
+            _ptr(device_errors), raw)
+    if rc:
+        raise PagedKVError("pkv_fork_requests", rc)
+
+
+def resize_requests(request_tables, ref_counts, rows, cached_lens, new_lens, granted_lens,
+                    new_blocks, block_pairs, block_size: int = 16, device_errors=None, stream=None):
+    """Requests grow and shrink from cached_lens to new_lens ([S] int32) tokens
+    (pkv_resize_requests): blocks behind the new lengths go back, new ones are taken in the
+    order of their ids, shared partial last blocks are replaced.
+
+    In/out: request_tables [R, MB], ref_counts [num_blocks] int32.  Outputs: granted_lens [S]
+    (cached where blocks did not suffice), new_blocks [N] (what build_step_maps takes; -1
+    behind the last), block_pairs [S, 2] ((-1, -1), or what copy_blocks_layers copies)."""
+    S, (R, MB), N, i32 = rows.numel(), request_tables.shape, new_blocks.numel(), torch.int32
+    raw, guard = _on_device(request_tables.device, stream, (
+        ("request_tables", request_tables, i32, (R, MB)),
+        ("ref_counts", ref_counts, i32, (ref_counts.numel(),)), ("rows", rows, i32, (S,)),
+        ("cached_lens", cached_lens, i32, (S,)), ("new_lens", new_lens, i32, (S,)),
+        ("granted_lens", granted_lens, i32, (S,)), ("new_blocks", new_blocks, i32, (N,)),
+        ("block_pairs", block_pairs, i32, (S, 2)), _word(device_errors)))
+    with guard:
+        rc = (_lib or load()).pkv_resize_requests(
+            request_tables.data_ptr(), ref_counts.data_ptr(), rows.data_ptr(),
+            cached_lens.data_ptr(), new_lens.data_ptr(), granted_lens.data_ptr(),
+            new_blocks.data_ptr(), block_pairs.data_ptr(), S, R, MB, N, block_size,
+            ref_counts.numel(), _ptr(device_errors), raw)
+    if rc:
+        raise PagedKVError("pkv_resize_requests", rc)
+
+
+def _layer_caches(k_caches, v_caches):
+    """The caches of all layers, each a sequence of tensors [num_blocks, H, 16, D] or one
+    tensor [L, num_blocks, H, 16, D] whose layers are contiguous: (host arrays of their
+    addresses, one of the tensors, its shape, all the tensors)."""
+    addresses, tensors = [], []
+    for name, caches in (("k_caches", k_caches), ("v_caches", v_caches)):
+        if isinstance(caches, torch.Tensor):
+            if caches.dim() != 5:
+                raise ValueError(f"{name} must be [L, num_blocks, H, 16, D] or a list of caches")
+            L, shape = caches.shape[0], caches.shape[1:]
+            st, inner = caches.stride(), 1
+            for n, s in zip(reversed(shape), reversed(st[1:])):
+                if n != 1 and s != inner:
+                    raise ValueError(f"{name}: each layer's cache must be contiguous")
+                inner *= n
+            step, at = st[0] * caches.element_size(), caches.data_ptr()
+            addresses.append((_P * max(L, 1))(*range(at, at + L * step, step)) if step else
+                             (_P * max(L, 1))(*[at] * L))
+            tensors.append(caches)
+        else:
+            L, shape = len(caches), caches[0].shape if len(caches) else None
+            for t in caches:
+                if t.shape != shape or t.dim() != 4 or not t.is_contiguous():
+                    raise ValueError(f"{name}: caches must be contiguous, [num_blocks, H, 16, D], "
+                                     "and of one shape")
+            addresses.append((_P * max(L, 1))(*[t.data_ptr() for t in caches]))
+            tensors.extend(caches)
+        if name == "k_caches":
+            first = (L, shape)
+    if first != (L, shape):
+        raise ValueError("k_caches and v_caches must have as many layers and the same shapes")
+    if not tensors or L == 0:
+        raise ValueError("at least one layer's caches are needed")
+    t0 = tensors[0]
+    for t in tensors:
+        if t.dtype is not t0.dtype or t.get_device() != t0.get_device():
+            raise ValueError("the caches must have one dtype and be on one device")
+    return addresses, L, tensors, tuple(shape)
+
+
+def copy_blocks_layers(k_caches, v_caches, block_pairs, device_errors=None, stream=None):
+    """Whole-block copies (block_pairs [n, 2] int32 on the device, rows (source, destination);
+    a negative source: none) in the K and V caches of all layers (pkv_copy_blocks_layers).
+    k_caches and v_caches: sequences of caches, or tensors [L, num_blocks, H, 16, D]."""
+    (k, v), L, tensors, (nb, hkv, bs, d) = _layer_caches(k_caches, v_caches)
+    t0, n = tensors[0], block_pairs.shape[0]
+    raw, guard = _on_device(t0.device, stream, (
+        ("block_pairs", block_pairs, torch.int32, (n, 2)), _word(device_errors)))
+    if stream is not None:
+        _stream_on(t0.device, stream, tensors)
+    with guard:
+        rc = (_lib or load()).pkv_copy_blocks_layers(
+            k, v, L, block_pairs.data_ptr(), n, hkv, d, bs, nb, _dtype_code(t0),
+            _ptr(device_errors), raw)
+    if rc:
+        raise PagedKVError("pkv_copy_blocks_layers", rc)
+
+
+def compact_tokens(k_caches, v_caches, block_tables, context_lens, base_lens, keep_start_loc, keep,
+                   new_lens, ref_counts=None, device_errors=None, stream=None):
+    """Moves the kept tokens of each sequence together in the K and V caches of all layers
+    (pkv_compact_tokens): the token at place keep[keep_start_loc[s] + j] (ascending, [K]
+    int32) goes to place base_lens[s] + j; new_lens [S] int32 receives the lengths.  With
+    ref_counts [num_blocks] int32 a sequence whose tokens would move into a shared block is
+    left as it was.  Caches as for copy_blocks_layers."""
+    (k, v), L, tensors, (nb, hkv, bs, d) = _layer_caches(k_caches, v_caches)
+    t0, S, K, i32 = tensors[0], context_lens.numel(), keep.numel(), torch.int32
+    raw, guard = _on_device(t0.device, stream, (
+        ("block_tables", block_tables, i32, (S, block_tables.shape[-1])),
+        ("context_lens", context_lens, i32, (S,)), ("base_lens", base_lens, i32, (S,)),
+        ("keep_start_loc", keep_start_loc, i32, (S + 1,)), ("keep", keep, i32, (K,)),
+        ("new_lens", new_lens, i32, (S,)), ("ref_counts", ref_counts, i32, (nb,)),
+        _word(device_errors)))
+    if stream is not None:
+        _stream_on(t0.device, stream, tensors)
+    with guard:
+        rc = (_lib or load()).pkv_compact_tokens(
+            k, v, L, block_tables.data_ptr(), context_lens.data_ptr(), base_lens.data_ptr(),
+            keep_start_loc.data_ptr(), keep.data_ptr(), new_lens.data_ptr(), _ptr(ref_counts), S, K,
+            hkv, d, bs, block_tables.shape[1], nb, _dtype_code(t0), _ptr(device_errors), raw)
+    if rc:
+        raise PagedKVError("pkv_compact_tokens", rc)
 
 
 class _Scratch:
