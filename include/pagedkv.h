@@ -552,6 +552,51 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
                                        float v_scale, uint32_t* device_errors, void* stream);
 
 /*
+ * Cross attention: query rows of a decoder over an encoder's states, whose K and V lie
+ * in a paged cache of the layout above (pkv_reshape_and_cache writes them once).  Every
+ * query of a sequence sees every state of its encoder input, whatever the lengths: one
+ * token, all beams of a request (one after the other: positions do not matter here, so
+ * beams are a sequence's queries), a target prompt.  (This call and the ones on requests
+ * below have no counterpart in the source pages.)
+ *
+ *   q, out    [total_q][num_heads][head_dim], q_dtype; out[t, h] is
+ *             sum_j softmax_j(scale * q[t,h] . K[s,j]) V[s,j] over j < encoder_lens[s]
+ *             of the sequence s that row t belongs to.  No state: zeros.
+ *   encoder_lens  [num_seqs] int32, states of each sequence, 0 included
+ *   query_start_loc [num_seqs + 1] int32, non-decreasing: sequence s owns the rows
+ *             query_start_loc[s] .. query_start_loc[s+1]-1.  Rows of no sequence (before
+ *             the first, behind the last: a captured step of fixed size) are left as they
+ *             were.
+ *   max_q_len, max_encoder_len  upper bounds of the sequences' queries and of encoder_lens
+ *             (they size the workspace; no device-to-host read).  Longer ones are cut
+ *             back and flagged PKV_DEVERR_CONTEXT: queries past max_q_len are left as
+ *             they were.
+ *   workspace at least pkv_cross_workspace_size(...) bytes, 256-byte aligned; NULL when
+ *             that is 0.  It holds nothing between calls, but is the call's until it has
+ *             run: calls that may run at the same time take one each.
+ *   kv_dtype  == q_dtype, or FP8_E4M3: decode(byte) * k_scale / v_scale.
+ * K and V behind a sequence's last state do not reach a row, whatever they hold.  Rows
+ * that see an infinity or NaN have results that are not finite, as the formula has.
+ * Rounding: scores, maxima, sums and outputs are fp32, the output rounded once; the
+ * softmax weights are rounded to q_dtype, to which E4M3 codes are widened exactly.
+ * The split of long inputs depends on the lengths of the whole batch: a row's last bits
+ * may differ between batches, never between two calls of one batch.
+ * out must not overlap q or the caches.  num_seqs == 0 or total_q == 0 launches nothing.
+ * Caches of up to 2^31 rows (num_blocks * num_kv_heads * 16) and queries of up to 2^31
+ * heads (total_q * num_heads); PKV_ERR_UNSUPPORTED beyond.
+ */
+size_t pkv_cross_workspace_size(int num_seqs, int total_q, int num_heads, int num_kv_heads,
+                                int head_dim, int max_encoder_len, int max_q_len);
+int pkv_paged_attention_cross(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, const int32_t* encoder_lens,
+                              const int32_t* query_start_loc, int num_seqs, int total_q,
+                              int max_q_len, int num_heads, int num_kv_heads, int head_dim,
+                              int block_size, int max_blocks_per_seq, int num_blocks,
+                              int max_encoder_len, float scale, pkv_dtype q_dtype,
+                              pkv_dtype kv_dtype, float k_scale, float v_scale, void* workspace,
+                              size_t workspace_bytes, uint32_t* device_errors, void* stream);
+
+/*
  * Requests whose block lists live on the GPU (these calls have no counterpart in the
  * source pages).  A program that keeps its request tables
  * there (pkv_build_step_maps) also keeps ref_counts [num_blocks] int32: how many entries

@@ -32,7 +32,8 @@ __all__ = [
     "copy_blocks", "BlockPool", "Request", "mixed_workspace_size", "paged_attention_mixed",
     "debug_arm_wait_timeout", "debug_prefill_pairs", "build_step_maps", "rotary_frequencies",
     "rotary_and_cache", "decode_biased_workspace_size", "paged_attention_decode_biased",
-    "paged_attention_prefill_biased", "fork_requests", "resize_requests", "copy_blocks_layers", "compact_tokens",
+    "paged_attention_prefill_biased", "cross_workspace_size", "paged_attention_cross", "fork_requests",
+    "resize_requests", "copy_blocks_layers", "compact_tokens",
 ]
 
 F16, BF16, FP8_E4M3 = 0, 1, 2
@@ -135,6 +136,11 @@ def load():
             lib.pkv_paged_attention_prefill_biased.restype = _I
             lib.pkv_paged_attention_prefill_biased.argtypes = (
                 [_P] * 8 + [_I] * 10 + [_F, _I, _I, _F, _F, _P, _P])
+            lib.pkv_cross_workspace_size.restype = _SZ
+            lib.pkv_cross_workspace_size.argtypes = [_I] * 7
+            lib.pkv_paged_attention_cross.restype = _I
+            lib.pkv_paged_attention_cross.argtypes = (
+                [_P] * 7 + [_I] * 10 + [_F, _I, _I, _F, _F, _P, _SZ, _P, _P])
             lib.pkv_fork_requests.restype = _I
             lib.pkv_fork_requests.argtypes = [_P] * 6 + [_I] * 5 + [_P, _P]
             lib.pkv_resize_requests.restype = _I
@@ -698,6 +704,50 @@ def paged_attention_prefill_biased(out, q, k_cache, v_cache, block_tables, conte
             _ptr(device_errors), raw)
     if rc:
         raise PagedKVError("pkv_paged_attention_prefill_biased", rc)
+    return out
+
+
+def cross_workspace_size(num_seqs: int, total_q: int, num_heads: int, num_kv_heads: int,
+                         head_dim: int, max_encoder_len: int, max_q_len: int) -> int:
+    return int(load().pkv_cross_workspace_size(num_seqs, total_q, num_heads, num_kv_heads, head_dim,
+                                               max_encoder_len, max_q_len))
+
+
+def paged_attention_cross(out, q, k_cache, v_cache, block_tables, encoder_lens, query_start_loc,
+                          scale: float, max_q_len: int | None = None,
+                          max_encoder_len: int | None = None, k_scale: float = 1.0,
+                          v_scale: float = 1.0, workspace=None, device_errors=None, stream=None):
+    """Cross attention of ragged queries (q [total_q, H, D], sequence s owning rows
+    query_start_loc[s] .. query_start_loc[s + 1] - 1) over the encoder states that
+    block_tables names, encoder_lens [S] int32 of them: pkv_paged_attention_cross.
+    Bounds that are left out are total_q and the block table's length, nothing is read
+    back; workspace (uint8, >= cross_workspace_size bytes) is allocated if omitted."""
+    TQ, H, D = q.shape
+    nb, hkv, bs, _ = k_cache.shape
+    S, i32 = encoder_lens.numel(), torch.int32
+    kv = (nb, hkv, bs, D)
+    raw, guard = _on_device(q.device, stream, (
+        ("q", q, q.dtype, (TQ, H, D)), ("out", out, q.dtype, (TQ, H, D)),
+        ("k_cache", k_cache, k_cache.dtype, kv), ("v_cache", v_cache, k_cache.dtype, kv),
+        ("encoder_lens", encoder_lens, i32, (S,)),
+        ("block_tables", block_tables, i32, (S, block_tables.shape[-1])),
+        ("query_start_loc", query_start_loc, i32, (S + 1,)), _word(device_errors)))
+    if max_q_len is None:
+        max_q_len = TQ
+    if max_encoder_len is None:
+        max_encoder_len = min(block_tables.shape[1] * bs, 2**31 - 1)
+    lib = _lib or load()
+    with guard:
+        ws, wsb = _scratch_on(stream, lib.pkv_cross_workspace_size(
+            S, TQ, H, hkv, D, max_encoder_len, max_q_len), workspace, q.device)
+        rc = lib.pkv_paged_attention_cross(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), encoder_lens.data_ptr(), query_start_loc.data_ptr(), S, TQ,
+            max_q_len, H, hkv, D, bs, block_tables.shape[1], nb, max_encoder_len, scale,
+            _dtype_code(q), _dtype_code(k_cache), k_scale, v_scale,
+            None if ws is None else ws.data_ptr(), wsb, _ptr(device_errors), raw)
+    if rc:
+        raise PagedKVError("pkv_paged_attention_cross", rc)
     return out
 
 

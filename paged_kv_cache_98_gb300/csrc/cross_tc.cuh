@@ -1,0 +1,1030 @@
+// Cross attention on the tcgen05 tensor cores: ragged query rows over the paged states of
+// an encoder, every query seeing every state of its sequence (head_dim 64 or 128, 16-bit
+// or E4M3 caches, any group size up to 16).
+//
+// A row is a (query token, head of the group) pair, a query tile is 128 rows of whole
+// tokens, a key tile 128 states.  The mathematics is that of prefill_tc.cuh:
+//   S = Q K^T in TMEM, P = 2^(s - m) back over S as 16-bit pairs, O += P V,
+// with a running maximum m that moves (and has O rescaled) only when a row's scores
+// exceed it by more than 2^8, and out = O / sum(P).
+//
+// Work.  A unit is a sequence, KV head and one or two query tiles.  With two, K and V of a
+// key tile feed both, each tile having its own softmax warpgroup; with one (a token, a
+// request's beams, the odd tile of a prompt) the warpgroups take the even and the odd key
+// tiles, each into an O of its own, and the first one joins the two at the end.
+// Sequences differ in both lengths and there may be one unit or many thousand, so units
+// are not dealt out: all key tiles of the call lie one behind the other on a line of work
+// (a tile counts kCost1 or kCost2, what a unit costs once kCostUnit), which is cut into
+// one equal part for each CTA, one CTA a processor.  Cuts fall inside units, also where
+// queries are few and inputs long; what a CTA has of a cut unit goes to the workspace as a
+// normalised partial and its log-sum-exp, at most two per CTA, and a second kernel, launched
+// as a dependent, joins the parts of a unit.  The line is walked with integers that every
+// CTA computes for itself, so the result depends on the batch alone.
+//
+// Warps: 0-3 softmax of tile a (or even key tiles), 4-7 of tile b (odd), 8 MMA issuer and
+// TMEM owner, 9-10 TMA producers, 11 makes the items from the line of work and loads the
+// V rows of partial last blocks, 12-15 (E4M3 caches) widen K and V tiles to the query's
+// type where they land.
+#ifndef PKV_CROSS_TC_CUH
+#define PKV_CROSS_TC_CUH
+
+#include "prefill_mods.cuh"
+
+namespace pkv {
+namespace cross_tc {
+namespace {
+using namespace pre_tc;
+using pre_mods::issue_mods_scores;
+using pre_mods::wait_for;
+using pre_mods::widen16;
+
+constexpr int kSoft = 8;       // softmax warps
+constexpr int kIssuer = 8, kTma = 9, kTmaWarps = 2, kMaker = 11, kConvert = 12, kConverts = 4;
+constexpr int cross_threads(bool fp8) { return fp8 ? 512 : 384; }
+// Registers: the launch holds 168 for each of 384 threads or 128 for each of 512; the
+// softmax warps take over what the others return.
+constexpr int cross_launch_regs(bool fp8) { return fp8 ? 128 : 168; }
+constexpr int cross_soft_regs(bool fp8) { return fp8 ? 168 : 200; }
+constexpr int cross_other_regs(bool fp8) { return fp8 ? 88 : 104; }
+constexpr bool cross_regs_fit(bool fp8) {
+  return 256 * cross_soft_regs(fp8) + (cross_threads(fp8) - 256) * cross_other_regs(fp8) <=
+         cross_threads(fp8) * cross_launch_regs(fp8);
+}
+static_assert(cross_regs_fit(false) && cross_regs_fit(true),
+              "setmaxnreg may only share out what the launch holds");
+
+// The line of work.
+constexpr int kCost1 = 1, kCost2 = 2;  // of a key tile, with one and with two query tiles
+constexpr int kCostUnit = 1;           // of a unit
+constexpr int kLeast = 4;              // of a CTA's part (above kCost2 + kCostUnit, so that every
+                                       // part inside a unit holds the start of a tile)
+constexpr int kItems = 4;              // made ahead
+
+struct CrossItem {
+  int live;            // 0: the end
+  int seq, kvh, len, q0;
+  int t0[2], nt[2];    // first token (within the sequence) and tokens of the query tiles
+  int kt0, kt1;        // key tiles (none: no states, the rows are zeros)
+  int part;            // slot of the partial, -1: all of the unit
+  int tail;            // 16-state step of tile kt1 - 1 with the partial last block, else -1
+};
+
+template <int D, bool kFP8>
+struct CrossSmem {
+  static constexpr int kTile = 128 * D * 2;                   // bytes of a 16-bit tile
+  static constexpr int kCodes = 16384;                        // place of E4M3 codes in a stage
+  static constexpr int kStage = kFP8 && D == 64 ? 24576 : kTile;
+  static constexpr int kSt = 131072 / kStage;                 // 4, 5 or 8 stages
+  static constexpr int kTail = kBlockSize * D * 2;
+  alignas(1024) uint8_t ring[kSt][kStage];
+  alignas(1024) uint8_t q[2][kTile];
+  alignas(1024) uint8_t tail[2][kTail];
+  long long start[kMaxSeqs + 1];  // of each sequence on the line of work
+  int qlen[kMaxSeqs], len[kMaxSeqs], q0[kMaxSeqs];
+  long long scan[16];
+  float2 other[128];  // maximum and sum of the odd key tiles
+  CrossItem item[kItems];
+  uint64_t item_full[kItems], item_read[kItems];
+  uint64_t landed[kSt], full[kSt], empty[kSt];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_ready[2], p_ready[2], o_done[2], o_free[2];
+  uint64_t other_ready;
+  uint64_t tail_full[2], tail_free[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
+
+// The next item, for a whole warp; false when the wait gave up.
+template <class SM>
+__device__ __forceinline__ bool take(SM& sm, uint32_t n, CrossItem& x, volatile int* abort,
+                                     unsigned long long lim) {
+  const int slot = n % kItems;
+  if (!__all_sync(kFull, wait_for(&sm.item_full[slot], (n / kItems) & 1, abort, lim))) return false;
+  x = sm.item[slot];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.item_read[slot]);
+  return true;
+}
+
+// ---- the line of work --------------------------------------------------------------------
+// Lengths of the sequences and where each begins on the line; ends with the CTA
+// synchronised.
+template <int D, bool kFP8>
+__device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs& c,
+                                            CrossSmem<D, kFP8>& sm) {
+  using SM = CrossSmem<D, kFP8>;
+  constexpr int kThreads = cross_threads(kFP8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < SM::kSt; ++s) {
+      mbar_init(&sm.landed[s], kTmaWarps);
+      mbar_init(&sm.full[s], kFP8 ? kConverts : kTmaWarps);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sm.q_full[x], 1);
+      mbar_init(&sm.q_empty[x], 1);
+      mbar_init(&sm.s_ready[x], 1);
+      mbar_init(&sm.p_ready[x], 4);
+      mbar_init(&sm.o_done[x], 1);
+      mbar_init(&sm.o_free[x], 4);
+      mbar_init(&sm.tail_full[x], 1);
+      mbar_init(&sm.tail_free[x], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sm.item_full[i], 1);
+      // the softmax warps, the issuer, the producers and the converters
+      mbar_init(&sm.item_read[i], kSoft + 1 + kTmaWarps + (kFP8 ? kConverts : 0));
+    }
+    mbar_init(&sm.other_ready, 4);
+    mbar_init(&sm.mma_done, 1);
+    sm.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kIssuer) {
+    tc::tmem_alloc(&sm.tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  const int S = p.num_seqs, tid = threadIdx.x;
+  const int chunk = (S + kThreads - 1) / kThreads;
+  const int cap = min(p.max_blocks_per_seq * kBlockSize, p.max_context);
+  const int rpt = kRowsM / p.group;
+  auto work = [&](int q, int len) -> long long {
+    const int tiles = (q + rpt - 1) / rpt, nk = tiles_of(len);
+    return (long long)p.num_kv_heads * ((long long)(tiles >> 1) * (nk * kCost2 + kCostUnit) +
+                                        (tiles & 1) * (nk * kCost1 + kCostUnit));
+  };
+  long long local = 0;
+  for (int i = 0; i < chunk; ++i) {
+    const int sq = tid * chunk + i;
+    if (sq < S) {
+      const int q0 = __ldg(p.query_start_loc + sq), q1 = __ldg(p.query_start_loc + sq + 1);
+      int len = __ldg(p.context_lens + sq), q = q1 - q0;
+      if (len < 0 || len > cap || q0 < 0 || q1 < q0 || q1 > p.num_rows || q > c.max_q) {
+        if (blockIdx.x == 0) flag_error(p.errors, PKV_DEVERR_CONTEXT);
+        len = len < 0 ? 0 : min(len, cap);
+        q = q0 < 0 || q1 < q0 || q1 > p.num_rows ? 0 : min(q, c.max_q);
+      }
+      sm.qlen[sq] = q;
+      sm.len[sq] = len;
+      sm.q0[sq] = q0;
+      local += work(q, len);
+    }
+  }
+  long long incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sm.scan[warp] = incl;
+  __syncthreads();
+  long long run = incl - local;
+  for (int w = 0; w < warp; ++w) run += sm.scan[w];
+  for (int i = 0; i < chunk; ++i) {
+    const int sq = tid * chunk + i;
+    if (sq < S) {
+      sm.start[sq] = run;
+      run += work(sm.qlen[sq], sm.len[sq]);
+    }
+  }
+  if (tid == kThreads - 1) sm.start[S] = run;  // (the last thread's run ends at the total)
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+}
+
+// The maker: this CTA's part of the line as items, the V rows of partial last blocks, and
+// which unit the part ends in.
+template <int D, bool kFP8>
+__device__ __forceinline__ void cross_maker(const AttnParams& p, const CrossArgs& c,
+                                            CrossSmem<D, kFP8>& sm) {
+  using SM = CrossSmem<D, kFP8>;
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  const int lane = threadIdx.x & 31, rpt = kRowsM / p.group, hkv = p.num_kv_heads;
+  const long long T = sm.start[p.num_seqs];
+  const int ctas = (int)max(min((long long)gridDim.x, T / kLeast), 1LL), cta = blockIdx.x;
+  long long w = cta < ctas ? T * cta / ctas : 0;
+  const long long w1 = cta < ctas ? T * (cta + 1) / ctas : 0;
+  int4 cut0 = make_int4(-1, 0, 0, 0), cut1 = cut0;
+  int s = 0;
+  if (w < w1) {  // the last sequence that begins at or before w
+    int hi = p.num_seqs - 1;
+    while (s < hi) {
+      const int mid = (s + hi + 1) >> 1;
+      if (sm.start[mid] <= w) s = mid; else hi = mid - 1;
+    }
+  }
+  uint32_t n = 0, ntail = 0;
+  bool ok = true;
+  for (; ok; ++n) {
+    CrossItem x = {};
+    while (w < w1) {
+      const int q = sm.qlen[s], len = sm.len[s], nk = tiles_of(len);
+      const int tiles = (q + rpt - 1) / rpt;
+      const long long u2 = (long long)nk * kCost2 + kCostUnit, u1 = (long long)nk * kCost1 + kCostUnit;
+      const long long twos = (long long)hkv * (tiles >> 1), off = w - sm.start[s];
+      const bool two = off < twos * u2;
+      const long long k = two ? off / u2 : twos + (off - twos * u2) / u1;
+      const long long u0 = sm.start[s] + (two ? k * u2 : twos * u2 + (k - twos) * u1);
+      const long long u = two ? u2 : u1;
+      const int cost = two ? kCost2 : kCost1;
+      // tiles whose place on the line is in [w, w1)
+      auto tile_at = [&](long long at) {
+        const long long d = at - u0 - kCostUnit;
+        return d <= 0 ? 0 : (int)min((d + cost - 1) / cost, (long long)nk);
+      };
+      const int a = w <= u0 ? 0 : tile_at(w), b = w1 >= u0 + u ? nk : tile_at(w1);
+      const bool begins = w <= u0;
+      w = u0 + u;
+      const int seq = s;
+      while (s + 1 < p.num_seqs && sm.start[s + 1] <= w) ++s;
+      if (a >= b && !(nk == 0 && begins)) continue;
+      const int pair = (int)(k / hkv);
+      x.live = 1;
+      x.seq = seq;
+      x.kvh = (int)(k % hkv);
+      x.len = len;
+      x.q0 = sm.q0[seq];
+      x.t0[0] = 2 * pair * rpt;
+      x.t0[1] = x.t0[0] + rpt;
+      x.nt[0] = min(rpt, q - x.t0[0]);
+      x.nt[1] = two ? min(rpt, q - x.t0[1]) : 0;
+      x.kt0 = a;
+      x.kt1 = b;
+      x.part = a == 0 && b == nk ? -1 : 2 * cta + (a == 0 ? 1 : 0);
+      x.tail = !kFP8 && b == nk && (len & (kBlockSize - 1)) != 0 ? ((len - 1) % kTileKeys) / kBlockSize
+                                                                  : -1;
+      if (a == 0 && b < nk) {
+        // the unit goes on in the parts up to the one with its last tile
+        const long long last = u0 + kCostUnit + (long long)(nk - 1) * cost;
+        cut0 = make_int4((int)(((last + 1) * ctas + T - 1) / T - 1), x.q0 + x.t0[0], x.nt[0], x.nt[1]);
+        cut1 = make_int4(x.kvh, 0, 0, 0);
+      }
+      break;
+    }
+    bool good = true;
+    if (lane == 0) {
+      const int slot = n % kItems;
+      if (n >= kItems) good = wait_for(&sm.item_read[slot], ((n / kItems) - 1) & 1, abort, lim);
+      if (good) {
+        sm.item[slot] = x;
+        mbar_arrive(&sm.item_full[slot]);
+      }
+    }
+    ok = __shfl_sync(kFull, (int)good, 0) != 0;
+    if (!ok || !x.live) break;
+    if (x.tail >= 0) {
+      // V rows of the step that holds the partial block, rows past the states as zeros (in
+      // the product 0 * NaN would be NaN), with the ring's swizzle
+      const int buf = ntail & 1;
+      if (lane == 0 && ntail >= 2) good = wait_for(&sm.tail_free[buf], ((ntail >> 1) - 1) & 1, abort, lim);
+      ok = __shfl_sync(kFull, (int)good, 0) != 0;
+      if (!ok) break;
+      constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+      const int b = (x.len - 1) / kBlockSize;
+      const int blk = __ldg(p.block_tables + (size_t)x.seq * p.max_blocks_per_seq + b);
+      const bool in = blk >= 0 && blk < p.num_blocks;
+#pragma unroll
+      for (int i = 0; i < kBlockSize * kChunks / 32; ++i) {
+        const int e = lane + 32 * i, r = e / kChunks, ch = e % kChunks;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (in && b * kBlockSize + r < x.len)
+          v = __ldg(reinterpret_cast<const uint4*>(
+                        p.v_cache + (((size_t)blk * hkv + x.kvh) * kBlockSize + r) * (kChunks * 16)) + ch);
+        *reinterpret_cast<uint4*>(&sm.tail[buf][0] + (ch >> 3) * (SM::kTail / 2) + r * 128 +
+                                  (((ch & 7) ^ (r & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.tail_full[buf]);
+      ++ntail;
+    }
+  }
+  if (lane == 0) {
+    if (!ok) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+    if (c.cuts) {
+      c.cuts[2 * cta] = cut0;
+      c.cuts[2 * cta + 1] = cut1;
+    }
+  }
+}
+
+// ---- loads ---------------------------------------------------------------------------------
+// Order of a unit's tiles in the ring, as the issuer takes them: with two query tiles K0, V0,
+// K1, V1, ...; with one K0, K1, V0, K2, V1, ...
+template <int D, bool kFP8>
+__device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossArgs& c,
+                                               CrossSmem<D, kFP8>& sm, const CUtensorMap& tm_k,
+                                               const CUtensorMap& tm_v, const CUtensorMap& tm_q,
+                                               int kv_rows, int pw) {
+  using SM = CrossSmem<D, kFP8>;
+  constexpr int kSt = SM::kSt;
+  constexpr int kRow = D * (kFP8 ? 1 : 2);          // bytes of a cache row
+  constexpr int kBoxRow = kRow < 128 ? kRow : 128;  // bytes of a row in a box
+  constexpr int kLoad = kTileKeys * kRow / kTmaWarps;
+  uint64_t* const bars = kFP8 ? sm.landed : sm.full;
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  const int lane = threadIdx.x & 31, g = p.group;
+  const bool my_lane = (lane & 1) == pw;            // blocks pw, pw + 2, ... of a tile
+  uint8_t* const ring = &sm.ring[0][0];
+  uint32_t pos = 0, nq = 0;
+  bool ok = true;
+  CrossItem x = {};
+  auto fetch = [&](int ch) -> int {                 // table entry of block 32 ch + lane
+    const int b = 32 * ch + lane;
+    return b < (x.len + kBlockSize - 1) / kBlockSize
+               ? __ldg(p.block_tables + (size_t)x.seq * p.max_blocks_per_seq + b)
+               : kBeyond;
+  };
+  auto to_row = [&](int blk) -> int {
+    if (blk == kBeyond) return kv_rows;             // past the pool: the box reads zeros
+    if (blk >= 0 && blk < p.num_blocks) return (blk * p.num_kv_heads + x.kvh) * kBlockSize;
+    flag_error(p.errors, PKV_DEVERR_BLOCK_ID);
+    return kv_rows;
+  };
+  auto issue = [&](int t, int row, bool is_v) -> bool {
+    const int st = pos % kSt;
+    // test hook: these boxes are never issued, so every wait for the tile runs out
+    const bool skip = pw == 0 && blockIdx.x == 0 && p.skip_copy > 0 && pos + 1 == (uint32_t)p.skip_copy;
+    bool good = true;
+    if (lane == 0) {
+      if (pos >= (uint32_t)kSt) good = wait_for(&sm.empty[st], ((pos / kSt) - 1) & 1, abort, lim);
+      if (good && !skip) mbar_arrive_expect_tx(&bars[st], kLoad);
+    }
+    if (!__shfl_sync(kFull, (int)good, 0)) return false;
+    if (!skip && (lane >> 3) == (t & 3) && my_lane) {
+      uint8_t* dst = ring + (size_t)st * SM::kStage + (kFP8 ? SM::kCodes : 0) +
+                     (lane & 7) * (kBlockSize * kBoxRow);
+      const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+      tc::tma_load_2d(dst, map, 0, row, &bars[st]);
+      if (kRow > 128) tc::tma_load_2d(dst + kHalf, map, 64, row, &bars[st]);
+    }
+    __syncwarp();
+    ++pos;
+    return true;
+  };
+  for (uint32_t n = 0; ok; ++n) {
+    ok = take(sm, n, x, abort, lim);
+    if (!ok || !x.live) break;
+    if (x.kt0 == x.kt1) continue;
+    const bool two = x.nt[1] > 0;
+    if (pw == 0) {
+      bool good = true;
+      for (int qt = 0; qt < (two ? 2 : 1); ++qt, ++nq) {
+        const int b = nq & 1;
+        if (lane == 0 && good) {
+          if (nq >= 2) good = wait_for(&sm.q_empty[b], ((nq >> 1) - 1) & 1, abort, lim);
+          if (good) {
+            uint8_t* dq = &sm.q[b][0];
+            mbar_arrive_expect_tx(&sm.q_full[b], c.box_tokens * g * D * 2);
+            const int tok = x.q0 + x.t0[qt];
+            tc::tma_load_3d(dq, &tm_q, 0, x.kvh * g, tok, &sm.q_full[b]);
+            if (D > 64) tc::tma_load_3d(dq + kHalf, &tm_q, 64, x.kvh * g, tok, &sm.q_full[b]);
+          }
+        }
+      }
+      ok = __shfl_sync(kFull, (int)good, 0) != 0;
+    }
+    // block rows of two chunks of 32 blocks (four key tiles), which K and V tiles are in,
+    // and the next one's entries, read ahead
+    int c0 = -1, c1 = -1, row0 = kv_rows, row1 = kv_rows;
+    int pre = x.kt0 >> 2, pre_raw = fetch(pre);
+    auto row_for = [&](int t) -> int {
+      const int ch = t >> 2;
+      if (c0 == ch) return row0;
+      if (c1 == ch) return row1;
+      const int r = to_row(pre == ch ? pre_raw : fetch(ch));
+      if (c0 < c1) {
+        c0 = ch;
+        row0 = r;
+      } else {
+        c1 = ch;
+        row1 = r;
+      }
+      pre = ch + 1;
+      pre_raw = 4 * pre < x.kt1 ? fetch(pre) : kBeyond;
+      return r;
+    };
+    if (two) {
+      for (int t = x.kt0; ok && t < x.kt1; ++t)
+        ok = issue(t, row_for(t), false) && issue(t, row_for(t), true);
+    } else {
+      if (ok) ok = issue(x.kt0, row_for(x.kt0), false);
+      for (int t = x.kt0; ok && t < x.kt1; ++t) {
+        if (t + 1 < x.kt1) ok = issue(t + 1, row_for(t + 1), false);
+        if (ok) ok = issue(t, row_for(t), true);
+      }
+    }
+  }
+  if (!ok && lane == 0) {
+    flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+    // tiles and queries still on their way land before the CTA goes away
+    for (uint32_t y = pos > (uint32_t)kSt ? pos - kSt : 0; y < pos; ++y)
+      mbar_wait(&bars[y % kSt], (y / kSt) & 1, 10000000ull);
+    if (pw == 0)
+      for (uint32_t y = nq > 2 ? nq - 2 : 0; y < nq; ++y)
+        mbar_wait(&sm.q_full[y & 1], (y >> 1) & 1, 10000000ull);
+  }
+}
+
+// Converter cw of an E4M3 cache: each tile that has landed, in ring order, from codes
+// [128 rows][D bytes] at kCodes of its stage to 16-bit elements, [D / 64 halves][128 rows]
+// [128 bytes] with the 128-byte swizzle; V rows past the states as zeros.  (head_dim 128:
+// row r of the codes lies where row r of the second half will, and a warp reads whole rows
+// before it writes them.)
+template <class QT, int D>
+__device__ __forceinline__ void cross_converter(const AttnParams& p, CrossSmem<D, true>& sm, int cw) {
+  using SM = CrossSmem<D, true>;
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  constexpr int kLanes = D / 16;      // 16-code chunks, and lanes, per row
+  constexpr int kRows = 32 / kLanes;  // rows a turn
+  const int lane = threadIdx.x & 31, ch = lane % kLanes;
+  uint32_t pos = 0;
+  bool ok = true;
+  CrossItem x = {};
+  auto convert = [&](int rows) -> bool {
+    const int st = pos % SM::kSt;
+    if (!__all_sync(kFull, wait_for(&sm.landed[st], (pos / SM::kSt) & 1, abort, lim))) return false;
+    ++pos;
+    uint8_t* tile = &sm.ring[st][0];
+    auto codes = [&](int u) {
+      const int r = kRows * u + lane / kLanes;
+      return *reinterpret_cast<const uint4*>(tile + SM::kCodes + r * D +
+                                             ((D == 128 ? ch ^ (r & 7) : ch) << 4));
+    };
+    uint4 w = codes(cw);
+#pragma unroll 1
+    for (int u = cw; u < kTileKeys / kRows; u += kConverts) {
+      const int r = kRows * u + lane / kLanes;
+      uint4 nw = w;
+      if (u + kConverts < kTileKeys / kRows) nw = codes(u + kConverts);
+      if (r >= rows) w = make_uint4(0, 0, 0, 0);
+      // (the halves' lanes store their two chunks in opposite order: eight lanes hit eight
+      // different bank groups)
+      const bool up = ch >> 2;
+      const uint32_t v[4] = {up ? w.z : w.x, up ? w.w : w.y, up ? w.x : w.z, up ? w.y : w.w};
+      uint4 a, b;
+      widen16<QT>(v, &a, &b);
+      __syncwarp();  // the rows have been read
+      uint8_t* d = tile + (ch >> 2) * kHalf + r * 128;
+      const int k0 = (2 * (ch & 3) + (up ? 1 : 0)) ^ (r & 7);
+      *reinterpret_cast<uint4*>(d + (k0 << 4)) = a;
+      *reinterpret_cast<uint4*>(d + ((k0 ^ 1) << 4)) = b;
+      w = nw;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.full[st]);
+    return true;
+  };
+  for (uint32_t n = 0; ok; ++n) {
+    ok = take(sm, n, x, abort, lim);
+    if (!ok || !x.live) break;
+    const bool two = x.nt[1] > 0;
+    auto rows = [&](int t) { return min(x.len - t * kTileKeys, kTileKeys); };
+    if (!two && x.kt0 < x.kt1) ok = convert(kTileKeys);
+    for (int t = x.kt0; ok && t < x.kt1; ++t) {
+      if (two || t + 1 < x.kt1) ok = convert(kTileKeys);
+      if (ok) ok = convert(rows(t));
+    }
+  }
+  if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+}
+
+// ---- MMA issuer ------------------------------------------------------------------------------
+// Two query tiles, per key tile t: P_a(t) V(t), S_a(t+1), P_b(t) V(t), S_b(t+1); one: S_0(0),
+// S_1(1), then P_x(t) V(t), S_x(t+2) with x = t & 1.  The whole warp runs the loop, so that
+// counters and descriptors are the same in all lanes; one elected lane issues.
+template <class QT, int D, bool kFP8>
+__device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, kFP8>& sm, uint32_t tmem) {
+  using SM = CrossSmem<D, kFP8>;
+  constexpr int kSt = SM::kSt;
+  constexpr uint32_t kAB = std::is_same<QT, BF16>::value ? 1u : 0u;
+  constexpr uint32_t kIdescS = tc::idesc_f16(kAB, 0, 0, 128, kTileKeys);
+  constexpr uint32_t kIdescO = tc::idesc_f16(kAB, 0, 1, 128, D);
+  constexpr uint64_t kStage = SM::kStage >> 4;
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  const bool leader = tc::elect_one();
+  auto commit = [&](uint64_t* bar) {
+    if (leader) tc::mma_commit(bar);
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __shfl_sync(kFull, (int)wait_bar(bar, parity, abort, lim), 0) != 0;
+  };
+  const uint64_t dq[2] = {tc::smem_desc(smem_u32(&sm.q[0][0]), 16, 1024, tc::kLayoutSw128),
+                          tc::smem_desc(smem_u32(&sm.q[1][0]), 16, 1024, tc::kLayoutSw128)};
+  const uint64_t dk0 = tc::smem_desc(smem_u32(&sm.ring[0][0]), 16, 1024, tc::kLayoutSw128);
+  const uint64_t dv0 = tc::smem_desc(smem_u32(&sm.ring[0][0]), kHalf, 1024, tc::kLayoutSw128);
+  const uint64_t dt0 = tc::smem_desc(smem_u32(&sm.tail[0][0]), SM::kTail / 2, 1024, tc::kLayoutSw128);
+  uint32_t pos = 0, np[2] = {0, 0}, nit[2] = {0, 0}, nq = 0, ntail = 0;
+  bool ok = true;
+  CrossItem x = {};
+  auto acquire = [&](int& st) -> bool {
+    st = pos % kSt;
+    const bool r = wait(&sm.full[st], (pos / kSt) & 1);
+    ++pos;
+    if (r) tc::fence_after_sync();
+    return r;
+  };
+  // scores of the query tile in buffer b, for softmax warpgroup y
+  auto scores = [&](int y, int b, int st) {
+    if (leader) issue_mods_scores<D>(tmem + y * 128, b ? dq[1] : dq[0], dk0 + st * kStage, kIdescS);
+    commit(&sm.s_ready[y]);
+  };
+  auto product = [&](int y, int st, int t, bool first, bool last) -> bool {
+    if (!wait(&sm.p_ready[y], np[y] & 1)) return false;
+    ++np[y];
+    if (first && nit[y] >= 1 && !wait(&sm.o_free[y], (nit[y] - 1) & 1))
+      return false;  // the previous item's O has been read out
+    const int ts = t == x.kt1 - 1 ? x.tail : -1;
+    if (ts >= 0 && !wait(&sm.tail_full[ntail & 1], (ntail >> 1) & 1)) return false;
+    tc::fence_after_sync();
+    if (leader)
+      issue_pv(tmem + kColO + y * 128, tmem + y * 128, dv0 + st * kStage,
+               dt0 + (ntail & 1) * (SM::kTail >> 4), ts, !first, kIdescO);
+    if (last) commit(&sm.o_done[y]);
+    return true;
+  };
+  for (uint32_t n = 0; ok; ++n) {
+    ok = take(sm, n, x, abort, lim);
+    if (!ok || !x.live) break;
+    if (x.kt0 == x.kt1) {  // nothing to multiply: the rows are zeros
+      continue;
+    }
+    const int t0 = x.kt0, t1 = x.kt1;
+    int kst = 0, vst = 0;
+    if (x.nt[1] > 0) {
+      const int b0 = nq & 1, b1 = b0 ^ 1;
+      ok = wait(&sm.q_full[b0], (nq >> 1) & 1) && wait(&sm.q_full[b1], ((nq + 1) >> 1) & 1);
+      nq += 2;
+      if (ok) ok = acquire(kst);
+      if (ok) {
+        scores(0, b0, kst);
+        if (t0 + 1 == t1) commit(&sm.q_empty[b0]);
+        scores(1, b1, kst);
+        if (t0 + 1 == t1) commit(&sm.q_empty[b1]);
+        commit(&sm.empty[kst]);
+      }
+      for (int t = t0; ok && t < t1; ++t) {
+        const bool more = t + 1 < t1;
+        ok = acquire(vst) && product(0, vst, t, t == t0, !more);
+        if (ok && more) {
+          ok = acquire(kst);
+          if (ok) scores(0, b0, kst);
+          if (ok && t + 2 == t1) commit(&sm.q_empty[b0]);
+        }
+        if (ok) ok = product(1, vst, t, t == t0, !more);
+        if (!ok) break;
+        commit(&sm.empty[vst]);
+        if (more) {
+          scores(1, b1, kst);
+          if (t + 2 == t1) commit(&sm.q_empty[b1]);
+          commit(&sm.empty[kst]);
+        }
+      }
+      ++nit[0];
+      ++nit[1];
+    } else {
+      const int b = nq & 1;
+      ok = wait(&sm.q_full[b], (nq >> 1) & 1);
+      ++nq;
+      auto next_scores = [&](int t) -> bool {
+        if (!acquire(kst)) return false;
+        scores((t - t0) & 1, b, kst);
+        commit(&sm.empty[kst]);
+        if (t == t1 - 1) commit(&sm.q_empty[b]);
+        return true;
+      };
+      if (ok) ok = next_scores(t0);
+      if (ok && t0 + 1 < t1) ok = next_scores(t0 + 1);
+      for (int t = t0; ok && t < t1; ++t) {
+        ok = acquire(vst) && product((t - t0) & 1, vst, t, t < t0 + 2, t >= t1 - 2);
+        if (!ok) break;
+        commit(&sm.empty[vst]);
+        if (t + 2 < t1) ok = next_scores(t + 2);
+      }
+      ++nit[0];
+      if (t1 - t0 > 1) ++nit[1];
+    }
+    if (ok && x.tail >= 0) {
+      commit(&sm.tail_free[ntail & 1]);
+      ++ntail;
+    }
+  }
+  if (!ok && leader) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+  commit(&sm.mma_done);
+  mbar_wait(&sm.mma_done, 0, 100000000ull);
+}
+
+// ---- softmax and epilogue ------------------------------------------------------------------
+// Thread = row of a query tile.  Warpgroup y: query tile y, or (one query tile) the even or
+// odd key tiles.
+template <class QT, int D, bool kFP8>
+__device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossArgs& c,
+                                              CrossSmem<D, kFP8>& sm, uint32_t tmem) {
+  using OutT = typename QT::T;
+  volatile int* abort = &sm.abort;
+  const unsigned long long lim = wait_limit(p);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int y = warp >> 2, g = p.group, r = threadIdx.x & 127;
+  const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t s_col = tmem + lane_off + y * 128;
+  const uint32_t o_col = tmem + lane_off + kColO + y * 128;
+  // scores are scaled inside the exponent; a negative scale is folded in by negating
+  // them, a zero one taken as 1e-30 (2^(s * 1e-30) rounds to 1)
+  const bool neg = p.q_scale < 0.0f;
+  const float qa = fmaxf(fabsf(p.q_scale), 1e-30f);
+  // with fewer registers (E4M3 caches) the scores are read twice, for the maxima and for the
+  // weights, instead of held
+  constexpr bool kTwice = kFP8;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(kFull, wait_for(bar, parity, abort, lim)) != 0;
+  };
+  uint32_t ns = 0, nit = 0, nother = 0;  // steps and items of this warpgroup; joins
+  bool ok = true;
+  for (uint32_t n = 0;; ++n) {
+    // the item stays in shared memory until the warp is done with it (its fields would cost
+    // the loop registers)
+    ok = wait(&sm.item_full[n % kItems], (n / kItems) & 1);
+    const CrossItem& x = sm.item[n % kItems];
+    if (!ok || !x.live) break;
+    auto done = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_read[n % kItems]);
+    };
+    const bool two = x.nt[1] > 0;
+    const int qt = two ? y : 0, kt0 = x.kt0, kt1 = x.kt1;
+    const int rows = x.nt[qt] * g;                    // rows past the tokens are never stored
+    const bool idle = 32 * (warp & 3) >= rows;        // the warp has no others
+    // the row's place in the output, in heads
+    auto head_of = [&]() { return (x.q0 + x.t0[qt] + r / g) * p.num_heads + x.kvh * g + r % g; };
+    if (kt0 == kt1) {  // no states
+      if (r < rows && (two || y == 0)) {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<OutT*>(p.out) + (size_t)head_of() * D);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
+      }
+      done();
+      continue;
+    }
+    const int step = two ? 1 : 2, first = two ? kt0 : kt0 + y;
+    if (first >= kt1) {  // one key tile: the other warpgroup's
+      done();
+      continue;
+    }
+    int left = x.len - first * kTileKeys;             // states from the tile on
+    float m_run = -INFINITY;
+    float2 l2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l2[i] = make_float2(0.0f, 0.0f);
+    for (int t = first; t < kt1; t += step, left -= step * kTileKeys, ++ns) {
+      ok = wait(&sm.s_ready[y], ns & 1);
+      if (!ok) break;
+      if (!idle) {
+        tc::fence_after_sync();
+        // scores of 32 states from k on, masked and with the scale's sign
+        auto scores = [&](int k, float* sv) {
+          if (neg) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sv[i] = -sv[i];
+          }
+          if (left < kTileKeys) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sv[i] = k + i < left ? sv[i] : -INFINITY;
+          }
+        };
+        float mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+        auto most = [&](const float* sv) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) mx[(i >> 1) & 7] = fmax3(mx[(i >> 1) & 7], sv[i], sv[i + 1]);
+        };
+        float sv[kTwice ? 32 : kTileKeys];
+        if constexpr (kTwice) {
+#pragma unroll
+          for (int k = 0; k < kTileKeys; k += 32) {
+            tc::tmem_ld32(s_col + k, sv);
+            tc::tmem_wait_ld();
+            scores(k, sv);
+            most(sv);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kTileKeys; k += 32) tc::tmem_ld32(s_col + k, sv + k);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < kTileKeys; k += 32) {
+            scores(k, sv + k);
+            most(sv + k);
+          }
+        }
+        const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * qa;
+        const bool need = mt > m_run + kRescaleAt;
+        float alpha = 1.0f;
+        if (need) {
+          alpha = t == first ? 0.0f : fast_exp2(m_run - mt);
+          m_run = mt;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l2[i] = __fmul2_rn(l2[i], make_float2(alpha, alpha));
+        }
+        const float m = m_run == -INFINITY ? 0.0f : m_run;  // (2^(-inf - 0) is 0)
+        const float2 f2 = make_float2(qa, qa), m2 = make_float2(-m, -m);
+#pragma unroll
+        for (int k = 0; k < kTileKeys; k += 32) {
+          float* const s = kTwice ? sv : sv + k;
+          if constexpr (kTwice) {
+            tc::tmem_ld32(s_col + k, sv);
+            tc::tmem_wait_ld();
+            scores(k, sv);
+          }
+          float pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 z = __ffma2_rn(make_float2(s[e], s[e + 1]), f2, m2);
+            const float2 w = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+            l2[(e >> 1) & 3] = __fadd2_rn(l2[(e >> 1) & 3], w);
+            pk[e >> 1] = __uint_as_float(pack2<QT>(w.x, w.y));
+          }
+          tc::tmem_st16(s_col + k / 2, pk);
+        }
+        // the product of this tile adds onto O, which is complete up to the one before (the
+        // scores were issued behind its product)
+        if (t > first && __any_sync(kFull, need)) {
+#pragma unroll 1
+          for (int k = 0; k < D; k += 32) {
+            float ov[32];
+            tc::tmem_ld32(o_col + k, ov);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+            tc::tmem_st32(o_col + k, ov);
+          }
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_ready[y]);
+    }
+    if (!ok) break;
+    ok = wait(&sm.o_done[y], nit & 1);
+    ++nit;
+    if (!ok) break;
+    tc::fence_after_sync();
+    float l = ((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y)) + ((l2[2].x + l2[2].y) + (l2[3].x + l2[3].y));
+    float a0 = 1.0f, a1 = 0.0f;
+    const bool join = !two && kt1 - kt0 > 1;
+    if (join) {
+      if (y == 1) {  // its maxima, sums and O are for the other warpgroup
+        sm.other[r] = make_float2(m_run, l);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.other_ready);
+        done();
+        continue;
+      }
+      ok = wait(&sm.other_ready, nother & 1);
+      ++nother;
+      if (!ok) break;
+      tc::fence_after_sync();
+      const float2 o = sm.other[r];
+      const float m = fmaxf(m_run, o.x), mm = m == -INFINITY ? 0.0f : m;
+      a0 = fast_exp2(m_run - mm);
+      a1 = fast_exp2(o.x - mm);
+      l = l * a0 + o.y * a1;
+      m_run = m;
+    }
+    const bool none = l == 0.0f;  // (every score -inf)
+    const float inv = p.v_scale / l;
+    a0 *= inv;
+    a1 *= inv;
+    // 32 dimensions of the row from k on, divided and (one query tile) joined
+    auto result = [&](int k, float* ov) {
+      tc::tmem_ld32(o_col + k, ov);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) ov[e] *= a0;
+      if (join) {
+#pragma unroll
+        for (int h = 0; h < 32; h += 16) {
+          float ow[16];
+          tc::tmem_ld16(o_col + 128 + k + h, ow);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) ov[h + e] = fmaf(ow[e], a1, ov[h + e]);
+        }
+      }
+    };
+    const int part = x.part;
+    if (!idle) {
+      if (part >= 0) {
+        const int at = part * c.part_rows + qt * 128 + r;
+        float4* o = reinterpret_cast<float4*>(p.o_part + (size_t)at * D);
+        if (r < rows) p.lse[at] = none ? -INFINITY : m_run + log2f(l);
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+          float ov[32];
+          result(k, ov);
+          if (r < rows) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              o[(k + e) / 4] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                    : make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+          }
+        }
+      } else {
+        // four lanes exchange their rows' 16-byte pieces, so that they store 64 contiguous
+        // bytes of one row at a time
+        const int head = r < rows ? head_of() : -1;
+        int place[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) place[i] = __shfl_sync(kFull, head, (lane & 28) + i);
+        const bool up2 = lane & 2, up1 = lane & 1;
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+          float ov[32];
+          result(k, ov);
+          uint4 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = make_uint4(pack2<QT>(ov[8 * i], ov[8 * i + 1]), pack2<QT>(ov[8 * i + 2], ov[8 * i + 3]),
+                              pack2<QT>(ov[8 * i + 4], ov[8 * i + 5]), pack2<QT>(ov[8 * i + 6], ov[8 * i + 7]));
+          auto swap = [&](uint4& a, uint4& b, bool up, int mask) {  // a of the upper lane for b of the lower
+            uint4 t = up ? a : b;
+            t.x = __shfl_xor_sync(kFull, t.x, mask);
+            t.y = __shfl_xor_sync(kFull, t.y, mask);
+            t.z = __shfl_xor_sync(kFull, t.z, mask);
+            t.w = __shfl_xor_sync(kFull, t.w, mask);
+            if (up) a = t; else b = t;
+          };
+          swap(w[0], w[2], up2, 2);
+          swap(w[1], w[3], up2, 2);
+          swap(w[0], w[1], up1, 1);
+          swap(w[2], w[3], up1, 1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (place[i] >= 0)
+              *reinterpret_cast<uint4*>(static_cast<OutT*>(p.out) + (size_t)place[i] * D + k +
+                                        8 * (lane & 3)) = w[i];
+        }
+      }
+    }
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sm.o_free[y]);
+      if (join) mbar_arrive(&sm.o_free[1]);
+    }
+    done();
+  }
+  if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+}
+
+template <class QT, int D, bool kFP8>
+__global__ void __launch_bounds__(cross_threads(kFP8), 1)
+    cross_kernel(const AttnParams p, const CrossArgs c, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
+                 int kv_rows) {
+  extern __shared__ uint8_t smem_raw[];
+  using SM = CrossSmem<D, kFP8>;
+  SM& sm = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  if (warp >= kTma && warp < kTma + kTmaWarps && (threadIdx.x & 31) == 0) {
+    tc::prefetch_tmap(&tm_k);
+    tc::prefetch_tmap(&tm_v);
+    tc::prefetch_tmap(&tm_q);
+  }
+  cross_setup<D, kFP8>(p, c, sm);
+  const uint32_t tmem = sm.tmem_base;
+  if (warp >= kSoft) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(cross_other_regs(kFP8)));
+    if (warp == kIssuer) cross_issuer<QT, D, kFP8>(p, sm, tmem);
+    else if (warp < kTma + kTmaWarps)
+      cross_producer<D, kFP8>(p, c, sm, tm_k, tm_v, tm_q, kv_rows, warp - kTma);
+    else if (warp == kMaker) cross_maker<D, kFP8>(p, c, sm);
+    else if constexpr (kFP8) cross_converter<QT, D>(p, sm, warp - kConvert);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(cross_soft_regs(kFP8)));
+    cross_softmax<QT, D, kFP8>(p, c, sm, tmem);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kIssuer) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of the unit that CTA blockIdx.x's part of the line ends in, if it ends
+// inside one: weights 2^(lse - max) of the parts, which CTA b wrote as its second partial and
+// the CTAs up to the last one as their first.  A warp per row.
+constexpr int kJoinThreads = 256;
+template <class QT, int D>
+__global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const AttnParams p, const CrossArgs c) {
+  using OutT = typename QT::T;
+  tc::grid_dependency_wait();
+  const int b = blockIdx.x, lane = threadIdx.x & 31;
+  const int4 cut = __ldcg(c.cuts + 2 * b);
+  if (cut.x < 0) return;
+  const int kvh = __ldcg(&c.cuts[2 * b + 1].x);
+  const int last = cut.x, g = p.group, rpt = kRowsM / g;
+  const int warps = gridDim.y * (kJoinThreads / 32);
+  for (int at = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); at < c.part_rows; at += warps) {
+    const int qt = at >> 7, r = at & 127;
+    if (r >= (qt ? cut.w : cut.z) * g) continue;
+    auto slot = [&](int i) { return (size_t)(2 * (b + i) + (i == 0 ? 1 : 0)) * c.part_rows + at; };
+    const int parts = last - b + 1;
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(p.lse + slot(i)));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    constexpr int kLanes = D / 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+      const float w = exp2f(__ldcg(p.lse + slot(i)) - m);
+      sum += w;
+      if (lane < kLanes) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.o_part + slot(i) * D) + lane);
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+      }
+    }
+    if (lane < kLanes) {
+      const float inv = 1.0f / sum;
+      OutT* o = static_cast<OutT*>(p.out) +
+                ((size_t)(cut.y + qt * rpt + r / g) * p.num_heads + kvh * g + r % g) * D + 4 * lane;
+      const uint2 w = make_uint2(pack2<QT>(acc.x * inv, acc.y * inv), pack2<QT>(acc.z * inv, acc.w * inv));
+      *reinterpret_cast<uint2*>(o) = w;
+    }
+  }
+}
+
+template <class QT, int D, bool kFP8>
+int launch_cross_typed(const AttnParams& p, const CrossArgs& c, int ctas, cudaStream_t stream) {
+  const bool bf16 = std::is_same<QT, BF16>::value;
+  const uint64_t kv_rows = (uint64_t)p.num_blocks * p.num_kv_heads * kBlockSize;
+  CUtensorMap tk, tv, tq;
+  const int type = kFP8 ? PKV_FP8_E4M3 : (bf16 ? PKV_BF16 : PKV_F16);
+  if (!make_map_rows(&tk, p.k_cache, kv_rows, D, type, kBlockSize) ||
+      !make_map_rows(&tv, p.v_cache, kv_rows, D, type, kBlockSize) ||
+      !make_map_heads(&tq, p.q, (uint64_t)p.num_rows, (uint32_t)p.num_heads, D, bf16,
+                      (uint32_t)p.group, (uint32_t)c.box_tokens))
+    return PKV_ERR_CUDA;
+  using SM = CrossSmem<D, kFP8>;
+  constexpr size_t smem = sizeof(SM) + 1024;
+  static_assert(smem <= 232448, "shared memory budget of one CTA");
+  static_assert(offsetof(SM, ring) % 1024 == 0 && offsetof(SM, q) % 1024 == 0 &&
+                    offsetof(SM, tail) % 1024 == 0 && SM::kStage % 1024 == 0 && SM::kTail % 1024 == 0,
+                "swizzled buffers must start on 1024-byte boundaries");
+  auto kern = cross_kernel<QT, D, kFP8>;
+  // the kernel's register shares add up to what its launch holds; with fewer its
+  // warpgroups would wait for registers without end
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
+  if (fa.numRegs != cross_launch_regs(kFP8)) return PKV_ERR_CUDA;
+  static std::atomic<unsigned long long> configured{0};
+  if (!smem_once(kern, smem, configured)) return PKV_ERR_CUDA;
+  kern<<<ctas, cross_threads(kFP8), smem, stream>>>(p, c, tk, tv, tq, (int)kv_rows);
+  if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+  if (!c.cuts) return PKV_OK;
+  // a CTA of the join for each part of the line and up to 32 rows
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, (c.part_rows + 31) / 32);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cross_join_kernel<QT, D>, p, c) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <int D>
+int launch_cross_dim(const AttnParams& p, const CrossArgs& c, int q_dtype, int kv_dtype, int ctas,
+                     cudaStream_t stream) {
+  const bool fp8 = kv_dtype == PKV_FP8_E4M3;
+  if (q_dtype == PKV_BF16)
+    return fp8 ? launch_cross_typed<BF16, D, true>(p, c, ctas, stream)
+               : launch_cross_typed<BF16, D, false>(p, c, ctas, stream);
+  return fp8 ? launch_cross_typed<F16, D, true>(p, c, ctas, stream)
+             : launch_cross_typed<F16, D, false>(p, c, ctas, stream);
+}
+
+}  // namespace
+}  // namespace cross_tc
+}  // namespace pkv
+
+#endif  // PKV_CROSS_TC_CUH
