@@ -58,6 +58,8 @@ __global__ void __launch_bounds__(kThreads)
 constexpr int kDeep = 8;        // rows a thread reads in a turn
 constexpr int kLongList = 96;   // from this many kept tokens a sequence on (on average), a CTA a unit
 
+constexpr long long kManyUnits = 608;  // below as many, CTAs' units are quarters or halves of rows
+
 struct CompactArgs {
   const int32_t *tables, *context, *base, *starts, *keep;
   int32_t* new_lens;
@@ -68,19 +70,21 @@ struct CompactArgs {
   uint32_t* errors;
 };
 
-template <int kWarps, int kRowBytes>
+template <int kWarps, int kRowBytes, int kPartBytes>
 __global__ void __launch_bounds__(kThreads)
     compact_kernel(const __grid_constant__ Caches caches, const CompactArgs a) {
   constexpr int kUnit = 32 * kWarps;             // threads of a unit
-  constexpr int kChunks = kRowBytes / 16;        // 16-byte chunks, and threads, of a row
+  constexpr int kParts = kRowBytes / kPartBytes; // units that share the rows
+  constexpr int kChunks = kPartBytes / 16;       // 16-byte chunks, and threads, of a row
   constexpr int kRows = kUnit / kChunks;         // rows read at once
   __shared__ int s_moved;
   const int t = threadIdx.x % kUnit;
   const long long unit = (long long)blockIdx.x * (kThreads / kUnit) + threadIdx.x / kUnit;
-  const int per_seq = a.caches * a.kv_heads;
+  const int per_seq = a.caches * a.kv_heads * kParts;
   const int s = (int)(unit / per_seq);
   if (s >= a.num_seqs) return;                   // (a CTA's units end together: kWarps = 8 has one)
-  const int of = (int)(unit % per_seq), cache = of / a.kv_heads, head = of % a.kv_heads;
+  const int of = (int)(unit % per_seq), part = of % kParts;
+  const int cache = of / kParts / a.kv_heads, head = of / kParts % a.kv_heads;
   auto any = [&](bool x) -> bool {
     if constexpr (kWarps == 1) return __any_sync(kFull, x);
     else return __syncthreads_or(x);
@@ -128,7 +132,8 @@ __global__ void __launch_bounds__(kThreads)
   }
   if (bad || shared) return;
   uint8_t* const rows = static_cast<uint8_t*>(caches.p[cache]) +
-                        (size_t)head * (kBlockSize * kRowBytes) + (t % kChunks) * 16;
+                        (size_t)head * (kBlockSize * kRowBytes) + part * kPartBytes +
+                        (t % kChunks) * 16;
   const size_t block_bytes = (size_t)a.kv_heads * (kBlockSize * kRowBytes);
   auto at = [&](int place) -> uint8_t* {  // NULL: in a block outside the pool
     const int blk = __ldg(table + place / kBlockSize);
@@ -160,16 +165,24 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <int kWarps>
-int launch_compact(const Caches& c, const CompactArgs& a, int row_bytes, cudaStream_t stream) {
-  const long long units = (long long)a.num_seqs * a.caches * a.kv_heads;
+template <int kWarps, int kRowBytes, int kPartBytes>
+int launch_compact(const Caches& c, const CompactArgs& a, cudaStream_t stream) {
+  const long long units = (long long)a.num_seqs * a.caches * a.kv_heads * (kRowBytes / kPartBytes);
   constexpr int kPer = kThreads / (32 * kWarps);
   const long long ctas = (units + kPer - 1) / kPer;
   if (ctas > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  if (row_bytes == 64) compact_kernel<kWarps, 64><<<(unsigned)ctas, kThreads, 0, stream>>>(c, a);
-  else if (row_bytes == 128) compact_kernel<kWarps, 128><<<(unsigned)ctas, kThreads, 0, stream>>>(c, a);
-  else compact_kernel<kWarps, 256><<<(unsigned)ctas, kThreads, 0, stream>>>(c, a);
+  compact_kernel<kWarps, kRowBytes, kPartBytes><<<(unsigned)ctas, kThreads, 0, stream>>>(c, a);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <int kRowBytes>
+int launch_compact_rows(const Caches& c, const CompactArgs& a, cudaStream_t stream) {
+  if (a.num_keep < (long long)kLongList * a.num_seqs)
+    return launch_compact<1, kRowBytes, kRowBytes>(c, a, stream);
+  if constexpr (kRowBytes > 64)
+    if ((long long)a.num_seqs * a.caches * a.kv_heads < kManyUnits)
+      return launch_compact<8, kRowBytes, 64>(c, a, stream);
+  return launch_compact<8, kRowBytes, kRowBytes>(c, a, stream);
 }
 
 // Every cache given, on a 16-byte boundary, and none overlapping another.
@@ -286,9 +299,10 @@ int pkv_compact_tokens(void* const* k_caches, void* const* v_caches, int num_lay
                         ref_counts, num_seqs, num_keep, num_kv_heads, max_blocks_per_seq,
                         num_blocks, 2 * n, l0 == 0, device_errors};
     const Caches c = caches_of(k_caches, v_caches, l0, n);
-    const int r = num_keep >= (long long)kLongList * num_seqs
-                      ? launch_compact<8>(c, a, row_bytes, static_cast<cudaStream_t>(stream))
-                      : launch_compact<1>(c, a, row_bytes, static_cast<cudaStream_t>(stream));
+    cudaStream_t on = static_cast<cudaStream_t>(stream);
+    const int r = row_bytes == 64    ? launch_compact_rows<64>(c, a, on)
+                  : row_bytes == 128 ? launch_compact_rows<128>(c, a, on)
+                                     : launch_compact_rows<256>(c, a, on);
     if (r != PKV_OK) return r;
   }
   return PKV_OK;

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a) {
 }
 
 // ---- resize ----------------------------------------------------------------------------
-// One cluster of eight CTAs, which can wait for each other in hardware and read each
+// One cluster of up to eight CTAs, which can wait for each other in hardware and read each
 // other's shared memory, so that the call is one launch:
 //   1  blocks behind the new lengths lose a reference
 //   2  what each sequence needs: a copy of a shared partial last block (how many of its
@@ -110,12 +110,14 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a) {
 //      and the blocks it opens
 //   3  prefix sums of the needs in batch order, and of the free blocks in the order of
 //      their ids; every CTA gets all the sequences' offsets
-//   4  the warp that meets the r-th free block gives it to the sequence whose needs hold r
+//   4  the warp that meets the r-th free block gives it to the sequence whose needs hold r.
+//      The pool is dealt out to the warps in small pieces, since the blocks handed out are
+//      those of its first ones
 // Every sum is one of integers and the hash table only counts and takes maxima, so the
 // result does not depend on the order of the atomics.  Bound by its dependent reads and
 // five cluster barriers for small batches, by reading the counts twice (up to the last
 // block handed out the second time) on eight processors for large pools.
-constexpr int kResizeCtas = 8;
+constexpr int kResizeCtas = 8;   // at most; one where that is enough (kOneCta...)
 constexpr int kResizeThreads = 1024;
 constexpr int kResizeWarps = kResizeThreads / 32;
 constexpr int kSat = 0x3fffffff;  // sums of needs end here; pools hold at most 2^30 - 1 blocks
@@ -127,9 +129,13 @@ struct ResizeArgs {
   const int32_t *rows, *cached, *lens;
   int32_t *granted, *new_blocks, *pairs;
   int num_seqs, num_rows, width, num_new, num_blocks;
-  int slots;  // of the hash table, in each CTA: a power of two, twice the sequences in all
+  int slots;   // of the hash table, in each CTA: a power of two, twice the sequences in all
+  int pieces;  // of the pool, and the blocks of each (a multiple of 128)
+  int piece;
   uint32_t* errors;
 };
+constexpr int kPieces = 8192;  // at most
+constexpr int kOneCtaSeqs = 512, kOneCtaBlocks = 32768;
 
 __device__ __forceinline__ int sat_add(int x, int y) { return min(x + y, kSat); }
 
@@ -151,28 +157,29 @@ __device__ __forceinline__ uint32_t free_bits(const int32_t* counts, int id, int
 
 struct ResizeShared {
   int warp_want[kResizeWarps], warp_open[kResizeWarps], warp_free[kResizeWarps];
-  int want[kResizeCtas], open[kResizeCtas], free[kResizeCtas];  // of every CTA
+  int want[kResizeCtas], open[kResizeCtas];  // of every CTA
+  int free;                                  // of the pool
 };
 
-__global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThreads)
-    resize_kernel(const ResizeArgs a) {
+__global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeArgs a) {
   extern __shared__ int s_dyn[];
   __shared__ ResizeShared sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int S = a.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cta = (int)cluster.block_rank();
+  const int cta = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
   unsigned* s_begin = reinterpret_cast<unsigned*>(s_dyn);  // [S + 1]: 2 * first rank + (copies?)
   int* s_open = s_dyn + S + 1;                             // [S + 1]: blocks opened before
   int* s_key = s_open + S + 1;                             // [slots] a block, -1: none
   int* s_holders = s_key + a.slots;                        // [slots] sequences that grow in it
   int* s_latest = s_holders + a.slots;                     // [slots] the last of them
+  int* s_free = s_latest + a.slots;                        // [pieces] free blocks, then those before
   for (int i = tid; i < a.slots; i += kResizeThreads) {
     s_key[i] = -1;
     s_holders[i] = 0;
     s_latest[i] = -1;
   }
   // ---- 1: this thread's sequences (consecutive in batch order), blocks given back ----------
-  const int per_cta = (S + kResizeCtas - 1) / kResizeCtas;
+  const int per_cta = (S + ctas - 1) / ctas;
   const int per = (per_cta + kResizeThreads - 1) / kResizeThreads;  // <= kPerThread
   const int i0 = cta * per_cta + tid * per;
   const int i1 = min(min(i0 + per, (cta + 1) * per_cta), S);
@@ -238,7 +245,7 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
       } else if ((held[k] = __ldcg(a.counts + b)) > 1) {
         tail[k] = b;
         // one table over the cluster (twice as many slots as sequences, so the search ends)
-        const int all = a.slots * kResizeCtas;
+        const int all = a.slots * ctas;
         int h = (int)(((uint32_t)b * 2654435761u) >> 7) & (all - 1);
         for (int n = 0; n < all; ++n, h = (h + 1) & (all - 1)) {
           int* key = cluster.map_shared_rank(s_key, h / a.slots) + h % a.slots;
@@ -251,19 +258,17 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
       }
     }
   }
-  // free blocks of this warp's part of the pool (whole groups of 128 ids)
-  const int groups = (a.num_blocks + 127) / 128;
-  const int per_warp = (groups + kResizeCtas * kResizeWarps - 1) / (kResizeCtas * kResizeWarps);
-  const long long lo_id = (long long)(cta * kResizeWarps + warp) * per_warp * 128;
-  const int id0 = (int)min(lo_id, (long long)a.num_blocks);
-  const int id1 = (int)min(lo_id + (long long)per_warp * 128, (long long)a.num_blocks);
+  // free blocks of this warp's pieces of the pool, for every CTA
   const bool vec = (reinterpret_cast<uintptr_t>(a.counts) & 15u) == 0;
-  int free_here = 0;
-#pragma unroll 8
-  for (int id = id0 + 4 * lane; id < id1; id += 128)
-    free_here += __popc(free_bits(a.counts, id, id1, vec));
-  free_here = (int)__reduce_add_sync(kFull, (unsigned)free_here);
-  if (lane == 0) sm.warp_free[warp] = free_here;
+  const int warps = ctas * kResizeWarps, me = warp * ctas + cta;
+#pragma unroll 4
+  for (int k = me; k < a.pieces; k += warps) {
+    const int id0 = k * a.piece, id1 = min(id0 + a.piece, a.num_blocks);
+    unsigned n = 0;
+    for (int id = id0 + 4 * lane; id < id1; id += 128) n += __popc(free_bits(a.counts, id, id1, vec));
+    n = __reduce_add_sync(kFull, n);
+    if (lane < ctas) cluster.map_shared_rank(s_free, lane)[k] = (int)n;
+  }
   cluster.sync();  // every holder has been counted
   // ---- 3: prefix sums ----------------------------------------------------------------------
   int want[kPerThread], opens[kPerThread], want_sum = 0, open_sum = 0;
@@ -294,10 +299,21 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
     sm.warp_want[warp] = want_incl;
     sm.warp_open[warp] = open_incl;
   }
+  // the pieces' free blocks become those before each piece, a few consecutive ones a thread
+  const int per_piece = (a.pieces + kResizeThreads - 1) / kResizeThreads;
+  const int k0 = min(tid * per_piece, a.pieces), k1 = min(k0 + per_piece, a.pieces);
+  int free_sum = 0;
+  for (int k = k0; k < k1; ++k) free_sum += s_free[k];
+  int free_incl = free_sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kFull, free_incl, o);
+    if (lane >= o) free_incl += x;
+  }
+  if (lane == 31) sm.warp_free[warp] = free_incl;
   __syncthreads();
   if (warp == 0) {  // the warps' sums become what is before each of them
-    const int w = sm.warp_want[lane], o = sm.warp_open[lane], f = sm.warp_free[lane];
-    int wi = w, oi = o, fi = f;
+    int wi = sm.warp_want[lane], oi = sm.warp_open[lane], fi = sm.warp_free[lane];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int x = __shfl_up_sync(kFull, wi, d), y = __shfl_up_sync(kFull, oi, d),
@@ -314,27 +330,32 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
     sm.warp_want[lane] = lane ? wb : 0;
     sm.warp_open[lane] = lane ? ob : 0;
     sm.warp_free[lane] = lane ? fb : 0;
-    const int wt = __shfl_sync(kFull, wi, 31), ot = __shfl_sync(kFull, oi, 31),
-              ft = __shfl_sync(kFull, fi, 31);
-    if (lane < kResizeCtas) {
+    if (lane == 31) sm.free = fi;
+    const int wt = __shfl_sync(kFull, wi, 31), ot = __shfl_sync(kFull, oi, 31);
+    if (lane < ctas) {
       ResizeShared* to = cluster.map_shared_rank(&sm, lane);
       to->want[cta] = wt;
       to->open[cta] = ot;
-      to->free[cta] = ft;
     }
   }
   cluster.sync();
-  int want_at = 0, open_at = 0, free_at = 0, want_all = 0, open_all = 0, free_all = 0;
-#pragma unroll
-  for (int c = 0; c < kResizeCtas; ++c) {
+  {
+    int at = sm.warp_free[warp] + free_incl - free_sum;
+    for (int k = k0; k < k1; ++k) {
+      const int n = s_free[k];
+      s_free[k] = at;
+      at += n;
+    }
+  }
+  const int free_all = sm.free;
+  int want_at = 0, open_at = 0, want_all = 0, open_all = 0;
+  for (int c = 0; c < ctas; ++c) {
     if (c == cta) {
       want_at = want_all;
       open_at = open_all;
-      free_at = free_all;
     }
     want_all = sat_add(want_all, sm.want[c]);
     open_all = sat_add(open_all, sm.open[c]);
-    free_all += sm.free[c];
   }
   {
     const int x = __shfl_up_sync(kFull, want_incl, 1), y = __shfl_up_sync(kFull, open_incl, 1);
@@ -346,8 +367,7 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
     const int i = i0 + k;
     if (i < i1) {
       const unsigned begin = 2u * (unsigned)want_at + (copies[k] ? 1u : 0u);
-#pragma unroll
-      for (int c = 0; c < kResizeCtas; ++c) {
+      for (int c = 0; c < ctas; ++c) {
         cluster.map_shared_rank(s_begin, c)[i] = begin;
         cluster.map_shared_rank(s_open, c)[i] = open_at;
       }
@@ -381,38 +401,41 @@ __global__ void __cluster_dims__(kResizeCtas, 1, 1) __launch_bounds__(kResizeThr
   };
   const int end = last_at_most(S, free_all);
   const int limit = (int)(s_begin[end] >> 1), opened = s_open[end];
-  for (int n = opened + cta * kResizeThreads + tid; n < a.num_new; n += kResizeCtas * kResizeThreads)
+  for (int n = opened + cta * kResizeThreads + tid; n < a.num_new; n += ctas * kResizeThreads)
     a.new_blocks[n] = -1;
   if (opened > a.num_new && cta == 0 && tid == 0) flag_error(a.errors, PKV_DEVERR_BLOCK_ID);
-  int r = free_at + sm.warp_free[warp];
-  for (int id = id0 + 4 * lane; r < limit && id - 4 * lane < id1; id += 128) {
-    const uint32_t bits = id < id1 ? free_bits(a.counts, id, id1, vec) : 0u;
-    int incl = __popc(bits);
+  for (int k = me; k < a.pieces && s_free[k] < limit; k += warps) {
+    const int id0 = k * a.piece, id1 = min(id0 + a.piece, a.num_blocks);
+    int r = s_free[k];
+    for (int id = id0 + 4 * lane; r < limit && id - 4 * lane < id1; id += 128) {
+      const uint32_t bits = id < id1 ? free_bits(a.counts, id, id1, vec) : 0u;
+      int incl = __popc(bits);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += y;
-    }
-    int mine = r + incl - __popc(bits);
-    r += __shfl_sync(kFull, incl, 31);
-    for (uint32_t m = bits; m != 0 && mine < limit; m &= m - 1, ++mine) {
-      const int b = id + __ffs(m) - 1;
-      const int i = last_at_most(S - 1, mine);
-      const unsigned begin = s_begin[i];
-      const int k = mine - (int)(begin >> 1), copy = (int)(begin & 1u);
-      const int cached = __ldg(a.cached + i);
-      // (a copy replaces the last entry, the others go behind it)
-      const int e = k < copy ? cached / kBlockSize : blocks_of(cached) + k - copy;
-      int32_t* at = a.tables + (size_t)__ldg(a.rows + i) * a.width + e;
-      a.counts[b] = 1;
-      if (k < copy) {
-        a.pairs[2 * i] = *at;
-        a.pairs[2 * i + 1] = b;
-      } else {
-        const int n = s_open[i] + k - copy;
-        if (n < a.num_new) a.new_blocks[n] = b;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
       }
-      *at = b;
+      int mine = r + incl - __popc(bits);
+      r += __shfl_sync(kFull, incl, 31);
+      for (uint32_t m = bits; m != 0 && mine < limit; m &= m - 1, ++mine) {
+        const int b = id + __ffs(m) - 1;
+        const int i = last_at_most(S - 1, mine);
+        const unsigned begin = s_begin[i];
+        const int k = mine - (int)(begin >> 1), copy = (int)(begin & 1u);
+        const int cached = __ldg(a.cached + i);
+        // (a copy replaces the last entry, the others go behind it)
+        const int e = k < copy ? cached / kBlockSize : blocks_of(cached) + k - copy;
+        int32_t* at = a.tables + (size_t)__ldg(a.rows + i) * a.width + e;
+        a.counts[b] = 1;
+        if (k < copy) {
+          a.pairs[2 * i] = *at;
+          a.pairs[2 * i + 1] = b;
+        } else {
+          const int n = s_open[i] + k - copy;
+          if (n < a.num_new) a.new_blocks[n] = b;
+        }
+        *at = b;
+      }
     }
   }
 }
@@ -501,16 +524,29 @@ int pkv_resize_requests(int32_t* request_tables, int32_t* ref_counts, const int3
   if (num_seqs == 0 && num_new_blocks == 0) return PKV_OK;
   ResizeArgs a{request_tables, ref_counts, rows, cached_lens, new_lens, granted_lens, new_blocks,
                block_pairs, num_seqs, num_request_rows, max_blocks_per_seq, num_new_blocks,
-               num_seqs > 0 ? num_blocks : 0, 64, device_errors};
-  while (a.slots * kResizeCtas < 2 * num_seqs) a.slots *= 2;
-  const size_t smem = 4 * (2 * ((size_t)num_seqs + 1) + 3 * (size_t)a.slots);
+               num_seqs > 0 ? num_blocks : 0, 64, 0, 128, device_errors};
+  const int ctas = num_seqs <= kOneCtaSeqs && num_blocks <= kOneCtaBlocks ? 1 : kResizeCtas;
+  while (a.slots * ctas < 2 * num_seqs) a.slots *= 2;
+  while ((long long)a.piece * kPieces < a.num_blocks) a.piece *= 2;
+  a.pieces = (a.num_blocks + a.piece - 1) / a.piece;
+  const size_t smem = 4 * (2 * ((size_t)num_seqs + 1) + 3 * (size_t)a.slots + a.pieces);
   constexpr size_t kMostSmem = 4 * (2 * (PKV_STEP_MAPS_MAX_SEQS + 1) +
-                                    3 * (2 * PKV_STEP_MAPS_MAX_SEQS / kResizeCtas));
+                                    3 * (2 * PKV_STEP_MAPS_MAX_SEQS / kResizeCtas) + kPieces);
   static_assert(kMostSmem + sizeof(ResizeShared) <= 232448, "shared memory budget of one CTA");
   static std::atomic<unsigned long long> configured{0};
   if (!smem_once(resize_kernel, kMostSmem, configured)) return PKV_ERR_CUDA;
-  resize_kernel<<<kResizeCtas, kResizeThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kResizeThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, resize_kernel, a) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // extern "C"
