@@ -14,7 +14,7 @@
 // tiles, each into an O of its own, and the first one joins the two at the end.
 // Sequences differ in both lengths and there may be one unit or many thousand, so units
 // are not dealt out: all key tiles of the call lie one behind the other on a line of work
-// (a tile counts kCost1 or kCost2, what a unit costs once kCostUnit), which is cut into
+// (a tile counts kCost1 or cost2, what a unit costs once kCostUnit), which is cut into
 // one equal part for each CTA, one CTA a processor.  Cuts fall inside units, also where
 // queries are few and inputs long; what a CTA has of a cut unit goes to the workspace as a
 // normalised partial and its log-sum-exp, at most two per CTA, and a second kernel, launched
@@ -53,11 +53,15 @@ constexpr bool cross_regs_fit(bool fp8) {
 static_assert(cross_regs_fit(false) && cross_regs_fit(true),
               "setmaxnreg may only share out what the launch holds");
 
-// The line of work.
-constexpr int kCost1 = 1, kCost2 = 2;  // of a key tile, with one and with two query tiles
-constexpr int kCostUnit = 1;           // of a unit
-constexpr int kLeast = 4;              // of a CTA's part (above kCost2 + kCostUnit, so that every
-                                       // part inside a unit holds the start of a tile)
+// The line of work, in quarters of a key tile's time with one query tile (measured: 1.03 us
+// with one, 1.78 with two, and 3 to 4 us for a unit once; a tile of an E4M3 cache goes by its
+// widening).
+constexpr int kCost1 = 4;
+constexpr int cost2(bool fp8) { return fp8 ? 6 : 7; }
+constexpr int kCostUnit = 14;  // at most a quarter of a CTA's part of the tiles: every part
+                               // begins with a unit, or what is left of one, anyway
+constexpr int kLeast = 8;  // of a CTA's part (at least cost2, so that every part inside a unit
+                           // holds the start of a tile)
 constexpr int kItems = 4;              // made ahead
 
 struct CrossItem {
@@ -82,6 +86,8 @@ struct CrossSmem {
   long long start[kMaxSeqs + 1];  // of each sequence on the line of work
   int qlen[kMaxSeqs], len[kMaxSeqs], q0[kMaxSeqs];
   long long scan[16];
+  int scan_units[16];
+  int cost_unit;
   float2 other[128];  // maximum and sum of the odd key tiles
   CrossItem item[kItems];
   uint64_t item_full[kItems], item_read[kItems];
@@ -152,12 +158,14 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
   const int chunk = (S + kThreads - 1) / kThreads;
   const int cap = min(p.max_blocks_per_seq * kBlockSize, p.max_context);
   const int rpt = kRowsM / p.group;
-  auto work = [&](int q, int len) -> long long {
+  auto work = [&](int q, int len) -> long long {  // of its key tiles
     const int tiles = (q + rpt - 1) / rpt, nk = tiles_of(len);
-    return (long long)p.num_kv_heads * ((long long)(tiles >> 1) * (nk * kCost2 + kCostUnit) +
-                                        (tiles & 1) * (nk * kCost1 + kCostUnit));
+    return (long long)p.num_kv_heads * nk * ((long long)(tiles >> 1) * cost2(kFP8) + (tiles & 1) * kCost1);
   };
+  // (a launch has below 2^31 units: its query heads)
+  auto units = [&](int q) { return p.num_kv_heads * (((q + rpt - 1) / rpt + 1) >> 1); };
   long long local = 0;
+  int mine = 0;
   for (int i = 0; i < chunk; ++i) {
     const int sq = tid * chunk + i;
     if (sq < S) {
@@ -172,26 +180,47 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
       sm.len[sq] = len;
       sm.q0[sq] = q0;
       local += work(q, len);
+      mine += units(q);
     }
   }
   long long incl = local;
+  int incl_u = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += y;
+    const int z = __shfl_up_sync(kFull, incl_u, o);
+    if (lane >= o) {
+      incl += y;
+      incl_u += z;
+    }
   }
-  if (lane == 31) sm.scan[warp] = incl;
+  if (lane == 31) {
+    sm.scan[warp] = incl;
+    sm.scan_units[warp] = incl_u;
+  }
   __syncthreads();
-  long long run = incl - local;
-  for (int w = 0; w < warp; ++w) run += sm.scan[w];
+  long long run = incl - local, total = 0;
+  int run_u = incl_u - mine;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) {
+      run += sm.scan[w];
+      run_u += sm.scan_units[w];
+    }
+    total += sm.scan[w];
+  }
+  const int unit = (int)max(min(total / (4 * (int)gridDim.x), (long long)kCostUnit), 1LL);
   for (int i = 0; i < chunk; ++i) {
     const int sq = tid * chunk + i;
     if (sq < S) {
-      sm.start[sq] = run;
+      sm.start[sq] = run + (long long)unit * run_u;
       run += work(sm.qlen[sq], sm.len[sq]);
+      run_u += units(sm.qlen[sq]);
     }
   }
-  if (tid == kThreads - 1) sm.start[S] = run;  // (the last thread's run ends at the total)
+  if (tid == kThreads - 1) {  // (the last thread's run ends at the total)
+    sm.start[S] = run + (long long)unit * run_u;
+    sm.cost_unit = unit;
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -207,6 +236,7 @@ __device__ __forceinline__ void cross_maker(const AttnParams& p, const CrossArgs
   const unsigned long long lim = wait_limit(p);
   const int lane = threadIdx.x & 31, rpt = kRowsM / p.group, hkv = p.num_kv_heads;
   const long long T = sm.start[p.num_seqs];
+  const int once = sm.cost_unit;
   const int ctas = (int)max(min((long long)gridDim.x, T / kLeast), 1LL), cta = blockIdx.x;
   long long w = cta < ctas ? T * cta / ctas : 0;
   const long long w1 = cta < ctas ? T * (cta + 1) / ctas : 0;
@@ -226,16 +256,16 @@ __device__ __forceinline__ void cross_maker(const AttnParams& p, const CrossArgs
     while (w < w1) {
       const int q = sm.qlen[s], len = sm.len[s], nk = tiles_of(len);
       const int tiles = (q + rpt - 1) / rpt;
-      const long long u2 = (long long)nk * kCost2 + kCostUnit, u1 = (long long)nk * kCost1 + kCostUnit;
+      const long long u2 = (long long)nk * cost2(kFP8) + once, u1 = (long long)nk * kCost1 + once;
       const long long twos = (long long)hkv * (tiles >> 1), off = w - sm.start[s];
       const bool two = off < twos * u2;
       const long long k = two ? off / u2 : twos + (off - twos * u2) / u1;
       const long long u0 = sm.start[s] + (two ? k * u2 : twos * u2 + (k - twos) * u1);
       const long long u = two ? u2 : u1;
-      const int cost = two ? kCost2 : kCost1;
+      const int cost = two ? cost2(kFP8) : kCost1;
       // tiles whose place on the line is in [w, w1)
       auto tile_at = [&](long long at) {
-        const long long d = at - u0 - kCostUnit;
+        const long long d = at - u0 - once;
         return d <= 0 ? 0 : (int)min((d + cost - 1) / cost, (long long)nk);
       };
       const int a = w <= u0 ? 0 : tile_at(w), b = w1 >= u0 + u ? nk : tile_at(w1);
@@ -261,7 +291,7 @@ __device__ __forceinline__ void cross_maker(const AttnParams& p, const CrossArgs
                                                                   : -1;
       if (a == 0 && b < nk) {
         // the unit goes on in the parts up to the one with its last tile
-        const long long last = u0 + kCostUnit + (long long)(nk - 1) * cost;
+        const long long last = u0 + once + (long long)(nk - 1) * cost;
         cut0 = make_int4((int)(((last + 1) * ctas + T - 1) / T - 1), x.q0 + x.t0[0], x.nt[0], x.nt[1]);
         cut1 = make_int4(x.kvh, 0, 0, 0);
       }
@@ -459,25 +489,32 @@ __device__ __forceinline__ void cross_converter(const AttnParams& p, CrossSmem<D
       return *reinterpret_cast<const uint4*>(tile + SM::kCodes + r * D +
                                              ((D == 128 ? ch ^ (r & 7) : ch) << 4));
     };
-    uint4 w = codes(cw);
+    // several turns' codes at a time: one after the other, a tile took 1000 ns, most of it
+    // latencies
+    constexpr int kTurns = kTileKeys / kRows / kConverts;
+    constexpr int kDeep = kTurns < 4 ? kTurns : 4;
 #pragma unroll 1
-    for (int u = cw; u < kTileKeys / kRows; u += kConverts) {
-      const int r = kRows * u + lane / kLanes;
-      uint4 nw = w;
-      if (u + kConverts < kTileKeys / kRows) nw = codes(u + kConverts);
-      if (r >= rows) w = make_uint4(0, 0, 0, 0);
-      // (the halves' lanes store their two chunks in opposite order: eight lanes hit eight
-      // different bank groups)
-      const bool up = ch >> 2;
-      const uint32_t v[4] = {up ? w.z : w.x, up ? w.w : w.y, up ? w.x : w.z, up ? w.y : w.w};
-      uint4 a, b;
-      widen16<QT>(v, &a, &b);
+    for (int u0 = cw; u0 < kTileKeys / kRows; u0 += kConverts * kDeep) {
+      uint4 w[kDeep];
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) w[i] = codes(u0 + i * kConverts);
       __syncwarp();  // the rows have been read
-      uint8_t* d = tile + (ch >> 2) * kHalf + r * 128;
-      const int k0 = (2 * (ch & 3) + (up ? 1 : 0)) ^ (r & 7);
-      *reinterpret_cast<uint4*>(d + (k0 << 4)) = a;
-      *reinterpret_cast<uint4*>(d + ((k0 ^ 1) << 4)) = b;
-      w = nw;
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        const int r = kRows * (u0 + i * kConverts) + lane / kLanes;
+        if (r >= rows) w[i] = make_uint4(0, 0, 0, 0);
+        // (the halves' lanes store their two chunks in opposite order: eight lanes hit eight
+        // different bank groups)
+        const bool up = ch >> 2;
+        const uint32_t v[4] = {up ? w[i].z : w[i].x, up ? w[i].w : w[i].y, up ? w[i].x : w[i].z,
+                               up ? w[i].y : w[i].w};
+        uint4 a, b;
+        widen16<QT>(v, &a, &b);
+        uint8_t* d = tile + (ch >> 2) * kHalf + r * 128;
+        const int k0 = (2 * (ch & 3) + (up ? 1 : 0)) ^ (r & 7);
+        *reinterpret_cast<uint4*>(d + (k0 << 4)) = a;
+        *reinterpret_cast<uint4*>(d + ((k0 ^ 1) << 4)) = b;
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
