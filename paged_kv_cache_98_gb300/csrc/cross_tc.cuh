@@ -21,6 +21,13 @@
 // as a dependent, joins the parts of a unit.  The line is walked with integers that every
 // CTA computes for itself, so the result depends on the batch alone.
 //
+// Pairs (kCS = 2).  Loads bind prompts: with 64 KB for every key tile and processor, L2 gives
+// 5.5 TB/s and a tile takes 1.8 us on most processors and up to 2.9 on some.  So there two
+// CTAs of a cluster share a unit of four query tiles and the same part of the line: each
+// issues half of the boxes of every K and V tile, multicast to both.  Products, softmax and
+// epilogue are each CTA's own; only the ring is common (a stage is empty when both have
+// released it).
+//
 // Warps: 0-3 softmax of tile a (or even key tiles), 4-7 of tile b (odd), 8 MMA issuer and
 // TMEM owner, 9-10 TMA producers, 11 makes the items from the line of work and loads the
 // V rows of partial last blocks, 12-15 (E4M3 caches) widen K and V tiles to the query's
@@ -52,6 +59,10 @@ constexpr bool cross_regs_fit(bool fp8) {
 }
 static_assert(cross_regs_fit(false) && cross_regs_fit(true),
               "setmaxnreg may only share out what the launch holds");
+
+// Query tiles of a unit: two in each CTA of its cluster, fewer in a sequence's last one.
+// CTA 0 has the larger half of those, CTA 1 the smaller, perhaps none.
+constexpr int tiles_of_rank(int n, int rank, int cs) { return cs == 1 ? n : rank == 0 ? (n + 1) / 2 : n / 2; }
 
 // The line of work, in quarters of a key tile's time with one query tile (measured: 1.03 us
 // with one, 1.78 with two, and 3 to 4 us for a unit once; a tile of an E4M3 cache goes by its
@@ -93,7 +104,7 @@ struct CrossSmem {
   uint64_t item_full[kItems], item_read[kItems];
   uint64_t landed[kSt], full[kSt], empty[kSt];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_ready[2], p_ready[2], o_done[2], o_free[2];
+  uint64_t s_ready[2], p_half[2], p_ready[2], o_done[2], o_free[2];
   uint64_t other_ready;
   uint64_t tail_full[2], tail_free[2];
   uint64_t mma_done;
@@ -102,6 +113,29 @@ struct CrossSmem {
 };
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
+
+// As wait_for, for arrivals from both CTAs of a cluster.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                             unsigned long long limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !tc::mbar_test_cluster(bar, parity); ++it) {
+    if ((it & 63u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort) return false;
+      if (now - t0 > limit_ns) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
+// Lets `ns` nanoseconds pass.
+__device__ __forceinline__ void settle(unsigned long long ns) {
+  for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < ns;) __nanosleep(1000);
+}
 
 // The next item, for a whole warp; false when the wait gave up.
 template <class SM>
@@ -118,7 +152,7 @@ __device__ __forceinline__ bool take(SM& sm, uint32_t n, CrossItem& x, volatile 
 // ---- the line of work --------------------------------------------------------------------
 // Lengths of the sequences and where each begins on the line; ends with the CTA
 // synchronised.
-template <int D, bool kFP8>
+template <int D, bool kFP8, int kCS>
 __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs& c,
                                             CrossSmem<D, kFP8>& sm) {
   using SM = CrossSmem<D, kFP8>;
@@ -126,14 +160,15 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < SM::kSt; ++s) {
-      mbar_init(&sm.landed[s], kTmaWarps);
-      mbar_init(&sm.full[s], kFP8 ? kConverts : kTmaWarps);
-      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.landed[s], 1);
+      mbar_init(&sm.full[s], kFP8 ? kConverts : 1);
+      mbar_init(&sm.empty[s], kCS);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sm.q_full[x], 1);
       mbar_init(&sm.q_empty[x], 1);
       mbar_init(&sm.s_ready[x], 1);
+      mbar_init(&sm.p_half[x], 4);
       mbar_init(&sm.p_ready[x], 4);
       mbar_init(&sm.o_done[x], 1);
       mbar_init(&sm.o_free[x], 4);
@@ -159,11 +194,12 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
   const int cap = min(p.max_blocks_per_seq * kBlockSize, p.max_context);
   const int rpt = kRowsM / p.group;
   auto work = [&](int q, int len) -> long long {  // of its key tiles
-    const int tiles = (q + rpt - 1) / rpt, nk = tiles_of(len);
-    return (long long)p.num_kv_heads * nk * ((long long)(tiles >> 1) * cost2(kFP8) + (tiles & 1) * kCost1);
+    const int tiles = (q + rpt - 1) / rpt, rest = tiles % (2 * kCS);
+    return (long long)p.num_kv_heads * tiles_of(len) *
+           ((long long)(tiles / (2 * kCS)) * cost2(kFP8) + (rest > kCS ? cost2(kFP8) : rest ? kCost1 : 0));
   };
   // (a launch has below 2^31 units: its query heads)
-  auto units = [&](int q) { return p.num_kv_heads * (((q + rpt - 1) / rpt + 1) >> 1); };
+  auto units = [&](int q) { return p.num_kv_heads * (((q + rpt - 1) / rpt + 2 * kCS - 1) / (2 * kCS)); };
   long long local = 0;
   int mine = 0;
   for (int i = 0; i < chunk; ++i) {
@@ -208,7 +244,7 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
     }
     total += sm.scan[w];
   }
-  const int unit = (int)max(min(total / (4 * (int)gridDim.x), (long long)kCostUnit), 1LL);
+  const int unit = (int)max(min(total / (4 * (int)gridDim.x / kCS), (long long)kCostUnit), 1LL);
   for (int i = 0; i < chunk; ++i) {
     const int sq = tid * chunk + i;
     if (sq < S) {
@@ -222,13 +258,14 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
     sm.cost_unit = unit;
   }
   tc::fence_before_sync();
-  __syncthreads();
+  if constexpr (kCS == 2) tc::cluster_sync();  // the other CTA's barriers are there, too
+  else __syncthreads();
   tc::fence_after_sync();
 }
 
 // The maker: this CTA's part of the line as items, the V rows of partial last blocks, and
 // which unit the part ends in.
-template <int D, bool kFP8>
+template <int D, bool kFP8, int kCS>
 __device__ __forceinline__ void cross_maker(const AttnParams& p, const CrossArgs& c,
                                             CrossSmem<D, kFP8>& sm) {
   using SM = CrossSmem<D, kFP8>;
@@ -237,9 +274,11 @@ __device__ __forceinline__ void cross_maker(const AttnParams& p, const CrossArgs
   const int lane = threadIdx.x & 31, rpt = kRowsM / p.group, hkv = p.num_kv_heads;
   const long long T = sm.start[p.num_seqs];
   const int once = sm.cost_unit;
-  const int ctas = (int)max(min((long long)gridDim.x, T / kLeast), 1LL), cta = blockIdx.x;
-  long long w = cta < ctas ? T * cta / ctas : 0;
-  const long long w1 = cta < ctas ? T * (cta + 1) / ctas : 0;
+  // parts of the line, one for each cluster
+  const int parts = (int)max(min((long long)gridDim.x / kCS, T / kLeast), 1LL), part = blockIdx.x / kCS;
+  const int rank = kCS == 2 ? (int)tc::cluster_rank() : 0;
+  long long w = part < parts ? T * part / parts : 0;
+  const long long w1 = part < parts ? T * (part + 1) / parts : 0;
   int4 cut0 = make_int4(-1, 0, 0, 0), cut1 = cut0;
   int s = 0;
   if (w < w1) {  // the last sequence that begins at or before w
@@ -255,14 +294,15 @@ __device__ __forceinline__ void cross_maker(const AttnParams& p, const CrossArgs
     CrossItem x = {};
     while (w < w1) {
       const int q = sm.qlen[s], len = sm.len[s], nk = tiles_of(len);
-      const int tiles = (q + rpt - 1) / rpt;
-      const long long u2 = (long long)nk * cost2(kFP8) + once, u1 = (long long)nk * kCost1 + once;
-      const long long twos = (long long)hkv * (tiles >> 1), off = w - sm.start[s];
-      const bool two = off < twos * u2;
-      const long long k = two ? off / u2 : twos + (off - twos * u2) / u1;
-      const long long u0 = sm.start[s] + (two ? k * u2 : twos * u2 + (k - twos) * u1);
-      const long long u = two ? u2 : u1;
-      const int cost = two ? cost2(kFP8) : kCost1;
+      const int tiles = (q + rpt - 1) / rpt, rest = tiles % (2 * kCS);
+      const int cost_rest = rest > kCS ? cost2(kFP8) : kCost1;
+      const long long u2 = (long long)nk * cost2(kFP8) + once, u1 = (long long)nk * cost_rest + once;
+      const long long wholes = (long long)hkv * (tiles / (2 * kCS)), off = w - sm.start[s];
+      const bool whole = off < wholes * u2;
+      const long long k = whole ? off / u2 : wholes + (off - wholes * u2) / u1;
+      const long long u0 = sm.start[s] + (whole ? k * u2 : wholes * u2 + (k - wholes) * u1);
+      const long long u = whole ? u2 : u1;
+      const int cost = whole ? cost2(kFP8) : cost_rest;
       // tiles whose place on the line is in [w, w1)
       auto tile_at = [&](long long at) {
         const long long d = at - u0 - once;
@@ -274,25 +314,25 @@ __device__ __forceinline__ void cross_maker(const AttnParams& p, const CrossArgs
       const int seq = s;
       while (s + 1 < p.num_seqs && sm.start[s + 1] <= w) ++s;
       if (a >= b && !(nk == 0 && begins)) continue;
-      const int pair = (int)(k / hkv);
       x.live = 1;
       x.seq = seq;
       x.kvh = (int)(k % hkv);
       x.len = len;
       x.q0 = sm.q0[seq];
-      x.t0[0] = 2 * pair * rpt;
+      const int n0 = whole ? 2 * kCS : rest, mine = tiles_of_rank(n0, rank, kCS);
+      x.t0[0] = ((int)(k / hkv) * (2 * kCS) + (rank ? tiles_of_rank(n0, 0, kCS) : 0)) * rpt;
       x.t0[1] = x.t0[0] + rpt;
-      x.nt[0] = min(rpt, q - x.t0[0]);
-      x.nt[1] = two ? min(rpt, q - x.t0[1]) : 0;
+      x.nt[0] = mine > 0 ? min(rpt, q - x.t0[0]) : 0;
+      x.nt[1] = mine > 1 ? min(rpt, q - x.t0[1]) : 0;
       x.kt0 = a;
       x.kt1 = b;
-      x.part = a == 0 && b == nk ? -1 : 2 * cta + (a == 0 ? 1 : 0);
+      x.part = a == 0 && b == nk ? -1 : 2 * (int)blockIdx.x + (a == 0 ? 1 : 0);
       x.tail = !kFP8 && b == nk && (len & (kBlockSize - 1)) != 0 ? ((len - 1) % kTileKeys) / kBlockSize
                                                                   : -1;
-      if (a == 0 && b < nk) {
+      if (a == 0 && b < nk && mine > 0) {
         // the unit goes on in the parts up to the one with its last tile
         const long long last = u0 + once + (long long)(nk - 1) * cost;
-        cut0 = make_int4((int)(((last + 1) * ctas + T - 1) / T - 1), x.q0 + x.t0[0], x.nt[0], x.nt[1]);
+        cut0 = make_int4((int)(((last + 1) * parts + T - 1) / T - 1), x.q0 + x.t0[0], x.nt[0], x.nt[1]);
         cut1 = make_int4(x.kvh, 0, 0, 0);
       }
       break;
@@ -338,16 +378,15 @@ __device__ __forceinline__ void cross_maker(const AttnParams& p, const CrossArgs
   if (lane == 0) {
     if (!ok) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
     if (c.cuts) {
-      c.cuts[2 * cta] = cut0;
-      c.cuts[2 * cta + 1] = cut1;
+      c.cuts[2 * blockIdx.x] = cut0;
+      c.cuts[2 * blockIdx.x + 1] = cut1;
     }
   }
 }
 
 // ---- loads ---------------------------------------------------------------------------------
-// Order of a unit's tiles in the ring, as the issuer takes them: with two query tiles K0, V0,
-// K1, V1, ...; with one K0, K1, V0, K2, V1, ...
-template <int D, bool kFP8>
+// Order of a unit's tiles in the ring, as the issuer takes them: K0, K1, V0, K2, V1, ...
+template <int D, bool kFP8, int kCS>
 __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossArgs& c,
                                                CrossSmem<D, kFP8>& sm, const CUtensorMap& tm_k,
                                                const CUtensorMap& tm_v, const CUtensorMap& tm_q,
@@ -356,12 +395,14 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
   constexpr int kSt = SM::kSt;
   constexpr int kRow = D * (kFP8 ? 1 : 2);          // bytes of a cache row
   constexpr int kBoxRow = kRow < 128 ? kRow : 128;  // bytes of a row in a box
-  constexpr int kLoad = kTileKeys * kRow / kTmaWarps;
+  constexpr int kLoad = kTileKeys * kRow;
   uint64_t* const bars = kFP8 ? sm.landed : sm.full;
   volatile int* abort = &sm.abort;
   const unsigned long long lim = wait_limit(p);
   const int lane = threadIdx.x & 31, g = p.group;
-  const bool my_lane = (lane & 1) == pw;            // blocks pw, pw + 2, ... of a tile
+  // the boxes of a tile's blocks are dealt out to the producer warps of all CTAs
+  const bool my_lane = (lane & (2 * kCS - 1)) == (kCS == 2 ? 2 * (int)tc::cluster_rank() : 0) + pw;
+  constexpr uint16_t kAll = (1u << kCS) - 1;
   uint8_t* const ring = &sm.ring[0][0];
   uint32_t pos = 0, nq = 0;
   bool ok = true;
@@ -381,19 +422,28 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
   auto issue = [&](int t, int row, bool is_v) -> bool {
     const int st = pos % kSt;
     // test hook: these boxes are never issued, so every wait for the tile runs out
-    const bool skip = pw == 0 && blockIdx.x == 0 && p.skip_copy > 0 && pos + 1 == (uint32_t)p.skip_copy;
+    const bool skip = blockIdx.x == 0 && p.skip_copy > 0 && pos + 1 == (uint32_t)p.skip_copy;
     bool good = true;
     if (lane == 0) {
-      if (pos >= (uint32_t)kSt) good = wait_for(&sm.empty[st], ((pos / kSt) - 1) & 1, abort, lim);
-      if (good && !skip) mbar_arrive_expect_tx(&bars[st], kLoad);
+      if (pos >= (uint32_t)kSt) {
+        const uint32_t parity = ((pos / kSt) - 1) & 1;
+        if constexpr (kCS == 2) good = wait_cluster(&sm.empty[st], parity, abort, lim);
+        else good = wait_for(&sm.empty[st], parity, abort, lim);
+      }
+      if (good && !skip && pw == 0) mbar_arrive_expect_tx(&bars[st], kLoad);
     }
     if (!__shfl_sync(kFull, (int)good, 0)) return false;
     if (!skip && (lane >> 3) == (t & 3) && my_lane) {
       uint8_t* dst = ring + (size_t)st * SM::kStage + (kFP8 ? SM::kCodes : 0) +
                      (lane & 7) * (kBlockSize * kBoxRow);
       const CUtensorMap* map = is_v ? &tm_v : &tm_k;
-      tc::tma_load_2d(dst, map, 0, row, &bars[st]);
-      if (kRow > 128) tc::tma_load_2d(dst + kHalf, map, 64, row, &bars[st]);
+      if constexpr (kCS == 2) {
+        tc::tma_load_2d_all(dst, map, 0, row, &bars[st], kAll);
+        if (kRow > 128) tc::tma_load_2d_all(dst + kHalf, map, 64, row, &bars[st], kAll);
+      } else {
+        tc::tma_load_2d(dst, map, 0, row, &bars[st]);
+        if (kRow > 128) tc::tma_load_2d(dst + kHalf, map, 64, row, &bars[st]);
+      }
     }
     __syncwarp();
     ++pos;
@@ -403,10 +453,9 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
     ok = take(sm, n, x, abort, lim);
     if (!ok || !x.live) break;
     if (x.kt0 == x.kt1) continue;
-    const bool two = x.nt[1] > 0;
     if (pw == 0) {
       bool good = true;
-      for (int qt = 0; qt < (two ? 2 : 1); ++qt, ++nq) {
+      for (int qt = 0; qt < 2 && x.nt[qt] > 0; ++qt, ++nq) {
         const int b = nq & 1;
         if (lane == 0 && good) {
           if (nq >= 2) good = wait_for(&sm.q_empty[b], ((nq >> 1) - 1) & 1, abort, lim);
@@ -441,15 +490,10 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
       pre_raw = 4 * pre < x.kt1 ? fetch(pre) : kBeyond;
       return r;
     };
-    if (two) {
-      for (int t = x.kt0; ok && t < x.kt1; ++t)
-        ok = issue(t, row_for(t), false) && issue(t, row_for(t), true);
-    } else {
-      if (ok) ok = issue(x.kt0, row_for(x.kt0), false);
-      for (int t = x.kt0; ok && t < x.kt1; ++t) {
-        if (t + 1 < x.kt1) ok = issue(t + 1, row_for(t + 1), false);
-        if (ok) ok = issue(t, row_for(t), true);
-      }
+    if (ok) ok = issue(x.kt0, row_for(x.kt0), false);
+    for (int t = x.kt0; ok && t < x.kt1; ++t) {
+      if (t + 1 < x.kt1) ok = issue(t + 1, row_for(t + 1), false);
+      if (ok) ok = issue(t, row_for(t), true);
     }
   }
   if (!ok && lane == 0) {
@@ -524,22 +568,34 @@ __device__ __forceinline__ void cross_converter(const AttnParams& p, CrossSmem<D
   for (uint32_t n = 0; ok; ++n) {
     ok = take(sm, n, x, abort, lim);
     if (!ok || !x.live) break;
-    const bool two = x.nt[1] > 0;
     auto rows = [&](int t) { return min(x.len - t * kTileKeys, kTileKeys); };
-    if (!two && x.kt0 < x.kt1) ok = convert(kTileKeys);
+    if (x.kt0 < x.kt1) ok = convert(kTileKeys);
     for (int t = x.kt0; ok && t < x.kt1; ++t) {
-      if (two || t + 1 < x.kt1) ok = convert(kTileKeys);
+      if (t + 1 < x.kt1) ok = convert(kTileKeys);
       if (ok) ok = convert(rows(t));
     }
   }
   if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
 }
 
+// Half of a tile's product, O (at d) (+)= P (TMEM at a, 16 states per 8 columns) V: the steps of
+// 16 states from kFrom on; step ts takes its V rows from the tail buffer.
+template <int kFrom>
+__device__ __forceinline__ void issue_half(uint32_t d, uint32_t a, uint64_t dv, uint64_t dtail, int ts,
+                                           uint32_t acc0, uint32_t idesc) {
+#pragma unroll
+  for (int kk = kFrom; kk < kFrom + kTileKeys / 32; ++kk) {
+    const uint64_t b = kk == ts ? dtail : dv + (uint64_t)((kk * (kBlockSize * 128)) >> 4);
+    mma_f16_tmem_a(d, a + kk * 8, b, idesc, acc0 | (kk != kFrom ? 1u : 0u));
+  }
+}
+
 // ---- MMA issuer ------------------------------------------------------------------------------
 // Two query tiles, per key tile t: P_a(t) V(t), S_a(t+1), P_b(t) V(t), S_b(t+1); one: S_0(0),
-// S_1(1), then P_x(t) V(t), S_x(t+2) with x = t & 1.  The whole warp runs the loop, so that
-// counters and descriptors are the same in all lanes; one elected lane issues.
-template <class QT, int D, bool kFP8>
+// S_1(1), then P_x(t) V(t), S_x(t+2) with x = t & 1; none (the other CTA's): stages are given
+// back as they fill.  The whole warp runs the loop, so that counters and descriptors are the
+// same in all lanes; one elected lane issues.
+template <class QT, int D, bool kFP8, int kCS>
 __device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, kFP8>& sm, uint32_t tmem) {
   using SM = CrossSmem<D, kFP8>;
   constexpr int kSt = SM::kSt;
@@ -552,6 +608,13 @@ __device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, k
   const bool leader = tc::elect_one();
   auto commit = [&](uint64_t* bar) {
     if (leader) tc::mma_commit(bar);
+  };
+  auto release = [&](int st) {  // a stage, to the producers of all CTAs
+    if constexpr (kCS == 2) {
+      if (leader) tc::mma_commit_all(&sm.empty[st], 3);
+    } else {
+      commit(&sm.empty[st]);
+    }
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __shfl_sync(kFull, (int)wait_bar(bar, parity, abort, lim), 0) != 0;
@@ -576,17 +639,21 @@ __device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, k
     if (leader) issue_mods_scores<D>(tmem + y * 128, b ? dq[1] : dq[0], dk0 + st * kStage, kIdescS);
     commit(&sm.s_ready[y]);
   };
+  // the product of 64 states' weights while the softmax is at the others'
   auto product = [&](int y, int st, int t, bool first, bool last) -> bool {
-    if (!wait(&sm.p_ready[y], np[y] & 1)) return false;
-    ++np[y];
+    if (!wait(&sm.p_half[y], np[y] & 1)) return false;
     if (first && nit[y] >= 1 && !wait(&sm.o_free[y], (nit[y] - 1) & 1))
       return false;  // the previous item's O has been read out
     const int ts = t == x.kt1 - 1 ? x.tail : -1;
     if (ts >= 0 && !wait(&sm.tail_full[ntail & 1], (ntail >> 1) & 1)) return false;
     tc::fence_after_sync();
-    if (leader)
-      issue_pv(tmem + kColO + y * 128, tmem + y * 128, dv0 + st * kStage,
-               dt0 + (ntail & 1) * (SM::kTail >> 4), ts, !first, kIdescO);
+    const uint64_t dv = dv0 + st * kStage, dt = dt0 + (ntail & 1) * (SM::kTail >> 4);
+    const uint32_t o = tmem + kColO + y * 128, at = tmem + y * 128;
+    if (leader) issue_half<0>(o, at, dv, dt, ts, !first, kIdescO);
+    if (!wait(&sm.p_ready[y], np[y] & 1)) return false;
+    ++np[y];
+    tc::fence_after_sync();
+    if (leader) issue_half<kTileKeys / 32>(o, at, dv, dt, ts, 1, kIdescO);
     if (last) commit(&sm.o_done[y]);
     return true;
   };
@@ -608,27 +675,35 @@ __device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, k
         if (t0 + 1 == t1) commit(&sm.q_empty[b0]);
         scores(1, b1, kst);
         if (t0 + 1 == t1) commit(&sm.q_empty[b1]);
-        commit(&sm.empty[kst]);
+        release(kst);
       }
       for (int t = t0; ok && t < t1; ++t) {
         const bool more = t + 1 < t1;
-        ok = acquire(vst) && product(0, vst, t, t == t0, !more);
+        ok = (!more || acquire(kst)) && acquire(vst) && product(0, vst, t, t == t0, !more);
         if (ok && more) {
-          ok = acquire(kst);
-          if (ok) scores(0, b0, kst);
-          if (ok && t + 2 == t1) commit(&sm.q_empty[b0]);
+          scores(0, b0, kst);
+          if (t + 2 == t1) commit(&sm.q_empty[b0]);
         }
         if (ok) ok = product(1, vst, t, t == t0, !more);
         if (!ok) break;
-        commit(&sm.empty[vst]);
+        release(vst);
         if (more) {
           scores(1, b1, kst);
           if (t + 2 == t1) commit(&sm.q_empty[b1]);
-          commit(&sm.empty[kst]);
+          release(kst);
         }
       }
       ++nit[0];
       ++nit[1];
+    } else if (kCS == 2 && x.nt[0] == 0) {
+      for (int i = 2 * (t1 - t0); ok && i > 0; --i) {
+        ok = acquire(kst);
+        if (ok && leader) {
+          const uint32_t bar = smem_u32(&sm.empty[kst]);
+          tc::mbar_arrive_cluster_release(tc::map_rank(bar, 0));  // (converters wrote there)
+          tc::mbar_arrive_cluster_release(tc::map_rank(bar, 1));
+        }
+      }
     } else {
       const int b = nq & 1;
       ok = wait(&sm.q_full[b], (nq >> 1) & 1);
@@ -636,7 +711,7 @@ __device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, k
       auto next_scores = [&](int t) -> bool {
         if (!acquire(kst)) return false;
         scores((t - t0) & 1, b, kst);
-        commit(&sm.empty[kst]);
+        release(kst);
         if (t == t1 - 1) commit(&sm.q_empty[b]);
         return true;
       };
@@ -645,7 +720,7 @@ __device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, k
       for (int t = t0; ok && t < t1; ++t) {
         ok = acquire(vst) && product((t - t0) & 1, vst, t, t < t0 + 2, t >= t1 - 2);
         if (!ok) break;
-        commit(&sm.empty[vst]);
+        release(vst);
         if (t + 2 < t1) ok = next_scores(t + 2);
       }
       ++nit[0];
@@ -659,6 +734,17 @@ __device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, k
   if (!ok && leader) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
   commit(&sm.mma_done);
   mbar_wait(&sm.mma_done, 0, 100000000ull);
+}
+
+// Weights 2^z of 32 states as 16 packed pairs, and their sums.
+template <class QT>
+__device__ __forceinline__ void weights(const float* z, float* pk, float2* sums) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const float2 w = make_float2(fast_exp2(z[e]), fast_exp2(z[e + 1]));
+    sums[(e >> 1) & 3] = __fadd2_rn(sums[(e >> 1) & 3], w);
+    pk[e >> 1] = __uint_as_float(pack2<QT>(w.x, w.y));
+  }
 }
 
 // ---- softmax and epilogue ------------------------------------------------------------------
@@ -675,13 +761,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t s_col = tmem + lane_off + y * 128;
   const uint32_t o_col = tmem + lane_off + kColO + y * 128;
-  // scores are scaled inside the exponent; a negative scale is folded in by negating
-  // them, a zero one taken as 1e-30 (2^(s * 1e-30) rounds to 1)
-  const bool neg = p.q_scale < 0.0f;
-  const float qa = fmaxf(fabsf(p.q_scale), 1e-30f);
-  // with fewer registers (E4M3 caches) the scores are read twice, for the maxima and for the
-  // weights, instead of held
-  constexpr bool kTwice = kFP8;
+  const float qs = p.q_scale;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(kFull, wait_for(bar, parity, abort, lim)) != 0;
   };
@@ -699,7 +779,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
     };
     const bool two = x.nt[1] > 0;
     const int qt = two ? y : 0, kt0 = x.kt0, kt1 = x.kt1;
-    const int rows = x.nt[qt] * g;                    // rows past the tokens are never stored
+    const int rows = x.nt[qt] * g;                    // rows past the tokens are not stored
     const bool idle = 32 * (warp & 3) >= rows;        // the warp has no others
     // the row's place in the output, in heads
     auto head_of = [&]() { return (x.q0 + x.t0[qt] + r / g) * p.num_heads + x.kvh * g + r % g; };
@@ -713,7 +793,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
       continue;
     }
     const int step = two ? 1 : 2, first = two ? kt0 : kt0 + y;
-    if (first >= kt1) {  // one key tile: the other warpgroup's
+    if (first >= kt1 || rows == 0) {  // one key tile, the other warpgroup's; no query tile
       done();
       continue;
     }
@@ -727,87 +807,82 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
       if (!ok) break;
       if (!idle) {
         tc::fence_after_sync();
-        // scores of 32 states from k on, masked and with the scale's sign
-        auto scores = [&](int k, float* sv) {
-          if (neg) {
+        // Exponents z = s * scale - m of the row's scores and their maximum, with m as it was
+        // after the last tile; the weights of the first 64 states.  Where no row of the warp
+        // exceeds its m by more than 8 (nearly always: m only has to be near the maximum, the
+        // weights are floating-point numbers) that is all; else those rows' m moves, what
+        // they have so far is scaled to it, and the tile is done over.  (With the maximum
+        // first, the exponentials wait for it: 570 of 2000 cycles.)
+        float pk[32], z2[64], m = m_run == -INFINITY ? 0.0f : m_run;
+        float2 t2[4];
+#pragma unroll 1
+        for (int again = 0;; again = 1) {
+          const float2 f2 = make_float2(qs, qs), m2 = make_float2(-m, -m);
+          float mx[4];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sv[i] = -sv[i];
+          for (int i = 0; i < 4; ++i) {
+            mx[i] = -INFINITY;
+            t2[i] = make_float2(0.0f, 0.0f);
           }
-          if (left < kTileKeys) {
+          float sv[2][32];
+          tc::tmem_ld32(s_col, sv[0]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sv[i] = k + i < left ? sv[i] : -INFINITY;
-          }
-        };
-        float mx[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
-        auto most = [&](const float* sv) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) mx[(i >> 1) & 7] = fmax3(mx[(i >> 1) & 7], sv[i], sv[i + 1]);
-        };
-        float sv[kTwice ? 32 : kTileKeys];
-        if constexpr (kTwice) {
-#pragma unroll
-          for (int k = 0; k < kTileKeys; k += 32) {
-            tc::tmem_ld32(s_col + k, sv);
+          for (int k = 0; k < 4; ++k) {
             tc::tmem_wait_ld();
-            scores(k, sv);
-            most(sv);
-          }
-        } else {
+            if (k < 3) tc::tmem_ld32(s_col + 32 * (k + 1), sv[(k + 1) & 1]);
+            float* const zk = k < 2 ? sv[k & 1] : z2 + 32 * (k - 2);
 #pragma unroll
-          for (int k = 0; k < kTileKeys; k += 32) tc::tmem_ld32(s_col + k, sv + k);
-          tc::tmem_wait_ld();
+            for (int e = 0; e < 32; e += 2) {
+              const float2 v = __ffma2_rn(make_float2(sv[k & 1][e], sv[k & 1][e + 1]), f2, m2);
+              zk[e] = v.x;
+              zk[e + 1] = v.y;
+            }
+            if (left < 32 * (k + 1)) {
 #pragma unroll
-          for (int k = 0; k < kTileKeys; k += 32) {
-            scores(k, sv + k);
-            most(sv + k);
+              for (int e = 0; e < 32; ++e) zk[e] = 32 * k + e < left ? zk[e] : -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], zk[e], zk[e + 1]);
+            if (k < 2) weights<QT>(zk, pk + 16 * k, t2);
           }
-        }
-        const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * qa;
-        const bool need = mt > m_run + kRescaleAt;
-        float alpha = 1.0f;
-        if (need) {
-          alpha = t == first ? 0.0f : fast_exp2(m_run - mt);
-          m_run = mt;
+          const float mz = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+          const bool need = m_run == -INFINITY ? mz > -INFINITY : mz > kRescaleAt;
+          // (once over is enough: only scores of 2^27 and more, whose differences fp32 does not
+          // hold, could exceed their own maximum again)
+          if (again || !__any_sync(kFull, need)) break;
+          // (a row without a weight so far has zeros)
+          const float alpha = !need ? 1.0f : m_run == -INFINITY ? 0.0f : fast_exp2(-mz);
+          if (need) m = m_run = m + mz;
 #pragma unroll
           for (int i = 0; i < 4; ++i) l2[i] = __fmul2_rn(l2[i], make_float2(alpha, alpha));
-        }
-        const float m = m_run == -INFINITY ? 0.0f : m_run;  // (2^(-inf - 0) is 0)
-        const float2 f2 = make_float2(qa, qa), m2 = make_float2(-m, -m);
-#pragma unroll
-        for (int k = 0; k < kTileKeys; k += 32) {
-          float* const s = kTwice ? sv : sv + k;
-          if constexpr (kTwice) {
-            tc::tmem_ld32(s_col + k, sv);
-            tc::tmem_wait_ld();
-            scores(k, sv);
-          }
-          float pk[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 z = __ffma2_rn(make_float2(s[e], s[e + 1]), f2, m2);
-            const float2 w = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-            l2[(e >> 1) & 3] = __fadd2_rn(l2[(e >> 1) & 3], w);
-            pk[e >> 1] = __uint_as_float(pack2<QT>(w.x, w.y));
-          }
-          tc::tmem_st16(s_col + k / 2, pk);
-        }
-        // the product of this tile adds onto O, which is complete up to the one before (the
-        // scores were issued behind its product)
-        if (t > first && __any_sync(kFull, need)) {
+          // O is complete up to the tile before (the scores were issued behind its product)
+          if (t > first) {
 #pragma unroll 1
-          for (int k = 0; k < D; k += 32) {
-            float ov[32];
-            tc::tmem_ld32(o_col + k, ov);
-            tc::tmem_wait_ld();
+            for (int k = 0; k < D; k += 32) {
+              float ov[32];
+              tc::tmem_ld32(o_col + k, ov);
+              tc::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-            tc::tmem_st32(o_col + k, ov);
+              for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+              tc::tmem_st32(o_col + k, ov);
+            }
           }
         }
+        // P over the scores, which have all been read
+        tc::tmem_st32(s_col, pk);
         tc::tmem_wait_st();
         tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_half[y]);
+        weights<QT>(z2, pk, t2);
+        weights<QT>(z2 + 32, pk + 16, t2);
+        tc::tmem_st32(s_col + 32, pk);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l2[i] = __fadd2_rn(l2[i], t2[i]);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+      } else if (lane == 0) {
+        mbar_arrive(&sm.p_half[y]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.p_ready[y]);
@@ -926,7 +1001,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
   if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
 }
 
-template <class QT, int D, bool kFP8>
+template <class QT, int D, bool kFP8, int kCS>
 __global__ void __launch_bounds__(cross_threads(kFP8), 1)
     cross_kernel(const AttnParams p, const CrossArgs c, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
@@ -940,21 +1015,29 @@ __global__ void __launch_bounds__(cross_threads(kFP8), 1)
     tc::prefetch_tmap(&tm_v);
     tc::prefetch_tmap(&tm_q);
   }
-  cross_setup<D, kFP8>(p, c, sm);
+  cross_setup<D, kFP8, kCS>(p, c, sm);
   const uint32_t tmem = sm.tmem_base;
   if (warp >= kSoft) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(cross_other_regs(kFP8)));
-    if (warp == kIssuer) cross_issuer<QT, D, kFP8>(p, sm, tmem);
+    if (warp == kIssuer) cross_issuer<QT, D, kFP8, kCS>(p, sm, tmem);
     else if (warp < kTma + kTmaWarps)
-      cross_producer<D, kFP8>(p, c, sm, tm_k, tm_v, tm_q, kv_rows, warp - kTma);
-    else if (warp == kMaker) cross_maker<D, kFP8>(p, c, sm);
+      cross_producer<D, kFP8, kCS>(p, c, sm, tm_k, tm_v, tm_q, kv_rows, warp - kTma);
+    else if (warp == kMaker) cross_maker<D, kFP8, kCS>(p, c, sm);
     else if constexpr (kFP8) cross_converter<QT, D>(p, sm, warp - kConvert);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(cross_soft_regs(kFP8)));
     cross_softmax<QT, D, kFP8>(p, c, sm, tmem);
   }
   tc::fence_before_sync();
-  __syncthreads();
+  if constexpr (kCS == 2) {
+    // the other CTA may still load for this one, or arrive on its barriers; where one has
+    // given up, its last copies to the other land meanwhile
+    if (*static_cast<volatile int*>(&sm.abort)) settle(5000000ull);
+    __syncwarp();
+    tc::cluster_sync();
+  } else {
+    __syncthreads();
+  }
   if (warp == kIssuer) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
@@ -962,8 +1045,8 @@ __global__ void __launch_bounds__(cross_threads(kFP8), 1)
 }
 
 // Joins the parts of the unit that CTA blockIdx.x's part of the line ends in, if it ends
-// inside one: weights 2^(lse - max) of the parts, which CTA b wrote as its second partial and
-// the CTAs up to the last one as their first.  A warp per row.
+// inside one: weights 2^(lse - max) of the parts, which that CTA wrote as its second partial
+// and those of its rank in the clusters up to the last one as their first.  A warp per row.
 constexpr int kJoinThreads = 256;
 template <class QT, int D>
 __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const AttnParams p, const CrossArgs c) {
@@ -978,8 +1061,8 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const AttnPara
   for (int at = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); at < c.part_rows; at += warps) {
     const int qt = at >> 7, r = at & 127;
     if (r >= (qt ? cut.w : cut.z) * g) continue;
-    auto slot = [&](int i) { return (size_t)(2 * (b + i) + (i == 0 ? 1 : 0)) * c.part_rows + at; };
-    const int parts = last - b + 1;
+    auto slot = [&](int i) { return (size_t)(2 * (b + i * c.cluster) + (i == 0 ? 1 : 0)) * c.part_rows + at; };
+    const int parts = last - b / c.cluster + 1;
     float m = -INFINITY;
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(p.lse + slot(i)));
 #pragma unroll
@@ -1008,7 +1091,7 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const AttnPara
   }
 }
 
-template <class QT, int D, bool kFP8>
+template <class QT, int D, bool kFP8, int kCS>
 int launch_cross_typed(const AttnParams& p, const CrossArgs& c, int ctas, cudaStream_t stream) {
   const bool bf16 = std::is_same<QT, BF16>::value;
   const uint64_t kv_rows = (uint64_t)p.num_blocks * p.num_kv_heads * kBlockSize;
@@ -1025,7 +1108,7 @@ int launch_cross_typed(const AttnParams& p, const CrossArgs& c, int ctas, cudaSt
   static_assert(offsetof(SM, ring) % 1024 == 0 && offsetof(SM, q) % 1024 == 0 &&
                     offsetof(SM, tail) % 1024 == 0 && SM::kStage % 1024 == 0 && SM::kTail % 1024 == 0,
                 "swizzled buffers must start on 1024-byte boundaries");
-  auto kern = cross_kernel<QT, D, kFP8>;
+  auto kern = cross_kernel<QT, D, kFP8, kCS>;
   // the kernel's register shares add up to what its launch holds; with fewer its
   // warpgroups would wait for registers without end
   cudaFuncAttributes fa;
@@ -1033,31 +1116,39 @@ int launch_cross_typed(const AttnParams& p, const CrossArgs& c, int ctas, cudaSt
   if (fa.numRegs != cross_launch_regs(kFP8)) return PKV_ERR_CUDA;
   static std::atomic<unsigned long long> configured{0};
   if (!smem_once(kern, smem, configured)) return PKV_ERR_CUDA;
-  kern<<<ctas, cross_threads(kFP8), smem, stream>>>(p, c, tk, tv, tq, (int)kv_rows);
-  if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
-  if (!c.cuts) return PKV_OK;
-  // a CTA of the join for each part of the line and up to 32 rows
+  ctas = ctas / kCS * kCS;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (c.part_rows + 31) / 32);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(cross_threads(kFP8));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kCS;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = kCS > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, p, c, tk, tv, tq, (int)kv_rows) != cudaSuccess) return PKV_ERR_CUDA;
+  if (!c.cuts) return PKV_OK;
+  // a CTA of the join for each of the kernel's and up to 32 rows
+  cfg.gridDim = dim3(ctas, (c.part_rows + 31) / 32);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, cross_join_kernel<QT, D>, p, c) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-template <int D>
+template <int D, int kCS>
 int launch_cross_dim(const AttnParams& p, const CrossArgs& c, int q_dtype, int kv_dtype, int ctas,
                      cudaStream_t stream) {
   const bool fp8 = kv_dtype == PKV_FP8_E4M3;
   if (q_dtype == PKV_BF16)
-    return fp8 ? launch_cross_typed<BF16, D, true>(p, c, ctas, stream)
-               : launch_cross_typed<BF16, D, false>(p, c, ctas, stream);
-  return fp8 ? launch_cross_typed<F16, D, true>(p, c, ctas, stream)
-             : launch_cross_typed<F16, D, false>(p, c, ctas, stream);
+    return fp8 ? launch_cross_typed<BF16, D, true, kCS>(p, c, ctas, stream)
+               : launch_cross_typed<BF16, D, false, kCS>(p, c, ctas, stream);
+  return fp8 ? launch_cross_typed<F16, D, true, kCS>(p, c, ctas, stream)
+             : launch_cross_typed<F16, D, false, kCS>(p, c, ctas, stream);
 }
 
 }  // namespace
