@@ -28,10 +28,10 @@
 // epilogue are each CTA's own; only the ring is common (a stage is empty when both have
 // released it).
 //
-// Warps: 0-3 softmax of tile a (or even key tiles), 4-7 of tile b (odd), 8 MMA issuer and
-// TMEM owner, 9-10 TMA producers, 11 makes the items from the line of work and loads the
-// V rows of partial last blocks, 12-15 (E4M3 caches) widen K and V tiles to the query's
-// type where they land.
+// Warps: 0-3 softmax of tile a (or even key tiles), 4-7 of tile b (odd), 8 and 9 issue the
+// MMAs of either (8 owns TMEM), 10 and 11 load, 10 also makes the items from the line of work
+// and loads the V rows of partial last blocks, 12-15 (E4M3 caches) widen K and V tiles to the
+// query's type where they land.
 #ifndef PKV_CROSS_TC_CUH
 #define PKV_CROSS_TC_CUH
 
@@ -46,7 +46,7 @@ using pre_mods::wait_for;
 using pre_mods::widen16;
 
 constexpr int kSoft = 8;       // softmax warps
-constexpr int kIssuer = 8, kTma = 9, kTmaWarps = 2, kMaker = 11, kConvert = 12, kConverts = 4;
+constexpr int kIssuer = 8, kIssuers = 2, kTma = 10, kTmaWarps = 2, kConvert = 12, kConverts = 4;
 constexpr int cross_threads(bool fp8) { return fp8 ? 512 : 384; }
 // Registers: the launch holds 168 for each of 384 threads or 128 for each of 512; the
 // softmax warps take over what the others return.
@@ -104,6 +104,7 @@ struct CrossSmem {
   uint64_t item_full[kItems], item_read[kItems];
   uint64_t landed[kSt], full[kSt], empty[kSt];
   uint64_t q_full[2], q_empty[2];
+  uint64_t turn[2];
   uint64_t s_ready[2], p_half[2], p_ready[2], o_done[2], o_free[2];
   uint64_t other_ready;
   uint64_t tail_full[2], tail_free[2];
@@ -162,26 +163,27 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
     for (int s = 0; s < SM::kSt; ++s) {
       mbar_init(&sm.landed[s], 1);
       mbar_init(&sm.full[s], kFP8 ? kConverts : 1);
-      mbar_init(&sm.empty[s], kCS);
+      mbar_init(&sm.empty[s], kIssuers * kCS);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sm.q_full[x], 1);
-      mbar_init(&sm.q_empty[x], 1);
+      mbar_init(&sm.q_empty[x], kIssuers);
       mbar_init(&sm.s_ready[x], 1);
+      mbar_init(&sm.turn[x], 1);
       mbar_init(&sm.p_half[x], 4);
       mbar_init(&sm.p_ready[x], 4);
       mbar_init(&sm.o_done[x], 1);
       mbar_init(&sm.o_free[x], 4);
       mbar_init(&sm.tail_full[x], 1);
-      mbar_init(&sm.tail_free[x], 1);
+      mbar_init(&sm.tail_free[x], kIssuers);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      // the softmax warps, the issuer, the producers and the converters
-      mbar_init(&sm.item_read[i], kSoft + 1 + kTmaWarps + (kFP8 ? kConverts : 0));
+      // the softmax warps, the issuers, the other producer and the converters
+      mbar_init(&sm.item_read[i], kSoft + kIssuers + kTmaWarps - 1 + (kFP8 ? kConverts : 0));
     }
     mbar_init(&sm.other_ready, 4);
-    mbar_init(&sm.mma_done, 1);
+    mbar_init(&sm.mma_done, kIssuers);
     sm.abort = 0;
     fence_barrier_init();
   }
@@ -263,125 +265,84 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
   tc::fence_after_sync();
 }
 
-// The maker: this CTA's part of the line as items, the V rows of partial last blocks, and
-// which unit the part ends in.
+// This CTA's part of the line, walked by one warp.
+struct Walk {
+  long long T, w, w1;  // the line, where the walk is and ends
+  int parts, s;        // parts of the line, the sequence at w
+  int4 cut0, cut1;     // the unit that the part ends in
+};
+
 template <int D, bool kFP8, int kCS>
-__device__ __forceinline__ void cross_maker(const AttnParams& p, const CrossArgs& c,
-                                            CrossSmem<D, kFP8>& sm) {
-  using SM = CrossSmem<D, kFP8>;
-  volatile int* abort = &sm.abort;
-  const unsigned long long lim = wait_limit(p);
-  const int lane = threadIdx.x & 31, rpt = kRowsM / p.group, hkv = p.num_kv_heads;
-  const long long T = sm.start[p.num_seqs];
-  const int once = sm.cost_unit;
-  // parts of the line, one for each cluster
-  const int parts = (int)max(min((long long)gridDim.x / kCS, T / kLeast), 1LL), part = blockIdx.x / kCS;
-  const int rank = kCS == 2 ? (int)tc::cluster_rank() : 0;
-  long long w = part < parts ? T * part / parts : 0;
-  const long long w1 = part < parts ? T * (part + 1) / parts : 0;
-  int4 cut0 = make_int4(-1, 0, 0, 0), cut1 = cut0;
-  int s = 0;
-  if (w < w1) {  // the last sequence that begins at or before w
+__device__ __forceinline__ Walk walk_begin(const AttnParams& p, const CrossSmem<D, kFP8>& sm) {
+  Walk k;
+  k.T = sm.start[p.num_seqs];
+  k.parts = (int)max(min((long long)gridDim.x / kCS, k.T / kLeast), 1LL);
+  const int part = blockIdx.x / kCS;
+  k.w = part < k.parts ? k.T * part / k.parts : 0;
+  k.w1 = part < k.parts ? k.T * (part + 1) / k.parts : 0;
+  k.cut0 = k.cut1 = make_int4(-1, 0, 0, 0);
+  k.s = 0;
+  if (k.w < k.w1) {  // the last sequence that begins at or before w
     int hi = p.num_seqs - 1;
-    while (s < hi) {
-      const int mid = (s + hi + 1) >> 1;
-      if (sm.start[mid] <= w) s = mid; else hi = mid - 1;
+    while (k.s < hi) {
+      const int mid = (k.s + hi + 1) >> 1;
+      if (sm.start[mid] <= k.w) k.s = mid; else hi = mid - 1;
     }
   }
-  uint32_t n = 0, ntail = 0;
-  bool ok = true;
-  for (; ok; ++n) {
-    CrossItem x = {};
-    while (w < w1) {
-      const int q = sm.qlen[s], len = sm.len[s], nk = tiles_of(len);
-      const int tiles = (q + rpt - 1) / rpt, rest = tiles % (2 * kCS);
-      const int cost_rest = rest > kCS ? cost2(kFP8) : kCost1;
-      const long long u2 = (long long)nk * cost2(kFP8) + once, u1 = (long long)nk * cost_rest + once;
-      const long long wholes = (long long)hkv * (tiles / (2 * kCS)), off = w - sm.start[s];
-      const bool whole = off < wholes * u2;
-      const long long k = whole ? off / u2 : wholes + (off - wholes * u2) / u1;
-      const long long u0 = sm.start[s] + (whole ? k * u2 : wholes * u2 + (k - wholes) * u1);
-      const long long u = whole ? u2 : u1;
-      const int cost = whole ? cost2(kFP8) : cost_rest;
-      // tiles whose place on the line is in [w, w1)
-      auto tile_at = [&](long long at) {
-        const long long d = at - u0 - once;
-        return d <= 0 ? 0 : (int)min((d + cost - 1) / cost, (long long)nk);
-      };
-      const int a = w <= u0 ? 0 : tile_at(w), b = w1 >= u0 + u ? nk : tile_at(w1);
-      const bool begins = w <= u0;
-      w = u0 + u;
-      const int seq = s;
-      while (s + 1 < p.num_seqs && sm.start[s + 1] <= w) ++s;
-      if (a >= b && !(nk == 0 && begins)) continue;
-      x.live = 1;
-      x.seq = seq;
-      x.kvh = (int)(k % hkv);
-      x.len = len;
-      x.q0 = sm.q0[seq];
-      const int n0 = whole ? 2 * kCS : rest, mine = tiles_of_rank(n0, rank, kCS);
-      x.t0[0] = ((int)(k / hkv) * (2 * kCS) + (rank ? tiles_of_rank(n0, 0, kCS) : 0)) * rpt;
-      x.t0[1] = x.t0[0] + rpt;
-      x.nt[0] = mine > 0 ? min(rpt, q - x.t0[0]) : 0;
-      x.nt[1] = mine > 1 ? min(rpt, q - x.t0[1]) : 0;
-      x.kt0 = a;
-      x.kt1 = b;
-      x.part = a == 0 && b == nk ? -1 : 2 * (int)blockIdx.x + (a == 0 ? 1 : 0);
-      x.tail = !kFP8 && b == nk && (len & (kBlockSize - 1)) != 0 ? ((len - 1) % kTileKeys) / kBlockSize
-                                                                  : -1;
-      if (a == 0 && b < nk && mine > 0) {
-        // the unit goes on in the parts up to the one with its last tile
-        const long long last = u0 + once + (long long)(nk - 1) * cost;
-        cut0 = make_int4((int)(((last + 1) * parts + T - 1) / T - 1), x.q0 + x.t0[0], x.nt[0], x.nt[1]);
-        cut1 = make_int4(x.kvh, 0, 0, 0);
-      }
-      break;
+  return k;
+}
+
+// The next item of the part (none: live is 0).
+template <int D, bool kFP8, int kCS>
+__device__ __forceinline__ CrossItem walk_on(const AttnParams& p, const CrossSmem<D, kFP8>& sm, Walk& v,
+                                             int rank) {
+  const int rpt = kRowsM / p.group, hkv = p.num_kv_heads, once = sm.cost_unit;
+  CrossItem x = {};
+  while (v.w < v.w1) {
+    const int q = sm.qlen[v.s], len = sm.len[v.s], nk = tiles_of(len);
+    const int tiles = (q + rpt - 1) / rpt, rest = tiles % (2 * kCS);
+    const int cost_rest = rest > kCS ? cost2(kFP8) : kCost1;
+    const long long u2 = (long long)nk * cost2(kFP8) + once, u1 = (long long)nk * cost_rest + once;
+    const long long wholes = (long long)hkv * (tiles / (2 * kCS)), off = v.w - sm.start[v.s];
+    const bool whole = off < wholes * u2;
+    const long long k = whole ? off / u2 : wholes + (off - wholes * u2) / u1;
+    const long long u0 = sm.start[v.s] + (whole ? k * u2 : wholes * u2 + (k - wholes) * u1);
+    const long long u = whole ? u2 : u1;
+    const int cost = whole ? cost2(kFP8) : cost_rest;
+    // tiles whose place on the line is in [w, w1)
+    auto tile_at = [&](long long at) {
+      const long long d = at - u0 - once;
+      return d <= 0 ? 0 : (int)min((d + cost - 1) / cost, (long long)nk);
+    };
+    const int a = v.w <= u0 ? 0 : tile_at(v.w), b = v.w1 >= u0 + u ? nk : tile_at(v.w1);
+    const bool begins = v.w <= u0;
+    const int seq = v.s;
+    v.w = u0 + u;
+    while (v.s + 1 < p.num_seqs && sm.start[v.s + 1] <= v.w) ++v.s;
+    if (a >= b && !(nk == 0 && begins)) continue;
+    x.live = 1;
+    x.seq = seq;
+    x.kvh = (int)(k % hkv);
+    x.len = len;
+    x.q0 = sm.q0[seq];
+    const int n0 = whole ? 2 * kCS : rest, mine = tiles_of_rank(n0, rank, kCS);
+    x.t0[0] = ((int)(k / hkv) * (2 * kCS) + (rank ? tiles_of_rank(n0, 0, kCS) : 0)) * rpt;
+    x.t0[1] = x.t0[0] + rpt;
+    x.nt[0] = mine > 0 ? min(rpt, q - x.t0[0]) : 0;
+    x.nt[1] = mine > 1 ? min(rpt, q - x.t0[1]) : 0;
+    x.kt0 = a;
+    x.kt1 = b;
+    x.part = a == 0 && b == nk ? -1 : 2 * (int)blockIdx.x + (a == 0 ? 1 : 0);
+    x.tail = !kFP8 && b == nk && (len & (kBlockSize - 1)) != 0 ? ((len - 1) % kTileKeys) / kBlockSize : -1;
+    if (a == 0 && b < nk && mine > 0) {
+      // the unit goes on in the parts up to the one with its last tile
+      const long long last = u0 + once + (long long)(nk - 1) * cost;
+      v.cut0 = make_int4((int)(((last + 1) * v.parts + v.T - 1) / v.T - 1), x.q0 + x.t0[0], x.nt[0], x.nt[1]);
+      v.cut1 = make_int4(x.kvh, 0, 0, 0);
     }
-    bool good = true;
-    if (lane == 0) {
-      const int slot = n % kItems;
-      if (n >= kItems) good = wait_for(&sm.item_read[slot], ((n / kItems) - 1) & 1, abort, lim);
-      if (good) {
-        sm.item[slot] = x;
-        mbar_arrive(&sm.item_full[slot]);
-      }
-    }
-    ok = __shfl_sync(kFull, (int)good, 0) != 0;
-    if (!ok || !x.live) break;
-    if (x.tail >= 0) {
-      // V rows of the step that holds the partial block, rows past the states as zeros (in
-      // the product 0 * NaN would be NaN), with the ring's swizzle
-      const int buf = ntail & 1;
-      if (lane == 0 && ntail >= 2) good = wait_for(&sm.tail_free[buf], ((ntail >> 1) - 1) & 1, abort, lim);
-      ok = __shfl_sync(kFull, (int)good, 0) != 0;
-      if (!ok) break;
-      constexpr int kChunks = D / 8;  // 16-byte chunks of a row
-      const int b = (x.len - 1) / kBlockSize;
-      const int blk = __ldg(p.block_tables + (size_t)x.seq * p.max_blocks_per_seq + b);
-      const bool in = blk >= 0 && blk < p.num_blocks;
-#pragma unroll
-      for (int i = 0; i < kBlockSize * kChunks / 32; ++i) {
-        const int e = lane + 32 * i, r = e / kChunks, ch = e % kChunks;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (in && b * kBlockSize + r < x.len)
-          v = __ldg(reinterpret_cast<const uint4*>(
-                        p.v_cache + (((size_t)blk * hkv + x.kvh) * kBlockSize + r) * (kChunks * 16)) + ch);
-        *reinterpret_cast<uint4*>(&sm.tail[buf][0] + (ch >> 3) * (SM::kTail / 2) + r * 128 +
-                                  (((ch & 7) ^ (r & 7)) << 4)) = v;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.tail_full[buf]);
-      ++ntail;
-    }
+    break;
   }
-  if (lane == 0) {
-    if (!ok) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
-    if (c.cuts) {
-      c.cuts[2 * blockIdx.x] = cut0;
-      c.cuts[2 * blockIdx.x + 1] = cut1;
-    }
-  }
+  return x;
 }
 
 // ---- loads ---------------------------------------------------------------------------------
@@ -401,10 +362,11 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
   const unsigned long long lim = wait_limit(p);
   const int lane = threadIdx.x & 31, g = p.group;
   // the boxes of a tile's blocks are dealt out to the producer warps of all CTAs
-  const bool my_lane = (lane & (2 * kCS - 1)) == (kCS == 2 ? 2 * (int)tc::cluster_rank() : 0) + pw;
+  const int rank = kCS == 2 ? (int)tc::cluster_rank() : 0;
+  const bool my_lane = (lane & (2 * kCS - 1)) == 2 * rank + pw;
   constexpr uint16_t kAll = (1u << kCS) - 1;
   uint8_t* const ring = &sm.ring[0][0];
-  uint32_t pos = 0, nq = 0;
+  uint32_t pos = 0, nq = 0, ntail = 0;
   bool ok = true;
   CrossItem x = {};
   auto fetch = [&](int ch) -> int {                 // table entry of block 32 ch + lane
@@ -449,8 +411,51 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
     ++pos;
     return true;
   };
+  // V rows of the step that holds the partial last block, rows past the states as zeros (in the
+  // product 0 * NaN would be NaN), with the ring's swizzle
+  auto load_tail = [&]() -> bool {
+    const int buf = ntail & 1;
+    bool good = true;
+    if (lane == 0 && ntail >= 2) good = wait_for(&sm.tail_free[buf], ((ntail >> 1) - 1) & 1, abort, lim);
+    if (!__shfl_sync(kFull, (int)good, 0)) return false;
+    constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+    const int b = (x.len - 1) / kBlockSize;
+    const int blk = __ldg(p.block_tables + (size_t)x.seq * p.max_blocks_per_seq + b);
+    const bool in = blk >= 0 && blk < p.num_blocks;
+#pragma unroll
+    for (int i = 0; i < kBlockSize * kChunks / 32; ++i) {
+      const int e = lane + 32 * i, r = e / kChunks, ch = e % kChunks;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (in && b * kBlockSize + r < x.len)
+        v = __ldg(reinterpret_cast<const uint4*>(
+                      p.v_cache + (((size_t)blk * p.num_kv_heads + x.kvh) * kBlockSize + r) * (kChunks * 16)) + ch);
+      *reinterpret_cast<uint4*>(&sm.tail[buf][0] + (ch >> 3) * (SM::kTail / 2) + r * 128 +
+                                (((ch & 7) ^ (r & 7)) << 4)) = v;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.tail_full[buf]);
+    ++ntail;
+    return true;
+  };
+  Walk walk = {};
+  if (pw == 0) walk = walk_begin<D, kFP8, kCS>(p, sm);
   for (uint32_t n = 0; ok; ++n) {
-    ok = take(sm, n, x, abort, lim);
+    if (pw == 0) {  // makes the items, for the others too
+      x = walk_on<D, kFP8, kCS>(p, sm, walk, rank);
+      bool good = true;
+      if (lane == 0) {
+        const int slot = n % kItems;
+        if (n >= kItems) good = wait_for(&sm.item_read[slot], ((n / kItems) - 1) & 1, abort, lim);
+        if (good) {
+          sm.item[slot] = x;
+          mbar_arrive(&sm.item_full[slot]);
+        }
+      }
+      ok = __shfl_sync(kFull, (int)good, 0) != 0;
+    } else {
+      ok = take(sm, n, x, abort, lim);
+    }
     if (!ok || !x.live) break;
     if (x.kt0 == x.kt1) continue;
     if (pw == 0) {
@@ -493,8 +498,13 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
     if (ok) ok = issue(x.kt0, row_for(x.kt0), false);
     for (int t = x.kt0; ok && t < x.kt1; ++t) {
       if (t + 1 < x.kt1) ok = issue(t + 1, row_for(t + 1), false);
+      if (ok && pw == 0 && t == x.kt1 - 1 && x.tail >= 0) ok = load_tail();
       if (ok) ok = issue(t, row_for(t), true);
     }
+  }
+  if (pw == 0 && lane == 0 && c.cuts) {
+    c.cuts[2 * blockIdx.x] = walk.cut0;
+    c.cuts[2 * blockIdx.x + 1] = walk.cut1;
   }
   if (!ok && lane == 0) {
     flag_error(p.errors, PKV_DEVERR_TIMEOUT);
@@ -590,13 +600,20 @@ __device__ __forceinline__ void issue_half(uint32_t d, uint32_t a, uint64_t dv, 
   }
 }
 
-// ---- MMA issuer ------------------------------------------------------------------------------
-// Two query tiles, per key tile t: P_a(t) V(t), S_a(t+1), P_b(t) V(t), S_b(t+1); one: S_0(0),
-// S_1(1), then P_x(t) V(t), S_x(t+2) with x = t & 1; none (the other CTA's): stages are given
-// back as they fill.  The whole warp runs the loop, so that counters and descriptors are the
-// same in all lanes; one elected lane issues.
+// ---- MMA issuers -----------------------------------------------------------------------------
+// One thread for each softmax warpgroup: with two query tiles P_y(t) V(t), S_y(t+1) for every
+// key tile t; with one, of every other key tile, t = y first; with none (the other CTA's) the
+// first one gives the stages back as they fill.  (One for both left the tensor pipe idle
+// while it waited and committed: without any softmax a key tile took 3100 cycles of which
+// 2050 are MMAs.)
+//
+// A stage is empty when both issuers of every CTA have released it; whoever uses it alone
+// does so twice.  Places of a unit's tiles in the ring: K0, K1, V0, K2, V1, ..., V(n-1).
+__device__ __forceinline__ uint32_t k_place(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ uint32_t v_place(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
+
 template <class QT, int D, bool kFP8, int kCS>
-__device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, kFP8>& sm, uint32_t tmem) {
+__device__ __forceinline__ bool issue_group(const AttnParams& p, CrossSmem<D, kFP8>& sm, uint32_t tmem, int y) {
   using SM = CrossSmem<D, kFP8>;
   constexpr int kSt = SM::kSt;
   constexpr uint32_t kAB = std::is_same<QT, BF16>::value ? 1u : 0u;
@@ -605,135 +622,124 @@ __device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, k
   constexpr uint64_t kStage = SM::kStage >> 4;
   volatile int* abort = &sm.abort;
   const unsigned long long lim = wait_limit(p);
-  const bool leader = tc::elect_one();
-  auto commit = [&](uint64_t* bar) {
-    if (leader) tc::mma_commit(bar);
-  };
-  auto release = [&](int st) {  // a stage, to the producers of all CTAs
-    if constexpr (kCS == 2) {
-      if (leader) tc::mma_commit_all(&sm.empty[st], 3);
-    } else {
-      commit(&sm.empty[st]);
-    }
-  };
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __shfl_sync(kFull, (int)wait_bar(bar, parity, abort, lim), 0) != 0;
-  };
-  const uint64_t dq[2] = {tc::smem_desc(smem_u32(&sm.q[0][0]), 16, 1024, tc::kLayoutSw128),
-                          tc::smem_desc(smem_u32(&sm.q[1][0]), 16, 1024, tc::kLayoutSw128)};
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_for(bar, parity, abort, lim); };
+  const uint64_t dq0 = tc::smem_desc(smem_u32(&sm.q[0][0]), 16, 1024, tc::kLayoutSw128);
   const uint64_t dk0 = tc::smem_desc(smem_u32(&sm.ring[0][0]), 16, 1024, tc::kLayoutSw128);
   const uint64_t dv0 = tc::smem_desc(smem_u32(&sm.ring[0][0]), kHalf, 1024, tc::kLayoutSw128);
   const uint64_t dt0 = tc::smem_desc(smem_u32(&sm.tail[0][0]), SM::kTail / 2, 1024, tc::kLayoutSw128);
-  uint32_t pos = 0, np[2] = {0, 0}, nit[2] = {0, 0}, nq = 0, ntail = 0;
-  bool ok = true;
+  const uint32_t s_col = tmem + y * 128, o_col = tmem + kColO + y * 128;
+  uint32_t base = 0, np = 0, nit = 0, nq = 0, ntail = 0;  // ring place of the unit, P consumed, ...
+  uint32_t turns = 0;   // handed over by the other issuer
+  bool last_other = false;  // the last product was the other's
   CrossItem x = {};
-  auto acquire = [&](int& st) -> bool {
-    st = pos % kSt;
-    const bool r = wait(&sm.full[st], (pos / kSt) & 1);
-    ++pos;
-    if (r) tc::fence_after_sync();
-    return r;
-  };
-  // scores of the query tile in buffer b, for softmax warpgroup y
-  auto scores = [&](int y, int b, int st) {
-    if (leader) issue_mods_scores<D>(tmem + y * 128, b ? dq[1] : dq[0], dk0 + st * kStage, kIdescS);
-    commit(&sm.s_ready[y]);
-  };
-  // the product of 64 states' weights while the softmax is at the others'
-  auto product = [&](int y, int st, int t, bool first, bool last) -> bool {
-    if (!wait(&sm.p_half[y], np[y] & 1)) return false;
-    if (first && nit[y] >= 1 && !wait(&sm.o_free[y], (nit[y] - 1) & 1))
-      return false;  // the previous item's O has been read out
-    const int ts = t == x.kt1 - 1 ? x.tail : -1;
-    if (ts >= 0 && !wait(&sm.tail_full[ntail & 1], (ntail >> 1) & 1)) return false;
-    tc::fence_after_sync();
-    const uint64_t dv = dv0 + st * kStage, dt = dt0 + (ntail & 1) * (SM::kTail >> 4);
-    const uint32_t o = tmem + kColO + y * 128, at = tmem + y * 128;
-    if (leader) issue_half<0>(o, at, dv, dt, ts, !first, kIdescO);
-    if (!wait(&sm.p_ready[y], np[y] & 1)) return false;
-    ++np[y];
-    tc::fence_after_sync();
-    if (leader) issue_half<kTileKeys / 32>(o, at, dv, dt, ts, 1, kIdescO);
-    if (last) commit(&sm.o_done[y]);
-    return true;
-  };
-  for (uint32_t n = 0; ok; ++n) {
-    ok = take(sm, n, x, abort, lim);
-    if (!ok || !x.live) break;
-    if (x.kt0 == x.kt1) {  // nothing to multiply: the rows are zeros
-      continue;
-    }
-    const int t0 = x.kt0, t1 = x.kt1;
-    int kst = 0, vst = 0;
-    if (x.nt[1] > 0) {
-      const int b0 = nq & 1, b1 = b0 ^ 1;
-      ok = wait(&sm.q_full[b0], (nq >> 1) & 1) && wait(&sm.q_full[b1], ((nq + 1) >> 1) & 1);
-      nq += 2;
-      if (ok) ok = acquire(kst);
-      if (ok) {
-        scores(0, b0, kst);
-        if (t0 + 1 == t1) commit(&sm.q_empty[b0]);
-        scores(1, b1, kst);
-        if (t0 + 1 == t1) commit(&sm.q_empty[b1]);
-        release(kst);
+  for (uint32_t n = 0;; ++n) {
+    const int slot = n % kItems;
+    if (!wait(&sm.item_full[slot], (n / kItems) & 1)) return false;
+    x = sm.item[slot];
+    mbar_arrive(&sm.item_read[slot]);
+    if (!x.live) return true;
+    const int tiles = x.kt1 - x.kt0;
+    if (tiles == 0) continue;  // nothing to multiply: the rows are zeros
+    const bool two = x.nt[1] > 0;
+    auto full = [&](uint32_t place, int& st) -> bool {
+      const uint32_t at = base + place;
+      st = at % kSt;
+      return wait(&sm.full[st], (at / kSt) & 1);
+    };
+    auto release = [&](int st) {  // a stage, to the producers of all CTAs
+      for (int i = two ? 1 : 0; i < 2; ++i) {
+        if constexpr (kCS == 2) tc::mma_commit_all(&sm.empty[st], 3);
+        else tc::mma_commit(&sm.empty[st]);
       }
-      for (int t = t0; ok && t < t1; ++t) {
-        const bool more = t + 1 < t1;
-        ok = (!more || acquire(kst)) && acquire(vst) && product(0, vst, t, t == t0, !more);
-        if (ok && more) {
-          scores(0, b0, kst);
-          if (t + 2 == t1) commit(&sm.q_empty[b0]);
-        }
-        if (ok) ok = product(1, vst, t, t == t0, !more);
-        if (!ok) break;
-        release(vst);
-        if (more) {
-          scores(1, b1, kst);
-          if (t + 2 == t1) commit(&sm.q_empty[b1]);
-          release(kst);
-        }
-      }
-      ++nit[0];
-      ++nit[1];
-    } else if (kCS == 2 && x.nt[0] == 0) {
-      for (int i = 2 * (t1 - t0); ok && i > 0; --i) {
-        ok = acquire(kst);
-        if (ok && leader) {
-          const uint32_t bar = smem_u32(&sm.empty[kst]);
-          tc::mbar_arrive_cluster_release(tc::map_rank(bar, 0));  // (converters wrote there)
-          tc::mbar_arrive_cluster_release(tc::map_rank(bar, 1));
-        }
+    };
+    if (kCS == 2 && x.nt[0] == 0) {
+      for (int i = 0; y == 0 && i < 2 * tiles; ++i) {
+        int st;
+        if (!full(i, st)) return false;
+        const uint32_t bar = smem_u32(&sm.empty[st]);
+        for (int j = 0; j < 2 * kCS; ++j)  // (converters wrote there)
+          tc::mbar_arrive_cluster_release(tc::map_rank(bar, j & 1));
       }
     } else {
-      const int b = nq & 1;
-      ok = wait(&sm.q_full[b], (nq >> 1) & 1);
-      ++nq;
-      auto next_scores = [&](int t) -> bool {
-        if (!acquire(kst)) return false;
-        scores((t - t0) & 1, b, kst);
-        release(kst);
-        if (t == t1 - 1) commit(&sm.q_empty[b]);
+      const int step = two ? 1 : 2, first = two ? 0 : y;
+      const int qb = (nq + (two ? y : 0)) & 1;
+      if (!wait(&sm.q_full[qb], ((nq + (two ? y : 0)) >> 1) & 1)) return false;
+      int kst, vst;
+      auto scores = [&](int i) -> bool {
+        if (!full(k_place(i), kst)) return false;
+        tc::fence_after_sync();
+        issue_mods_scores<D>(s_col, dq0 + qb * (SM::kTile >> 4), dk0 + kst * kStage, kIdescS);
+        tc::mma_commit(&sm.s_ready[y]);
         return true;
       };
-      if (ok) ok = next_scores(t0);
-      if (ok && t0 + 1 < t1) ok = next_scores(t0 + 1);
-      for (int t = t0; ok && t < t1; ++t) {
-        ok = acquire(vst) && product((t - t0) & 1, vst, t, t < t0 + 2, t >= t1 - 2);
-        if (!ok) break;
-        release(vst);
-        if (t + 2 < t1) ok = next_scores(t + 2);
+      if (first < tiles) {
+        if (!scores(first)) return false;
+        release(kst);
       }
-      ++nit[0];
-      if (t1 - t0 > 1) ++nit[1];
+      if (first + step >= tiles) {
+        tc::mma_commit(&sm.q_empty[nq & 1]);
+        if (two) tc::mma_commit(&sm.q_empty[(nq + 1) & 1]);
+      }
+      for (int i = first; i < tiles; i += step) {
+        if (!wait(&sm.p_half[y], np & 1)) return false;
+        if (i == first && nit >= 1 && !wait(&sm.o_free[y], (nit - 1) & 1))
+          return false;  // the previous item's O has been read out
+        if (!full(v_place(i, tiles), vst)) return false;
+        const int ts = i == tiles - 1 ? x.tail : -1;
+        const uint64_t dv = dv0 + vst * kStage, dt = dt0 + (ntail & 1) * (SM::kTail >> 4);
+        if (ts >= 0 && !wait(&sm.tail_full[ntail & 1], (ntail >> 1) & 1)) return false;
+        // the products take turns, in the order of the tiles: the two softmax warpgroups then
+        // stay half a period apart, one at work while the other's MMAs run
+        if (i > 0 || y == 1 || last_other) {
+          if (!wait(&sm.turn[y], turns & 1)) return false;
+          ++turns;
+        }
+        tc::fence_after_sync();
+        // 64 states' weights while the softmax is at the others'
+        issue_half<0>(o_col, s_col, dv, dt, ts, i != first, kIdescO);
+        if (!wait(&sm.p_ready[y], np & 1)) return false;
+        ++np;
+        tc::fence_after_sync();
+        issue_half<kTileKeys / 32>(o_col, s_col, dv, dt, ts, 1, kIdescO);
+        const bool hand = two || i + 1 < tiles || y == 1;  // (a unit begins with the first)
+        if (i + step < tiles) {
+          if (!scores(i + step)) return false;
+          if (hand) mbar_arrive(&sm.turn[y ^ 1]);
+          release(vst);
+          release(kst);
+          if (i + 2 * step >= tiles) {  // the item's last scores
+            tc::mma_commit(&sm.q_empty[nq & 1]);
+            if (two) tc::mma_commit(&sm.q_empty[(nq + 1) & 1]);
+          }
+        } else {
+          if (hand) mbar_arrive(&sm.turn[y ^ 1]);
+          tc::mma_commit(&sm.o_done[y]);
+          release(vst);
+        }
+      }
+      if (first < tiles) ++nit;
+      last_other = (two || (tiles & 1) == 0 ? 1 : 0) != y;
     }
-    if (ok && x.tail >= 0) {
-      commit(&sm.tail_free[ntail & 1]);
+    if (x.tail >= 0) {
+      // (waited for also where the other one used it: the buffer's phases keep their order)
+      if (!wait(&sm.tail_full[ntail & 1], (ntail >> 1) & 1)) return false;
+      tc::mma_commit(&sm.tail_free[ntail & 1]);
       ++ntail;
     }
+    nq += (x.nt[0] > 0) + two;
+    base += 2 * tiles;
   }
-  if (!ok && leader) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
-  commit(&sm.mma_done);
-  mbar_wait(&sm.mma_done, 0, 100000000ull);
+}
+
+template <class QT, int D, bool kFP8, int kCS>
+__device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, kFP8>& sm, uint32_t tmem, int y) {
+  y = __shfl_sync(kFull, y, 0);  // (the same in every lane for the compiler, too)
+  if (tc::elect_one()) {
+    if (!issue_group<QT, D, kFP8, kCS>(p, sm, tmem, y)) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+    tc::mma_commit(&sm.mma_done);
+    mbar_wait(&sm.mma_done, 0, 100000000ull);
+  }
+  __syncwarp();
 }
 
 // Weights 2^z of 32 states as 16 packed pairs, and their sums.
@@ -1019,10 +1025,9 @@ __global__ void __launch_bounds__(cross_threads(kFP8), 1)
   const uint32_t tmem = sm.tmem_base;
   if (warp >= kSoft) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(cross_other_regs(kFP8)));
-    if (warp == kIssuer) cross_issuer<QT, D, kFP8, kCS>(p, sm, tmem);
+    if (warp < kIssuer + kIssuers) cross_issuer<QT, D, kFP8, kCS>(p, sm, tmem, warp - kIssuer);
     else if (warp < kTma + kTmaWarps)
       cross_producer<D, kFP8, kCS>(p, c, sm, tm_k, tm_v, tm_q, kv_rows, warp - kTma);
-    else if (warp == kMaker) cross_maker<D, kFP8, kCS>(p, c, sm);
     else if constexpr (kFP8) cross_converter<QT, D>(p, sm, warp - kConvert);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(cross_soft_regs(kFP8)));
