@@ -30,7 +30,7 @@ bool may_cut(int max_encoder_len) { return max_encoder_len > 128; }
 bool pairs(int group, int max_q_len, int total_q, int num_seqs) {
   if (const char* e = getenv("PKV_PAIR")) return e[0] == '1' && max_q_len > 128 / group;
   const int tokens = 128 / group;
-  return max_q_len > 2 * tokens && total_q >= 2LL * tokens * num_seqs;
+  return false && max_q_len > 2 * tokens && total_q >= 2LL * tokens * num_seqs;
 }
 
 constexpr size_t kCutBytes = 2 * kCtas * 16;

@@ -5,8 +5,9 @@
 // A row is a (query token, head of the group) pair, a query tile is 128 rows of whole
 // tokens, a key tile 128 states.  The mathematics is that of prefill_tc.cuh:
 //   S = Q K^T in TMEM, P = 2^(s - m) back over S as 16-bit pairs, O += P V,
-// with a running maximum m that moves (and has O rescaled) only when a row's scores
-// exceed it by more than 2^8, and out = O / sum(P).
+// where m only has to be near the row's maximum, since P, sums and O are floating-point
+// numbers: it starts as the maximum of the first 64 states' scores and moves (and O is
+// rescaled) only when the weights of 64 states add up to more than 2^12; out = O / sum(P).
 //
 // Work.  A unit is a sequence, KV head and one or two query tiles.  With two, K and V of a
 // key tile feed both, each tile having its own softmax warpgroup; with one (a token, a
@@ -73,6 +74,7 @@ constexpr int kCostUnit = 14;  // at most a quarter of a CTA's part of the tiles
                                // begins with a unit, or what is left of one, anyway
 constexpr int kLeast = 8;  // of a CTA's part (at least cost2, so that every part inside a unit
                            // holds the start of a tile)
+constexpr float kMostSum = 4096.0f;    // of 64 weights, before m moves
 constexpr int kItems = 4;              // made ahead
 
 struct CrossItem {
@@ -105,7 +107,7 @@ struct CrossSmem {
   uint64_t landed[kSt], full[kSt], empty[kSt];
   uint64_t q_full[2], q_empty[2];
   uint64_t turn[2];
-  uint64_t s_ready[2], p_half[2], p_ready[2], o_done[2], o_free[2];
+  uint64_t s_ready[2], p_half[2], p_ready[2], o_half[2], o_done[2], o_free[2];
   uint64_t other_ready;
   uint64_t tail_full[2], tail_free[2];
   uint64_t mma_done;
@@ -172,6 +174,7 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
       mbar_init(&sm.turn[x], 1);
       mbar_init(&sm.p_half[x], 4);
       mbar_init(&sm.p_ready[x], 4);
+      mbar_init(&sm.o_half[x], 1);
       mbar_init(&sm.o_done[x], 1);
       mbar_init(&sm.o_free[x], 4);
       mbar_init(&sm.tail_full[x], 1);
@@ -697,6 +700,7 @@ __device__ __forceinline__ bool issue_group(const AttnParams& p, CrossSmem<D, kF
         tc::fence_after_sync();
         // 64 states' weights while the softmax is at the others'
         issue_half<0>(o_col, s_col, dv, dt, ts, i != first, kIdescO);
+        tc::mma_commit(&sm.o_half[y]);
         if (!wait(&sm.p_ready[y], np & 1)) return false;
         ++np;
         tc::fence_after_sync();
@@ -813,80 +817,97 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
       if (!ok) break;
       if (!idle) {
         tc::fence_after_sync();
-        // Exponents z = s * scale - m of the row's scores and their maximum, with m as it was
-        // after the last tile; the weights of the first 64 states.  Where no row of the warp
-        // exceeds its m by more than 8 (nearly always: m only has to be near the maximum, the
-        // weights are floating-point numbers) that is all; else those rows' m moves, what
-        // they have so far is scaled to it, and the tile is done over.  (With the maximum
-        // first, the exponentials wait for it: 570 of 2000 cycles.)
-        float pk[32], z2[64], m = m_run == -INFINITY ? 0.0f : m_run;
-        float2 t2[4];
+        // 64 states at a time: weights 2^(s * scale - m) with m as it is.  Their sum tells
+        // whether that m will do for all rows of the warp, as it nearly always does; else m
+        // moves for those that it does not do for, what they have so far is scaled to it, and
+        // the weights are taken again.  (The maximum of every tile first costs 570 of a
+        // step's 2000 cycles.)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float pk[32];
+          float2 t2[4];
+          const uint32_t s_at = s_col + 64 * half;
+          const int more = left - 64 * half;   // states from the half on
 #pragma unroll 1
-        for (int again = 0;; again = 1) {
-          const float2 f2 = make_float2(qs, qs), m2 = make_float2(-m, -m);
-          float mx[4];
+          for (int again = 0;; again = 1) {
+            const float m = m_run == -INFINITY ? 0.0f : m_run;
+            const float2 f2 = make_float2(qs, qs), m2 = make_float2(-m, -m);
+            auto exponents = [&](float* sv, int k) {  // of 32 states from k on, in place
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            mx[i] = -INFINITY;
-            t2[i] = make_float2(0.0f, 0.0f);
-          }
-          float sv[2][32];
-          tc::tmem_ld32(s_col, sv[0]);
+              for (int e = 0; e < 32; e += 2) {
+                const float2 v = __ffma2_rn(make_float2(sv[e], sv[e + 1]), f2, m2);
+                sv[e] = v.x;
+                sv[e + 1] = v.y;
+              }
+              if (more < k + 32) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+                for (int e = 0; e < 32; ++e) sv[e] = k + e < more ? sv[e] : -INFINITY;
+              }
+            };
+            float sv[2][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t2[i] = make_float2(0.0f, 0.0f);
+            tc::tmem_ld32(s_at, sv[0]);
             tc::tmem_wait_ld();
-            if (k < 3) tc::tmem_ld32(s_col + 32 * (k + 1), sv[(k + 1) & 1]);
-            float* const zk = k < 2 ? sv[k & 1] : z2 + 32 * (k - 2);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 v = __ffma2_rn(make_float2(sv[k & 1][e], sv[k & 1][e + 1]), f2, m2);
-              zk[e] = v.x;
-              zk[e + 1] = v.y;
-            }
-            if (left < 32 * (k + 1)) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) zk[e] = 32 * k + e < left ? zk[e] : -INFINITY;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], zk[e], zk[e + 1]);
-            if (k < 2) weights<QT>(zk, pk + 16 * k, t2);
-          }
-          const float mz = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-          const bool need = m_run == -INFINITY ? mz > -INFINITY : mz > kRescaleAt;
-          // (once over is enough: only scores of 2^27 and more, whose differences fp32 does not
-          // hold, could exceed their own maximum again)
-          if (again || !__any_sync(kFull, need)) break;
-          // (a row without a weight so far has zeros)
-          const float alpha = !need ? 1.0f : m_run == -INFINITY ? 0.0f : fast_exp2(-mz);
-          if (need) m = m_run = m + mz;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) l2[i] = __fmul2_rn(l2[i], make_float2(alpha, alpha));
-          // O is complete up to the tile before (the scores were issued behind its product)
-          if (t > first) {
+            tc::tmem_ld32(s_at + 32, sv[1]);
+            exponents(sv[0], 0);
+            weights<QT>(sv[0], pk, t2);
+            tc::tmem_wait_ld();
+            exponents(sv[1], 32);
+            weights<QT>(sv[1], pk + 16, t2);
+            const float sum = ((t2[0].x + t2[0].y) + (t2[1].x + t2[1].y)) +
+                              ((t2[2].x + t2[2].y) + (t2[3].x + t2[3].y));
+            // (what rows past the tokens hold does not matter)
+            const bool off = r < rows && (m_run == -INFINITY || sum > kMostSum);
+            // (once over is enough: only scores of 2^27 and more, whose differences fp32 does
+            // not hold, could exceed their own maximum)
+            if (again || !__any_sync(kFull, off)) break;
+            float mz = -INFINITY;
 #pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
-              float ov[32];
-              tc::tmem_ld32(o_col + k, ov);
+            for (int k = 0; k < 64; k += 32) {
+              float z[32];
+              tc::tmem_ld32(s_at + k, z);
               tc::tmem_wait_ld();
+              exponents(z, k);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-              tc::tmem_st32(o_col + k, ov);
+              for (int e = 0; e < 32; e += 2) mz = fmax3(mz, z[e], z[e + 1]);
+            }
+            const bool move = off && mz > -INFINITY;
+            // (a row without a weight so far has zeros)
+            const float alpha = !move ? 1.0f : m_run == -INFINITY ? 0.0f : fast_exp2(-mz);
+            if (move) m_run = m + mz;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l2[i] = __fmul2_rn(l2[i], make_float2(alpha, alpha));
+            // O holds the tiles before this one (its scores were issued behind their product),
+            // and the first half of this one
+            if (half == 1 || t > first) {
+              if (half == 1) {
+                ok = wait(&sm.o_half[y], ns & 1);
+                if (!ok) break;
+                tc::fence_after_sync();
+              }
+#pragma unroll 1
+              for (int k = 0; k < D; k += 32) {
+                float ov[32];
+                tc::tmem_ld32(o_col + k, ov);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+                tc::tmem_st32(o_col + k, ov);
+              }
             }
           }
-        }
-        // P over the scores, which have all been read
-        tc::tmem_st32(s_col, pk);
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_half[y]);
-        weights<QT>(z2, pk, t2);
-        weights<QT>(z2 + 32, pk + 16, t2);
-        tc::tmem_st32(s_col + 32, pk);
+          if (!ok) break;
+          // P over scores that have been read
+          tc::tmem_st32(s_col + 32 * half, pk);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) l2[i] = __fadd2_rn(l2[i], t2[i]);
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
+          for (int i = 0; i < 4; ++i) l2[i] = __fadd2_rn(l2[i], t2[i]);
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (half == 0 && lane == 0) mbar_arrive(&sm.p_half[y]);
+        }
+        if (!ok) break;
       } else if (lane == 0) {
         mbar_arrive(&sm.p_half[y]);
       }
