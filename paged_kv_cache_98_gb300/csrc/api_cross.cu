@@ -3,7 +3,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 
 #include "common.cuh"
 #include "launch.h"
@@ -25,13 +24,6 @@ int part_rows(int group, int max_q_len) {
 
 // Units of one key tile are never cut.
 bool may_cut(int max_encoder_len) { return max_encoder_len > 128; }
-
-// Pairs of CTAs share units of four query tiles.
-bool pairs(int group, int max_q_len, int total_q, int num_seqs) {
-  if (const char* e = getenv("PKV_PAIR")) return e[0] == '1' && max_q_len > 128 / group;
-  const int tokens = 128 / group;
-  return false && max_q_len > 2 * tokens && total_q >= 2LL * tokens * num_seqs;
-}
 
 constexpr size_t kCutBytes = 2 * kCtas * 16;
 static_assert(kCutBytes % 256 == 0, "what follows is aligned");
@@ -113,7 +105,6 @@ int pkv_paged_attention_cross(void* out, const void* q, const void* k_cache, con
   c.max_q = std::min(max_q_len, total_q);
   c.part_rows = part_rows(p.group, c.max_q);
   c.box_tokens = std::min(128 / p.group, c.max_q);
-  c.cluster = pairs(p.group, c.max_q, total_q, num_seqs) ? 2 : 1;
   if (need > 0) {
     uint8_t* w = static_cast<uint8_t*>(workspace);
     const size_t rows = 2 * (size_t)kCtas * c.part_rows;
@@ -128,8 +119,7 @@ int pkv_paged_attention_cross(void* out, const void* q, const void* k_cache, con
     p.block_tables = block_tables + (size_t)s0 * max_blocks_per_seq;
     p.context_lens = encoder_lens + s0;
     p.query_start_loc = query_start_loc + s0;
-    const auto launch = c.cluster == 2 ? (head_dim == 64 ? pkv::launch_cross_pair_d64 : pkv::launch_cross_pair_d128)
-                                       : (head_dim == 64 ? pkv::launch_cross_one_d64 : pkv::launch_cross_one_d128);
+    const auto launch = head_dim == 64 ? pkv::launch_cross_d64 : pkv::launch_cross_d128;
     const int rc = launch(p, c, (int)q_dtype, (int)kv_dtype, ctas, static_cast<cudaStream_t>(stream));
     if (rc != PKV_OK) return rc;
   }

@@ -15,19 +15,17 @@
 // tiles, each into an O of its own, and the first one joins the two at the end.
 // Sequences differ in both lengths and there may be one unit or many thousand, so units
 // are not dealt out: all key tiles of the call lie one behind the other on a line of work
-// (a tile counts kCost1 or cost2, what a unit costs once kCostUnit), which is cut into
+// (a tile counts kCost1 or kCost2, what a unit costs once kCostUnit), which is cut into
 // one equal part for each CTA, one CTA a processor.  Cuts fall inside units, also where
 // queries are few and inputs long; what a CTA has of a cut unit goes to the workspace as a
 // normalised partial and its log-sum-exp, at most two per CTA, and a second kernel, launched
 // as a dependent, joins the parts of a unit.  The line is walked with integers that every
 // CTA computes for itself, so the result depends on the batch alone.
 //
-// Pairs (kCS = 2).  Loads bind prompts: with 64 KB for every key tile and processor, L2 gives
-// 5.5 TB/s and a tile takes 1.8 us on most processors and up to 2.9 on some.  So there two
-// CTAs of a cluster share a unit of four query tiles and the same part of the line: each
-// issues half of the boxes of every K and V tile, multicast to both.  Products, softmax and
-// epilogue are each CTA's own; only the ring is common (a stage is empty when both have
-// released it).
+// Two CTAs of a cluster that share four query tiles, each loading half of every K and V tile
+// and multicasting it to both, were built and measured: 741 against 747 us for four prompts of
+// 1024 tokens over 16384 states, and slower with ragged prompts (in a unit of few tiles
+// one CTA waits for the other).  Loads alone take 515 us of those, MMAs alone 495.
 //
 // Warps: 0-3 softmax of tile a (or even key tiles), 4-7 of tile b (odd), 8 and 9 issue the
 // MMAs of either (8 owns TMEM), 10 and 11 load, 10 also makes the items from the line of work
@@ -61,18 +59,13 @@ constexpr bool cross_regs_fit(bool fp8) {
 static_assert(cross_regs_fit(false) && cross_regs_fit(true),
               "setmaxnreg may only share out what the launch holds");
 
-// Query tiles of a unit: two in each CTA of its cluster, fewer in a sequence's last one.
-// CTA 0 has the larger half of those, CTA 1 the smaller, perhaps none.
-constexpr int tiles_of_rank(int n, int rank, int cs) { return cs == 1 ? n : rank == 0 ? (n + 1) / 2 : n / 2; }
-
 // The line of work, in quarters of a key tile's time with one query tile (measured: 1.03 us
-// with one, 1.78 with two, and 3 to 4 us for a unit once; a tile of an E4M3 cache goes by its
-// widening).
+// with one, 1.6 with two, and 3 to 4 us for a unit once).
 constexpr int kCost1 = 4;
-constexpr int cost2(bool fp8) { return fp8 ? 6 : 7; }
-constexpr int kCostUnit = 14;  // at most a quarter of a CTA's part of the tiles: every part
+constexpr int kCost2 = 6;
+constexpr int kCostUnit = 14;  // at most half of a CTA's part of the tiles: every part
                                // begins with a unit, or what is left of one, anyway
-constexpr int kLeast = 8;  // of a CTA's part (at least cost2, so that every part inside a unit
+constexpr int kLeast = 8;  // of a CTA's part (at least kCost2, so that every part inside a unit
                            // holds the start of a tile)
 constexpr float kMostSum = 4096.0f;    // of 64 weights, before m moves
 constexpr int kItems = 4;              // made ahead
@@ -117,29 +110,6 @@ struct CrossSmem {
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
 
-// As wait_for, for arrivals from both CTAs of a cluster.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                             unsigned long long limit_ns) {
-  uint64_t t0 = 0;
-  for (uint32_t it = 1; !tc::mbar_test_cluster(bar, parity); ++it) {
-    if ((it & 63u) == 0) {
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (*abort) return false;
-      if (now - t0 > limit_ns) {
-        *abort = 1;
-        return false;
-      }
-    }
-  }
-  return true;
-}
-
-// Lets `ns` nanoseconds pass.
-__device__ __forceinline__ void settle(unsigned long long ns) {
-  for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < ns;) __nanosleep(1000);
-}
-
 // The next item, for a whole warp; false when the wait gave up.
 template <class SM>
 __device__ __forceinline__ bool take(SM& sm, uint32_t n, CrossItem& x, volatile int* abort,
@@ -155,7 +125,7 @@ __device__ __forceinline__ bool take(SM& sm, uint32_t n, CrossItem& x, volatile 
 // ---- the line of work --------------------------------------------------------------------
 // Lengths of the sequences and where each begins on the line; ends with the CTA
 // synchronised.
-template <int D, bool kFP8, int kCS>
+template <int D, bool kFP8>
 __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs& c,
                                             CrossSmem<D, kFP8>& sm) {
   using SM = CrossSmem<D, kFP8>;
@@ -165,7 +135,7 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
     for (int s = 0; s < SM::kSt; ++s) {
       mbar_init(&sm.landed[s], 1);
       mbar_init(&sm.full[s], kFP8 ? kConverts : 1);
-      mbar_init(&sm.empty[s], kIssuers * kCS);
+      mbar_init(&sm.empty[s], kIssuers);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sm.q_full[x], 1);
@@ -199,12 +169,11 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
   const int cap = min(p.max_blocks_per_seq * kBlockSize, p.max_context);
   const int rpt = kRowsM / p.group;
   auto work = [&](int q, int len) -> long long {  // of its key tiles
-    const int tiles = (q + rpt - 1) / rpt, rest = tiles % (2 * kCS);
-    return (long long)p.num_kv_heads * tiles_of(len) *
-           ((long long)(tiles / (2 * kCS)) * cost2(kFP8) + (rest > kCS ? cost2(kFP8) : rest ? kCost1 : 0));
+    const int tiles = (q + rpt - 1) / rpt;
+    return (long long)p.num_kv_heads * tiles_of(len) * ((long long)(tiles >> 1) * kCost2 + (tiles & 1) * kCost1);
   };
   // (a launch has below 2^31 units: its query heads)
-  auto units = [&](int q) { return p.num_kv_heads * (((q + rpt - 1) / rpt + 2 * kCS - 1) / (2 * kCS)); };
+  auto units = [&](int q) { return p.num_kv_heads * (((q + rpt - 1) / rpt + 1) >> 1); };
   long long local = 0;
   int mine = 0;
   for (int i = 0; i < chunk; ++i) {
@@ -249,7 +218,7 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
     }
     total += sm.scan[w];
   }
-  const int unit = (int)max(min(total / (4 * (int)gridDim.x / kCS), (long long)kCostUnit), 1LL);
+  const int unit = (int)max(min(total / (2 * (int)gridDim.x), (long long)kCostUnit), 1LL);
   for (int i = 0; i < chunk; ++i) {
     const int sq = tid * chunk + i;
     if (sq < S) {
@@ -263,8 +232,7 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
     sm.cost_unit = unit;
   }
   tc::fence_before_sync();
-  if constexpr (kCS == 2) tc::cluster_sync();  // the other CTA's barriers are there, too
-  else __syncthreads();
+  __syncthreads();
   tc::fence_after_sync();
 }
 
@@ -275,12 +243,12 @@ struct Walk {
   int4 cut0, cut1;     // the unit that the part ends in
 };
 
-template <int D, bool kFP8, int kCS>
+template <int D, bool kFP8>
 __device__ __forceinline__ Walk walk_begin(const AttnParams& p, const CrossSmem<D, kFP8>& sm) {
   Walk k;
   k.T = sm.start[p.num_seqs];
-  k.parts = (int)max(min((long long)gridDim.x / kCS, k.T / kLeast), 1LL);
-  const int part = blockIdx.x / kCS;
+  k.parts = (int)max(min((long long)gridDim.x, k.T / kLeast), 1LL);
+  const int part = blockIdx.x;
   k.w = part < k.parts ? k.T * part / k.parts : 0;
   k.w1 = part < k.parts ? k.T * (part + 1) / k.parts : 0;
   k.cut0 = k.cut1 = make_int4(-1, 0, 0, 0);
@@ -296,22 +264,20 @@ __device__ __forceinline__ Walk walk_begin(const AttnParams& p, const CrossSmem<
 }
 
 // The next item of the part (none: live is 0).
-template <int D, bool kFP8, int kCS>
-__device__ __forceinline__ CrossItem walk_on(const AttnParams& p, const CrossSmem<D, kFP8>& sm, Walk& v,
-                                             int rank) {
+template <int D, bool kFP8>
+__device__ __forceinline__ CrossItem walk_on(const AttnParams& p, const CrossSmem<D, kFP8>& sm, Walk& v) {
   const int rpt = kRowsM / p.group, hkv = p.num_kv_heads, once = sm.cost_unit;
   CrossItem x = {};
   while (v.w < v.w1) {
     const int q = sm.qlen[v.s], len = sm.len[v.s], nk = tiles_of(len);
-    const int tiles = (q + rpt - 1) / rpt, rest = tiles % (2 * kCS);
-    const int cost_rest = rest > kCS ? cost2(kFP8) : kCost1;
-    const long long u2 = (long long)nk * cost2(kFP8) + once, u1 = (long long)nk * cost_rest + once;
-    const long long wholes = (long long)hkv * (tiles / (2 * kCS)), off = v.w - sm.start[v.s];
-    const bool whole = off < wholes * u2;
-    const long long k = whole ? off / u2 : wholes + (off - wholes * u2) / u1;
-    const long long u0 = sm.start[v.s] + (whole ? k * u2 : wholes * u2 + (k - wholes) * u1);
-    const long long u = whole ? u2 : u1;
-    const int cost = whole ? cost2(kFP8) : cost_rest;
+    const int tiles = (q + rpt - 1) / rpt;
+    const long long u2 = (long long)nk * kCost2 + once, u1 = (long long)nk * kCost1 + once;
+    const long long twos = (long long)hkv * (tiles >> 1), off = v.w - sm.start[v.s];
+    const bool two = off < twos * u2;
+    const long long k = two ? off / u2 : twos + (off - twos * u2) / u1;
+    const long long u0 = sm.start[v.s] + (two ? k * u2 : twos * u2 + (k - twos) * u1);
+    const long long u = two ? u2 : u1;
+    const int cost = two ? kCost2 : kCost1;
     // tiles whose place on the line is in [w, w1)
     auto tile_at = [&](long long at) {
       const long long d = at - u0 - once;
@@ -328,16 +294,15 @@ __device__ __forceinline__ CrossItem walk_on(const AttnParams& p, const CrossSme
     x.kvh = (int)(k % hkv);
     x.len = len;
     x.q0 = sm.q0[seq];
-    const int n0 = whole ? 2 * kCS : rest, mine = tiles_of_rank(n0, rank, kCS);
-    x.t0[0] = ((int)(k / hkv) * (2 * kCS) + (rank ? tiles_of_rank(n0, 0, kCS) : 0)) * rpt;
+    x.t0[0] = 2 * (int)(k / hkv) * rpt;
     x.t0[1] = x.t0[0] + rpt;
-    x.nt[0] = mine > 0 ? min(rpt, q - x.t0[0]) : 0;
-    x.nt[1] = mine > 1 ? min(rpt, q - x.t0[1]) : 0;
+    x.nt[0] = min(rpt, q - x.t0[0]);
+    x.nt[1] = two ? min(rpt, q - x.t0[1]) : 0;
     x.kt0 = a;
     x.kt1 = b;
     x.part = a == 0 && b == nk ? -1 : 2 * (int)blockIdx.x + (a == 0 ? 1 : 0);
     x.tail = !kFP8 && b == nk && (len & (kBlockSize - 1)) != 0 ? ((len - 1) % kTileKeys) / kBlockSize : -1;
-    if (a == 0 && b < nk && mine > 0) {
+    if (a == 0 && b < nk) {
       // the unit goes on in the parts up to the one with its last tile
       const long long last = u0 + once + (long long)(nk - 1) * cost;
       v.cut0 = make_int4((int)(((last + 1) * v.parts + v.T - 1) / v.T - 1), x.q0 + x.t0[0], x.nt[0], x.nt[1]);
@@ -350,7 +315,7 @@ __device__ __forceinline__ CrossItem walk_on(const AttnParams& p, const CrossSme
 
 // ---- loads ---------------------------------------------------------------------------------
 // Order of a unit's tiles in the ring, as the issuer takes them: K0, K1, V0, K2, V1, ...
-template <int D, bool kFP8, int kCS>
+template <int D, bool kFP8>
 __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossArgs& c,
                                                CrossSmem<D, kFP8>& sm, const CUtensorMap& tm_k,
                                                const CUtensorMap& tm_v, const CUtensorMap& tm_q,
@@ -364,10 +329,7 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
   volatile int* abort = &sm.abort;
   const unsigned long long lim = wait_limit(p);
   const int lane = threadIdx.x & 31, g = p.group;
-  // the boxes of a tile's blocks are dealt out to the producer warps of all CTAs
-  const int rank = kCS == 2 ? (int)tc::cluster_rank() : 0;
-  const bool my_lane = (lane & (2 * kCS - 1)) == 2 * rank + pw;
-  constexpr uint16_t kAll = (1u << kCS) - 1;
+  const bool my_lane = (lane & 1) == pw;            // blocks pw, pw + 2, ... of a tile
   uint8_t* const ring = &sm.ring[0][0];
   uint32_t pos = 0, nq = 0, ntail = 0;
   bool ok = true;
@@ -390,11 +352,7 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
     const bool skip = blockIdx.x == 0 && p.skip_copy > 0 && pos + 1 == (uint32_t)p.skip_copy;
     bool good = true;
     if (lane == 0) {
-      if (pos >= (uint32_t)kSt) {
-        const uint32_t parity = ((pos / kSt) - 1) & 1;
-        if constexpr (kCS == 2) good = wait_cluster(&sm.empty[st], parity, abort, lim);
-        else good = wait_for(&sm.empty[st], parity, abort, lim);
-      }
+      if (pos >= (uint32_t)kSt) good = wait_for(&sm.empty[st], ((pos / kSt) - 1) & 1, abort, lim);
       if (good && !skip && pw == 0) mbar_arrive_expect_tx(&bars[st], kLoad);
     }
     if (!__shfl_sync(kFull, (int)good, 0)) return false;
@@ -402,13 +360,8 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
       uint8_t* dst = ring + (size_t)st * SM::kStage + (kFP8 ? SM::kCodes : 0) +
                      (lane & 7) * (kBlockSize * kBoxRow);
       const CUtensorMap* map = is_v ? &tm_v : &tm_k;
-      if constexpr (kCS == 2) {
-        tc::tma_load_2d_all(dst, map, 0, row, &bars[st], kAll);
-        if (kRow > 128) tc::tma_load_2d_all(dst + kHalf, map, 64, row, &bars[st], kAll);
-      } else {
-        tc::tma_load_2d(dst, map, 0, row, &bars[st]);
-        if (kRow > 128) tc::tma_load_2d(dst + kHalf, map, 64, row, &bars[st]);
-      }
+      tc::tma_load_2d(dst, map, 0, row, &bars[st]);
+      if (kRow > 128) tc::tma_load_2d(dst + kHalf, map, 64, row, &bars[st]);
     }
     __syncwarp();
     ++pos;
@@ -442,10 +395,10 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
     return true;
   };
   Walk walk = {};
-  if (pw == 0) walk = walk_begin<D, kFP8, kCS>(p, sm);
+  if (pw == 0) walk = walk_begin<D, kFP8>(p, sm);
   for (uint32_t n = 0; ok; ++n) {
     if (pw == 0) {  // makes the items, for the others too
-      x = walk_on<D, kFP8, kCS>(p, sm, walk, rank);
+      x = walk_on<D, kFP8>(p, sm, walk);
       bool good = true;
       if (lane == 0) {
         const int slot = n % kItems;
@@ -605,17 +558,15 @@ __device__ __forceinline__ void issue_half(uint32_t d, uint32_t a, uint64_t dv, 
 
 // ---- MMA issuers -----------------------------------------------------------------------------
 // One thread for each softmax warpgroup: with two query tiles P_y(t) V(t), S_y(t+1) for every
-// key tile t; with one, of every other key tile, t = y first; with none (the other CTA's) the
-// first one gives the stages back as they fill.  (One for both left the tensor pipe idle
-// while it waited and committed: without any softmax a key tile took 3100 cycles of which
-// 2050 are MMAs.)
+// key tile t; with one, of every other key tile, t = y first.  (One for both left the tensor
+// pipe idle while it waited and committed: without any softmax a key tile took 3100 cycles of
+// which 2050 are MMAs.)
 //
-// A stage is empty when both issuers of every CTA have released it; whoever uses it alone
-// does so twice.  Places of a unit's tiles in the ring: K0, K1, V0, K2, V1, ..., V(n-1).
+// A stage is empty when both issuers have released it; whoever uses it alone does so twice.  Places of a unit's tiles in the ring: K0, K1, V0, K2, V1, ..., V(n-1).
 __device__ __forceinline__ uint32_t k_place(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ uint32_t v_place(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
 
-template <class QT, int D, bool kFP8, int kCS>
+template <class QT, int D, bool kFP8>
 __device__ __forceinline__ bool issue_group(const AttnParams& p, CrossSmem<D, kFP8>& sm, uint32_t tmem, int y) {
   using SM = CrossSmem<D, kFP8>;
   constexpr int kSt = SM::kSt;
@@ -649,97 +600,85 @@ __device__ __forceinline__ bool issue_group(const AttnParams& p, CrossSmem<D, kF
       st = at % kSt;
       return wait(&sm.full[st], (at / kSt) & 1);
     };
-    auto release = [&](int st) {  // a stage, to the producers of all CTAs
-      for (int i = two ? 1 : 0; i < 2; ++i) {
-        if constexpr (kCS == 2) tc::mma_commit_all(&sm.empty[st], 3);
-        else tc::mma_commit(&sm.empty[st]);
-      }
+    auto release = [&](int st) {
+      tc::mma_commit(&sm.empty[st]);
+      if (!two) tc::mma_commit(&sm.empty[st]);
     };
-    if (kCS == 2 && x.nt[0] == 0) {
-      for (int i = 0; y == 0 && i < 2 * tiles; ++i) {
-        int st;
-        if (!full(i, st)) return false;
-        const uint32_t bar = smem_u32(&sm.empty[st]);
-        for (int j = 0; j < 2 * kCS; ++j)  // (converters wrote there)
-          tc::mbar_arrive_cluster_release(tc::map_rank(bar, j & 1));
-      }
-    } else {
-      const int step = two ? 1 : 2, first = two ? 0 : y;
-      const int qb = (nq + (two ? y : 0)) & 1;
-      if (!wait(&sm.q_full[qb], ((nq + (two ? y : 0)) >> 1) & 1)) return false;
-      int kst, vst;
-      auto scores = [&](int i) -> bool {
-        if (!full(k_place(i), kst)) return false;
-        tc::fence_after_sync();
-        issue_mods_scores<D>(s_col, dq0 + qb * (SM::kTile >> 4), dk0 + kst * kStage, kIdescS);
-        tc::mma_commit(&sm.s_ready[y]);
-        return true;
-      };
-      if (first < tiles) {
-        if (!scores(first)) return false;
-        release(kst);
-      }
-      if (first + step >= tiles) {
-        tc::mma_commit(&sm.q_empty[nq & 1]);
-        if (two) tc::mma_commit(&sm.q_empty[(nq + 1) & 1]);
-      }
-      for (int i = first; i < tiles; i += step) {
-        if (!wait(&sm.p_half[y], np & 1)) return false;
-        if (i == first && nit >= 1 && !wait(&sm.o_free[y], (nit - 1) & 1))
-          return false;  // the previous item's O has been read out
-        if (!full(v_place(i, tiles), vst)) return false;
-        const int ts = i == tiles - 1 ? x.tail : -1;
-        const uint64_t dv = dv0 + vst * kStage, dt = dt0 + (ntail & 1) * (SM::kTail >> 4);
-        if (ts >= 0 && !wait(&sm.tail_full[ntail & 1], (ntail >> 1) & 1)) return false;
-        // the products take turns, in the order of the tiles: the two softmax warpgroups then
-        // stay half a period apart, one at work while the other's MMAs run
-        if (i > 0 || y == 1 || last_other) {
-          if (!wait(&sm.turn[y], turns & 1)) return false;
-          ++turns;
-        }
-        tc::fence_after_sync();
-        // 64 states' weights while the softmax is at the others'
-        issue_half<0>(o_col, s_col, dv, dt, ts, i != first, kIdescO);
-        tc::mma_commit(&sm.o_half[y]);
-        if (!wait(&sm.p_ready[y], np & 1)) return false;
-        ++np;
-        tc::fence_after_sync();
-        issue_half<kTileKeys / 32>(o_col, s_col, dv, dt, ts, 1, kIdescO);
-        const bool hand = two || i + 1 < tiles || y == 1;  // (a unit begins with the first)
-        if (i + step < tiles) {
-          if (!scores(i + step)) return false;
-          if (hand) mbar_arrive(&sm.turn[y ^ 1]);
-          release(vst);
-          release(kst);
-          if (i + 2 * step >= tiles) {  // the item's last scores
-            tc::mma_commit(&sm.q_empty[nq & 1]);
-            if (two) tc::mma_commit(&sm.q_empty[(nq + 1) & 1]);
-          }
-        } else {
-          if (hand) mbar_arrive(&sm.turn[y ^ 1]);
-          tc::mma_commit(&sm.o_done[y]);
-          release(vst);
-        }
-      }
-      if (first < tiles) ++nit;
-      last_other = (two || (tiles & 1) == 0 ? 1 : 0) != y;
+    const int step = two ? 1 : 2, first = two ? 0 : y;
+    const int qb = (nq + (two ? y : 0)) & 1;
+    if (!wait(&sm.q_full[qb], ((nq + (two ? y : 0)) >> 1) & 1)) return false;
+    int kst, vst;
+    auto scores = [&](int i) -> bool {
+      if (!full(k_place(i), kst)) return false;
+      tc::fence_after_sync();
+      issue_mods_scores<D>(s_col, dq0 + qb * (SM::kTile >> 4), dk0 + kst * kStage, kIdescS);
+      tc::mma_commit(&sm.s_ready[y]);
+      return true;
+    };
+    if (first < tiles) {
+      if (!scores(first)) return false;
+      release(kst);
     }
+    if (first + step >= tiles) {
+      tc::mma_commit(&sm.q_empty[nq & 1]);
+      if (two) tc::mma_commit(&sm.q_empty[(nq + 1) & 1]);
+    }
+    for (int i = first; i < tiles; i += step) {
+      if (!wait(&sm.p_half[y], np & 1)) return false;
+      if (i == first && nit >= 1 && !wait(&sm.o_free[y], (nit - 1) & 1))
+        return false;  // the previous item's O has been read out
+      if (!full(v_place(i, tiles), vst)) return false;
+      const int ts = i == tiles - 1 ? x.tail : -1;
+      const uint64_t dv = dv0 + vst * kStage, dt = dt0 + (ntail & 1) * (SM::kTail >> 4);
+      if (ts >= 0 && !wait(&sm.tail_full[ntail & 1], (ntail >> 1) & 1)) return false;
+      // the products take turns, in the order of the tiles: the two softmax warpgroups then
+      // stay half a period apart, one at work while the other's MMAs run
+      if (i > 0 || y == 1 || last_other) {
+        if (!wait(&sm.turn[y], turns & 1)) return false;
+        ++turns;
+      }
+      tc::fence_after_sync();
+      // 64 states' weights while the softmax is at the others'
+      issue_half<0>(o_col, s_col, dv, dt, ts, i != first, kIdescO);
+      tc::mma_commit(&sm.o_half[y]);
+      if (!wait(&sm.p_ready[y], np & 1)) return false;
+      ++np;
+      tc::fence_after_sync();
+      issue_half<kTileKeys / 32>(o_col, s_col, dv, dt, ts, 1, kIdescO);
+      const bool hand = two || i + 1 < tiles || y == 1;  // (a unit begins with the first)
+      if (i + step < tiles) {
+        if (!scores(i + step)) return false;
+        if (hand) mbar_arrive(&sm.turn[y ^ 1]);
+        release(vst);
+        release(kst);
+        if (i + 2 * step >= tiles) {  // the item's last scores
+          tc::mma_commit(&sm.q_empty[nq & 1]);
+          if (two) tc::mma_commit(&sm.q_empty[(nq + 1) & 1]);
+        }
+      } else {
+        if (hand) mbar_arrive(&sm.turn[y ^ 1]);
+        tc::mma_commit(&sm.o_done[y]);
+        release(vst);
+      }
+    }
+    if (first < tiles) ++nit;
+    last_other = (two || (tiles & 1) == 0 ? 1 : 0) != y;
     if (x.tail >= 0) {
       // (waited for also where the other one used it: the buffer's phases keep their order)
       if (!wait(&sm.tail_full[ntail & 1], (ntail >> 1) & 1)) return false;
       tc::mma_commit(&sm.tail_free[ntail & 1]);
       ++ntail;
     }
-    nq += (x.nt[0] > 0) + two;
+    nq += two ? 2 : 1;
     base += 2 * tiles;
   }
 }
 
-template <class QT, int D, bool kFP8, int kCS>
+template <class QT, int D, bool kFP8>
 __device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, kFP8>& sm, uint32_t tmem, int y) {
   y = __shfl_sync(kFull, y, 0);  // (the same in every lane for the compiler, too)
   if (tc::elect_one()) {
-    if (!issue_group<QT, D, kFP8, kCS>(p, sm, tmem, y)) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
+    if (!issue_group<QT, D, kFP8>(p, sm, tmem, y)) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
     tc::mma_commit(&sm.mma_done);
     mbar_wait(&sm.mma_done, 0, 100000000ull);
   }
@@ -789,7 +728,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
     };
     const bool two = x.nt[1] > 0;
     const int qt = two ? y : 0, kt0 = x.kt0, kt1 = x.kt1;
-    const int rows = x.nt[qt] * g;                    // rows past the tokens are not stored
+    const int rows = x.nt[qt] * g;                    // rows past the tokens are never stored
     const bool idle = 32 * (warp & 3) >= rows;        // the warp has no others
     // the row's place in the output, in heads
     auto head_of = [&]() { return (x.q0 + x.t0[qt] + r / g) * p.num_heads + x.kvh * g + r % g; };
@@ -803,7 +742,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
       continue;
     }
     const int step = two ? 1 : 2, first = two ? kt0 : kt0 + y;
-    if (first >= kt1 || rows == 0) {  // one key tile, the other warpgroup's; no query tile
+    if (first >= kt1) {  // one key tile: the other warpgroup's
       done();
       continue;
     }
@@ -1028,7 +967,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
   if (!ok && lane == 0) flag_error(p.errors, PKV_DEVERR_TIMEOUT);
 }
 
-template <class QT, int D, bool kFP8, int kCS>
+template <class QT, int D, bool kFP8>
 __global__ void __launch_bounds__(cross_threads(kFP8), 1)
     cross_kernel(const AttnParams p, const CrossArgs c, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
@@ -1042,28 +981,20 @@ __global__ void __launch_bounds__(cross_threads(kFP8), 1)
     tc::prefetch_tmap(&tm_v);
     tc::prefetch_tmap(&tm_q);
   }
-  cross_setup<D, kFP8, kCS>(p, c, sm);
+  cross_setup<D, kFP8>(p, c, sm);
   const uint32_t tmem = sm.tmem_base;
   if (warp >= kSoft) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(cross_other_regs(kFP8)));
-    if (warp < kIssuer + kIssuers) cross_issuer<QT, D, kFP8, kCS>(p, sm, tmem, warp - kIssuer);
+    if (warp < kIssuer + kIssuers) cross_issuer<QT, D, kFP8>(p, sm, tmem, warp - kIssuer);
     else if (warp < kTma + kTmaWarps)
-      cross_producer<D, kFP8, kCS>(p, c, sm, tm_k, tm_v, tm_q, kv_rows, warp - kTma);
+      cross_producer<D, kFP8>(p, c, sm, tm_k, tm_v, tm_q, kv_rows, warp - kTma);
     else if constexpr (kFP8) cross_converter<QT, D>(p, sm, warp - kConvert);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(cross_soft_regs(kFP8)));
     cross_softmax<QT, D, kFP8>(p, c, sm, tmem);
   }
   tc::fence_before_sync();
-  if constexpr (kCS == 2) {
-    // the other CTA may still load for this one, or arrive on its barriers; where one has
-    // given up, its last copies to the other land meanwhile
-    if (*static_cast<volatile int*>(&sm.abort)) settle(5000000ull);
-    __syncwarp();
-    tc::cluster_sync();
-  } else {
-    __syncthreads();
-  }
+  __syncthreads();
   if (warp == kIssuer) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
@@ -1072,7 +1003,7 @@ __global__ void __launch_bounds__(cross_threads(kFP8), 1)
 
 // Joins the parts of the unit that CTA blockIdx.x's part of the line ends in, if it ends
 // inside one: weights 2^(lse - max) of the parts, which that CTA wrote as its second partial
-// and those of its rank in the clusters up to the last one as their first.  A warp per row.
+// and the CTAs up to the last one as their first.  A warp per row.
 constexpr int kJoinThreads = 256;
 template <class QT, int D>
 __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const AttnParams p, const CrossArgs c) {
@@ -1087,8 +1018,8 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const AttnPara
   for (int at = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); at < c.part_rows; at += warps) {
     const int qt = at >> 7, r = at & 127;
     if (r >= (qt ? cut.w : cut.z) * g) continue;
-    auto slot = [&](int i) { return (size_t)(2 * (b + i * c.cluster) + (i == 0 ? 1 : 0)) * c.part_rows + at; };
-    const int parts = last - b / c.cluster + 1;
+    auto slot = [&](int i) { return (size_t)(2 * (b + i) + (i == 0 ? 1 : 0)) * c.part_rows + at; };
+    const int parts = last - b + 1;
     float m = -INFINITY;
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(p.lse + slot(i)));
 #pragma unroll
@@ -1117,7 +1048,7 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const AttnPara
   }
 }
 
-template <class QT, int D, bool kFP8, int kCS>
+template <class QT, int D, bool kFP8>
 int launch_cross_typed(const AttnParams& p, const CrossArgs& c, int ctas, cudaStream_t stream) {
   const bool bf16 = std::is_same<QT, BF16>::value;
   const uint64_t kv_rows = (uint64_t)p.num_blocks * p.num_kv_heads * kBlockSize;
@@ -1134,7 +1065,7 @@ int launch_cross_typed(const AttnParams& p, const CrossArgs& c, int ctas, cudaSt
   static_assert(offsetof(SM, ring) % 1024 == 0 && offsetof(SM, q) % 1024 == 0 &&
                     offsetof(SM, tail) % 1024 == 0 && SM::kStage % 1024 == 0 && SM::kTail % 1024 == 0,
                 "swizzled buffers must start on 1024-byte boundaries");
-  auto kern = cross_kernel<QT, D, kFP8, kCS>;
+  auto kern = cross_kernel<QT, D, kFP8>;
   // the kernel's register shares add up to what its launch holds; with fewer its
   // warpgroups would wait for registers without end
   cudaFuncAttributes fa;
@@ -1142,39 +1073,31 @@ int launch_cross_typed(const AttnParams& p, const CrossArgs& c, int ctas, cudaSt
   if (fa.numRegs != cross_launch_regs(kFP8)) return PKV_ERR_CUDA;
   static std::atomic<unsigned long long> configured{0};
   if (!smem_once(kern, smem, configured)) return PKV_ERR_CUDA;
-  ctas = ctas / kCS * kCS;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(cross_threads(kFP8));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = kCS;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = kCS > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, kern, p, c, tk, tv, tq, (int)kv_rows) != cudaSuccess) return PKV_ERR_CUDA;
+  kern<<<ctas, cross_threads(kFP8), smem, stream>>>(p, c, tk, tv, tq, (int)kv_rows);
+  if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   if (!c.cuts) return PKV_OK;
   // a CTA of the join for each of the kernel's and up to 32 rows
+  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, (c.part_rows + 31) / 32);
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, cross_join_kernel<QT, D>, p, c) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-template <int D, int kCS>
+template <int D>
 int launch_cross_dim(const AttnParams& p, const CrossArgs& c, int q_dtype, int kv_dtype, int ctas,
                      cudaStream_t stream) {
   const bool fp8 = kv_dtype == PKV_FP8_E4M3;
   if (q_dtype == PKV_BF16)
-    return fp8 ? launch_cross_typed<BF16, D, true, kCS>(p, c, ctas, stream)
-               : launch_cross_typed<BF16, D, false, kCS>(p, c, ctas, stream);
-  return fp8 ? launch_cross_typed<F16, D, true, kCS>(p, c, ctas, stream)
-             : launch_cross_typed<F16, D, false, kCS>(p, c, ctas, stream);
+    return fp8 ? launch_cross_typed<BF16, D, true>(p, c, ctas, stream)
+               : launch_cross_typed<BF16, D, false>(p, c, ctas, stream);
+  return fp8 ? launch_cross_typed<F16, D, true>(p, c, ctas, stream)
+             : launch_cross_typed<F16, D, false>(p, c, ctas, stream);
 }
 
 }  // namespace

@@ -198,17 +198,12 @@ struct CrossArgs {
   int max_q;       // bound of the sequences' queries
   int part_rows;   // rows of a partial
   int box_tokens;  // tokens of a query box
-  int cluster;     // CTAs that share a part of the work: 1 or 2
   int4* cuts;      // [2 * ctas]: last part, first token, tokens of both query tiles; KV head
 };
-int launch_cross_one_d64(const AttnParams& p, const CrossArgs& c, int q_dtype, int kv_dtype, int ctas,
-                         cudaStream_t stream);
-int launch_cross_one_d128(const AttnParams& p, const CrossArgs& c, int q_dtype, int kv_dtype, int ctas,
-                          cudaStream_t stream);
-int launch_cross_pair_d64(const AttnParams& p, const CrossArgs& c, int q_dtype, int kv_dtype, int ctas,
-                          cudaStream_t stream);
-int launch_cross_pair_d128(const AttnParams& p, const CrossArgs& c, int q_dtype, int kv_dtype, int ctas,
-                           cudaStream_t stream);
+int launch_cross_d64(const AttnParams& p, const CrossArgs& c, int q_dtype, int kv_dtype, int ctas,
+                     cudaStream_t stream);
+int launch_cross_d128(const AttnParams& p, const CrossArgs& c, int q_dtype, int kv_dtype, int ctas,
+                      cudaStream_t stream);
 
 // One launch for a mixed batch: pd describes the decode rows (as for
 // launch_paged_decode_tc), pp the prefill chunks (as for launch_prefill_tc);

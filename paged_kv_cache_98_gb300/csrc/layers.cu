@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads)
 // units, few rows each) and a CTA's where they are long (few units, 128 rows of 256 bytes
 // a turn).  Bound by HBM, two row bytes a moved token; by launch and four dependent reads
 // (list, table, row) for short ones.
-constexpr int kDeep = 8;        // rows a thread reads in a turn
+constexpr int kDeep = 4;        // rows a thread reads in a turn
 constexpr int kLongList = 96;   // from this many kept tokens a sequence on (on average), a CTA a unit
 
 constexpr long long kManyUnits = 608;  // below as many, CTAs' units are quarters or halves of rows
@@ -71,7 +71,7 @@ struct CompactArgs {
 };
 
 template <int kWarps, int kRowBytes, int kPartBytes>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     compact_kernel(const __grid_constant__ Caches caches, const CompactArgs a) {
   constexpr int kUnit = 32 * kWarps;             // threads of a unit
   constexpr int kParts = kRowBytes / kPartBytes; // units that share the rows
@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kThreads)
   // the list ascends within [base, ctx); its tokens before `moved` are in place
   bool bad = !fits;
   int moved = n;
+#pragma unroll 8
   for (int j = t; j < n; j += kUnit) {
     const int v = __ldg(keep + j), before = j ? __ldg(keep + j - 1) : base - 1;
     bad |= v <= before || v >= ctx;
@@ -135,33 +136,46 @@ __global__ void __launch_bounds__(kThreads)
                         (size_t)head * (kBlockSize * kRowBytes) + part * kPartBytes +
                         (t % kChunks) * 16;
   const size_t block_bytes = (size_t)a.kv_heads * (kBlockSize * kRowBytes);
-  auto at = [&](int place) -> uint8_t* {  // NULL: in a block outside the pool
+  // block and row of the j-th kept token (to: of its new place) as 16 block + row; -1 past the
+  // list or in a block outside the pool
+  auto slot = [&](int j, bool to) -> int {
+    if (j >= n) return -1;
+    const int place = to ? base + j : __ldg(keep + j);
     const int blk = __ldg(table + place / kBlockSize);
     if (blk < 0 || blk >= a.num_blocks) {
       if (tell) flag_error(a.errors, PKV_DEVERR_BLOCK_ID);
-      return nullptr;
+      return -1;
     }
-    return rows + blk * block_bytes + (place % kBlockSize) * kRowBytes;
+    return blk * kBlockSize + place % kBlockSize;
   };
-  for (int j0 = moved + t / kChunks; j0 - t / kChunks < n; j0 += kRows * kDeep) {
-    uint4 w[kDeep];
-    uint8_t* to[kDeep];
+  auto at = [&](int s) {
+    return reinterpret_cast<uint4*>(rows + (size_t)(s / kBlockSize) * block_bytes + (s % kBlockSize) * kRowBytes);
+  };
+  // the next turn's places are looked up while a turn's rows are on their way
+  int from[kDeep], to[kDeep];
+  auto look_up = [&](int j0) {
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
-      const int j = j0 + u * kRows;
-      to[u] = nullptr;
-      if (j < n) {
-        const uint8_t* from = at(__ldg(keep + j));
-        to[u] = at(base + j);
-        if (from) w[u] = *reinterpret_cast<const uint4*>(from);
-        else to[u] = nullptr;
-      }
+      from[u] = slot(j0 + u * kRows, false);
+      to[u] = slot(j0 + u * kRows, true);
     }
+  };
+  int j0 = moved + t / kChunks;
+  look_up(j0);
+  for (; j0 - t / kChunks < n; j0 += kRows * kDeep) {
+    uint4 w[kDeep];
+    int dst[kDeep];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      dst[u] = from[u] < 0 ? -1 : to[u];
+      if (dst[u] >= 0) w[u] = *at(from[u]);
+    }
+    look_up(j0 + kRows * kDeep);
     if constexpr (kWarps == 1) __syncwarp();
     else __syncthreads();
 #pragma unroll
     for (int u = 0; u < kDeep; ++u)
-      if (to[u]) *reinterpret_cast<uint4*>(to[u]) = w[u];
+      if (dst[u] >= 0) *at(dst[u]) = w[u];
   }
 }
 
@@ -280,7 +294,9 @@ int pkv_compact_tokens(void* const* k_caches, void* const* v_caches, int num_lay
   if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
   if (cache_dtype != PKV_F16 && cache_dtype != PKV_BF16 && cache_dtype != PKV_FP8_E4M3)
     return PKV_ERR_UNSUPPORTED;
-  if ((long long)max_blocks_per_seq * kBlockSize > (1LL << 30)) return PKV_ERR_UNSUPPORTED;
+  if ((long long)max_blocks_per_seq * kBlockSize > (1LL << 30) ||
+      (long long)num_blocks * kBlockSize > 0x7fffffffLL)
+    return PKV_ERR_UNSUPPORTED;
   const int row_bytes = head_dim * (cache_dtype == PKV_FP8_E4M3 ? 1 : 2);
   const unsigned long long bytes = (unsigned long long)num_blocks * num_kv_heads * kBlockSize * row_bytes;
   const int rc = check_caches(k_caches, v_caches, num_layers, bytes);

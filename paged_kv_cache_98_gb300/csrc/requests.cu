@@ -20,7 +20,8 @@ namespace {
 // (integers: the order of the atomics does not matter).  Bound by the reads and writes of
 // the tables for long ones, by launch and two dependent reads for short ones.
 constexpr int kForkThreads = 256;
-constexpr int kForkChunk = 1024;   // entries of a row a CTA handles: four a thread
+constexpr int kForkChunk = 1024;   // entries of a row a CTA of several rows handles: four a thread
+constexpr int kForkDeep = 16;      // entries of its one row that a thread holds at most
 constexpr int kForkTile = 2048;    // parents looked through at a time
 constexpr int kForkRows = 64;
 constexpr int kForkCtas = 1216;    // rows share CTAs beyond this many (eight a processor)
@@ -101,8 +102,63 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a) {
   }
 }
 
+// The same for one old row a CTA, whose entries its threads hold: they are read while the
+// parents are looked through, once.  512 rows of up to 8192 entries: 4096 entries a CTA 10.9
+// us, 1024 of them, read again for the counts, 16.8.
+template <int kDeep>
+__global__ void __launch_bounds__(kForkThreads) fork_row_kernel(const ForkArgs a) {
+  __shared__ int s_child[kForkTile];
+  __shared__ int s_matches;
+  const int tid = threadIdx.x, row = blockIdx.x, e0 = blockIdx.y * (kForkThreads * kDeep) + tid;
+  const bool first = blockIdx.y == 0;
+  const int cap = a.width * kBlockSize;
+  int len = __ldg(a.lens + row);
+  if (len < 0 || len > cap) {
+    if (first && tid == 0) flag_error(a.errors, PKV_DEVERR_CONTEXT);
+    len = len < 0 ? 0 : cap;
+  }
+  const int n = (len + kBlockSize - 1) / kBlockSize;
+  if (!first && e0 - tid >= n) return;
+  const int32_t* src = a.tables + (size_t)row * a.width;
+  int v[kDeep];
+#pragma unroll
+  for (int u = 0; u < kDeep; ++u) v[u] = e0 + u * kForkThreads < n ? __ldg(src + e0 + u * kForkThreads) : 0;
+  int children = 0;
+  for (int t0 = 0; t0 < a.num_out; t0 += kForkTile) {
+    if (tid == 0) s_matches = 0;
+    __syncthreads();
+    const int t1 = min(t0 + kForkTile, a.num_out);
+    for (int i = t0 + tid; i < t1; i += kForkThreads) {
+      const int p = __ldg(a.parents + i);
+      if (p == row) {
+        s_child[atomicAdd(&s_matches, 1)] = i;
+        if (first) a.lens_out[i] = len;
+      } else if (first && row == 0 && (p < 0 || p >= a.num_in)) {
+        a.lens_out[i] = 0;
+        if (p >= 0) flag_error(a.errors, PKV_DEVERR_CONTEXT);
+      }
+    }
+    __syncthreads();
+    const int matches = s_matches;
+    for (int k = 0; k < matches; ++k) {
+      int32_t* dst = a.tables_out + (size_t)s_child[k] * a.width;
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u)
+        if (e0 + u * kForkThreads < n) dst[e0 + u * kForkThreads] = v[u];
+    }
+    children += matches;
+    __syncthreads();  // the list has been read
+  }
+#pragma unroll
+  for (int u = 0; u < kDeep; ++u) {
+    if (e0 + u * kForkThreads >= n) continue;
+    if (v[u] < 0 || v[u] >= a.num_blocks) flag_error(a.errors, PKV_DEVERR_BLOCK_ID);
+    else if (children != 1) atomicAdd(a.counts + v[u], children - 1);
+  }
+}
+
 // ---- resize ----------------------------------------------------------------------------
-// One cluster of up to eight CTAs, which can wait for each other in hardware and read each
+// One cluster of up to sixteen CTAs, which can wait for each other in hardware and read each
 // other's shared memory, so that the call is one launch:
 //   1  blocks behind the new lengths lose a reference
 //   2  what each sequence needs: a copy of a shared partial last block (how many of its
@@ -116,8 +172,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a) {
 // Every sum is one of integers and the hash table only counts and takes maxima, so the
 // result does not depend on the order of the atomics.  Bound by its dependent reads and
 // five cluster barriers for small batches, by reading the counts twice (up to the last
-// block handed out the second time) on eight processors for large pools.
-constexpr int kResizeCtas = 8;   // at most; one where that is enough (kOneCta...)
+// block handed out the second time) on sixteen processors for large pools.
+constexpr int kResizeCtas = 16;  // at most; one where that is enough (kOneCta...)
 constexpr int kResizeThreads = 1024;
 constexpr int kResizeWarps = kResizeThreads / 32;
 constexpr int kSat = 0x3fffffff;  // sums of needs end here; pools hold at most 2^30 - 1 blocks
@@ -478,13 +534,23 @@ int pkv_fork_requests(int32_t* tables_out, int32_t* lens_out, const int32_t* tab
   if (num_out == 0 && num_in == 0) return PKV_OK;
   ForkArgs a{tables_out, lens_out, tables, lens, ref_counts, parents, num_out, num_in,
              max_blocks_per_seq, num_blocks, 1, 32, device_errors};
+  cudaStream_t on = static_cast<cudaStream_t>(stream);
+  if (num_in > 0 && num_in <= kForkCtas) {
+    const bool longer = max_blocks_per_seq > kForkThreads * 4;
+    const int per = kForkThreads * (longer ? kForkDeep : 4);
+    const int chunks = (max_blocks_per_seq + per - 1) / per;
+    if (chunks > 65535) return PKV_ERR_UNSUPPORTED;
+    if (longer) fork_row_kernel<kForkDeep><<<dim3(num_in, chunks), kForkThreads, 0, on>>>(a);
+    else fork_row_kernel<4><<<dim3(num_in, chunks), kForkThreads, 0, on>>>(a);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  }
   a.rows = num_in > kForkCtas ? (num_in + kForkCtas - 1) / kForkCtas : 1;
   while (a.lanes < kForkThreads && 4 * a.lanes < max_blocks_per_seq) a.lanes *= 2;
   const int ctas = num_in > 0 ? (num_in + a.rows - 1) / a.rows : 1;
   const int chunks = (max_blocks_per_seq + kForkChunk - 1) / kForkChunk;
   static_assert((PKV_FORK_MAX_ROWS + kForkCtas - 1) / kForkCtas <= kForkRows, "rows of a CTA");
   if (chunks > 65535) return PKV_ERR_UNSUPPORTED;
-  fork_kernel<<<dim3(ctas, chunks), kForkThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  fork_kernel<<<dim3(ctas, chunks), kForkThreads, 0, on>>>(a);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -535,6 +601,10 @@ int pkv_resize_requests(int32_t* request_tables, int32_t* ref_counts, const int3
   static_assert(kMostSmem + sizeof(ResizeShared) <= 232448, "shared memory budget of one CTA");
   static std::atomic<unsigned long long> configured{0};
   if (!smem_once(resize_kernel, kMostSmem, configured)) return PKV_ERR_CUDA;
+  // (more than eight CTAs to a cluster have to be asked for)
+  if (ctas > 8 && cudaFuncSetAttribute(resize_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                      cudaSuccess)
+    return PKV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kResizeThreads);

@@ -293,25 +293,6 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
-// ---- CTAs of a cluster that load for each other --------------------------------------
-// TMA box into the shared memory of every CTA in `mask`, at this CTA's offset, its bytes
-// counted on each one's own barrier at `bar`'s offset.
-__device__ __forceinline__ void tma_load_2d_all(void* dst, const CUtensorMap* map, int c0, int c1,
-                                                uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster "
-      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "h"(mask)
-      : "memory");
-}
-// Arrives once on the barrier at `bar`'s offset of every CTA in `mask` when every MMA this
-// thread issued so far has completed.
-__device__ __forceinline__ void mma_commit_all(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(smem_u32(bar)), "h"(mask)
-      : "memory");
-}
 // Arrivals on a barrier of either CTA of the pair (release at CTA scope, as
 // for a local arrival: the data they publish is TMA- or tcgen05-written, ordered
 // by the async proxy or by the tcgen05 fences around the synchronisation).
