@@ -12,6 +12,8 @@ namespace cg = cooperative_groups;
 namespace pkv {
 namespace {
 
+__device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlockSize - 1) / kBlockSize; }
+
 // ---- fork ------------------------------------------------------------------------------
 // T'[i] = T[p_i], L'[i] = L[p_i], and count[b] += children(p) - 1 for every entry b of an
 // old row p: a move (one child) touches no count.  So the work goes by old rows: a CTA has
@@ -21,7 +23,7 @@ namespace {
 // the tables for long ones, by launch and two dependent reads for short ones.
 constexpr int kForkThreads = 256;
 constexpr int kForkChunk = 1024;   // entries of a row a CTA of several rows handles: four a thread
-constexpr int kForkDeep = 16;      // entries of its one row that a thread holds at most
+constexpr long long kForkLong = 1 << 20;  // entries of all tables
 constexpr int kForkTile = 2048;    // parents looked through at a time
 constexpr int kForkRows = 64;
 constexpr int kForkCtas = 1216;    // rows share CTAs beyond this many (eight a processor)
@@ -102,58 +104,86 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a) {
   }
 }
 
-// The same for one old row a CTA, whose entries its threads hold: they are read while the
-// parents are looked through, once.  512 rows of up to 8192 entries: 4096 entries a CTA 10.9
-// us, 1024 of them, read again for the counts, 16.8.
-template <int kDeep>
-__global__ void __launch_bounds__(kForkThreads) fork_row_kernel(const ForkArgs a) {
-  __shared__ int s_child[kForkTile];
-  __shared__ int s_matches;
-  const int tid = threadIdx.x, row = blockIdx.x, e0 = blockIdx.y * (kForkThreads * kDeep) + tid;
+// The same for kRows consecutive old rows a CTA, whose entries its threads hold: they are
+// read once, while the parents are looked through.  Neighbours often share the front of
+// their lists (samples of one prompt), and where they have the same block in the same
+// place its count changes once by what all of them together change it: 512 rows of up to
+// 8192 entries in groups of 8 take 9 us with eight rows a CTA, 14 with one.
+template <int kRows, int kDeep, int kTile>
+__global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(const ForkArgs a) {
+  __shared__ int s_child[kRows][kTile];
+  __shared__ int s_matches[kRows];
+  const int tid = threadIdx.x, r0 = blockIdx.x * kRows, e0 = blockIdx.y * (kForkThreads * kDeep) + tid;
   const bool first = blockIdx.y == 0;
   const int cap = a.width * kBlockSize;
-  int len = __ldg(a.lens + row);
-  if (len < 0 || len > cap) {
-    if (first && tid == 0) flag_error(a.errors, PKV_DEVERR_CONTEXT);
-    len = len < 0 ? 0 : cap;
-  }
-  const int n = (len + kBlockSize - 1) / kBlockSize;
-  if (!first && e0 - tid >= n) return;
-  const int32_t* src = a.tables + (size_t)row * a.width;
-  int v[kDeep];
+  int len[kRows], most = 0;
 #pragma unroll
-  for (int u = 0; u < kDeep; ++u) v[u] = e0 + u * kForkThreads < n ? __ldg(src + e0 + u * kForkThreads) : 0;
-  int children = 0;
-  for (int t0 = 0; t0 < a.num_out; t0 += kForkTile) {
-    if (tid == 0) s_matches = 0;
+  for (int r = 0; r < kRows; ++r) {
+    len[r] = r0 + r < a.num_in ? __ldg(a.lens + r0 + r) : 0;
+    if (len[r] < 0 || len[r] > cap) {
+      if (first && tid == 0) flag_error(a.errors, PKV_DEVERR_CONTEXT);
+      len[r] = len[r] < 0 ? 0 : cap;
+    }
+    most = max(most, len[r]);
+  }
+  if (!first && (e0 - tid) * kBlockSize >= most) return;
+  int v[kRows][kDeep], children[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    children[r] = 0;
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int e = e0 + u * kForkThreads;
+      v[r][u] = e < blocks_of(len[r]) ? __ldg(a.tables + (size_t)(r0 + r) * a.width + e) : 0;
+    }
+  }
+  for (int t0 = 0; t0 < a.num_out; t0 += kTile) {
+    if (tid < kRows) s_matches[tid] = 0;
     __syncthreads();
-    const int t1 = min(t0 + kForkTile, a.num_out);
+    const int t1 = min(t0 + kTile, a.num_out);
     for (int i = t0 + tid; i < t1; i += kForkThreads) {
       const int p = __ldg(a.parents + i);
-      if (p == row) {
-        s_child[atomicAdd(&s_matches, 1)] = i;
-        if (first) a.lens_out[i] = len;
-      } else if (first && row == 0 && (p < 0 || p >= a.num_in)) {
+      if (p >= r0 && p - r0 < kRows && p < a.num_in) {
+        s_child[p - r0][atomicAdd(&s_matches[p - r0], 1)] = i;
+        if (first) a.lens_out[i] = min(max(__ldg(a.lens + p), 0), cap);
+      } else if (first && r0 == 0 && (p < 0 || p >= a.num_in)) {
         a.lens_out[i] = 0;
         if (p >= 0) flag_error(a.errors, PKV_DEVERR_CONTEXT);
       }
     }
     __syncthreads();
-    const int matches = s_matches;
-    for (int k = 0; k < matches; ++k) {
-      int32_t* dst = a.tables_out + (size_t)s_child[k] * a.width;
 #pragma unroll
-      for (int u = 0; u < kDeep; ++u)
-        if (e0 + u * kForkThreads < n) dst[e0 + u * kForkThreads] = v[u];
+    for (int r = 0; r < kRows; ++r) {
+      const int matches = s_matches[r], n = blocks_of(len[r]);
+      for (int k = 0; k < matches; ++k) {
+        int32_t* dst = a.tables_out + (size_t)s_child[r][k] * a.width;
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u)
+          if (e0 + u * kForkThreads < n) dst[e0 + u * kForkThreads] = v[r][u];
+      }
+      children[r] += matches;
     }
-    children += matches;
-    __syncthreads();  // the list has been read
+    __syncthreads();  // the lists have been read
   }
 #pragma unroll
   for (int u = 0; u < kDeep; ++u) {
-    if (e0 + u * kForkThreads >= n) continue;
-    if (v[u] < 0 || v[u] >= a.num_blocks) flag_error(a.errors, PKV_DEVERR_BLOCK_ID);
-    else if (children != 1) atomicAdd(a.counts + v[u], children - 1);
+    int block = -1, change = 0;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (e0 + u * kForkThreads >= blocks_of(len[r])) continue;
+      const int b = v[r][u];
+      if (b < 0 || b >= a.num_blocks) {
+        flag_error(a.errors, PKV_DEVERR_BLOCK_ID);
+        continue;
+      }
+      if (b != block) {
+        if (change != 0) atomicAdd(a.counts + block, change);
+        block = b;
+        change = 0;
+      }
+      change += children[r] - 1;
+    }
+    if (change != 0) atomicAdd(a.counts + block, change);
   }
 }
 
@@ -194,8 +224,6 @@ constexpr int kPieces = 8192;  // at most
 constexpr int kOneCtaSeqs = 512, kOneCtaBlocks = 32768;
 
 __device__ __forceinline__ int sat_add(int x, int y) { return min(x + y, kSat); }
-
-__device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlockSize - 1) / kBlockSize; }
 
 // Number of the four counts from id on (below end) that are 0, as bits.
 __device__ __forceinline__ uint32_t free_bits(const int32_t* counts, int id, int end, bool vec) {
@@ -269,20 +297,29 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeA
       if (lane >= o) incl += y;
     }
     const unsigned total = __shfl_sync(kFull, incl, 31);
-    for (unsigned f = lane; f < ((total + 31u) & ~31u); f += 32) {
-      int lo = 0;  // first lane with incl > f
+    constexpr int kBatch = 4;  // entries in flight
+    for (unsigned f0 = lane; f0 - lane < total; f0 += 32 * kBatch) {
+      int32_t* at[kBatch];
+      int b[kBatch];
 #pragma unroll
-      for (int o = 16; o; o >>= 1)
-        if (__shfl_sync(kFull, incl, lo + o - 1) <= f) lo += o;
-      lo = min(lo, 31);
-      const int r = __shfl_sync(kFull, row[k], lo);
-      const int e = __shfl_sync(kFull, need[k], lo) +
-                    (int)(f - (__shfl_sync(kFull, incl, lo) - __shfl_sync(kFull, back, lo)));
-      if (f < total) {
-        int32_t* at = a.tables + (size_t)r * a.width + e;
-        const int b = *at;
-        *at = -1;
-        if (b >= 0 && b < a.num_blocks) atomicSub(a.counts + b, 1);
+      for (int u = 0; u < kBatch; ++u) {
+        const unsigned f = f0 + 32 * u;
+        int lo = 0;  // first lane with incl > f
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+          if (__shfl_sync(kFull, incl, lo + o - 1) <= f) lo += o;
+        lo = min(lo, 31);
+        const int r = __shfl_sync(kFull, row[k], lo);
+        const int e = __shfl_sync(kFull, need[k], lo) +
+                      (int)(f - (__shfl_sync(kFull, incl, lo) - __shfl_sync(kFull, back, lo)));
+        at[u] = f < total ? a.tables + (size_t)r * a.width + e : nullptr;
+        b[u] = at[u] ? *at[u] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (!at[u]) continue;
+        *at[u] = -1;
+        if (b[u] >= 0 && b[u] < a.num_blocks) atomicSub(a.counts + b[u], 1);
         else flag_error(a.errors, PKV_DEVERR_BLOCK_ID);
       }
     }
@@ -317,13 +354,22 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeA
   // free blocks of this warp's pieces of the pool, for every CTA
   const bool vec = (reinterpret_cast<uintptr_t>(a.counts) & 15u) == 0;
   const int warps = ctas * kResizeWarps, me = warp * ctas + cta;
-#pragma unroll 4
-  for (int k = me; k < a.pieces; k += warps) {
-    const int id0 = k * a.piece, id1 = min(id0 + a.piece, a.num_blocks);
-    unsigned n = 0;
-    for (int id = id0 + 4 * lane; id < id1; id += 128) n += __popc(free_bits(a.counts, id, id1, vec));
-    n = __reduce_add_sync(kFull, n);
-    if (lane < ctas) cluster.map_shared_rank(s_free, lane)[k] = (int)n;
+  constexpr int kScan = 8;  // pieces in flight
+  for (int k0 = me; k0 < a.pieces; k0 += kScan * warps) {
+    unsigned n[kScan];
+#pragma unroll
+    for (int u = 0; u < kScan; ++u) n[u] = 0;
+    for (int d = 4 * lane; d < a.piece; d += 128)
+#pragma unroll
+      for (int u = 0; u < kScan; ++u) {
+        const long long id = (long long)(k0 + u * warps) * a.piece + d;
+        if (id < a.num_blocks) n[u] += __popc(free_bits(a.counts, (int)id, a.num_blocks, vec));
+      }
+#pragma unroll
+    for (int u = 0; u < kScan; ++u) {
+      n[u] = __reduce_add_sync(kFull, n[u]);
+      if (lane < ctas && k0 + u * warps < a.pieces) cluster.map_shared_rank(s_free, lane)[k0 + u * warps] = (int)n[u];
+    }
   }
   cluster.sync();  // every holder has been counted
   // ---- 3: prefix sums ----------------------------------------------------------------------
@@ -536,12 +582,14 @@ int pkv_fork_requests(int32_t* tables_out, int32_t* lens_out, const int32_t* tab
              max_blocks_per_seq, num_blocks, 1, 32, device_errors};
   cudaStream_t on = static_cast<cudaStream_t>(stream);
   if (num_in > 0 && num_in <= kForkCtas) {
-    const bool longer = max_blocks_per_seq > kForkThreads * 4;
-    const int per = kForkThreads * (longer ? kForkDeep : 4);
+    // eight rows a CTA where that leaves the processors enough of them
+    const bool eight = (long long)num_in * max_blocks_per_seq >= kForkLong;
+    const int per = kForkThreads * (eight ? 2 : 4), rows = eight ? 8 : 1;
     const int chunks = (max_blocks_per_seq + per - 1) / per;
     if (chunks > 65535) return PKV_ERR_UNSUPPORTED;
-    if (longer) fork_row_kernel<kForkDeep><<<dim3(num_in, chunks), kForkThreads, 0, on>>>(a);
-    else fork_row_kernel<4><<<dim3(num_in, chunks), kForkThreads, 0, on>>>(a);
+    const dim3 grid((num_in + rows - 1) / rows, chunks);
+    if (eight) fork_rows_kernel<8, 2, 512><<<grid, kForkThreads, 0, on>>>(a);
+    else fork_rows_kernel<1, 4, kForkTile><<<grid, kForkThreads, 0, on>>>(a);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
   }
   a.rows = num_in > kForkCtas ? (num_in + kForkCtas - 1) / kForkCtas : 1;
