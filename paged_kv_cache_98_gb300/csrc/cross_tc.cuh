@@ -761,7 +761,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
         // moves for those that it does not do for, what they have so far is scaled to it, and
         // the weights are taken again.  (The maximum of every tile first costs 570 of a
         // step's 2000 cycles.)
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           float pk[32];
           float2 t2[4];
