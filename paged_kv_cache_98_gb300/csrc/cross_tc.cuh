@@ -499,10 +499,10 @@ __device__ __forceinline__ void cross_converter(const AttnParams& p, CrossSmem<D
       return *reinterpret_cast<const uint4*>(tile + SM::kCodes + r * D +
                                              ((D == 128 ? ch ^ (r & 7) : ch) << 4));
     };
-    // several turns' codes at a time: one after the other, a tile took 1000 ns, most of it
-    // latencies
+    // two turns' codes at a time (beams 124 us with one, 110 with two, 126 with four, whose code
+    // the instruction cache has no room for beside the softmax's)
     constexpr int kTurns = kTileKeys / kRows / kConverts;
-    constexpr int kDeep = kTurns < 4 ? kTurns : 4;
+    constexpr int kDeep = kTurns < 2 ? kTurns : 2;
 #pragma unroll 1
     for (int u0 = cw; u0 < kTileKeys / kRows; u0 += kConverts * kDeep) {
       uint4 w[kDeep];
@@ -710,7 +710,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t s_col = tmem + lane_off + y * 128;
   const uint32_t o_col = tmem + lane_off + kColO + y * 128;
-  const float qs = p.q_scale;
+  const float qs = p.q_scale == 0.0f ? 1e-30f : p.q_scale;  // (2^(s * 1e-30) rounds to 1)
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(kFull, wait_for(bar, parity, abort, lim)) != 0;
   };
@@ -756,6 +756,21 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
       if (!ok) break;
       if (!idle) {
         tc::fence_after_sync();
+        if (left < kTileKeys) {
+          // the last tile: scores past the states become those of weight zero, where they are
+          // (tests in the loop below would cost every tile 128 selections)
+          const float none = qs > 0.0f ? -INFINITY : INFINITY;
+#pragma unroll 1
+          for (int k = left & ~31; k < kTileKeys; k += 32) {
+            float sv[32];
+            tc::tmem_ld32(s_col + k, sv);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sv[e] = k + e < left ? sv[e] : none;
+            tc::tmem_st32(s_col + k, sv);
+          }
+          tc::tmem_wait_st();
+        }
         // 64 states at a time: weights 2^(s * scale - m) with m as it is.  Their sum tells
         // whether that m will do for all rows of the warp, as it nearly always does; else m
         // moves for those that it does not do for, what they have so far is scaled to it, and
@@ -766,21 +781,16 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
           float pk[32];
           float2 t2[4];
           const uint32_t s_at = s_col + 64 * half;
-          const int more = left - 64 * half;   // states from the half on
 #pragma unroll 1
           for (int again = 0;; again = 1) {
             const float m = m_run == -INFINITY ? 0.0f : m_run;
             const float2 f2 = make_float2(qs, qs), m2 = make_float2(-m, -m);
-            auto exponents = [&](float* sv, int k) {  // of 32 states from k on, in place
+            auto exponents = [&](float* sv) {  // of 32 scores, in place
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 const float2 v = __ffma2_rn(make_float2(sv[e], sv[e + 1]), f2, m2);
                 sv[e] = v.x;
                 sv[e + 1] = v.y;
-              }
-              if (more < k + 32) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) sv[e] = k + e < more ? sv[e] : -INFINITY;
               }
             };
             float sv[2][32];
@@ -789,10 +799,10 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
             tc::tmem_ld32(s_at, sv[0]);
             tc::tmem_wait_ld();
             tc::tmem_ld32(s_at + 32, sv[1]);
-            exponents(sv[0], 0);
+            exponents(sv[0]);
             weights<QT>(sv[0], pk, t2);
             tc::tmem_wait_ld();
-            exponents(sv[1], 32);
+            exponents(sv[1]);
             weights<QT>(sv[1], pk + 16, t2);
             const float sum = ((t2[0].x + t2[0].y) + (t2[1].x + t2[1].y)) +
                               ((t2[2].x + t2[2].y) + (t2[3].x + t2[3].y));
@@ -807,7 +817,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
               float z[32];
               tc::tmem_ld32(s_at + k, z);
               tc::tmem_wait_ld();
-              exponents(z, k);
+              exponents(z);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) mz = fmax3(mz, z[e], z[e + 1]);
             }
