@@ -12,7 +12,8 @@
 // Work.  A unit is a sequence, KV head and one or two query tiles.  With two, K and V of a
 // key tile feed both, each tile having its own softmax warpgroup; with one (a token, a
 // request's beams, the odd tile of a prompt) the warpgroups take the even and the odd key
-// tiles, each into an O of its own, and the first one joins the two at the end.
+// tiles, each into an O of its own, and the one with the last tile joins the two (the other
+// goes on to the next unit meanwhile).
 // Sequences differ in both lengths and there may be one unit or many thousand, so units
 // are not dealt out: all key tiles of the call lie one behind the other on a line of work
 // (a tile counts kCost1 or kCost2, what a unit costs once kCostUnit), which is cut into
@@ -94,7 +95,7 @@ struct CrossSmem {
   long long scan[16];
   int scan_units[16];
   int cost_unit;
-  float2 other[128];  // maximum and sum of the odd key tiles
+  float2 other[128];  // maxima and sums of the warpgroup that does not join
   CrossItem item[kItems];
   uint64_t item_full[kItems], item_read[kItems];
   uint64_t landed[kSt], full[kSt], empty[kSt];
@@ -105,6 +106,7 @@ struct CrossSmem {
   uint64_t tail_full[2], tail_free[2];
   uint64_t mma_done;
   uint32_t tmem_base;
+  uint32_t issued;  // places of the ring that producer 0 has come to
   int abort;
 };
 
@@ -158,6 +160,7 @@ __device__ __forceinline__ void cross_setup(const AttnParams& p, const CrossArgs
     mbar_init(&sm.other_ready, 4);
     mbar_init(&sm.mma_done, kIssuers);
     sm.abort = 0;
+    sm.issued = 0;
     fence_barrier_init();
   }
   if (warp == kIssuer) {
@@ -354,6 +357,10 @@ __device__ __forceinline__ void cross_producer(const AttnParams& p, const CrossA
     if (lane == 0) {
       if (pos >= (uint32_t)kSt) good = wait_for(&sm.empty[st], ((pos / kSt) - 1) & 1, abort, lim);
       if (good && !skip && pw == 0) mbar_arrive_expect_tx(&bars[st], kLoad);
+      if (good && pw == 0) {
+        __threadfence_block();
+        *static_cast<volatile uint32_t*>(&sm.issued) = pos + 1;
+      }
     }
     if (!__shfl_sync(kFull, (int)good, 0)) return false;
     if (!skip && (lane >> 3) == (t & 3) && my_lane) {
@@ -562,7 +569,10 @@ __device__ __forceinline__ void issue_half(uint32_t d, uint32_t a, uint64_t dv, 
 // pipe idle while it waited and committed: without any softmax a key tile took 3100 cycles of
 // which 2050 are MMAs.)
 //
-// A stage is empty when both issuers have released it; whoever uses it alone does so twice.  Places of a unit's tiles in the ring: K0, K1, V0, K2, V1, ..., V(n-1).
+// A stage is empty when both issuers have released it; whoever uses it alone does so twice.
+// An issuer that does not use a stage for a while waits for the producer to have come to its
+// tile's place first: a barrier tells one phase from the one before, not from the one before
+// that, so the wait for a tile may only begin when the one before in its stage has landed.  Places of a unit's tiles in the ring: K0, K1, V0, K2, V1, ..., V(n-1).
 __device__ __forceinline__ uint32_t k_place(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ uint32_t v_place(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
 
@@ -583,6 +593,21 @@ __device__ __forceinline__ bool issue_group(const AttnParams& p, CrossSmem<D, kF
   const uint64_t dt0 = tc::smem_desc(smem_u32(&sm.tail[0][0]), SM::kTail / 2, 1024, tc::kLayoutSw128);
   const uint32_t s_col = tmem + y * 128, o_col = tmem + kColO + y * 128;
   uint32_t base = 0, np = 0, nit = 0, nq = 0, ntail = 0;  // ring place of the unit, P consumed, ...
+  uint32_t seen = 0;    // places that the producer has come to, as last read
+  auto issued = [&](uint32_t at) -> bool {
+    for (uint64_t t0 = 0; (int32_t)(seen - at) <= 0;) {
+      seen = *static_cast<volatile uint32_t*>(&sm.issued);
+      if ((int32_t)(seen - at) > 0) break;
+      if (*abort) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > lim) {
+        *abort = 1;
+        return false;
+      }
+    }
+    return true;
+  };
   uint32_t turns = 0;   // handed over by the other issuer
   bool last_other = false;  // the last product was the other's
   CrossItem x = {};
@@ -598,6 +623,7 @@ __device__ __forceinline__ bool issue_group(const AttnParams& p, CrossSmem<D, kF
     auto full = [&](uint32_t place, int& st) -> bool {
       const uint32_t at = base + place;
       st = at % kSt;
+      if (!issued(at)) return false;
       return wait(&sm.full[st], (at / kSt) & 1);
     };
     auto release = [&](int st) {
@@ -710,6 +736,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t s_col = tmem + lane_off + y * 128;
   const uint32_t o_col = tmem + lane_off + kColO + y * 128;
+  const uint32_t o_other = tmem + lane_off + kColO + (y ^ 1) * 128;
   const float qs = p.q_scale == 0.0f ? 1e-30f : p.q_scale;  // (2^(s * 1e-30) rounds to 1)
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(kFull, wait_for(bar, parity, abort, lim)) != 0;
@@ -872,11 +899,12 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
     float a0 = 1.0f, a1 = 0.0f;
     const bool join = !two && kt1 - kt0 > 1;
     if (join) {
-      if (y == 1) {  // its maxima, sums and O are for the other warpgroup
+      if (y != ((kt1 - kt0 - 1) & 1)) {  // its maxima, sums and O are for the other warpgroup
         sm.other[r] = make_float2(m_run, l);
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.other_ready);
+        ++nother;
         done();
         continue;
       }
@@ -905,7 +933,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
 #pragma unroll
         for (int h = 0; h < 32; h += 16) {
           float ow[16];
-          tc::tmem_ld16(o_col + 128 + k + h, ow);
+          tc::tmem_ld16(o_other + k + h, ow);
           tc::tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) ov[h + e] = fmaf(ow[e], a1, ov[h + e]);
@@ -970,7 +998,7 @@ __device__ __forceinline__ void cross_softmax(const AttnParams& p, const CrossAr
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(&sm.o_free[y]);
-      if (join) mbar_arrive(&sm.o_free[1]);
+      if (join) mbar_arrive(&sm.o_free[y ^ 1]);
     }
     done();
   }
