@@ -609,7 +609,7 @@ __device__ __forceinline__ bool issue_group(const AttnParams& p, CrossSmem<D, kF
     return true;
   };
   uint32_t turns = 0;   // handed over by the other issuer
-  bool last_other = false;  // the last product was the other's
+  bool others = false;  // (the first issuer) the last product of two query tiles is the other's
   CrossItem x = {};
   for (uint32_t n = 0;; ++n) {
     const int slot = n % kItems;
@@ -657,12 +657,14 @@ __device__ __forceinline__ bool issue_group(const AttnParams& p, CrossSmem<D, kF
       const int ts = i == tiles - 1 ? x.tail : -1;
       const uint64_t dv = dv0 + vst * kStage, dt = dt0 + (ntail & 1) * (SM::kTail >> 4);
       if (ts >= 0 && !wait(&sm.tail_full[ntail & 1], (ntail >> 1) & 1)) return false;
-      // the products take turns, in the order of the tiles: the two softmax warpgroups then
-      // stay half a period apart, one at work while the other's MMAs run
-      if (i > 0 || y == 1 || last_other) {
+      // with two query tiles the products take turns, in the order of the tiles: the two
+      // softmax warpgroups then stay half a period apart, one at work while the other's
+      // MMAs run (1054 against 807 us with 16384 states)
+      if (two && (y == 1 || others)) {
         if (!wait(&sm.turn[y], turns & 1)) return false;
         ++turns;
       }
+      others |= two;
       tc::fence_after_sync();
       // 64 states' weights while the softmax is at the others'
       issue_half<0>(o_col, s_col, dv, dt, ts, i != first, kIdescO);
@@ -671,10 +673,9 @@ __device__ __forceinline__ bool issue_group(const AttnParams& p, CrossSmem<D, kF
       ++np;
       tc::fence_after_sync();
       issue_half<kTileKeys / 32>(o_col, s_col, dv, dt, ts, 1, kIdescO);
-      const bool hand = two || i + 1 < tiles || y == 1;  // (a unit begins with the first)
       if (i + step < tiles) {
         if (!scores(i + step)) return false;
-        if (hand) mbar_arrive(&sm.turn[y ^ 1]);
+        if (two) mbar_arrive(&sm.turn[y ^ 1]);
         release(vst);
         release(kst);
         if (i + 2 * step >= tiles) {  // the item's last scores
@@ -682,13 +683,12 @@ __device__ __forceinline__ bool issue_group(const AttnParams& p, CrossSmem<D, kF
           if (two) tc::mma_commit(&sm.q_empty[(nq + 1) & 1]);
         }
       } else {
-        if (hand) mbar_arrive(&sm.turn[y ^ 1]);
+        if (two) mbar_arrive(&sm.turn[y ^ 1]);
         tc::mma_commit(&sm.o_done[y]);
         release(vst);
       }
     }
     if (first < tiles) ++nit;
-    last_other = (two || (tiles & 1) == 0 ? 1 : 0) != y;
     if (x.tail >= 0) {
       // (waited for also where the other one used it: the buffer's phases keep their order)
       if (!wait(&sm.tail_full[ntail & 1], (ntail >> 1) & 1)) return false;
