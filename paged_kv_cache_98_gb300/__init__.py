@@ -449,7 +449,8 @@ def _on_device(device, stream, specs):
     caller's."""
     index = -1 if device.index is None else device.index
     for name, t, dtype, shape in specs:
-        if t is None:
+        if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                         and t.get_device() == index):
             continue
         if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -801,41 +802,40 @@ def resize_requests(request_tables, ref_counts, rows, cached_lens, new_lens, gra
 def _layer_caches(k_caches, v_caches):
     """The caches of all layers, each a sequence of tensors [num_blocks, H, 16, D] or one
     tensor [L, num_blocks, H, 16, D] whose layers are contiguous: (host arrays of their
-    addresses, one of the tensors, its shape, all the tensors)."""
-    addresses, tensors = [], []
+    addresses, the number of layers, all the tensors, the shape of a cache)."""
+    addresses, tensors, first = [], [], None
     for name, caches in (("k_caches", k_caches), ("v_caches", v_caches)):
         if isinstance(caches, torch.Tensor):
             if caches.dim() != 5:
                 raise ValueError(f"{name} must be [L, num_blocks, H, 16, D] or a list of caches")
-            L, shape = caches.shape[0], caches.shape[1:]
-            st, inner = caches.stride(), 1
-            for n, s in zip(reversed(shape), reversed(st[1:])):
-                if n != 1 and s != inner:
-                    raise ValueError(f"{name}: each layer's cache must be contiguous")
-                inner *= n
-            step, at = st[0] * caches.element_size(), caches.data_ptr()
-            addresses.append((_P * max(L, 1))(*range(at, at + L * step, step)) if step else
-                             (_P * max(L, 1))(*[at] * L))
+            L, nb, h, bs, d = caches.shape
+            shape = (nb, h, bs, d)
+            step, *strides = caches.stride()
+            if strides != [h * bs * d, bs * d, d, 1] and not (L and caches[0].is_contiguous()):
+                raise ValueError(f"{name}: each layer's cache must be contiguous")
+            step, at = step * caches.element_size(), caches.data_ptr()
+            addresses.append((_P * L)(*[at + i * step for i in range(L)]))
             tensors.append(caches)
         else:
-            L, shape = len(caches), caches[0].shape if len(caches) else None
+            L = len(caches)
+            shape = tuple(caches[0].shape) if L else None
             for t in caches:
-                if t.shape != shape or t.dim() != 4 or not t.is_contiguous():
+                if t.shape != shape or len(shape) != 4 or not t.is_contiguous():
                     raise ValueError(f"{name}: caches must be contiguous, [num_blocks, H, 16, D], "
                                      "and of one shape")
-            addresses.append((_P * max(L, 1))(*[t.data_ptr() for t in caches]))
-            tensors.extend(caches)
-        if name == "k_caches":
-            first = (L, shape)
+            addresses.append((_P * L)(*[t.data_ptr() for t in caches]))
+            tensors += caches
+        if first is None:
+            first = L, shape
     if first != (L, shape):
         raise ValueError("k_caches and v_caches must have as many layers and the same shapes")
-    if not tensors or L == 0:
+    if L == 0:
         raise ValueError("at least one layer's caches are needed")
-    t0 = tensors[0]
+    dtype, index = tensors[0].dtype, tensors[0].get_device()
     for t in tensors:
-        if t.dtype is not t0.dtype or t.get_device() != t0.get_device():
+        if t.dtype is not dtype or t.get_device() != index:
             raise ValueError("the caches must have one dtype and be on one device")
-    return addresses, L, tensors, tuple(shape)
+    return addresses, L, tensors, shape
 
 
 def copy_blocks_layers(k_caches, v_caches, block_pairs, device_errors=None, stream=None):

@@ -1106,9 +1106,13 @@ int launch_cross_typed(const AttnParams& p, const CrossArgs& c, int ctas, cudaSt
   auto kern = cross_kernel<QT, D, kFP8>;
   // the kernel's register shares add up to what its launch holds; with fewer its
   // warpgroups would wait for registers without end
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
-  if (fa.numRegs != cross_launch_regs(kFP8)) return PKV_ERR_CUDA;
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != cross_launch_regs(kFP8)) return PKV_ERR_CUDA;
   static std::atomic<unsigned long long> configured{0};
   if (!smem_once(kern, smem, configured)) return PKV_ERR_CUDA;
   kern<<<ctas, cross_threads(kFP8), smem, stream>>>(p, c, tk, tv, tq, (int)kv_rows);
