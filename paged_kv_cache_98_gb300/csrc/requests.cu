@@ -253,10 +253,13 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeA
   const int cta = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
   unsigned* s_begin = reinterpret_cast<unsigned*>(s_dyn);  // [S + 1]: 2 * first rank + (copies?)
   int* s_open = s_dyn + S + 1;                             // [S + 1]: blocks opened before
-  int* s_key = s_open + S + 1;                             // [slots] a block, -1: none
+  int* s_key = s_open + S + 1 + 2 * (S + 1) % 4;           // [slots] a block, -1: none
   int* s_holders = s_key + a.slots;                        // [slots] sequences that grow in it
   int* s_latest = s_holders + a.slots;                     // [slots] the last of them
-  int* s_free = s_latest + a.slots;                        // [pieces] free blocks, then those before
+  int* s_free = s_latest + a.slots;                        // [pieces] free blocks before each piece
+  // free blocks of this CTA's pieces: eight consecutive ones, then eight of the next CTA
+  const int per_piece_cta = ((a.pieces + 8 * ctas - 1) / (8 * ctas)) * 8;
+  int* s_count = s_free + ((a.pieces + 3) & ~3);
   for (int i = tid; i < a.slots; i += kResizeThreads) {
     s_key[i] = -1;
     s_holders[i] = 0;
@@ -355,20 +358,21 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeA
   const bool vec = (reinterpret_cast<uintptr_t>(a.counts) & 15u) == 0;
   const int warps = ctas * kResizeWarps, me = warp * ctas + cta;
   constexpr int kScan = 8;  // pieces in flight
-  for (int k0 = me; k0 < a.pieces; k0 += kScan * warps) {
+  for (int l0 = warp; l0 < per_piece_cta; l0 += kScan * kResizeWarps) {
     unsigned n[kScan];
 #pragma unroll
     for (int u = 0; u < kScan; ++u) n[u] = 0;
     for (int d = 4 * lane; d < a.piece; d += 128)
 #pragma unroll
       for (int u = 0; u < kScan; ++u) {
-        const long long id = (long long)(k0 + u * warps) * a.piece + d;
-        if (id < a.num_blocks) n[u] += __popc(free_bits(a.counts, (int)id, a.num_blocks, vec));
+        const int l = l0 + u * kResizeWarps;
+        const long long id = (long long)((l / 8 * ctas + cta) * 8 + l % 8) * a.piece + d;
+        if (l < per_piece_cta && id < a.num_blocks) n[u] += __popc(free_bits(a.counts, (int)id, a.num_blocks, vec));
       }
 #pragma unroll
     for (int u = 0; u < kScan; ++u) {
       n[u] = __reduce_add_sync(kFull, n[u]);
-      if (lane < ctas && k0 + u * warps < a.pieces) cluster.map_shared_rank(s_free, lane)[k0 + u * warps] = (int)n[u];
+      if (lane == 0 && l0 + u * kResizeWarps < per_piece_cta) s_count[l0 + u * kResizeWarps] = (int)n[u];
     }
   }
   cluster.sync();  // every holder has been counted
@@ -401,11 +405,17 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeA
     sm.warp_want[warp] = want_incl;
     sm.warp_open[warp] = open_incl;
   }
-  // the pieces' free blocks become those before each piece, a few consecutive ones a thread
-  const int per_piece = (a.pieces + kResizeThreads - 1) / kResizeThreads;
-  const int k0 = min(tid * per_piece, a.pieces), k1 = min(k0 + per_piece, a.pieces);
-  int free_sum = 0;
-  for (int k = k0; k < k1; ++k) free_sum += s_free[k];
+  // free blocks before each piece: eight pieces a thread, from the CTA that counted them
+  static_assert(kPieces <= 8 * kResizeThreads, "eight pieces a thread");
+  int mine[8] = {0, 0, 0, 0, 0, 0, 0, 0}, free_sum = 0;
+  if (8 * tid < a.pieces) {
+    const int4* from = reinterpret_cast<const int4*>(cluster.map_shared_rank(s_count, tid % ctas) + tid / ctas * 8);
+    const int4 x = from[0], y = from[1];
+    mine[0] = x.x; mine[1] = x.y; mine[2] = x.z; mine[3] = x.w;
+    mine[4] = y.x; mine[5] = y.y; mine[6] = y.z; mine[7] = y.w;
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u) free_sum += mine[u];
   int free_incl = free_sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -443,10 +453,10 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeA
   cluster.sync();
   {
     int at = sm.warp_free[warp] + free_incl - free_sum;
-    for (int k = k0; k < k1; ++k) {
-      const int n = s_free[k];
-      s_free[k] = at;
-      at += n;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (8 * tid + u < a.pieces) s_free[8 * tid + u] = at;
+      at += mine[u];
     }
   }
   const int free_all = sm.free;
@@ -469,10 +479,8 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeA
     const int i = i0 + k;
     if (i < i1) {
       const unsigned begin = 2u * (unsigned)want_at + (copies[k] ? 1u : 0u);
-      for (int c = 0; c < ctas; ++c) {
-        cluster.map_shared_rank(s_begin, c)[i] = begin;
-        cluster.map_shared_rank(s_open, c)[i] = open_at;
-      }
+      s_begin[i] = begin;
+      s_open[i] = open_at;
       want_at = sat_add(want_at, want[k]);
       open_at = sat_add(open_at, opens[k]);
       const bool ok = want[k] == 0 || want_at <= free_all;
@@ -486,11 +494,35 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeA
       }
     }
   }
-  if (tid == 0) {
+  if (tid == 0) {  // (each CTA's own; not among those copied)
     s_begin[S] = 2u * (unsigned)want_all;
     s_open[S] = open_all;
   }
-  cluster.sync();  // the offsets are here
+  cluster.sync();  // the offsets are there
+  if (ctas > 1) {
+    constexpr int kCopy = 4;
+    for (int i0 = tid; i0 < S; i0 += kCopy * kResizeThreads) {
+      unsigned b[kCopy];
+      int o[kCopy];
+#pragma unroll
+      for (int u = 0; u < kCopy; ++u) {
+        const int i = i0 + u * kResizeThreads, of = i / per_cta;
+        if (i < S && of != cta) {
+          b[u] = cluster.map_shared_rank(s_begin, of)[i];
+          o[u] = cluster.map_shared_rank(s_open, of)[i];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kCopy; ++u) {
+        const int i = i0 + u * kResizeThreads;
+        if (i < S && i / per_cta != cta) {
+          s_begin[i] = b[u];
+          s_open[i] = o[u];
+        }
+      }
+    }
+    cluster.sync();  // (also: nobody leaves while its memory is read)
+  }
   // ---- 4: blocks handed out ------------------------------------------------------------------
   // sequences whose needs end within the free blocks: up to the last offset that does
   auto last_at_most = [&](int n, int r) {  // the last i <= n whose offset is at most r
@@ -643,9 +675,11 @@ int pkv_resize_requests(int32_t* request_tables, int32_t* ref_counts, const int3
   while (a.slots * ctas < 2 * num_seqs) a.slots *= 2;
   while ((long long)a.piece * kPieces < a.num_blocks) a.piece *= 2;
   a.pieces = (a.num_blocks + a.piece - 1) / a.piece;
-  const size_t smem = 4 * (2 * ((size_t)num_seqs + 1) + 3 * (size_t)a.slots + a.pieces);
+  const size_t smem = 4 * (2 * ((size_t)num_seqs + 1) + 2 + 3 * (size_t)a.slots + (a.pieces + 3) / 4 * 4 +
+                           (a.pieces + 8 * ctas - 1) / (8 * ctas) * 8);
   constexpr size_t kMostSmem = 4 * (2 * (PKV_STEP_MAPS_MAX_SEQS + 1) +
-                                    3 * (2 * PKV_STEP_MAPS_MAX_SEQS / kResizeCtas) + kPieces);
+                                    3 * (2 * PKV_STEP_MAPS_MAX_SEQS / kResizeCtas) + kPieces +
+                                    kPieces / kResizeCtas + 16);
   static_assert(kMostSmem + sizeof(ResizeShared) <= 232448, "shared memory budget of one CTA");
   static std::atomic<unsigned long long> configured{0};
   if (!smem_once(resize_kernel, kMostSmem, configured)) return PKV_ERR_CUDA;
