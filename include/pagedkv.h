@@ -577,8 +577,10 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
  *   kv_dtype  == q_dtype, or FP8_E4M3: decode(byte) * k_scale / v_scale.
  * K and V behind a sequence's last state do not reach a row, whatever they hold.  Rows
  * that see an infinity or NaN have results that are not finite, as the formula has.
- * Rounding: scores, maxima, sums and outputs are fp32, the output rounded once; the
- * softmax weights are rounded to q_dtype, to which E4M3 codes are widened exactly.
+ * Rounding: scores, sums and outputs are fp32, the output rounded once; the softmax
+ * weights are rounded to q_dtype, on an E4M3 cache to fp16, and summed as rounded (E4M3
+ * codes are widened exactly).  Scores (times scale and log2 e) from 2^27 on, whose
+ * differences fp32 no longer holds, may give rows that are not finite.
  * The split of long inputs depends on the lengths of the whole batch: a row's last bits
  * may differ between batches, never between two calls of one batch.
  * out must not overlap q or the caches.  num_seqs == 0 or total_q == 0 launches nothing.
