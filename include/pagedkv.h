@@ -694,7 +694,8 @@ int pkv_copy_blocks_layers(void* const* k_caches, void* const* v_caches, int num
  * as it was (new_lens = its context cut back to the table; PKV_DEVERR_CONTEXT).  A token
  * in a block outside the pool does not move, nor does one whose place is there
  * (PKV_DEVERR_BLOCK_ID).  Positions are kept as they were rotated.
- * Caches as for pkv_copy_blocks_layers.
+ * Caches as for pkv_copy_blocks_layers, of fewer than 2^27 blocks (PKV_ERR_UNSUPPORTED
+ * beyond).
  */
 int pkv_compact_tokens(void* const* k_caches, void* const* v_caches, int num_layers,
                        const int32_t* block_tables, const int32_t* context_lens,

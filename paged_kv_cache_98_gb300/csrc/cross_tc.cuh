@@ -10,8 +10,8 @@
 // rescaled) only when the weights of 64 states add up to more than 2^15; out = O / sum(P).
 // The sum is that of the rounded weights: with bf16 ones and rows of 300 states the error of
 // out, against that of an exact result's rounding, is 1.25 times as large instead of 1.35 (up to
-// 1.4 instead of 1.7 in a call of 16 rows), for 224 us instead of 213 with prompts of 448
-// tokens; decode waits for memory.
+// 1.4 instead of 1.7 in a call of 16 rows), for 224 us instead of 213 with six prompts of 300
+// to 1500 tokens; decode waits for memory.
 //
 // Work.  A unit is a sequence, KV head and one or two query tiles.  With two, K and V of a
 // key tile feed both, each tile having its own softmax warpgroup; with one (a token, a

@@ -51,14 +51,22 @@ __global__ void __launch_bounds__(kThreads)
 // tokens go to is no source of a later one.  So a unit, the rows of one sequence, cache and
 // KV head, can be moved in place by threads that walk its list in ascending turns: all rows
 // of a turn are read, then (a barrier) written, and the next turn's reads need no barrier
-// behind those writes.  A unit is a warp's where lists are short (a drafted path: many
-// units, few rows each) and a CTA's where they are long (few units, 128 rows of 256 bytes
-// a turn).  Bound by HBM, two row bytes a moved token; by launch and four dependent reads
-// (list, table, row) for short ones.
+// behind those writes.  A unit is a warp's where lists are short for how many units there are
+// (a drafted path) and a CTA's where they are long.  Bound by HBM, two row bytes a moved
+// token (6.4 TB/s with 16 sequences of 8192 tokens, 8 layers), with few units by their turns, one
+// after the other (4 sequences of up to 16384 tokens, 2 layers: 105 us, 4.2 TB/s); by launch
+// and four dependent reads (list, table, row) for short lists.  (The next turn's rows loaded
+// before this one's are stored, in as many or twice the registers: 108 to 116 us.)
 constexpr int kDeep = 4;        // rows a thread reads in a turn
-constexpr int kLongList = 96;   // from this many kept tokens a sequence on (on average), a CTA a unit
-
-constexpr long long kManyUnits = 608;  // below as many, CTAs' units are quarters or halves of rows
+// Kept tokens a sequence (on average) from which a CTA moves a unit: one for every kLongUnits
+// units, but within the other two.  Measured with a warp and a CTA: 128 units 3.6 and 4.1 us with 8
+// kept tokens, 5.0 and 4.0 with 16; 1024 units 5.2 and 6.5 with 16, 7.4 and 7.0 with 32; 2048
+// units 13.4 and 14.3 with 64, 23.2 and 22.5 with 128; 4096 units 47 and 54 with 128, 99 and
+// 93 with 256.
+constexpr int kLongUnits = 20, kLeastLong = 12, kMostLong = 256;
+// Below as many, CTAs' units are 64 bytes of each row: 4 x 16384 tokens kept by half in 128 units
+// take 105 us instead of 198, 16 x in 512 units 315 instead of 331.
+constexpr long long kManyUnits = 608;
 
 struct CompactArgs {
   const int32_t *tables, *context, *base, *starts, *keep;
@@ -191,10 +199,11 @@ int launch_compact(const Caches& c, const CompactArgs& a, cudaStream_t stream) {
 
 template <int kRowBytes>
 int launch_compact_rows(const Caches& c, const CompactArgs& a, cudaStream_t stream) {
-  if (a.num_keep < (long long)kLongList * a.num_seqs)
+  const long long units = (long long)a.num_seqs * a.caches * a.kv_heads;
+  if (a.num_keep < std::clamp(units / kLongUnits, (long long)kLeastLong, (long long)kMostLong) * a.num_seqs)
     return launch_compact<1, kRowBytes, kRowBytes>(c, a, stream);
   if constexpr (kRowBytes > 64)
-    if ((long long)a.num_seqs * a.caches * a.kv_heads < kManyUnits)
+    if (units < kManyUnits)
       return launch_compact<8, kRowBytes, 64>(c, a, stream);
   return launch_compact<8, kRowBytes, kRowBytes>(c, a, stream);
 }

@@ -20,10 +20,10 @@ __device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlockSi
 // up to kForkRows of them and kForkChunk of their entries, looks through the parents for
 // their children, copies the chunk for each, and adds children - 1 to its blocks' counts
 // (integers: the order of the atomics does not matter).  Bound by the reads and writes of
-// the tables for long ones, by launch and two dependent reads for short ones.
+// the tables for long ones, by launch and two dependent reads for short ones (64 rows of up to
+// 94 entries: 1.8 us in a graph).
 constexpr int kForkThreads = 256;
-constexpr int kForkChunk = 1024;   // entries of a row a CTA of several rows handles: four a thread
-constexpr long long kForkLong = 1 << 20;  // entries of all tables
+constexpr int kForkChunk = 1024;   // entries of a row a CTA handles: four a thread
 constexpr int kForkTile = 2048;    // parents looked through at a time
 constexpr int kForkRows = 64;
 constexpr int kForkCtas = 1216;    // rows share CTAs beyond this many (eight a processor)
@@ -104,86 +104,62 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a) {
   }
 }
 
-// The same for kRows consecutive old rows a CTA, whose entries its threads hold: they are
-// read once, while the parents are looked through.  Neighbours often share the front of
-// their lists (samples of one prompt), and where they have the same block in the same
-// place its count changes once by what all of them together change it: 512 rows of up to
-// 8192 entries in groups of 8 take 9 us with eight rows a CTA, 14 with one.
-template <int kRows, int kDeep, int kTile>
-__global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(const ForkArgs a) {
-  __shared__ int s_child[kRows][kTile];
-  __shared__ int s_matches[kRows];
-  const int tid = threadIdx.x, r0 = blockIdx.x * kRows, e0 = blockIdx.y * (kForkThreads * kDeep) + tid;
+// The same with one old row a CTA, whose entries its threads hold: they are read once, while
+// the parents are looked through.  (512 rows of up to 8192 entries: 9 us with tables in L2, 12
+// from memory, where samples in groups of eight share the front of their lists and their
+// counts change eight times.  Eight rows a CTA, which add up what they change of a shared count,
+// take 8 and 12, but 9 instead of 6 where nothing is shared, and 5.7 instead of 4.8 with 128 rows.)
+__global__ void __launch_bounds__(kForkThreads) fork_row_kernel(const ForkArgs a) {
+  constexpr int kDeep = kForkChunk / kForkThreads;
+  __shared__ int s_child[kForkTile];
+  __shared__ int s_matches;
+  const int tid = threadIdx.x, row = blockIdx.x, e0 = blockIdx.y * kForkChunk + tid;
   const bool first = blockIdx.y == 0;
   const int cap = a.width * kBlockSize;
-  int len[kRows], most = 0;
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    len[r] = r0 + r < a.num_in ? __ldg(a.lens + r0 + r) : 0;
-    if (len[r] < 0 || len[r] > cap) {
-      if (first && tid == 0) flag_error(a.errors, PKV_DEVERR_CONTEXT);
-      len[r] = len[r] < 0 ? 0 : cap;
-    }
-    most = max(most, len[r]);
+  int len = __ldg(a.lens + row);
+  if (len < 0 || len > cap) {
+    if (first && tid == 0) flag_error(a.errors, PKV_DEVERR_CONTEXT);
+    len = len < 0 ? 0 : cap;
   }
-  if (!first && (e0 - tid) * kBlockSize >= most) return;
-  int v[kRows][kDeep], children[kRows];
+  const int n = blocks_of(len);
+  if (!first && e0 - tid >= n) return;
+  const int32_t* src = a.tables + (size_t)row * a.width;
+  int v[kDeep], children = 0;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    children[r] = 0;
-#pragma unroll
-    for (int u = 0; u < kDeep; ++u) {
-      const int e = e0 + u * kForkThreads;
-      v[r][u] = e < blocks_of(len[r]) ? __ldg(a.tables + (size_t)(r0 + r) * a.width + e) : 0;
-    }
+  for (int u = 0; u < kDeep; ++u) {
+    const int e = e0 + u * kForkThreads;
+    v[u] = e < n ? __ldg(src + e) : 0;
   }
-  for (int t0 = 0; t0 < a.num_out; t0 += kTile) {
-    if (tid < kRows) s_matches[tid] = 0;
+  for (int t0 = 0; t0 < a.num_out; t0 += kForkTile) {
+    if (tid == 0) s_matches = 0;
     __syncthreads();
-    const int t1 = min(t0 + kTile, a.num_out);
+    const int t1 = min(t0 + kForkTile, a.num_out);
     for (int i = t0 + tid; i < t1; i += kForkThreads) {
       const int p = __ldg(a.parents + i);
-      if (p >= r0 && p - r0 < kRows && p < a.num_in) {
-        s_child[p - r0][atomicAdd(&s_matches[p - r0], 1)] = i;
-        if (first) a.lens_out[i] = min(max(__ldg(a.lens + p), 0), cap);
-      } else if (first && r0 == 0 && (p < 0 || p >= a.num_in)) {
+      if (p == row) {
+        s_child[atomicAdd(&s_matches, 1)] = i;
+        if (first) a.lens_out[i] = len;
+      } else if (first && row == 0 && (p < 0 || p >= a.num_in)) {
         a.lens_out[i] = 0;
         if (p >= 0) flag_error(a.errors, PKV_DEVERR_CONTEXT);
       }
     }
     __syncthreads();
+    const int matches = s_matches;
+    for (int k = 0; k < matches; ++k) {
+      int32_t* dst = a.tables_out + (size_t)s_child[k] * a.width;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int matches = s_matches[r], n = blocks_of(len[r]);
-      for (int k = 0; k < matches; ++k) {
-        int32_t* dst = a.tables_out + (size_t)s_child[r][k] * a.width;
-#pragma unroll
-        for (int u = 0; u < kDeep; ++u)
-          if (e0 + u * kForkThreads < n) dst[e0 + u * kForkThreads] = v[r][u];
-      }
-      children[r] += matches;
+      for (int u = 0; u < kDeep; ++u)
+        if (e0 + u * kForkThreads < n) dst[e0 + u * kForkThreads] = v[u];
     }
-    __syncthreads();  // the lists have been read
+    children += matches;
+    __syncthreads();  // the list has been read
   }
 #pragma unroll
   for (int u = 0; u < kDeep; ++u) {
-    int block = -1, change = 0;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      if (e0 + u * kForkThreads >= blocks_of(len[r])) continue;
-      const int b = v[r][u];
-      if (b < 0 || b >= a.num_blocks) {
-        flag_error(a.errors, PKV_DEVERR_BLOCK_ID);
-        continue;
-      }
-      if (b != block) {
-        if (change != 0) atomicAdd(a.counts + block, change);
-        block = b;
-        change = 0;
-      }
-      change += children[r] - 1;
-    }
-    if (change != 0) atomicAdd(a.counts + block, change);
+    if (e0 + u * kForkThreads >= n) continue;
+    if (v[u] < 0 || v[u] >= a.num_blocks) flag_error(a.errors, PKV_DEVERR_BLOCK_ID);
+    else if (children != 1) atomicAdd(a.counts + v[u], children - 1);
   }
 }
 
@@ -202,7 +178,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(const ForkArgs 
 // Every sum is one of integers and the hash table only counts and takes maxima, so the
 // result does not depend on the order of the atomics.  Bound by its dependent reads and
 // five cluster barriers for small batches, by reading the counts twice (up to the last
-// block handed out the second time) on sixteen processors for large pools.
+// block handed out the second time) on sixteen processors for large pools: 35 us for 8000 sequences
+// that give back or open blocks of a pool of 1000000, of which the scan takes 10.
 constexpr int kResizeCtas = 16;  // at most; one where that is enough (kOneCta...)
 constexpr int kResizeThreads = 1024;
 constexpr int kResizeWarps = kResizeThreads / 32;
@@ -221,7 +198,10 @@ struct ResizeArgs {
   uint32_t* errors;
 };
 constexpr int kPieces = 8192;  // at most
-constexpr int kOneCtaSeqs = 512, kOneCtaBlocks = 32768;
+// A cluster costs more to start than one CTA, whose scan is longer: 64 sequences take 10.7 us
+// with one CTA and 11.8 with sixteen from a pool of 8192 blocks, 12.4 and 12.1 of 32768, 15.0
+// and 12.2 of 65536, 32.2 and 13.9 of 262144; 512 take 16.8 and 13.6 of 65536.
+constexpr int kOneCtaSeqs = 512, kOneCtaBlocks = 16384;
 
 __device__ __forceinline__ int sat_add(int x, int y) { return min(x + y, kSat); }
 
@@ -613,23 +593,16 @@ int pkv_fork_requests(int32_t* tables_out, int32_t* lens_out, const int32_t* tab
   ForkArgs a{tables_out, lens_out, tables, lens, ref_counts, parents, num_out, num_in,
              max_blocks_per_seq, num_blocks, 1, 32, device_errors};
   cudaStream_t on = static_cast<cudaStream_t>(stream);
+  const int chunks = (max_blocks_per_seq + kForkChunk - 1) / kForkChunk;
+  if (chunks > 65535) return PKV_ERR_UNSUPPORTED;
   if (num_in > 0 && num_in <= kForkCtas) {
-    // eight rows a CTA where that leaves the processors enough of them
-    const bool eight = (long long)num_in * max_blocks_per_seq >= kForkLong;
-    const int per = kForkThreads * (eight ? 2 : 4), rows = eight ? 8 : 1;
-    const int chunks = (max_blocks_per_seq + per - 1) / per;
-    if (chunks > 65535) return PKV_ERR_UNSUPPORTED;
-    const dim3 grid((num_in + rows - 1) / rows, chunks);
-    if (eight) fork_rows_kernel<8, 2, 512><<<grid, kForkThreads, 0, on>>>(a);
-    else fork_rows_kernel<1, 4, kForkTile><<<grid, kForkThreads, 0, on>>>(a);
+    fork_row_kernel<<<dim3(num_in, chunks), kForkThreads, 0, on>>>(a);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
   }
   a.rows = num_in > kForkCtas ? (num_in + kForkCtas - 1) / kForkCtas : 1;
   while (a.lanes < kForkThreads && 4 * a.lanes < max_blocks_per_seq) a.lanes *= 2;
   const int ctas = num_in > 0 ? (num_in + a.rows - 1) / a.rows : 1;
-  const int chunks = (max_blocks_per_seq + kForkChunk - 1) / kForkChunk;
   static_assert((PKV_FORK_MAX_ROWS + kForkCtas - 1) / kForkCtas <= kForkRows, "rows of a CTA");
-  if (chunks > 65535) return PKV_ERR_UNSUPPORTED;
   fork_kernel<<<dim3(ctas, chunks), kForkThreads, 0, on>>>(a);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

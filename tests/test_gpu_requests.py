@@ -408,6 +408,29 @@ def test_compact(layers, heads, d, kind, S, most, tail, share):
     assert got[2] == want[2] == 0
 
 
+@pytest.mark.parametrize("d,kind", [(64, "e4m3"), (64, "f16"), (128, "e4m3"), (128, "bf16")])
+@pytest.mark.parametrize("S,layers,heads,most", [
+    (20, 8, 5, 150),     # lists of tens of tokens and many units: a warp moves one
+    (12, 8, 5, 400),     # longer lists: a CTA moves one, of whole rows
+    (9, 2, 3, 90),       # few units, short lists: a CTA moves 64 bytes of each row
+    (1, 1, 1, 30),       # one unit
+])
+def test_compact_units(S, layers, heads, most, d, kind):
+    """Short and long lists in many and few units, several turns each, every row size."""
+    r = np.random.RandomState(S + d)
+    tables, ctx, base, starts, keep = lists(r, S, most, 0, 0.6)
+    ctx[0], base[0] = most, 1
+    keep0 = 1 + np.flatnonzero(r.rand(most - 1) < 0.6)
+    keep, starts = np.concatenate([keep0, keep[starts[1]:]]), starts + len(keep0) - starts[1]
+    starts[0] = 0
+    x = caches(layers, tables.size + 5, heads, d, kind, seed=S)
+    want = plain_compact(raw(x), tables, ctx, base, starts, keep, None)
+    got = run_compact(x, tables, ctx, base, starts, keep, np.ones(tables.size + 5))
+    np.testing.assert_array_equal(got[0], want[0])
+    np.testing.assert_array_equal(got[1], want[1])
+    assert got[2] == want[2] == 0
+
+
 @pytest.mark.parametrize("long", [False, True])
 @pytest.mark.parametrize("what", ["twice", "falls", "early", "late", "context", "base", "starts", "shared",
                                   "shared but in place", "source block", "place's block"])
