@@ -10,7 +10,7 @@
 // rescaled) only when the weights of 64 states add up to more than 2^15; out = O / sum(P).
 // The sum is that of the rounded weights: with bf16 ones and rows of 300 states the error of
 // out, against that of an exact result's rounding, is 1.25 times as large instead of 1.35 (up to
-// 1.4 instead of 1.7 in a call of 16 rows), for 224 us instead of 213 with six prompts of 300
+// 1.4 instead of 1.7 in a call of 16 rows), for 222 us instead of 213 with six prompts of 300
 // to 1500 tokens; decode waits for memory.
 //
 // Work.  A unit is a sequence, KV head and one or two query tiles.  With two, K and V of a
@@ -29,8 +29,14 @@
 //
 // Two CTAs of a cluster that share four query tiles, each loading half of every K and V tile
 // and multicasting it to both, were built and measured: 741 against 747 us for four prompts of
-// 1024 tokens over 16384 states, and slower with ragged prompts (in a unit of few tiles
+// 1024 tokens over 16384 states (before the sums of rounded weights), and slower with ragged prompts (in a unit of few tiles
 // one CTA waits for the other).  Loads alone take 515 us of those, MMAs alone 495.
+//
+// Bounds, and what was measured (calls in a graph, join included; heads of 128 on 8): HBM for
+// few queries (1.5 GB of states 234 us, 6.5 TB/s); for prompts the softmax's exponentials and
+// conversions beside the MMAs (four of 1024 tokens over 16384 states 766 us, 1440 TFLOP/s; six
+// ragged ones 222 us, 1130); on E4M3 caches the converters' and the softmax's instructions
+// (260 MB of codes 108 us); latency for small calls (eight tokens, 16 heads of 64, 23 MB: 21 us).
 //
 // Warps: 0-3 softmax of tile a (or even key tiles), 4-7 of tile b (odd), 8 and 9 issue the
 // MMAs of either (8 owns TMEM), 10 and 11 load, 10 also makes the items from the line of work
@@ -726,18 +732,21 @@ __device__ __forceinline__ void cross_issuer(const AttnParams& p, CrossSmem<D, k
 
 // Weights 2^z of 32 states, rounded to 16 bits, as 16 packed pairs, and the fp32 sums of what
 // they were rounded to: out = sum(p v) / sum(p) is then a mean with weights a rounding off, and
-// a state that has all but all the weight is given back as it is.
+// a state that has all but all the weight is given back as it is.  (Sums that take the 16-bit
+// halves as they are: 766 us for four prompts of 1024 tokens over 16384 states, 779 with
+// halves widened before.)
 template <class PT>
 __device__ __forceinline__ void weights(const float* z, float* pk, float2* sums) {
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
     const uint32_t u = pack2<PT>(fast_exp2(z[e]), fast_exp2(z[e + 1]));
-    float2 w;
+    float2& t = sums[(e >> 1) & 3];
     if constexpr (std::is_same<PT, BF16>::value)
-      w = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.f32.bf16 %0, lo, %0;\n\tadd.f32.bf16 %1, hi, %1;\n\t}"
+          : "+f"(t.x), "+f"(t.y) : "r"(u));
     else
-      w = __half22float2(*reinterpret_cast<const __half2*>(&u));
-    sums[(e >> 1) & 3] = __fadd2_rn(sums[(e >> 1) & 3], w);
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.f32.f16 %0, lo, %0;\n\tadd.f32.f16 %1, hi, %1;\n\t}"
+          : "+f"(t.x), "+f"(t.y) : "r"(u));
     pk[e >> 1] = __uint_as_float(u);
   }
 }

