@@ -1089,22 +1089,38 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const AttnPara
     if (r >= (qt ? cut.w : cut.z) * g) continue;
     auto slot = [&](int i) { return (size_t)(2 * (b + i) + (i == 0 ? 1 : 0)) * c.part_rows + at; };
     const int parts = last - b + 1;
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(p.lse + slot(i)));
+    constexpr int kLanes = D / 4, kAhead = 4;
+    auto value = [&](int i) {
+      return i < parts && lane < kLanes
+                 ? __ldcg(reinterpret_cast<const float4*>(p.o_part + slot(i) * D) + lane)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 v[kAhead];  // on their way while the weights are found
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) v[u] = value(u);
+    const float lse = lane < parts ? __ldcg(p.lse + slot(lane)) : -INFINITY;
+    float m = lse;
+    for (int i = lane + 32; i < parts; i += 32) m = fmaxf(m, __ldcg(p.lse + slot(i)));
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    constexpr int kLanes = D / 4;
+    const float mine = exp2f(lse - m);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.0f;
-    for (int i = 0; i < parts; ++i) {
-      const float w = exp2f(__ldcg(p.lse + slot(i)) - m);
-      sum += w;
-      if (lane < kLanes) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.o_part + slot(i) * D) + lane);
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+    for (int i0 = 0; i0 < parts; i0 += kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u;
+        if (i >= parts) break;
+        const float w = i < 32 ? __shfl_sync(kFull, mine, i) : exp2f(__ldcg(p.lse + slot(i)) - m);
+        sum += w;
+        acc.x = fmaf(w, v[u].x, acc.x);
+        acc.y = fmaf(w, v[u].y, acc.y);
+        acc.z = fmaf(w, v[u].z, acc.z);
+        acc.w = fmaf(w, v[u].w, acc.w);
+      }
+      if (i0 + kAhead < parts) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) v[u] = value(i0 + kAhead + u);
       }
     }
     if (lane < kLanes) {
