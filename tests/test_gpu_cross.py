@@ -384,3 +384,18 @@ def test_refusals():
     refused(pkv.PagedKVError, 0, c.q)                        # in place
     refused(pkv.PagedKVError, 7, float("nan"))
     refused(ValueError, 0, torch.empty(2, 8, 256, dtype=c.q.dtype, device=DEV)[..., ::2])
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+def test_blocks_past_32_bits(kv):
+    """States in blocks whose elements lie more than 2^32 into caches of 10 or 20 GB."""
+    c = Case(18, [1, 3, 150], [333, 2000, 140], H=16, hkv=8, kv=kv)
+    want, nb = run(c), (1 << 32) // (8 * 16 * 128) + c.nb + 1000
+    for name in ("kc", "vc"):
+        small = getattr(c, name)
+        big = torch.empty(nb, *small.shape[1:], dtype=small.dtype, device=DEV)
+        big.view(torch.uint8)[-c.nb:] = small.view(torch.uint8)
+        setattr(c, name, big)
+    c.tables += nb - c.nb         # (entries behind a sequence's last stay outside the pool)
+    assert torch.equal(want, c.call())
+    assert pkv.check_errors(c.err) == 0

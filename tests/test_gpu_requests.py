@@ -408,6 +408,29 @@ def test_compact(layers, heads, d, kind, S, most, tail, share):
     assert got[2] == want[2] == 0
 
 
+def test_blocks_past_32_bits():
+    """Copies and moves between the first and the last blocks of caches of more than 2^32 elements."""
+    nb, heads, d = (1 << 32) // (8 * 16 * 128) + 600, 8, 128
+    x = torch.empty(1, 2, nb, heads, 16, d, dtype=torch.float16, device=DEV)
+    small = caches(1, 12, heads, d, "f16", seed=3)
+    ids = np.array([0, 1, 2, 3, 4, 5] + [nb - i for i in range(6, 0, -1)])
+    at = ints(ids).long()
+    x[:, :, at] = small
+    pairs = np.array([[0, 11], [10, 1], [3, 6]])
+    pkv.copy_blocks_layers(x[:, 0], x[:, 1], ints(ids[pairs]))
+    tables = np.array([[2, 9, 8, 4], [5, 7, 10, 0]])
+    ctx, base, starts = np.array([64, 60]), np.array([3, 0]), np.array([0, 20, 50])
+    keep = np.concatenate([np.arange(20) * 3 + 4, np.arange(30) * 2])
+    new = ints([0, 0])
+    pkv.compact_tokens(x[:, 0], x[:, 1], ints(ids[tables]), ints(ctx), ints(base), ints(starts), ints(keep), new)
+    want = raw(small)
+    for a, b in pairs:
+        want[:, :, b] = want[:, :, a]
+    want = plain_compact(want, tables, ctx, base, starts, keep, None)
+    np.testing.assert_array_equal(raw(x[:, :, at].contiguous()), want[0])
+    np.testing.assert_array_equal(new.cpu().numpy(), want[1])
+
+
 @pytest.mark.parametrize("d,kind", [(64, "e4m3"), (64, "f16"), (128, "e4m3"), (128, "bf16")])
 @pytest.mark.parametrize("S,layers,heads,most", [
     (20, 8, 5, 150),     # lists of tens of tokens and many units: a warp moves one
