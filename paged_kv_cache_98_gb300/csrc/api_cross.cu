@@ -5,7 +5,7 @@
 #include <cstdint>
 
 #include "common.cuh"
-#include "launch.h"
+#include "cross.h"
 
 namespace {
 

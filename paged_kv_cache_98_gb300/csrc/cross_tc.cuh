@@ -35,8 +35,8 @@
 // Bounds, and what was measured (calls in a graph, join included; heads of 128 on 8): HBM for
 // few queries (1.5 GB of states 234 us, 6.5 TB/s); for prompts the softmax's exponentials and
 // conversions beside the MMAs (four of 1024 tokens over 16384 states 766 us, 1440 TFLOP/s; six
-// ragged ones 222 us, 1130); on E4M3 caches the converters' and the softmax's instructions
-// (260 MB of codes 108 us); latency for small calls (eight tokens, 16 heads of 64, 23 MB: 21 us).
+// ragged ones 218 us, 1150); on E4M3 caches the converters' and the softmax's instructions
+// (260 MB of codes 107 us); latency for small calls (eight tokens, 16 heads of 64, 23 MB: 20 us).
 //
 // Warps: 0-3 softmax of tile a (or even key tiles), 4-7 of tile b (odd), 8 and 9 issue the
 // MMAs of either (8 owns TMEM), 10 and 11 load, 10 also makes the items from the line of work
@@ -45,6 +45,7 @@
 #ifndef PKV_CROSS_TC_CUH
 #define PKV_CROSS_TC_CUH
 
+#include "cross.h"
 #include "prefill_mods.cuh"
 
 namespace pkv {

@@ -191,20 +191,6 @@ int launch_prefill_cap_bias_d64(const AttnParams& p, int q_dtype, int kv_dtype, 
 int launch_prefill_cap_bias_d128(const AttnParams& p, int q_dtype, int kv_dtype, int total_q,
                                  cudaStream_t stream);
 
-// Cross attention: query rows over an encoder's states (context_lens; max_context bounds
-// them).  Work is cut into `ctas` parts; o_part and lse hold two partials of part_rows rows
-// for each, cuts what the join needs (all null where no unit can be cut).
-struct CrossArgs {
-  int max_q;       // bound of the sequences' queries
-  int part_rows;   // rows of a partial
-  int box_tokens;  // tokens of a query box
-  int4* cuts;      // [2 * ctas]: last part, first token, tokens of both query tiles; KV head
-};
-int launch_cross_d64(const AttnParams& p, const CrossArgs& c, int q_dtype, int kv_dtype, int ctas,
-                     cudaStream_t stream);
-int launch_cross_d128(const AttnParams& p, const CrossArgs& c, int q_dtype, int kv_dtype, int ctas,
-                      cudaStream_t stream);
-
 // One launch for a mixed batch: pd describes the decode rows (as for
 // launch_paged_decode_tc), pp the prefill chunks (as for launch_prefill_tc);
 // the CTAs are split between the two (prefill_ctas > 0 fixes the chunks'
