@@ -29,8 +29,9 @@
 //
 // Two CTAs of a cluster that share four query tiles, each loading half of every K and V tile
 // and multicasting it to both, were built and measured: 741 against 747 us for four prompts of
-// 1024 tokens over 16384 states (before the sums of rounded weights), and slower with ragged prompts (in a unit of few tiles
-// one CTA waits for the other).  Loads alone take 515 us of those, MMAs alone 495.
+// 1024 tokens over 16384 states (before the sums of rounded weights), and slower with ragged
+// prompts (in a unit of few tiles one CTA waits for the other).  Loads alone take 515 us of
+// those, MMAs alone 495.
 //
 // Bounds, and what was measured (calls in a graph, join included; heads of 128 on 8): HBM for
 // few queries (1.5 GB of states 234 us, 6.5 TB/s); for prompts the softmax's exponentials and
@@ -591,7 +592,8 @@ __device__ __forceinline__ void issue_half(uint32_t d, uint32_t a, uint64_t dv, 
 // A stage is empty when both issuers have released it; whoever uses it alone does so twice.
 // An issuer that does not use a stage for a while waits for the producer to have come to its
 // tile's place first: a barrier tells one phase from the one before, not from the one before
-// that, so the wait for a tile may only begin when the one before in its stage has landed.  Places of a unit's tiles in the ring: K0, K1, V0, K2, V1, ..., V(n-1).
+// that, so the wait for a tile may only begin when the one before in its stage has landed.
+// Places of a unit's tiles in the ring: K0, K1, V0, K2, V1, ..., V(n-1).
 __device__ __forceinline__ uint32_t k_place(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ uint32_t v_place(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
 
