@@ -641,7 +641,8 @@ int pkv_fork_requests(int32_t* tables_out, int32_t* lens_out, const int32_t* tab
  * Blocks for 2 and 3 are the free ones (count 0 after 1) in the order of their ids,
  * handed out in batch order, a sequence's copy first.  Where a sequence's do not suffice,
  * it and all behind it that need blocks keep their cached length and everything they have
- * (PKV_DEVERR_NO_BLOCKS).
+ * (PKV_DEVERR_NO_BLOCKS).  So does the last holder of 2 if one of the others, denied its copy,
+ * goes on holding the block: nobody is granted a token in a block that others hold.
  *   granted_lens [num_seqs]: new, or cached where blocks did not suffice, 0 for padding
  *   new_blocks [num_new_blocks]: the opened blocks of 3 in batch order, as
  *         pkv_build_step_maps takes them (with q_lens = granted - cached of what grows),

@@ -169,7 +169,9 @@ __global__ void __launch_bounds__(kForkThreads) fork_row_kernel(const ForkArgs a
 //   1  blocks behind the new lengths lose a reference
 //   2  what each sequence needs: a copy of a shared partial last block (how many of its
 //      holders grow, and the last of them: a hash table over the cluster's shared memory),
-//      and the blocks it opens
+//      and the blocks it opens.  The last of holders that all grow needs no copy, as the others
+//      leave; so if one of those is denied its copy, it marks the block, and the last one
+//      stays as it is too
 //   3  prefix sums of the needs in batch order, and of the free blocks in the order of
 //      their ids; every CTA gets all the sequences' offsets
 //   4  the warp that meets the r-th free block gives it to the sequence whose needs hold r.
@@ -464,7 +466,12 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeA
       want_at = sat_add(want_at, want[k]);
       open_at = sat_add(open_at, opens[k]);
       const bool ok = want[k] == 0 || want_at <= free_all;
-      if (!ok) flag_error(a.errors, PKV_DEVERR_NO_BLOCKS);
+      if (!ok) {
+        flag_error(a.errors, PKV_DEVERR_NO_BLOCKS);
+        // it goes on holding its block, whatever the block's last holder counts on (the numbers
+        // of holders have been read: a barrier ago)
+        if (copies[k]) cluster.map_shared_rank(s_holders, slot[k] / a.slots)[slot[k] % a.slots] = -1;
+      }
       a.granted[i] = row[k] < 0 ? 0 : ok ? new_len[k] : old_len[k];
       if (!(ok && copies[k])) {
         a.pairs[2 * i] = -1;
@@ -478,7 +485,14 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeA
     s_begin[S] = 2u * (unsigned)want_all;
     s_open[S] = open_all;
   }
-  cluster.sync();  // the offsets are there
+  cluster.sync();  // the offsets are there, and the marks
+  // one that keeps its block while another still holds it does not grow (if it needs blocks, it is
+  // behind one that got none, and has none either)
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k)
+    if (slot[k] >= 0 && !copies[k] &&
+        cluster.map_shared_rank(s_holders, slot[k] / a.slots)[slot[k] % a.slots] < 0)
+      a.granted[i0 + k] = old_len[k];
   if (ctas > 1) {
     constexpr int kCopy = 4;
     for (int i0 = tid; i0 < S; i0 += kCopy * kResizeThreads) {
