@@ -653,6 +653,11 @@ __device__ __forceinline__ bool issue_group(const AttnParams& p, CrossSmem<D, kF
       if (!two) tc::mma_commit(&sm.empty[st]);
     };
     const int step = two ? 1 : 2, first = two ? 0 : y;
+    // Of a pair of query tiles an issuer waits for its own only, and yet never takes the phase
+    // before last of the other's buffer when it comes to the next tile there.  Issuer 1 has gone
+    // on to its product behind issuer 0's (the turn), so the pair's first tile has landed.
+    // For issuer 0 a tile of its own lies between (were it of a pair, the next would be issuer 1's),
+    // loaded when both had given the pair back: issuer 1 did so behind the second tile's landing.
     const int qb = (nq + (two ? y : 0)) & 1;
     if (!wait(&sm.q_full[qb], ((nq + (two ? y : 0)) >> 1) & 1)) return false;
     int kst, vst;
