@@ -228,7 +228,7 @@ struct ResizeShared {
 };
 
 __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeArgs a) {
-  extern __shared__ int s_dyn[];
+  extern __shared__ __align__(16) int s_dyn[];  // (counts of pieces are read four at a time)
   __shared__ ResizeShared sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int S = a.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
