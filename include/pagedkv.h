@@ -537,8 +537,8 @@ int pkv_paged_attention_decode_biased(void* out, const void* q, const void* k_ca
 /*
  * Chunked-prefill attention under pkv_score_mods; other arguments as for
  * pkv_paged_attention_prefill_chunk (max_q_len only has to be at least 0).
- * No workspace.  Caches of up to 2^31 rows (num_blocks * num_kv_heads * 16) and
- * queries of up to 2^31 heads (total_q * num_heads); PKV_ERR_UNSUPPORTED beyond.
+ * No workspace.  Caches of fewer than 2^31 - 16 rows (num_blocks * num_kv_heads * 16) and
+ * queries of fewer than 2^31 heads (total_q * num_heads); PKV_ERR_UNSUPPORTED beyond.
  */
 int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_cache,
                                        const void* v_cache, const int32_t* block_tables,
@@ -583,9 +583,14 @@ int pkv_paged_attention_prefill_biased(void* out, const void* q, const void* k_c
  * differences fp32 no longer holds, may give rows that are not finite.
  * The split of long inputs depends on the lengths of the whole batch: a row's last bits
  * may differ between batches, never between two calls of one batch.
- * out must not overlap q or the caches.  num_seqs == 0 or total_q == 0 launches nothing.
- * Caches of up to 2^31 rows (num_blocks * num_kv_heads * 16) and queries of up to 2^31
- * heads (total_q * num_heads); PKV_ERR_UNSUPPORTED beyond.
+ * One token a sequence is pkv_paged_attention_decode's case, too, with encoder_lens as its
+ * context_lens: all of a context's keys are visible there.  That call is faster on E4M3
+ * caches (with head_dim 128 and groups of heads it rounds the weights to E4M3, though, 2 % of
+ * the output) and where every query head has a KV head of its own; this one for groups of heads
+ * with head_dim 64.
+ * out must not overlap q or the caches.  num_seqs, total_q or max_q_len of 0 launches nothing.
+ * Caches of fewer than 2^31 rows (num_blocks * num_kv_heads * 16) and queries of fewer than
+ * 2^31 heads (total_q * num_heads); PKV_ERR_UNSUPPORTED beyond.
  */
 size_t pkv_cross_workspace_size(int num_seqs, int total_q, int num_heads, int num_kv_heads,
                                 int head_dim, int max_encoder_len, int max_q_len);
@@ -653,7 +658,8 @@ int pkv_fork_requests(int32_t* tables_out, int32_t* lens_out, const int32_t* tab
  * holds, and not counted (PKV_DEVERR_BLOCK_ID).  Two sequences of one row are a caller's
  * error (that row's entries and the counts of its blocks are unspecified).
  * No output may share memory with an input or another output.  At most
- * PKV_STEP_MAPS_MAX_SEQS sequences and 2^30 blocks (PKV_ERR_UNSUPPORTED beyond).
+ * PKV_STEP_MAPS_MAX_SEQS sequences, and fewer than 2^30 - 1 blocks (PKV_ERR_UNSUPPORTED
+ * beyond).
  */
 int pkv_resize_requests(int32_t* request_tables, int32_t* ref_counts, const int32_t* rows,
                         const int32_t* cached_lens, const int32_t* new_lens,
@@ -794,7 +800,8 @@ int pkv_check_errors(uint32_t* device_errors, uint32_t* bits_out, void* stream);
  * Test hook for the failure detection above (the pages have no counterpart:
  * "第34讲 …", §1.2 speaks of preemption and service levels only).  Arms the
  * next attention call made in this process (decode, prefill chunk, draft
- * tree, mixed batch or cascade): in that call's tensor-core kernel(s) the
+ * tree, mixed batch, cascade, biased decode or prefill, cross attention): in that
+ * call's tensor-core kernel(s) the
  * first copy producer of the first CTA does not issue its skip_copy-th tile
  * copy
  * (counted from 1), and every device-side wait is bounded by wait_limit_us

@@ -722,7 +722,8 @@ def paged_attention_cross(out, q, k_cache, v_cache, block_tables, encoder_lens, 
     query_start_loc[s] .. query_start_loc[s + 1] - 1) over the encoder states that
     block_tables names, encoder_lens [S] int32 of them: pkv_paged_attention_cross.
     Bounds that are left out are total_q and the block table's length, nothing is read
-    back; workspace (uint8, >= cross_workspace_size bytes) is allocated if omitted."""
+    back; workspace (uint8, >= cross_workspace_size bytes) is allocated if omitted.  One token
+    a sequence: paged_attention_decode, with encoder_lens as its lengths, computes the same."""
     TQ, H, D = q.shape
     nb, hkv, bs, _ = k_cache.shape
     S, i32 = encoder_lens.numel(), torch.int32

@@ -8,10 +8,11 @@
 // where m only has to be near the row's maximum, since P, sums and O are floating-point
 // numbers: it starts 4 below the maximum of the first 64 states' scores and moves (and O is
 // rescaled) only when the weights of 64 states add up to more than 2^15; out = O / sum(P).
-// The sum is that of the rounded weights: with bf16 ones and rows of 300 states the error of
-// out, against that of an exact result's rounding, is 1.25 times as large instead of 1.35 (up to
-// 1.4 instead of 1.7 in a call of 16 rows), for 222 us instead of 213 with six prompts of 300
-// to 1500 tokens; decode waits for memory.
+// The sum is that of the rounded weights.  With bf16 ones (16 rows over 300 / 1500 / 16000
+// normal states, heads of 128) the error of out is 1.26 / 1.33 / 1.38 times that of an exact
+// result's rounding, at most 1.5 / 1.7 / 1.6 times in a call, instead of 1.36 / 1.41 / 1.40 and
+// 1.7 / 1.9 / 1.6 with sums of the weights as they were, for 219 us instead of 209 with six
+// prompts of 300 to 1500 tokens (both on this kernel); decode waits for memory.
 //
 // Work.  A unit is a sequence, KV head and one or two query tiles.  With two, K and V of a
 // key tile feed both, each tile having its own softmax warpgroup; with one (a token, a
@@ -35,9 +36,11 @@
 //
 // Bounds, and what was measured (calls in a graph, join included; heads of 128 on 8): HBM for
 // few queries (1.5 GB of states 234 us, 6.5 TB/s); for prompts the softmax's exponentials and
-// conversions beside the MMAs (four of 1024 tokens over 16384 states 766 us, 1440 TFLOP/s; six
-// ragged ones 218 us, 1150); on E4M3 caches the converters' and the softmax's instructions
+// conversions beside the MMAs (four of 1024 tokens over 16384 states 762 us, 1440 TFLOP/s; six
+// ragged ones 219 us, 1145); on E4M3 caches the converters' and the softmax's instructions
 // (260 MB of codes 107 us); latency for small calls (eight tokens, 16 heads of 64, 23 MB: 20 us).
+// A key tile takes its 1.03 us however few rows it has, which bounds few queries where its bytes
+// take less (heads of 64: 16 sequences of 8192 states on 8 heads, 268 MB, 58 us).
 //
 // Warps: 0-3 softmax of tile a (or even key tiles), 4-7 of tile b (odd), 8 and 9 issue the
 // MMAs of either (8 owns TMEM), 10 and 11 load, 10 also makes the items from the line of work

@@ -213,7 +213,8 @@ int launch_compact_rows(const Caches& c, const CompactArgs& a, cudaStream_t stre
 int check_caches(void* const* k, void* const* v, int num_layers, unsigned long long bytes) {
   if (!k || !v) return PKV_ERR_INVALID_ARG;
   uintptr_t at[2 * PKV_LAYERS_PER_LAUNCH];
-  // (all pairs of caches: in runs of what fits the array, each against every other cache)
+  // (overlaps: of neighbours in the order of their addresses, or of every pair where the array
+  // does not hold all caches)
   for (int i = 0; i < 2 * num_layers; ++i) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(i < num_layers ? k[i] : v[i - num_layers]);
     if (!p || (p & 15u)) return PKV_ERR_INVALID_ARG;

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_row_kernel(const ForkArgs a
 //   4  the warp that meets the r-th free block gives it to the sequence whose needs hold r.
 //      The pool is dealt out to the warps in small pieces, since the blocks handed out are
 //      those of its first ones
-// Every sum is one of integers and the hash table only counts and takes maxima, so the
+// Every sum is one of integers and the hash table only counts, takes maxima and is marked, so the
 // result does not depend on the order of the atomics.  Bound by its dependent reads and
 // five cluster barriers for small batches, by reading the counts twice (up to the last
 // block handed out the second time) on sixteen processors for large pools: 35 us for 8000 sequences
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_row_kernel(const ForkArgs a
 constexpr int kResizeCtas = 16;  // at most; one where that is enough (kOneCta...)
 constexpr int kResizeThreads = 1024;
 constexpr int kResizeWarps = kResizeThreads / 32;
-constexpr int kSat = 0x3fffffff;  // sums of needs end here; pools hold at most 2^30 - 1 blocks
+constexpr int kSat = 0x3fffffff;  // sums of needs end here; pools hold fewer blocks
 constexpr int kPerThread =
     (PKV_STEP_MAPS_MAX_SEQS + kResizeCtas * kResizeThreads - 1) / (kResizeCtas * kResizeThreads);
 
